@@ -50,10 +50,12 @@ typedef enum {
     DSPARK_ERR_TIMEOUT = 4,     /* device: a grid-wide wait gave up (status word only) */
     DSPARK_ERR_BUDGET = 5,      /* scheduler: budget < B */
     DSPARK_ERR_WORKSPACE = 6,   /* workspace NULL, misaligned or too small */
-    DSPARK_ERR_TOKEN_RANGE = 7  /* device: a token/anchor id outside [0, V) or a bad row count (status word only) */
+    DSPARK_ERR_TOKEN_RANGE = 7, /* device: a token/anchor id outside [0, V) or a bad row count (status word only) */
+    DSPARK_ERR_CACHE = 8        /* device: the paged cache's lengths, tables or pages do not fit (status word only) */
 } dspark_status;
 
-enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 };
+/* Logits and weights are DSPARK_F32 or DSPARK_BF16; the paged cache takes the other two as well. */
+enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2, DSPARK_E4M3 = 3 };
 
 /* Random-draw purposes (the fourth Philox counter word). */
 enum {
@@ -345,6 +347,140 @@ dspark_status dspark_markov_sample_block_noalloc(const dspark_sample_params* p, 
                                                  const void* W1, const void* W2, const int32_t* anchor,
                                                  int32_t* tokens, float* draft_lse, float* draft_logit_at_tok,
                                                  dspark_stream_t stream);
+
+/*
+ * The target's paged key-value cache, between the verify schedule and the verification: the target
+ * scores each request's anchor and its L_j drafted tokens in one flattened pass (P2 section 3.7.2),
+ * over what the cache holds of the request, and forgets afterwards what was rejected.  (The pages
+ * leave the cache to the serving engine; these entry points are this library's own.)
+ *
+ * Layout
+ *   A pool has num_pages pages of page_size tokens (a power of two, 1 .. 4096).  K and V are two pools
+ *   of the same layout: token i of page p, kv head h starts at p kv_page_stride + i kv_token_stride +
+ *   h kv_head_stride (elements), its D values are adjacent.  Both pools start on, and all three strides
+ *   are multiples of, 16 bytes, so [pages, tokens, heads, D] and [pages, heads, tokens, D] both serve.
+ *   block_table [B, max_blocks] int32: page of request j's tokens b page_size .. + page_size - 1 at
+ *   [j, b], for b < n_blocks[j]; what lies past that is neither read nor meant.
+ *   free_pages [num_pages] int32 with n_free [1] int32: a stack of the pages nobody holds (its top is
+ *   free_pages[n_free - 1]).
+ *   A slot is page * page_size + token within the page (int64).
+ *
+ * One step of the requests j = 0 .. B-1, whose caches hold cache_len[j] tokens:
+ *   n_j = new_len[j] + extra      tokens this step feeds (verify: new_len = verify_len, extra = 1 for
+ *                                 the anchor; new_len may be NULL for zeros)
+ *   seq_len[j] = cache_len[j] + n_j;  offsets [B+1] = exclusive prefix sum of n (CSR of the flattened
+ *   tokens; dspark_verify takes it as target_row_offsets)
+ *   need_j = max(0, ceil(seq_len[j] / page_size) - n_blocks[j]) pages: the k-th page of the step, requests
+ *   in order and blocks in order, is free_pages[n_free - 1 - k], written to block_table
+ *   slots [max_tokens]: of token offsets[j] + i, whose position is cache_len[j] + i; -1 from offsets[B] on
+ *   positions [max_tokens] int32 (or NULL): those positions, -1 from offsets[B] on
+ *   n_blocks_out[j] = n_blocks[j] + need_j;  n_free_out = n_free - sum need
+ * Outputs must not overlap cache_len, new_len, n_blocks or n_free (DSPARK_ERR_INVALID_ARG).
+ * free_pages is not written.  The same inputs give the same outputs bit for bit.
+ * Device status DSPARK_ERR_CACHE: a negative length, n_blocks outside [0, max_blocks], n_free outside
+ * [0, num_pages] (each is clamped), more pages needed than the stack or a table row holds (pages are given
+ * in order while they last), more than max_tokens tokens.  A token whose page is missing or outside the
+ * pool gets slot -1, which dspark_cache_append skips.
+ * Host errors: DSPARK_ERR_UNSUPPORTED for B > 8192.
+ * dspark_cache_workspace_size serves dspark_cache_plan and dspark_cache_commit.
+ */
+typedef struct {
+    int B;          /* requests */
+    int page_size;  /* tokens of a page: a power of two, 1 .. 4096 */
+    int num_pages;  /* pages of a pool, entries of free_pages */
+    int max_blocks; /* columns of block_table */
+    int max_tokens; /* entries of slots and positions (dspark_cache_plan) */
+    int extra;      /* tokens a request feeds or keeps beyond its new_len / add_len (>= 0) */
+} dspark_cache_params;
+
+size_t dspark_cache_workspace_size(const dspark_cache_params* p);
+dspark_status dspark_cache_plan(const dspark_cache_params* p, const int32_t* cache_len, const int32_t* new_len,
+                                int32_t* block_table, const int32_t* n_blocks, const int32_t* free_pages,
+                                const int32_t* n_free, int32_t* seq_len, int32_t* offsets, int64_t* slots,
+                                int32_t* positions, int32_t* n_blocks_out, int32_t* n_free_out, void* workspace,
+                                size_t ws_bytes, dspark_stream_t stream);
+
+/*
+ * After the verification: the requests' lengths, and the pages past them given back.
+ *   len_j = cache_len[j] + add_len[j] + extra (verify: add_len = n_accepted, extra = 1 for the anchor;
+ *   add_len may be NULL for zeros), or 0 where done[j] != 0 (done [B] uint8 or NULL: finished requests)
+ *   cache_len_out[j] = len_j;  n_blocks_out[j] = ceil(len_j / page_size)
+ *   the pages at blocks n_blocks_out[j] .. n_blocks[j] - 1 go onto the stack, requests in order and blocks
+ *   in order: free_pages[n_free], free_pages[n_free + 1], ...;  n_free_out = n_free + their number
+ * block_table and n_blocks are dspark_cache_plan's; the table is not written.  cache_len_out,
+ * n_blocks_out and n_free_out must not overlap the inputs.
+ * Device status DSPARK_ERR_CACHE: a length that is negative or longer than the request's pages, n_blocks or
+ * n_free out of range (each is clamped), more pages than the stack has room for (the rest is dropped).
+ */
+dspark_status dspark_cache_commit(const dspark_cache_params* p, const int32_t* cache_len, const int32_t* add_len,
+                                  const uint8_t* done, const int32_t* block_table, const int32_t* n_blocks,
+                                  int32_t* free_pages, const int32_t* n_free, int32_t* cache_len_out,
+                                  int32_t* n_blocks_out, int32_t* n_free_out, void* workspace, size_t ws_bytes,
+                                  dspark_stream_t stream);
+
+/*
+ * Writes the keys and values of T tokens to their slots: k, v [T, Hk, D] (dtype DSPARK_BF16 or DSPARK_F16, D
+ * adjacent values, the strides in elements).  Slots outside [0, num_pages page_size) are skipped; two
+ * tokens of one slot leave either.  kv_dtype is dtype (a copy), or DSPARK_E4M3: the value divided by
+ * k_scale[h] (v_scale[h]; [Hk] float, NULL = 1) in fp32 and rounded to nearest even, finite values clamped
+ * to +-448, NaN kept.
+ * Host errors: DSPARK_ERR_UNSUPPORTED unless D is a multiple of 16 up to 4096.  No workspace, no
+ * device-side errors; T = 0 enqueues nothing.
+ */
+typedef struct {
+    int T, Hk, D;
+    int page_size, num_pages;
+    int dtype;    /* of k and v: DSPARK_BF16 or DSPARK_F16 */
+    int kv_dtype; /* of the pools: dtype or DSPARK_E4M3 */
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int64_t kv_page_stride, kv_token_stride, kv_head_stride;
+} dspark_append_params;
+
+dspark_status dspark_cache_append(const dspark_append_params* p, const void* k, const void* v, void* k_pages,
+                                  void* v_pages, const int64_t* slots, const float* k_scale, const float* v_scale,
+                                  dspark_stream_t stream);
+
+/*
+ * Attention of the new tokens over the paged cache, which already holds their own keys and values.
+ * For token i (0 .. n_j - 1) of request j, position pos = seq_len[j] - n_j + i, and query head h, which
+ * reads kv head h / (Hq / Hk):
+ *   s_l = scale (q . k_l);  with softcap c > 0: s_l = c tanh(s_l / c)
+ *   over the keys l < seq_len[j], if causal l <= pos, with a window w > 0 also l > pos - w:
+ *   out = sum_l e^(s_l - lse) v_l,   lse = ln sum_l e^(s_l)
+ * A row that sees no key gets out = 0 and lse = -inf, as does every row of q from offsets[B] on.
+ * causal = 1, n_j = 1 is a decoding step; causal = 1, n_j = 1 + L_j the flattened verify; causal = 0 a
+ * draft block, whose positions all see the context and each other (P1, the block attention mask).
+ * Arguments
+ *   q [T, Hq, D] (dtype; D adjacent values, strides in elements); block_table, seq_len as above;
+ *   offsets [B+1] int32, or NULL for one token a request (T >= B then); k_pages, v_pages
+ *   (kv_dtype: dtype, or DSPARK_E4M3 with k_scale, v_scale [Hk] float, NULL = 1).
+ *   max_new: the most new tokens of one request, if known (0 = not): it only chooses between kernels.
+ * Outputs: out [T, Hq, D] dense (dtype), 16-byte aligned; lse [T, Hq] float or NULL.
+ * Scores, sums and outputs are held in fp32; probabilities are rounded to 16 bits (dtype; fp16 with an
+ * 8-bit cache) before they meet the values.  What a row does not see never touches it, whatever is
+ * stored there (NaN included).  The same inputs give the same outputs bit for bit.
+ * Device status DSPARK_ERR_CACHE: a negative seq_len or one past max_blocks page_size, offsets that descend or
+ * leave [0, T], a page outside the pool: each is clamped, such a page reads as zeros, and the outputs of
+ * that request are undefined.
+ * Host errors: DSPARK_ERR_UNSUPPORTED unless D is a multiple of 16 up to 256 and T Hq < 2^31.
+ */
+typedef struct {
+    int T, B, Hq, Hk, D;
+    int page_size, num_pages, max_blocks;
+    int max_new;
+    int dtype;    /* of q and out: DSPARK_BF16 or DSPARK_F16 */
+    int kv_dtype; /* of the pools: dtype or DSPARK_E4M3 */
+    int causal, window;
+    float scale, softcap;
+    int64_t q_token_stride, q_head_stride;
+    int64_t kv_page_stride, kv_token_stride, kv_head_stride;
+} dspark_attention_params;
+
+size_t dspark_paged_attention_workspace_size(const dspark_attention_params* p);
+dspark_status dspark_paged_attention(const dspark_attention_params* p, const void* q, const void* k_pages,
+                                     const void* v_pages, const int32_t* block_table, const int32_t* seq_len,
+                                     const int32_t* offsets, const float* k_scale, const float* v_scale, void* out,
+                                     float* lse, void* workspace, size_t ws_bytes, dspark_stream_t stream);
 
 /* Reads the device status word of `workspace` after synchronising `stream`
  * (DSPARK_OK when no device-side error was recorded).  `workspace` is a device pointer;

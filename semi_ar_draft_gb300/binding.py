@@ -14,9 +14,9 @@ import torch
 
 from .build import LIB
 
-F32, BF16 = 0, 1
+F32, BF16, F16, E4M3 = 0, 1, 2, 3
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "CUDA error", 4: "device wait timed out",
-          5: "budget < B", 6: "bad workspace", 7: "token out of range"}
+          5: "budget < B", 6: "bad workspace", 7: "token out of range", 8: "paged cache out of range"}
 
 
 class DsparkError(RuntimeError):
@@ -36,6 +36,27 @@ class Head(C.Structure):
 class SampleParams(C.Structure):
     _fields_ = [("B", C.c_int), ("gamma", C.c_int), ("V", C.c_int), ("r", C.c_int), ("temperature", C.c_float),
                 ("seed", C.c_uint64), ("logits_dtype", C.c_int), ("w_dtype", C.c_int), ("softcap", C.c_float)]
+
+
+class CacheParams(C.Structure):
+    _fields_ = [("B", C.c_int), ("page_size", C.c_int), ("num_pages", C.c_int), ("max_blocks", C.c_int),
+                ("max_tokens", C.c_int), ("extra", C.c_int)]
+
+
+class AppendParams(C.Structure):
+    _fields_ = [("T", C.c_int), ("Hk", C.c_int), ("D", C.c_int), ("page_size", C.c_int), ("num_pages", C.c_int),
+                ("dtype", C.c_int), ("kv_dtype", C.c_int), ("k_token_stride", C.c_int64), ("k_head_stride", C.c_int64),
+                ("v_token_stride", C.c_int64), ("v_head_stride", C.c_int64), ("kv_page_stride", C.c_int64),
+                ("kv_token_stride", C.c_int64), ("kv_head_stride", C.c_int64)]
+
+
+class AttentionParams(C.Structure):
+    _fields_ = [("T", C.c_int), ("B", C.c_int), ("Hq", C.c_int), ("Hk", C.c_int), ("D", C.c_int),
+                ("page_size", C.c_int), ("num_pages", C.c_int), ("max_blocks", C.c_int), ("max_new", C.c_int),
+                ("dtype", C.c_int), ("kv_dtype", C.c_int), ("causal", C.c_int), ("window", C.c_int),
+                ("scale", C.c_float), ("softcap", C.c_float), ("q_token_stride", C.c_int64),
+                ("q_head_stride", C.c_int64), ("kv_page_stride", C.c_int64), ("kv_token_stride", C.c_int64),
+                ("kv_head_stride", C.c_int64)]
 
 
 _L = None
@@ -82,6 +103,20 @@ def lib():
         L.dspark_tv_l1_loss.restype = i32
         L.dspark_theta_schedule.argtypes = [i32, i32, vp, vp, vp, vp, vp]
         L.dspark_theta_schedule.restype = i32
+        K = C.POINTER(CacheParams)
+        L.dspark_cache_workspace_size.argtypes = [K]
+        L.dspark_cache_workspace_size.restype = sz
+        L.dspark_cache_plan.argtypes = [K, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dspark_cache_plan.restype = i32
+        L.dspark_cache_commit.argtypes = [K, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dspark_cache_commit.restype = i32
+        L.dspark_cache_append.argtypes = [C.POINTER(AppendParams), vp, vp, vp, vp, vp, vp, vp, vp]
+        L.dspark_cache_append.restype = i32
+        A = C.POINTER(AttentionParams)
+        L.dspark_paged_attention_workspace_size.argtypes = [A]
+        L.dspark_paged_attention_workspace_size.restype = sz
+        L.dspark_paged_attention.argtypes = [A, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dspark_paged_attention.restype = i32
         L.dspark_get_device_status.argtypes = [vp, vp, C.POINTER(C.c_int32)]
         L.dspark_get_device_status.restype = i32
         L.dspark_set_wait_limit_ns.argtypes = [u64]
@@ -244,6 +279,74 @@ def dspark_theta_schedule(B, gamma, conf, sps, ell, theta=None, stream=None):
     st = lib().dspark_theta_schedule(int(B), int(gamma), _ptr(conf), _ptr(sps), _ptr(ell), _ptr(theta),
                                      _stream(stream))
     _check(st, "dspark_theta_schedule")
+
+
+_CACHE_DTYPES = {torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: E4M3}
+
+
+def cache_dtype_code(dt: torch.dtype) -> int:
+    code = _CACHE_DTYPES.get(dt)
+    if code is None:
+        raise TypeError(f"the paged cache takes bf16, fp16 and e4m3, got {dt}")
+    return code
+
+
+def _rows_ptr(t):
+    """Address of a device tensor whose last dimension is dense (the other strides are passed on)."""
+    if not t.is_cuda:
+        raise ValueError("libdspark takes device tensors")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError("the last dimension must be dense")
+    return t.data_ptr()
+
+
+def pool_layout(k_pages, v_pages):
+    """(pages, page_size, Hk, D, page / token / head stride) of two pools [pages, page_size, Hk, D]."""
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
+        raise ValueError("k_pages and v_pages are [pages, page_size, Hk, D] of one shape and layout")
+    if k_pages.dtype != v_pages.dtype:
+        raise TypeError("k_pages and v_pages are of one type")
+    return (*k_pages.shape, *k_pages.stride()[:3])
+
+
+def dspark_cache_workspace_size(p: CacheParams) -> int:
+    return int(lib().dspark_cache_workspace_size(C.byref(p)))
+
+
+def dspark_cache_plan(p, cache_len, new_len, block_table, n_blocks, free_pages, n_free, seq_len, offsets, slots,
+                      positions, n_blocks_out, n_free_out, workspace, stream=None):
+    st = lib().dspark_cache_plan(C.byref(p), _ptr(cache_len), _ptr(new_len), _ptr(block_table), _ptr(n_blocks),
+                                 _ptr(free_pages), _ptr(n_free), _ptr(seq_len), _ptr(offsets), _ptr(slots),
+                                 _ptr(positions), _ptr(n_blocks_out), _ptr(n_free_out), _ptr(workspace),
+                                 workspace.nbytes, _stream(stream))
+    _check(st, "dspark_cache_plan")
+
+
+def dspark_cache_commit(p, cache_len, add_len, done, block_table, n_blocks, free_pages, n_free, cache_len_out,
+                        n_blocks_out, n_free_out, workspace, stream=None):
+    st = lib().dspark_cache_commit(C.byref(p), _ptr(cache_len), _ptr(add_len), _ptr(done), _ptr(block_table),
+                                   _ptr(n_blocks), _ptr(free_pages), _ptr(n_free), _ptr(cache_len_out),
+                                   _ptr(n_blocks_out), _ptr(n_free_out), _ptr(workspace), workspace.nbytes,
+                                   _stream(stream))
+    _check(st, "dspark_cache_commit")
+
+
+def dspark_cache_append(p, k, v, k_pages, v_pages, slots, k_scale=None, v_scale=None, stream=None):
+    st = lib().dspark_cache_append(C.byref(p), _rows_ptr(k), _rows_ptr(v), _rows_ptr(k_pages), _rows_ptr(v_pages),
+                                   _ptr(slots), _ptr(k_scale), _ptr(v_scale), _stream(stream))
+    _check(st, "dspark_cache_append")
+
+
+def dspark_paged_attention_workspace_size(p: AttentionParams) -> int:
+    return int(lib().dspark_paged_attention_workspace_size(C.byref(p)))
+
+
+def dspark_paged_attention(p, q, k_pages, v_pages, block_table, seq_len, offsets, k_scale, v_scale, out, lse,
+                           workspace, stream=None):
+    st = lib().dspark_paged_attention(C.byref(p), _rows_ptr(q), _rows_ptr(k_pages), _rows_ptr(v_pages),
+                                      _ptr(block_table), _ptr(seq_len), _ptr(offsets), _ptr(k_scale), _ptr(v_scale),
+                                      _ptr(out), _ptr(lse), _ptr(workspace), workspace.nbytes, _stream(stream))
+    _check(st, "dspark_paged_attention")
 
 
 def dspark_get_device_status(workspace, stream=None) -> int:

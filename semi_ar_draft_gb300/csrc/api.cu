@@ -172,6 +172,7 @@ extern "C" const char* dspark_status_string(dspark_status s) {
         case DSPARK_ERR_BUDGET: return "verify budget smaller than the number of requests";
         case DSPARK_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
         case DSPARK_ERR_TOKEN_RANGE: return "token id out of range or too few target rows";
+        case DSPARK_ERR_CACHE: return "paged cache lengths, tables or pages out of range";
         default: return "unknown status";
     }
 }

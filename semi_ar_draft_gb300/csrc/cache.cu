@@ -1,0 +1,505 @@
+// cache.cu -- bookkeeping of the paged key-value cache: dspark_cache_plan (block tables, slots and
+// positions of a step's new tokens), dspark_cache_commit (lengths after the verification, pages
+// given back) and dspark_cache_append (new keys and values written into their pages).
+//
+// plan and commit are prefix sums over the requests followed by one independent action per new
+// token or page.  Each block repeats the prefix sum over all B requests (two 4-byte reads a request,
+// from L2) and keeps it in shared memory, so that tokens and pages can be dealt out over any number
+// of blocks with no second launch and no grid-wide wait.  Both are bound by the latency of one launch
+// with three dependent rounds of memory (lengths, stack or table, result), not by their bytes.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "host_util.h"
+
+namespace dspark {
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kMaxRequests = 8192;  // two 32 KB prefix arrays in shared memory
+constexpr int kItemsPerBlock = 2 * kPlanThreads;
+
+// Exclusive prefix sums over the block of two non-negative 64-bit values per thread, and their totals.
+__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long& ta, long long& tb) {
+    __shared__ long long sa[kPlanWarps], sb[kPlanWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long ia = a, ib = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, ia, o), y = __shfl_up_sync(0xffffffffu, ib, o);
+        if (lane >= o) {
+            ia += x;
+            ib += y;
+        }
+    }
+    if (lane == 31) {
+        sa[warp] = ia;
+        sb[warp] = ib;
+    }
+    __syncthreads();
+    long long pa = 0, pb = 0;
+    ta = tb = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWarps; ++w) {
+        if (w == warp) {
+            pa = ta;
+            pb = tb;
+        }
+        ta += sa[w];
+        tb += sb[w];
+    }
+    a = pa + ia - a;
+    b = pb + ib - b;
+}
+
+// The request whose range [pre[j], pre[j + 1]) holds x (pre ascending, pre[0] = 0 <= x < pre[B]).
+__device__ __forceinline__ int find_range(const int32_t* pre, int B, int x) {
+    int lo = 0, hi = B;  // pre[lo] <= x < pre[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int32_t sat32(long long x) { return (int32_t)(x > INT32_MAX ? INT32_MAX : x); }
+
+struct PlanArgs {
+    int B, page_shift, num_pages, max_blocks, max_tokens, extra;
+    const int32_t* cache_len;
+    const int32_t* new_len;  // or null: no tokens but the extra ones
+    int32_t* block_table;
+    const int32_t* n_blocks;
+    const int32_t* free_pages;
+    const int32_t* n_free;
+    int32_t* seq_len;
+    int32_t* offsets;
+    int64_t* slots;
+    int32_t* positions;  // or null
+    int32_t* n_blocks_out;
+    int32_t* n_free_out;
+    int32_t* status;
+};
+
+// One request's numbers, with every input clamped to what the other inputs allow (bad: it was not).
+struct PlanReq {
+    long long seq;
+    int old, n, have, need;
+    bool bad;
+};
+__device__ __forceinline__ PlanReq plan_request(const PlanArgs& a, int j) {
+    PlanReq r;
+    const int len = a.cache_len[j], add = a.new_len ? a.new_len[j] : 0, have = a.n_blocks[j];
+    const long long n = (long long)add + a.extra;
+    r.old = max(len, 0);
+    r.n = (int)min(max(n, 0ll), (long long)INT32_MAX);
+    r.have = min(max(have, 0), a.max_blocks);
+    r.seq = (long long)r.old + r.n;
+    const long long blocks = (r.seq + (1ll << a.page_shift) - 1) >> a.page_shift;
+    r.need = (int)max(min(blocks, (long long)a.max_blocks) - r.have, 0ll);
+    r.bad = len < 0 || n < 0 || have != r.have || blocks > a.max_blocks || r.seq > INT32_MAX;
+    return r;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(PlanArgs a) {
+    extern __shared__ int32_t sm[];
+    int32_t* off = sm;               // [B + 1] first token of each request
+    int32_t* page0 = sm + a.B + 1;   // [B + 1] first new page of each request (those the stack holds)
+    const int tid = threadIdx.x;
+    const int m = (a.B + kPlanThreads - 1) / kPlanThreads;
+    const int j0 = min(tid * m, a.B), j1 = min(j0 + m, a.B);
+    const int n_free_in = *a.n_free;
+    const int n_free = min(max(n_free_in, 0), a.num_pages);
+    long long tok = 0, pg = 0, T, P;
+    bool bad = n_free != n_free_in;
+    for (int j = j0; j < j1; ++j) {
+        const PlanReq r = plan_request(a, j);
+        tok += r.n;
+        pg += r.need;
+        bad |= r.bad;
+    }
+    block_scan2(tok, pg, T, P);
+    bad |= T > a.max_tokens || P > n_free;
+    const int given = (int)min(P, (long long)n_free);
+    const bool first = blockIdx.x == 0;
+    for (int j = j0; j < j1; ++j) {
+        const PlanReq r = plan_request(a, j);
+        const int p = (int)min(pg, (long long)given);
+        off[j] = sat32(tok);
+        page0[j] = p;
+        if (first) {
+            a.offsets[j] = sat32(tok);
+            a.seq_len[j] = sat32(r.seq);
+            a.n_blocks_out[j] = r.have + (int)min((long long)r.need, (long long)given - p);
+        }
+        tok += r.n;
+        pg += r.need;
+    }
+    if (tid == 0) {
+        off[a.B] = sat32(T);
+        page0[a.B] = given;
+    }
+    const int any_bad = __syncthreads_or(bad);
+    if (first && tid == 0) {
+        a.offsets[a.B] = sat32(T);
+        *a.n_free_out = n_free - given;
+        *a.status = any_bad ? DSPARK_ERR_CACHE : DSPARK_OK;
+    }
+    const int stride = gridDim.x * kPlanThreads;
+    // The new pages' table entries.  A page is known from the stack alone, so the tokens below look
+    // it up there too and nothing waits for these writes.
+    for (int k = blockIdx.x * kPlanThreads + tid; k < given; k += stride) {
+        const int j = find_range(page0, a.B, k);
+        const int have = min(max(a.n_blocks[j], 0), a.max_blocks);
+        a.block_table[(size_t)j * a.max_blocks + have + (k - page0[j])] = a.free_pages[n_free - 1 - k];
+    }
+    const int live = off[a.B];
+    for (long long t = blockIdx.x * kPlanThreads + tid; t < a.max_tokens; t += stride) {
+        long long slot = -1;
+        int pos = -1;
+        if (t < live) {
+            const int j = find_range(off, a.B, (int)t);
+            const long long at = (long long)max(a.cache_len[j], 0) + (t - off[j]);
+            pos = sat32(at);
+            const int have = min(max(a.n_blocks[j], 0), a.max_blocks);
+            const long long blk = at >> a.page_shift;
+            int page = -1;
+            if (blk < have)
+                page = a.block_table[(size_t)j * a.max_blocks + blk];
+            else if (blk - have < page0[j + 1] - page0[j])
+                page = a.free_pages[n_free - 1 - (page0[j] + (int)(blk - have))];
+            if (page >= 0 && page < a.num_pages)
+                slot = ((long long)page << a.page_shift) | (at & ((1 << a.page_shift) - 1));
+        }
+        a.slots[t] = slot;
+        if (a.positions) a.positions[t] = pos;
+    }
+}
+
+struct CommitArgs {
+    int B, page_shift, num_pages, max_blocks, extra;
+    const int32_t* cache_len;
+    const int32_t* add_len;  // or null
+    const uint8_t* done;     // or null
+    const int32_t* block_table;
+    const int32_t* n_blocks;
+    int32_t* free_pages;
+    const int32_t* n_free;
+    int32_t* cache_len_out;
+    int32_t* n_blocks_out;
+    int32_t* n_free_out;
+    int32_t* status;
+};
+
+struct CommitReq {
+    int len, have, keep;
+    bool bad;
+};
+__device__ __forceinline__ CommitReq commit_request(const CommitArgs& a, int j) {
+    CommitReq r;
+    const int have = a.n_blocks[j];
+    long long len = (long long)a.cache_len[j] + (a.add_len ? a.add_len[j] : 0) + a.extra;
+    r.have = min(max(have, 0), a.max_blocks);
+    r.bad = have != r.have;
+    if (a.done && a.done[j]) len = 0;
+    const long long most = (long long)r.have << a.page_shift;
+    r.bad |= len < 0 || len > most;
+    len = min(max(len, 0ll), min(most, (long long)INT32_MAX));
+    r.len = (int)len;
+    r.keep = (int)((len + (1ll << a.page_shift) - 1) >> a.page_shift);
+    return r;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) cache_commit_kernel(CommitArgs a) {
+    extern __shared__ int32_t sm[];
+    int32_t* page0 = sm;            // [B + 1] first returned page of each request
+    int32_t* keep = sm + a.B + 1;   // [B] blocks kept
+    const int tid = threadIdx.x;
+    const int m = (a.B + kPlanThreads - 1) / kPlanThreads;
+    const int j0 = min(tid * m, a.B), j1 = min(j0 + m, a.B);
+    const int n_free_in = *a.n_free;
+    const int n_free = min(max(n_free_in, 0), a.num_pages);
+    long long pg = 0, none = 0, P, unused;
+    bool bad = n_free != n_free_in;
+    for (int j = j0; j < j1; ++j) {
+        const CommitReq r = commit_request(a, j);
+        pg += r.have - r.keep;
+        bad |= r.bad;
+    }
+    block_scan2(pg, none, P, unused);
+    bad |= n_free + P > a.num_pages;
+    const int back = (int)min(P, (long long)(a.num_pages - n_free));
+    const bool first = blockIdx.x == 0;
+    for (int j = j0; j < j1; ++j) {
+        const CommitReq r = commit_request(a, j);
+        page0[j] = (int)min(pg, (long long)back);
+        keep[j] = r.keep;
+        if (first) {
+            a.cache_len_out[j] = r.len;
+            a.n_blocks_out[j] = r.keep;
+        }
+        pg += r.have - r.keep;
+    }
+    if (tid == 0) page0[a.B] = back;
+    const int any_bad = __syncthreads_or(bad);
+    if (first && tid == 0) {
+        *a.n_free_out = n_free + back;
+        *a.status = any_bad ? DSPARK_ERR_CACHE : DSPARK_OK;
+    }
+    for (int k = blockIdx.x * kPlanThreads + tid; k < back; k += gridDim.x * kPlanThreads) {
+        const int j = find_range(page0, a.B, k);
+        a.free_pages[n_free + k] = a.block_table[(size_t)j * a.max_blocks + keep[j] + (k - page0[j])];
+    }
+}
+
+// ---------------------------------------------------------------- append
+struct AppendArgs {
+    int T, chunks, page_shift;  // chunks: 8-element groups of one head's row
+    uint32_t per_token;         // Hk * chunks
+    long long slots_end;        // num_pages * page_size
+    const uint16_t* k;
+    const uint16_t* v;
+    long long k_token, k_head, v_token, v_head;  // strides, elements
+    unsigned char* k_pages;
+    unsigned char* v_pages;
+    long long page, token, head;  // strides of the pools, elements
+    const int64_t* slots;
+    const float* k_scale;
+    const float* v_scale;
+};
+
+constexpr int kAppendThreads = 256;
+
+template <bool ALIGNED>
+__device__ __forceinline__ uint4 load_row8(const uint16_t* p) {
+    if constexpr (ALIGNED) {
+        return *reinterpret_cast<const uint4*>(p);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+    if (BF16) return make_float2(bf16_lo(w), bf16_hi(w));
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Eight values divided by the head's scale (IEEE division, so that the stored byte does not depend on
+// how the quotient was formed) and rounded to e4m3, to nearest even, finite values clamped to +-448.
+template <bool BF16>
+__device__ __forceinline__ uint2 quantize8(uint4 x, float scale) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t r[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack16<BF16>(w[i]);
+        const float2 q = make_float2(__fdiv_rn(f.x, scale), __fdiv_rn(f.y, scale));
+        const uint32_t b = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+        r[i >> 1] |= b << (16 * (i & 1));
+    }
+    return make_uint2(r[0], r[1]);
+}
+
+// One thread moves one 8-element group of K and the same one of V.  CACHE8: e4m3 pages.
+template <bool CACHE8, bool BF16, bool ALIGNED>
+__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs a) {
+    const long long total = (long long)a.T * a.per_token;
+    const long long stride = (long long)gridDim.x * kAppendThreads;
+    for (long long i = (long long)blockIdx.x * kAppendThreads + threadIdx.x; i < total; i += stride) {
+        const long long t = total <= UINT32_MAX ? (long long)((uint32_t)i / a.per_token) : i / a.per_token;
+        const uint32_t rest = (uint32_t)(i - t * a.per_token);
+        const int h = (int)(rest / (uint32_t)a.chunks), c = (int)(rest % (uint32_t)a.chunks);
+        const long long slot = a.slots[t];
+        if (slot < 0 || slot >= a.slots_end) continue;
+        const uint4 kx = load_row8<ALIGNED>(a.k + t * a.k_token + h * a.k_head + 8 * c);
+        const uint4 vx = load_row8<ALIGNED>(a.v + t * a.v_token + h * a.v_head + 8 * c);
+        const long long at = (slot >> a.page_shift) * a.page + (slot & ((1 << a.page_shift) - 1)) * a.token +
+                             h * a.head + 8 * c;
+        if (CACHE8) {
+            const float ks = a.k_scale ? a.k_scale[h] : 1.f, vs = a.v_scale ? a.v_scale[h] : 1.f;
+            *reinterpret_cast<uint2*>(a.k_pages + at) = quantize8<BF16>(kx, ks);
+            *reinterpret_cast<uint2*>(a.v_pages + at) = quantize8<BF16>(vx, vs);
+        } else {
+            *reinterpret_cast<uint4*>(a.k_pages + 2 * at) = kx;
+            *reinterpret_cast<uint4*>(a.v_pages + 2 * at) = vx;
+        }
+    }
+}
+
+template <bool CACHE8, bool BF16>
+void launch_append(const AppendArgs& a, bool aligned, int blocks, cudaStream_t s) {
+    if (aligned)
+        cache_append_kernel<CACHE8, BF16, true><<<blocks, kAppendThreads, 0, s>>>(a);
+    else
+        cache_append_kernel<CACHE8, BF16, false><<<blocks, kAppendThreads, 0, s>>>(a);
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && x < y + nb && y < x + na;
+}
+
+dspark_status check_cache_params(const dspark_cache_params* p) {
+    if (!p || p->B < 1 || p->num_pages < 1 || p->max_blocks < 1 || page_shift_of(p->page_size) < 0)
+        return DSPARK_ERR_INVALID_ARG;
+    if (p->B > kMaxRequests) return DSPARK_ERR_UNSUPPORTED;
+    return DSPARK_OK;
+}
+
+int blocks_for(long long items, int sms) {
+    const long long b = (items + kItemsPerBlock - 1) / kItemsPerBlock;
+    return (int)(b < 1 ? 1 : (b > sms ? sms : b));
+}
+
+}  // namespace
+
+int page_shift_of(int page_size) {
+    if (page_size < 1 || page_size > 4096 || (page_size & (page_size - 1))) return -1;
+    int s = 0;
+    while ((1 << s) < page_size) ++s;
+    return s;
+}
+
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" size_t dspark_cache_workspace_size(const dspark_cache_params* p) {
+    return check_cache_params(p) == DSPARK_OK ? kHeaderBytes : 0;
+}
+
+extern "C" dspark_status dspark_cache_plan(const dspark_cache_params* p, const int32_t* cache_len,
+                                           const int32_t* new_len, int32_t* block_table, const int32_t* n_blocks,
+                                           const int32_t* free_pages, const int32_t* n_free, int32_t* seq_len,
+                                           int32_t* offsets, int64_t* slots, int32_t* positions, int32_t* n_blocks_out,
+                                           int32_t* n_free_out, void* workspace, size_t ws_bytes,
+                                           dspark_stream_t stream) {
+    dspark_status st = check_cache_params(p);
+    if (st != DSPARK_OK) return st;
+    if (p->max_tokens < 0 || p->extra < 0) return DSPARK_ERR_INVALID_ARG;
+    if (!cache_len || !block_table || !n_blocks || !free_pages || !n_free || !seq_len || !offsets ||
+        (!slots && p->max_tokens) || !n_blocks_out || !n_free_out)
+        return DSPARK_ERR_INVALID_ARG;
+    // Every block reads all of the inputs while the first one writes the outputs.
+    const size_t nb = sizeof(int32_t) * (size_t)p->B;
+    const void* ins[] = {cache_len, new_len, n_blocks, n_free};
+    const size_t in_bytes[] = {nb, nb, nb, sizeof(int32_t)};
+    const void* outs[] = {seq_len, offsets, n_blocks_out, n_free_out};
+    const size_t out_bytes[] = {nb, nb + sizeof(int32_t), nb, sizeof(int32_t)};
+    for (int i = 0; i < 4; ++i)
+        for (int o = 0; o < 4; ++o)
+            if (overlap(ins[i], in_bytes[i], outs[o], out_bytes[o])) return DSPARK_ERR_INVALID_ARG;
+    if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < kHeaderBytes) return DSPARK_ERR_WORKSPACE;
+    int sms = 0, per_sm = 0;
+    if (device_sm_count(&sms) != cudaSuccess) return DSPARK_ERR_CUDA;
+    const size_t smem = sizeof(int32_t) * 2 * ((size_t)p->B + 1);
+    if (prepare_kernel((const void*)cache_plan_kernel, smem, kPlanThreads, &per_sm) != cudaSuccess)
+        return DSPARK_ERR_CUDA;
+    PlanArgs a{p->B, page_shift_of(p->page_size), p->num_pages, p->max_blocks, p->max_tokens, p->extra, cache_len,
+               new_len, block_table, n_blocks, free_pages, n_free, seq_len, offsets, slots, positions, n_blocks_out,
+               n_free_out, &static_cast<WsHeader*>(workspace)->status};
+    cache_plan_kernel<<<blocks_for(p->max_tokens, sms), kPlanThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return DSPARK_ERR_CUDA;
+    note_launch();
+    return DSPARK_OK;
+}
+
+extern "C" dspark_status dspark_cache_commit(const dspark_cache_params* p, const int32_t* cache_len,
+                                             const int32_t* add_len, const uint8_t* done, const int32_t* block_table,
+                                             const int32_t* n_blocks, int32_t* free_pages, const int32_t* n_free,
+                                             int32_t* cache_len_out, int32_t* n_blocks_out, int32_t* n_free_out,
+                                             void* workspace, size_t ws_bytes, dspark_stream_t stream) {
+    dspark_status st = check_cache_params(p);
+    if (st != DSPARK_OK) return st;
+    if (p->extra < 0) return DSPARK_ERR_INVALID_ARG;
+    if (!cache_len || !block_table || !n_blocks || !free_pages || !n_free || !cache_len_out || !n_blocks_out ||
+        !n_free_out)
+        return DSPARK_ERR_INVALID_ARG;
+    const size_t nb = sizeof(int32_t) * (size_t)p->B;
+    const void* ins[] = {cache_len, add_len, n_blocks, n_free, done};
+    const size_t in_bytes[] = {nb, nb, nb, sizeof(int32_t), (size_t)p->B};
+    const void* outs[] = {cache_len_out, n_blocks_out, n_free_out};
+    const size_t out_bytes[] = {nb, nb, sizeof(int32_t)};
+    for (int i = 0; i < 5; ++i)
+        for (int o = 0; o < 3; ++o)
+            if (overlap(ins[i], in_bytes[i], outs[o], out_bytes[o])) return DSPARK_ERR_INVALID_ARG;
+    if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < kHeaderBytes) return DSPARK_ERR_WORKSPACE;
+    int sms = 0, per_sm = 0;
+    if (device_sm_count(&sms) != cudaSuccess) return DSPARK_ERR_CUDA;
+    const size_t smem = sizeof(int32_t) * 2 * ((size_t)p->B + 1);
+    if (prepare_kernel((const void*)cache_commit_kernel, smem, kPlanThreads, &per_sm) != cudaSuccess)
+        return DSPARK_ERR_CUDA;
+    CommitArgs a{p->B, page_shift_of(p->page_size), p->num_pages, p->max_blocks, p->extra, cache_len, add_len, done,
+                 block_table, n_blocks, free_pages, n_free, cache_len_out, n_blocks_out, n_free_out,
+                 &static_cast<WsHeader*>(workspace)->status};
+    // The pages that come back are known on the device only: a block for every 64 requests spreads
+    // those of finished requests, and one block does for the usual few.
+    const int blocks = (p->B + 63) / 64;
+    cache_commit_kernel<<<blocks, kPlanThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return DSPARK_ERR_CUDA;
+    note_launch();
+    return DSPARK_OK;
+}
+
+extern "C" dspark_status dspark_cache_append(const dspark_append_params* p, const void* k, const void* v, void* k_pages,
+                                             void* v_pages, const int64_t* slots, const float* k_scale,
+                                             const float* v_scale, dspark_stream_t stream) {
+    if (!p || p->T < 0 || p->Hk < 1 || p->D < 1 || p->num_pages < 1 || page_shift_of(p->page_size) < 0)
+        return DSPARK_ERR_INVALID_ARG;
+    if (p->dtype != DSPARK_BF16 && p->dtype != DSPARK_F16) return DSPARK_ERR_INVALID_ARG;
+    const bool e4m3 = p->kv_dtype == DSPARK_E4M3;
+    if (!e4m3 && p->kv_dtype != p->dtype) return DSPARK_ERR_INVALID_ARG;
+    if (!k_pages || !v_pages || (p->T && (!k || !v || !slots))) return DSPARK_ERR_INVALID_ARG;
+    if (p->D % 16 || p->D > 4096 || (long long)p->Hk * p->D > (1 << 22)) return DSPARK_ERR_UNSUPPORTED;
+    const size_t esz = e4m3 ? 1 : 2;
+    if ((((uintptr_t)k_pages | (uintptr_t)v_pages) & 15u) || (p->kv_page_stride * esz) % 16 ||
+        (p->kv_token_stride * esz) % 16 || (p->kv_head_stride * esz) % 16)
+        return DSPARK_ERR_INVALID_ARG;
+    if (p->T == 0) return DSPARK_OK;
+    int sms = 0;
+    if (device_sm_count(&sms) != cudaSuccess) return DSPARK_ERR_CUDA;
+    AppendArgs a;
+    a.T = p->T;
+    a.chunks = p->D / 8;
+    a.page_shift = page_shift_of(p->page_size);
+    a.per_token = (uint32_t)p->Hk * (uint32_t)a.chunks;
+    a.slots_end = (long long)p->num_pages * p->page_size;
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.k_token = p->k_token_stride;
+    a.k_head = p->k_head_stride;
+    a.v_token = p->v_token_stride;
+    a.v_head = p->v_head_stride;
+    a.k_pages = static_cast<unsigned char*>(k_pages);
+    a.v_pages = static_cast<unsigned char*>(v_pages);
+    a.page = p->kv_page_stride;
+    a.token = p->kv_token_stride;
+    a.head = p->kv_head_stride;
+    a.slots = slots;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    const bool aligned = !((((uintptr_t)k | (uintptr_t)v) & 15u) || (a.k_token | a.k_head | a.v_token | a.v_head) % 8);
+    const long long total = (long long)a.T * a.per_token;
+    const long long want = (total + kAppendThreads - 1) / kAppendThreads, most = (long long)sms * 16;
+    const int blocks = (int)(want < most ? want : most);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool bf16 = p->dtype == DSPARK_BF16;
+    if (!e4m3)
+        launch_append<false, true>(a, aligned, blocks, s);  // a copy of the bits, whichever 16-bit type
+    else if (bf16)
+        launch_append<true, true>(a, aligned, blocks, s);
+    else
+        launch_append<true, false>(a, aligned, blocks, s);
+    if (cudaGetLastError() != cudaSuccess) return DSPARK_ERR_CUDA;
+    note_launch();
+    return DSPARK_OK;
+}

@@ -20,6 +20,8 @@ cudaError_t prepare_kernel(const void* fn, size_t smem, int threads, int* per_sm
 cudaError_t max_active_clusters(const void* fn, int cs, int threads, size_t smem, int* n);
 uint64_t wait_limit_ns();               // bound of every grid-wide wait
 
+int page_shift_of(int page_size);  // log2 of a cache page's tokens (1 .. 4096, a power of two), else -1
+
 dspark_status validate_sample_params(const dspark_sample_params* p);
 size_t sample_workspace_bytes(const dspark_sample_params* p);
 bool markov_use_mma(const dspark_sample_params* p);

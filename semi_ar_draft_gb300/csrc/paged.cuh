@@ -1,0 +1,226 @@
+// paged.cuh -- attention over a paged key-value cache: the arguments, the split of a call's work over
+// the grid, and the buffers through which parts of one row meet (GPU side only).
+//
+// Work.  A request j with n_j new tokens gives, for each kv head, G n_j rows (G = Hq / Hk query heads
+// share a kv head; row r is token r / G, head r % G), cut into row tiles; each (request, kv head, row
+// tile) is an item, and an item is a run of key tiles over the cache.  All items' key tiles, in order
+// (request, kv head, row tile, key tile), form one list of units that is cut into equal contiguous
+// ranges, one a block.  The lengths are on the device only, so every block adds them up itself (a
+// block-wide prefix sum over the requests) and finds its own range; nothing is planned on the host
+// and a call can be replayed from a graph with other lengths.
+//
+// Join.  A range may begin or end inside an item.  Such a segment's (maximum, sum, unnormalised output)
+// goes to one of the block's two partial buffers -- kTail when the segment does not begin the item,
+// kHead when it does but does not end it -- and the block in which the item begins describes it.  A
+// second kernel joins the parts in the order of the keys, so results do not depend on timing.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace dspark {
+
+struct AttnArgs {
+    int T, B, Hq, Hk, G, D;
+    int page_shift, num_pages, max_blocks;
+    int causal, window;
+    float scale, softcap;
+    const unsigned char* q;
+    long long q_token, q_head;  // strides, elements
+    const unsigned char* k_pages;
+    const unsigned char* v_pages;
+    long long page, token, head;  // strides of the pools, bytes
+    const int32_t* block_table;
+    const int32_t* seq_len;
+    const int32_t* offsets;  // or null: one token a request
+    const float* k_scale;
+    const float* v_scale;
+    unsigned char* out;  // [T, Hq, D]
+    float* lse;          // [T, Hq] or null
+    // workspace
+    int32_t* status;
+    struct PartItem* items;  // [parts]
+    float2* part_ml;         // [2 parts][rows of a tile]: (maximum, log2 domain; sum)
+    float* part_o;           // [2 parts][rows of a tile][D]
+};
+
+// The item that begins in a block and ends in a later one (last < 0: none), and the block's error.
+struct PartItem {
+    int last;       // block that ends it
+    int row0;       // first row of the tile within the request and kv head
+    int rows;       // real rows of the tile
+    int token0;     // row of q and out of the request's first token
+    int head;       // kv head
+    int err;        // DSPARK_* recorded by this block
+    int pad[2];
+};
+
+enum { kTail = 0, kHead = 1 };
+constexpr int kMaxParts = 320;  // blocks of the largest grid (two a multiprocessor)
+
+// One request as the kernels see it: every number clamped to the buffers (bad: it was not).
+struct AttnReq {
+    int token0, n, seq, lo;  // lo: first key that any row sees
+    bool bad;
+};
+__device__ __forceinline__ AttnReq attn_request(const AttnArgs& a, int j) {
+    AttnReq r;
+    int o0 = j, o1 = j + 1;
+    if (a.offsets) {
+        o0 = __ldg(a.offsets + j);
+        o1 = __ldg(a.offsets + j + 1);
+    }
+    const int t0 = min(max(o0, 0), a.T), t1 = min(max(o1, t0), a.T);
+    const int len = __ldg(a.seq_len + j);
+    const long long cap = (long long)a.max_blocks << a.page_shift;
+    r.token0 = t0;
+    r.n = t1 - t0;
+    r.seq = (int)min((long long)max(len, 0), cap);
+    r.bad = t0 != o0 || t1 != o1 || len != r.seq;
+    r.lo = a.window > 0 ? (int)max((long long)r.seq - r.n - a.window + 1, 0ll) : 0;
+    return r;
+}
+// Row tiles and key tiles of a request's items (an item has at least one key tile, so that rows that
+// see nothing are written too).
+__device__ __forceinline__ int row_tiles(const AttnArgs& a, int n, int row_tile) {
+    return (int)(((long long)n * a.G + row_tile - 1) / row_tile);
+}
+__device__ __forceinline__ int key_tiles(const AttnReq& r, int key_tile) {
+    const int first = r.lo / key_tile;
+    return max((r.seq + key_tile - 1) / key_tile - first, 1);
+}
+
+// Where a block's range begins: request, unit within the request.
+struct AttnStart {
+    long long begin, end, per, total;  // this block's units, units a block, all units
+    int j;
+    long long at;
+};
+
+// Adds up all requests' units and finds the range of block `part` of `parts`.  All threads of the block.
+// min_units: a block takes no fewer (a short range would cost more to join than it saves).
+template <int THREADS>
+__device__ AttnStart attn_start(const AttnArgs& a, int row_tile, int key_tile, int parts, int part, int min_units,
+                                bool* bad) {
+    __shared__ long long warp_sum_[THREADS / 32];
+    __shared__ int s_j;
+    __shared__ long long s_at;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int m = (a.B + THREADS - 1) / THREADS;
+    const int j0 = min(tid * m, a.B), j1 = min(j0 + m, a.B);
+    long long u = 0;
+    bool b = false;
+    for (int j = j0; j < j1; ++j) {
+        const AttnReq r = attn_request(a, j);
+        b |= r.bad;
+        u += (long long)row_tiles(a, r.n, row_tile) * a.Hk * key_tiles(r, key_tile);
+    }
+    long long inc = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) warp_sum_[warp] = inc;
+    if (tid == 0) s_j = a.B;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w == warp) before = total;
+        total += warp_sum_[w];
+    }
+    AttnStart s;
+    s.total = total;
+    s.per = max((total + parts - 1) / parts, (long long)min_units);
+    s.begin = min((long long)part * s.per, total);
+    s.end = min(s.begin + s.per, total);
+    long long at = before + inc - u;  // units before this thread's requests
+    if (s.begin < s.end && at <= s.begin && s.begin < at + u) {
+        int j = j0;
+        for (; j < j1; ++j) {
+            const AttnReq r = attn_request(a, j);
+            const long long x = (long long)row_tiles(a, r.n, row_tile) * a.Hk * key_tiles(r, key_tile);
+            if (s.begin < at + x) break;
+            at += x;
+        }
+        s_j = j;
+        s_at = s.begin - at;
+    }
+    *bad = __syncthreads_or(b) != 0;
+    s.j = s_j;
+    s.at = s_at;
+    return s;
+}
+
+// A walk over a block's units, one key tile at a time.
+struct AttnWalk {
+    AttnReq r;
+    int j, item, items, kt, kts, rts, kt_first;
+    long long left;  // units left in the block's range, this one included
+    __device__ __forceinline__ bool done() const { return left <= 0; }
+};
+__device__ __forceinline__ void walk_request(const AttnArgs& a, AttnWalk& w, int row_tile, int key_tile) {
+    w.r = attn_request(a, w.j);
+    w.rts = row_tiles(a, w.r.n, row_tile);
+    w.items = w.rts * a.Hk;
+    w.kts = key_tiles(w.r, key_tile);
+    w.kt_first = w.r.lo / key_tile;
+}
+__device__ __forceinline__ AttnWalk walk_begin(const AttnArgs& a, const AttnStart& s, int row_tile, int key_tile) {
+    AttnWalk w;
+    w.left = s.end - s.begin;
+    w.j = s.j;
+    w.item = w.kt = 0;
+    w.items = w.kts = w.rts = 1;
+    w.kt_first = 0;
+    w.r = AttnReq{0, 0, 0, 0, false};
+    if (w.left > 0) {
+        walk_request(a, w, row_tile, key_tile);
+        w.item = (int)(s.at / w.kts);
+        w.kt = (int)(s.at - (long long)w.item * w.kts);
+    }
+    return w;
+}
+__device__ __forceinline__ void walk_next(const AttnArgs& a, AttnWalk& w, int row_tile, int key_tile) {
+    --w.left;
+    if (++w.kt < w.kts) return;
+    w.kt = 0;
+    if (++w.item < w.items || w.left <= 0) return;
+    w.item = 0;
+    do {  // requests without new tokens have no units
+        ++w.j;
+        walk_request(a, w, row_tile, key_tile);
+    } while (w.items == 0 && w.j + 1 < a.B);
+}
+
+// tanh from its definition, (1 - e) / (1 + e) with e = e^(-2 |x|); near 0, where that cancels, the odd
+// series to x^7 (relative error below 1e-6 for |x| < 1/8).
+__device__ __forceinline__ float attn_tanh(float x) {
+    const float ax = fabsf(x);
+    if (ax < 0.125f) {
+        const float s = x * x;
+        return x * fmaf(s, fmaf(s, fmaf(s, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+    }
+    const float e = ex2(-2.f * kLog2e * ax);
+    return copysignf(__fdividef(1.f - e, 1.f + e), x);  // NaN stays NaN: e is
+}
+
+// Two floats rounded to the 16-bit type, first in the low half.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    uint32_t r;
+    if (BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Secondary-launch controls: the join kernel is launched while the attention kernel still runs and
+// waits there for its end.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+}  // namespace dspark
