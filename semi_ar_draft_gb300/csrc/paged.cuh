@@ -57,7 +57,8 @@ struct PartItem {
 };
 
 enum { kTail = 0, kHead = 1 };
-constexpr int kMaxParts = 320;  // blocks of the largest grid (two a multiprocessor)
+constexpr int kMaxParts = 320;    // blocks of the largest grid with row tiles of 16 (two a multiprocessor)
+constexpr int kMaxTcParts = 160;  // and of 128 (one)
 
 // One request as the kernels see it: every number clamped to the buffers (bad: it was not).
 struct AttnReq {
@@ -98,14 +99,17 @@ struct AttnStart {
     long long at;
 };
 
+struct AttnScratch {  // in shared memory, for attn_start
+    long long warp_sum[16], at;
+    int j;
+};
+
 // Adds up all requests' units and finds the range of block `part` of `parts`.  All threads of the block.
 // min_units: a block takes no fewer (a short range would cost more to join than it saves).
 template <int THREADS>
 __device__ AttnStart attn_start(const AttnArgs& a, int row_tile, int key_tile, int parts, int part, int min_units,
-                                bool* bad) {
-    __shared__ long long warp_sum_[THREADS / 32];
-    __shared__ int s_j;
-    __shared__ long long s_at;
+                                AttnScratch* scratch, bool* bad) {
+    static_assert(THREADS / 32 <= 16, "scratch");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int m = (a.B + THREADS - 1) / THREADS;
     const int j0 = min(tid * m, a.B), j1 = min(j0 + m, a.B);
@@ -122,14 +126,14 @@ __device__ AttnStart attn_start(const AttnArgs& a, int row_tile, int key_tile, i
         const long long x = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += x;
     }
-    if (lane == 31) warp_sum_[warp] = inc;
-    if (tid == 0) s_j = a.B;
+    if (lane == 31) scratch->warp_sum[warp] = inc;
+    if (tid == 0) scratch->j = a.B;
     __syncthreads();
     long long before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
         if (w == warp) before = total;
-        total += warp_sum_[w];
+        total += scratch->warp_sum[w];
     }
     AttnStart s;
     s.total = total;
@@ -145,12 +149,12 @@ __device__ AttnStart attn_start(const AttnArgs& a, int row_tile, int key_tile, i
             if (s.begin < at + x) break;
             at += x;
         }
-        s_j = j;
-        s_at = s.begin - at;
+        scratch->j = j;
+        scratch->at = s.begin - at;
     }
     *bad = __syncthreads_or(b) != 0;
-    s.j = s_j;
-    s.at = s_at;
+    s.j = scratch->j;
+    s.at = scratch->at;
     return s;
 }
 
@@ -195,6 +199,26 @@ __device__ __forceinline__ void walk_next(const AttnArgs& a, AttnWalk& w, int ro
     } while (w.items == 0 && w.j + 1 < a.B);
 }
 
+// Rows of out (and lse) past the last request's tokens: no request owns them.  i0: this thread of n.
+__device__ __forceinline__ void attn_tail_rows(const AttnArgs& a, size_t i0, size_t n) {
+    const int end = a.offsets ? min(max(__ldg(a.offsets + a.B), 0), a.T) : a.B;
+    const size_t row = (size_t)a.Hq * a.D * 2 / 16;  // 16-byte groups of a token
+    for (size_t i = end * row + i0; i < a.T * row; i += n) reinterpret_cast<uint4*>(a.out)[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+        for (size_t i = (size_t)end * a.Hq + i0; i < (size_t)a.T * a.Hq; i += n) a.lse[i] = -CUDART_INF_F;
+}
+
+// Row of [T Hq] of row `row` of a request and kv head.
+__device__ __forceinline__ long long attn_out_row(const AttnArgs& a, int token0, int head, int row) {
+    return (long long)(token0 + row / a.G) * a.Hq + head * a.G + row % a.G;
+}
+
+// 16 bytes, or 16 zero bytes where !real (src is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
+    const int n = real ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
 // tanh from its definition, (1 - e) / (1 + e) with e = e^(-2 |x|); near 0, where that cancels, the odd
 // series to x^7 (relative error below 1e-6 for |x| < 1/8).
 __device__ __forceinline__ float attn_tanh(float x) {
@@ -222,5 +246,9 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // waits there for its end.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Row tiles of 128 on the fifth-generation tensor cores (paged_attn_tc.cu): 16-bit caches, 16-byte
+// aligned query rows.
+dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int sms, cudaStream_t s, int* parts);
 
 }  // namespace dspark

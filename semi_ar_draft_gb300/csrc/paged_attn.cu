@@ -25,6 +25,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 16;
+constexpr int kTcRows = 128;  // rows of a tile of launch_attn_tc
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -50,11 +51,6 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// 16 bytes, or 16 zero bytes where !real (src is then not read).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
-    const int n = real ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 // Two e4m3 values (low 16 bits) as two halves.
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t w) {
@@ -91,11 +87,6 @@ struct Rows16 {
     }
 };
 
-// Row of [T Hq] of an item's row.
-__device__ __forceinline__ long long out_row(const AttnArgs& a, int token0, int head, int row) {
-    return (long long)(token0 + row / a.G) * a.Hq + head * a.G + row % a.G;
-}
-
 template <bool BF16>
 __device__ __forceinline__ void store_out4(const AttnArgs& a, long long row, int col, float4 v) {
     uint2 w = make_uint2(pack16<BF16>(v.x, v.y), pack16<BF16>(v.z, v.w));
@@ -112,26 +103,16 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float2 s_ml[kWarps][kRows];
     __shared__ int s_err;
+    __shared__ AttnScratch s_start;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int part = blockIdx.x, parts = gridDim.x;
     launch_dependents();
     if (tid == 0) s_err = 0;
     bool bad;
-    const AttnStart start = attn_start<kThreads>(a, kRows, C::kKeyTile, parts, part, 2, &bad);
+    const AttnStart start = attn_start<kThreads>(a, kRows, C::kKeyTile, parts, part, 2, &s_start, &bad);
 
-    // Rows of q and out past the last request's tokens: no request owns them.
-    {
-        const int end = a.offsets ? min(max(__ldg(a.offsets + a.B), 0), a.T) : a.B;
-        const size_t row = (size_t)a.Hq * a.D * 2 / 16, n0 = end * row, n1 = a.T * row;
-        for (size_t i = n0 + (size_t)part * kThreads + tid; i < n1; i += (size_t)parts * kThreads)
-            reinterpret_cast<uint4*>(a.out)[i] = make_uint4(0, 0, 0, 0);
-        if (a.lse)
-            for (size_t i = (size_t)end * a.Hq + (size_t)part * kThreads + tid; i < (size_t)a.T * a.Hq;
-                 i += (size_t)parts * kThreads)
-                a.lse[i] = -CUDART_INF_F;
-    }
-
+    attn_tail_rows(a, (size_t)part * kThreads + tid, (size_t)parts * kThreads);
     unsigned char* ring = smem + (size_t)warp * C::kStages * C::kStage;
     const uint32_t ring_addr = smem_addr(ring);
     uint4* qs = reinterpret_cast<uint4*>(smem + (size_t)kWarps * C::kStages * C::kStage);
@@ -484,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
                     v.w = fmaf(y.w, f, v.w);
                 }
                 if (whole) {
-                    const long long at = out_row(a, w.r.token0, head, row0 + row);
+                    const long long at = attn_out_row(a, w.r.token0, head, row0 + row);
                     if (col < a.D) {
                         const float inv = ll == 0.f ? 0.f : vscale / ll;
                         store_out4<BF16>(a, at, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
@@ -529,8 +510,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
     wait_primary();
     if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
         int err = 0;
-        for (int p = lane; p < parts; p += 32) err |= a.items[p].err;
-        err = __reduce_or_sync(0xffffffffu, err);
+        for (int p = lane; p < parts; p += 32) err = max(err, a.items[p].err);
+        err = __reduce_max_sync(0xffffffffu, err);
         if (lane == 0) *a.status = err;
     }
     const PartItem it = a.items[blockIdx.x];
@@ -549,7 +530,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
         ll = warp_sum(ll);
         const float vscale = a.v_scale ? __ldg(a.v_scale + it.head) : 1.f;
         const float inv = ll == 0.f ? 0.f : vscale / ll;
-        const long long at = out_row(a, it.token0, it.head, it.row0 + row);
+        const long long at = attn_out_row(a, it.token0, it.head, it.row0 + row);
         for (int col = 4 * lane; col < a.D; col += 128) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -594,12 +575,19 @@ dspark_status launch_rows16_d(const AttnArgs& a, int sms, cudaStream_t s, int* p
 struct AttnWs {
     size_t items, ml, o, bytes;
 };
-AttnWs attn_ws(int D) {
+// Whether a call takes row tiles of 128: the most rows a request and kv head can have (from max_new, or
+// the mean number of tokens where it is not given) against the 16 of the other kernel.
+bool wide_rows(const dspark_attention_params* p) {
+    const int n = p->max_new > 0 ? p->max_new : (p->T + p->B - 1) / p->B;
+    return p->kv_dtype == p->dtype && (long long)n * (p->Hq / p->Hk) > kRows;
+}
+AttnWs attn_ws(const dspark_attention_params* p) {
+    const size_t rows = wide_rows(p) ? (size_t)2 * kMaxTcParts * kTcRows : (size_t)2 * kMaxParts * kRows;
     AttnWs w;
     w.items = kHeaderBytes;
     w.ml = align_up(w.items + sizeof(PartItem) * kMaxParts, 256);
-    w.o = align_up(w.ml + sizeof(float2) * 2 * kMaxParts * kRows, 256);
-    w.bytes = align_up(w.o + sizeof(float) * 2 * kMaxParts * kRows * (size_t)D, 256);
+    w.o = align_up(w.ml + sizeof(float2) * rows, 256);
+    w.bytes = align_up(w.o + sizeof(float) * rows * (size_t)p->D, 256);
     return w;
 }
 
@@ -620,7 +608,7 @@ dspark_status check_attention_params(const dspark_attention_params* p) {
 using namespace dspark;
 
 extern "C" size_t dspark_paged_attention_workspace_size(const dspark_attention_params* p) {
-    return check_attention_params(p) == DSPARK_OK ? attn_ws(p->D).bytes : 0;
+    return check_attention_params(p) == DSPARK_OK ? attn_ws(p).bytes : 0;
 }
 
 extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p, const void* q, const void* k_pages,
@@ -637,7 +625,7 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     if ((((uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)out) & 15u) || ((uintptr_t)q & 1u) ||
         (p->kv_page_stride * esz) % 16 || (p->kv_token_stride * esz) % 16 || (p->kv_head_stride * esz) % 16)
         return DSPARK_ERR_INVALID_ARG;
-    const AttnWs w = attn_ws(p->D);
+    const AttnWs w = attn_ws(p);
     if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < w.bytes) return DSPARK_ERR_WORKSPACE;
     int sms = 0;
     if (device_sm_count(&sms) != cudaSuccess) return DSPARK_ERR_CUDA;
@@ -678,24 +666,28 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     a.part_o = reinterpret_cast<float*>(ws + w.o);
     const bool bf16 = p->dtype == DSPARK_BF16;
     int parts = 0;
-    const dspark_status ls = bf16 ? (e4m3 ? launch_rows16_d<true, true>(a, sms, s, &parts)
+    const bool aligned_q = !((uintptr_t)q & 15u) && p->q_token_stride % 8 == 0 && p->q_head_stride % 8 == 0;
+    const bool tc = wide_rows(p) && aligned_q;
+    const dspark_status ls = tc     ? launch_attn_tc(a, bf16, sms, s, &parts)
+                             : bf16 ? (e4m3 ? launch_rows16_d<true, true>(a, sms, s, &parts)
                                           : launch_rows16_d<true, false>(a, sms, s, &parts))
                                   : (e4m3 ? launch_rows16_d<false, true>(a, sms, s, &parts)
                                           : launch_rows16_d<false, false>(a, sms, s, &parts));
     if (ls != DSPARK_OK) return ls;
     note_launch();
+    const int row_tile = tc ? kTcRows : kRows;
     // The join is enqueued while the attention kernel runs (its blocks wait for that kernel's end).
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(parts, kRows / kJoinWarps);
+    cfg.gridDim = dim3(parts, tc ? 8 : kRows / kJoinWarps);
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = bf16 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<true>, a, kRows, parts)
-                               : cudaLaunchKernelEx(&cfg, attn_join_kernel<false>, a, kRows, parts);
+    const cudaError_t e = bf16 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<true>, a, row_tile, parts)
+                               : cudaLaunchKernelEx(&cfg, attn_join_kernel<false>, a, row_tile, parts);
     if (e != cudaSuccess) return DSPARK_ERR_CUDA;
     note_launch();
     return DSPARK_OK;

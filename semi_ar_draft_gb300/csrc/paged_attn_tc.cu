@@ -1,0 +1,607 @@
+// paged_attn_tc.cu -- dspark_paged_attention on the fifth-generation tensor cores: row tiles of 128 for
+// requests whose new tokens give more than 16 rows a kv head (the flattened verify, draft blocks).
+//
+// One persistent CTA a multiprocessor walks its range of units (paged.cuh).  Roles:
+//   loaders (2 warps)    copy the item's queries and, tile by tile, KT keys and values into a ring in
+//                        shared memory, 16 bytes a thread and copy, in the 128-byte-swizzled layout the MMA
+//                        reads; several tiles in flight, across items
+//   MMA (1 thread)       S = Q K^T into tensor memory, and O += P V with P from tensor memory
+//   softmax (4 warps a   thread = row: takes S, writes P (16 bits) back to tensor memory, keeps the row's
+//     stream)            maximum and sum; at an item's end joins the streams and writes the output
+// A unit's key tiles go to kStreams streams in turn, each with its own S, P, O and statistics (heads up to
+// 128): while one stream's softmax runs, the tensor cores have the other's products.  With heads of
+// 256 the output alone takes half of tensor memory, and one stream with tiles of 32 keys is used.
+//
+// Values are the second product's B operand as they lie in the cache (one row a key, so N-major).
+// An output starts at zero, so every product accumulates; it is scaled when a row's maximum has grown by
+// 2^8, which needs the stream's earlier products done, and P's buffer needs that anyway.
+#include "host_util.h"
+#include "paged.cuh"
+#include "tc05.cuh"
+
+namespace dspark {
+namespace {
+
+constexpr int kTcRowTile = 128;
+
+template <int DP>
+struct TcAttn {
+    static constexpr int kStreams = DP == 256 ? 1 : 2;
+    static constexpr int kKt = DP == 256 ? 32 : 64;  // keys of a tile
+    static constexpr int kUnit = kStreams * kKt;
+    static constexpr int kSoftmaxWarps = 4 * kStreams;
+    static constexpr int kLoaders = 2;  // (11 warps: 168 registers a thread; a twelfth and more would leave 128)
+    static constexpr int kWarps = kSoftmaxWarps + kLoaders + 1;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kSub = DP / 64;                  // 64-value groups of a row
+    static constexpr int kTile = kKt * DP * 2;            // bytes of a tile's K (or V)
+    static constexpr int kQ = kTcRowTile * DP * 2;
+    static constexpr int kQBufs = DP == 256 ? 1 : 2;
+    static constexpr int kSlots = DP == 64 ? 10 : (DP == 128 ? 5 : 4);
+    // Tiles that may be in flight unannounced.  The loaders wait for slot t - kSlots before they issue tile
+    // t, and the MMA frees it after the products of kStreams later tiles, which must be announced by then.
+    static constexpr int kDepth = kSlots - 1 - kStreams;
+    static constexpr int kRing = kQBufs * kQ;
+    static constexpr int kMeta = kRing + kSlots * 2 * kTile;
+    static constexpr size_t kSmem = (size_t)kMeta + 2 * kTcRowTile * 8 + 512;
+    // tensor memory columns
+    static constexpr int kColS = kStreams * DP, kColP = kColS + kStreams * kKt;
+    static_assert(kColP + kStreams * kKt / 2 <= 512, "tensor memory");
+    static_assert(kSmem <= kMaxSmem, "shared memory");
+};
+
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr) : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(v)::"memory");
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+// Descriptor of an N-major (values as they lie: N adjacent, one 128-byte row a K index) operand with the
+// 128-byte swizzle: the leading offset goes from one group of 64 N to the next, the stride offset from
+// eight K rows to the next eight.
+__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t lead, uint32_t stride) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lead >> 4) & 0x3FFFu) << 16 |
+           (uint64_t)((stride >> 4) & 0x3FFFu) << 32 | (uint64_t)1u << 46 | (uint64_t)2u << 61;
+}
+// kind::f16 with fp32 accumulation, A and B of one 16-bit type; bit 16: B is N-major.
+template <bool BF16>
+__host__ __device__ constexpr uint32_t idesc16(int M, int N, bool b_mn) {
+    return (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+template <bool BF16>
+__device__ __forceinline__ bool is_odd16(uint32_t half) {  // NaN or inf in the low 16 bits
+    const uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
+    return (half & e) == e;
+}
+template <bool BF16>
+__device__ __forceinline__ float from16(uint32_t half) {
+    return BF16 ? bf16_bits_to_f32(half & 0xffffu) : __half2float(__ushort_as_half((unsigned short)half));
+}
+
+struct TcBars {
+    uint64_t full[10], empty[10], qempty[2], sfull[2], sfree[2], pfull[2], pvdone[2], smeet[2], meet, drain;
+    uint32_t tmem;
+    int abort, status, misaligned;
+    int odd[2][2];
+    AttnScratch scratch;
+};
+static_assert(sizeof(TcBars) <= 512, "barriers");
+
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnArgs a, uint64_t limit_ns) {
+    using C = TcAttn<DP>;
+    constexpr int KT = C::kKt, NS = C::kStreams;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    float2* s_ml = reinterpret_cast<float2*>(smem + C::kMeta);  // [kStreams][128]
+    TcBars* bars = reinterpret_cast<TcBars*>(smem + C::kMeta + 2 * kTcRowTile * 8);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int part = blockIdx.x, parts = gridDim.x;
+    launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(&bars->full[i], C::kLoaders);
+            mbar_init(&bars->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->qempty[i], 1);
+            mbar_init(&bars->sfull[i], 1);
+            mbar_init(&bars->sfree[i], 4);
+            mbar_init(&bars->pfull[i], 4);
+            mbar_init(&bars->pvdone[i], 1);
+            mbar_init(&bars->smeet[i], 4);
+            bars->odd[i][0] = bars->odd[i][1] = 0;
+        }
+        mbar_init(&bars->meet, C::kSoftmaxWarps);
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        // the swizzled tiles need 1024-byte alignment; where it is not given nothing is computed
+        bars->misaligned = (smem_addr(smem) & 1023u) != 0;
+        bars->status = bars->misaligned ? DSPARK_ERR_UNSUPPORTED : 0;
+        mbar_init_fence();
+    }
+    constexpr int kMmaWarp = C::kWarps - 1;
+    if (warp == kMmaWarp) {
+        tmem_alloc(&bars->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    bool bad;
+    AttnStart start = attn_start<C::kThreads>(a, kTcRowTile, C::kUnit, parts, part, 2, &bars->scratch, &bad);  // (barriers inside)
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+    if (bars->misaligned) start.end = start.begin;
+    volatile int* abort = &bars->abort;
+    int32_t* status = &bars->status;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_hint_or_abort(bar, parity, abort, status, limit_ns); };
+    // by a whole warp, with one answer for all lanes
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    attn_tail_rows(a, (size_t)part * C::kThreads + tid, (size_t)parts * C::kThreads);
+    PartItem mine{-1, 0, 0, 0, 0, 0, {0, 0}};
+
+    if (warp >= C::kSoftmaxWarps && warp < kMmaWarp) {
+        // ---------------------------------------------------------------- loaders
+        constexpr int kKeys = KT / C::kLoaders;      // keys of a tile that this warp copies
+        constexpr int kChunks = DP / 8;              // 16-byte groups of a row
+        constexpr int kPer = 32 / kChunks;           // rows a warp copies at a time
+        const int lw = warp - C::kSoftmaxWarps;
+        const int chunk = lane % kChunks;
+        const bool inside = chunk * 8 < a.D;
+        const uint32_t chunk_at = (uint32_t)(chunk >> 3);  // 64-value group
+        const uint32_t base = smem_addr(smem);
+        AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit);
+        int err = 0, tile = 0, told = 0, seg = 0, stream = 0;  // told: tiles announced
+        auto tile_key = [&]() { return (w.kt_first + w.kt) * C::kUnit + stream * KT; };
+        auto fetch_page = [&]() -> int {
+            const int key = tile_key() + lw * kKeys + lane;
+            if (w.done() || lane >= kKeys || key >= w.r.seq) return -1;
+            return __ldg(a.block_table + (size_t)w.j * a.max_blocks + (key >> a.page_shift));
+        };
+        auto signal = [&](int t) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive_local(&bars->full[t % C::kSlots]);
+        };
+        int pid = fetch_page();
+        bool fresh = true, ok = true;
+        while (!w.done()) {
+            const int head = w.item / w.rts;
+            if (stream == 0 && fresh) {
+                fresh = false;
+                const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
+                if (use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1)))) {
+                    // the products that still read it may be waiting for tiles not announced yet
+                    cp_async_wait_group<0>();
+                    for (; told < tile; ++told) signal(told);
+                    if (!warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) {
+                        ok = false;
+                        break;
+                    }
+                }
+                ++seg;
+                const int row0 = (w.item % w.rts) * kTcRowTile;
+                const int rows = min(w.r.n * a.G - row0, kTcRowTile);
+                const uint32_t qbase = base + (uint32_t)qb * C::kQ + chunk_at * (kTcRowTile * 128);
+                for (int r = lw * kPer + lane / kChunks; r < ((rows + 31) & ~31); r += C::kLoaders * kPer) {
+                    const bool real = inside && r < rows;
+                    const int row = row0 + r;
+                    const long long src = real ? (w.r.token0 + row / a.G) * a.q_token +
+                                                     (head * a.G + row % a.G) * a.q_head + chunk * 8
+                                               : 0;
+                    copy16(qbase + sw128_offset(r, chunk & 7), a.q + 2 * src, real);
+                }
+            }
+            const int slot = tile % C::kSlots;
+            if (tile >= C::kSlots && !warp_wait(&bars->empty[slot], (uint32_t)((tile / C::kSlots - 1) & 1))) {
+                ok = false;
+                break;
+            }
+            {
+                const int key = tile_key() + lw * kKeys + lane;
+                const bool live = lane < kKeys && key < w.r.seq;
+                const bool found = live && pid >= 0 && pid < a.num_pages;
+                if (live && !found) err = DSPARK_ERR_CACHE;
+                const long long off =
+                    found ? pid * a.page + (key & ((1 << a.page_shift) - 1)) * a.token + head * a.head : -1;
+                const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + chunk_at * (KT * 128);
+#pragma unroll
+                for (int i = 0; i < kKeys / kPer; ++i) {
+                    const int r = i * kPer + lane / kChunks;
+                    const long long o = __shfl_sync(0xffffffffu, off, r);
+                    const bool real = inside && o >= 0;
+                    const long long src = real ? o + chunk * 16 : 0;
+                    const uint32_t dst = kb + sw128_offset(lw * kKeys + r, chunk & 7);
+                    copy16(dst, a.k_pages + src, real);
+                    copy16(dst + C::kTile, a.v_pages + src, real);
+                }
+            }
+            cp_async_commit();
+            if (told <= tile - C::kDepth) {
+                cp_async_wait_group<C::kDepth>();
+                for (; told <= tile - C::kDepth; ++told) signal(told);
+            }
+            ++tile;
+            if (++stream == NS) {
+                stream = 0;
+                fresh = w.kt + 1 == w.kts;
+                walk_next(a, w, kTcRowTile, C::kUnit);
+            }
+            pid = fetch_page();
+        }
+        cp_async_wait_group<0>();
+        if (ok)
+            for (; told < tile; ++told) signal(told);
+        if (err) bars->status = err;
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------------- MMA issue
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc16<BF16>(kTcRowTile, KT, false);
+            constexpr uint32_t idesc_o = idesc16<BF16>(kTcRowTile, DP, true);
+            const uint32_t base = smem_addr(smem);
+            const uint64_t q_desc = umma_desc_sw128(base, 1024);
+            const uint64_t k_desc = umma_desc_sw128(base + C::kRing, 1024);
+            // (one group of 64 values: the leading offset is not used)
+            const uint64_t v_desc =
+                umma_desc_sw128_mn(base + C::kRing + C::kTile, C::kSub > 1 ? KT * 128 : 1024, 1024);
+            AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit);
+            int tile = 0, seg = 0, unit = 0;
+            int pending[NS];
+#pragma unroll
+            for (int s = 0; s < NS; ++s) pending[s] = -1;
+            bool ok = true;
+            auto values = [&](int s, int n) {  // O_s += P_s V of the stream's n-th tile
+                const int slot = pending[s] % C::kSlots;
+                if (!wait(&bars->pfull[s], (uint32_t)(n & 1))) return false;
+                tc_fence_after();
+                const uint64_t vd = v_desc + (uint64_t)(slot * (2 * C::kTile >> 4));
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k)
+                    umma_bf16_ts(tmem + s * DP, tmem + C::kColP + s * (KT / 2) + 8 * k, vd + (uint64_t)(k * (2048 >> 4)),
+                                 idesc_o, 1u);
+                umma_commit(&bars->empty[slot]);
+                umma_commit(&bars->pvdone[s]);
+                return true;
+            };
+            while (!w.done() && ok) {
+                const int qb = seg % C::kQBufs;
+#pragma unroll
+                for (int s = 0; s < NS; ++s) {
+                    const int slot = tile % C::kSlots;
+                    if (!wait(&bars->full[slot], (uint32_t)((tile / C::kSlots) & 1)) ||
+                        (unit > 0 && !wait(&bars->sfree[s], (uint32_t)((unit - 1) & 1)))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t qd = q_desc + (uint64_t)(qb * (C::kQ >> 4));
+                    const uint64_t kd = k_desc + (uint64_t)(slot * (2 * C::kTile >> 4));
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k)
+                        umma_bf16(tmem + C::kColS + s * KT, qd + (uint64_t)((k >> 2) * (kTcRowTile * 128 >> 4) + 2 * (k & 3)),
+                                  kd + (uint64_t)((k >> 2) * (KT * 128 >> 4) + 2 * (k & 3)), idesc_s, k > 0 ? 1u : 0u);
+                    umma_commit(&bars->sfull[s]);
+                    if (pending[s] >= 0 && !values(s, unit - 1)) {
+                        ok = false;
+                        break;
+                    }
+                    pending[s] = tile++;
+                }
+                if (!ok) break;
+                if (w.kt + 1 == w.kts) {
+                    umma_commit(&bars->qempty[qb]);
+                    ++seg;
+                }
+                ++unit;
+                walk_next(a, w, kTcRowTile, C::kUnit);
+            }
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+                if (ok && pending[s] >= 0) ok = values(s, unit - 1);
+            umma_commit(&bars->drain);  // everything issued has completed before tensor memory is freed
+            mbar_wait_bounded(&bars->drain, 0, status, limit_ns);
+        }
+        __syncwarp();
+    } else if (warp < C::kSoftmaxWarps) {
+        // ---------------------------------------------------------------- softmax
+        const int s = warp >> 2, row = tid & 127, quarter = warp & 3;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const uint32_t ts = tmem + lanes + C::kColS + s * KT, tp = tmem + lanes + C::kColP + s * (KT / 2);
+        const float c = a.scale * kLog2e;
+        const bool plain = a.softcap == 0.f && c > 0.f;
+        uint32_t zero[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) zero[i] = 0u;
+        if (s == 0)
+            for (int i = 0; i < NS * DP; i += 32) tmem_st32(tmem + lanes + i, zero);
+        tmem_wait_st();
+        tc_fence_before();
+        uint32_t meets = 0, smeets = 0;
+        auto meet = [&]() {  // all softmax warps
+            __syncwarp();
+            if (lane == 0) mbar_arrive_local(&bars->meet);
+            return warp_wait(&bars->meet, meets++ & 1);
+        };
+        auto stream_meet = [&]() {  // the stream's
+            __syncwarp();
+            if (lane == 0) mbar_arrive_local(&bars->smeet[s]);
+            return warp_wait(&bars->smeet[s], smeets++ & 1);
+        };
+        AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit);
+        float m = -CUDART_INF_F, l = 0.f;
+        int n = 0, seg_first = 0, row0 = 0, rows = 0, head = 0, see_lo = 0, see_hi = 0, all_lo = 0, all_hi = 0;
+        bool fresh = true, ok = meet();
+        while (ok && !w.done()) {
+            if (fresh) {
+                fresh = false;
+                seg_first = w.kt;
+                head = w.item / w.rts;
+                row0 = (w.item % w.rts) * kTcRowTile;
+                rows = min(w.r.n * a.G - row0, kTcRowTile);
+                const int pos0 = w.r.seq - w.r.n;
+                auto lo_of = [&](int token) { return a.window > 0 ? max(pos0 + token - a.window + 1, 0) : 0; };
+                auto hi_of = [&](int token) { return a.causal ? min(pos0 + token + 1, w.r.seq) : w.r.seq; };
+                all_lo = lo_of((row0 + rows - 1) / a.G);
+                all_hi = hi_of(row0 / a.G);
+                const int token = (row0 + row) / a.G;
+                see_lo = row < rows ? lo_of(token) : 0;
+                see_hi = row < rows ? hi_of(token) : 0;
+                m = -CUDART_INF_F;
+                l = 0.f;
+            }
+            const int key0 = (w.kt_first + w.kt) * C::kUnit + s * KT;
+            const bool edge = key0 < all_lo || key0 + KT > all_hi;  // some row does not see all of the tile
+            const bool live = 32 * quarter < rows;
+            if (!warp_wait(&bars->sfull[s], (uint32_t)(n & 1))) break;
+            tc_fence_after();
+            uint32_t p[KT / 2];
+            float grow = 1.f;
+            if (live) {
+                uint32_t x[KT / 32][32];
+#pragma unroll
+                for (int h = 0; h < KT / 32; ++h) tmem_ld32(ts + 32 * h, x[h]);
+#pragma unroll
+                for (int h = 0; h < KT / 32; ++h) tmem_wait_ld(x[h]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_local(&bars->sfree[s]);
+                float z[KT];
+#pragma unroll
+                for (int i = 0; i < KT; ++i) z[i] = __uint_as_float(x[i >> 5][i & 31]);
+                float f = c;
+                if (!plain) {
+                    f = 1.f;
+                    if (a.softcap > 0.f) {
+                        const float in = a.scale / a.softcap, out = a.softcap * kLog2e;
+#pragma unroll
+                        for (int i = 0; i < KT; ++i) z[i] = attn_tanh(z[i] * in) * out;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < KT; ++i) z[i] *= c;
+                    }
+                }
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < KT; ++i)
+                        if (key0 + i < see_lo || key0 + i >= see_hi) z[i] = -CUDART_INF_F;
+                }
+                float mx = -CUDART_INF_F;
+#pragma unroll
+                for (int i = 0; i < KT; i += 2) mx = fmax3(mx, z[i], z[i + 1]);
+                mx *= f;  // (f > 0)
+                if (mx > m + 8.f) {
+                    if (m != -CUDART_INF_F) grow = ex2(m - mx);  // (else sum and output are still zero)
+                    m = mx;
+                    l *= grow;
+                }
+                const float ref = m == -CUDART_INF_F ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < KT; i += 2) {
+                    const float p0 = ex2(fmaf(z[i], f, -ref)), p1 = ex2(fmaf(z[i + 1], f, -ref));
+                    sum[i & 2] += p0;
+                    sum[(i & 2) + 1] += p1;
+                    p[i / 2] = pack16<BF16>(p0, p1);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive_local(&bars->sfree[s]);
+            }
+            // the stream's earlier products are done: P's buffer is free and O stands still
+            if (n > 0 && !warp_wait(&bars->pvdone[s], (uint32_t)((n - 1) & 1))) break;
+            tc_fence_after();
+            if (live) {
+                if (__any_sync(0xffffffffu, grow != 1.f)) {
+#pragma unroll 1
+                    for (int i = 0; i < DP; i += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tmem + lanes + s * DP + i, o);
+                        tmem_wait_ld(o);
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * grow);
+                        tmem_st32(tmem + lanes + s * DP + i, o);
+                    }
+                }
+                if constexpr (KT == 64)
+                    tmem_st32(tp, p);
+                else
+                    tmem_st16(tp, p);
+                tmem_wait_st();
+            }
+            // A hidden key's value must not reach a row that does not see it, even as 0 x inf: values of an
+            // edge tile that are not finite (never, in a healthy cache) are added by hand to the rows that
+            // see them, and taken out of the tile.
+            if (edge) {
+                const int tile = n * NS + s, slot = tile % C::kSlots;
+                if (!warp_wait(&bars->full[slot], (uint32_t)((tile / C::kSlots) & 1))) break;
+                unsigned char* v = smem + C::kRing + slot * (2 * C::kTile) + C::kTile;
+                bool any = false;
+                for (int i = row; i < C::kTile / 16; i += 128) {
+                    const uint4 y = reinterpret_cast<const uint4*>(v)[i];
+                    any |= is_odd16<BF16>(y.x) | is_odd16<BF16>(y.x >> 16) | is_odd16<BF16>(y.y) | is_odd16<BF16>(y.y >> 16) |
+                           is_odd16<BF16>(y.z) | is_odd16<BF16>(y.z >> 16) | is_odd16<BF16>(y.w) | is_odd16<BF16>(y.w >> 16);
+                }
+                int* odd = &bars->odd[s][n & 1];  // (cleared before the tile after next can set it)
+                if (any) *odd = 1;
+                if (!stream_meet()) break;
+                const bool found = *reinterpret_cast<volatile int*>(odd) != 0;
+                if (found) {
+                    for (int k = 0; k < KT; ++k) {
+                        uint32_t pk = 0;
+                        if (live) tmem_ld1(tp + (k >> 1), pk);
+                        const float pv = from16<BF16>((k & 1) ? pk >> 16 : pk);
+                        const bool see = key0 + k >= see_lo && key0 + k < see_hi;
+                        for (int d = 0; d < DP; ++d) {
+                            const uint32_t bits = *reinterpret_cast<const uint16_t*>(
+                                v + (d >> 6) * (KT * 128) + sw128_offset(k, (d & 63) >> 3) + 2 * (d & 7));
+                            if (live && is_odd16<BF16>(bits)) {
+                                uint32_t o;
+                                tmem_ld1(tmem + lanes + s * DP + d, o);
+                                if (see) o = __float_as_uint(fmaf(pv, from16<BF16>(bits), __uint_as_float(o)));
+                                tmem_st1(tmem + lanes + s * DP + d, o);
+                                tmem_wait_st();
+                            }
+                        }
+                    }
+                    if (!stream_meet()) break;
+                    for (int i = row; i < C::kTile / 2; i += 128) {
+                        uint16_t* y = reinterpret_cast<uint16_t*>(v) + i;
+                        if (is_odd16<BF16>(*y)) *y = 0;
+                    }
+                    if (row == 0) *odd = 0;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_local(&bars->pfull[s]);
+
+            const bool last_of_item = w.kt + 1 == w.kts;
+            if (last_of_item || w.left == 1) {
+                // ---- the streams' parts of the segment meet: WG s takes the s-th half of the columns
+                bool done = true;
+#pragma unroll
+                for (int q = 0; q < NS; ++q) done = done && warp_wait(&bars->pvdone[q], (uint32_t)(n & 1));
+                if (!done) break;
+                tc_fence_after();
+                s_ml[s * kTcRowTile + row] = make_float2(m, l);
+                if (!meet()) break;
+                float f[NS], mm = -CUDART_INF_F, ll = 0.f;
+#pragma unroll
+                for (int q = 0; q < NS; ++q) mm = fmaxf(mm, s_ml[q * kTcRowTile + row].x);
+                const float ref = mm == -CUDART_INF_F ? 0.f : mm;
+#pragma unroll
+                for (int q = 0; q < NS; ++q) {
+                    const float2 ml = s_ml[q * kTcRowTile + row];
+                    f[q] = ml.y == 0.f ? 0.f : ex2(ml.x - ref);
+                    ll = fmaf(ml.y, f[q], ll);
+                }
+                const bool whole = last_of_item && seg_first == 0;
+                const size_t slot = 2 * (size_t)part + (seg_first == 0 ? kHead : kTail);
+                const float inv = !whole ? 1.f : (ll == 0.f ? 0.f : 1.f / ll);
+                const long long at = attn_out_row(a, w.r.token0, head, row0 + row);
+                if (live) {
+#pragma unroll 1
+                    for (int i = s * (DP / NS); i < (s + 1) * (DP / NS); i += 32) {
+                        float v[32];
+#pragma unroll
+                        for (int q = 0; q < NS; ++q) {
+                            uint32_t o[32];
+                            tmem_ld32(tmem + lanes + q * DP + i, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float y = __uint_as_float(o[e]);
+                                v[e] = q == 0 ? y * f[0] : fmaf(y, f[q], v[e]);
+                            }
+                            tmem_st32(tmem + lanes + q * DP + i, zero);
+                        }
+                        if (row < rows) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                if (i + e >= a.D) continue;
+                                if (whole) {
+                                    uint4 y;
+                                    y.x = pack16<BF16>(v[e] * inv, v[e + 1] * inv);
+                                    y.y = pack16<BF16>(v[e + 2] * inv, v[e + 3] * inv);
+                                    y.z = pack16<BF16>(v[e + 4] * inv, v[e + 5] * inv);
+                                    y.w = pack16<BF16>(v[e + 6] * inv, v[e + 7] * inv);
+                                    *reinterpret_cast<uint4*>(a.out + ((size_t)at * a.D + i + e) * 2) = y;
+                                } else {
+                                    float4* dst = reinterpret_cast<float4*>(
+                                        a.part_o + (slot * kTcRowTile + row) * a.D + i + e);
+                                    dst[0] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                                    dst[1] = make_float4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
+                                }
+                            }
+                        }
+                    }
+                } else {  // rows of nobody have gathered whatever lay in P
+                    for (int i = s * (DP / NS); i < (s + 1) * (DP / NS); i += 32)
+#pragma unroll
+                        for (int q = 0; q < NS; ++q) tmem_st32(tmem + lanes + q * DP + i, zero);
+                }
+                tmem_wait_st();
+                if (s == 0 && row < rows) {
+                    if (!whole)
+                        a.part_ml[slot * kTcRowTile + row] = make_float2(mm, ll);
+                    else if (a.lse)
+                        a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll)) * kLn2;
+                }
+                if (!last_of_item && seg_first == 0) {  // the item ends in the block that holds its last unit
+                    mine.last = (int)((start.end + (w.kts - 1 - w.kt) - 1) / start.per);
+                    mine.row0 = row0;
+                    mine.rows = rows;
+                    mine.token0 = w.r.token0;
+                    mine.head = head;
+                }
+                tc_fence_before();
+                if (!meet()) break;  // the outputs are zero again, and the statistics have been read
+                tc_fence_after();
+                fresh = true;
+            }
+            ++n;
+            walk_next(a, w, kTcRowTile, C::kUnit);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    if (tid == 0) {
+        mine.err = bars->status ? bars->status : (bad ? DSPARK_ERR_CACHE : 0);
+        a.items[part] = mine;
+    }
+}
+
+template <bool BF16, int DP>
+dspark_status launch_tc(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
+    using C = TcAttn<DP>;
+    int per_sm = 0;
+    auto fn = attn_tc_kernel<BF16, DP>;
+    if (prepare_kernel((const void*)fn, C::kSmem, C::kThreads, &per_sm) != cudaSuccess || per_sm < 1)
+        return DSPARK_ERR_CUDA;
+    const int n = sms < kMaxTcParts ? sms : kMaxTcParts;
+    fn<<<n, C::kThreads, C::kSmem, s>>>(a, wait_limit_ns());
+    *parts = n;
+    return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+}  // namespace
+
+dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int sms, cudaStream_t s, int* parts) {
+    if (a.D <= 64) return bf16 ? launch_tc<true, 64>(a, sms, s, parts) : launch_tc<false, 64>(a, sms, s, parts);
+    if (a.D <= 128) return bf16 ? launch_tc<true, 128>(a, sms, s, parts) : launch_tc<false, 128>(a, sms, s, parts);
+    return bf16 ? launch_tc<true, 256>(a, sms, s, parts) : launch_tc<false, 256>(a, sms, s, parts);
+}
+
+}  // namespace dspark

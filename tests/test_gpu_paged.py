@@ -250,11 +250,12 @@ def test_one_token(dtype, cache, Hq, Hk, D, page):
 @pytest.mark.parametrize("dtype,cache", TYPES)
 @pytest.mark.parametrize("Hq,Hk,D,page", [(4, 4, 64, 16), (8, 2, 128, 16), (16, 2, 128, 64), (8, 1, 256, 32), (7, 1, 96, 4)])
 @pytest.mark.parametrize("causal", [True, False])
-def test_several_tokens(dtype, cache, Hq, Hk, D, page, causal):
+@pytest.mark.parametrize("max_new", [1, 33])  # what chooses between row tiles of 16 and of 128
+def test_several_tokens(dtype, cache, Hq, Hk, D, page, causal, max_new):
     news = [1, 17, 0, 5, 9, 2, 33]
     lens = [1, 17, 0, 70, 129, 300, 40]
     c, lens, offsets = make_case(lens, news, Hq, Hk, D, page, dtype, cache, 3 * D + page, pad=3)
-    out, lse = check(c, lens, offsets, causal=causal)
+    out, lse = check(c, lens, offsets, causal=causal, max_new=max_new)
     assert not out[offsets[-1]:].any() and bool((lse[offsets[-1]:] == -math.inf).all())
 
 
@@ -262,43 +263,49 @@ def test_several_tokens(dtype, cache, Hq, Hk, D, page, causal):
 @pytest.mark.parametrize("softcap", [0.0, 5.0])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("cache", [torch.bfloat16, E4M3])
-def test_window_and_softcap(window, softcap, causal, cache):
+@pytest.mark.parametrize("max_new", [1, 17])
+def test_window_and_softcap(window, softcap, causal, cache, max_new):
     news, lens = [1, 9, 4, 17], [500, 9, 130, 201]
     c, lens, offsets = make_case(lens, news, 8, 2, 128, 16, torch.bfloat16, cache, window)
-    check(c, lens, offsets, causal=causal, window=window, softcap=softcap)
+    check(c, lens, offsets, causal=causal, window=window, softcap=softcap, max_new=max_new)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
-def test_other_scales(scale):
+@pytest.mark.parametrize("max_new", [1, 17])
+def test_other_scales(scale, max_new):
     c, lens, offsets = make_case([200, 9], [3, 2], 4, 1, 64, 16, torch.float16, torch.float16, 1)
-    check(c, lens, offsets, scale=scale)
+    check(c, lens, offsets, scale=scale, max_new=max_new)
 
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
 @pytest.mark.parametrize("lens,news,Hq,Hk,D", [([20000], [1], 8, 1, 128), ([9000, 1, 5000], [1, 1, 4], 4, 1, 256),
-                                               ([33, 12000, 700], [2, 17, 3], 8, 2, 64)])
-def test_long_caches_are_split_and_joined(dtype, cache, lens, news, Hq, Hk, D):
+                                               ([33, 12000, 700], [2, 17, 3], 8, 2, 64), ([15000, 2000], [9, 1], 16, 1, 128)])
+@pytest.mark.parametrize("max_new", [1, 17])
+def test_long_caches_are_split_and_joined(dtype, cache, lens, news, Hq, Hk, D, max_new):
     c, lens, offsets = make_case(lens, news, Hq, Hk, D, 64, dtype, cache, sum(lens))
-    out, lse = check(c, lens, offsets)
-    again, lse2, _ = attend(c)
+    out, lse = check(c, lens, offsets, max_new=max_new)
+    again, lse2, _ = attend(c, max_new=max_new)
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
-def test_many_requests():
+@pytest.mark.parametrize("max_new", [1, 40])
+def test_many_requests(max_new):
     g = torch.Generator().manual_seed(3)
     news = torch.randint(0, 4, (900,), generator=g).tolist()
     lens = [n + int(x) for n, x in zip(news, torch.randint(0, 60, (900,), generator=g))]
     c, lens, offsets = make_case(lens, news, 2, 1, 64, 16, torch.bfloat16, torch.bfloat16, 8)
-    check(c, lens, offsets)
+    check(c, lens, offsets, max_new=max_new)
 
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
 @pytest.mark.parametrize("Hq,Hk", [(4, 1), (8, 2), (16, 1)])
-def test_what_is_not_seen_does_not_matter(dtype, cache, Hq, Hk):
+@pytest.mark.parametrize("max_new", [1, 17])
+def test_what_is_not_seen_does_not_matter(dtype, cache, Hq, Hk, max_new):
     """NaN and inf in later tokens, before the window, past a request's length and in pages of nobody."""
     D, page, news, lens = 128, 16, [9, 1, 5], [100, 37, 200]
     c, lens, offsets = make_case(lens, news, Hq, Hk, D, page, dtype, cache, 77)
     for kw in ({"causal": True}, {"causal": True, "window": 20}, {"causal": False, "window": 30}):
+        kw["max_new"] = max_new
         ref, ref_lse, _ = attend(c, **kw)
         bad = {**c, "k_pages": c["k_pages"].clone(), "v_pages": c["v_pages"].clone()}
         owned = torch.zeros(bad["k_pages"].shape[:2], dtype=torch.bool, device="cuda")
@@ -335,40 +342,44 @@ def test_what_is_not_seen_does_not_matter(dtype, cache, Hq, Hk):
                 assert not bool(out[offsets[j + 1] - 1].isfinite().all())
 
 
-def test_values_that_are_seen_go_through():
+@pytest.mark.parametrize("max_new", [1, 17])
+def test_values_that_are_seen_go_through(max_new):
     """A NaN or an infinite value that a row sees reaches it, and only it."""
     c, lens, offsets = make_case([50, 60], [3, 2], 2, 1, 64, 16, torch.bfloat16, torch.bfloat16, 4)
-    ref, _, _ = attend(c)
+    ref, _, _ = attend(c, max_new=max_new)
     c["v_pages"][c["block_table"][0, 2].long(), 15, 0, 5] = float("nan")  # request 0, position 47: its first new token
     c["v_pages"][c["block_table"][1, 3].long(), 11, 0, 6] = float("inf")  # request 1, position 59: its last
-    out, _, _ = attend(c)
+    out, _, _ = attend(c, max_new=max_new)
     assert bool(out[0:3, :, 5].isnan().all()) and bool((out[4, :, 6] == math.inf).all())
     out[0:3, :, 5] = ref[0:3, :, 5]
     out[4, :, 6] = ref[4, :, 6]
     assert bool(((out - ref).abs() <= 8 * 2.0 ** -8 * 4).all())
 
 
-def test_rows_that_see_nothing():
+@pytest.mark.parametrize("max_new", [1, 17])
+def test_rows_that_see_nothing(max_new):
     """More new tokens than the cache holds: the first rows stand before position 0."""
     c, lens, offsets = make_case([4, 1, 0], [4, 3, 2], 4, 2, 64, 16, torch.float16, torch.float16, 2)
     for window in (0, 3):
-        out, lse, ws = attend(c, window=window)
+        out, lse, ws = attend(c, window=window, max_new=max_new)
         assert not out[4:6].any() and bool((lse[4:6] == -math.inf).all()) and not out[7:].any()
         assert bool((lse[6].isfinite()).all()) and status(ws) == 0
-        check(c, lens, offsets, window=window)
+        check(c, lens, offsets, window=window, max_new=max_new)
 
 
 @pytest.mark.parametrize("q_shift", [1, 2, 8])
 @pytest.mark.parametrize("heads_first", [False, True])
 @pytest.mark.parametrize("cache", [torch.bfloat16, E4M3])
-def test_strides_and_alignment(q_shift, heads_first, cache):
+@pytest.mark.parametrize("max_new", [1, 17])
+def test_strides_and_alignment(q_shift, heads_first, cache, max_new):
     c, lens, offsets = make_case([33, 100, 7], [2, 9, 1], 6, 2, 128, 16, torch.bfloat16, cache, 6, heads_first=heads_first,
                                  q_shift=q_shift)
-    check(c, lens, offsets)
+    check(c, lens, offsets, max_new=max_new)
 
 
 @pytest.mark.parametrize("cache", [torch.bfloat16, E4M3])
-def test_pools_past_4_gib(cache):
+@pytest.mark.parametrize("max_new", [1, 10])
+def test_pools_past_4_gib(cache, max_new):
     """Pages whose byte offsets pass 32 bits."""
     page, Hk, D, P = 64, 8, 128, 70000 if cache == torch.bfloat16 else 140000
     kp, vp = (torch.empty((P, page, Hk, D), dtype=cache, device="cuda") for _ in range(2))
@@ -381,24 +392,26 @@ def test_pools_past_4_gib(cache):
     q = torch.randn((T, 16, D), generator=g, device="cuda").to(torch.bfloat16)
     c = {"q": q, "k_pages": kp, "v_pages": vp, "block_table": i32([use]), "seq_len": i32([200]), "offsets": i32([0, T]),
          "k_scale": None, "v_scale": None}
-    check(c, [200], [0, T])
+    check(c, [200], [0, T], max_new=max_new)
 
 
-def test_large_scores_and_queries():
+@pytest.mark.parametrize("max_new", [1, 17])
+def test_large_scores_and_queries(max_new):
     """Scores far apart, and bf16 queries beyond the halves' range over an 8-bit cache."""
     for cache in (torch.bfloat16, E4M3):
         c, lens, offsets = make_case([300, 40], [2, 3], 4, 1, 128, 16, torch.bfloat16, cache, 11)
         c["q"].mul_(20.0)
-        check(c, lens, offsets)
+        check(c, lens, offsets, max_new=max_new)
         c["q"].mul_(2.0 ** 60)
-        check(c, lens, offsets, scale=2.0 ** -63)
+        check(c, lens, offsets, scale=2.0 ** -63, max_new=max_new)
         c["q"].mul_(2.0 ** -160)
-        check(c, lens, offsets, scale=2.0 ** 97)
+        check(c, lens, offsets, scale=2.0 ** 97, max_new=max_new)
 
 
-def test_bad_tables_are_reported():
+@pytest.mark.parametrize("max_new", [1, 17])
+def test_bad_tables_are_reported(max_new):
     c, lens, offsets = make_case([40, 50], [1, 1], 4, 1, 64, 16, torch.bfloat16, torch.bfloat16, 9)
-    ref, _, _ = attend(c)
+    ref, _, _ = attend(c, max_new=max_new)
     for what in ("page", "negative", "long", "offsets"):
         d = {**c, "block_table": c["block_table"].clone(), "seq_len": c["seq_len"].clone(), "offsets": c["offsets"].clone()}
         if what == "page":
@@ -409,36 +422,37 @@ def test_bad_tables_are_reported():
             d["seq_len"][0] = 1 << 30
         if what == "offsets":
             d["offsets"][0] = -5
-        out, _, ws = attend(d)
+        out, _, ws = attend(d, max_new=max_new)
         assert status(ws) == 8, what
         assert torch.equal(out[1], ref[1])
-        _, _, ws = attend(c)
+        _, _, ws = attend(c, max_new=max_new)
         assert status(ws) == 0
 
 
-def test_other_stream_and_graph():
+@pytest.mark.parametrize("max_new", [1, 5])
+def test_other_stream_and_graph(max_new):
     """On a side stream, and replayed from a graph after the lengths changed."""
     c, lens, offsets = make_case([700, 200, 64], [1, 5, 2], 8, 2, 128, 16, torch.bfloat16, torch.bfloat16, 12)
-    ref, ref_lse, _ = attend(c)
+    ref, ref_lse, _ = attend(c, max_new=max_new)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        out, lse, _ = attend(c)
+        out, lse, _ = attend(c, max_new=max_new)
     side.synchronize()
     assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
     out = torch.zeros_like(ref)
     ws = torch.empty(api.b.dspark_paged_attention_workspace_size(api.b.AttentionParams(
-        8, 3, 8, 2, 128, 16, 100, 50, 0, api.b.BF16, api.b.BF16, 1, 0, 1.0, 0.0, 1, 1, 8, 8, 8)), dtype=torch.uint8, device="cuda")
+        8, 3, 8, 2, 128, 16, 100, 50, max_new, api.b.BF16, api.b.BF16, 1, 0, 1.0, 0.0, 1, 1, 8, 8, 8)), dtype=torch.uint8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        attend(c, out=out, ws=ws)
+        attend(c, out=out, ws=ws, max_new=max_new)
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, ref)
     c["seq_len"].copy_(i32([333, 150, 2]))
     graph.replay()
     torch.cuda.synchronize()
-    want, _, _ = attend(c)
+    want, _, _ = attend(c, max_new=max_new)
     assert torch.equal(out, want) and not torch.equal(out, ref)
 
 
