@@ -2,7 +2,7 @@
 // requests whose new tokens give more than 16 rows a kv head (the flattened verify, draft blocks).
 //
 // One persistent CTA a multiprocessor walks its range of units (paged.cuh).  Roles:
-//   loaders (2 warps)    copy the item's queries and, tile by tile, KT keys and values into a ring in
+//   loaders (3 warps)    copy the item's queries and, tile by tile, KT keys and values into a ring in
 //                        shared memory, 16 bytes a thread and copy, in the 128-byte-swizzled layout the MMA
 //                        reads; several tiles in flight, across items
 //   MMA (1 thread)       S = Q K^T into tensor memory, and O += P V with P from tensor memory
@@ -30,7 +30,7 @@ struct TcAttn {
     static constexpr int kKt = DP == 256 ? 32 : 64;  // keys of a tile
     static constexpr int kUnit = kStreams * kKt;
     static constexpr int kSoftmaxWarps = 4 * kStreams;
-    static constexpr int kLoaders = 2;  // (11 warps: 168 registers a thread; a twelfth and more would leave 128)
+    static constexpr int kLoaders = 3;  // (12 warps: 168 registers a thread; a thirteenth would leave 128)
     static constexpr int kWarps = kSoftmaxWarps + kLoaders + 1;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSub = DP / 64;                  // 64-value groups of a row
@@ -38,9 +38,6 @@ struct TcAttn {
     static constexpr int kQ = kTcRowTile * DP * 2;
     static constexpr int kQBufs = DP == 256 ? 1 : 2;
     static constexpr int kSlots = DP == 64 ? 10 : (DP == 128 ? 5 : 4);
-    // Tiles that may be in flight unannounced.  The loaders wait for slot t - kSlots before they issue tile
-    // t, and the MMA frees it after the products of kStreams later tiles, which must be announced by then.
-    static constexpr int kDepth = kSlots - 1 - kStreams;
     static constexpr int kRing = kQBufs * kQ;
     static constexpr int kMeta = kRing + kSlots * 2 * kTile;
     static constexpr size_t kSmem = (size_t)kMeta + 2 * kTcRowTile * 8 + 512;
@@ -87,6 +84,11 @@ __device__ __forceinline__ float from16(uint32_t half) {
     return BF16 ? bf16_bits_to_f32(half & 0xffffu) : __half2float(__ushort_as_half((unsigned short)half));
 }
 
+// One arrival on `bar` (counted in its expected arrivals) once this thread's copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 struct TcBars {
     uint64_t full[10], empty[10], qempty[2], sfull[2], sfree[2], pfull[2], pvdone[2], smeet[2], meet, drain;
     uint32_t tmem;
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
     launch_dependents();
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(&bars->full[i], C::kLoaders);
+            mbar_init(&bars->full[i], 32 * C::kLoaders);
             mbar_init(&bars->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -150,48 +152,46 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
 
     if (warp >= C::kSoftmaxWarps && warp < kMmaWarp) {
         // ---------------------------------------------------------------- loaders
-        constexpr int kKeys = KT / C::kLoaders;      // keys of a tile that this warp copies
         constexpr int kChunks = DP / 8;              // 16-byte groups of a row
         constexpr int kPer = 32 / kChunks;           // rows a warp copies at a time
         const int lw = warp - C::kSoftmaxWarps;
-        const int chunk = lane % kChunks;
+        const int chunk = lane % kChunks, sub_row = lane / kChunks;
         const bool inside = chunk * 8 < a.D;
         const uint32_t chunk_at = (uint32_t)(chunk >> 3);  // 64-value group
         const uint32_t base = smem_addr(smem);
+        const int mask = (1 << a.page_shift) - 1;
         AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit);
-        int err = 0, tile = 0, told = 0, seg = 0, stream = 0;  // told: tiles announced
+        int err = 0, tile = 0, seg = 0, stream = 0;
         auto tile_key = [&]() { return (w.kt_first + w.kt) * C::kUnit + stream * KT; };
-        auto fetch_page = [&]() -> int {
-            const int key = tile_key() + lw * kKeys + lane;
-            if (w.done() || lane >= kKeys || key >= w.r.seq) return -1;
-            return __ldg(a.block_table + (size_t)w.j * a.max_blocks + (key >> a.page_shift));
-        };
-        auto signal = [&](int t) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive_local(&bars->full[t % C::kSlots]);
-        };
-        int pid = fetch_page();
-        bool fresh = true, ok = true;
-        while (!w.done()) {
-            const int head = w.item / w.rts;
-            if (stream == 0 && fresh) {
-                fresh = false;
-                const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
-                if (use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1)))) {
-                    // the products that still read it may be waiting for tiles not announced yet
-                    cp_async_wait_group<0>();
-                    for (; told < tile; ++told) signal(told);
-                    if (!warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) {
-                        ok = false;
-                        break;
+        // Pages of the next tile's keys (lane: keys lane and lane + 32), fetched a tile ahead; -1: no key.
+        int pid[KT / 32];
+        auto fetch_pages = [&]() {
+#pragma unroll
+            for (int h = 0; h < KT / 32; ++h) {
+                const int key = tile_key() + 32 * h + lane;
+                pid[h] = -1;
+                if (!w.done() && key < w.r.seq) {
+                    pid[h] = __ldg(a.block_table + (size_t)w.j * a.max_blocks + (key >> a.page_shift));
+                    if (pid[h] < 0 || pid[h] >= a.num_pages) {
+                        pid[h] = -1;
+                        err = DSPARK_ERR_CACHE;
                     }
                 }
+            }
+        };
+        fetch_pages();
+        bool fresh = true;
+        while (!w.done()) {
+            const int head = w.item / w.rts;
+            if (fresh) {
+                fresh = false;
+                const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
+                if (use > 0 && !warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) break;
                 ++seg;
                 const int row0 = (w.item % w.rts) * kTcRowTile;
                 const int rows = min(w.r.n * a.G - row0, kTcRowTile);
                 const uint32_t qbase = base + (uint32_t)qb * C::kQ + chunk_at * (kTcRowTile * 128);
-                for (int r = lw * kPer + lane / kChunks; r < ((rows + 31) & ~31); r += C::kLoaders * kPer) {
+                for (int r = lw * kPer + sub_row; r < ((rows + 31) & ~31); r += C::kLoaders * kPer) {
                     const bool real = inside && r < rows;
                     const int row = row0 + r;
                     const long long src = real ? (w.r.token0 + row / a.G) * a.q_token +
@@ -201,45 +201,34 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 }
             }
             const int slot = tile % C::kSlots;
-            if (tile >= C::kSlots && !warp_wait(&bars->empty[slot], (uint32_t)((tile / C::kSlots - 1) & 1))) {
-                ok = false;
-                break;
-            }
+            if (tile >= C::kSlots && !warp_wait(&bars->empty[slot], (uint32_t)((tile / C::kSlots - 1) & 1))) break;
             {
-                const int key = tile_key() + lw * kKeys + lane;
-                const bool live = lane < kKeys && key < w.r.seq;
-                const bool found = live && pid >= 0 && pid < a.num_pages;
-                if (live && !found) err = DSPARK_ERR_CACHE;
-                const long long off =
-                    found ? pid * a.page + (key & ((1 << a.page_shift) - 1)) * a.token + head * a.head : -1;
+                const int key0 = tile_key();
+                const long long head_at = head * a.head + chunk * 16;
                 const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + chunk_at * (KT * 128);
-#pragma unroll
-                for (int i = 0; i < kKeys / kPer; ++i) {
-                    const int r = i * kPer + lane / kChunks;
-                    const long long o = __shfl_sync(0xffffffffu, off, r);
-                    const bool real = inside && o >= 0;
-                    const long long src = real ? o + chunk * 16 : 0;
-                    const uint32_t dst = kb + sw128_offset(lw * kKeys + r, chunk & 7);
+#pragma unroll 4
+                for (int i = lw; i < KT / kPer; i += C::kLoaders) {
+                    const int r = i * kPer + sub_row;  // (32 rows are a whole number of steps)
+                    const int p = __shfl_sync(0xffffffffu, KT > 32 && i * kPer >= 32 ? pid[KT / 32 - 1] : pid[0], r & 31);
+                    const bool real = inside && p >= 0;
+                    const long long src = real ? p * a.page + ((key0 + r) & mask) * a.token + head_at : 0;
+                    const uint32_t dst = kb + sw128_offset(r, chunk & 7);
                     copy16(dst, a.k_pages + src, real);
                     copy16(dst + C::kTile, a.v_pages + src, real);
                 }
             }
-            cp_async_commit();
-            if (told <= tile - C::kDepth) {
-                cp_async_wait_group<C::kDepth>();
-                for (; told <= tile - C::kDepth; ++told) signal(told);
-            }
+            // The slot is full once every loader thread's copies so far have landed (its queries among
+            // them); nobody waits for that here, so the whole ring can be in flight.
+            copy_arrive(&bars->full[slot]);
             ++tile;
             if (++stream == NS) {
                 stream = 0;
                 fresh = w.kt + 1 == w.kts;
                 walk_next(a, w, kTcRowTile, C::kUnit);
             }
-            pid = fetch_page();
+            fetch_pages();
         }
-        cp_async_wait_group<0>();
-        if (ok)
-            for (; told < tile; ++told) signal(told);
+        asm volatile("cp.async.wait_all;" ::: "memory");
         if (err) bars->status = err;
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA issue
@@ -281,6 +270,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                         ok = false;
                         break;
                     }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the loaders' copies, to the MMA
                     tc_fence_after();
                     const uint64_t qd = q_desc + (uint64_t)(qb * (C::kQ >> 4));
                     const uint64_t kd = k_desc + (uint64_t)(slot * (2 * C::kTile >> 4));
@@ -393,10 +383,14 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                     for (int i = 0; i < KT; ++i)
                         if (key0 + i < see_lo || key0 + i >= see_hi) z[i] = -CUDART_INF_F;
                 }
-                float mx = -CUDART_INF_F;
+                float mx4[4];
 #pragma unroll
-                for (int i = 0; i < KT; i += 2) mx = fmax3(mx, z[i], z[i + 1]);
-                mx *= f;  // (f > 0)
+                for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(z[i], z[4 + i]);
+#pragma unroll
+                for (int i = 8; i < KT; i += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) mx4[q] = fmax3(mx4[q], z[i + q], z[i + 4 + q]);
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * f;  // (f > 0)
                 if (mx > m + 8.f) {
                     if (m != -CUDART_INF_F) grow = ex2(m - mx);  // (else sum and output are still zero)
                     m = mx;
