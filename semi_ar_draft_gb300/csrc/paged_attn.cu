@@ -627,6 +627,8 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
         return DSPARK_ERR_INVALID_ARG;
     const AttnWs w = attn_ws(p);
     if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < w.bytes) return DSPARK_ERR_WORKSPACE;
+    for (const long long x : {p->kv_page_stride, p->kv_token_stride, p->kv_head_stride})  // 32 bits of 16 bytes
+        if (x < 0 || x * esz / 16 > INT32_MAX) return DSPARK_ERR_INVALID_ARG;
     int sms = 0;
     if (device_sm_count(&sms) != cudaSuccess) return DSPARK_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -84,6 +84,33 @@ __device__ __forceinline__ float from16(uint32_t half) {
     return BF16 ? bf16_bits_to_f32(half & 0xffffu) : __half2float(__ushort_as_half((unsigned short)half));
 }
 
+// MMAs and commits by one elected lane of a converged warp (always the same one).  Descriptors come in
+// halves; kind::f16, fp32 accumulation; accumulate = 0 overwrites D.
+__device__ __forceinline__ void mma_elect_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 x, y;\n mov.b64 x, {%1, %2};\n mov.b64 y, {%3, %4};\n"
+        " setp.ne.b32 p, %6, 0;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_elect_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 y;\n mov.b64 y, {%2, %3};\n"
+        " setp.ne.b32 p, %5, 0;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void commit_elect(uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_addr(bar))
+        : "memory");
+}
+
 // One arrival on `bar` (counted in its expected arrivals) once this thread's copies so far have landed.
 __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -159,24 +186,23 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         const bool inside = chunk * 8 < a.D;
         const uint32_t chunk_at = (uint32_t)(chunk >> 3);  // 64-value group
         const uint32_t base = smem_addr(smem);
-        const int mask = (1 << a.page_shift) - 1;
+        const uint32_t mask = (1u << a.page_shift) - 1;
+        const uint32_t page16 = (uint32_t)(a.page >> 4), token16 = (uint32_t)(a.token >> 4);
+        const unsigned char* k_at = a.k_pages + chunk * 16;
+        const long long v_after_k = a.v_pages - a.k_pages;
         AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit);
         int err = 0, tile = 0, seg = 0, stream = 0;
         auto tile_key = [&]() { return (w.kt_first + w.kt) * C::kUnit + stream * KT; };
-        // Pages of the next tile's keys (lane: keys lane and lane + 32), fetched a tile ahead; -1: no key.
+        // Pages of the next tile's keys (lane: keys lane and lane + 32), asked for a tile ahead; kNone: no key.
+        constexpr int kNone = INT32_MIN;
         int pid[KT / 32];
         auto fetch_pages = [&]() {
 #pragma unroll
             for (int h = 0; h < KT / 32; ++h) {
                 const int key = tile_key() + 32 * h + lane;
-                pid[h] = -1;
-                if (!w.done() && key < w.r.seq) {
+                pid[h] = kNone;
+                if (!w.done() && key < w.r.seq)
                     pid[h] = __ldg(a.block_table + (size_t)w.j * a.max_blocks + (key >> a.page_shift));
-                    if (pid[h] < 0 || pid[h] >= a.num_pages) {
-                        pid[h] = -1;
-                        err = DSPARK_ERR_CACHE;
-                    }
-                }
             }
         };
         fetch_pages();
@@ -203,18 +229,27 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
             const int slot = tile % C::kSlots;
             if (tile >= C::kSlots && !warp_wait(&bars->empty[slot], (uint32_t)((tile / C::kSlots - 1) & 1))) break;
             {
-                const int key0 = tile_key();
-                const long long head_at = head * a.head + chunk * 16;
+                const uint32_t key0 = (uint32_t)tile_key();
+                const unsigned char* head_at = k_at + head * a.head;
                 const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + chunk_at * (KT * 128);
-#pragma unroll 4
-                for (int i = lw; i < KT / kPer; i += C::kLoaders) {
+#pragma unroll
+                for (int h = 0; h < KT / 32; ++h) {
+                    const bool out = (uint32_t)pid[h] >= (uint32_t)a.num_pages;
+                    if (out && pid[h] != kNone) err = DSPARK_ERR_CACHE;
+                    if (out) pid[h] = -1;
+                }
+#pragma unroll
+                for (int u = 0; u < (KT / kPer + C::kLoaders - 1) / C::kLoaders; ++u) {
+                    const int i = u * C::kLoaders + lw;
+                    if ((u + 1) * C::kLoaders > KT / kPer && i >= KT / kPer) break;
                     const int r = i * kPer + sub_row;  // (32 rows are a whole number of steps)
                     const int p = __shfl_sync(0xffffffffu, KT > 32 && i * kPer >= 32 ? pid[KT / 32 - 1] : pid[0], r & 31);
                     const bool real = inside && p >= 0;
-                    const long long src = real ? p * a.page + ((key0 + r) & mask) * a.token + head_at : 0;
+                    const uint64_t at16 = (uint64_t)(uint32_t)max(p, 0) * page16 + (uint64_t)((key0 + r) & mask) * token16;
+                    const unsigned char* src = real ? head_at + 16 * at16 : a.k_pages;
                     const uint32_t dst = kb + sw128_offset(r, chunk & 7);
-                    copy16(dst, a.k_pages + src, real);
-                    copy16(dst + C::kTile, a.v_pages + src, real);
+                    copy16(dst, src, real);
+                    copy16(dst + C::kTile, src + v_after_k, real);
                 }
             }
             // The slot is full once every loader thread's copies so far have landed (its queries among
@@ -232,73 +267,74 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         if (err) bars->status = err;
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA issue
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = idesc16<BF16>(kTcRowTile, KT, false);
-            constexpr uint32_t idesc_o = idesc16<BF16>(kTcRowTile, DP, true);
-            const uint32_t base = smem_addr(smem);
-            const uint64_t q_desc = umma_desc_sw128(base, 1024);
-            const uint64_t k_desc = umma_desc_sw128(base + C::kRing, 1024);
-            // (one group of 64 values: the leading offset is not used)
-            const uint64_t v_desc =
-                umma_desc_sw128_mn(base + C::kRing + C::kTile, C::kSub > 1 ? KT * 128 : 1024, 1024);
-            AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit);
-            int tile = 0, seg = 0, unit = 0;
-            int pending[NS];
+        // The whole warp runs this with equal values and one elected lane issues: descriptors then stay in
+        // uniform registers (from one divergent lane each MMA cost 90 to 160 cycles to issue).
+        constexpr uint32_t idesc_s = idesc16<BF16>(kTcRowTile, KT, false);
+        constexpr uint32_t idesc_o = idesc16<BF16>(kTcRowTile, DP, true);
+        const uint32_t base = smem_addr(smem);
+        // The upper halves of the descriptors hold layout and stride only (and the leading offset, V's, sits in
+        // the lower half's upper bits; with one group of 64 values it is not used).
+        const uint64_t k_desc = umma_desc_sw128(base, 1024);
+        const uint64_t v_desc = umma_desc_sw128_mn(base, C::kSub > 1 ? KT * 128 : 1024, 1024);
+        const uint32_t k_hi = (uint32_t)(k_desc >> 32), k_lo = (uint32_t)k_desc & 0xffff0000u;
+        const uint32_t v_hi = (uint32_t)(v_desc >> 32), v_lo = (uint32_t)v_desc & 0xffff0000u;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit);
+        const int units = __shfl_sync(0xffffffffu, (int)w.left, 0);
+        int seg = 0, slot = 0, turn = 0;  // turn: parity of the ring's round
+        int held[NS] = {};                          // slot of the stream's tile whose values are still to come
+        bool ok = true;
+        auto values = [&](int s, int n) {  // O_s += P_s V of the stream's n-th tile
+            if (!warp_wait(&bars->pfull[s], (uint32_t)(n & 1))) return false;
+            tc_fence_after();
+            const uint32_t vd = v_lo + ((base + C::kRing + (uint32_t)held[s] * (2 * C::kTile) + C::kTile) >> 4);
 #pragma unroll
-            for (int s = 0; s < NS; ++s) pending[s] = -1;
-            bool ok = true;
-            auto values = [&](int s, int n) {  // O_s += P_s V of the stream's n-th tile
-                const int slot = pending[s] % C::kSlots;
-                if (!wait(&bars->pfull[s], (uint32_t)(n & 1))) return false;
+            for (int k = 0; k < KT / 16; ++k)
+                mma_elect_ts(tm + s * DP, tm + C::kColP + s * (KT / 2) + 8 * k, vd + k * (2048 >> 4), v_hi, idesc_o, 1u);
+            commit_elect(&bars->empty[held[s]]);
+            commit_elect(&bars->pvdone[s]);
+            return true;
+        };
+        for (int unit = 0; unit < units && ok; ++unit) {
+            const int qb = seg % C::kQBufs;
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                if (!warp_wait(&bars->full[slot], (uint32_t)turn) ||
+                    (unit > 0 && !warp_wait(&bars->sfree[s], (uint32_t)((unit - 1) & 1)))) {
+                    ok = false;
+                    break;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the loaders' copies, to the MMA
                 tc_fence_after();
-                const uint64_t vd = v_desc + (uint64_t)(slot * (2 * C::kTile >> 4));
+                const uint32_t qd = k_lo + ((base + (uint32_t)qb * C::kQ) >> 4);
+                const uint32_t kd = k_lo + ((base + C::kRing + (uint32_t)slot * (2 * C::kTile)) >> 4);
 #pragma unroll
-                for (int k = 0; k < KT / 16; ++k)
-                    umma_bf16_ts(tmem + s * DP, tmem + C::kColP + s * (KT / 2) + 8 * k, vd + (uint64_t)(k * (2048 >> 4)),
-                                 idesc_o, 1u);
-                umma_commit(&bars->empty[slot]);
-                umma_commit(&bars->pvdone[s]);
-                return true;
-            };
-            while (!w.done() && ok) {
-                const int qb = seg % C::kQBufs;
-#pragma unroll
-                for (int s = 0; s < NS; ++s) {
-                    const int slot = tile % C::kSlots;
-                    if (!wait(&bars->full[slot], (uint32_t)((tile / C::kSlots) & 1)) ||
-                        (unit > 0 && !wait(&bars->sfree[s], (uint32_t)((unit - 1) & 1)))) {
-                        ok = false;
-                        break;
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the loaders' copies, to the MMA
-                    tc_fence_after();
-                    const uint64_t qd = q_desc + (uint64_t)(qb * (C::kQ >> 4));
-                    const uint64_t kd = k_desc + (uint64_t)(slot * (2 * C::kTile >> 4));
-#pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        umma_bf16(tmem + C::kColS + s * KT, qd + (uint64_t)((k >> 2) * (kTcRowTile * 128 >> 4) + 2 * (k & 3)),
-                                  kd + (uint64_t)((k >> 2) * (KT * 128 >> 4) + 2 * (k & 3)), idesc_s, k > 0 ? 1u : 0u);
-                    umma_commit(&bars->sfull[s]);
-                    if (pending[s] >= 0 && !values(s, unit - 1)) {
-                        ok = false;
-                        break;
-                    }
-                    pending[s] = tile++;
+                for (int k = 0; k < DP / 16; ++k)
+                    mma_elect_ss(tm + C::kColS + s * KT, qd + (k >> 2) * (kTcRowTile * 128 >> 4) + 2 * (k & 3), k_hi,
+                                 kd + (k >> 2) * (KT * 128 >> 4) + 2 * (k & 3), k_hi, idesc_s, k > 0 ? 1u : 0u);
+                commit_elect(&bars->sfull[s]);
+                if (unit > 0 && !values(s, unit - 1)) {
+                    ok = false;
+                    break;
                 }
-                if (!ok) break;
-                if (w.kt + 1 == w.kts) {
-                    umma_commit(&bars->qempty[qb]);
-                    ++seg;
+                held[s] = slot;
+                if (++slot == C::kSlots) {
+                    slot = 0;
+                    turn ^= 1;
                 }
-                ++unit;
-                walk_next(a, w, kTcRowTile, C::kUnit);
             }
-#pragma unroll
-            for (int s = 0; s < NS; ++s)
-                if (ok && pending[s] >= 0) ok = values(s, unit - 1);
-            umma_commit(&bars->drain);  // everything issued has completed before tensor memory is freed
-            mbar_wait_bounded(&bars->drain, 0, status, limit_ns);
+            if (!ok) break;
+            if (__shfl_sync(0xffffffffu, w.kt + 1 == w.kts, 0)) {
+                commit_elect(&bars->qempty[qb]);
+                ++seg;
+            }
+            walk_next(a, w, kTcRowTile, C::kUnit);
         }
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+            if (ok && units > 0) ok = values(s, units - 1);
+        commit_elect(&bars->drain);  // everything issued has completed before tensor memory is freed
+        mbar_wait_bounded(&bars->drain, 0, status, limit_ns);
         __syncwarp();
     } else if (warp < C::kSoftmaxWarps) {
         // ---------------------------------------------------------------- softmax
@@ -397,15 +433,17 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                     l *= grow;
                 }
                 const float ref = m == -CUDART_INF_F ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t f2 = pk2(f, f), r2 = pk2(-ref, -ref);
+                uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < KT; i += 2) {
-                    const float p0 = ex2(fmaf(z[i], f, -ref)), p1 = ex2(fmaf(z[i + 1], f, -ref));
-                    sum[i & 2] += p0;
-                    sum[(i & 2) + 1] += p1;
+                    const float2 e = up2(fma2(pk2(z[i], z[i + 1]), f2, r2));
+                    const float p0 = ex2(e.x), p1 = ex2(e.y);
+                    sum[(i >> 1) & 3] = add2(sum[(i >> 1) & 3], pk2(p0, p1));
                     p[i / 2] = pack16<BF16>(p0, p1);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const float2 total = up2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+                l += total.x + total.y;
             } else {
                 __syncwarp();
                 if (lane == 0) mbar_arrive_local(&bars->sfree[s]);
