@@ -23,6 +23,7 @@ namespace dspark {
 
 struct AttnArgs {
     int T, B, Hq, Hk, G, D;
+    uint32_t g_mul, g_shift;  // row / G = umulhi(2 row, g_mul) >> g_shift for rows below 2^31 (group_division)
     int page_shift, num_pages, max_blocks;
     int causal, window;
     float scale, softcap;
@@ -208,9 +209,15 @@ __device__ __forceinline__ void attn_tail_rows(const AttnArgs& a, size_t i0, siz
         for (size_t i = (size_t)end * a.Hq + i0; i < (size_t)a.T * a.Hq; i += n) a.lse[i] = -CUDART_INF_F;
 }
 
+// Token of a row of a request and kv head.
+__device__ __forceinline__ int attn_token(const AttnArgs& a, int row) {
+    return (int)(__umulhi(2u * (uint32_t)row, a.g_mul) >> a.g_shift);
+}
+
 // Row of [T Hq] of row `row` of a request and kv head.
 __device__ __forceinline__ long long attn_out_row(const AttnArgs& a, int token0, int head, int row) {
-    return (long long)(token0 + row / a.G) * a.Hq + head * a.G + row % a.G;
+    const int token = attn_token(a, row);
+    return (long long)(token0 + token) * a.Hq + head * a.G + (row - token * a.G);
 }
 
 // 16 bytes, or 16 zero bytes where !real (src is then not read).

@@ -180,18 +180,18 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
             const int pos0 = w.r.seq - w.r.n;  // position of the request's first new token
             auto lo_of = [&](int token) { return a.window > 0 ? max(pos0 + token - a.window + 1, 0) : 0; };
             auto hi_of = [&](int token) { return a.causal ? min(pos0 + token + 1, w.r.seq) : w.r.seq; };
-            all_lo = lo_of((row0 + rows - 1) / a.G);
-            all_hi = hi_of(row0 / a.G);
+            all_lo = lo_of(attn_token(a, row0 + rows - 1));
+            all_hi = hi_of(attn_token(a, row0));
             const unsigned char* qrow[2];
             bool real[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int row = g + 8 * r, token = (row0 + row) / a.G;
+                const int row = g + 8 * r, token = attn_token(a, row0 + row);
                 real[r] = row < rows;
                 see_lo[r] = real[r] ? lo_of(token) : 0;
                 see_hi[r] = real[r] ? hi_of(token) : 0;
                 qrow[r] = real[r] ? a.q + 2 * ((w.r.token0 + token) * a.q_token +
-                                               (head * a.G + (row0 + row) % a.G) * a.q_head)
+                                               (head * a.G + row0 + row - token * a.G) * a.q_head)
                                   : a.q;
                 m[r] = -CUDART_INF_F;
                 l[r] = 0.f;
@@ -639,6 +639,11 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     a.Hq = p->Hq;
     a.Hk = p->Hk;
     a.G = p->Hq / p->Hk;
+    // Division by G: with 2^(s-1) < G <= 2^s and m = floor(2^(31+s) / G) + 1, m G exceeds 2^(31+s) by at most G
+    // <= 2^s, so floor(row m / 2^(31+s)) = floor(row / G) for row < 2^31.
+    a.g_shift = 0;
+    while ((1ll << a.g_shift) < a.G) ++a.g_shift;
+    a.g_mul = (uint32_t)((1ull << (31 + a.g_shift)) / (uint64_t)a.G + 1);
     a.D = p->D;
     a.page_shift = page_shift_of(p->page_size);
     a.num_pages = p->num_pages;

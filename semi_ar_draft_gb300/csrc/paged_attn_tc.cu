@@ -2,7 +2,7 @@
 // requests whose new tokens give more than 16 rows a kv head (the flattened verify, draft blocks).
 //
 // One persistent CTA a multiprocessor walks its range of units (paged.cuh).  Roles:
-//   loaders (3 warps)    copy the item's queries and, tile by tile, KT keys and values into a ring in
+//   loaders (4 warps)    copy the item's queries and, tile by tile, KT keys and values into a ring in
 //                        shared memory, 16 bytes a thread and copy, in the 128-byte-swizzled layout the MMA
 //                        reads; several tiles in flight, across items
 //   MMA (1 thread)       S = Q K^T into tensor memory, and O += P V with P from tensor memory
@@ -30,7 +30,7 @@ struct TcAttn {
     static constexpr int kKt = DP == 256 ? 32 : 64;  // keys of a tile
     static constexpr int kUnit = kStreams * kKt;
     static constexpr int kSoftmaxWarps = 4 * kStreams;
-    static constexpr int kLoaders = 3;  // (12 warps: 168 registers a thread; a thirteenth would leave 128)
+    static constexpr int kLoaders = 4;
     static constexpr int kWarps = kSoftmaxWarps + kLoaders + 1;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSub = DP / 64;                  // 64-value groups of a row
@@ -60,6 +60,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+          "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {  // (as tmem_wait_ld: tied to the registers)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+// c tanh(s / c) log2 e as c log2 e (1 - 2 / (1 + e^(2 s / c))), in = 2 log2 e scale / c of the unscaled
+// score: off by at most 3e-7 c, without a branch.
+__device__ __forceinline__ float softcap(float x, float in, float out) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x * in)));
+    return fmaf(-2.f * out, r, out);
 }
 // Descriptor of an N-major (values as they lie: N adjacent, one 128-byte row a K index) operand with the
 // 128-byte swizzle: the leading offset goes from one group of 64 N to the next, the stride offset from
@@ -193,16 +215,16 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit);
         int err = 0, tile = 0, seg = 0, stream = 0;
         auto tile_key = [&]() { return (w.kt_first + w.kt) * C::kUnit + stream * KT; };
-        // Pages of the next tile's keys (lane: keys lane and lane + 32), asked for a tile ahead; kNone: no key.
-        constexpr int kNone = INT32_MIN;
+        // Pages of the next tile's keys (lane: keys lane and lane + 32), asked for a tile ahead.  The load is
+        // unconditional (entry 0 where there is no key) and looked at when the tile's copies are issued, so
+        // that nothing waits for it here.
         int pid[KT / 32];
         auto fetch_pages = [&]() {
 #pragma unroll
             for (int h = 0; h < KT / 32; ++h) {
-                const int key = tile_key() + 32 * h + lane;
-                pid[h] = kNone;
-                if (!w.done() && key < w.r.seq)
-                    pid[h] = __ldg(a.block_table + (size_t)w.j * a.max_blocks + (key >> a.page_shift));
+                const int key = min(tile_key() + 32 * h + lane, w.r.seq - 1);
+                const size_t at = w.done() || key < 0 ? 0 : (size_t)w.j * a.max_blocks + (key >> a.page_shift);
+                pid[h] = __ldg(a.block_table + at);
             }
         };
         fetch_pages();
@@ -220,8 +242,9 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 for (int r = lw * kPer + sub_row; r < ((rows + 31) & ~31); r += C::kLoaders * kPer) {
                     const bool real = inside && r < rows;
                     const int row = row0 + r;
-                    const long long src = real ? (w.r.token0 + row / a.G) * a.q_token +
-                                                     (head * a.G + row % a.G) * a.q_head + chunk * 8
+                    const int token = attn_token(a, row);
+                    const long long src = real ? (w.r.token0 + token) * a.q_token +
+                                                     (head * a.G + row - token * a.G) * a.q_head + chunk * 8
                                                : 0;
                     copy16(qbase + sw128_offset(r, chunk & 7), a.q + 2 * src, real);
                 }
@@ -234,9 +257,12 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + chunk_at * (KT * 128);
 #pragma unroll
                 for (int h = 0; h < KT / 32; ++h) {
-                    const bool out = (uint32_t)pid[h] >= (uint32_t)a.num_pages;
-                    if (out && pid[h] != kNone) err = DSPARK_ERR_CACHE;
-                    if (out) pid[h] = -1;
+                    const bool none = (int)key0 + 32 * h + lane >= w.r.seq;
+                    if ((uint32_t)pid[h] >= (uint32_t)a.num_pages) {
+                        if (!none) err = DSPARK_ERR_CACHE;
+                        pid[h] = -1;
+                    }
+                    if (none) pid[h] = -1;
                 }
 #pragma unroll
                 for (int u = 0; u < (KT / kPer + C::kLoaders - 1) / C::kLoaders; ++u) {
@@ -283,7 +309,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         const int units = __shfl_sync(0xffffffffu, (int)w.left, 0);
         int seg = 0, slot = 0, turn = 0;  // turn: parity of the ring's round
         int held[NS] = {};                          // slot of the stream's tile whose values are still to come
-        bool ok = true;
+        bool ok = true, behind = false;             // behind: the last unit's values are still to come
         auto values = [&](int s, int n) {  // O_s += P_s V of the stream's n-th tile
             if (!warp_wait(&bars->pfull[s], (uint32_t)(n & 1))) return false;
             tc_fence_after();
@@ -313,7 +339,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                     mma_elect_ss(tm + C::kColS + s * KT, qd + (k >> 2) * (kTcRowTile * 128 >> 4) + 2 * (k & 3), k_hi,
                                  kd + (k >> 2) * (KT * 128 >> 4) + 2 * (k & 3), k_hi, idesc_s, k > 0 ? 1u : 0u);
                 commit_elect(&bars->sfull[s]);
-                if (unit > 0 && !values(s, unit - 1)) {
+                if (behind && !values(s, unit - 1)) {
                     ok = false;
                     break;
                 }
@@ -324,15 +350,17 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 }
             }
             if (!ok) break;
-            if (__shfl_sync(0xffffffffu, w.kt + 1 == w.kts, 0)) {
+            // An item's last values do not wait for the next item's keys.
+            const bool end = __shfl_sync(0xffffffffu, w.kt + 1 == w.kts || w.left == 1, 0);
+            if (end) {
                 commit_elect(&bars->qempty[qb]);
                 ++seg;
+#pragma unroll
+                for (int s = 0; s < NS; ++s) ok = ok && values(s, unit);
             }
+            behind = !end;
             walk_next(a, w, kTcRowTile, C::kUnit);
         }
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-            if (ok && units > 0) ok = values(s, units - 1);
         commit_elect(&bars->drain);  // everything issued has completed before tensor memory is freed
         mbar_wait_bounded(&bars->drain, 0, status, limit_ns);
         __syncwarp();
@@ -343,11 +371,13 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         const uint32_t ts = tmem + lanes + C::kColS + s * KT, tp = tmem + lanes + C::kColP + s * (KT / 2);
         const float c = a.scale * kLog2e;
         const bool plain = a.softcap == 0.f && c > 0.f;
-        uint32_t zero[32];
+        const float cap_in = a.softcap > 0.f ? 2.f * kLog2e * a.scale / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
+        uint32_t zero[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) zero[i] = 0u;
+        for (int i = 0; i < 16; ++i) zero[i] = 0u;
         if (s == 0)
-            for (int i = 0; i < NS * DP; i += 32) tmem_st32(tmem + lanes + i, zero);
+#pragma unroll 1
+            for (int i = 0; i < NS * DP; i += 16) tmem_st16(tmem + lanes + i, zero);
         tmem_wait_st();
         tc_fence_before();
         uint32_t meets = 0, smeets = 0;
@@ -375,9 +405,9 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 const int pos0 = w.r.seq - w.r.n;
                 auto lo_of = [&](int token) { return a.window > 0 ? max(pos0 + token - a.window + 1, 0) : 0; };
                 auto hi_of = [&](int token) { return a.causal ? min(pos0 + token + 1, w.r.seq) : w.r.seq; };
-                all_lo = lo_of((row0 + rows - 1) / a.G);
-                all_hi = hi_of(row0 / a.G);
-                const int token = (row0 + row) / a.G;
+                all_lo = lo_of(attn_token(a, row0 + rows - 1));
+                all_hi = hi_of(attn_token(a, row0));
+                const int token = attn_token(a, row0 + row);
                 see_lo = row < rows ? lo_of(token) : 0;
                 see_hi = row < rows ? hi_of(token) : 0;
                 m = -CUDART_INF_F;
@@ -388,65 +418,51 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
             const bool live = 32 * quarter < rows;
             if (!warp_wait(&bars->sfull[s], (uint32_t)(n & 1))) break;
             tc_fence_after();
-            uint32_t p[KT / 2];
-            float grow = 1.f;
+            // Two passes over S, 32 columns at a time in rolled loops (unrolled over the whole tile, the code
+            // of the rare paths alone cost thousands of cycles an item in instruction fetches).
+            float grow = 1.f, f = plain ? c : 1.f;
             if (live) {
-                uint32_t x[KT / 32][32];
+                float top = -CUDART_INF_F;
+#pragma unroll 1
+                for (int h = 0; h < KT; h += 32) {
+                    uint32_t x[32];
+                    tmem_ld32(ts + h, x);
+                    tmem_wait_ld(x);
+                    if (!plain || edge) {  // what the second pass is to see goes back
+                        if (a.softcap > 0.f) {
 #pragma unroll
-                for (int h = 0; h < KT / 32; ++h) tmem_ld32(ts + 32 * h, x[h]);
+                            for (int i = 0; i < 32; ++i)
+                                x[i] = __float_as_uint(softcap(__uint_as_float(x[i]), cap_in, cap_out));
+                        } else if (!plain) {
 #pragma unroll
-                for (int h = 0; h < KT / 32; ++h) tmem_wait_ld(x[h]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_local(&bars->sfree[s]);
-                float z[KT];
+                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * c);
+                        }
+                        if (edge) {
+                            const int from = see_lo - key0 - h;
+                            const uint32_t count = (uint32_t)max(see_hi - see_lo, 0);
 #pragma unroll
-                for (int i = 0; i < KT; ++i) z[i] = __uint_as_float(x[i >> 5][i & 31]);
-                float f = c;
-                if (!plain) {
-                    f = 1.f;
-                    if (a.softcap > 0.f) {
-                        const float in = a.scale / a.softcap, out = a.softcap * kLog2e;
-#pragma unroll
-                        for (int i = 0; i < KT; ++i) z[i] = attn_tanh(z[i] * in) * out;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < KT; ++i) z[i] *= c;
+                            for (int i = 0; i < 32; ++i)
+                                if ((uint32_t)(i - from) >= count) x[i] = 0xff800000u;  // -inf
+                        }
+                        tmem_st32(ts + h, x);
                     }
+                    float t4[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) t4[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[4 + i]));
+#pragma unroll
+                    for (int i = 8; i < 32; i += 8)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            t4[q] = fmax3(t4[q], __uint_as_float(x[i + q]), __uint_as_float(x[i + 4 + q]));
+                    top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
                 }
-                if (edge) {
-#pragma unroll
-                    for (int i = 0; i < KT; ++i)
-                        if (key0 + i < see_lo || key0 + i >= see_hi) z[i] = -CUDART_INF_F;
-                }
-                float mx4[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(z[i], z[4 + i]);
-#pragma unroll
-                for (int i = 8; i < KT; i += 8)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) mx4[q] = fmax3(mx4[q], z[i + q], z[i + 4 + q]);
-                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * f;  // (f > 0)
-                if (mx > m + 8.f) {
-                    if (m != -CUDART_INF_F) grow = ex2(m - mx);  // (else sum and output are still zero)
-                    m = mx;
+                top *= f;  // (f > 0)
+                if (top > m + 8.f) {
+                    if (m != -CUDART_INF_F) grow = ex2(m - top);  // (else sum and output are still zero)
+                    m = top;
                     l *= grow;
                 }
-                const float ref = m == -CUDART_INF_F ? 0.f : m;
-                const uint64_t f2 = pk2(f, f), r2 = pk2(-ref, -ref);
-                uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int i = 0; i < KT; i += 2) {
-                    const float2 e = up2(fma2(pk2(z[i], z[i + 1]), f2, r2));
-                    const float p0 = ex2(e.x), p1 = ex2(e.y);
-                    sum[(i >> 1) & 3] = add2(sum[(i >> 1) & 3], pk2(p0, p1));
-                    p[i / 2] = pack16<BF16>(p0, p1);
-                }
-                const float2 total = up2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
-                l += total.x + total.y;
-            } else {
-                __syncwarp();
-                if (lane == 0) mbar_arrive_local(&bars->sfree[s]);
+                tmem_wait_st();
             }
             // the stream's earlier products are done: P's buffer is free and O stands still
             if (n > 0 && !warp_wait(&bars->pvdone[s], (uint32_t)((n - 1) & 1))) break;
@@ -463,11 +479,34 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                         tmem_st32(tmem + lanes + s * DP + i, o);
                     }
                 }
-                if constexpr (KT == 64)
-                    tmem_st32(tp, p);
-                else
-                    tmem_st16(tp, p);
+                const float ref = m == -CUDART_INF_F ? 0.f : m;
+                const uint64_t f2 = pk2(f, f), r2 = pk2(-ref, -ref);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+                for (int h = 0; h < KT; h += 32) {
+                    uint32_t x[32], p[16];
+                    tmem_ld32(ts + h, x);
+                    tmem_wait_ld(x);
+                    if (h + 32 == KT) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_local(&bars->sfree[s]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 e = up2(fma2(pk2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f2, r2));
+                        const float p0 = ex2(e.x), p1 = ex2(e.y);
+                        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pk2(p0, p1));
+                        p[i / 2] = pack16<BF16>(p0, p1);
+                    }
+                    tmem_st16(tp + h / 2, p);
+                }
+                const float2 total = up2(add2(sum[0], sum[1]));
+                l += total.x + total.y;
                 tmem_wait_st();
+            } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive_local(&bars->sfree[s]);
             }
             // A hidden key's value must not reach a row that does not see it, even as 0 x inf: values of an
             // edge tile that are not finite (never, in a healthy cache) are added by hand to the rows that
@@ -541,46 +580,40 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 const size_t slot = 2 * (size_t)part + (seg_first == 0 ? kHead : kTail);
                 const float inv = !whole ? 1.f : (ll == 0.f ? 0.f : 1.f / ll);
                 const long long at = attn_out_row(a, w.r.token0, head, row0 + row);
-                if (live) {
+                unsigned char* dst = a.out + (size_t)at * a.D * 2;
+                float* part_dst = a.part_o + (slot * kTcRowTile + row) * a.D;
 #pragma unroll 1
-                    for (int i = s * (DP / NS); i < (s + 1) * (DP / NS); i += 32) {
-                        float v[32];
+                for (int i = s * (DP / NS); i < (s + 1) * (DP / NS); i += 16) {
+                    if (live) {
+                        uint32_t o[NS][16];
 #pragma unroll
-                        for (int q = 0; q < NS; ++q) {
-                            uint32_t o[32];
-                            tmem_ld32(tmem + lanes + q * DP + i, o);
-                            tmem_wait_ld(o);
+                        for (int q = 0; q < NS; ++q) tmem_ld16(tmem + lanes + q * DP + i, o[q]);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float y = __uint_as_float(o[e]);
-                                v[e] = q == 0 ? y * f[0] : fmaf(y, f[q], v[e]);
-                            }
-                            tmem_st32(tmem + lanes + q * DP + i, zero);
+                        for (int q = 0; q < NS; ++q) tmem_wait_ld16(o[q]);
+                        float v[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            v[e] = __uint_as_float(o[0][e]) * f[0];
+                            if (NS == 2) v[e] = fmaf(__uint_as_float(o[NS - 1][e]), f[NS - 1], v[e]);
                         }
-                        if (row < rows) {
+                        if (row < rows && i < a.D) {
+                            if (whole) {
+                                uint32_t y[8];
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                if (i + e >= a.D) continue;
-                                if (whole) {
-                                    uint4 y;
-                                    y.x = pack16<BF16>(v[e] * inv, v[e + 1] * inv);
-                                    y.y = pack16<BF16>(v[e + 2] * inv, v[e + 3] * inv);
-                                    y.z = pack16<BF16>(v[e + 4] * inv, v[e + 5] * inv);
-                                    y.w = pack16<BF16>(v[e + 6] * inv, v[e + 7] * inv);
-                                    *reinterpret_cast<uint4*>(a.out + ((size_t)at * a.D + i + e) * 2) = y;
-                                } else {
-                                    float4* dst = reinterpret_cast<float4*>(
-                                        a.part_o + (slot * kTcRowTile + row) * a.D + i + e);
-                                    dst[0] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                                    dst[1] = make_float4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
-                                }
+                                for (int e = 0; e < 8; ++e) y[e] = pack16<BF16>(v[2 * e] * inv, v[2 * e + 1] * inv);
+                                uint4* to = reinterpret_cast<uint4*>(dst + 2 * i);
+                                to[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                                to[1] = make_uint4(y[4], y[5], y[6], y[7]);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 16; e += 4)
+                                    *reinterpret_cast<float4*>(part_dst + i + e) =
+                                        make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                             }
                         }
-                    }
-                } else {  // rows of nobody have gathered whatever lay in P
-                    for (int i = s * (DP / NS); i < (s + 1) * (DP / NS); i += 32)
+                    }  // (rows of nobody have gathered whatever lay in P)
 #pragma unroll
-                        for (int q = 0; q < NS; ++q) tmem_st32(tmem + lanes + q * DP + i, zero);
+                    for (int q = 0; q < NS; ++q) tmem_st16(tmem + lanes + q * DP + i, zero);
                 }
                 tmem_wait_st();
                 if (s == 0 && row < rows) {
