@@ -5,7 +5,7 @@
 //   loaders (4 warps)    copy the item's queries and, tile by tile, KT keys and values into a ring in
 //                        shared memory, 16 bytes a thread and copy, in the 128-byte-swizzled layout the MMA
 //                        reads; several tiles in flight, across items
-//   MMA (1 thread)       S = Q K^T into tensor memory, and O += P V with P from tensor memory
+//   MMA (1 warp a stream) S = Q K^T into tensor memory, and O += P V with P from tensor memory
 //   softmax (4 warps a   thread = row: takes S, writes P (16 bits) back to tensor memory, keeps the row's
 //     stream)            maximum and sum; at an item's end joins the streams and writes the output
 // A unit's key tiles go to kStreams streams in turn, each with its own S, P, O and statistics (heads up to
@@ -31,7 +31,17 @@ struct TcAttn {
     static constexpr int kUnit = kStreams * kKt;
     static constexpr int kSoftmaxWarps = 4 * kStreams;
     static constexpr int kLoaders = 4;
-    static constexpr int kWarps = kSoftmaxWarps + kLoaders + 1;
+    // Warps after the softmax's: multiprocessor quarter (warp % 4) 0 has none of them and quarter 1 the MMA
+    // warps, one a stream; the loaders are in quarters 2 and 3.  Short row tiles keep quarter 0 busiest.
+    static constexpr int kWarps = kSoftmaxWarps + 8;
+    static __device__ __forceinline__ int loader_of(int warp) {  // 0 .. 3, or -1
+        const int h = warp - kSoftmaxWarps;
+        return h >= 0 && (h & 2) ? (h >> 2) * 2 + (h & 1) : -1;
+    }
+    static __device__ __forceinline__ int mma_of(int warp) {  // the stream, or -1
+        const int h = warp - kSoftmaxWarps;
+        return h == 1 ? 0 : (h == 5 && kStreams == 2 ? 1 : -1);
+    }
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSub = DP / 64;                  // 64-value groups of a row
     static constexpr int kTile = kKt * DP * 2;            // bytes of a tile's K (or V)
@@ -139,7 +149,7 @@ __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
 }
 
 struct TcBars {
-    uint64_t full[10], empty[10], qempty[2], sfull[2], sfree[2], pfull[2], pvdone[2], smeet[2], meet, drain;
+    uint64_t full[10], empty[10], qempty[2], sfull[2], sfree[2], pfull[2], pvdone[2], smeet[2], drain[2], meet;
     uint32_t tmem;
     int abort, status, misaligned;
     int odd[2][2];
@@ -163,7 +173,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
             mbar_init(&bars->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->qempty[i], 1);
+            mbar_init(&bars->qempty[i], NS);
             mbar_init(&bars->sfull[i], 1);
             mbar_init(&bars->sfree[i], 4);
             mbar_init(&bars->pfull[i], 4);
@@ -172,15 +182,16 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
             bars->odd[i][0] = bars->odd[i][1] = 0;
         }
         mbar_init(&bars->meet, C::kSoftmaxWarps);
-        mbar_init(&bars->drain, 1);
+        mbar_init(&bars->drain[0], 1);
+        mbar_init(&bars->drain[1], 1);
         bars->abort = 0;
         // the swizzled tiles need 1024-byte alignment; where it is not given nothing is computed
         bars->misaligned = (smem_addr(smem) & 1023u) != 0;
         bars->status = bars->misaligned ? DSPARK_ERR_UNSUPPORTED : 0;
         mbar_init_fence();
     }
-    constexpr int kMmaWarp = C::kWarps - 1;
-    if (warp == kMmaWarp) {
+    constexpr int kAllocWarp = C::kSoftmaxWarps + 1;
+    if (warp == kAllocWarp) {
         tmem_alloc(&bars->tmem, 512);
         tmem_relinquish();
     }
@@ -199,11 +210,11 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
     attn_tail_rows(a, (size_t)part * C::kThreads + tid, (size_t)parts * C::kThreads);
     PartItem mine{-1, 0, 0, 0, 0, 0, {0, 0}};
 
-    if (warp >= C::kSoftmaxWarps && warp < kMmaWarp) {
+    if (C::loader_of(warp) >= 0) {
         // ---------------------------------------------------------------- loaders
         constexpr int kChunks = DP / 8;              // 16-byte groups of a row
         constexpr int kPer = 32 / kChunks;           // rows a warp copies at a time
-        const int lw = warp - C::kSoftmaxWarps;
+        const int lw = C::loader_of(warp);
         const int chunk = lane % kChunks, sub_row = lane / kChunks;
         const bool inside = chunk * 8 < a.D;
         const uint32_t chunk_at = (uint32_t)(chunk >> 3);  // 64-value group
@@ -213,7 +224,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         const unsigned char* k_at = a.k_pages + chunk * 16;
         const long long v_after_k = a.v_pages - a.k_pages;
         AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit);
-        int err = 0, tile = 0, seg = 0, stream = 0;
+        int err = 0, seg = 0, stream = 0;
         auto tile_key = [&]() { return (w.kt_first + w.kt) * C::kUnit + stream * KT; };
         // Pages of the next tile's keys (lane: keys lane and lane + 32), asked for a tile ahead.  The load is
         // unconditional (entry 0 where there is no key) and looked at when the tile's copies are issued, so
@@ -229,14 +240,15 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         };
         fetch_pages();
         bool fresh = true;
+        int head = 0, slot = 0, round = 0;
         while (!w.done()) {
-            const int head = w.item / w.rts;
             if (fresh) {
                 fresh = false;
+                head = w.item / w.rts;
                 const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
                 if (use > 0 && !warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) break;
                 ++seg;
-                const int row0 = (w.item % w.rts) * kTcRowTile;
+                const int row0 = (w.item - head * w.rts) * kTcRowTile;
                 const int rows = min(w.r.n * a.G - row0, kTcRowTile);
                 const uint32_t qbase = base + (uint32_t)qb * C::kQ + chunk_at * (kTcRowTile * 128);
                 for (int r = lw * kPer + sub_row; r < ((rows + 31) & ~31); r += C::kLoaders * kPer) {
@@ -249,8 +261,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                     copy16(qbase + sw128_offset(r, chunk & 7), a.q + 2 * src, real);
                 }
             }
-            const int slot = tile % C::kSlots;
-            if (tile >= C::kSlots && !warp_wait(&bars->empty[slot], (uint32_t)((tile / C::kSlots - 1) & 1))) break;
+            if (round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) break;
             {
                 const uint32_t key0 = (uint32_t)tile_key();
                 const unsigned char* head_at = k_at + head * a.head;
@@ -281,7 +292,10 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
             // The slot is full once every loader thread's copies so far have landed (its queries among
             // them); nobody waits for that here, so the whole ring can be in flight.
             copy_arrive(&bars->full[slot]);
-            ++tile;
+            if (++slot == C::kSlots) {
+                slot = 0;
+                ++round;
+            }
             if (++stream == NS) {
                 stream = 0;
                 fresh = w.kt + 1 == w.kts;
@@ -291,7 +305,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (err) bars->status = err;
-    } else if (warp == kMmaWarp) {
+    } else if (C::mma_of(warp) >= 0) {
         // ---------------------------------------------------------------- MMA issue
         // The whole warp runs this with equal values and one elected lane issues: descriptors then stay in
         // uniform registers (from one divergent lane each MMA cost 90 to 160 cycles to issue).
@@ -307,62 +321,53 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit);
         const int units = __shfl_sync(0xffffffffu, (int)w.left, 0);
-        int seg = 0, slot = 0, turn = 0;  // turn: parity of the ring's round
-        int held[NS] = {};                          // slot of the stream's tile whose values are still to come
-        bool ok = true, behind = false;             // behind: the last unit's values are still to come
-        auto values = [&](int s, int n) {  // O_s += P_s V of the stream's n-th tile
+        const int s = C::mma_of(warp);
+        int seg = 0, slot = s, turn = 0, held = 0;  // turn: parity of the ring's round; held: the slot whose values
+        bool ok = true, behind = false;             // are still to come, if behind
+        auto values = [&](int n) {  // O_s += P_s V of the stream's n-th tile
             if (!warp_wait(&bars->pfull[s], (uint32_t)(n & 1))) return false;
             tc_fence_after();
-            const uint32_t vd = v_lo + ((base + C::kRing + (uint32_t)held[s] * (2 * C::kTile) + C::kTile) >> 4);
+            const uint32_t vd = v_lo + ((base + C::kRing + (uint32_t)held * (2 * C::kTile) + C::kTile) >> 4);
 #pragma unroll
             for (int k = 0; k < KT / 16; ++k)
                 mma_elect_ts(tm + s * DP, tm + C::kColP + s * (KT / 2) + 8 * k, vd + k * (2048 >> 4), v_hi, idesc_o, 1u);
-            commit_elect(&bars->empty[held[s]]);
+            commit_elect(&bars->empty[held]);
             commit_elect(&bars->pvdone[s]);
             return true;
         };
         for (int unit = 0; unit < units && ok; ++unit) {
             const int qb = seg % C::kQBufs;
+            if (!warp_wait(&bars->full[slot], (uint32_t)turn) ||
+                (unit > 0 && !warp_wait(&bars->sfree[s], (uint32_t)((unit - 1) & 1))))
+                break;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the loaders' copies, to the MMA
+            tc_fence_after();
+            const uint32_t qd = k_lo + ((base + (uint32_t)qb * C::kQ) >> 4);
+            const uint32_t kd = k_lo + ((base + C::kRing + (uint32_t)slot * (2 * C::kTile)) >> 4);
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                if (!warp_wait(&bars->full[slot], (uint32_t)turn) ||
-                    (unit > 0 && !warp_wait(&bars->sfree[s], (uint32_t)((unit - 1) & 1)))) {
-                    ok = false;
-                    break;
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the loaders' copies, to the MMA
-                tc_fence_after();
-                const uint32_t qd = k_lo + ((base + (uint32_t)qb * C::kQ) >> 4);
-                const uint32_t kd = k_lo + ((base + C::kRing + (uint32_t)slot * (2 * C::kTile)) >> 4);
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-                    mma_elect_ss(tm + C::kColS + s * KT, qd + (k >> 2) * (kTcRowTile * 128 >> 4) + 2 * (k & 3), k_hi,
-                                 kd + (k >> 2) * (KT * 128 >> 4) + 2 * (k & 3), k_hi, idesc_s, k > 0 ? 1u : 0u);
-                commit_elect(&bars->sfull[s]);
-                if (behind && !values(s, unit - 1)) {
-                    ok = false;
-                    break;
-                }
-                held[s] = slot;
-                if (++slot == C::kSlots) {
-                    slot = 0;
-                    turn ^= 1;
-                }
+            for (int k = 0; k < DP / 16; ++k)
+                mma_elect_ss(tm + C::kColS + s * KT, qd + (k >> 2) * (kTcRowTile * 128 >> 4) + 2 * (k & 3), k_hi,
+                             kd + (k >> 2) * (KT * 128 >> 4) + 2 * (k & 3), k_hi, idesc_s, k > 0 ? 1u : 0u);
+            commit_elect(&bars->sfull[s]);
+            if (behind && !values(unit - 1)) break;
+            held = slot;
+            slot += NS;
+            if (slot >= C::kSlots) {
+                slot -= C::kSlots;
+                turn ^= 1;
             }
-            if (!ok) break;
             // An item's last values do not wait for the next item's keys.
             const bool end = __shfl_sync(0xffffffffu, w.kt + 1 == w.kts || w.left == 1, 0);
             if (end) {
                 commit_elect(&bars->qempty[qb]);
                 ++seg;
-#pragma unroll
-                for (int s = 0; s < NS; ++s) ok = ok && values(s, unit);
+                ok = values(unit);
             }
             behind = !end;
             walk_next(a, w, kTcRowTile, C::kUnit);
         }
-        commit_elect(&bars->drain);  // everything issued has completed before tensor memory is freed
-        mbar_wait_bounded(&bars->drain, 0, status, limit_ns);
+        commit_elect(&bars->drain[s]);  // everything issued has completed before tensor memory is freed
+        mbar_wait_bounded(&bars->drain[s], 0, status, limit_ns);
         __syncwarp();
     } else if (warp < C::kSoftmaxWarps) {
         // ---------------------------------------------------------------- softmax
@@ -641,7 +646,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    if (warp == kAllocWarp) tmem_dealloc(tmem, 512);
     if (tid == 0) {
         mine.err = bars->status ? bars->status : (bad ? DSPARK_ERR_CACHE : 0);
         a.items[part] = mine;
