@@ -11,8 +11,9 @@
 //
 // Join.  A range may begin or end inside an item.  Such a segment's (maximum, sum, unnormalised output)
 // goes to one of the block's two partial buffers -- kTail when the segment does not begin the item,
-// kHead when it does but does not end it -- and the block in which the item begins describes it.  A
-// second kernel joins the parts in the order of the keys, so results do not depend on timing.
+// kHead when it does but does not end it -- with a description of the item.  A second kernel joins the
+// parts in a fixed order, so results do not depend on timing; the rows of an item are dealt out over
+// as many of its blocks as it has parts.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -46,15 +47,17 @@ struct AttnArgs {
     float* part_o;           // [2 parts][rows of a tile][D]
 };
 
-// The item that begins in a block and ends in a later one (last < 0: none), and the block's error.
-struct PartItem {
-    int last;       // block that ends it
-    int row0;       // first row of the tile within the request and kv head
-    int rows;       // real rows of the tile
-    int token0;     // row of q and out of the request's first token
-    int head;       // kv head
-    int err;        // DSPARK_* recorded by this block
+// An item spread over blocks, as each of them describes it (first < 0: none).
+struct PartDesc {
+    int first, last;  // blocks that begin and end it
+    int row0, rows;   // first row of the tile within the request and kv head, its real rows
+    int token0;       // row of q and out of the request's first token
+    int head;         // kv head
     int pad[2];
+};
+struct PartItem {
+    PartDesc d[2];    // of the block's kTail and kHead segment
+    int err, pad[7];  // DSPARK_* recorded by the block
 };
 
 enum { kTail = 0, kHead = 1 };
@@ -224,6 +227,20 @@ __device__ __forceinline__ long long attn_out_row(const AttnArgs& a, int token0,
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
     const int n = real ? 16 : 0;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// The description of a segment that is not a whole item.
+__device__ __forceinline__ PartDesc part_desc(const AttnStart& s, const AttnWalk& w, int row0, int rows, int head) {
+    const long long unit = s.end - w.left;
+    PartDesc d;
+    d.first = (int)((unit - w.kt) / s.per);
+    d.last = (int)((unit + (w.kts - 1 - w.kt)) / s.per);
+    d.row0 = row0;
+    d.rows = rows;
+    d.token0 = w.r.token0;
+    d.head = head;
+    d.pad[0] = d.pad[1] = 0;
+    return d;
 }
 
 // tanh from its definition, (1 - e) / (1 + e) with e = e^(-2 |x|); near 0, where that cancels, the odd

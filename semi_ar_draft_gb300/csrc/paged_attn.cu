@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
 
     // ---- arithmetic
     AttnWalk w = walk_begin(a, start, kRows, C::kKeyTile);
-    PartItem mine{-1, 0, 0, 0, 0, 0, {0, 0}};
+    PartItem* mine = a.items + part;  // written by thread 0
+    if (tid == 0) mine->d[kTail].first = mine->d[kHead].first = -1;
     float o[DT][4];
     uint32_t qf[C::kQInSmem ? 1 : KS][4];
     float m[2], l[2], row_scale[2];
@@ -477,15 +478,7 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
                     if (col == 0) a.part_ml[(size_t)slot * kRows + row] = make_float2(mm, ll);
                 }
             }
-            if (!last_of_item && seg_first == 0) {
-                // the item ends in the block that holds its last unit
-                const long long end_unit = start.end + (w.kts - 1 - w.kt) - 1;
-                mine.last = (int)(end_unit / start.per);
-                mine.row0 = row0;
-                mine.rows = rows;
-                mine.token0 = w.r.token0;
-                mine.head = head;
-            }
+            if (!whole && tid == 0) mine->d[seg_first == 0 ? kHead : kTail] = part_desc(start, w, row0, rows, head);
             __syncthreads();
             fresh = true;
         }
@@ -495,18 +488,22 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
     cp_async_wait_group<0>();
     if (err) s_err = err;  // any of the block's errors: all are the same code
     __syncthreads();
-    if (tid == 0) {
-        mine.err = s_err;
-        a.items[part] = mine;
-    }
+    if (tid == 0) mine->err = s_err;
 }
 
-// Joins the parts of the items that are spread over blocks: one warp a row, the lanes over the parts for
-// the statistics and over the head dimension for the outputs.
+// Joins the parts of the items that are spread over blocks.  Block (p, y) takes rows of the items that
+// part p belongs to: of an item of n parts, rows k, k + n Y, ... with k = Y (p - first) + y, so that few
+// items of many parts keep as many blocks busy as many items of few.  The four warps share a row's parts,
+// or, where the parts are few, take rows of their own; either way the first parts are asked for before the
+// weights are known.
 constexpr int kJoinWarps = 4;
+constexpr int kJoinAhead = 4;
+constexpr int kJoinFew = 8;  // up to so many parts, a warp joins a row by itself (20 -> 8 us for 64 rows of 2 parts)
 template <bool BF16>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, int row_tile, int parts) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float s_f[kMaxParts];
+    __shared__ float4 s_acc[kJoinWarps][32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     wait_primary();
     if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
         int err = 0;
@@ -514,40 +511,115 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
         err = __reduce_max_sync(0xffffffffu, err);
         if (lane == 0) *a.status = err;
     }
-    const PartItem it = a.items[blockIdx.x];
-    if (it.last < 0) return;
-    const int first = blockIdx.x, n = it.last - first + 1;  // parts: the first block's head, then tails
-    auto slot_of = [&](int i) { return (size_t)(2 * (first + i) + (i == 0 ? kHead : kTail)); };
-    for (int row = blockIdx.y * kJoinWarps + warp; row < it.rows; row += gridDim.y * kJoinWarps) {
-        float mm = -CUDART_INF_F, ll = 0.f;
-        for (int i = lane; i < n; i += 32) mm = fmaxf(mm, a.part_ml[slot_of(i) * row_tile + row].x);
-        mm = warp_max(mm);
-        const float ref = mm == -CUDART_INF_F ? 0.f : mm;
-        for (int i = lane; i < n; i += 32) {
-            const float2 ml = a.part_ml[slot_of(i) * row_tile + row];
-            if (ml.y != 0.f) ll = fmaf(ml.y, ex2(ml.x - ref), ll);
-        }
-        ll = warp_sum(ll);
-        const float vscale = a.v_scale ? __ldg(a.v_scale + it.head) : 1.f;
-        const float inv = ll == 0.f ? 0.f : vscale / ll;
-        const long long at = attn_out_row(a, it.token0, it.head, it.row0 + row);
-        for (int col = 4 * lane; col < a.D; col += 128) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-                const float2 ml = a.part_ml[slot_of(i) * row_tile + row];
-                const float4 y = *reinterpret_cast<const float4*>(a.part_o + (slot_of(i) * row_tile + row) * a.D + col);
-                const float f = ml.y == 0.f ? 0.f : ex2(ml.x - ref);
-                if (f != 0.f) {  // NaN is not 0: it goes on
-                    v.x = fmaf(y.x, f, v.x);
-                    v.y = fmaf(y.y, f, v.y);
-                    v.z = fmaf(y.z, f, v.z);
-                    v.w = fmaf(y.w, f, v.w);
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+        const PartDesc it = a.items[blockIdx.x].d[side];
+        if (it.first < 0) continue;
+        const int n = it.last - it.first + 1;  // parts: the first block's head, then tails
+        auto slot_of = [&](int i) { return (size_t)(2 * (it.first + i) + (i == 0 ? kHead : kTail)); };
+        if (n <= kJoinFew) {
+            const int worker = (((int)blockIdx.x - it.first) * gridDim.y + blockIdx.y) * kJoinWarps + warp;
+#pragma unroll 1
+            for (int row = worker; row < it.rows; row += n * gridDim.y * kJoinWarps) {
+                const float2 ml = lane < n ? a.part_ml[slot_of(lane) * row_tile + row] : make_float2(-CUDART_INF_F, 0.f);
+                const float vscale = a.v_scale ? __ldg(a.v_scale + it.head) : 1.f;
+                const long long at = attn_out_row(a, it.token0, it.head, it.row0 + row);
+#pragma unroll 1
+                for (int col = 4 * lane; col - 4 * lane < a.D; col += 128) {
+                    const bool in = col < a.D;
+                    float4 y[kJoinFew];
+#pragma unroll
+                    for (int i = 0; i < kJoinFew; ++i)
+                        if (i < n && in)
+                            y[i] = *reinterpret_cast<const float4*>(a.part_o + (slot_of(i) * row_tile + row) * a.D + col);
+                    const float mm = warp_max(ml.x);
+                    const float f = ml.y == 0.f ? 0.f : ex2(ml.x - (mm == -CUDART_INF_F ? 0.f : mm));
+                    const float ll = warp_sum(ml.y * f);
+                    const float inv = ll == 0.f ? 0.f : vscale / ll;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < kJoinFew; ++i) {
+                        const float fi = __shfl_sync(0xffffffffu, f, i);
+                        if (i < n && in) {
+                            v.x = fmaf(y[i].x, fi, v.x);
+                            v.y = fmaf(y[i].y, fi, v.y);
+                            v.z = fmaf(y[i].z, fi, v.z);
+                            v.w = fmaf(y[i].w, fi, v.w);
+                        }
+                    }
+                    if (in) store_out4<BF16>(a, at, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                    if (a.lse && col == 0) a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll)) * kLn2;
                 }
             }
-            store_out4<BF16>(a, at, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+            continue;
         }
-        if (a.lse && lane == 0) a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll)) * kLn2;
+#pragma unroll 1
+        for (int row = ((int)blockIdx.x - it.first) * gridDim.y + blockIdx.y; row < it.rows; row += n * gridDim.y) {
+            const float vscale = a.v_scale ? __ldg(a.v_scale + it.head) : 1.f;
+            float ll = 0.f, mm = -CUDART_INF_F;
+#pragma unroll 1
+            for (int col = 4 * lane; col - 4 * lane < a.D; col += 128) {
+                const bool in = col < a.D;
+                auto part = [&](int i) {
+                    return *reinterpret_cast<const float4*>(a.part_o + (slot_of(i) * row_tile + row) * a.D + col);
+                };
+                float4 y[kJoinAhead];
+#pragma unroll
+                for (int u = 0; u < kJoinAhead; ++u) {
+                    const int i = warp + u * kJoinWarps;
+                    y[u] = in && i < n ? part(i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                if (col < 128) {  // the parts' weights, once a row
+                    for (int i = tid; i < n; i += 32 * kJoinWarps) s_f[i] = a.part_ml[slot_of(i) * row_tile + row].x;
+                    __syncthreads();
+                    for (int i = lane; i < n; i += 32) mm = fmaxf(mm, s_f[i]);
+                    mm = warp_max(mm);
+                    const float ref = mm == -CUDART_INF_F ? 0.f : mm;
+                    __syncthreads();
+                    for (int i = lane; i < n; i += 32) {  // (every warp: the same sum in the same order)
+                        const float2 ml = a.part_ml[slot_of(i) * row_tile + row];
+                        const float f = ml.y == 0.f ? 0.f : ex2(ml.x - ref);
+                        ll = fmaf(ml.y, f, ll);
+                        if (warp == 0) s_f[i] = f;
+                    }
+                    ll = warp_sum(ll);
+                    __syncthreads();
+                }
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                auto add = [&](float f, const float4& x) {
+                    v.x = fmaf(x.x, f, v.x);
+                    v.y = fmaf(x.y, f, v.y);
+                    v.z = fmaf(x.z, f, v.z);
+                    v.w = fmaf(x.w, f, v.w);
+                };
+#pragma unroll
+                for (int u = 0; u < kJoinAhead; ++u) {
+                    const int i = warp + u * kJoinWarps;
+                    if (i < n) add(s_f[i], y[u]);
+                }
+                if (in)
+#pragma unroll 4
+                    for (int i = warp + kJoinAhead * kJoinWarps; i < n; i += kJoinWarps) add(s_f[i], part(i));
+                s_acc[warp][lane] = v;
+                __syncthreads();
+                if (warp == 0 && in) {
+                    const float inv = ll == 0.f ? 0.f : vscale / ll;
+                    float4 t = s_acc[0][lane];
+#pragma unroll
+                    for (int x = 1; x < kJoinWarps; ++x) {
+                        const float4 z = s_acc[x][lane];
+                        t.x += z.x;
+                        t.y += z.y;
+                        t.z += z.z;
+                        t.w += z.w;
+                    }
+                    const long long at = attn_out_row(a, it.token0, it.head, it.row0 + row);
+                    store_out4<BF16>(a, at, col, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
+                    if (a.lse && col == 0) a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll)) * kLn2;
+                }
+                __syncthreads();
+            }
+        }
     }
 }
 
@@ -688,7 +760,7 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(parts, tc ? 8 : kRows / kJoinWarps);
+    cfg.gridDim = dim3(parts, 8);
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = s;
     cfg.attrs = attr;

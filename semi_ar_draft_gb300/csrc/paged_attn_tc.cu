@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
     // by a whole warp, with one answer for all lanes
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     attn_tail_rows(a, (size_t)part * C::kThreads + tid, (size_t)parts * C::kThreads);
-    PartItem mine{-1, 0, 0, 0, 0, 0, {0, 0}};
+    PartItem* mine = a.items + part;  // written by thread 0
+    if (tid == 0) mine->d[kTail].first = mine->d[kHead].first = -1;
 
     if (C::loader_of(warp) >= 0) {
         // ---------------------------------------------------------------- loaders
@@ -627,13 +628,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                     else if (a.lse)
                         a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll)) * kLn2;
                 }
-                if (!last_of_item && seg_first == 0) {  // the item ends in the block that holds its last unit
-                    mine.last = (int)((start.end + (w.kts - 1 - w.kt) - 1) / start.per);
-                    mine.row0 = row0;
-                    mine.rows = rows;
-                    mine.token0 = w.r.token0;
-                    mine.head = head;
-                }
+                if (!whole && tid == 0) mine->d[seg_first == 0 ? kHead : kTail] = part_desc(start, w, row0, rows, head);
                 tc_fence_before();
                 if (!meet()) break;  // the outputs are zero again, and the statistics have been read
                 tc_fence_after();
@@ -647,10 +642,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
     __syncthreads();
     tc_fence_after();
     if (warp == kAllocWarp) tmem_dealloc(tmem, 512);
-    if (tid == 0) {
-        mine.err = bars->status ? bars->status : (bad ? DSPARK_ERR_CACHE : 0);
-        a.items[part] = mine;
-    }
+    if (tid == 0) mine->err = bars->status ? bars->status : (bad ? DSPARK_ERR_CACHE : 0);
 }
 
 template <bool BF16, int DP>
