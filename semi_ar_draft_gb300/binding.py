@@ -146,7 +146,9 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the address of torch's current stream, without the Stream object that
+        # torch.cuda.current_stream() makes around it (0.2 us against 2.9 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -302,11 +304,12 @@ def _rows_ptr(t):
 
 def pool_layout(k_pages, v_pages):
     """(pages, page_size, Hk, D, page / token / head stride) of two pools [pages, page_size, Hk, D]."""
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
+    shape, stride = k_pages.shape, k_pages.stride()
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.stride() != stride:
         raise ValueError("k_pages and v_pages are [pages, page_size, Hk, D] of one shape and layout")
-    if k_pages.dtype != v_pages.dtype:
+    if k_pages.dtype is not v_pages.dtype:
         raise TypeError("k_pages and v_pages are of one type")
-    return (*k_pages.shape, *k_pages.stride()[:3])
+    return (*shape, stride[0], stride[1], stride[2])
 
 
 def dspark_cache_workspace_size(p: CacheParams) -> int:
