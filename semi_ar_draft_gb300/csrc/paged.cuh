@@ -7,7 +7,10 @@
 // (request, kv head, row tile, key tile), form one list of units that is cut into equal contiguous
 // ranges, one a block.  The lengths are on the device only, so every block adds them up itself (a
 // block-wide prefix sum over the requests) and finds its own range; nothing is planned on the host
-// and a call can be replayed from a graph with other lengths.
+// and a call can be replayed from a graph with other lengths.  An item's beginning and end (its queries,
+// the meeting of the warps, its rows written) cost about as much as a few key tiles, so each item
+// counts `extra` units before its first tile; without them the block that met a run of one-tile items took
+// a third longer than the others.
 //
 // Join.  A range may begin or end inside an item.  Such a segment's (maximum, sum, unnormalised output)
 // goes to one of the block's two partial buffers -- kTail when the segment does not begin the item,
@@ -27,6 +30,7 @@ struct AttnArgs {
     uint32_t g_mul, g_shift;  // row / G = umulhi(2 row, g_mul) >> g_shift for rows below 2^31 (group_division)
     int page_shift, num_pages, max_blocks;
     int causal, window;
+    int q_pairs;  // rows of q start on 4-byte boundaries
     float scale, softcap;
     const unsigned char* q;
     long long q_token, q_head;  // strides, elements
@@ -111,7 +115,7 @@ struct AttnScratch {  // in shared memory, for attn_start
 // Adds up all requests' units and finds the range of block `part` of `parts`.  All threads of the block.
 // min_units: a block takes no fewer (a short range would cost more to join than it saves).
 template <int THREADS>
-__device__ AttnStart attn_start(const AttnArgs& a, int row_tile, int key_tile, int parts, int part, int min_units,
+__device__ AttnStart attn_start(const AttnArgs& a, int row_tile, int key_tile, int extra, int parts, int part, int min_units,
                                 AttnScratch* scratch, bool* bad) {
     static_assert(THREADS / 32 <= 16, "scratch");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -122,7 +126,7 @@ __device__ AttnStart attn_start(const AttnArgs& a, int row_tile, int key_tile, i
     for (int j = j0; j < j1; ++j) {
         const AttnReq r = attn_request(a, j);
         b |= r.bad;
-        u += (long long)row_tiles(a, r.n, row_tile) * a.Hk * key_tiles(r, key_tile);
+        u += (long long)row_tiles(a, r.n, row_tile) * a.Hk * (key_tiles(r, key_tile) + extra);
     }
     long long inc = u;
 #pragma unroll
@@ -149,7 +153,7 @@ __device__ AttnStart attn_start(const AttnArgs& a, int row_tile, int key_tile, i
         int j = j0;
         for (; j < j1; ++j) {
             const AttnReq r = attn_request(a, j);
-            const long long x = (long long)row_tiles(a, r.n, row_tile) * a.Hk * key_tiles(r, key_tile);
+            const long long x = (long long)row_tiles(a, r.n, row_tile) * a.Hk * (key_tiles(r, key_tile) + extra);
             if (s.begin < at + x) break;
             at += x;
         }
@@ -162,11 +166,11 @@ __device__ AttnStart attn_start(const AttnArgs& a, int row_tile, int key_tile, i
     return s;
 }
 
-// A walk over a block's units, one key tile at a time.
+// A walk over a block's range, one key tile at a time.
 struct AttnWalk {
     AttnReq r;
-    int j, item, items, kt, kts, rts, kt_first;
-    long long left;  // units left in the block's range, this one included
+    int j, item, items, kt, kts, rts, kt_first, extra;
+    long long left;  // units left in the block's range, this tile's included
     __device__ __forceinline__ bool done() const { return left <= 0; }
 };
 __device__ __forceinline__ void walk_request(const AttnArgs& a, AttnWalk& w, int row_tile, int key_tile) {
@@ -176,25 +180,31 @@ __device__ __forceinline__ void walk_request(const AttnArgs& a, AttnWalk& w, int
     w.kts = key_tiles(w.r, key_tile);
     w.kt_first = w.r.lo / key_tile;
 }
-__device__ __forceinline__ AttnWalk walk_begin(const AttnArgs& a, const AttnStart& s, int row_tile, int key_tile) {
+__device__ __forceinline__ AttnWalk walk_begin(const AttnArgs& a, const AttnStart& s, int row_tile, int key_tile, int extra) {
     AttnWalk w;
     w.left = s.end - s.begin;
     w.j = s.j;
     w.item = w.kt = 0;
     w.items = w.kts = w.rts = 1;
     w.kt_first = 0;
+    w.extra = extra;
     w.r = AttnReq{0, 0, 0, 0, false};
     if (w.left > 0) {
         walk_request(a, w, row_tile, key_tile);
-        w.item = (int)(s.at / w.kts);
-        w.kt = (int)(s.at - (long long)w.item * w.kts);
+        w.item = (int)(s.at / (w.kts + extra));
+        w.kt = (int)(s.at - (long long)w.item * (w.kts + extra)) - extra;
+        if (w.kt < 0) {  // the range begins before the item's first tile
+            w.left += w.kt;
+            w.kt = 0;
+        }
     }
     return w;
 }
 __device__ __forceinline__ void walk_next(const AttnArgs& a, AttnWalk& w, int row_tile, int key_tile) {
     --w.left;
-    if (++w.kt < w.kts) return;
+    if (++w.kt < w.kts || w.left <= 0) return;
     w.kt = 0;
+    w.left -= w.extra;
     if (++w.item < w.items || w.left <= 0) return;
     w.item = 0;
     do {  // requests without new tokens have no units

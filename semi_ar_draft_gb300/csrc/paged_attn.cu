@@ -74,6 +74,7 @@ struct Rows16 {
     static constexpr int kHalf = kKeys * kRowBytes;      // K (or V) of a slice
     static constexpr int kStage = 2 * kHalf;             // = 64 DP: also a warp's output in fp32
     static constexpr int kStages = DP == 64 ? 6 : 3;
+    static constexpr int kExtra = DP == 64 ? 4 : 2;      // what an item costs beside its key tiles
     static constexpr int kBlocksPerSm = DP == 256 ? 1 : 2;
     static constexpr bool kQInSmem = DP == 256;          // 64 registers of q beside 128 of output do not fit
     static constexpr int kQBytes = kQInSmem ? DP / 16 * 32 * 16 : 0;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
     launch_dependents();
     if (tid == 0) s_err = 0;
     bool bad;
-    const AttnStart start = attn_start<kThreads>(a, kRows, C::kKeyTile, parts, part, 2, &s_start, &bad);
+    const AttnStart start = attn_start<kThreads>(a, kRows, C::kKeyTile, C::kExtra, parts, part, 2 + C::kExtra, &s_start, &bad);
 
     attn_tail_rows(a, (size_t)part * kThreads + tid, (size_t)parts * kThreads);
     unsigned char* ring = smem + (size_t)warp * C::kStages * C::kStage;
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
     int err = bad ? DSPARK_ERR_CACHE : 0;
 
     // ---- loads: `ld` walks ahead of the arithmetic; `pid` is the page of this lane's key of its slice
-    AttnWalk ld = walk_begin(a, start, kRows, C::kKeyTile);
+    AttnWalk ld = walk_begin(a, start, kRows, C::kKeyTile, C::kExtra);
     auto slice_key = [&](const AttnWalk& w) { return (w.kt_first + w.kt) * C::kKeyTile + warp * C::kKeys; };
     auto fetch_page = [&]() -> int {
         const int key = slice_key(ld) + lane;
@@ -128,6 +129,18 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
     };
     int pid = fetch_page();
     int ld_stage = 0;
+    // An item's queries, asked for (into L1) when its first keys are: 16 rows of up to four 128-byte lines.
+    auto touch_queries = [&]() {
+        const int head = ld.item / ld.rts, first = (ld.item - head * ld.rts) * kRows;
+        const int last = min(ld.r.n * a.G, first + kRows);
+        for (int i = lane; i < kRows * (DP / 64); i += 32) {
+            const int row = first + i / (DP / 64), token = attn_token(a, row), d = 64 * (i % (DP / 64));
+            if (row < last && d < a.D)
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + 2 * ((ld.r.token0 + token) * a.q_token +
+                                                                        (head * a.G + row - token * a.G) * a.q_head + d)));
+        }
+    };
+    if (warp == 0 && !ld.done()) touch_queries();
     auto load_step = [&]() {
         if (!ld.done() && slice_key(ld) < ld.r.seq) {
             const int key = slice_key(ld) + lane;
@@ -156,13 +169,14 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
         if (!ld.done()) {
             walk_next(a, ld, kRows, C::kKeyTile);
             pid = fetch_page();
+            if (warp == 0 && ld.kt == 0 && !ld.done()) touch_queries();
         }
     };
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) load_step();
 
     // ---- arithmetic
-    AttnWalk w = walk_begin(a, start, kRows, C::kKeyTile);
+    AttnWalk w = walk_begin(a, start, kRows, C::kKeyTile, C::kExtra);
     PartItem* mine = a.items + part;  // written by thread 0
     if (tid == 0) mine->d[kTail].first = mine->d[kHead].first = -1;
     float o[DT][4];
@@ -198,10 +212,11 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
                 l[r] = 0.f;
                 row_scale[r] = a.scale * (F8 && a.k_scale ? __ldg(a.k_scale + head) : 1.f);
             }
-            // Two consecutive values of q, as the MMA's pair (16-bit loads: q may start at any element).
+            // Two consecutive values of q, as the MMA's pair (q may start at any element: then one by one).
             auto pair = [&](int r, int d) -> uint32_t {
                 if (!real[r] || d >= a.D) return 0u;
                 const uint16_t* p = reinterpret_cast<const uint16_t*>(qrow[r]) + d;
+                if (a.q_pairs) return __ldg(reinterpret_cast<const uint32_t*>(p));
                 return (uint32_t)__ldg(p) | ((uint32_t)__ldg(p + 1) << 16);
             };
             auto load_q = [&](auto&& put) {
@@ -727,6 +742,7 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     a.q = static_cast<const unsigned char*>(q);
     a.q_token = p->q_token_stride;
     a.q_head = p->q_head_stride;
+    a.q_pairs = !((uintptr_t)q & 3u) && p->q_token_stride % 2 == 0 && p->q_head_stride % 2 == 0;
     a.k_pages = static_cast<const unsigned char*>(k_pages);
     a.v_pages = static_cast<const unsigned char*>(v_pages);
     a.page = p->kv_page_stride * esz;

@@ -29,6 +29,7 @@ struct TcAttn {
     static constexpr int kStreams = DP == 256 ? 1 : 2;
     static constexpr int kKt = DP == 256 ? 32 : 64;  // keys of a tile
     static constexpr int kUnit = kStreams * kKt;
+    static constexpr int kExtra = DP == 128 ? 2 : 4;  // what an item costs beside its key tiles
     static constexpr int kSoftmaxWarps = 4 * kStreams;
     static constexpr int kLoaders = 4;
     // Warps after the softmax's: multiprocessor quarter (warp % 4) 0 has none of them and quarter 1 the MMA
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
     }
     tc_fence_before();
     bool bad;
-    AttnStart start = attn_start<C::kThreads>(a, kTcRowTile, C::kUnit, parts, part, 2, &bars->scratch, &bad);  // (barriers inside)
+    AttnStart start = attn_start<C::kThreads>(a, kTcRowTile, C::kUnit, C::kExtra, parts, part, 2 + C::kExtra, &bars->scratch, &bad);  // (barriers inside)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         const uint32_t page16 = (uint32_t)(a.page >> 4), token16 = (uint32_t)(a.token >> 4);
         const unsigned char* k_at = a.k_pages + chunk * 16;
         const long long v_after_k = a.v_pages - a.k_pages;
-        AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit);
+        AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit, C::kExtra);
         int err = 0, seg = 0, stream = 0;
         auto tile_key = [&]() { return (w.kt_first + w.kt) * C::kUnit + stream * KT; };
         // Pages of the next tile's keys (lane: keys lane and lane + 32), asked for a tile ahead.  The load is
@@ -320,8 +321,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         const uint32_t k_hi = (uint32_t)(k_desc >> 32), k_lo = (uint32_t)k_desc & 0xffff0000u;
         const uint32_t v_hi = (uint32_t)(v_desc >> 32), v_lo = (uint32_t)v_desc & 0xffff0000u;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit);
-        const int units = __shfl_sync(0xffffffffu, (int)w.left, 0);
+        AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit, C::kExtra);
         const int s = C::mma_of(warp);
         int seg = 0, slot = s, turn = 0, held = 0;  // turn: parity of the ring's round; held: the slot whose values
         bool ok = true, behind = false;             // are still to come, if behind
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
             commit_elect(&bars->pvdone[s]);
             return true;
         };
-        for (int unit = 0; unit < units && ok; ++unit) {
+        for (int unit = 0; ok && __shfl_sync(0xffffffffu, !w.done(), 0); ++unit) {
             const int qb = seg % C::kQBufs;
             if (!warp_wait(&bars->full[slot], (uint32_t)turn) ||
                 (unit > 0 && !warp_wait(&bars->sfree[s], (uint32_t)((unit - 1) & 1))))
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
             if (lane == 0) mbar_arrive_local(&bars->smeet[s]);
             return warp_wait(&bars->smeet[s], smeets++ & 1);
         };
-        AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit);
+        AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit, C::kExtra);
         float m = -CUDART_INF_F, l = 0.f;
         int n = 0, seg_first = 0, row0 = 0, rows = 0, head = 0, see_lo = 0, see_hi = 0, all_lo = 0, all_hi = 0;
         bool fresh = true, ok = meet();
