@@ -73,10 +73,15 @@ struct Rows16 {
     static constexpr int kChunks = kRowBytes / 16;       // 16-byte groups of a row
     static constexpr int kHalf = kKeys * kRowBytes;      // K (or V) of a slice
     static constexpr int kStage = 2 * kHalf;             // = 64 DP: also a warp's output in fp32
-    static constexpr int kStages = DP == 64 ? 6 : 3;
+    // Blocks a multiprocessor and stages a warp, measured: 16-bit heads of 128 want two blocks of three (98
+    // us for 32 requests up to 8192 tokens, 102 us with three of two); heads of 64, and 8-bit ones of 128, which
+    // are bound by their conversions, three blocks (62 against 74 us; 221 against 238 us).
+    static constexpr bool kThree = DP == 64 || (F8 && DP == 128);
+    static constexpr int kStages = DP == 64 ? 4 : (kThree ? 2 : 3);
     static constexpr int kExtra = DP == 64 ? 4 : 2;      // what an item costs beside its key tiles
-    static constexpr int kBlocksPerSm = DP == 256 ? 1 : 2;
-    static constexpr bool kQInSmem = DP == 256;          // 64 registers of q beside 128 of output do not fit
+    static constexpr int kBlocksPerSm = DP == 256 ? 1 : (kThree ? 3 : 2);
+    // Registers: 64 of q beside 128 of output do not fit a thread, nor 32 beside 64 three blocks.
+    static constexpr bool kQInSmem = DP == 256 || (kThree && DP == 128);
     static constexpr int kQBytes = kQInSmem ? DP / 16 * 32 * 16 : 0;
     static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage + kQBytes;
     static_assert(kStage == kRows * DP * 4, "a stage holds a warp's output");
@@ -666,7 +671,7 @@ struct AttnWs {
 // the mean number of tokens where it is not given) against the 16 of the other kernel.
 bool wide_rows(const dspark_attention_params* p) {
     const int n = p->max_new > 0 ? p->max_new : (p->T + p->B - 1) / p->B;
-    return p->kv_dtype == p->dtype && (long long)n * (p->Hq / p->Hk) > kRows;
+    return (long long)n * (p->Hq / p->Hk) > kRows;
 }
 AttnWs attn_ws(const dspark_attention_params* p) {
     const size_t rows = wide_rows(p) ? (size_t)2 * kMaxTcParts * kTcRows : (size_t)2 * kMaxParts * kRows;
@@ -763,7 +768,7 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     int parts = 0;
     const bool aligned_q = !((uintptr_t)q & 15u) && p->q_token_stride % 8 == 0 && p->q_head_stride % 8 == 0;
     const bool tc = wide_rows(p) && aligned_q;
-    const dspark_status ls = tc     ? launch_attn_tc(a, bf16, sms, s, &parts)
+    const dspark_status ls = tc     ? launch_attn_tc(a, bf16, e4m3, sms, s, &parts)
                              : bf16 ? (e4m3 ? launch_rows16_d<true, true>(a, sms, s, &parts)
                                           : launch_rows16_d<true, false>(a, sms, s, &parts))
                                   : (e4m3 ? launch_rows16_d<false, true>(a, sms, s, &parts)
