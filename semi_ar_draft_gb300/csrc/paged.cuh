@@ -281,8 +281,8 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Row tiles of 128 on the fifth-generation tensor cores (paged_attn_tc.cu); needs 16-byte aligned query
-// rows.
-dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, bool e4m3, int sms, cudaStream_t s, int* parts);
+// Row tiles of 128 on the fifth-generation tensor cores (paged_attn_tc.cu): 16-bit caches, 16-byte
+// aligned query rows.
+dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int sms, cudaStream_t s, int* parts);
 
 }  // namespace dspark

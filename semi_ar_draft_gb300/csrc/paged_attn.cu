@@ -668,10 +668,12 @@ struct AttnWs {
     size_t items, ml, o, bytes;
 };
 // Whether a call takes row tiles of 128: the most rows a request and kv head can have (from max_new, or
-// the mean number of tokens where it is not given) against the 16 of the other kernel.
+// the mean number of tokens where it is not given) against the 16 of the other kernel, and a 16-bit cache.
+// (8-bit tiles widened on their way into the wide kernel's ring took 101 us where five row tiles of 16 take
+// 65, and 170 against 195 with heads of 256: not worth a second path.)
 bool wide_rows(const dspark_attention_params* p) {
     const int n = p->max_new > 0 ? p->max_new : (p->T + p->B - 1) / p->B;
-    return (long long)n * (p->Hq / p->Hk) > kRows;
+    return p->kv_dtype == p->dtype && (long long)n * (p->Hq / p->Hk) > kRows;
 }
 AttnWs attn_ws(const dspark_attention_params* p) {
     const size_t rows = wide_rows(p) ? (size_t)2 * kMaxTcParts * kTcRows : (size_t)2 * kMaxParts * kRows;
@@ -768,7 +770,7 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     int parts = 0;
     const bool aligned_q = !((uintptr_t)q & 15u) && p->q_token_stride % 8 == 0 && p->q_head_stride % 8 == 0;
     const bool tc = wide_rows(p) && aligned_q;
-    const dspark_status ls = tc     ? launch_attn_tc(a, bf16, e4m3, sms, s, &parts)
+    const dspark_status ls = tc     ? launch_attn_tc(a, bf16, sms, s, &parts)
                              : bf16 ? (e4m3 ? launch_rows16_d<true, true>(a, sms, s, &parts)
                                           : launch_rows16_d<true, false>(a, sms, s, &parts))
                                   : (e4m3 ? launch_rows16_d<false, true>(a, sms, s, &parts)

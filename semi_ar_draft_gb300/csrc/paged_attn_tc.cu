@@ -14,7 +14,7 @@
 //
 // Values are the second product's B operand as they lie in the cache (one row a key, so N-major).
 // An output starts at zero, so every product accumulates; it is scaled when a row's maximum has grown by
-// 2^8, which needs the stream's earlier products done, and P's buffer needs that anyway.
+// 2^8, which needs the stream's earlier products done.
 #include "host_util.h"
 #include "paged.cuh"
 #include "tc05.cuh"
@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kTcRowTile = 128;
 
-template <bool F8, int DP>
+template <int DP>
 struct TcAttn {
     static constexpr int kStreams = DP == 256 ? 1 : 2;
     static constexpr int kKt = DP == 256 ? 32 : 64;  // keys of a tile
@@ -48,17 +48,13 @@ struct TcAttn {
     static constexpr int kTile = kKt * DP * 2;            // bytes of a tile's K (or V)
     static constexpr int kQ = kTcRowTile * DP * 2;
     static constexpr int kQBufs = DP == 256 ? 1 : 2;
-    static constexpr int kSlots = F8 ? (DP == 64 ? 8 : 3) : (DP == 64 ? 10 : (DP == 128 ? 5 : 4));
-    // 8-bit caches: tiles as they lie in the cache, on their way to a slot, thread by thread
-    static constexpr int kRawTile = 2 * kKt * DP;
-    static constexpr int kRawSlots = F8 ? (DP == 64 ? 6 : 4) : 0;
+    static constexpr int kSlots = DP == 64 ? 10 : (DP == 128 ? 5 : 4);
     static constexpr int kRing = kQBufs * kQ;
-    static constexpr int kRaw = kRing + kSlots * 2 * kTile;
-    static constexpr int kMeta = kRaw + kRawSlots * kRawTile;
+    static constexpr int kMeta = kRing + kSlots * 2 * kTile;
     static constexpr size_t kSmem = (size_t)kMeta + 2 * kTcRowTile * 8 + 512;
     // tensor memory columns
     static constexpr int kColS = kStreams * DP, kColP = kColS + kStreams * kKt;
-    static_assert(kColP + kStreams * kKt / 2 <= 512, "tensor memory");
+    static_assert(kColP + kStreams * kKt <= 512, "tensor memory");  // (two buffers of P a stream)
     static_assert(kSmem <= kMaxSmem, "shared memory");
 };
 
@@ -121,27 +117,6 @@ __device__ __forceinline__ float from16(uint32_t half) {
     return BF16 ? bf16_bits_to_f32(half & 0xffffu) : __half2float(__ushort_as_half((unsigned short)half));
 }
 
-// Sixteen e4m3 values as bf16 or fp16 values (both hold them exactly), in order.
-template <bool BF16>
-__device__ __forceinline__ void widen16(const uint4 v, uint4& lo, uint4& hi) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t r[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t h;
-        const uint32_t pair = i & 1 ? w[i >> 1] >> 16 : w[i >> 1];
-        asm("{ .reg .b16 x; cvt.u16.u32 x, %1; cvt.rn.f16x2.e4m3x2 %0, x; }" : "=r"(h) : "r"(pair));
-        if (BF16) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            r[i] = pack16<true>(f.x, f.y);
-        } else {
-            r[i] = h;
-        }
-    }
-    lo = make_uint4(r[0], r[1], r[2], r[3]);
-    hi = make_uint4(r[4], r[5], r[6], r[7]);
-}
-
 // MMAs and commits by one elected lane of a converged warp (always the same one).  Descriptors come in
 // halves; kind::f16, fp32 accumulation; accumulate = 0 overwrites D.
 __device__ __forceinline__ void mma_elect_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
@@ -183,10 +158,9 @@ struct TcBars {
 };
 static_assert(sizeof(TcBars) <= 512, "barriers");
 
-template <bool BF16, bool F8, int DP>
-__global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(AttnArgs a, uint64_t limit_ns) {
-    using C = TcAttn<F8, DP>;
-    constexpr bool VB = BF16 && !F8;  // P and V: an 8-bit cache's values meet the probabilities as halves
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnArgs a, uint64_t limit_ns) {
+    using C = TcAttn<DP>;
     constexpr int KT = C::kKt, NS = C::kStreams;
     extern __shared__ __align__(1024) unsigned char smem[];
     float2* s_ml = reinterpret_cast<float2*>(smem + C::kMeta);  // [kStreams][128]
@@ -240,27 +214,28 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
 
     if (C::loader_of(warp) >= 0) {
         // ---------------------------------------------------------------- loaders
-        constexpr int kChunks = DP / (F8 ? 16 : 8);  // 16-byte groups of a row in the cache
+        constexpr int kChunks = DP / 8;              // 16-byte groups of a row
         constexpr int kPer = 32 / kChunks;           // rows a warp copies at a time
         const int lw = C::loader_of(warp);
         const int chunk = lane % kChunks, sub_row = lane / kChunks;
-        const bool inside = chunk * (F8 ? 16 : 8) < a.D;
+        const bool inside = chunk * 8 < a.D;
         const uint32_t base = smem_addr(smem);
         const uint32_t mask = (1u << a.page_shift) - 1;
         const uint32_t page16 = (uint32_t)(a.page >> 4), token16 = (uint32_t)(a.token >> 4);
         const unsigned char* k_at = a.k_pages + chunk * 16;
         const long long v_after_k = a.v_pages - a.k_pages;
         AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit, C::kExtra);
-        int err = 0, seg = 0, stream = 0;
-        auto tile_key = [&]() { return (w.kt_first + w.kt) * C::kUnit + stream * KT; };
-        // Pages of the next tile's keys (lane: keys lane and lane + 32), asked for a tile ahead.  The load is
-        // unconditional (entry 0 where there is no key) and looked at when the tile's copies are issued, so
-        // that nothing waits for it here.
-        int pid[KT / 32];
+        int err = 0, seg = 0;
+        auto unit_key = [&]() { return (w.kt_first + w.kt) * C::kUnit; };
+        // Pages of the next unit's keys (lane: keys lane, lane + 32, ...), asked for a unit ahead.  The load is
+        // unconditional (entry 0 where there is no key) and looked at when the copies are issued, so that
+        // nothing waits for it here.
+        constexpr int kPids = C::kUnit / 32;
+        int pid[kPids];
         auto fetch_pages = [&]() {
 #pragma unroll
-            for (int h = 0; h < KT / 32; ++h) {
-                const int key = min(tile_key() + 32 * h + lane, w.r.seq - 1);
+            for (int h = 0; h < kPids; ++h) {
+                const int key = min(unit_key() + 32 * h + lane, w.r.seq - 1);
                 const size_t at = w.done() || key < 0 ? 0 : (size_t)w.j * a.max_blocks + (key >> a.page_shift);
                 pid[h] = __ldg(a.block_table + at);
             }
@@ -268,110 +243,58 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
         fetch_pages();
         bool fresh = true;
         int head = 0, slot = 0, round = 0;
-        // 8-bit caches: `ahead` raw tiles are on their way; the oldest, once landed, is written to its slot as
-        // 16-bit values (keys in q's type, values as halves: both exact) by the threads that copied it.
-        int raw_slot = 0, raw_old = 0, ahead = 0;
-        const int lt = lw * 32 + lane;
-        const uint32_t raw = base + C::kRaw;
-        auto convert = [&]() {
-            if (round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) return false;
-            const uint32_t to = (uint32_t)slot * (2 * C::kTile) + C::kRing;
-            const uint4* from = reinterpret_cast<const uint4*>(smem + C::kRaw + raw_old * C::kRawTile) + lt;
-#pragma unroll 2
-            for (int u = 0; u < KT / kPer / C::kLoaders; ++u) {
-                const int r = (u * C::kLoaders + lw) * kPer + sub_row;
-                const uint32_t lo = to + (uint32_t)((2 * chunk) >> 3) * (KT * 128);
-                const uint32_t at0 = lo + sw128_offset(r, (2 * chunk) & 7), at1 = lo + sw128_offset(r, (2 * chunk + 1) & 7);
-                uint4 x, y;
-                widen16<BF16>(from[(2 * u) * 32 * C::kLoaders], x, y);
-                *reinterpret_cast<uint4*>(smem + at0) = x;
-                *reinterpret_cast<uint4*>(smem + at1) = y;
-                widen16<false>(from[(2 * u + 1) * 32 * C::kLoaders], x, y);
-                *reinterpret_cast<uint4*>(smem + at0 + C::kTile) = x;
-                *reinterpret_cast<uint4*>(smem + at1 + C::kTile) = y;
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive_local(&bars->full[slot]);
-            if (++slot == C::kSlots) {
-                slot = 0;
-                ++round;
-            }
-            if (++raw_old == C::kRawSlots) raw_old = 0;
-            return true;
-        };
         while (!w.done()) {
             if (fresh) {
                 fresh = false;
                 head = w.item / w.rts;
                 const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
-                if (use > 0) {
-                    // The products that still read the buffer may be waiting for raw tiles.
-                    if (F8 && !__all_sync(0xffffffffu, mbar_try_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1)))) {
-                        asm volatile("cp.async.wait_all;" ::: "memory");
-                        while (ahead > 0 && convert()) --ahead;
-                    }
-                    if (!warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) break;
-                }
+                if (use > 0 && !warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) break;
                 ++seg;
                 const int row0 = (w.item - head * w.rts) * kTcRowTile;
                 const int rows = min(w.r.n * a.G - row0, kTcRowTile);
-                constexpr int kQChunks = DP / 8, kQPer = 32 / kQChunks;
-                const int qc = lane % kQChunks;
-                const uint32_t qbase = base + (uint32_t)qb * C::kQ + (uint32_t)(qc >> 3) * (kTcRowTile * 128);
-                for (int r = lw * kQPer + lane / kQChunks; r < ((rows + 31) & ~31); r += C::kLoaders * kQPer) {
-                    const bool real = qc * 8 < a.D && r < rows;
+                const uint32_t qbase = base + (uint32_t)qb * C::kQ + (uint32_t)(chunk >> 3) * (kTcRowTile * 128);
+                for (int r = lw * kPer + sub_row; r < ((rows + 31) & ~31); r += C::kLoaders * kPer) {
+                    const bool real = inside && r < rows;
                     const int row = row0 + r;
                     const int token = attn_token(a, row);
                     const long long src = real ? (w.r.token0 + token) * a.q_token +
-                                                     (head * a.G + row - token * a.G) * a.q_head + qc * 8
+                                                     (head * a.G + row - token * a.G) * a.q_head + chunk * 8
                                                : 0;
-                    copy16(qbase + sw128_offset(r, qc & 7), a.q + 2 * src, real);
+                    copy16(qbase + sw128_offset(r, chunk & 7), a.q + 2 * src, real);
                 }
             }
-            if (!F8 && round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) break;
-            {
-                const uint32_t key0 = (uint32_t)tile_key();
-                const unsigned char* head_at = k_at + head * a.head;
-                [[maybe_unused]] const uint32_t kb =
-                    base + C::kRing + (uint32_t)slot * (2 * C::kTile) + (uint32_t)(chunk >> 3) * (KT * 128);
+            const uint32_t key0 = (uint32_t)unit_key();
+            const unsigned char* head_at = k_at + head * a.head;
 #pragma unroll
-                for (int h = 0; h < KT / 32; ++h) {
-                    const bool none = (int)key0 + 32 * h + lane >= w.r.seq;
-                    if ((uint32_t)pid[h] >= (uint32_t)a.num_pages) {
-                        if (!none) err = DSPARK_ERR_CACHE;
-                        pid[h] = -1;
-                    }
-                    if (none) pid[h] = -1;
+            for (int h = 0; h < kPids; ++h) {
+                const bool none = (int)key0 + 32 * h + lane >= w.r.seq;
+                if ((uint32_t)pid[h] >= (uint32_t)a.num_pages) {
+                    if (!none) err = DSPARK_ERR_CACHE;
+                    pid[h] = -1;
                 }
+                if (none) pid[h] = -1;
+            }
+            bool ok = true;
+#pragma unroll 1
+            for (int stream = 0; stream < NS; ++stream) {  // (rolled: less code, and pid moves along)
+                if (round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + (uint32_t)(chunk >> 3) * (KT * 128);
 #pragma unroll
-                for (int u = 0; u < (KT / kPer + C::kLoaders - 1) / C::kLoaders; ++u) {
+                for (int u = 0; u < KT / kPer / C::kLoaders; ++u) {
                     const int i = u * C::kLoaders + lw;
-                    if ((u + 1) * C::kLoaders > KT / kPer && i >= KT / kPer) break;
                     const int r = i * kPer + sub_row;  // (32 rows are a whole number of steps)
                     const int p = __shfl_sync(0xffffffffu, KT > 32 && i * kPer >= 32 ? pid[KT / 32 - 1] : pid[0], r & 31);
                     const bool real = inside && p >= 0;
-                    const uint64_t at16 = (uint64_t)(uint32_t)max(p, 0) * page16 + (uint64_t)((key0 + r) & mask) * token16;
+                    const uint64_t at16 = (uint64_t)(uint32_t)max(p, 0) * page16 +
+                                          (uint64_t)((key0 + stream * KT + r) & mask) * token16;
                     const unsigned char* src = real ? head_at + 16 * at16 : a.k_pages;
-                    if (F8) {  // to the thread's own place among the raw tiles
-                        const uint32_t dst = raw + (uint32_t)(raw_slot * C::kRawTile + (u * 2 * 32 * C::kLoaders + lt) * 16);
-                        copy16(dst, src, real);
-                        copy16(dst + 32 * C::kLoaders * 16, src + v_after_k, real);
-                    } else {
-                        const uint32_t dst = kb + sw128_offset(r, chunk & 7);
-                        copy16(dst, src, real);
-                        copy16(dst + C::kTile, src + v_after_k, real);
-                    }
+                    const uint32_t dst = kb + sw128_offset(r, chunk & 7);
+                    copy16(dst, src, real);
+                    copy16(dst + C::kTile, src + v_after_k, real);
                 }
-            }
-            if constexpr (F8) {
-                cp_async_commit();
-                if (++raw_slot == C::kRawSlots) raw_slot = 0;
-                if (++ahead == C::kRawSlots) {  // the oldest raw tile has landed
-                    cp_async_wait_group<C::kRawSlots - 1>();
-                    --ahead;
-                    if (!convert()) break;
-                }
-            } else {
                 // The slot is full once every loader thread's copies so far have landed (its queries among
                 // them); nobody waits for that here, so the whole ring can be in flight.
                 copy_arrive(&bars->full[slot]);
@@ -379,24 +302,22 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
                     slot = 0;
                     ++round;
                 }
+#pragma unroll
+                for (int h = 0; h + KT / 32 < kPids; ++h) pid[h] = pid[h + KT / 32];
             }
-            if (++stream == NS) {
-                stream = 0;
-                fresh = w.kt + 1 == w.kts;
-                walk_next(a, w, kTcRowTile, C::kUnit);
-            }
+            if (!ok) break;
+            fresh = w.kt + 1 == w.kts;
+            walk_next(a, w, kTcRowTile, C::kUnit);
             fetch_pages();
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if constexpr (F8)
-            while (ahead > 0 && convert()) --ahead;
         if (err) bars->status = err;
     } else if (C::mma_of(warp) >= 0) {
         // ---------------------------------------------------------------- MMA issue
         // The whole warp runs this with equal values and one elected lane issues: descriptors then stay in
         // uniform registers (from one divergent lane each MMA cost 90 to 160 cycles to issue).
         constexpr uint32_t idesc_s = idesc16<BF16>(kTcRowTile, KT, false);
-        constexpr uint32_t idesc_o = idesc16<VB>(kTcRowTile, DP, true);
+        constexpr uint32_t idesc_o = idesc16<BF16>(kTcRowTile, DP, true);
         const uint32_t base = smem_addr(smem);
         // The upper halves of the descriptors hold layout and stride only (and the leading offset, V's, sits in
         // the lower half's upper bits; with one group of 64 values it is not used).
@@ -415,7 +336,8 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
             const uint32_t vd = v_lo + ((base + C::kRing + (uint32_t)held * (2 * C::kTile) + C::kTile) >> 4);
 #pragma unroll
             for (int k = 0; k < KT / 16; ++k)
-                mma_elect_ts(tm + s * DP, tm + C::kColP + s * (KT / 2) + 8 * k, vd + k * (2048 >> 4), v_hi, idesc_o, 1u);
+                mma_elect_ts(tm + s * DP, tm + C::kColP + (2 * s + (n & 1)) * (KT / 2) + 8 * k, vd + k * (2048 >> 4), v_hi, idesc_o,
+                             1u);
             commit_elect(&bars->empty[held]);
             commit_elect(&bars->pvdone[s]);
             return true;
@@ -458,10 +380,10 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
         // ---------------------------------------------------------------- softmax
         const int s = warp >> 2, row = tid & 127, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-        const uint32_t ts = tmem + lanes + C::kColS + s * KT, tp = tmem + lanes + C::kColP + s * (KT / 2);
-        float c = a.scale * kLog2e;  // (times the head's key scale)
-        bool plain = a.softcap == 0.f && c > 0.f;
-        float cap_in = a.softcap > 0.f ? 2.f * c / a.softcap : 0.f;
+        const uint32_t ts = tmem + lanes + C::kColS + s * KT;
+        const float c = a.scale * kLog2e;
+        const bool plain = a.softcap == 0.f && c > 0.f;
+        const float cap_in = a.softcap > 0.f ? 2.f * c / a.softcap : 0.f;
         const float cap_out = a.softcap * kLog2e;
         uint32_t zero[16];
 #pragma unroll
@@ -503,28 +425,33 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
                 see_hi = row < rows ? hi_of(token) : 0;
                 m = -CUDART_INF_F;
                 l = 0.f;
-                if (F8 && a.k_scale) {
-                    c = a.scale * kLog2e * __ldg(a.k_scale + head);
-                    plain = a.softcap == 0.f && c > 0.f;
-                    cap_in = a.softcap > 0.f ? 2.f * c / a.softcap : 0.f;
-                }
             }
             const int key0 = (w.kt_first + w.kt) * C::kUnit + s * KT;
             const bool edge = key0 < all_lo || key0 + KT > all_hi;  // some row does not see all of the tile
             const bool live = 32 * quarter < rows;
             if (!warp_wait(&bars->sfull[s], (uint32_t)(n & 1))) break;
             tc_fence_after();
-            // Two passes over S, 32 columns at a time in rolled loops (unrolled over the whole tile, the code
-            // of the rare paths alone cost thousands of cycles an item in instruction fetches).
-            float grow = 1.f, f = plain ? c : 1.f;
+            // P has two buffers: the MMA warp issues S of this tile after the values of the last but one, so the
+            // buffer they read is free once S is here.
+            const uint32_t tp = tmem + lanes + C::kColP + (2 * s + (n & 1)) * (KT / 2);
+            // The output stands still once the stream's earlier products are done: awaited before it is touched,
+            // and in any case before this tile's P is announced, so that no phase of the barrier is skipped.
+            bool stands = n == 0;
+            auto still = [&]() {
+                if (stands) return true;
+                stands = warp_wait(&bars->pvdone[s], (uint32_t)((n - 1) & 1));
+                tc_fence_after();
+                return stands;
+            };
             if (live) {
-                float top = -CUDART_INF_F;
+                // What is not a plain scaled score is prepared in tensor memory first, 32 columns at a time in a
+                // rolled loop: unrolled beside the common path its code cost more in instruction fetches.
+                if (!plain || edge) {
 #pragma unroll 1
-                for (int h = 0; h < KT; h += 32) {
-                    uint32_t x[32];
-                    tmem_ld32(ts + h, x);
-                    tmem_wait_ld(x);
-                    if (!plain || edge) {  // what the second pass is to see goes back
+                    for (int h = 0; h < KT; h += 32) {
+                        uint32_t x[32];
+                        tmem_ld32(ts + h, x);
+                        tmem_wait_ld(x);
                         if (a.softcap > 0.f) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
@@ -542,62 +469,60 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
                         }
                         tmem_st32(ts + h, x);
                     }
-                    float t4[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) t4[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[4 + i]));
-#pragma unroll
-                    for (int i = 8; i < 32; i += 8)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            t4[q] = fmax3(t4[q], __uint_as_float(x[i + q]), __uint_as_float(x[i + 4 + q]));
-                    top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+                    tmem_wait_st();
                 }
-                top *= f;  // (f > 0)
+                const float f = plain ? c : 1.f;  // (f > 0)
+                uint32_t x[KT / 32][32];
+#pragma unroll
+                for (int h = 0; h < KT / 32; ++h) tmem_ld32(ts + 32 * h, x[h]);
+#pragma unroll
+                for (int h = 0; h < KT / 32; ++h) tmem_wait_ld(x[h]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_local(&bars->sfree[s]);
+                float t4[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t4[i] = fmaxf(__uint_as_float(x[0][i]), __uint_as_float(x[0][4 + i]));
+#pragma unroll
+                for (int i = 8; i < KT; i += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        t4[q] = fmax3(t4[q], __uint_as_float(x[i >> 5][(i & 31) + q]), __uint_as_float(x[i >> 5][(i & 31) + 4 + q]));
+                const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f;
+                float grow = 1.f;
                 if (top > m + 8.f) {
                     if (m != -CUDART_INF_F) grow = ex2(m - top);  // (else sum and output are still zero)
                     m = top;
                     l *= grow;
                 }
-                tmem_wait_st();
-            }
-            // the stream's earlier products are done: P's buffer is free and O stands still
-            if (n > 0 && !warp_wait(&bars->pvdone[s], (uint32_t)((n - 1) & 1))) break;
-            tc_fence_after();
-            if (live) {
                 if (__any_sync(0xffffffffu, grow != 1.f)) {
+                    if (!still()) break;
 #pragma unroll 1
-                    for (int i = 0; i < DP; i += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tmem + lanes + s * DP + i, o);
-                        tmem_wait_ld(o);
+                    for (int i = 0; i < DP; i += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(tmem + lanes + s * DP + i, o);
+                        tmem_wait_ld16(o);
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * grow);
-                        tmem_st32(tmem + lanes + s * DP + i, o);
+                        for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * grow);
+                        tmem_st16(tmem + lanes + s * DP + i, o);
                     }
                 }
                 const float ref = m == -CUDART_INF_F ? 0.f : m;
                 const uint64_t f2 = pk2(f, f), r2 = pk2(-ref, -ref);
-                uint64_t sum[2] = {0, 0};
-#pragma unroll 1
+                uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
                 for (int h = 0; h < KT; h += 32) {
-                    uint32_t x[32], p[16];
-                    tmem_ld32(ts + h, x);
-                    tmem_wait_ld(x);
-                    if (h + 32 == KT) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_local(&bars->sfree[s]);
-                    }
+                    uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
-                        const float2 e = up2(fma2(pk2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), f2, r2));
+                        const float2 e = up2(fma2(pk2(__uint_as_float(x[h >> 5][i]), __uint_as_float(x[h >> 5][i + 1])), f2, r2));
                         const float p0 = ex2(e.x), p1 = ex2(e.y);
-                        sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pk2(p0, p1));
-                        p[i / 2] = pack16<VB>(p0, p1);
+                        sum[(i >> 1) & 3] = add2(sum[(i >> 1) & 3], pk2(p0, p1));
+                        p[i / 2] = pack16<BF16>(p0, p1);
                     }
                     tmem_st16(tp + h / 2, p);
                 }
-                const float2 total = up2(add2(sum[0], sum[1]));
+                const float2 total = up2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
                 l += total.x + total.y;
                 tmem_wait_st();
             } else {
@@ -614,26 +539,27 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
                 bool any = false;
                 for (int i = row; i < C::kTile / 16; i += 128) {
                     const uint4 y = reinterpret_cast<const uint4*>(v)[i];
-                    any |= is_odd16<VB>(y.x) | is_odd16<VB>(y.x >> 16) | is_odd16<VB>(y.y) | is_odd16<VB>(y.y >> 16) |
-                           is_odd16<VB>(y.z) | is_odd16<VB>(y.z >> 16) | is_odd16<VB>(y.w) | is_odd16<VB>(y.w >> 16);
+                    any |= is_odd16<BF16>(y.x) | is_odd16<BF16>(y.x >> 16) | is_odd16<BF16>(y.y) | is_odd16<BF16>(y.y >> 16) |
+                           is_odd16<BF16>(y.z) | is_odd16<BF16>(y.z >> 16) | is_odd16<BF16>(y.w) | is_odd16<BF16>(y.w >> 16);
                 }
                 int* odd = &bars->odd[s][n & 1];  // (cleared before the tile after next can set it)
                 if (any) *odd = 1;
                 if (!stream_meet()) break;
                 const bool found = *reinterpret_cast<volatile int*>(odd) != 0;
                 if (found) {
+                    if (!still()) break;
                     for (int k = 0; k < KT; ++k) {
                         uint32_t pk = 0;
                         if (live) tmem_ld1(tp + (k >> 1), pk);
-                        const float pv = from16<VB>((k & 1) ? pk >> 16 : pk);
+                        const float pv = from16<BF16>((k & 1) ? pk >> 16 : pk);
                         const bool see = key0 + k >= see_lo && key0 + k < see_hi;
                         for (int d = 0; d < DP; ++d) {
                             const uint32_t bits = *reinterpret_cast<const uint16_t*>(
                                 v + (d >> 6) * (KT * 128) + sw128_offset(k, (d & 63) >> 3) + 2 * (d & 7));
-                            if (live && is_odd16<VB>(bits)) {
+                            if (live && is_odd16<BF16>(bits)) {
                                 uint32_t o;
                                 tmem_ld1(tmem + lanes + s * DP + d, o);
-                                if (see) o = __float_as_uint(fmaf(pv, from16<VB>(bits), __uint_as_float(o)));
+                                if (see) o = __float_as_uint(fmaf(pv, from16<BF16>(bits), __uint_as_float(o)));
                                 tmem_st1(tmem + lanes + s * DP + d, o);
                                 tmem_wait_st();
                             }
@@ -642,12 +568,13 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
                     if (!stream_meet()) break;
                     for (int i = row; i < C::kTile / 2; i += 128) {
                         uint16_t* y = reinterpret_cast<uint16_t*>(v) + i;
-                        if (is_odd16<VB>(*y)) *y = 0;
+                        if (is_odd16<BF16>(*y)) *y = 0;
                     }
                     if (row == 0) *odd = 0;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
             }
+            if (!still()) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_local(&bars->pfull[s]);
@@ -655,13 +582,12 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
             const bool last_of_item = w.kt + 1 == w.kts;
             if (last_of_item || w.left == 1) {
                 // ---- the streams' parts of the segment meet: WG s takes the s-th half of the columns
-                bool done = true;
-#pragma unroll
-                for (int q = 0; q < NS; ++q) done = done && warp_wait(&bars->pvdone[q], (uint32_t)(n & 1));
-                if (!done) break;
+                if (!warp_wait(&bars->pvdone[s], (uint32_t)(n & 1))) break;
                 tc_fence_after();
                 s_ml[s * kTcRowTile + row] = make_float2(m, l);
-                if (!meet()) break;
+                tc_fence_before();
+                if (!meet()) break;  // (every stream has seen its own products done)
+                tc_fence_after();
                 float f[NS], mm = -CUDART_INF_F, ll = 0.f;
 #pragma unroll
                 for (int q = 0; q < NS; ++q) mm = fmaxf(mm, s_ml[q * kTcRowTile + row].x);
@@ -674,7 +600,7 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
                 }
                 const bool whole = last_of_item && seg_first == 0;
                 const size_t slot = 2 * (size_t)part + (seg_first == 0 ? kHead : kTail);
-                const float inv = !whole ? 1.f : (ll == 0.f ? 0.f : (F8 && a.v_scale ? __ldg(a.v_scale + head) : 1.f) / ll);
+                const float inv = !whole ? 1.f : (ll == 0.f ? 0.f : 1.f / ll);
                 const long long at = attn_out_row(a, w.r.token0, head, row0 + row);
                 unsigned char* dst = a.out + (size_t)at * a.D * 2;
                 float* part_dst = a.part_o + (slot * kTcRowTile + row) * a.D;
@@ -735,11 +661,11 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
     if (tid == 0) mine->err = bars->status ? bars->status : (bad ? DSPARK_ERR_CACHE : 0);
 }
 
-template <bool BF16, bool F8, int DP>
+template <bool BF16, int DP>
 dspark_status launch_tc(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
-    using C = TcAttn<F8, DP>;
+    using C = TcAttn<DP>;
     int per_sm = 0;
-    auto fn = attn_tc_kernel<BF16, F8, DP>;
+    auto fn = attn_tc_kernel<BF16, DP>;
     if (prepare_kernel((const void*)fn, C::kSmem, C::kThreads, &per_sm) != cudaSuccess || per_sm < 1)
         return DSPARK_ERR_CUDA;
     const int n = sms < kMaxTcParts ? sms : kMaxTcParts;
@@ -748,18 +674,12 @@ dspark_status launch_tc(const AttnArgs& a, int sms, cudaStream_t s, int* parts) 
     return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
-template <bool BF16, bool F8>
-dspark_status launch_tc_d(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
-    if (a.D <= 64) return launch_tc<BF16, F8, 64>(a, sms, s, parts);
-    if (a.D <= 128) return launch_tc<BF16, F8, 128>(a, sms, s, parts);
-    return launch_tc<BF16, F8, 256>(a, sms, s, parts);
-}
-
 }  // namespace
 
-dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, bool e4m3, int sms, cudaStream_t s, int* parts) {
-    if (e4m3) return bf16 ? launch_tc_d<true, true>(a, sms, s, parts) : launch_tc_d<false, true>(a, sms, s, parts);
-    return bf16 ? launch_tc_d<true, false>(a, sms, s, parts) : launch_tc_d<false, false>(a, sms, s, parts);
+dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int sms, cudaStream_t s, int* parts) {
+    if (a.D <= 64) return bf16 ? launch_tc<true, 64>(a, sms, s, parts) : launch_tc<false, 64>(a, sms, s, parts);
+    if (a.D <= 128) return bf16 ? launch_tc<true, 128>(a, sms, s, parts) : launch_tc<false, 128>(a, sms, s, parts);
+    return bf16 ? launch_tc<true, 256>(a, sms, s, parts) : launch_tc<false, 256>(a, sms, s, parts);
 }
 
 }  // namespace dspark
