@@ -138,24 +138,16 @@ def schedule_verify_len(conf, budget, ws=None, out=None, stream=None):
 
 
 # ------------------------------------------------------------------ the paged key-value cache
-_I32 = torch.int32
+# The tensors are checked in csrc/native.cpp, on their way into the library.
+_WS = b.CacheParams(1, 1, 1, 1, 0, 0)  # cache_plan's and cache_commit's workspace does not depend on the sizes
 
 
-def _i32(what, t, n):
-    if t.dtype is not _I32 or t.numel() != n:
-        raise ValueError(f"{what} is int32 with {n} values")
+def _raw(stream):
+    return stream if stream is None else b._stream(stream)
 
 
-def _cache_params(cache_len, block_table, n_blocks, free_pages, n_free, page_size, max_tokens, extra):
-    B, pages = cache_len.numel(), free_pages.numel()
-    if cache_len.dtype is not _I32 or free_pages.dtype is not _I32 or block_table.dtype is not _I32:
-        raise ValueError("cache_len, free_pages and block_table are int32")
-    _i32("n_blocks", n_blocks, B)
-    _i32("n_free", n_free, 1)
-    shape = block_table.shape
-    if len(shape) != 2 or shape[0] != B:
-        raise ValueError("block_table is [B, max_blocks]")
-    return b.CacheParams(B, page_size, pages, shape[1], max_tokens, extra)
+def _cache_ws(ws, like):
+    return b.workspace(b.dspark_cache_workspace_size(_WS), like.device) if ws is None else ws
 
 
 def cache_plan(cache_len, new_len, block_table, n_blocks, free_pages, n_free, page_size, max_tokens, extra=0,
@@ -164,27 +156,14 @@ def cache_plan(cache_len, new_len, block_table, n_blocks, free_pages, n_free, pa
     None), n_blocks [B], free_pages [pages], n_free [1], all int32; block_table [B, max_blocks] int32 gains the new
     pages.  Returns (seq_len [B], offsets [B+1], slots [max_tokens] int64, positions [max_tokens] or None,
     n_blocks [B], n_free [1], workspace); n_blocks and n_free are new tensors."""
-    p = _cache_params(cache_len, block_table, n_blocks, free_pages, n_free, page_size, max_tokens, extra)
-    B = p.B
-    if new_len is not None:
-        _i32("new_len", new_len, B)
     if out is None:
-        dev = cache_len.device
-        i32 = {"dtype": _I32, "device": dev}
-        out = (torch.empty(B, **i32), torch.empty(B + 1, **i32), torch.empty(max_tokens, dtype=torch.int64, device=dev),
+        B, i32 = cache_len.numel(), {"dtype": torch.int32, "device": cache_len.device}
+        out = (torch.empty(B, **i32), torch.empty(B + 1, **i32), torch.empty(max_tokens, dtype=torch.int64, device=i32["device"]),
                torch.empty(max_tokens, **i32) if positions else None, torch.empty(B, **i32), torch.empty(1, **i32))
-    else:
-        _i32("seq_len", out[0], B)
-        _i32("offsets", out[1], B + 1)
-        if out[2].dtype is not torch.int64 or out[2].numel() != max_tokens:
-            raise ValueError(f"slots is int64 with {max_tokens} values")
-        if out[3] is not None:
-            _i32("positions", out[3], max_tokens)
-        _i32("n_blocks", out[4], B)
-        _i32("n_free", out[5], 1)
-    if ws is None:
-        ws = b.workspace(b.dspark_cache_workspace_size(p), cache_len.device)
-    b.dspark_cache_plan(p, cache_len, new_len, block_table, n_blocks, free_pages, n_free, *out, ws, stream)
+    ws = _cache_ws(ws, cache_len)
+    st = b.native().cache_plan(cache_len, new_len, block_table, n_blocks, free_pages, n_free, page_size, max_tokens, extra, *out,
+                               ws, _raw(stream))
+    b._check(st, "dspark_cache_plan")
     return (*out, ws)
 
 
@@ -193,52 +172,20 @@ def cache_commit(cache_len, add_len, block_table, n_blocks, free_pages, n_free, 
     """The requests' lengths after the verification, and the pages past them back on the stack
     (dspark_cache_commit): add_len [B] int32 (n_accepted) or None, done [B] uint8 or bool, or None; free_pages is
     written in place.  Returns (cache_len [B], n_blocks [B], n_free [1], workspace), new tensors."""
-    p = _cache_params(cache_len, block_table, n_blocks, free_pages, n_free, page_size, 0, extra)
-    B = p.B
-    if add_len is not None:
-        _i32("add_len", add_len, B)
-    if done is not None and (done.dtype not in (torch.uint8, torch.bool) or done.numel() != B):
-        raise ValueError("done is uint8 or bool [B]")
     if out is None:
-        i32 = {"dtype": _I32, "device": cache_len.device}
+        B, i32 = cache_len.numel(), {"dtype": torch.int32, "device": cache_len.device}
         out = (torch.empty(B, **i32), torch.empty(B, **i32), torch.empty(1, **i32))
-    else:
-        _i32("cache_len", out[0], B)
-        _i32("n_blocks", out[1], B)
-        _i32("n_free", out[2], 1)
-    if ws is None:
-        ws = b.workspace(b.dspark_cache_workspace_size(p), cache_len.device)
-    b.dspark_cache_commit(p, cache_len, add_len, done, block_table, n_blocks, free_pages, n_free, *out, ws, stream)
+    ws = _cache_ws(ws, cache_len)
+    st = b.native().cache_commit(cache_len, add_len, done, block_table, n_blocks, free_pages, n_free, page_size, extra, *out, ws,
+                                 _raw(stream))
+    b._check(st, "dspark_cache_commit")
     return (*out, ws)
-
-
-def _scales(kv_dtype, k_scale, v_scale, Hk):
-    for s in (k_scale, v_scale):
-        if s is None:
-            continue
-        if kv_dtype is not torch.float8_e4m3fn:
-            raise ValueError("scales belong to an e4m3 cache")
-        if s.dtype is not torch.float32 or s.numel() != Hk:
-            raise ValueError("a scale is fp32 [Hk]")
 
 
 def cache_append(k, v, k_pages, v_pages, slots, k_scale=None, v_scale=None, stream=None):
     """Writes k, v [T, Hk, D] (bf16 or fp16; any strides with a dense last dimension) to their slots [T] int64 of
     k_pages, v_pages [pages, page_size, Hk, D] (their type, or e4m3 with k_scale, v_scale [Hk] fp32)."""
-    pages, page_size, Hk, D, sp, st, sh = b.pool_layout(k_pages, v_pages)
-    shape = k.shape
-    if v.shape != shape or len(shape) != 3 or shape[1] != Hk or shape[2] != D or k.dtype is not v.dtype:
-        raise ValueError("k and v are [T, Hk, D] of one type")
-    T = shape[0]
-    if slots.dtype is not torch.int64 or slots.numel() != T:
-        raise ValueError("slots is int64 [T]")
-    if k_scale is not None or v_scale is not None:
-        _scales(k_pages.dtype, k_scale, v_scale, Hk)
-    kt, kh, _ = k.stride()
-    vt, vh, _ = v.stride()
-    p = b.AppendParams(T, Hk, D, page_size, pages, b.cache_dtype_code(k.dtype), b.cache_dtype_code(k_pages.dtype), kt, kh,
-                       vt, vh, sp, st, sh)
-    b.dspark_cache_append(p, k, v, k_pages, v_pages, slots, k_scale, v_scale, stream)
+    b._check(b.native().cache_append(k, v, k_pages, v_pages, slots, k_scale, v_scale, _raw(stream)), "dspark_cache_append")
 
 
 def paged_attention(q, k_pages, v_pages, block_table, seq_len, offsets=None, scale=None, causal=True, window=0,
@@ -247,33 +194,12 @@ def paged_attention(q, k_pages, v_pages, block_table, seq_len, offsets=None, sca
     (dspark_paged_attention): block_table [B, max_blocks], seq_len [B], offsets [B+1] int32 (None: one token a
     request).  scale defaults to D ** -0.5.  lse: None, True, or a [T, Hq] fp32 tensor to write.
     Returns (out [T, Hq, D], lse or None, workspace)."""
-    pages, page_size, Hk, D, sp, st, sh = b.pool_layout(k_pages, v_pages)
-    shape = q.shape
-    if len(shape) != 3 or shape[2] != D:
-        raise ValueError("q is [T, Hq, D]")
-    T, Hq, _ = shape
-    B = seq_len.numel()
-    tables = block_table.shape
-    if seq_len.dtype is not _I32 or block_table.dtype is not _I32 or len(tables) != 2 or tables[0] != B:
-        raise ValueError("block_table [B, max_blocks] and seq_len [B] are int32")
-    if offsets is not None:
-        _i32("offsets", offsets, B + 1)
-    if k_scale is not None or v_scale is not None:
-        _scales(k_pages.dtype, k_scale, v_scale, Hk)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    elif out.shape != shape or out.dtype is not q.dtype:
-        raise ValueError("out is [T, Hq, D] of q's type")
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if lse is True:
-        lse = torch.empty((T, Hq), device=q.device)
-    elif lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (T, Hq)):
-        raise ValueError("lse is fp32 [T, Hq]")
-    qt, qh, _ = q.stride()
-    p = b.AttentionParams(T, B, Hq, Hk, D, page_size, pages, tables[1], max_new, b.cache_dtype_code(q.dtype),
-                          b.cache_dtype_code(k_pages.dtype), 1 if causal else 0, window,
-                          D ** -0.5 if scale is None else scale, softcap, qt, qh, sp, st, sh)
-    if ws is None:
-        ws = b.workspace(b.dspark_paged_attention_workspace_size(p), q.device)
-    b.dspark_paged_attention(p, q, k_pages, v_pages, block_table, seq_len, offsets, k_scale, v_scale, out, lse, ws,
-                             stream)
+        lse = torch.empty(q.shape[:2], device=q.device)
+    st, ws = b.native().paged_attention(q, k_pages, v_pages, block_table, seq_len, offsets, k_scale, v_scale,
+                                        q.shape[-1] ** -0.5 if scale is None else scale, softcap, causal, window, max_new, out,
+                                        lse, ws, _raw(stream))
+    b._check(st, "dspark_paged_attention")
     return out, lse, ws

@@ -12,7 +12,7 @@ import os
 
 import torch
 
-from .build import LIB
+from .build import LIB, NATIVE
 
 F32, BF16, F16, E4M3 = 0, 1, 2, 3
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "CUDA error", 4: "device wait timed out",
@@ -129,6 +129,22 @@ def lib():
         L.dspark_kernel_launches.restype = u64
         _L = L
     return _L
+
+
+_N = None
+
+
+def native():
+    """The CPython module of the paged-cache calls (csrc/native.cpp), which checks tensors and calls libdspark."""
+    global _N
+    if _N is None:
+        lib()
+        if not os.path.exists(NATIVE):
+            raise RuntimeError(f"the native module is not built ({NATIVE} missing); run __graft_entry__.build()")
+        from . import _native
+
+        _N = _native
+    return _N
 
 
 # ------------------------------------------------------------------ marshalling helpers
