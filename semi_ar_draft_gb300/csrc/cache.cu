@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "host_util.h"
+#include "pdl.cuh"
 
 namespace dspark {
 namespace {
@@ -113,6 +114,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(PlanArgs a) {
     const int tid = threadIdx.x;
     const int m = (a.B + kPlanThreads - 1) / kPlanThreads;
     const int j0 = min(tid * m, a.B), j1 = min(j0 + m, a.B);
+    wait_primary();
+    launch_dependents();
     const int n_free_in = *a.n_free;
     const int n_free = min(max(n_free_in, 0), a.num_pages);
     long long tok = 0, pg = 0, T, P;
@@ -222,6 +225,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_commit_kernel(CommitArgs a
     const int tid = threadIdx.x;
     const int m = (a.B + kPlanThreads - 1) / kPlanThreads;
     const int j0 = min(tid * m, a.B), j1 = min(j0 + m, a.B);
+    wait_primary();
+    launch_dependents();
     const int n_free_in = *a.n_free;
     const int n_free = min(max(n_free_in, 0), a.num_pages);
     long long pg = 0, none = 0, P, unused;
@@ -312,6 +317,8 @@ __device__ __forceinline__ uint2 quantize8(uint4 x, float scale) {
 // One thread moves one 8-element group of K and the same one of V.  CACHE8: e4m3 pages.
 template <bool CACHE8, bool BF16, bool ALIGNED>
 __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs a) {
+    wait_primary();
+    launch_dependents();
     const long long total = (long long)a.T * a.per_token;
     const long long stride = (long long)gridDim.x * kAppendThreads;
     for (long long i = (long long)blockIdx.x * kAppendThreads + threadIdx.x; i < total; i += stride) {
@@ -336,11 +343,9 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(AppendArgs
 }
 
 template <bool CACHE8, bool BF16>
-void launch_append(const AppendArgs& a, bool aligned, int blocks, cudaStream_t s) {
-    if (aligned)
-        cache_append_kernel<CACHE8, BF16, true><<<blocks, kAppendThreads, 0, s>>>(a);
-    else
-        cache_append_kernel<CACHE8, BF16, false><<<blocks, kAppendThreads, 0, s>>>(a);
+cudaError_t launch_append(const AppendArgs& a, bool aligned, int blocks, cudaStream_t s) {
+    return launch_overlapped(aligned ? cache_append_kernel<CACHE8, BF16, true> : cache_append_kernel<CACHE8, BF16, false>,
+                             blocks, kAppendThreads, 0, s, a);
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -407,8 +412,9 @@ extern "C" dspark_status dspark_cache_plan(const dspark_cache_params* p, const i
     PlanArgs a{p->B, page_shift_of(p->page_size), p->num_pages, p->max_blocks, p->max_tokens, p->extra, cache_len,
                new_len, block_table, n_blocks, free_pages, n_free, seq_len, offsets, slots, positions, n_blocks_out,
                n_free_out, &static_cast<WsHeader*>(workspace)->status};
-    cache_plan_kernel<<<blocks_for(p->max_tokens, sms), kPlanThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return DSPARK_ERR_CUDA;
+    if (launch_overlapped(cache_plan_kernel, blocks_for(p->max_tokens, sms), kPlanThreads, smem,
+                          reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
+        return DSPARK_ERR_CUDA;
     note_launch();
     return DSPARK_OK;
 }
@@ -444,8 +450,9 @@ extern "C" dspark_status dspark_cache_commit(const dspark_cache_params* p, const
     // The pages that come back are known on the device only: a block for every 64 requests spreads
     // those of finished requests, and one block does for the usual few.
     const int blocks = (p->B + 63) / 64;
-    cache_commit_kernel<<<blocks, kPlanThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return DSPARK_ERR_CUDA;
+    if (launch_overlapped(cache_commit_kernel, blocks, kPlanThreads, smem, reinterpret_cast<cudaStream_t>(stream), a) !=
+        cudaSuccess)
+        return DSPARK_ERR_CUDA;
     note_launch();
     return DSPARK_OK;
 }
@@ -493,13 +500,11 @@ extern "C" dspark_status dspark_cache_append(const dspark_append_params* p, cons
     const int blocks = (int)(want < most ? want : most);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = p->dtype == DSPARK_BF16;
-    if (!e4m3)
-        launch_append<false, true>(a, aligned, blocks, s);  // a copy of the bits, whichever 16-bit type
-    else if (bf16)
-        launch_append<true, true>(a, aligned, blocks, s);
-    else
-        launch_append<true, false>(a, aligned, blocks, s);
-    if (cudaGetLastError() != cudaSuccess) return DSPARK_ERR_CUDA;
+    // (without e4m3 a copy of the bits, whichever 16-bit type)
+    const cudaError_t e = !e4m3  ? launch_append<false, true>(a, aligned, blocks, s)
+                          : bf16 ? launch_append<true, true>(a, aligned, blocks, s)
+                                 : launch_append<true, false>(a, aligned, blocks, s);
+    if (e != cudaSuccess) return DSPARK_ERR_CUDA;
     note_launch();
     return DSPARK_OK;
 }

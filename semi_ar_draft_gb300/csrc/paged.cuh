@@ -30,7 +30,7 @@ struct AttnArgs {
     uint32_t g_mul, g_shift;  // row / G = umulhi(2 row, g_mul) >> g_shift for rows below 2^31 (group_division)
     int page_shift, num_pages, max_blocks;
     int causal, window;
-    int q_pairs;  // rows of q start on 4-byte boundaries
+    int q_vec;  // rows of q start on 16-byte boundaries
     float scale, softcap;
     const unsigned char* q;
     long long q_token, q_head;  // strides, elements
@@ -276,10 +276,6 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     return r;
 }
 
-// Secondary-launch controls: the join kernel is launched while the attention kernel still runs and
-// waits there for its end.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Row tiles of 128 on the fifth-generation tensor cores (paged_attn_tc.cu): 16-bit caches, 16-byte
 // aligned query rows.

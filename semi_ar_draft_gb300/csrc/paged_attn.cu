@@ -17,6 +17,7 @@
 
 #include "host_util.h"
 #include "paged.cuh"
+#include "pdl.cuh"
 #include "tc05.cuh"
 
 namespace dspark {
@@ -80,9 +81,10 @@ struct Rows16 {
     static constexpr int kStages = DP == 64 ? 4 : (kThree ? 2 : 3);
     static constexpr int kExtra = DP == 64 ? 4 : 2;      // what an item costs beside its key tiles
     static constexpr int kBlocksPerSm = DP == 256 ? 1 : (kThree ? 3 : 2);
-    // Registers: 64 of q beside 128 of output do not fit a thread, nor 32 beside 64 three blocks.
+    // Registers: 64 of q beside 128 of output do not fit a thread, nor 32 beside 64 three blocks; the MMAs
+    // then take q from shared memory every time.
     static constexpr bool kQInSmem = DP == 256 || (kThree && DP == 128);
-    static constexpr int kQBytes = kQInSmem ? DP / 16 * 32 * 16 : 0;
+    static constexpr int kQBytes = kRows * DP * 2;
     static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage + kQBytes;
     static_assert(kStage == kRows * DP * 4, "a stage holds a warp's output");
     // Rows are a multiple of 128 bytes apart (or 64): the swizzle spreads eight rows' same 16-byte group
@@ -90,6 +92,9 @@ struct Rows16 {
     static __device__ __forceinline__ uint32_t at(int row, int chunk) {
         const int x = kChunks >= 8 ? (row & 7) : ((row >> 1) & 3);
         return (uint32_t)(row * kRowBytes + ((chunk ^ x) << 4));
+    }
+    static __device__ __forceinline__ uint32_t q_at(int row, int chunk) {  // 16-bit rows of q
+        return (uint32_t)(row * (DP * 2) + ((chunk ^ (row & 7)) << 4));
     }
 };
 
@@ -110,9 +115,11 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
     __shared__ float2 s_ml[kWarps][kRows];
     __shared__ int s_err;
     __shared__ AttnScratch s_start;
+    __shared__ uint32_t s_qmax[kRows];  // largest |q| of each row (its bits)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int part = blockIdx.x, parts = gridDim.x;
+    wait_primary();
     launch_dependents();
     if (tid == 0) s_err = 0;
     bool bad;
@@ -121,7 +128,8 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
     attn_tail_rows(a, (size_t)part * kThreads + tid, (size_t)parts * kThreads);
     unsigned char* ring = smem + (size_t)warp * C::kStages * C::kStage;
     const uint32_t ring_addr = smem_addr(ring);
-    uint4* qs = reinterpret_cast<uint4*>(smem + (size_t)kWarps * C::kStages * C::kStage);
+    unsigned char* qs = smem + (size_t)kWarps * C::kStages * C::kStage;
+    const uint32_t qs_addr = smem_addr(qs);
     int err = bad ? DSPARK_ERR_CACHE : 0;
 
     // ---- loads: `ld` walks ahead of the arithmetic; `pid` is the page of this lane's key of its slice
@@ -202,73 +210,81 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
             auto hi_of = [&](int token) { return a.causal ? min(pos0 + token + 1, w.r.seq) : w.r.seq; };
             all_lo = lo_of(attn_token(a, row0 + rows - 1));
             all_hi = hi_of(attn_token(a, row0));
-            const unsigned char* qrow[2];
-            bool real[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = g + 8 * r, token = attn_token(a, row0 + row);
-                real[r] = row < rows;
-                see_lo[r] = real[r] ? lo_of(token) : 0;
-                see_hi[r] = real[r] ? hi_of(token) : 0;
-                qrow[r] = real[r] ? a.q + 2 * ((w.r.token0 + token) * a.q_token +
-                                               (head * a.G + row0 + row - token * a.G) * a.q_head)
-                                  : a.q;
-                m[r] = -CUDART_INF_F;
-                l[r] = 0.f;
-                row_scale[r] = a.scale * (F8 && a.k_scale ? __ldg(a.k_scale + head) : 1.f);
+            // The queries, through shared memory: 16 bytes a thread, then the MMA's fragments by ldmatrix.  (The
+            // previous segment's readers are past its last barrier.)
+            constexpr int kQc = DP / 8;
+            uint4 qv[kRows * kQc / kThreads];
+            constexpr bool kRescale = F8 && BF16;
+            if (kRescale) {
+                if (tid < kRows) s_qmax[tid] = 0;
+                __syncthreads();
             }
-            // Two consecutive values of q, as the MMA's pair (q may start at any element: then one by one).
-            auto pair = [&](int r, int d) -> uint32_t {
-                if (!real[r] || d >= a.D) return 0u;
-                const uint16_t* p = reinterpret_cast<const uint16_t*>(qrow[r]) + d;
-                if (a.q_pairs) return __ldg(reinterpret_cast<const uint32_t*>(p));
-                return (uint32_t)__ldg(p) | ((uint32_t)__ldg(p + 1) << 16);
-            };
-            auto load_q = [&](auto&& put) {
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    // 8-bit keys arrive four k a lane: k slots (2t, 2t + 1 | 2t + 8, 2t + 9) hold k = 4t .. 4t + 3
-                    const int d0 = ks * 16 + (F8 ? 4 * t : 2 * t), d1 = d0 + (F8 ? 2 : 8);
-                    const uint32_t x[4] = {pair(0, d0), pair(1, d0), pair(0, d1), pair(1, d1)};
-                    put(ks, x);
+            for (int u = 0; u < kRows * kQc / kThreads; ++u) {
+                const int row = (tid + u * kThreads) / kQc, c = (tid + u * kThreads) % kQc, token = attn_token(a, row0 + row);
+                qv[u] = make_uint4(0, 0, 0, 0);
+                if (row < rows && 8 * c < a.D) {
+                    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (w.r.token0 + token) * a.q_token +
+                                          (head * a.G + row0 + row - token * a.G) * a.q_head + 8 * c;
+                    if (a.q_vec) {
+                        qv[u] = __ldg(reinterpret_cast<const uint4*>(src));
+                    } else {  // rows may start at any element
+                        uint32_t* y = reinterpret_cast<uint32_t*>(&qv[u]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = (uint32_t)__ldg(src + 2 * e) | ((uint32_t)__ldg(src + 2 * e + 1) << 16);
+                    }
                 }
+                if (kRescale) {
+                    float big = 0.f;
+                    const uint32_t* y = reinterpret_cast<const uint32_t*>(&qv[u]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) big = fmaxf(big, fmaxf(fabsf(bf16_lo(y[e])), fabsf(bf16_hi(y[e]))));
+                    atomicMax(&s_qmax[row], __float_as_uint(big));
+                }
+            }
+            // bf16 queries as halves (an 8-bit cache): each row times the power of two that brings its largest
+            // value to 2^14, taken back in the scores' scale; what a half then cannot hold is below 2^-38 of the
+            // row's largest, less than fp32 keeps of the sum.
+            auto raise = [&](int row) {
+                const int e = (int)(s_qmax[row] >> 23) - 127;  // floor(log2) of a normal number
+                return e > -127 && e < 128 ? min(max(14 - e, -120), 120) : 0;
             };
-            float back[2] = {1.f, 1.f};
-            if (F8 && BF16) {
-                // bf16 queries as halves: each row times the power of two that brings its largest value to
-                // 2^14, taken back in the scores' scale; what a half then cannot hold is below 2^-38 of the
-                // row's largest, less than fp32 keeps of the sum.
-                float big[2] = {0.f, 0.f};
-                load_q([&](int, const uint32_t(&x)[4]) {
+            if (kRescale) __syncthreads();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        big[i & 1] = fmaxf(big[i & 1], fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
-                });
+            for (int u = 0; u < kRows * kQc / kThreads; ++u) {
+                const int row = (tid + u * kThreads) / kQc, c = (tid + u * kThreads) % kQc;
+                if (!F8) {
+                    *reinterpret_cast<uint4*>(qs + C::q_at(row, c)) = qv[u];
+                } else {
+                    // 8-bit keys arrive four k a lane: the MMA's k slots (2t, 2t + 1 | 2t + 8, 2t + 9) hold k = 4t .. 4t + 3,
+                    // so pair p of 16 values goes to pair p / 2 + 4 (p % 2)
+                    const uint32_t* y = reinterpret_cast<const uint32_t*>(&qv[u]);
+                    const float up = kRescale ? __uint_as_float((uint32_t)(127 + raise(row)) << 23) : 1.f;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    big[r] = fmaxf(big[r], __shfl_xor_sync(0xffffffffu, big[r], 1));
-                    big[r] = fmaxf(big[r], __shfl_xor_sync(0xffffffffu, big[r], 2));
-                    const int e = (int)(__float_as_uint(big[r]) >> 23) - 127;  // floor(log2), big >= 2^-126
-                    if (e > -127 && e < 128) {
-                        const int up = min(max(14 - e, -120), 120);
-                        back[r] = __uint_as_float((uint32_t)(127 + up) << 23);
-                        row_scale[r] *= __uint_as_float((uint32_t)(127 - up) << 23);
+                    for (int e = 0; e < 4; ++e) {
+                        const int p = 4 * (c & 1) + e, to = (p >> 1) + 4 * (p & 1);
+                        const uint32_t x = kRescale ? pack16<false>(bf16_lo(y[e]) * up, bf16_hi(y[e]) * up) : y[e];
+                        *reinterpret_cast<uint32_t*>(qs + C::q_at(row, (c & ~1) + (to >> 2)) + 4 * (to & 3)) = x;
                     }
                 }
             }
-            load_q([&](int ks, const uint32_t(&x)[4]) {
-                uint32_t y[4];
+            __syncthreads();
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    y[i] = F8 && BF16 ? pack16<false>(bf16_lo(x[i]) * back[i & 1], bf16_hi(x[i]) * back[i & 1]) : x[i];
-                if (C::kQInSmem) {
-                    if (warp == 0) qs[ks * 32 + lane] = make_uint4(y[0], y[1], y[2], y[3]);
-                } else {
+            for (int r = 0; r < 2; ++r) {
+                const int row = g + 8 * r, token = attn_token(a, row0 + row);
+                const bool real = row < rows;
+                see_lo[r] = real ? lo_of(token) : 0;
+                see_hi[r] = real ? hi_of(token) : 0;
+                m[r] = -CUDART_INF_F;
+                l[r] = 0.f;
+                row_scale[r] = a.scale * (F8 && a.k_scale ? __ldg(a.k_scale + head) : 1.f);
+                if (kRescale) row_scale[r] *= __uint_as_float((uint32_t)(127 - raise(row)) << 23);
+            }
+            if (!C::kQInSmem) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) qf[C::kQInSmem ? 0 : ks][i] = y[i];
-                }
-            });
-            if (C::kQInSmem) __syncthreads();
+                for (int ks = 0; ks < KS; ++ks)
+                    ldsm4(qf[C::kQInSmem ? 0 : ks], qs_addr + C::q_at((lane & 7) + ((lane >> 3) & 1) * 8, 2 * ks + (lane >> 4)));
+            }
 #pragma unroll
             for (int i = 0; i < DT; ++i)
 #pragma unroll
@@ -289,8 +305,7 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
             for (int ks = 0; ks < KS; ++ks) {
                 uint32_t q4[4];
                 if (C::kQInSmem) {
-                    const uint4 x = qs[ks * 32 + lane];
-                    q4[0] = x.x; q4[1] = x.y; q4[2] = x.z; q4[3] = x.w;
+                    ldsm4(q4, qs_addr + C::q_at((lane & 7) + ((lane >> 3) & 1) * 8, 2 * ks + (lane >> 4)));
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) q4[i] = qf[C::kQInSmem ? 0 : ks][i];
@@ -412,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
                 const unsigned char* vs = ring + st * C::kStage + C::kHalf;
 #pragma unroll
                 for (int i = 0; i < KT; ++i)
+#pragma unroll 1
                     for (int k = 0; k < 8; ++k) {
                         const int key = key0 + 8 * i + k, from = (lane & ~3) | (k >> 1);
                         float p[2];
@@ -652,9 +668,8 @@ dspark_status launch_rows16(const AttnArgs& a, int sms, cudaStream_t s, int* par
         return DSPARK_ERR_CUDA;
     int n = sms * (per_sm < C::kBlocksPerSm ? per_sm : C::kBlocksPerSm);
     if (n > kMaxParts) n = kMaxParts;
-    fn<<<n, kThreads, C::kSmem, s>>>(a);
     *parts = n;
-    return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+    return launch_overlapped(fn, n, kThreads, C::kSmem, s, a) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 template <bool BF16, bool F8>
@@ -749,7 +764,7 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     a.q = static_cast<const unsigned char*>(q);
     a.q_token = p->q_token_stride;
     a.q_head = p->q_head_stride;
-    a.q_pairs = !((uintptr_t)q & 3u) && p->q_token_stride % 2 == 0 && p->q_head_stride % 2 == 0;
+    a.q_vec = !((uintptr_t)q & 15u) && p->q_token_stride % 8 == 0 && p->q_head_stride % 8 == 0;
     a.k_pages = static_cast<const unsigned char*>(k_pages);
     a.v_pages = static_cast<const unsigned char*>(v_pages);
     a.page = p->kv_page_stride * esz;
@@ -768,8 +783,7 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     a.part_o = reinterpret_cast<float*>(ws + w.o);
     const bool bf16 = p->dtype == DSPARK_BF16;
     int parts = 0;
-    const bool aligned_q = !((uintptr_t)q & 15u) && p->q_token_stride % 8 == 0 && p->q_head_stride % 8 == 0;
-    const bool tc = wide_rows(p) && aligned_q;
+    const bool tc = wide_rows(p) && a.q_vec;
     const dspark_status ls = tc     ? launch_attn_tc(a, bf16, sms, s, &parts)
                              : bf16 ? (e4m3 ? launch_rows16_d<true, true>(a, sms, s, &parts)
                                           : launch_rows16_d<true, false>(a, sms, s, &parts))
@@ -778,18 +792,10 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     if (ls != DSPARK_OK) return ls;
     note_launch();
     const int row_tile = tc ? kTcRows : kRows;
-    // The join is enqueued while the attention kernel runs (its blocks wait for that kernel's end).
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(parts, 8);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = bf16 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<true>, a, row_tile, parts)
-                               : cudaLaunchKernelEx(&cfg, attn_join_kernel<false>, a, row_tile, parts);
+    // The join's blocks become resident as the attention kernel's leave.
+    const dim3 grid(parts, 8), block(32 * kJoinWarps);
+    const cudaError_t e = bf16 ? launch_overlapped(attn_join_kernel<true>, grid, block, 0, s, a, row_tile, parts)
+                               : launch_overlapped(attn_join_kernel<false>, grid, block, 0, s, a, row_tile, parts);
     if (e != cudaSuccess) return DSPARK_ERR_CUDA;
     note_launch();
     return DSPARK_OK;

@@ -17,6 +17,7 @@
 // 2^8, which needs the stream's earlier products done.
 #include "host_util.h"
 #include "paged.cuh"
+#include "pdl.cuh"
 #include "tc05.cuh"
 
 namespace dspark {
@@ -167,7 +168,6 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
     TcBars* bars = reinterpret_cast<TcBars*>(smem + C::kMeta + 2 * kTcRowTile * 8);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int part = blockIdx.x, parts = gridDim.x;
-    launch_dependents();
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(&bars->full[i], 32 * C::kLoaders);
@@ -197,6 +197,8 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         tmem_relinquish();
     }
     tc_fence_before();
+    wait_primary();
+    launch_dependents();
     bool bad;
     AttnStart start = attn_start<C::kThreads>(a, kTcRowTile, C::kUnit, C::kExtra, parts, part, 2 + C::kExtra, &bars->scratch, &bad);  // (barriers inside)
     __syncthreads();
@@ -548,11 +550,13 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 const bool found = *reinterpret_cast<volatile int*>(odd) != 0;
                 if (found) {
                     if (!still()) break;
+#pragma unroll 1
                     for (int k = 0; k < KT; ++k) {
                         uint32_t pk = 0;
                         if (live) tmem_ld1(tp + (k >> 1), pk);
                         const float pv = from16<BF16>((k & 1) ? pk >> 16 : pk);
                         const bool see = key0 + k >= see_lo && key0 + k < see_hi;
+#pragma unroll 1
                         for (int d = 0; d < DP; ++d) {
                             const uint32_t bits = *reinterpret_cast<const uint16_t*>(
                                 v + (d >> 6) * (KT * 128) + sw128_offset(k, (d & 63) >> 3) + 2 * (d & 7));
@@ -669,9 +673,8 @@ dspark_status launch_tc(const AttnArgs& a, int sms, cudaStream_t s, int* parts) 
     if (prepare_kernel((const void*)fn, C::kSmem, C::kThreads, &per_sm) != cudaSuccess || per_sm < 1)
         return DSPARK_ERR_CUDA;
     const int n = sms < kMaxTcParts ? sms : kMaxTcParts;
-    fn<<<n, C::kThreads, C::kSmem, s>>>(a, wait_limit_ns());
     *parts = n;
-    return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+    return launch_overlapped(fn, n, C::kThreads, C::kSmem, s, a, wait_limit_ns()) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 }  // namespace
