@@ -253,16 +253,12 @@ __device__ __forceinline__ PartDesc part_desc(const AttnStart& s, const AttnWalk
     return d;
 }
 
-// tanh from its definition, (1 - e) / (1 + e) with e = e^(-2 |x|); near 0, where that cancels, the odd
-// series to x^7 (relative error below 1e-6 for |x| < 1/8).
-__device__ __forceinline__ float attn_tanh(float x) {
-    const float ax = fabsf(x);
-    if (ax < 0.125f) {
-        const float s = x * x;
-        return x * fmaf(s, fmaf(s, fmaf(s, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
-    }
-    const float e = ex2(-2.f * kLog2e * ax);
-    return copysignf(__fdividef(1.f - e, 1.f + e), x);  // NaN stays NaN: e is
+// c tanh(s / c) log2 e as c log2 e (1 - 2 / (1 + e^(2 s / c))), in = 2 log2 e scale / c of the unscaled
+// score: off by at most 3e-7 c, without a branch.
+__device__ __forceinline__ float softcap(float x, float in, float out) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x * in)));
+    return fmaf(-2.f * out, r, out);
 }
 
 // Two floats rounded to the 16-bit type, first in the low half.

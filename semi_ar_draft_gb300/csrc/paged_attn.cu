@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
     if (tid == 0) mine->d[kTail].first = mine->d[kHead].first = -1;
     float o[DT][4];
     uint32_t qf[C::kQInSmem ? 1 : KS][4];
+    const float cap_out = a.softcap * kLog2e;
     float m[2], l[2], row_scale[2];
     int see_lo[2], see_hi[2], all_lo = 0, all_hi = 0, rows = 0, head = 0, row0 = 0, seg_first = 0;
     bool fresh = true;
@@ -277,7 +278,9 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
                 see_hi[r] = real ? hi_of(token) : 0;
                 m[r] = -CUDART_INF_F;
                 l[r] = 0.f;
-                row_scale[r] = a.scale * (F8 && a.k_scale ? __ldg(a.k_scale + head) : 1.f);
+                // to the log2 domain, or to the cap's exponent
+                row_scale[r] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale *
+                               (F8 && a.k_scale ? __ldg(a.k_scale + head) : 1.f);
                 if (kRescale) row_scale[r] *= __uint_as_float((uint32_t)(127 - raise(row)) << 23);
             }
             if (!C::kQInSmem) {
@@ -331,8 +334,7 @@ __global__ void __launch_bounds__(kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_r
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int r = c >> 1;
-                    float x = s[i][c] * row_scale[r];
-                    x = a.softcap > 0.f ? a.softcap * attn_tanh(x / a.softcap) * kLog2e : x * kLog2e;
+                    float x = a.softcap > 0.f ? softcap(s[i][c], row_scale[r], cap_out) : s[i][c] * row_scale[r];
                     if (edge) {
                         const int key = key0 + 8 * i + 2 * t + (c & 1);
                         if (key < see_lo[r] || key >= see_hi[r]) x = -CUDART_INF_F;

@@ -88,13 +88,6 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {  // (as tmem
                  :
                  : "memory");
 }
-// c tanh(s / c) log2 e as c log2 e (1 - 2 / (1 + e^(2 s / c))), in = 2 log2 e scale / c of the unscaled
-// score: off by at most 3e-7 c, without a branch.
-__device__ __forceinline__ float softcap(float x, float in, float out) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x * in)));
-    return fmaf(-2.f * out, r, out);
-}
 // Descriptor of an N-major (values as they lie: N adjacent, one 128-byte row a K index) operand with the
 // 128-byte swizzle: the leading offset goes from one group of 64 N to the next, the stride offset from
 // eight K rows to the next eight.
