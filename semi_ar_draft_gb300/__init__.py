@@ -2,11 +2,12 @@
 
 libdspark (CUDA, C ABI in include/dspark.h) runs every step; this package holds its build
 script, its ctypes binding (`binding`, same names as the C entry points), allocation helpers
-(`api`) and the seeded synthetic workloads (`workloads`).  The binding is imported lazily so
+(`api`), a paged key-value cache over them (`paged`), decoding rounds that use both
+(`decode_round`) and the seeded synthetic workloads (`workloads`).  The binding is imported lazily so
 that the workloads module can be used without the compiled library.
 """
 
-__all__ = ["binding", "api", "workloads", "build"]
+__all__ = ["binding", "api", "paged", "decode_round", "workloads", "build"]
 
 
 def __getattr__(name):

@@ -1,0 +1,90 @@
+"""A paged key-value cache for the verify step, over the calls of `api`.
+
+The cache of `requests` slots lives in pools of pages shared by all layers' tables: one block table, one page
+stack, and per layer a pool of keys and one of values.  A round is
+
+    plan(new_len, extra)      pages, slots and offsets of the step's new tokens
+    append(layer, k, v)       a layer's new keys and values into their slots
+    attend(layer, q)          a layer's attention of the new tokens
+    commit(add_len, extra)    how many of them stay; pages past them go back
+
+and nothing in it reads the device from the host.  plan and commit write their results to other tensors than
+they read, so the lengths and counts have two buffers each, used in turn."""
+from __future__ import annotations
+
+import torch
+
+from . import api
+from . import binding as b
+
+
+class PagedCache:
+    """requests slots of at most max_blocks pages each; num_pages pages of page_size tokens in all; max_tokens:
+    the most new tokens of a step.  kv_dtype: dtype or torch.float8_e4m3fn, then with k_scale, v_scale
+    [layers, Hk] fp32 (ones if not given)."""
+
+    def __init__(self, requests, num_pages, page_size, max_blocks, layers, Hk, D, max_tokens, dtype=torch.bfloat16,
+                 kv_dtype=None, k_scale=None, v_scale=None, device="cuda"):
+        i32 = {"dtype": torch.int32, "device": device}
+        shape = (layers, num_pages, page_size, Hk, D)
+        self.k_pages = torch.zeros(shape, dtype=dtype, device=device).to(kv_dtype or dtype)
+        self.v_pages = torch.zeros_like(self.k_pages)
+        if kv_dtype == torch.float8_e4m3fn:
+            ones = torch.ones((layers, Hk), device=device)
+            k_scale, v_scale = (ones if s is None else s for s in (k_scale, v_scale))
+        self.k_scale = [None] * layers if k_scale is None else k_scale
+        self.v_scale = [None] * layers if v_scale is None else v_scale
+        self.page_size, self.max_tokens = page_size, max_tokens
+        self.block_table = torch.full((requests, max_blocks), -1, **i32)
+        self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)
+        self._len = [torch.zeros(requests, **i32) for _ in range(2)]
+        self._blocks = [torch.zeros(requests, **i32) for _ in range(2)]
+        self._free = [torch.full((1,), num_pages, **i32) for _ in range(2)]
+        self.seq_len, self.offsets = torch.empty(requests, **i32), torch.empty(requests + 1, **i32)
+        self.slots = torch.empty(max_tokens, dtype=torch.int64, device=device)
+        self.positions = torch.empty(max_tokens, **i32)
+        self.ws = torch.zeros(256, dtype=torch.uint8, device=device)
+        self.max_new = 0
+
+    @property
+    def cache_len(self):
+        """Tokens of each request in the cache [requests] (what plan last read or commit last wrote)."""
+        return self._len[0]
+
+    @property
+    def n_free(self):
+        return self._free[0]
+
+    def plan(self, new_len=None, extra=0, max_new=0, stream=None):
+        """Pages and slots for new_len[j] + extra tokens of each request.  Sets seq_len, offsets, slots, positions.
+        max_new: the most new tokens of one request, if known (it chooses attend's kernel)."""
+        api.cache_plan(self._len[0], new_len, self.block_table, self._blocks[0], self.free_pages, self._free[0],
+                       self.page_size, self.max_tokens, extra=extra, ws=self.ws, stream=stream,
+                       out=(self.seq_len, self.offsets, self.slots, self.positions, self._blocks[1], self._free[1]))
+        self._blocks.reverse()
+        self._free.reverse()
+        self.max_new = max_new
+
+    def append(self, layer, k, v, stream=None):
+        """k, v [max_tokens, Hk, D]: rows past offsets[-1] have no slot and are skipped."""
+        api.cache_append(k, v, self.k_pages[layer], self.v_pages[layer], self.slots, self.k_scale[layer], self.v_scale[layer],
+                         stream)
+
+    def attend(self, layer, q, stream=None, **kw):
+        """q [max_tokens, Hq, D]; kw as for api.paged_attention.  Returns (out, lse or None)."""
+        out, lse, _ = api.paged_attention(q, self.k_pages[layer], self.v_pages[layer], self.block_table, self.seq_len,
+                                          self.offsets, k_scale=self.k_scale[layer], v_scale=self.v_scale[layer],
+                                          max_new=self.max_new, stream=stream, **kw)
+        return out, lse
+
+    def commit(self, add_len=None, extra=0, done=None, stream=None):
+        """Keeps add_len[j] + extra of each request's new tokens (none of the whole request where done)."""
+        api.cache_commit(self._len[0], add_len, self.block_table, self._blocks[0], self.free_pages, self._free[0],
+                         self.page_size, extra=extra, done=done, ws=self.ws, stream=stream,
+                         out=(self._len[1], self._blocks[1], self._free[1]))
+        for pair in (self._len, self._blocks, self._free):
+            pair.reverse()
+
+    def status(self, stream=None):
+        """Device status of the last plan or commit (synchronises)."""
+        return b.dspark_get_device_status(self.ws, stream)
