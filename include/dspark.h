@@ -459,9 +459,10 @@ dspark_status dspark_cache_append(const dspark_append_params* p, const void* k, 
  * Scores, sums and outputs are held in fp32; probabilities are rounded to 16 bits (dtype; fp16 with an
  * 8-bit cache) before they meet the values.  What a row does not see never touches it, whatever is
  * stored there (NaN included).  The same inputs give the same outputs bit for bit.
- * Device status DSPARK_ERR_CACHE: a negative seq_len or one past max_blocks page_size, offsets that descend or
- * leave [0, T], a page outside the pool: each is clamped, such a page reads as zeros, and the outputs of
- * that request are undefined.
+ * Device status DSPARK_ERR_CACHE: a negative seq_len or one past max_blocks page_size (or 2^31 - 4097),
+ * offsets that descend or leave [0, T], a page outside the pool that some row needs (pages wholly before a
+ * request's window may be gone): each is clamped, such a page reads as zeros, and the outputs of that
+ * request are undefined.
  * Host errors: DSPARK_ERR_UNSUPPORTED unless D is a multiple of 16 up to 256 and T Hq < 2^31.
  */
 typedef struct {

@@ -142,8 +142,15 @@ def schedule_verify_len(conf, budget, ws=None, out=None, stream=None):
 _WS = b.CacheParams(1, 1, 1, 1, 0, 0)  # cache_plan's and cache_commit's workspace does not depend on the sizes
 
 
-def _raw(stream):
-    return stream if stream is None else b._stream(stream)
+def _raw(stream, *made):
+    """The stream's address.  Tensors made here for a call on a stream of its own stay reserved for it."""
+    if stream is None:
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+    return b._stream(stream)
 
 
 def _cache_ws(ws, like):
@@ -156,13 +163,14 @@ def cache_plan(cache_len, new_len, block_table, n_blocks, free_pages, n_free, pa
     None), n_blocks [B], free_pages [pages], n_free [1], all int32; block_table [B, max_blocks] int32 gains the new
     pages.  Returns (seq_len [B], offsets [B+1], slots [max_tokens] int64, positions [max_tokens] or None,
     n_blocks [B], n_free [1], workspace); n_blocks and n_free are new tensors."""
+    made = ()
     if out is None:
         B, i32 = cache_len.numel(), {"dtype": torch.int32, "device": cache_len.device}
-        out = (torch.empty(B, **i32), torch.empty(B + 1, **i32), torch.empty(max_tokens, dtype=torch.int64, device=i32["device"]),
-               torch.empty(max_tokens, **i32) if positions else None, torch.empty(B, **i32), torch.empty(1, **i32))
+        made = out = (torch.empty(B, **i32), torch.empty(B + 1, **i32), torch.empty(max_tokens, dtype=torch.int64, device=i32["device"]),
+                      torch.empty(max_tokens, **i32) if positions else None, torch.empty(B, **i32), torch.empty(1, **i32))
     ws = _cache_ws(ws, cache_len)
     st = b.native().cache_plan(cache_len, new_len, block_table, n_blocks, free_pages, n_free, page_size, max_tokens, extra, *out,
-                               ws, _raw(stream))
+                               ws, _raw(stream, ws, *made))
     b._check(st, "dspark_cache_plan")
     return (*out, ws)
 
@@ -172,12 +180,13 @@ def cache_commit(cache_len, add_len, block_table, n_blocks, free_pages, n_free, 
     """The requests' lengths after the verification, and the pages past them back on the stack
     (dspark_cache_commit): add_len [B] int32 (n_accepted) or None, done [B] uint8 or bool, or None; free_pages is
     written in place.  Returns (cache_len [B], n_blocks [B], n_free [1], workspace), new tensors."""
+    made = ()
     if out is None:
         B, i32 = cache_len.numel(), {"dtype": torch.int32, "device": cache_len.device}
-        out = (torch.empty(B, **i32), torch.empty(B, **i32), torch.empty(1, **i32))
+        made = out = (torch.empty(B, **i32), torch.empty(B, **i32), torch.empty(1, **i32))
     ws = _cache_ws(ws, cache_len)
     st = b.native().cache_commit(cache_len, add_len, done, block_table, n_blocks, free_pages, n_free, page_size, extra, *out, ws,
-                                 _raw(stream))
+                                 _raw(stream, ws, *made))
     b._check(st, "dspark_cache_commit")
     return (*out, ws)
 
@@ -186,6 +195,13 @@ def cache_append(k, v, k_pages, v_pages, slots, k_scale=None, v_scale=None, stre
     """Writes k, v [T, Hk, D] (bf16 or fp16; any strides with a dense last dimension) to their slots [T] int64 of
     k_pages, v_pages [pages, page_size, Hk, D] (their type, or e4m3 with k_scale, v_scale [Hk] fp32)."""
     b._check(b.native().cache_append(k, v, k_pages, v_pages, slots, k_scale, v_scale, _raw(stream)), "dspark_cache_append")
+
+
+def _attention_sizes(q, k_pages, seq_len, max_new):
+    """The parameters that decide the workspace's size."""
+    T, Hq, D = q.shape
+    return b.AttentionParams(T, seq_len.numel(), Hq, k_pages.shape[2], D, 1, 1, 1, max_new, b.cache_dtype_code(q.dtype),
+                             b.cache_dtype_code(k_pages.dtype), 1, 0, 1.0, 0.0, 0, 0, 0, 0, 0)
 
 
 def paged_attention(q, k_pages, v_pages, block_table, seq_len, offsets=None, scale=None, causal=True, window=0,
@@ -198,8 +214,10 @@ def paged_attention(q, k_pages, v_pages, block_table, seq_len, offsets=None, sca
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if lse is True:
         lse = torch.empty(q.shape[:2], device=q.device)
+    if ws is None and stream is not None:  # (else it is made in the native call, on the current stream)
+        ws = b.workspace(b.dspark_paged_attention_workspace_size(_attention_sizes(q, k_pages, seq_len, max_new)), q.device)
     st, ws = b.native().paged_attention(q, k_pages, v_pages, block_table, seq_len, offsets, k_scale, v_scale,
                                         q.shape[-1] ** -0.5 if scale is None else scale, softcap, causal, window, max_new, out,
-                                        lse, ws, _raw(stream))
+                                        lse, ws, _raw(stream, ws, out, lse))
     b._check(st, "dspark_paged_attention")
     return out, lse, ws

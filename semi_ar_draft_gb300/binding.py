@@ -103,19 +103,18 @@ def lib():
         L.dspark_tv_l1_loss.restype = i32
         L.dspark_theta_schedule.argtypes = [i32, i32, vp, vp, vp, vp, vp]
         L.dspark_theta_schedule.restype = i32
-        K = C.POINTER(CacheParams)
-        L.dspark_cache_workspace_size.argtypes = [K]
+        # (structures by address: C.byref of any of them)
+        L.dspark_cache_workspace_size.argtypes = [vp]
         L.dspark_cache_workspace_size.restype = sz
-        L.dspark_cache_plan.argtypes = [K, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dspark_cache_plan.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.dspark_cache_plan.restype = i32
-        L.dspark_cache_commit.argtypes = [K, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dspark_cache_commit.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.dspark_cache_commit.restype = i32
-        L.dspark_cache_append.argtypes = [C.POINTER(AppendParams), vp, vp, vp, vp, vp, vp, vp, vp]
+        L.dspark_cache_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp]
         L.dspark_cache_append.restype = i32
-        A = C.POINTER(AttentionParams)
-        L.dspark_paged_attention_workspace_size.argtypes = [A]
+        L.dspark_paged_attention_workspace_size.argtypes = [vp]
         L.dspark_paged_attention_workspace_size.restype = sz
-        L.dspark_paged_attention.argtypes = [A, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dspark_paged_attention.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.dspark_paged_attention.restype = i32
         L.dspark_get_device_status.argtypes = [vp, vp, C.POINTER(C.c_int32)]
         L.dspark_get_device_status.restype = i32

@@ -68,9 +68,10 @@ enum { kTail = 0, kHead = 1 };
 constexpr int kMaxParts = 480;    // blocks of the largest grid with row tiles of 16 (three a multiprocessor)
 constexpr int kMaxTcParts = 160;  // and of 128 (one)
 
-// One request as the kernels see it: every number clamped to the buffers (bad: it was not).
+// One request as the kernels see it: every number clamped to the buffers (bad: it was not).  Keys before lo,
+// the first that any row sees, have no pages any more as far as a call is concerned.
 struct AttnReq {
-    int token0, n, seq, lo;  // lo: first key that any row sees
+    int token0, n, seq, lo;
     bool bad;
 };
 __device__ __forceinline__ AttnReq attn_request(const AttnArgs& a, int j) {
@@ -82,7 +83,7 @@ __device__ __forceinline__ AttnReq attn_request(const AttnArgs& a, int j) {
     }
     const int t0 = min(max(o0, 0), a.T), t1 = min(max(o1, t0), a.T);
     const int len = __ldg(a.seq_len + j);
-    const long long cap = (long long)a.max_blocks << a.page_shift;
+    const long long cap = min((long long)a.max_blocks << a.page_shift, (long long)INT32_MAX - 4096);  // (tiles end past seq)
     r.token0 = t0;
     r.n = t1 - t0;
     r.seq = (int)min((long long)max(len, 0), cap);
@@ -211,6 +212,14 @@ __device__ __forceinline__ void walk_next(const AttnArgs& a, AttnWalk& w, int ro
         ++w.j;
         walk_request(a, w, row_tile, key_tile);
     } while (w.items == 0 && w.j + 1 < a.B);
+}
+
+// The first key that a request's token sees, and the end of those it sees.
+__device__ __forceinline__ int attn_see_lo(const AttnArgs& a, const AttnReq& r, int token) {
+    return a.window > 0 ? (int)max((long long)r.seq - r.n + token - a.window + 1, 0ll) : 0;
+}
+__device__ __forceinline__ int attn_see_hi(const AttnArgs& a, const AttnReq& r, int token) {
+    return a.causal ? min(r.seq - r.n + token + 1, r.seq) : r.seq;
 }
 
 // Rows of out (and lse) past the last request's tokens: no request owns them.  i0: this thread of n.

@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(Rows16<F8, DP>::kThreads, Rows16<F8, DP>::kBlo
     auto load_step = [&]() {
         if (!ld.done() && slice_key(ld) < ld.r.seq) {
             const int key = slice_key(ld) + lane;
-            const bool live = lane < C::kKeys && key < ld.r.seq;
+            const bool live = lane < C::kKeys && key < ld.r.seq && key >= ld.r.lo;
             const bool found = live && pid >= 0 && pid < a.num_pages;
             if (live && !found) err = DSPARK_ERR_CACHE;
             const long long off = found ? pid * a.page + (key & ((1 << a.page_shift) - 1)) * a.token +
@@ -212,11 +212,8 @@ __global__ void __launch_bounds__(Rows16<F8, DP>::kThreads, Rows16<F8, DP>::kBlo
             head = w.item / w.rts;
             row0 = (w.item % w.rts) * kRows;
             rows = min(w.r.n * a.G - row0, kRows);
-            const int pos0 = w.r.seq - w.r.n;  // position of the request's first new token
-            auto lo_of = [&](int token) { return a.window > 0 ? max(pos0 + token - a.window + 1, 0) : 0; };
-            auto hi_of = [&](int token) { return a.causal ? min(pos0 + token + 1, w.r.seq) : w.r.seq; };
-            all_lo = lo_of(attn_token(a, row0 + rows - 1));
-            all_hi = hi_of(attn_token(a, row0));
+            all_lo = attn_see_lo(a, w.r, attn_token(a, row0 + rows - 1));
+            all_hi = attn_see_hi(a, w.r, attn_token(a, row0));
             // The queries, through shared memory: 16 bytes a thread, then the MMA's fragments by ldmatrix.  (The
             // previous segment's readers are past its last barrier.)
             constexpr int kQc = DP / 8;
@@ -283,8 +280,8 @@ __global__ void __launch_bounds__(Rows16<F8, DP>::kThreads, Rows16<F8, DP>::kBlo
             for (int r = 0; r < 2; ++r) {
                 const int row = g + 8 * r, token = attn_token(a, row0 + row);
                 const bool real = row < rows;
-                see_lo[r] = real ? lo_of(token) : 0;
-                see_hi[r] = real ? hi_of(token) : 0;
+                see_lo[r] = real ? attn_see_lo(a, w.r, token) : 0;
+                see_hi[r] = real ? attn_see_hi(a, w.r, token) : 0;
                 m[r] = -CUDART_INF_F;
                 l[r] = 0.f;
                 // to the log2 domain, or to the cap's exponent

@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
             const unsigned char* head_at = k_at + head * a.head;
 #pragma unroll
             for (int h = 0; h < kPids; ++h) {
-                const bool none = (int)key0 + 32 * h + lane >= w.r.seq;
+                const int key = (int)key0 + 32 * h + lane;
+                const bool none = key >= w.r.seq || key < w.r.lo;
                 if ((uint32_t)pid[h] >= (uint32_t)a.num_pages) {
                     if (!none) err = DSPARK_ERR_CACHE;
                     pid[h] = -1;
@@ -415,14 +416,11 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 head = w.item / w.rts;
                 row0 = (w.item % w.rts) * kTcRowTile;
                 rows = min(w.r.n * a.G - row0, kTcRowTile);
-                const int pos0 = w.r.seq - w.r.n;
-                auto lo_of = [&](int token) { return a.window > 0 ? max(pos0 + token - a.window + 1, 0) : 0; };
-                auto hi_of = [&](int token) { return a.causal ? min(pos0 + token + 1, w.r.seq) : w.r.seq; };
-                all_lo = lo_of(attn_token(a, row0 + rows - 1));
-                all_hi = hi_of(attn_token(a, row0));
+                all_lo = attn_see_lo(a, w.r, attn_token(a, row0 + rows - 1));
+                all_hi = attn_see_hi(a, w.r, attn_token(a, row0));
                 const int token = attn_token(a, row0 + row);
-                see_lo = row < rows ? lo_of(token) : 0;
-                see_hi = row < rows ? hi_of(token) : 0;
+                see_lo = row < rows ? attn_see_lo(a, w.r, token) : 0;
+                see_hi = row < rows ? attn_see_hi(a, w.r, token) : 0;
                 m = -CUDART_INF_F;
                 l = 0.f;
             }

@@ -409,6 +409,30 @@ def test_large_scores_and_queries(max_new):
 
 
 @pytest.mark.parametrize("max_new", [1, 17])
+def test_pages_before_the_window_may_be_gone(max_new):
+    """A sliding window's caller gives old pages back: their table entries are not looked at."""
+    for cache in (torch.bfloat16, E4M3):
+        c, lens, offsets = make_case([400, 130], [3, 2], 4, 2, 128, 16, torch.bfloat16, cache, 5)
+        ref, _, ws = attend(c, window=70, max_new=max_new)
+        c["block_table"][0, : (400 - 3 - 70 + 1) // 16] = -1
+        c["block_table"][1, : (130 - 2 - 70 + 1) // 16] = 1 << 30
+        out, _, ws = attend(c, window=70, max_new=max_new)
+        assert status(ws) == 0 and torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("max_new", [1, 17])
+def test_no_tokens_at_all(max_new):
+    c, lens, offsets = make_case([40, 50], [0, 0], 4, 1, 64, 16, torch.bfloat16, torch.bfloat16, 9, pad=2)
+    out, lse, ws = attend(c, max_new=max_new)
+    assert not out.any() and bool((lse == -math.inf).all()) and status(ws) == 0
+    c["q"] = c["q"][:0]
+    out, lse, ws = attend(c, max_new=max_new)
+    assert out.numel() == 0 and status(ws) == 0
+    seq, off, slots, pos, *_ = api.cache_plan(i32([3]), None, i32([[0]]), i32([1]), i32([1]), i32([0]), 16, 0)
+    assert slots.numel() == 0 and off.tolist() == [0, 0] and seq.tolist() == [3]
+
+
+@pytest.mark.parametrize("max_new", [1, 17])
 def test_bad_tables_are_reported(max_new):
     c, lens, offsets = make_case([40, 50], [1, 1], 4, 1, 64, 16, torch.bfloat16, torch.bfloat16, 9)
     ref, _, _ = attend(c, max_new=max_new)
@@ -438,6 +462,9 @@ def test_other_stream_and_graph(max_new):
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
         out, lse, _ = attend(c, max_new=max_new)
+    side.synchronize()
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    out, lse, _ = attend(c, max_new=max_new, stream=side)
     side.synchronize()
     assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
     out = torch.zeros_like(ref)
