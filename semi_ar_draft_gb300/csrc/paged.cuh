@@ -270,6 +270,21 @@ __device__ __forceinline__ float softcap(float x, float in, float out) {
     return fmaf(-2.f * out, r, out);
 }
 
+// Whether one of a word's values is NaN or inf, gathered over words: note(w, acc), then found(acc).
+template <bool F8, bool BF16>
+__device__ __forceinline__ void odd_note(uint32_t w, uint32_t& acc) {
+    if (F8)  // e4m3 has no inf: NaN is 0x7f but for the sign
+        acc |= (w & 0x7f7f7f7fu) + 0x01010101u;
+    else  // the largest magnitude of either half
+        acc = __vmaxu2(acc, w & 0x7fff7fffu);
+}
+template <bool F8, bool BF16>
+__device__ __forceinline__ bool odd_found(uint32_t acc) {
+    if (F8) return (acc & 0x80808080u) != 0;
+    constexpr uint32_t inf = BF16 ? 0x7f80u : 0x7c00u;
+    return (acc & 0xffffu) >= inf || (acc >> 16) >= inf;
+}
+
 // Two floats rounded to the 16-bit type, first in the low half.
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {

@@ -384,18 +384,16 @@ __global__ void __launch_bounds__(Rows16<F8, DP>::kThreads, Rows16<F8, DP>::kBlo
             // key, over the rows that see it.
             bool odd = false;
             if (edge) {
-                uint32_t any = 0;
-                const unsigned char* vs = ring + st * C::kStage + C::kHalf;
-                for (int i = lane; i < C::kHalf / 4; i += 32) {
-                    const uint32_t x = reinterpret_cast<const uint32_t*>(vs)[i];
-                    if (F8)
-                        any |= (__vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu));
-                    else if (BF16)
-                        any |= (__vcmpeq2(x & 0x7f807f80u, 0x7f807f80u));
-                    else
-                        any |= (__vcmpeq2(x & 0x7c007c00u, 0x7c007c00u));
+                uint32_t acc = 0;
+                const uint4* vs = reinterpret_cast<const uint4*>(ring + st * C::kStage + C::kHalf);
+                for (int i = lane; i < C::kHalf / 16; i += 32) {
+                    const uint4 y = vs[i];
+                    odd_note<F8, BF16>(y.x, acc);
+                    odd_note<F8, BF16>(y.y, acc);
+                    odd_note<F8, BF16>(y.z, acc);
+                    odd_note<F8, BF16>(y.w, acc);
                 }
-                odd = __any_sync(0xffffffffu, any != 0);
+                odd = __any_sync(0xffffffffu, odd_found<F8, BF16>(acc));
             }
             if (!odd) {
                 // Probabilities are rounded to the cache's 16-bit type (halves for an 8-bit cache) for

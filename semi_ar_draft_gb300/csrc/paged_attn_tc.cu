@@ -534,14 +534,16 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 const int tile = n * NS + s, slot = tile % C::kSlots;
                 if (!warp_wait(&bars->full[slot], (uint32_t)((tile / C::kSlots) & 1))) break;
                 unsigned char* v = smem + C::kRing + slot * (2 * C::kTile) + C::kTile;
-                bool any = false;
+                uint32_t acc = 0;
                 for (int i = row; i < C::kTile / 16; i += 128) {
                     const uint4 y = reinterpret_cast<const uint4*>(v)[i];
-                    any |= is_odd16<BF16>(y.x) | is_odd16<BF16>(y.x >> 16) | is_odd16<BF16>(y.y) | is_odd16<BF16>(y.y >> 16) |
-                           is_odd16<BF16>(y.z) | is_odd16<BF16>(y.z >> 16) | is_odd16<BF16>(y.w) | is_odd16<BF16>(y.w >> 16);
+                    odd_note<false, BF16>(y.x, acc);
+                    odd_note<false, BF16>(y.y, acc);
+                    odd_note<false, BF16>(y.z, acc);
+                    odd_note<false, BF16>(y.w, acc);
                 }
                 int* odd = &bars->odd[s][n & 1];  // (cleared before the tile after next can set it)
-                if (any) *odd = 1;
+                if (odd_found<false, BF16>(acc)) *odd = 1;
                 if (!stream_meet()) break;
                 const bool found = *reinterpret_cast<volatile int*>(odd) != 0;
                 if (found) {
