@@ -37,7 +37,10 @@ struct TcAttn {
     static constexpr int kUnit = kStreams * kKt;
     static constexpr int kExtra = DP == 128 ? 2 : 4;  // what an item costs beside its key tiles
     static constexpr int kSoftmaxWarps = 4 * kStreams;
+    // Four loader warps, two a stream: a warp that copied a part of every tile spent more time between tiles
+    // (waits, page numbers, the walk) than on its copies.
     static constexpr int kLoaders = 4;
+    static constexpr int kTileLoaders = kLoaders / kStreams;
     // Warps after the softmax's: multiprocessor quarter (warp % 4) 0 has none of them and quarter 1 the MMA
     // warps, one a stream; the loaders are in quarters 2 and 3.  Short row tiles keep quarter 0 busiest.
     static constexpr int kWarps = kSoftmaxWarps + 8;
@@ -53,8 +56,9 @@ struct TcAttn {
     static constexpr int kSub = DP / 64;                  // 64-value groups of a row
     static constexpr int kTile = kKt * DP * 2;            // bytes of a tile's K (or V)
     static constexpr int kQ = kTcRowTile * DP * 2;
-    static constexpr int kQBufs = DP == 256 ? 1 : 2;
-    static constexpr int kSlots = DP == 64 ? 10 : (DP == 128 ? 5 : 4);
+    static constexpr int kQBufs = DP == 64 ? 2 : 1;
+    static constexpr int kSlots = DP == 64 ? 10 : (DP == 128 ? 6 : 4);
+    static_assert(kSlots % kStreams == 0, "a slot belongs to one stream, whose loaders wait for no other's turn");
     static constexpr int kRing = kQBufs * kQ;
     static constexpr int kMeta = kRing + kSlots * 2 * kTile;
     static constexpr size_t kSmem = (size_t)kMeta + 2 * kTcRowTile * 8 + 512;
@@ -149,7 +153,7 @@ __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
 }
 
 struct TcBars {
-    uint64_t full[10], empty[10], qempty[2], sfull[2], sfree[2], pfull[2], pvdone[2], smeet[2], drain[2], meet;
+    uint64_t full[10], empty[10], qfull[2], qempty[2], sfull[2], sfree[2], pfull[2], pvdone[2], smeet[2], drain[2], meet;
     uint32_t tmem;
     int abort, status, misaligned;
     int odd[2][2];
@@ -168,11 +172,12 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
     const int part = blockIdx.x, parts = gridDim.x;
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(&bars->full[i], 32 * C::kLoaders);
+            mbar_init(&bars->full[i], 32 * C::kTileLoaders);
             mbar_init(&bars->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->qempty[i], NS);
+            mbar_init(&bars->qfull[i], 32 * C::kLoaders);
             mbar_init(&bars->sfull[i], 1);
             mbar_init(&bars->sfree[i], 4);
             mbar_init(&bars->pfull[i], 4);
@@ -226,27 +231,55 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         const long long v_after_k = a.v_pages - a.k_pages;
         AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit, C::kExtra);
         int err = 0, seg = 0;
-        auto unit_key = [&]() { return (w.kt_first + w.kt) * C::kUnit; };
-        // Pages of the next unit's keys (lane: keys lane, lane + 32, ...), asked for a unit ahead.  The load is
-        // unconditional (entry 0 where there is no key) and looked at when the copies are issued, so that
-        // nothing waits for it here.
-        constexpr int kPids = C::kUnit / 32;
-        int pid[kPids];
+        // This warp's keys of its stream's tiles.
+        constexpr int kKeys = KT / C::kTileLoaders;
+        const int first_key = (lw / C::kTileLoaders) * KT + (lw % C::kTileLoaders) * kKeys;
+        auto tile_key = [&]() { return (w.kt_first + w.kt) * C::kUnit + first_key; };
+        // Page of this lane's key of the next tile, asked for a tile ahead.  The load is unconditional (entry 0
+        // where there is no key) and looked at when the copies are issued, so that nothing waits for it here.
+        int pid;
         auto fetch_pages = [&]() {
-#pragma unroll
-            for (int h = 0; h < kPids; ++h) {
-                const int key = min(unit_key() + 32 * h + lane, w.r.seq - 1);
-                const size_t at = w.done() || key < 0 ? 0 : (size_t)w.j * a.max_blocks + (key >> a.page_shift);
-                pid[h] = __ldg(a.block_table + at);
-            }
+            const int key = min(tile_key() + lane, w.r.seq - 1);
+            const size_t at = w.done() || key < 0 ? 0 : (size_t)w.j * a.max_blocks + (key >> a.page_shift);
+            pid = __ldg(a.block_table + at);
         };
         fetch_pages();
         bool fresh = true;
-        int head = 0, slot = 0, round = 0;
+        int head = 0, slot = lw / C::kTileLoaders, round = 0;
         while (!w.done()) {
-            if (fresh) {
+            if (fresh) head = w.item / w.rts;
+            if (round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) break;
+            const int key0 = tile_key();
+            const unsigned char* head_at = k_at + head * a.head;
+            const bool none = key0 + lane >= w.r.seq || key0 + lane < w.r.lo;
+            if ((uint32_t)pid >= (uint32_t)a.num_pages) {
+                if (!none && lane < kKeys) err = DSPARK_ERR_CACHE;
+                pid = -1;
+            }
+            if (none) pid = -1;
+            const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + (uint32_t)(chunk >> 3) * (KT * 128);
+            const int tile_row = (lw % C::kTileLoaders) * kKeys + sub_row;
+#pragma unroll 8
+            for (int i = 0; i < kKeys; i += kPer) {
+                const int p = __shfl_sync(0xffffffffu, pid, i + sub_row);
+                const bool real = inside && p >= 0;
+                const uint64_t at16 = (uint64_t)(uint32_t)max(p, 0) * page16 +
+                                      (uint64_t)((uint32_t)(key0 + i + sub_row) & mask) * token16;
+                const unsigned char* src = real ? head_at + 16 * at16 : a.k_pages;
+                const uint32_t dst = kb + sw128_offset(tile_row + i, chunk & 7);
+                copy16(dst, src, real);
+                copy16(dst + C::kTile, src + v_after_k, real);
+            }
+            // The slot is full once its loaders' copies so far have landed; nobody waits for that here, so the
+            // whole ring can be in flight.
+            copy_arrive(&bars->full[slot]);
+            slot += NS;
+            if (slot >= C::kSlots) {
+                slot -= C::kSlots;
+                ++round;
+            }
+            if (fresh) {  // an item's queries, after its first keys: their buffer is free later than a slot
                 fresh = false;
-                head = w.item / w.rts;
                 const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
                 if (use > 0 && !warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) break;
                 ++seg;
@@ -262,51 +295,8 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                                                : 0;
                     copy16(qbase + sw128_offset(r, chunk & 7), a.q + 2 * src, real);
                 }
+                copy_arrive(&bars->qfull[qb]);
             }
-            const uint32_t key0 = (uint32_t)unit_key();
-            const unsigned char* head_at = k_at + head * a.head;
-#pragma unroll
-            for (int h = 0; h < kPids; ++h) {
-                const int key = (int)key0 + 32 * h + lane;
-                const bool none = key >= w.r.seq || key < w.r.lo;
-                if ((uint32_t)pid[h] >= (uint32_t)a.num_pages) {
-                    if (!none) err = DSPARK_ERR_CACHE;
-                    pid[h] = -1;
-                }
-                if (none) pid[h] = -1;
-            }
-            bool ok = true;
-#pragma unroll 1
-            for (int stream = 0; stream < NS; ++stream) {  // (rolled: less code, and pid moves along)
-                if (round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + (uint32_t)(chunk >> 3) * (KT * 128);
-#pragma unroll
-                for (int u = 0; u < KT / kPer / C::kLoaders; ++u) {
-                    const int i = u * C::kLoaders + lw;
-                    const int r = i * kPer + sub_row;  // (32 rows are a whole number of steps)
-                    const int p = __shfl_sync(0xffffffffu, KT > 32 && i * kPer >= 32 ? pid[KT / 32 - 1] : pid[0], r & 31);
-                    const bool real = inside && p >= 0;
-                    const uint64_t at16 = (uint64_t)(uint32_t)max(p, 0) * page16 +
-                                          (uint64_t)((key0 + stream * KT + r) & mask) * token16;
-                    const unsigned char* src = real ? head_at + 16 * at16 : a.k_pages;
-                    const uint32_t dst = kb + sw128_offset(r, chunk & 7);
-                    copy16(dst, src, real);
-                    copy16(dst + C::kTile, src + v_after_k, real);
-                }
-                // The slot is full once every loader thread's copies so far have landed (its queries among
-                // them); nobody waits for that here, so the whole ring can be in flight.
-                copy_arrive(&bars->full[slot]);
-                if (++slot == C::kSlots) {
-                    slot = 0;
-                    ++round;
-                }
-#pragma unroll
-                for (int h = 0; h + KT / 32 < kPids; ++h) pid[h] = pid[h + KT / 32];
-            }
-            if (!ok) break;
             fresh = w.kt + 1 == w.kts;
             walk_next(a, w, kTcRowTile, C::kUnit);
             fetch_pages();
@@ -345,7 +335,8 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         };
         for (int unit = 0; ok && __shfl_sync(0xffffffffu, !w.done(), 0); ++unit) {
             const int qb = seg % C::kQBufs;
-            if (!warp_wait(&bars->full[slot], (uint32_t)turn) ||
+            if ((!behind && !warp_wait(&bars->qfull[qb], (uint32_t)((seg / C::kQBufs) & 1))) ||  // an item's first tile
+                !warp_wait(&bars->full[slot], (uint32_t)turn) ||
                 (unit > 0 && !warp_wait(&bars->sfree[s], (uint32_t)((unit - 1) & 1))))
                 break;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the loaders' copies, to the MMA
