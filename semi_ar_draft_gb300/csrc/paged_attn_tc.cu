@@ -246,8 +246,34 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         fetch_pages();
         bool fresh = true;
         int head = 0, slot = lw / C::kTileLoaders, round = 0;
+        // An item's queries: with two streams after its first keys, since their buffer is free later than a
+        // slot (421 against 426 us for the 512-request verify); with heads of 256, where they are as large as two
+        // tiles, before (122 against 131 us for three long contexts).
+        constexpr bool kQueriesFirst = NS == 1;
+        auto queries = [&]() {
+            const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
+            if (use > 0 && !warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) return false;
+            ++seg;
+            const int row0 = (w.item - head * w.rts) * kTcRowTile;
+            const int rows = min(w.r.n * a.G - row0, kTcRowTile);
+            const uint32_t qbase = base + (uint32_t)qb * C::kQ + (uint32_t)(chunk >> 3) * (kTcRowTile * 128);
+            for (int r = lw * kPer + sub_row; r < ((rows + 31) & ~31); r += C::kLoaders * kPer) {
+                const bool real = inside && r < rows;
+                const int row = row0 + r;
+                const int token = attn_token(a, row);
+                const long long src = real ? (w.r.token0 + token) * a.q_token +
+                                                 (head * a.G + row - token * a.G) * a.q_head + chunk * 8
+                                           : 0;
+                copy16(qbase + sw128_offset(r, chunk & 7), a.q + 2 * src, real);
+            }
+            copy_arrive(&bars->qfull[qb]);
+            return true;
+        };
         while (!w.done()) {
-            if (fresh) head = w.item / w.rts;
+            if (fresh) {
+                head = w.item / w.rts;
+                if (kQueriesFirst && !queries()) break;
+            }
             if (round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) break;
             const int key0 = tile_key();
             const unsigned char* head_at = k_at + head * a.head;
@@ -278,25 +304,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 slot -= C::kSlots;
                 ++round;
             }
-            if (fresh) {  // an item's queries, after its first keys: their buffer is free later than a slot
-                fresh = false;
-                const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
-                if (use > 0 && !warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) break;
-                ++seg;
-                const int row0 = (w.item - head * w.rts) * kTcRowTile;
-                const int rows = min(w.r.n * a.G - row0, kTcRowTile);
-                const uint32_t qbase = base + (uint32_t)qb * C::kQ + (uint32_t)(chunk >> 3) * (kTcRowTile * 128);
-                for (int r = lw * kPer + sub_row; r < ((rows + 31) & ~31); r += C::kLoaders * kPer) {
-                    const bool real = inside && r < rows;
-                    const int row = row0 + r;
-                    const int token = attn_token(a, row);
-                    const long long src = real ? (w.r.token0 + token) * a.q_token +
-                                                     (head * a.G + row - token * a.G) * a.q_head + chunk * 8
-                                               : 0;
-                    copy16(qbase + sw128_offset(r, chunk & 7), a.q + 2 * src, real);
-                }
-                copy_arrive(&bars->qfull[qb]);
-            }
+            if (fresh && !kQueriesFirst && !queries()) break;
             fresh = w.kt + 1 == w.kts;
             walk_next(a, w, kTcRowTile, C::kUnit);
             fetch_pages();
