@@ -18,8 +18,8 @@
 //
 // Bound by the cache's bytes where a unit's softmax (about 2000 cycles for a stream's tile of 64 keys) is
 // shorter than its loads: 512 requests of up to 4096 tokens, 8 query heads of 128 a kv head, 5 new tokens on
-// average: 467 us = 5.3 TB/s (0.79 of the measured copy rate).  With heads of 64 a tile is half the bytes and the
-// softmax decides: 32 draft blocks of 16 over up to 4100 tokens 56 us = 2.7 TB/s (0.39).
+// average: 419 us = 6.0 TB/s (0.88 of the measured copy rate).  With heads of 64 a tile is half the bytes and the
+// softmax decides: 32 draft blocks of 16 over up to 4100 tokens 52 us = 2.9 TB/s (0.42).
 #include "host_util.h"
 #include "paged.cuh"
 #include "pdl.cuh"
