@@ -454,7 +454,8 @@ dspark_status dspark_cache_append(const dspark_append_params* p, const void* k, 
  *   q [T, Hq, D] (dtype; D adjacent values, strides in elements); block_table, seq_len as above;
  *   offsets [B+1] int32, or NULL for one token a request (T >= B then); k_pages, v_pages
  *   (kv_dtype: dtype, or DSPARK_E4M3 with k_scale, v_scale [Hk] float, NULL = 1).
- *   max_new: the most new tokens of one request, if known (0 = not): it only chooses between kernels.
+ *   max_new: the most new tokens of one request, if known (0 = not): with T / B it only chooses between
+ *   kernels.
  * Outputs: out [T, Hq, D] dense (dtype), 16-byte aligned; lse [T, Hq] float or NULL.
  * Scores, sums and outputs are held in fp32; probabilities are rounded to 16 bits (dtype; fp16 with an
  * 8-bit cache) before they meet the values.  What a row does not see never touches it, whatever is

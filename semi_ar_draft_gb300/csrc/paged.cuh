@@ -297,8 +297,8 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 
 
-// Row tiles of 128 on the fifth-generation tensor cores (paged_attn_tc.cu): 16-bit caches, 16-byte
+// Row tiles of 128 on the fifth-generation tensor cores (paged_attn_tc.cu); needs 16-byte
 // aligned query rows.
-dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int sms, cudaStream_t s, int* parts);
+dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, bool e4m3, int sms, cudaStream_t s, int* parts);
 
 }  // namespace dspark

@@ -5,13 +5,13 @@
 //   o = sum_l 2^(s_l log2 e - m) v_l / sum
 //
 // attn_rows16_kernel: row tiles of 16 (one token of up to 16 query heads a kv head, or a few tokens of
-// fewer; any number of rows of an 8-bit cache).  A cache row of D 16-bit values is used for 4 D operations a row,
-// so at 16 rows the kernel is bound by the cache's bytes: 16 operations a byte against the card's several
-// hundred.  What it needs is loads in flight, so each warp streams key slices of its own (16 keys, or 32 of an
-// 8-bit cache) through a ring of its own in shared memory, 16 bytes a copy, with no barrier between warps; the
-// page numbers of a slice are fetched a step before its copies are issued.  The warps' statistics and outputs
-// meet once per segment, in the stages just consumed (a stage is as large as a warp's output: 64 D bytes).
-// Two blocks a multiprocessor or more, so that one streams while another joins.
+// fewer; up to some 48 rows of an 8-bit cache: wide_rows).  A cache row of D 16-bit values is used for 4 D
+// operations a row, so at 16 rows the kernel is bound by the cache's bytes: 16 operations a byte against the
+// card's several hundred.  What it needs is loads in flight, so each warp streams key slices of its own (16
+// keys, or 32 of an 8-bit cache) through a ring of its own in shared memory, 16 bytes a copy, with no barrier
+// between warps; the page numbers of a slice are fetched a step before its copies are issued.  The warps'
+// statistics and outputs meet once per segment, in the stages just consumed (a stage is as large as a warp's
+// output: 64 D bytes).  Two blocks a multiprocessor or more, so that one streams while another joins.
 // Measured: 32 requests of up to 8192 tokens, 8 kv heads of 128, bf16: 94 us = 6.0 TB/s (0.89 of the measured copy
 // rate), of which 5 us are the join; 128 requests over an e4m3 cache 204 us = 5.5 TB/s (0.81), where the
 // conversions keep the issue slots busy; one request of 1024 tokens 12 us, latency.
@@ -688,13 +688,15 @@ dspark_status launch_rows16_d(const AttnArgs& a, int sms, cudaStream_t s, int* p
 struct AttnWs {
     size_t items, ml, o, bytes;
 };
-// Whether a call takes row tiles of 128: the most rows a request and kv head can have (from max_new, or
-// the mean number of tokens where it is not given) against the 16 of the other kernel, and a 16-bit cache.
-// (8-bit tiles widened on their way into the wide kernel's ring took 101 us where five row tiles of 16 take
-// 65, and 170 against 195 with heads of 256: not worth a second path.)
+// Whether a call takes row tiles of 128: when a request has more rows a kv head than the limit, on average
+// (T / B tokens) and at most (max_new, if given).  Measured, tiles of 16 against tiles of 128, us:
+//   16-bit   mean 11 rows 117 / 116 (long contexts) and 63 / 87 (short); mean 14: 130 / 111 and 71 / 86;
+//            mean 24: 88 / 69; heads of 256, mean 11: 214 / 249, mean 24: 159 / 135
+//   e4m3     mean 35 rows 72 / 88 and 37 / 43; 68 rows: 80 / 53; mean 70: 166 / 102; 119 rows: 267 / 93
+// (an 8-bit tile has to be widened for the wide kernel, so it needs more rows to pay).
 bool wide_rows(const dspark_attention_params* p) {
-    const int n = p->max_new > 0 ? p->max_new : (p->T + p->B - 1) / p->B;
-    return p->kv_dtype == p->dtype && (long long)n * (p->Hq / p->Hk) > kRows;
+    const long long G = p->Hq / p->Hk, limit = p->kv_dtype == p->dtype ? kRows : 48;
+    return G * p->T > limit * p->B && (p->max_new <= 0 || G * p->max_new > limit);
 }
 AttnWs attn_ws(const dspark_attention_params* p) {
     const size_t rows = wide_rows(p) ? (size_t)2 * kMaxTcParts * kTcRows : (size_t)2 * kMaxParts * kRows;
@@ -790,7 +792,7 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     const bool bf16 = p->dtype == DSPARK_BF16;
     int parts = 0;
     const bool tc = wide_rows(p) && a.q_vec;
-    const dspark_status ls = tc     ? launch_attn_tc(a, bf16, sms, s, &parts)
+    const dspark_status ls = tc     ? launch_attn_tc(a, bf16, e4m3, sms, s, &parts)
                              : bf16 ? (e4m3 ? launch_rows16_d<true, true>(a, sms, s, &parts)
                                           : launch_rows16_d<true, false>(a, sms, s, &parts))
                                   : (e4m3 ? launch_rows16_d<false, true>(a, sms, s, &parts)

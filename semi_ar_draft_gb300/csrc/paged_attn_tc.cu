@@ -1,10 +1,12 @@
 // paged_attn_tc.cu -- dspark_paged_attention on the fifth-generation tensor cores: row tiles of 128 for
-// requests whose new tokens give more than 16 rows a kv head (the flattened verify, draft blocks).
+// requests whose new tokens give more than 16 rows a kv head, 48 with an 8-bit cache (the flattened verify, draft
+// blocks).
 //
 // One persistent CTA a multiprocessor walks its range of units (paged.cuh).  Roles:
 //   loaders (4 warps)    copy the item's queries and, tile by tile, KT keys and values into a ring in
 //                        shared memory, 16 bytes a thread and copy, in the 128-byte-swizzled layout the MMA
-//                        reads; several tiles in flight, across items
+//                        reads; several tiles in flight, across items; tiles of an 8-bit cache arrive as they are
+//                        and are widened into the ring by the lanes that copied them
 //   MMA (1 warp a stream) S = Q K^T into tensor memory, and O += P V with P from tensor memory
 //   softmax (4 warps a   thread = row: takes S, writes P (16 bits) back to tensor memory, keeps the row's
 //     stream)            maximum and sum; at an item's end joins the streams and writes the output
@@ -20,6 +22,8 @@
 // shorter than its loads: 512 requests of up to 4096 tokens, 8 query heads of 128 a kv head, 5 new tokens on
 // average: 419 us = 6.0 TB/s (0.88 of the measured copy rate).  With heads of 64 a tile is half the bytes and the
 // softmax decides: 32 draft blocks of 16 over up to 4100 tokens 52 us = 2.9 TB/s (0.42).
+// Over an 8-bit cache the loaders' widening decides at few rows (32 requests, 35 rows on average: 88 us, of row
+// tiles of 16: 72) and pays at many (145 requests, 119 rows of 192 over 200 keys: 93 us against 267).
 #include "host_util.h"
 #include "paged.cuh"
 #include "pdl.cuh"
@@ -30,7 +34,7 @@ namespace {
 
 constexpr int kTcRowTile = 128;
 
-template <int DP>
+template <bool F8, int DP>
 struct TcAttn {
     static constexpr int kStreams = DP == 256 ? 1 : 2;
     static constexpr int kKt = DP == 256 ? 32 : 64;  // keys of a tile
@@ -57,10 +61,14 @@ struct TcAttn {
     static constexpr int kTile = kKt * DP * 2;            // bytes of a tile's K (or V)
     static constexpr int kQ = kTcRowTile * DP * 2;
     static constexpr int kQBufs = DP == 64 ? 2 : 1;
-    static constexpr int kSlots = DP == 64 ? 10 : (DP == 128 ? 6 : 4);
+    static constexpr int kSlots = F8 ? (DP == 64 ? 6 : (DP == 128 ? 4 : 3)) : (DP == 64 ? 10 : (DP == 128 ? 6 : 4));
+    // 8-bit caches: raw tiles a loader keeps on their way, 16 bytes a lane and copy, K and V of its rows
+    static constexpr int kRawSlots = F8 ? (DP == 128 ? 2 : 4) : 0;
+    static constexpr int kRawTile = 2 * (kKt / kTileLoaders) * DP;  // bytes of a loader's part of one
     static_assert(kSlots % kStreams == 0, "a slot belongs to one stream, whose loaders wait for no other's turn");
     static constexpr int kRing = kQBufs * kQ;
-    static constexpr int kMeta = kRing + kSlots * 2 * kTile;
+    static constexpr int kRaw = kRing + kSlots * 2 * kTile;
+    static constexpr int kMeta = kRaw + kLoaders * kRawSlots * kRawTile;
     static constexpr size_t kSmem = (size_t)kMeta + 2 * kTcRowTile * 8 + 512;
     // tensor memory columns
     static constexpr int kColS = kStreams * DP, kColP = kColS + kStreams * kKt;
@@ -120,6 +128,27 @@ __device__ __forceinline__ float from16(uint32_t half) {
     return BF16 ? bf16_bits_to_f32(half & 0xffffu) : __half2float(__ushort_as_half((unsigned short)half));
 }
 
+// Sixteen e4m3 values as bf16 or fp16 values (both hold them exactly), in order.
+template <bool BF16>
+__device__ __forceinline__ void widen16(const uint4 v, uint4& lo, uint4& hi) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t h;
+        const uint32_t pair = i & 1 ? w[i >> 1] >> 16 : w[i >> 1];
+        asm("{ .reg .b16 x; cvt.u16.u32 x, %1; cvt.rn.f16x2.e4m3x2 %0, x; }" : "=r"(h) : "r"(pair));
+        if (BF16) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            r[i] = pack16<true>(f.x, f.y);
+        } else {
+            r[i] = h;
+        }
+    }
+    lo = make_uint4(r[0], r[1], r[2], r[3]);
+    hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
 // MMAs and commits by one elected lane of a converged warp (always the same one).  Descriptors come in
 // halves; kind::f16, fp32 accumulation; accumulate = 0 overwrites D.
 __device__ __forceinline__ void mma_elect_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
@@ -161,9 +190,10 @@ struct TcBars {
 };
 static_assert(sizeof(TcBars) <= 512, "barriers");
 
-template <bool BF16, int DP>
-__global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnArgs a, uint64_t limit_ns) {
-    using C = TcAttn<DP>;
+template <bool BF16, bool F8, int DP>
+__global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(AttnArgs a, uint64_t limit_ns) {
+    using C = TcAttn<F8, DP>;
+    constexpr bool VB = BF16 && !F8;  // type of P and V: an 8-bit cache's values meet the probabilities as halves
     constexpr int KT = C::kKt, NS = C::kStreams;
     extern __shared__ __align__(1024) unsigned char smem[];
     float2* s_ml = reinterpret_cast<float2*>(smem + C::kMeta);  // [kStreams][128]
@@ -219,11 +249,11 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
 
     if (C::loader_of(warp) >= 0) {
         // ---------------------------------------------------------------- loaders
-        constexpr int kChunks = DP / 8;              // 16-byte groups of a row
+        constexpr int kChunks = DP / (F8 ? 16 : 8);  // 16-byte groups of a row in the cache
         constexpr int kPer = 32 / kChunks;           // rows a warp copies at a time
         const int lw = C::loader_of(warp);
         const int chunk = lane % kChunks, sub_row = lane / kChunks;
-        const bool inside = chunk * 8 < a.D;
+        const bool inside = chunk * (F8 ? 16 : 8) < a.D;
         const uint32_t base = smem_addr(smem);
         const uint32_t mask = (1u << a.page_shift) - 1;
         const uint32_t page16 = (uint32_t)(a.page >> 4), token16 = (uint32_t)(a.token >> 4);
@@ -246,25 +276,66 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         fetch_pages();
         bool fresh = true;
         int head = 0, slot = lw / C::kTileLoaders, round = 0;
+        const int tile_row = (lw % C::kTileLoaders) * kKeys + sub_row;
+        // 8-bit caches: a tile arrives as it is, each lane's pieces in places of its own, `ahead` tiles at a time; the
+        // lane that copied a piece widens it into the slot, keys to q's type, values to halves (both exact).
+        constexpr int kSteps = kKeys / kPer;
+        int raw_slot = 0, raw_old = 0, ahead = 0;
+        unsigned char* raw = smem + C::kRaw + lw * (C::kRawSlots * C::kRawTile) + lane * 16;
+        auto widen = [&]() {
+            if (round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) return false;
+            unsigned char* to = smem + C::kRing + slot * (2 * C::kTile) + ((2 * chunk) >> 3) * (KT * 128);
+            const unsigned char* from = raw + raw_old * C::kRawTile;
+#pragma unroll 2
+            for (int u = 0; u < kSteps; ++u) {
+                const uint32_t at0 = sw128_offset(tile_row + u * kPer, (2 * chunk) & 7);
+                const uint32_t at1 = sw128_offset(tile_row + u * kPer, (2 * chunk + 1) & 7);
+                const uint4 k = *reinterpret_cast<const uint4*>(from + 2 * u * 512);
+                const uint4 v = *reinterpret_cast<const uint4*>(from + (2 * u + 1) * 512);
+                uint4 x, y;
+                widen16<BF16>(k, x, y);
+                *reinterpret_cast<uint4*>(to + at0) = x;
+                *reinterpret_cast<uint4*>(to + at1) = y;
+                widen16<false>(v, x, y);
+                *reinterpret_cast<uint4*>(to + at0 + C::kTile) = x;
+                *reinterpret_cast<uint4*>(to + at1 + C::kTile) = y;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive_local(&bars->full[slot]);
+            slot += NS;
+            if (slot >= C::kSlots) {
+                slot -= C::kSlots;
+                ++round;
+            }
+            if (++raw_old == C::kRawSlots) raw_old = 0;
+            return true;
+        };
         // An item's queries: with two streams after its first keys, since their buffer is free later than a
         // slot (421 against 426 us for the 512-request verify); with heads of 256, where they are as large as two
         // tiles, before (122 against 131 us for three long contexts).
         constexpr bool kQueriesFirst = NS == 1;
         auto queries = [&]() {
             const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
+            if (F8 && use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1)))) {
+                // the products that still read it may be waiting for raw tiles
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                while (ahead > 0 && widen()) --ahead;
+            }
             if (use > 0 && !warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) return false;
             ++seg;
             const int row0 = (w.item - head * w.rts) * kTcRowTile;
             const int rows = min(w.r.n * a.G - row0, kTcRowTile);
-            const uint32_t qbase = base + (uint32_t)qb * C::kQ + (uint32_t)(chunk >> 3) * (kTcRowTile * 128);
-            for (int r = lw * kPer + sub_row; r < ((rows + 31) & ~31); r += C::kLoaders * kPer) {
-                const bool real = inside && r < rows;
+            constexpr int kQPer = 256 / DP;  // rows a warp copies at a time
+            const int qc = lane % (DP / 8);
+            const uint32_t qbase = base + (uint32_t)qb * C::kQ + (uint32_t)(qc >> 3) * (kTcRowTile * 128);
+            for (int r = lw * kQPer + lane / (DP / 8); r < ((rows + 31) & ~31); r += C::kLoaders * kQPer) {
+                const bool real = qc * 8 < a.D && r < rows;
                 const int row = row0 + r;
                 const int token = attn_token(a, row);
                 const long long src = real ? (w.r.token0 + token) * a.q_token +
-                                                 (head * a.G + row - token * a.G) * a.q_head + chunk * 8
+                                                 (head * a.G + row - token * a.G) * a.q_head + qc * 8
                                            : 0;
-                copy16(qbase + sw128_offset(r, chunk & 7), a.q + 2 * src, real);
+                copy16(qbase + sw128_offset(r, qc & 7), a.q + 2 * src, real);
             }
             copy_arrive(&bars->qfull[qb]);
             return true;
@@ -274,7 +345,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 head = w.item / w.rts;
                 if (kQueriesFirst && !queries()) break;
             }
-            if (round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) break;
+            if (!F8 && round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) break;
             const int key0 = tile_key();
             const unsigned char* head_at = k_at + head * a.head;
             const bool none = key0 + lane >= w.r.seq || key0 + lane < w.r.lo;
@@ -284,7 +355,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
             }
             if (none) pid = -1;
             const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + (uint32_t)(chunk >> 3) * (KT * 128);
-            const int tile_row = (lw % C::kTileLoaders) * kKeys + sub_row;
+            const uint32_t rb = smem_addr(raw) + (uint32_t)(raw_slot * C::kRawTile);
 #pragma unroll 8
             for (int i = 0; i < kKeys; i += kPer) {
                 const int p = __shfl_sync(0xffffffffu, pid, i + sub_row);
@@ -292,17 +363,27 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 const uint64_t at16 = (uint64_t)(uint32_t)max(p, 0) * page16 +
                                       (uint64_t)((uint32_t)(key0 + i + sub_row) & mask) * token16;
                 const unsigned char* src = real ? head_at + 16 * at16 : a.k_pages;
-                const uint32_t dst = kb + sw128_offset(tile_row + i, chunk & 7);
+                const uint32_t dst = F8 ? rb + (uint32_t)(i / kPer) * 1024u : kb + sw128_offset(tile_row + i, chunk & 7);
                 copy16(dst, src, real);
-                copy16(dst + C::kTile, src + v_after_k, real);
+                copy16(dst + (F8 ? 512 : C::kTile), src + v_after_k, real);
             }
-            // The slot is full once its loaders' copies so far have landed; nobody waits for that here, so the
-            // whole ring can be in flight.
-            copy_arrive(&bars->full[slot]);
-            slot += NS;
-            if (slot >= C::kSlots) {
-                slot -= C::kSlots;
-                ++round;
+            if constexpr (F8) {
+                cp_async_commit();
+                if (++raw_slot == C::kRawSlots) raw_slot = 0;
+                if (++ahead == C::kRawSlots) {  // the oldest has landed once the others alone are in flight
+                    cp_async_wait_group<C::kRawSlots - 1>();
+                    --ahead;
+                    if (!widen()) break;
+                }
+            } else {
+                // The slot is full once its loaders' copies so far have landed; nobody waits for that here, so
+                // the whole ring can be in flight.
+                copy_arrive(&bars->full[slot]);
+                slot += NS;
+                if (slot >= C::kSlots) {
+                    slot -= C::kSlots;
+                    ++round;
+                }
             }
             if (fresh && !kQueriesFirst && !queries()) break;
             fresh = w.kt + 1 == w.kts;
@@ -310,13 +391,15 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
             fetch_pages();
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (F8)
+            while (ahead > 0 && widen()) --ahead;
         if (err) bars->status = err;
     } else if (C::mma_of(warp) >= 0) {
         // ---------------------------------------------------------------- MMA issue
         // The whole warp runs this with equal values and one elected lane issues: descriptors then stay in
         // uniform registers (from one divergent lane each MMA cost 90 to 160 cycles to issue).
         constexpr uint32_t idesc_s = idesc16<BF16>(kTcRowTile, KT, false);
-        constexpr uint32_t idesc_o = idesc16<BF16>(kTcRowTile, DP, true);
+        constexpr uint32_t idesc_o = idesc16<VB>(kTcRowTile, DP, true);
         const uint32_t base = smem_addr(smem);
         // The upper halves of the descriptors hold layout and stride only (and the leading offset, V's, sits in
         // the lower half's upper bits; with one group of 64 values it is not used).
@@ -381,9 +464,9 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
         const int s = warp >> 2, row = tid & 127, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const uint32_t ts = tmem + lanes + C::kColS + s * KT;
-        const float c = a.scale * kLog2e;
-        const bool plain = a.softcap == 0.f && c > 0.f;
-        const float cap_in = a.softcap > 0.f ? 2.f * c / a.softcap : 0.f;
+        float c = a.scale * kLog2e;  // (times the head's key scale)
+        bool plain = a.softcap == 0.f && c > 0.f;
+        float cap_in = a.softcap > 0.f ? 2.f * c / a.softcap : 0.f;
         const float cap_out = a.softcap * kLog2e;
         uint32_t zero[16];
 #pragma unroll
@@ -422,6 +505,11 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 see_hi = row < rows ? attn_see_hi(a, w.r, token) : 0;
                 m = -CUDART_INF_F;
                 l = 0.f;
+                if (F8 && a.k_scale) {
+                    c = a.scale * kLog2e * __ldg(a.k_scale + head);
+                    plain = a.softcap == 0.f && c > 0.f;
+                    cap_in = a.softcap > 0.f ? 2.f * c / a.softcap : 0.f;
+                }
             }
             const int key0 = (w.kt_first + w.kt) * C::kUnit + s * KT;
             const bool edge = key0 < all_lo || key0 + KT > all_hi;  // some row does not see all of the tile
@@ -515,7 +603,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                         const float2 e = up2(fma2(pk2(__uint_as_float(x[h >> 5][i]), __uint_as_float(x[h >> 5][i + 1])), f2, r2));
                         const float p0 = ex2(e.x), p1 = ex2(e.y);
                         sum[(i >> 1) & 3] = add2(sum[(i >> 1) & 3], pk2(p0, p1));
-                        p[i / 2] = pack16<BF16>(p0, p1);
+                        p[i / 2] = pack16<VB>(p0, p1);
                     }
                     tmem_st16(tp + h / 2, p);
                 }
@@ -536,13 +624,13 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 uint32_t acc = 0;
                 for (int i = row; i < C::kTile / 16; i += 128) {
                     const uint4 y = reinterpret_cast<const uint4*>(v)[i];
-                    odd_note<false, BF16>(y.x, acc);
-                    odd_note<false, BF16>(y.y, acc);
-                    odd_note<false, BF16>(y.z, acc);
-                    odd_note<false, BF16>(y.w, acc);
+                    odd_note<false, VB>(y.x, acc);
+                    odd_note<false, VB>(y.y, acc);
+                    odd_note<false, VB>(y.z, acc);
+                    odd_note<false, VB>(y.w, acc);
                 }
                 int* odd = &bars->odd[s][n & 1];  // (cleared before the tile after next can set it)
-                if (odd_found<false, BF16>(acc)) *odd = 1;
+                if (odd_found<false, VB>(acc)) *odd = 1;
                 if (!stream_meet()) break;
                 const bool found = *reinterpret_cast<volatile int*>(odd) != 0;
                 if (found) {
@@ -551,16 +639,16 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                     for (int k = 0; k < KT; ++k) {
                         uint32_t pk = 0;
                         if (live) tmem_ld1(tp + (k >> 1), pk);
-                        const float pv = from16<BF16>((k & 1) ? pk >> 16 : pk);
+                        const float pv = from16<VB>((k & 1) ? pk >> 16 : pk);
                         const bool see = key0 + k >= see_lo && key0 + k < see_hi;
 #pragma unroll 1
                         for (int d = 0; d < DP; ++d) {
                             const uint32_t bits = *reinterpret_cast<const uint16_t*>(
                                 v + (d >> 6) * (KT * 128) + sw128_offset(k, (d & 63) >> 3) + 2 * (d & 7));
-                            if (live && is_odd16<BF16>(bits)) {
+                            if (live && is_odd16<VB>(bits)) {
                                 uint32_t o;
                                 tmem_ld1(tmem + lanes + s * DP + d, o);
-                                if (see) o = __float_as_uint(fmaf(pv, from16<BF16>(bits), __uint_as_float(o)));
+                                if (see) o = __float_as_uint(fmaf(pv, from16<VB>(bits), __uint_as_float(o)));
                                 tmem_st1(tmem + lanes + s * DP + d, o);
                                 tmem_wait_st();
                             }
@@ -569,7 +657,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                     if (!stream_meet()) break;
                     for (int i = row; i < C::kTile / 2; i += 128) {
                         uint16_t* y = reinterpret_cast<uint16_t*>(v) + i;
-                        if (is_odd16<BF16>(*y)) *y = 0;
+                        if (is_odd16<VB>(*y)) *y = 0;
                     }
                     if (row == 0) *odd = 0;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -601,7 +689,7 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
                 }
                 const bool whole = last_of_item && seg_first == 0;
                 const size_t slot = 2 * (size_t)part + (seg_first == 0 ? kHead : kTail);
-                const float inv = !whole ? 1.f : (ll == 0.f ? 0.f : 1.f / ll);
+                const float inv = !whole ? 1.f : (ll == 0.f ? 0.f : (F8 && a.v_scale ? __ldg(a.v_scale + head) : 1.f) / ll);
                 const long long at = attn_out_row(a, w.r.token0, head, row0 + row);
                 unsigned char* dst = a.out + (size_t)at * a.D * 2;
                 float* part_dst = a.part_o + (slot * kTcRowTile + row) * a.D;
@@ -662,11 +750,11 @@ __global__ void __launch_bounds__(TcAttn<DP>::kThreads, 1) attn_tc_kernel(AttnAr
     if (tid == 0) mine->err = bars->status ? bars->status : (bad ? DSPARK_ERR_CACHE : 0);
 }
 
-template <bool BF16, int DP>
+template <bool BF16, bool F8, int DP>
 dspark_status launch_tc(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
-    using C = TcAttn<DP>;
+    using C = TcAttn<F8, DP>;
     int per_sm = 0;
-    auto fn = attn_tc_kernel<BF16, DP>;
+    auto fn = attn_tc_kernel<BF16, F8, DP>;
     if (prepare_kernel((const void*)fn, C::kSmem, C::kThreads, &per_sm) != cudaSuccess || per_sm < 1)
         return DSPARK_ERR_CUDA;
     const int n = sms < kMaxTcParts ? sms : kMaxTcParts;
@@ -674,12 +762,18 @@ dspark_status launch_tc(const AttnArgs& a, int sms, cudaStream_t s, int* parts) 
     return launch_overlapped(fn, n, C::kThreads, C::kSmem, s, a, wait_limit_ns()) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
+template <bool BF16, bool F8>
+dspark_status launch_tc_d(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
+    if (a.D <= 64) return launch_tc<BF16, F8, 64>(a, sms, s, parts);
+    if (a.D <= 128) return launch_tc<BF16, F8, 128>(a, sms, s, parts);
+    return launch_tc<BF16, F8, 256>(a, sms, s, parts);
+}
+
 }  // namespace
 
-dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int sms, cudaStream_t s, int* parts) {
-    if (a.D <= 64) return bf16 ? launch_tc<true, 64>(a, sms, s, parts) : launch_tc<false, 64>(a, sms, s, parts);
-    if (a.D <= 128) return bf16 ? launch_tc<true, 128>(a, sms, s, parts) : launch_tc<false, 128>(a, sms, s, parts);
-    return bf16 ? launch_tc<true, 256>(a, sms, s, parts) : launch_tc<false, 256>(a, sms, s, parts);
+dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, bool e4m3, int sms, cudaStream_t s, int* parts) {
+    if (e4m3) return bf16 ? launch_tc_d<true, true>(a, sms, s, parts) : launch_tc_d<false, true>(a, sms, s, parts);
+    return bf16 ? launch_tc_d<true, false>(a, sms, s, parts) : launch_tc_d<false, false>(a, sms, s, parts);
 }
 
 }  // namespace dspark

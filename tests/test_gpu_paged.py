@@ -238,7 +238,7 @@ TYPES = [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float16), (torc
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
 @pytest.mark.parametrize("Hq,Hk,D,page", [(4, 4, 64, 16), (8, 1, 128, 16), (8, 2, 256, 32), (5, 1, 80, 1), (14, 2, 96, 64),
-                                          (32, 2, 192, 8), (3, 3, 16, 128)])
+                                          (32, 2, 192, 8), (3, 3, 16, 128), (64, 1, 64, 16), (104, 2, 128, 64)])
 def test_one_token(dtype, cache, Hq, Hk, D, page):
     lens = [1, 15, 16, 17, 0, 63, 64, 65, 300]
     c, lens, offsets = make_case(lens, [1] * len(lens), Hq, Hk, D, page, dtype, cache, D + page)
@@ -248,7 +248,7 @@ def test_one_token(dtype, cache, Hq, Hk, D, page):
 
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
-@pytest.mark.parametrize("Hq,Hk,D,page", [(4, 4, 64, 16), (8, 2, 128, 16), (16, 2, 128, 64), (8, 1, 256, 32), (7, 1, 96, 4)])
+@pytest.mark.parametrize("Hq,Hk,D,page", [(4, 4, 64, 16), (8, 2, 128, 16), (16, 2, 128, 64), (8, 1, 256, 32), (7, 1, 96, 4), (14, 2, 80, 16)])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("max_new", [1, 33])  # what chooses between row tiles of 16 and of 128
 def test_several_tokens(dtype, cache, Hq, Hk, D, page, causal, max_new):
@@ -263,23 +263,24 @@ def test_several_tokens(dtype, cache, Hq, Hk, D, page, causal, max_new):
 @pytest.mark.parametrize("softcap", [0.0, 5.0])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("cache", [torch.bfloat16, E4M3])
-@pytest.mark.parametrize("max_new", [1, 17])
-def test_window_and_softcap(window, softcap, causal, cache, max_new):
+@pytest.mark.parametrize("Hq,max_new", [(8, 1), (8, 17), (32, 17)])
+def test_window_and_softcap(window, softcap, causal, cache, Hq, max_new):
     news, lens = [1, 9, 4, 17], [500, 9, 130, 201]
-    c, lens, offsets = make_case(lens, news, 8, 2, 128, 16, torch.bfloat16, cache, window)
+    c, lens, offsets = make_case(lens, news, Hq, 2, 128, 16, torch.bfloat16, cache, window)
     check(c, lens, offsets, causal=causal, window=window, softcap=softcap, max_new=max_new)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
 @pytest.mark.parametrize("max_new", [1, 17])
 def test_other_scales(scale, max_new):
-    c, lens, offsets = make_case([200, 9], [3, 2], 4, 1, 64, 16, torch.float16, torch.float16, 1)
+    c, lens, offsets = make_case([200, 9], [3, 2], 16, 1, 64, 16, torch.float16, torch.float16, 1)
     check(c, lens, offsets, scale=scale, max_new=max_new)
 
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
 @pytest.mark.parametrize("lens,news,Hq,Hk,D", [([20000], [1], 8, 1, 128), ([9000, 1, 5000], [1, 1, 4], 4, 1, 256),
-                                               ([33, 12000, 700], [2, 17, 3], 8, 2, 64), ([15000, 2000], [9, 1], 16, 1, 128)])
+                                               ([33, 12000, 700], [2, 17, 3], 8, 2, 64), ([15000, 2000], [9, 1], 16, 1, 128),
+                                               ([9000, 500], [16, 1], 64, 8, 64), ([11000], [13], 9, 1, 256)])
 @pytest.mark.parametrize("max_new", [1, 17])
 def test_long_caches_are_split_and_joined(dtype, cache, lens, news, Hq, Hk, D, max_new):
     c, lens, offsets = make_case(lens, news, Hq, Hk, D, 64, dtype, cache, sum(lens))
@@ -293,12 +294,12 @@ def test_many_requests(max_new):
     g = torch.Generator().manual_seed(3)
     news = torch.randint(0, 4, (900,), generator=g).tolist()
     lens = [n + int(x) for n, x in zip(news, torch.randint(0, 60, (900,), generator=g))]
-    c, lens, offsets = make_case(lens, news, 2, 1, 64, 16, torch.bfloat16, torch.bfloat16, 8)
+    c, lens, offsets = make_case(lens, news, 16, 1, 64, 16, torch.bfloat16, torch.bfloat16, 8)
     check(c, lens, offsets, max_new=max_new)
 
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
-@pytest.mark.parametrize("Hq,Hk", [(4, 1), (8, 2), (16, 1)])
+@pytest.mark.parametrize("Hq,Hk", [(4, 1), (8, 2), (16, 1), (32, 1)])
 @pytest.mark.parametrize("max_new", [1, 17])
 def test_what_is_not_seen_does_not_matter(dtype, cache, Hq, Hk, max_new):
     """NaN and inf in later tokens, before the window, past a request's length and in pages of nobody."""
@@ -345,7 +346,7 @@ def test_what_is_not_seen_does_not_matter(dtype, cache, Hq, Hk, max_new):
 @pytest.mark.parametrize("max_new", [1, 17])
 def test_values_that_are_seen_go_through(max_new):
     """A NaN or an infinite value that a row sees reaches it, and only it."""
-    c, lens, offsets = make_case([50, 60], [3, 2], 2, 1, 64, 16, torch.bfloat16, torch.bfloat16, 4)
+    c, lens, offsets = make_case([50, 60], [3, 2], 16, 1, 64, 16, torch.bfloat16, torch.bfloat16, 4)
     ref, _, _ = attend(c, max_new=max_new)
     c["v_pages"][c["block_table"][0, 2].long(), 15, 0, 5] = float("nan")  # request 0, position 47: its first new token
     c["v_pages"][c["block_table"][1, 3].long(), 11, 0, 6] = float("inf")  # request 1, position 59: its last
@@ -359,7 +360,7 @@ def test_values_that_are_seen_go_through(max_new):
 @pytest.mark.parametrize("max_new", [1, 17])
 def test_rows_that_see_nothing(max_new):
     """More new tokens than the cache holds: the first rows stand before position 0."""
-    c, lens, offsets = make_case([4, 1, 0], [4, 3, 2], 4, 2, 64, 16, torch.float16, torch.float16, 2)
+    c, lens, offsets = make_case([4, 1, 0], [4, 3, 2], 16, 2, 64, 16, torch.float16, torch.float16, 2)
     for window in (0, 3):
         out, lse, ws = attend(c, window=window, max_new=max_new)
         assert not out[4:6].any() and bool((lse[4:6] == -math.inf).all()) and not out[7:].any()
@@ -367,12 +368,12 @@ def test_rows_that_see_nothing(max_new):
         check(c, lens, offsets, window=window, max_new=max_new)
 
 
-@pytest.mark.parametrize("q_shift", [1, 2, 8])
+@pytest.mark.parametrize("q_shift", [0, 1, 2, 8])
 @pytest.mark.parametrize("heads_first", [False, True])
 @pytest.mark.parametrize("cache", [torch.bfloat16, E4M3])
 @pytest.mark.parametrize("max_new", [1, 17])
 def test_strides_and_alignment(q_shift, heads_first, cache, max_new):
-    c, lens, offsets = make_case([33, 100, 7], [2, 9, 1], 6, 2, 128, 16, torch.bfloat16, cache, 6, heads_first=heads_first,
+    c, lens, offsets = make_case([33, 100, 7], [2, 9, 1], 32, 2, 128, 16, torch.bfloat16, cache, 6, heads_first=heads_first,
                                  q_shift=q_shift)
     check(c, lens, offsets, max_new=max_new)
 
@@ -389,7 +390,7 @@ def test_pools_past_4_gib(cache, max_new):
     slots = torch.tensor([use[i // page] * page + i % page for i in range(200)], device="cuda")
     k, v = (torch.randn((200, Hk, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
     api.cache_append(k, v, kp, vp, slots)
-    q = torch.randn((T, 16, D), generator=g, device="cuda").to(torch.bfloat16)
+    q = torch.randn((T, 64, D), generator=g, device="cuda").to(torch.bfloat16)
     c = {"q": q, "k_pages": kp, "v_pages": vp, "block_table": i32([use]), "seq_len": i32([200]), "offsets": i32([0, T]),
          "k_scale": None, "v_scale": None}
     check(c, [200], [0, T], max_new=max_new)
@@ -399,7 +400,7 @@ def test_pools_past_4_gib(cache, max_new):
 def test_large_scores_and_queries(max_new):
     """Scores far apart, and bf16 queries beyond the halves' range over an 8-bit cache."""
     for cache in (torch.bfloat16, E4M3):
-        c, lens, offsets = make_case([300, 40], [2, 3], 4, 1, 128, 16, torch.bfloat16, cache, 11)
+        c, lens, offsets = make_case([300, 40], [2, 3], 32, 1, 128, 16, torch.bfloat16, cache, 11)
         c["q"].mul_(20.0)
         check(c, lens, offsets, max_new=max_new)
         c["q"].mul_(2.0 ** 60)
@@ -412,7 +413,7 @@ def test_large_scores_and_queries(max_new):
 def test_pages_before_the_window_may_be_gone(max_new):
     """A sliding window's caller gives old pages back: their table entries are not looked at."""
     for cache in (torch.bfloat16, E4M3):
-        c, lens, offsets = make_case([400, 130], [3, 2], 4, 2, 128, 16, torch.bfloat16, cache, 5)
+        c, lens, offsets = make_case([400, 130], [3, 2], 64, 2, 128, 16, torch.bfloat16, cache, 5)
         ref, _, ws = attend(c, window=70, max_new=max_new)
         c["block_table"][0, : (400 - 3 - 70 + 1) // 16] = -1
         c["block_table"][1, : (130 - 2 - 70 + 1) // 16] = 1 << 30
@@ -434,7 +435,7 @@ def test_no_tokens_at_all(max_new):
 
 @pytest.mark.parametrize("max_new", [1, 17])
 def test_bad_tables_are_reported(max_new):
-    c, lens, offsets = make_case([40, 50], [1, 1], 4, 1, 64, 16, torch.bfloat16, torch.bfloat16, 9)
+    c, lens, offsets = make_case([40, 50], [1, 1], 32 if max_new > 1 else 4, 1, 64, 16, torch.bfloat16, torch.bfloat16, 9)
     ref, _, _ = attend(c, max_new=max_new)
     for what in ("page", "negative", "long", "offsets"):
         d = {**c, "block_table": c["block_table"].clone(), "seq_len": c["seq_len"].clone(), "offsets": c["offsets"].clone()}
@@ -456,7 +457,8 @@ def test_bad_tables_are_reported(max_new):
 @pytest.mark.parametrize("max_new", [1, 5])
 def test_other_stream_and_graph(max_new):
     """On a side stream, and replayed from a graph after the lengths changed."""
-    c, lens, offsets = make_case([700, 200, 64], [1, 5, 2], 8, 2, 128, 16, torch.bfloat16, torch.bfloat16, 12)
+    Hq = 32
+    c, lens, offsets = make_case([700, 200, 64], [1, 5, 2], Hq, 2, 128, 16, torch.bfloat16, torch.bfloat16, 12)
     ref, ref_lse, _ = attend(c, max_new=max_new)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -469,7 +471,7 @@ def test_other_stream_and_graph(max_new):
     assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
     out = torch.zeros_like(ref)
     ws = torch.empty(api.b.dspark_paged_attention_workspace_size(api.b.AttentionParams(
-        8, 3, 8, 2, 128, 16, 100, 50, max_new, api.b.BF16, api.b.BF16, 1, 0, 1.0, 0.0, 1, 1, 8, 8, 8)), dtype=torch.uint8, device="cuda")
+        8, 3, Hq, 2, 128, 16, 100, 50, max_new, api.b.BF16, api.b.BF16, 1, 0, 1.0, 0.0, 1, 1, 8, 8, 8)), dtype=torch.uint8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         attend(c, out=out, ws=ws, max_new=max_new)
