@@ -357,6 +357,26 @@ def test_values_that_are_seen_go_through(max_new):
     assert bool(((out - ref).abs() <= 8 * 2.0 ** -8 * 4).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("max_new", [1, 8])
+def test_every_8_bit_value(dtype, max_new):
+    """Eight equal keys and values: an output is the value itself, and a one-hot query's lse is its key plus ln 8."""
+    codes = torch.arange(256, dtype=torch.uint8).view(2, 1, 1, 128).expand(2, 8, 1, 128).clone()  # a page a request
+    keys = codes.clone()
+    keys[(codes & 0x7F) == 0x7F] = 0  # (a NaN key is a NaN score for every query)
+    pool = lambda x: torch.cat([x, torch.zeros_like(x)]).view(E4M3).cuda()
+    q = torch.eye(128).view(1, 8, 16, 128).expand(2, 8, 16, 128).reshape(16, 16, 128).to("cuda", dtype)
+    c = {"q": q, "k_pages": pool(keys), "v_pages": pool(codes), "block_table": i32([[0], [1]]), "seq_len": i32([8, 8]),
+         "offsets": i32([0, 8, 16]), "k_scale": None, "v_scale": None}
+    out, lse, ws = attend(c, causal=False, scale=1.0, max_new=max_new)
+    assert status(ws) == 0
+    v = codes[:, 0, 0].view(E4M3).float().cuda()
+    assert torch.equal(out.float().nan_to_num(nan=1e9), v.view(2, 1, 1, 128).expand(2, 8, 16, 128).reshape(16, 16, 128).nan_to_num(nan=1e9))
+    k = keys[:, 0, 0].view(E4M3).double().cuda().view(16, 16)
+    # products with the two logarithms' constants, the sum and the logarithm of 8: a few roundings of fp32
+    assert bool(((lse.double() - k - math.log(8)).abs() <= 2.0 ** -21 * (k.abs() + 3)).all())
+
+
 @pytest.mark.parametrize("max_new", [1, 17])
 def test_rows_that_see_nothing(max_new):
     """More new tokens than the cache holds: the first rows stand before position 0."""
