@@ -13,7 +13,7 @@
 // statistics and outputs meet once per segment, in the stages just consumed (a stage is as large as a warp's
 // output: 64 D bytes).  Two blocks a multiprocessor or more, so that one streams while another joins.
 // Measured: 32 requests of up to 8192 tokens, 8 kv heads of 128, bf16: 94 us = 6.0 TB/s (0.89 of the measured copy
-// rate), of which 5 us are the join; 128 requests over an e4m3 cache 204 us = 5.5 TB/s (0.81), where the
+// rate), of which 5 us are the join; 128 requests over an e4m3 cache 209 us = 5.4 TB/s (0.79), where the
 // conversions keep the issue slots busy; one request of 1024 tokens 12 us, latency.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
