@@ -169,6 +169,14 @@ def _stream(stream):
     return int(stream)
 
 
+def torch_stream(stream):
+    """A stream given as torch's object or as its address, as torch's object."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    # (torch makes a new stream of the address 0)
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+
+
 def dtype_code(dt: torch.dtype) -> int:
     if dt == torch.float32:
         return F32

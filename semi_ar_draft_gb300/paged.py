@@ -9,13 +9,21 @@ stack, and per layer a pool of keys and one of values.  A round is
     commit(add_len, extra)    how many of them stay; pages past them go back
 
 and nothing in it reads the device from the host.  plan and commit write their results to other tensors than
-they read, so the lengths and counts have two buffers each, used in turn."""
+they read; a copy of a few bytes a request then brings them back, so that every call reads the same addresses and any
+sequence of calls can be captured into a graph and replayed."""
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
 from . import api
 from . import binding as b
+
+
+def _on(stream):
+    """torch's current stream made the given one; None leaves it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(b.torch_stream(stream))
 
 
 class PagedCache:
@@ -37,9 +45,11 @@ class PagedCache:
         self.page_size, self.max_tokens = page_size, max_tokens
         self.block_table = torch.full((requests, max_blocks), -1, **i32)
         self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)
-        self._len = [torch.zeros(requests, **i32) for _ in range(2)]
-        self._blocks = [torch.zeros(requests, **i32) for _ in range(2)]
-        self._free = [torch.full((1,), num_pages, **i32) for _ in range(2)]
+        # lengths, blocks held, pages free: what every call reads, and where plan and commit write them
+        self._counts = [torch.zeros(2 * requests + 1, **i32) for _ in range(2)]
+        self._len, self._blocks, self._free = ([x[a:b] for x in self._counts] for a, b in
+                                               ((0, requests), (requests, 2 * requests), (2 * requests, 2 * requests + 1)))
+        self._free[0].fill_(num_pages)
         self.seq_len, self.offsets = torch.empty(requests, **i32), torch.empty(requests + 1, **i32)
         self.slots = torch.empty(max_tokens, dtype=torch.int64, device=device)
         self.positions = torch.empty(max_tokens, **i32)
@@ -48,7 +58,7 @@ class PagedCache:
 
     @property
     def cache_len(self):
-        """Tokens of each request in the cache [requests] (what plan last read or commit last wrote)."""
+        """Tokens of each request in the cache [requests] (the tensor stays; commit changes what it holds)."""
         return self._len[0]
 
     @property
@@ -61,8 +71,7 @@ class PagedCache:
         api.cache_plan(self._len[0], new_len, self.block_table, self._blocks[0], self.free_pages, self._free[0],
                        self.page_size, self.max_tokens, extra=extra, ws=self.ws, stream=stream,
                        out=(self.seq_len, self.offsets, self.slots, self.positions, self._blocks[1], self._free[1]))
-        self._blocks.reverse()
-        self._free.reverse()
+        self._keep(len(self._len[0]), stream)
         self.max_new = max_new
 
     def append(self, layer, k, v, stream=None):
@@ -82,8 +91,12 @@ class PagedCache:
         api.cache_commit(self._len[0], add_len, self.block_table, self._blocks[0], self.free_pages, self._free[0],
                          self.page_size, extra=extra, done=done, ws=self.ws, stream=stream,
                          out=(self._len[1], self._blocks[1], self._free[1]))
-        for pair in (self._len, self._blocks, self._free):
-            pair.reverse()
+        self._keep(0, stream)
+
+    def _keep(self, first, stream):
+        """The counts just written (from `first` on) to where the next call reads them."""
+        with _on(stream):
+            self._counts[0][first:].copy_(self._counts[1][first:])
 
     def status(self, stream=None):
         """Device status of the last plan or commit (synchronises)."""

@@ -1,0 +1,94 @@
+"""PagedCache: rounds replayed from a graph, errors kept until they are read, memory at construction, steps of other
+token counts."""
+import pytest
+import torch
+
+from semi_ar_draft_gb300 import api
+from semi_ar_draft_gb300.paged import PagedCache
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Round:
+    """A round's inputs in tensors that stay where they are, and the round itself."""
+
+    def __init__(self, B, T, Hq=4, Hk=1, D=64):
+        self.new, self.acc, self.done = i32([0] * B), i32([0] * B), torch.zeros(B, dtype=torch.uint8, device="cuda")
+        self.q, self.k, self.v = (torch.zeros((T, h, D), dtype=torch.bfloat16, device="cuda") for h in (Hq, Hk, Hk))
+
+    def fill(self, seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.new.random_(0, 8, generator=g)
+        self.acc.copy_((torch.rand(len(self.new), generator=g, device="cuda") * (self.new + 1)).int())
+        self.done.copy_(torch.rand(len(self.new), generator=g, device="cuda") < 0.2)
+        for x in (self.q, self.k, self.v):
+            x.normal_(generator=g)
+
+    def run(self, cache, stream=None):
+        cache.plan(self.new, extra=1, max_new=8, stream=stream)
+        cache.append(0, self.k, self.v, stream=stream)
+        out, _ = cache.attend(0, self.q, stream=stream)
+        cache.commit(self.acc, extra=1, done=self.done, stream=stream)
+        return out
+
+
+@pytest.mark.parametrize("calls", [1, 2])
+def test_rounds_replay_from_a_graph(calls):
+    """A graph of one round (or of two), replayed: every replay goes on from where the last one stopped."""
+    B, T = 6, 48
+    eager, replayed = (PagedCache(B, 80, 8, 40, 1, 1, 64, T) for _ in range(2))
+    inputs = [Round(B, T) for _ in range(calls)]
+    inputs[0].run(PagedCache(B, 80, 8, 40, 1, 1, 64, T))  # the kernels' first launches, beside both caches
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [r.run(replayed) for r in inputs]
+    for n in range(4):
+        for i, r in enumerate(inputs):
+            r.fill(10 * n + i)
+        want = [r.run(eager) for r in inputs]
+        graph.replay()
+        torch.cuda.synchronize()
+        for out, ref in zip(outs, want):
+            assert torch.equal(out, ref), n
+        assert replayed.cache_len.tolist() == eager.cache_len.tolist(), n
+        assert int(replayed.n_free) == int(eager.n_free) and torch.equal(replayed.offsets, eager.offsets)
+    assert eager.status() == 0 and replayed.status() == 0 and int(eager.cache_len.max()) > 8
+
+
+def test_finished_requests_replay_from_a_graph():
+    """A graph of a commit alone."""
+    cache = PagedCache(3, 12, 4, 4, 1, 1, 64, 24)
+    done = torch.ones(3, dtype=torch.uint8, device="cuda")
+    new = i32([5, 1, 8])
+    cache.plan(new)
+    cache.commit(new)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        cache.commit(done=done)
+    for _ in range(3):
+        graph.replay()
+        assert int(cache.n_free) == 12 and cache.cache_len.tolist() == [0, 0, 0]
+        cache.plan(new)
+        cache.commit(new)
+        assert int(cache.n_free) == 12 - 5 and cache.cache_len.tolist() == [5, 1, 8]
+
+
+def test_counts_are_read_through_the_same_tensors():
+    """cache_len and n_free taken once show the counts after every later call, also on a stream of its own."""
+    cache = PagedCache(2, 9, 4, 4, 1, 1, 64, 16)
+    lengths, free = cache.cache_len, cache.n_free
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, side, side.cuda_stream, 0):
+        cache.plan(i32([3, 1]), stream=stream)
+        cache.commit(i32([3, 1]), stream=stream)
+        torch.cuda.synchronize()
+    assert lengths.tolist() == [12, 4] and int(free) == 9 - 4 and cache.status() == 0
