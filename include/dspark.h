@@ -407,10 +407,13 @@ dspark_status dspark_cache_plan(const dspark_cache_params* p, const int32_t* cac
  *   cache_len_out[j] = len_j;  n_blocks_out[j] = ceil(len_j / page_size)
  *   the pages at blocks n_blocks_out[j] .. n_blocks[j] - 1 go onto the stack, requests in order and blocks
  *   in order: free_pages[n_free], free_pages[n_free + 1], ...;  n_free_out = n_free + their number
+ *   A negative entry names no page and is left out: a caller that gives a page back itself (one wholly before a
+ *   sliding window) puts the page on the stack and -1 in the table.
  * block_table and n_blocks are dspark_cache_plan's; the table is not written.  cache_len_out,
  * n_blocks_out and n_free_out must not overlap the inputs.
  * Device status DSPARK_ERR_CACHE: a length that is negative or longer than the request's pages, n_blocks or
- * n_free out of range (each is clamped), more pages than the stack has room for (the rest is dropped).
+ * n_free out of range (each is clamped), an entry past the pool (left out), more pages than the stack has room for
+ * (the rest is dropped).
  */
 dspark_status dspark_cache_commit(const dspark_cache_params* p, const int32_t* cache_len, const int32_t* add_len,
                                   const uint8_t* done, const int32_t* block_table, const int32_t* n_blocks,

@@ -1,0 +1,83 @@
+"""Pages on their way through plan and commit where some are missing: given back early, not to be had, or not of the pool."""
+import pytest
+import torch
+
+from semi_ar_draft_gb300 import api, binding
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def commit_reference(cache_len, add, table, n_blocks, free, n_free, page, extra, done, num_pages):
+    """(cache_len, n_blocks, n_free, free, bad): entries that are no page do not go back, those past the pool are an error."""
+    free, top, bad, length, held = list(free), n_free, False, [], []
+    for j in range(len(cache_len)):
+        n = 0 if done[j] else cache_len[j] + add[j] + extra
+        bad |= n < 0 or n > n_blocks[j] * page
+        n = min(max(n, 0), n_blocks[j] * page)
+        keep = -(-n // page)
+        for p in table[j][keep:n_blocks[j]]:
+            if p < 0:
+                continue
+            if p >= num_pages or top == num_pages:
+                bad = True
+                continue
+            free[top] = p
+            top += 1
+        length.append(n)
+        held.append(keep)
+    return length, held, top, free, bad
+
+
+@pytest.mark.parametrize("B,most,window,beyond", [(1, 9, 3, 0), (3, 40, 5, 0), (64, 30, 7, 0), (65, 33, 1, 0), (200, 70, 30, 0),
+                                                  (700, 20, 8, 0), (3000, 9, 2, 0), (2, 3000, 700, 0), (90, 40, 5, 4)])
+def test_commit_of_requests_whose_first_pages_are_gone(B, most, window, beyond):
+    """Sliding windows: a request keeps `window` pages, its first entries are -1 (or, `beyond`, past the pool)."""
+    page = 16
+    g = torch.Generator().manual_seed(B + most)
+    n_blocks = torch.randint(0, most + 1, (B,), generator=g).tolist()
+    live = [min(n, window) for n in n_blocks]
+    P = sum(live) + 5
+    perm = torch.randperm(P, generator=g).tolist()
+    table, used = [], 0
+    for n, k in zip(n_blocks, live):
+        gone = [-1 - (i % 3) for i in range(n - k)]
+        if beyond and len(gone) > beyond:
+            gone[beyond] = P + 7
+        table.append(gone + perm[used:used + k] + [-9] * (most - n))
+        used += k
+    free, n_free = perm[used:] + [-5] * used, P - used
+    cache_len = [max(n * page - 3, 0) for n in n_blocks]
+    add = [0] * B
+    done = [int(x) for x in torch.rand(B, generator=g) < 0.4]
+    f = i32(free)
+    length, held, left, ws = api.cache_commit(i32(cache_len), i32(add), i32(table), i32(n_blocks), f, i32([n_free]), page,
+                                              done=torch.tensor(done, dtype=torch.uint8, device="cuda"))
+    ref = commit_reference(cache_len, add, table, n_blocks, free, n_free, page, 0, done, P)
+    got = (length.tolist(), held.tolist(), left.item(), f.tolist(), binding.dspark_get_device_status(ws) == 8)
+    assert got == ref
+    on_stack = got[3][: got[2]]
+    assert len(set(on_stack)) == len(on_stack) and min(on_stack) >= 0 and max(on_stack) < P
+
+
+def test_pages_of_windowed_requests_are_given_out_once():
+    """Pages before a window go back by the caller's hand, the rest by commit, and all are handed out again."""
+    page, P, width = 4, 12, 8
+    table = i32([[0, 1, 2, 3, 4, -1, -1, -1], [5, 6, 7, -1, -1, -1, -1, -1]])
+    free, n_free, n_blocks, cache_len = i32([11, 10, 9, 8] + [-1] * 8), i32([4]), i32([5, 3]), i32([18, 11])
+    # request 0 keeps a window of two pages
+    free[4:7], n_free = table[0, :3], i32([7])
+    table[0, :3] = -1
+    cache_len, n_blocks, n_free, ws = api.cache_commit(cache_len, None, table, n_blocks, free, n_free, page,
+                                                       done=torch.tensor([1, 0], dtype=torch.uint8, device="cuda"))
+    assert binding.dspark_get_device_status(ws) == 0 and int(n_free) == 9
+    assert sorted(free[:9].tolist()) == [0, 1, 2, 3, 4, 8, 9, 10, 11]
+    seq, off, slots, pos, n_blocks, n_free, ws = api.cache_plan(cache_len, i32([32, 5]), table, n_blocks, free, n_free, page, 40)
+    assert binding.dspark_get_device_status(ws) == 0 and int(n_free) == 0
+    held = table[0, :8].tolist() + table[1, :4].tolist()
+    assert sorted(held) == list(range(P))
+    live = slots[: int(off[-1])]
+    assert int(live.min()) >= 0 and live.unique().numel() == live.numel()
