@@ -379,7 +379,8 @@ dspark_status dspark_markov_sample_block_noalloc(const dspark_sample_params* p, 
  * free_pages is not written.  The same inputs give the same outputs bit for bit.
  * Device status DSPARK_ERR_CACHE: a negative length, n_blocks outside [0, max_blocks], n_free outside
  * [0, num_pages] (each is clamped), more pages needed than the stack or a table row holds (pages are given
- * in order while they last), more than max_tokens tokens.  A token whose page is missing or outside the
+ * in order while they last, and the table's entries of the blocks left without one become -1, so that attention
+ * over such a step reports it), more than max_tokens tokens.  A token whose page is missing or outside the
  * pool gets slot -1, which dspark_cache_append skips.
  * Host errors: DSPARK_ERR_UNSUPPORTED for B > 8192.
  * dspark_cache_workspace_size serves dspark_cache_plan and dspark_cache_commit.

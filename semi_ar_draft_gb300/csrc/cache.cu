@@ -165,6 +165,14 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(PlanArgs a) {
         const int have = min(max(a.n_blocks[j], 0), a.max_blocks);
         a.block_table[(size_t)j * a.max_blocks + have + (k - page0[j])] = a.free_pages[n_free - 1 - k];
     }
+    // Blocks for which the stack had no page: their entries must not go on naming pages of earlier rounds, which
+    // are other requests' by now.
+    if (P > given)
+        for (int j = blockIdx.x * kPlanWarps + (tid >> 5); j < a.B; j += gridDim.x * kPlanWarps) {
+            const PlanReq r = plan_request(a, j);
+            for (int b = page0[j + 1] - page0[j] + (tid & 31); b < r.need; b += 32)
+                a.block_table[(size_t)j * a.max_blocks + r.have + b] = -1;
+        }
     const int live = off[a.B];
     for (long long t = blockIdx.x * kPlanThreads + tid; t < a.max_tokens; t += stride) {
         long long slot = -1;

@@ -81,3 +81,37 @@ def test_pages_of_windowed_requests_are_given_out_once():
     assert sorted(held) == list(range(P))
     live = slots[: int(off[-1])]
     assert int(live.min()) >= 0 and live.unique().numel() == live.numel()
+
+
+@pytest.mark.parametrize("B,short", [(3, 4), (70, 30), (400, 333)])
+def test_blocks_without_a_page_name_none(B, short):
+    """Where the stack runs out, the table does not go on naming pages that were given back: their keys are others' now."""
+    page, width = 4, 9
+    g = torch.Generator().manual_seed(B)
+    cache_len = torch.randint(0, 13, (B,), generator=g).tolist()
+    new = torch.randint(0, 20, (B,), generator=g).tolist()
+    n_blocks = [-(-x // page) for x in cache_len]
+    need = [-(-(x + n) // page) - h for x, n, h in zip(cache_len, new, n_blocks)]
+    short = min(short, sum(need))
+    assert short > 0
+    held, P = sum(n_blocks), sum(n_blocks) + sum(need) - short
+    perm = torch.randperm(P, generator=g).tolist()
+    table, used = [], 0
+    for h in n_blocks:
+        table.append(perm[used:used + h] + [perm[i % P] for i in range(width - h)])  # what earlier rounds left behind
+        used += h
+    free = perm[used:] + [-1] * used
+    t = i32(table)
+    seq, off, slots, pos, blocks, left, ws = api.cache_plan(i32(cache_len), i32(new), t, i32(n_blocks), i32(free), i32([P - held]),
+                                                            page, sum(new) + 3)
+    assert binding.dspark_get_device_status(ws) == 8 and left.item() == 0
+    stack, want = free[: P - held][::-1], [list(r) for r in table]
+    for j in range(B):
+        for b in range(n_blocks[j], n_blocks[j] + need[j]):
+            want[j][b] = stack.pop(0) if stack else -1
+    assert t.tolist() == want
+    # attention over such a step says so
+    q = torch.zeros((sum(new), 1, 64), dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros((P, page, 1, 64), dtype=torch.bfloat16, device="cuda")
+    _, _, ws = api.paged_attention(q, pool, pool, t, seq, off)
+    assert binding.dspark_get_device_status(ws) == 8
