@@ -28,9 +28,13 @@ class ToyTarget:
         self.proj = [rnd(Hq * D, d, std=0.5 * (Hq * D) ** -0.5) for _ in range(layers)]
         self.head = rnd(d, V, std=3.0 * d ** -0.5)
 
+    def places(self, positions):
+        """The positions' embeddings; -1 (padding) and what lies past the table read its first and last row."""
+        return self.place[positions.long().clamp(0, len(self.place) - 1)]
+
     def forward(self, tokens, positions, cache):
         """Logits [T, V] fp32 of the planned tokens, whose keys and values go into the cache."""
-        x = self.embed[tokens] + self.place[positions]
+        x = self.embed[tokens] + self.places(positions)
         for layer, (w, p) in enumerate(zip(self.qkv, self.proj)):
             h = torch.nn.functional.rms_norm(x, (x.shape[-1],))
             qkv = (h @ w).view(len(tokens), self.Hq + 2 * self.Hk, self.D)
@@ -57,9 +61,13 @@ class ToyDraft:
 
 def generate(target, draft, prompts, rounds, T=0.0, budget=None, page_size=16, kv_dtype=None, seed=0, max_len=512):
     """prompts [B, n] int32 on the device.  Returns (per request the tokens emitted in `rounds` rounds, the mean
-    number of tokens a round, the cache)."""
+    number of tokens a round, the cache).  A round adds up to gamma + 1 tokens to a request: ValueError if a request
+    could outgrow max_len or the target's positions."""
     B, n = prompts.shape
     dev, gamma = prompts.device, draft.gamma
+    longest = n + rounds * (gamma + 1)
+    if longest > min(max_len, len(target.place)):
+        raise ValueError(f"a request may grow to {longest} tokens; the cache holds {max_len}, the target places {len(target.place)}")
     budget = budget or B * gamma
     most = max(budget + B, B * n)
     blocks = -(-max_len // page_size)
@@ -73,7 +81,7 @@ def generate(target, draft, prompts, rounds, T=0.0, budget=None, page_size=16, k
 
     # the prompts, whose last position gives the first token
     cache.plan(None, extra=n, max_new=n)
-    logits = target.forward(flat(prompts), cache.positions.clamp(min=0), cache)
+    logits = target.forward(flat(prompts), cache.positions, cache)
     anchor = logits[(cache.offsets[1:] - 1).long()].argmax(-1).int()
     cache.commit(None, extra=n)
     emitted = [anchor.tolist()]
@@ -83,7 +91,7 @@ def generate(target, draft, prompts, rounds, T=0.0, budget=None, page_size=16, k
         tok, lse, zat, _ = api.markov_sample_block(base, draft.W1, draft.W2, anchor, T, seed + r)
         L, _, _, _ = api.schedule_verify_len(conf, budget)
         cache.plan(L, extra=1, max_new=gamma + 1)
-        logits = target.forward(flat(torch.cat([anchor[:, None], tok], 1)), cache.positions.clamp(min=0), cache)
+        logits = target.forward(flat(torch.cat([anchor[:, None], tok], 1)), cache.positions, cache)
         # draft logits are bf16, so the target's are rounded to it for the verification
         n_acc, corr, _ = api.verify(base, draft.W1, draft.W2, anchor, tok, lse, zat, logits.to(base.dtype), T, seed + r,
                                     verify_len=L, target_row_offsets=cache.offsets)
@@ -104,12 +112,13 @@ def main(argv=None):
     ap.add_argument("--rounds", type=int, default=16)
     ap.add_argument("--e4m3", action="store_true", help="an 8-bit cache")
     a = ap.parse_args(argv)
-    V, d, gamma = 4096, 64, 8
-    target = ToyTarget(V, d, 2, 8, 2, 64, 512)
+    V, d, gamma, n = 4096, 64, 8, 24
+    max_len = max(512, n + a.rounds * (gamma + 1))
+    target = ToyTarget(V, d, 2, 8, 2, 64, max_len)
     draft = ToyDraft(gamma, target)
     g = torch.Generator(device="cuda").manual_seed(3)
-    prompts = torch.randint(0, V, (a.requests, 24), generator=g, device="cuda", dtype=torch.int32)
-    out, mean, cache = generate(target, draft, prompts, a.rounds, budget=a.requests * gamma // 2,
+    prompts = torch.randint(0, V, (a.requests, n), generator=g, device="cuda", dtype=torch.int32)
+    out, mean, cache = generate(target, draft, prompts, a.rounds, budget=a.requests * gamma // 2, max_len=max_len,
                                 kv_dtype=torch.float8_e4m3fn if a.e4m3 else None)
     print(f"{a.requests} requests, {a.rounds} rounds: {mean:.2f} tokens a request and round "
           f"({sum(map(len, out))} in all), cache status {cache.status()}, {int(cache.n_free)} pages free")

@@ -1,0 +1,22 @@
+"""Refusals of the paged cache's Python side and of the decoding rounds, on the host (no GPU is touched)."""
+
+import pytest
+import torch
+
+from semi_ar_draft_gb300 import decode_round as D
+
+
+@pytest.mark.parametrize("n,rounds,max_len,places", [(24, 100, 512, 512), (513, 0, 512, 1024), (24, 9, 200, 100), (9, 1, 17, 64)])
+def test_rounds_that_could_outgrow_the_cache_or_the_positions_are_refused(n, rounds, max_len, places):
+    """A round feeds up to gamma + 1 = 9 tokens a request; positions past the table would be read out of bounds."""
+    target = D.ToyTarget(32, 16, 1, 2, 1, 16, places, device="cpu")
+    draft = D.ToyDraft(8, target)
+    with pytest.raises(ValueError, match="tokens"):
+        D.generate(target, draft, torch.zeros((2, n), dtype=torch.int32), rounds, max_len=max_len)
+
+
+def test_positions_past_the_table_are_not_read():
+    """What plan reports as an error must not fault in the embedding of the positions: they stop at the table's end."""
+    target = D.ToyTarget(32, 16, 1, 2, 1, 16, 8, device="cpu")
+    got = target.places(torch.tensor([-1, 0, 7, 8, 1 << 30], dtype=torch.int32))
+    assert torch.equal(got, target.place[torch.tensor([0, 0, 7, 7, 7])])
