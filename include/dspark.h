@@ -384,6 +384,9 @@ dspark_status dspark_markov_sample_block_noalloc(const dspark_sample_params* p, 
  * pool gets slot -1, which dspark_cache_append skips.
  * Host errors: DSPARK_ERR_UNSUPPORTED for B > 8192.
  * dspark_cache_workspace_size serves dspark_cache_plan and dspark_cache_commit.
+ * error (of dspark_cache_params and dspark_attention_params): a call's device status replaces the one its workspace
+ * held before.  A caller that looks at it less often than every call gives them one int32 of its own, set to
+ * DSPARK_OK: a call that ends in an error stores its status there if it still holds DSPARK_OK, and no call clears it.
  */
 typedef struct {
     int B;          /* requests */
@@ -392,6 +395,7 @@ typedef struct {
     int max_blocks; /* columns of block_table */
     int max_tokens; /* entries of slots and positions (dspark_cache_plan) */
     int extra;      /* tokens a request feeds or keeps beyond its new_len / add_len (>= 0) */
+    int32_t* error; /* device word or NULL: see below */
 } dspark_cache_params;
 
 size_t dspark_cache_workspace_size(const dspark_cache_params* p);
@@ -480,6 +484,7 @@ typedef struct {
     float scale, softcap;
     int64_t q_token_stride, q_head_stride;
     int64_t kv_page_stride, kv_token_stride, kv_head_stride;
+    int32_t* error; /* device word or NULL: as of dspark_cache_params */
 } dspark_attention_params;
 
 size_t dspark_paged_attention_workspace_size(const dspark_attention_params* p);

@@ -158,11 +158,12 @@ def _cache_ws(ws, like):
 
 
 def cache_plan(cache_len, new_len, block_table, n_blocks, free_pages, n_free, page_size, max_tokens, extra=0,
-               positions=True, out=None, ws=None, stream=None):
+               positions=True, out=None, ws=None, stream=None, error=None):
     """A step's pages, slots and offsets from the requests' lengths (dspark_cache_plan): cache_len, new_len (or
     None), n_blocks [B], free_pages [pages], n_free [1], all int32; block_table [B, max_blocks] int32 gains the new
     pages.  Returns (seq_len [B], offsets [B+1], slots [max_tokens] int64, positions [max_tokens] or None,
-    n_blocks [B], n_free [1], workspace); n_blocks and n_free are new tensors."""
+    n_blocks [B], n_free [1], workspace); n_blocks and n_free are new tensors.  error [1] int32, or None: the
+    caller's, in which the first device error of its calls stays until it is cleared."""
     made = ()
     if out is None:
         B, i32 = cache_len.numel(), {"dtype": torch.int32, "device": cache_len.device}
@@ -170,23 +171,24 @@ def cache_plan(cache_len, new_len, block_table, n_blocks, free_pages, n_free, pa
                       torch.empty(max_tokens, **i32) if positions else None, torch.empty(B, **i32), torch.empty(1, **i32))
     ws = _cache_ws(ws, cache_len)
     st = b.native().cache_plan(cache_len, new_len, block_table, n_blocks, free_pages, n_free, page_size, max_tokens, extra, *out,
-                               ws, _raw(stream, ws, *made))
+                               ws, _raw(stream, ws, *made), error)
     b._check(st, "dspark_cache_plan")
     return (*out, ws)
 
 
 def cache_commit(cache_len, add_len, block_table, n_blocks, free_pages, n_free, page_size, extra=0, done=None, out=None,
-                 ws=None, stream=None):
+                 ws=None, stream=None, error=None):
     """The requests' lengths after the verification, and the pages past them back on the stack
     (dspark_cache_commit): add_len [B] int32 (n_accepted) or None, done [B] uint8 or bool, or None; free_pages is
-    written in place.  Returns (cache_len [B], n_blocks [B], n_free [1], workspace), new tensors."""
+    written in place.  Returns (cache_len [B], n_blocks [B], n_free [1], workspace), new tensors.  error as for
+    cache_plan."""
     made = ()
     if out is None:
         B, i32 = cache_len.numel(), {"dtype": torch.int32, "device": cache_len.device}
         made = out = (torch.empty(B, **i32), torch.empty(B, **i32), torch.empty(1, **i32))
     ws = _cache_ws(ws, cache_len)
     st = b.native().cache_commit(cache_len, add_len, done, block_table, n_blocks, free_pages, n_free, page_size, extra, *out, ws,
-                                 _raw(stream, ws, *made))
+                                 _raw(stream, ws, *made), error)
     b._check(st, "dspark_cache_commit")
     return (*out, ws)
 
@@ -205,10 +207,11 @@ def _attention_sizes(q, k_pages, seq_len, max_new):
 
 
 def paged_attention(q, k_pages, v_pages, block_table, seq_len, offsets=None, scale=None, causal=True, window=0,
-                    softcap=0.0, k_scale=None, v_scale=None, max_new=0, out=None, lse=None, ws=None, stream=None):
+                    softcap=0.0, k_scale=None, v_scale=None, max_new=0, out=None, lse=None, ws=None, stream=None, error=None):
     """Attention of the new tokens q [T, Hq, D] over the paged cache, which holds their keys and values already
     (dspark_paged_attention): block_table [B, max_blocks], seq_len [B], offsets [B+1] int32 (None: one token a
-    request).  scale defaults to D ** -0.5.  lse: None, True, or a [T, Hq] fp32 tensor to write.
+    request).  scale defaults to D ** -0.5.  lse: None, True, or a [T, Hq] fp32 tensor to write.  error as for
+    cache_plan.
     Returns (out [T, Hq, D], lse or None, workspace)."""
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -218,6 +221,6 @@ def paged_attention(q, k_pages, v_pages, block_table, seq_len, offsets=None, sca
         ws = b.workspace(b.dspark_paged_attention_workspace_size(_attention_sizes(q, k_pages, seq_len, max_new)), q.device)
     st, ws = b.native().paged_attention(q, k_pages, v_pages, block_table, seq_len, offsets, k_scale, v_scale,
                                         q.shape[-1] ** -0.5 if scale is None else scale, softcap, causal, window, max_new, out,
-                                        lse, ws, _raw(stream, ws, out, lse))
+                                        lse, ws, _raw(stream, ws, out, lse), error)
     b._check(st, "dspark_paged_attention")
     return out, lse, ws

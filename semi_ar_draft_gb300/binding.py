@@ -40,7 +40,7 @@ class SampleParams(C.Structure):
 
 class CacheParams(C.Structure):
     _fields_ = [("B", C.c_int), ("page_size", C.c_int), ("num_pages", C.c_int), ("max_blocks", C.c_int),
-                ("max_tokens", C.c_int), ("extra", C.c_int)]
+                ("max_tokens", C.c_int), ("extra", C.c_int), ("error", C.c_void_p)]
 
 
 class AppendParams(C.Structure):
@@ -56,7 +56,7 @@ class AttentionParams(C.Structure):
                 ("dtype", C.c_int), ("kv_dtype", C.c_int), ("causal", C.c_int), ("window", C.c_int),
                 ("scale", C.c_float), ("softcap", C.c_float), ("q_token_stride", C.c_int64),
                 ("q_head_stride", C.c_int64), ("kv_page_stride", C.c_int64), ("kv_token_stride", C.c_int64),
-                ("kv_head_stride", C.c_int64)]
+                ("kv_head_stride", C.c_int64), ("error", C.c_void_p)]
 
 
 _L = None

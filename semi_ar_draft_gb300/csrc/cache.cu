@@ -89,6 +89,7 @@ struct PlanArgs {
     int32_t* n_blocks_out;
     int32_t* n_free_out;
     int32_t* status;
+    int32_t* error;  // or null
 };
 
 // One request's numbers, with every input clamped to what the other inputs allow (bad: it was not).
@@ -156,6 +157,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(PlanArgs a) {
         a.offsets[a.B] = sat32(T);
         *a.n_free_out = n_free - given;
         *a.status = any_bad ? DSPARK_ERR_CACHE : DSPARK_OK;
+        if (any_bad && a.error) record_status(a.error, DSPARK_ERR_CACHE);
     }
     const int stride = gridDim.x * kPlanThreads;
     // The new pages' table entries.  A page is known from the stack alone, so the tokens below look
@@ -209,6 +211,7 @@ struct CommitArgs {
     int32_t* n_blocks_out;
     int32_t* n_free_out;
     int32_t* status;
+    int32_t* error;  // or null
 };
 
 struct CommitReq {
@@ -327,6 +330,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_commit_kernel(CommitArgs a
     if (first && tid == 0) {
         *a.n_free_out = n_free + min(total, room);
         *a.status = any_bad ? DSPARK_ERR_CACHE : DSPARK_OK;
+        if (any_bad && a.error) record_status(a.error, DSPARK_ERR_CACHE);
     }
 #pragma unroll 1
     for (long long from = begin; from < end; from += 32 * kHeldSteps) {
@@ -475,7 +479,8 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 }
 
 dspark_status check_cache_params(const dspark_cache_params* p) {
-    if (!p || p->B < 1 || p->num_pages < 1 || p->max_blocks < 1 || page_shift_of(p->page_size) < 0)
+    if (!p || p->B < 1 || p->num_pages < 1 || p->max_blocks < 1 || page_shift_of(p->page_size) < 0 ||
+        ((uintptr_t)p->error & 3u))
         return DSPARK_ERR_INVALID_ARG;
     if (p->B > kMaxRequests) return DSPARK_ERR_UNSUPPORTED;
     return DSPARK_OK;
@@ -532,7 +537,7 @@ extern "C" dspark_status dspark_cache_plan(const dspark_cache_params* p, const i
         return DSPARK_ERR_CUDA;
     PlanArgs a{p->B, page_shift_of(p->page_size), p->num_pages, p->max_blocks, p->max_tokens, p->extra, cache_len,
                new_len, block_table, n_blocks, free_pages, n_free, seq_len, offsets, slots, positions, n_blocks_out,
-               n_free_out, &static_cast<WsHeader*>(workspace)->status};
+               n_free_out, &static_cast<WsHeader*>(workspace)->status, p->error};
     if (launch_overlapped(cache_plan_kernel, blocks_for(p->max_tokens, sms), kPlanThreads, smem,
                           reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
         return DSPARK_ERR_CUDA;
@@ -571,7 +576,7 @@ extern "C" dspark_status dspark_cache_commit(const dspark_cache_params* p, const
         return DSPARK_ERR_CUDA;
     CommitArgs a{p->B, page_shift_of(p->page_size), p->num_pages, p->max_blocks, p->extra, cache_len, add_len, done,
                  block_table, n_blocks, free_pages, n_free, cache_len_out, n_blocks_out, n_free_out,
-                 &static_cast<WsHeader*>(workspace)->status};
+                 &static_cast<WsHeader*>(workspace)->status, p->error};
     if (launch_overlapped_clusters(kernel, blocks, blocks, kPlanThreads, smem,
                                    reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
         return DSPARK_ERR_CUDA;

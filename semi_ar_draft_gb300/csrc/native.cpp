@@ -83,6 +83,13 @@ dspark_stream_t stream_of(PyObject* o, const at::Tensor& t) {
     return reinterpret_cast<dspark_stream_t>((uintptr_t)number(o));
 }
 
+// The caller's word for the first device error of its calls, or none.
+int32_t* error_word(PyObject* o) {
+    const at::Tensor* t = tensor(o);
+    want(t, at::kInt, 1, "error is int32 [1]");
+    return as<int32_t>(address(t));
+}
+
 int type_code(at::ScalarType t) {
     switch (t) {
         case at::kBFloat16: return DSPARK_BF16;
@@ -127,26 +134,26 @@ void count_args(Py_ssize_t n, Py_ssize_t wanted) {
 
 dspark_cache_params cache_params(const at::Tensor& cache_len, const at::Tensor& table, const at::Tensor& n_blocks,
                                  const at::Tensor& free_pages, const at::Tensor& n_free, PyObject* page_size,
-                                 int max_tokens, PyObject* extra) {
+                                 int max_tokens, PyObject* extra, PyObject* error) {
     if (cache_len.scalar_type() != at::kInt || free_pages.scalar_type() != at::kInt || table.scalar_type() != at::kInt)
         refuse(PyExc_ValueError, "cache_len, free_pages and block_table are int32");
     const int64_t B = cache_len.numel();
     want(&n_blocks, at::kInt, B, "n_blocks is int32 [B]");
     want(&n_free, at::kInt, 1, "n_free is int32 [1]");
     if (table.dim() != 2 || table.size(0) != B) refuse(PyExc_ValueError, "block_table is [B, max_blocks]");
-    return {size32(B), small(page_size), size32(free_pages.numel()), size32(table.size(1)), max_tokens, small(extra)};
+    return {size32(B), small(page_size), size32(free_pages.numel()), size32(table.size(1)), max_tokens, small(extra), error_word(error)};
 }
 
 // cache_len, new_len, block_table, n_blocks, free_pages, n_free, page_size, max_tokens, extra,
-// seq_len, offsets, slots, positions, n_blocks_out, n_free_out, workspace, stream
+// seq_len, offsets, slots, positions, n_blocks_out, n_free_out, workspace, stream, error
 PyObject* cache_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&] {
-        count_args(n, 17);
+        count_args(n, 18);
         const at::Tensor &cache_len = needed(a[0]), &table = needed(a[2]), &n_blocks = needed(a[3]), &free_pages = needed(a[4]),
                          &n_free = needed(a[5]), &seq = needed(a[9]), &off = needed(a[10]), &slots = needed(a[11]),
                          &n_blocks_out = needed(a[13]), &n_free_out = needed(a[14]), &ws = needed(a[15]);
         const at::Tensor *new_len = tensor(a[1]), *positions = tensor(a[12]);
-        const dspark_cache_params p = cache_params(cache_len, table, n_blocks, free_pages, n_free, a[6], small(a[7]), a[8]);
+        const dspark_cache_params p = cache_params(cache_len, table, n_blocks, free_pages, n_free, a[6], small(a[7]), a[8], a[17]);
         want(new_len, at::kInt, p.B, "new_len is int32 [B]");
         want(&seq, at::kInt, p.B, "seq_len is int32 [B]");
         want(&off, at::kInt, (int64_t)p.B + 1, "offsets is int32 [B + 1]");
@@ -164,15 +171,15 @@ PyObject* cache_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // cache_len, add_len, done, block_table, n_blocks, free_pages, n_free, page_size, extra, cache_len_out,
-// n_blocks_out, n_free_out, workspace, stream
+// n_blocks_out, n_free_out, workspace, stream, error
 PyObject* cache_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&] {
-        count_args(n, 14);
+        count_args(n, 15);
         const at::Tensor &cache_len = needed(a[0]), &table = needed(a[3]), &n_blocks = needed(a[4]), &free_pages = needed(a[5]),
                          &n_free = needed(a[6]), &len_out = needed(a[9]), &n_blocks_out = needed(a[10]),
                          &n_free_out = needed(a[11]), &ws = needed(a[12]);
         const at::Tensor *add_len = tensor(a[1]), *done = tensor(a[2]);
-        const dspark_cache_params p = cache_params(cache_len, table, n_blocks, free_pages, n_free, a[7], 0, a[8]);
+        const dspark_cache_params p = cache_params(cache_len, table, n_blocks, free_pages, n_free, a[7], 0, a[8], a[14]);
         want(add_len, at::kInt, p.B, "add_len is int32 [B]");
         if (done && ((done->scalar_type() != at::kByte && done->scalar_type() != at::kBool) || done->numel() != p.B))
             refuse(PyExc_ValueError, "done is uint8 or bool [B]");
@@ -209,10 +216,10 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // q, k_pages, v_pages, block_table, seq_len, offsets, k_scale, v_scale, scale, softcap, causal, window,
-// max_new, out, lse, workspace (or None: one is allocated), stream.  Returns (status, workspace).
+// max_new, out, lse, workspace (or None: one is allocated), stream, error.  Returns (status, workspace).
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        count_args(n, 17);
+        count_args(n, 18);
         const at::Tensor &q = needed(a[0]), &kp = needed(a[1]), &vp = needed(a[2]), &table = needed(a[3]), &seq = needed(a[4]),
                          &out = needed(a[13]);
         const at::Tensor *off = tensor(a[5]), *ks = tensor(a[6]), *vs = tensor(a[7]), *lse = tensor(a[14]);
@@ -248,6 +255,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         p.kv_page_stride = x.page;
         p.kv_token_stride = x.token;
         p.kv_head_stride = x.head;
+        p.error = error_word(a[17]);
         const dspark_stream_t s = stream_of(a[16], q);
         at::Tensor made;
         const at::Tensor* ws = tensor(a[15]);

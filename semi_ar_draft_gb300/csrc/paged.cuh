@@ -46,6 +46,7 @@ struct AttnArgs {
     float* lse;          // [T, Hq] or null
     // workspace
     int32_t* status;
+    int32_t* error;  // the caller's word for the first error, or null
     struct PartItem* items;  // [parts]
     float2* part_ml;         // [2 parts][rows of a tile]: (maximum, log2 domain; sum)
     float* part_o;           // [2 parts][rows of a tile][D]

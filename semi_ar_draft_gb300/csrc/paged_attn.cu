@@ -551,7 +551,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
         int err = 0;
         for (int p = lane; p < parts; p += 32) err = max(err, a.items[p].err);
         err = __reduce_max_sync(0xffffffffu, err);
-        if (lane == 0) *a.status = err;
+        if (lane == 0) {
+            *a.status = err;
+            if (err && a.error) record_status(a.error, err);
+        }
     }
 #pragma unroll 1
     for (int side = 0; side < 2; ++side) {
@@ -710,7 +713,7 @@ AttnWs attn_ws(const dspark_attention_params* p) {
 
 dspark_status check_attention_params(const dspark_attention_params* p) {
     if (!p || p->T < 0 || p->B < 1 || p->Hk < 1 || p->Hq < 1 || p->D < 1 || p->num_pages < 1 || p->max_blocks < 1 ||
-        page_shift_of(p->page_size) < 0 || p->window < 0)
+        page_shift_of(p->page_size) < 0 || p->window < 0 || ((uintptr_t)p->error & 3u))
         return DSPARK_ERR_INVALID_ARG;
     if (p->Hq % p->Hk || !(p->softcap >= 0.f) || isinf(p->softcap) || !isfinite(p->scale)) return DSPARK_ERR_INVALID_ARG;
     if (p->dtype != DSPARK_BF16 && p->dtype != DSPARK_F16) return DSPARK_ERR_INVALID_ARG;
@@ -786,6 +789,7 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     a.out = static_cast<unsigned char*>(out);
     a.lse = lse;
     a.status = &reinterpret_cast<WsHeader*>(ws)->status;
+    a.error = p->error;
     a.items = reinterpret_cast<PartItem*>(ws + w.items);
     a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
     a.part_o = reinterpret_cast<float*>(ws + w.o);

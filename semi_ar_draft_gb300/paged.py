@@ -54,6 +54,7 @@ class PagedCache:
         self.slots = torch.empty(max_tokens, dtype=torch.int64, device=device)
         self.positions = torch.empty(max_tokens, **i32)
         self.ws = torch.zeros(256, dtype=torch.uint8, device=device)
+        self._error = torch.zeros(1, **i32)  # the first device error since status() was last called
         self.max_new = 0
 
     @property
@@ -69,7 +70,7 @@ class PagedCache:
         """Pages and slots for new_len[j] + extra tokens of each request.  Sets seq_len, offsets, slots, positions.
         max_new: the most new tokens of one request, if known (it chooses attend's kernel)."""
         api.cache_plan(self._len[0], new_len, self.block_table, self._blocks[0], self.free_pages, self._free[0],
-                       self.page_size, self.max_tokens, extra=extra, ws=self.ws, stream=stream,
+                       self.page_size, self.max_tokens, extra=extra, ws=self.ws, stream=stream, error=self._error,
                        out=(self.seq_len, self.offsets, self.slots, self.positions, self._blocks[1], self._free[1]))
         self._keep(len(self._len[0]), stream)
         self.max_new = max_new
@@ -83,13 +84,13 @@ class PagedCache:
         """q [max_tokens, Hq, D]; kw as for api.paged_attention.  Returns (out, lse or None)."""
         out, lse, _ = api.paged_attention(q, self.k_pages[layer], self.v_pages[layer], self.block_table, self.seq_len,
                                           self.offsets, k_scale=self.k_scale[layer], v_scale=self.v_scale[layer],
-                                          max_new=self.max_new, stream=stream, **kw)
+                                          max_new=self.max_new, stream=stream, error=self._error, **kw)
         return out, lse
 
     def commit(self, add_len=None, extra=0, done=None, stream=None):
         """Keeps add_len[j] + extra of each request's new tokens (none of the whole request where done)."""
         api.cache_commit(self._len[0], add_len, self.block_table, self._blocks[0], self.free_pages, self._free[0],
-                         self.page_size, extra=extra, done=done, ws=self.ws, stream=stream,
+                         self.page_size, extra=extra, done=done, ws=self.ws, stream=stream, error=self._error,
                          out=(self._len[1], self._blocks[1], self._free[1]))
         self._keep(0, stream)
 
@@ -99,5 +100,10 @@ class PagedCache:
             self._counts[0][first:].copy_(self._counts[1][first:])
 
     def status(self, stream=None):
-        """Device status of the last plan or commit (synchronises)."""
-        return b.dspark_get_device_status(self.ws, stream)
+        """The first device error of plan, attend and commit since this was last called, 0 if there was none
+        (synchronises the stream; calls made on others count once they have run)."""
+        code = b.dspark_get_device_status(self._error, stream)
+        if code:
+            with _on(stream):
+                self._error.zero_()
+        return code

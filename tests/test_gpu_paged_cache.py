@@ -92,3 +92,61 @@ def test_counts_are_read_through_the_same_tensors():
         cache.commit(i32([3, 1]), stream=stream)
         torch.cuda.synchronize()
     assert lengths.tolist() == [12, 4] and int(free) == 9 - 4 and cache.status() == 0
+
+
+# ------------------------------------------------------------------ errors
+def test_a_plans_error_outlives_the_commit():
+    """More tokens than max_tokens: some have no slot, their keys are never written, and the commit finds nothing wrong."""
+    cache = PagedCache(2, 9, 4, 4, 1, 1, 64, 8)
+    cache.plan(i32([6, 6]))
+    cache.commit(i32([1, 1]))
+    assert cache.status() == 8
+    cache.plan(i32([3, 3]))
+    cache.commit(i32([1, 1]))
+    assert cache.status() == 0  # reading it clears it
+
+
+def test_a_full_pool_is_still_known_after_the_commit():
+    cache = PagedCache(2, 3, 4, 8, 1, 1, 64, 40)
+    cache.plan(i32([9, 9]))
+    cache.commit(i32([1, 1]))
+    assert cache.status() == 8 and cache.status() == 0
+
+
+@pytest.mark.parametrize("Hq,max_new", [(4, 1), (64, 9)])  # row tiles of 16, of 128
+@pytest.mark.parametrize("other_stream", [False, True])
+def test_an_error_of_attention_is_seen(Hq, max_new, other_stream):
+    cache = PagedCache(2, 8, 4, 4, 1, 1, 64, 16)
+    cache.plan(i32([8, 3]), max_new=max_new)
+    good = int(cache.block_table[0, 1])
+    q = torch.randn((16, Hq, 64), device="cuda").to(torch.bfloat16)
+    cache.block_table[0, 1] = 77
+    side = torch.cuda.Stream() if other_stream else None
+    torch.cuda.synchronize()
+    cache.attend(0, q, stream=side)
+    torch.cuda.synchronize()
+    cache.block_table[0, 1] = good
+    cache.attend(0, q)
+    cache.commit(i32([8, 3]))
+    assert cache.status() == 8 and cache.status() == 0
+
+
+def test_the_error_word_of_the_calls():
+    """The first error stays until its owner clears it; the workspace's status is each call's own."""
+    error = i32([0])
+    args = lambda n_free: (i32([3]), i32([4]), i32([[0, -1]]), i32([1]), i32([1, 2, 3, 0]), i32([n_free]), 4, 8)  # noqa: E731
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    status = lambda: api.b.dspark_get_device_status(ws)  # noqa: E731
+    api.cache_plan(*args(3), ws=ws, error=error)
+    assert status() == 0 and int(error) == 0
+    api.cache_plan(*args(0), ws=ws, error=error)
+    assert status() == 8 and int(error) == 8
+    api.cache_plan(*args(3), ws=ws, error=error)
+    assert status() == 0 and int(error) == 8
+    error.fill_(4)
+    api.cache_commit(i32([99]), None, i32([[0, -1]]), i32([1]), i32([1, 2, 3, 0]), i32([3]), 4, ws=ws, error=error)
+    assert status() == 8 and int(error) == 4
+    with pytest.raises(ValueError):
+        api.cache_plan(*args(3), error=torch.zeros(1, device="cuda"))
+    with pytest.raises(ValueError):
+        api.cache_commit(i32([9]), None, i32([[0, -1]]), i32([1]), i32([1, 2, 3, 0]), i32([3]), 4, error=i32([0, 0]))

@@ -20,3 +20,15 @@ def test_positions_past_the_table_are_not_read():
     target = D.ToyTarget(32, 16, 1, 2, 1, 16, 8, device="cpu")
     got = target.places(torch.tensor([-1, 0, 7, 8, 1 << 30], dtype=torch.int32))
     assert torch.equal(got, target.place[torch.tensor([0, 0, 7, 7, 7])])
+
+
+def test_a_misaligned_error_word_is_refused():
+    from semi_ar_draft_gb300 import binding as b, build
+
+    build.build()
+    assert b.dspark_cache_workspace_size(b.CacheParams(4, 16, 10, 5, 40, 1, 0x1004)) == 256
+    assert b.dspark_cache_workspace_size(b.CacheParams(4, 16, 10, 5, 40, 1, 0x1002)) == 0
+    p = b.AttentionParams(4, 4, 8, 2, 128, 16, 9, 3, 1, b.BF16, b.BF16, 1, 0, 0.1, 0.0, 1024, 128, 4096, 256, 128, 0x1004)
+    assert b.dspark_paged_attention_workspace_size(p) > 256
+    p.error = 0x1001
+    assert b.dspark_paged_attention_workspace_size(p) == 0
