@@ -465,7 +465,8 @@ dspark_status dspark_cache_append(const dspark_append_params* p, const void* k, 
  *   max_new: the most new tokens of one request, if known (0 = not): with T / B it only chooses between
  *   kernels.
  * Outputs: out [T, Hq, D] dense (dtype), 16-byte aligned; lse [T, Hq] float or NULL.
- * Scores, sums and outputs are held in fp32; probabilities are rounded to 16 bits (dtype; fp16 with an
+ * Scores, sums and outputs are held in fp32 (the softcap within 2e-6 of a score, a cap past 2^100 leaves scores as they
+ * are); probabilities are rounded to 16 bits (dtype; fp16 with an
  * 8-bit cache) before they meet the values.  What a row does not see never touches it, whatever is
  * stored there (NaN included).  The same inputs give the same outputs bit for bit.
  * Device status DSPARK_ERR_CACHE: a negative seq_len or one past max_blocks page_size (or 2^31 - 4097),

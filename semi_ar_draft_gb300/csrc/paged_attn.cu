@@ -338,15 +338,17 @@ __global__ void __launch_bounds__(Rows16<F8, DP>::kThreads, Rows16<F8, DP>::kBlo
 #pragma unroll
             for (int i = 0; i < KT; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int r = c >> 1;
-                    float x = a.softcap > 0.f ? softcap(s[i][c], row_scale[r], cap_out) : s[i][c] * row_scale[r];
+                for (int r = 0; r < 2; ++r) {
+                    float2 x = make_float2(s[i][2 * r] * row_scale[r], s[i][2 * r + 1] * row_scale[r]);
+                    if (a.softcap > 0.f) x = softcap2(s[i][2 * r], s[i][2 * r + 1], row_scale[r], cap_out);
                     if (edge) {
-                        const int key = key0 + 8 * i + 2 * t + (c & 1);
-                        if (key < see_lo[r] || key >= see_hi[r]) x = -CUDART_INF_F;
+                        const int key = key0 + 8 * i + 2 * t;
+                        if (key < see_lo[r] || key >= see_hi[r]) x.x = -CUDART_INF_F;
+                        if (key + 1 < see_lo[r] || key + 1 >= see_hi[r]) x.y = -CUDART_INF_F;
                     }
-                    s[i][c] = x;
-                    mx[r] = fmaxf(mx[r], x);
+                    s[i][2 * r] = x.x;
+                    s[i][2 * r + 1] = x.y;
+                    mx[r] = fmaxf(mx[r], fmaxf(x.x, x.y));
                 }
             bool grow = false;
 #pragma unroll
@@ -771,7 +773,9 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     a.causal = p->causal != 0;
     a.window = p->window;
     a.scale = p->scale;
-    a.softcap = p->softcap;
+    // A cap past 2^100 leaves every score as it is (s^2 / 3 c^2 is below 2^-24 for |s| up to 2^88); 1 / c would come near
+    // the smallest normal number.
+    a.softcap = p->softcap > 0x1p100f ? 0.f : p->softcap;
     a.q = static_cast<const unsigned char*>(q);
     a.q_token = p->q_token_stride;
     a.q_head = p->q_head_stride;

@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
         };
         // An item's queries: with two streams after its first keys, since their buffer is free later than a
         // slot (421 against 426 us for the 512-request verify); with heads of 256, where they are as large as two
-        // tiles, before (122 against 131 us for three long contexts).
+        // tiles, before (122 against 131 us for three long contexts, with a softcap 8 us cheaper than now).
         constexpr bool kQueriesFirst = NS == 1;
         auto queries = [&]() {
             const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
@@ -539,8 +539,11 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
                         tmem_wait_ld(x);
                         if (a.softcap > 0.f) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                x[i] = __float_as_uint(softcap(__uint_as_float(x[i]), cap_in, cap_out));
+                            for (int i = 0; i < 32; i += 2) {
+                                const float2 y = softcap2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]), cap_in, cap_out);
+                                x[i] = __float_as_uint(y.x);
+                                x[i + 1] = __float_as_uint(y.y);
+                            }
                         } else if (!plain) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * c);
