@@ -30,7 +30,8 @@ struct AttnArgs {
     uint32_t g_mul, g_shift;  // row / G = umulhi(2 row, g_mul) >> g_shift for rows below 2^31 (group_division)
     int page_shift, num_pages, max_blocks;
     int causal, window;
-    int q_vec;  // rows of q start on 16-byte boundaries
+    float sum_scale;  // ProbScale's inverse, for lse
+    int q_vec;        // rows of q start on 16-byte boundaries
     float scale, softcap;
     const unsigned char* q;
     long long q_token, q_head;  // strides, elements
@@ -298,6 +299,15 @@ __device__ __forceinline__ bool odd_found(uint32_t acc) {
     constexpr uint32_t inf = BF16 ? 0x7f80u : 0x7c00u;
     return (acc & 0xffffu) >= inf || (acc >> 16) >= inf;
 }
+
+// Probabilities as halves are taken against a reference 2^7 below the running maximum's (which follows within 2^8, so
+// they stay below 2^15): halves lose bits below 2^-14, which is then 2^-21 of the largest.  bf16 has fp32's exponents.
+// Sums carry the same factor; it cancels in the output and is taken out of lse.
+template <bool BF16>
+struct ProbScale {
+    static constexpr float kBits = BF16 ? 0.f : 7.f;
+    static constexpr float kInverse = BF16 ? 1.f : 0x1p-7f;
+};
 
 // Two floats rounded to the 16-bit type, first in the low half.
 template <bool BF16>

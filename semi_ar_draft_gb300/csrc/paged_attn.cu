@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(Rows16<F8, DP>::kThreads, Rows16<F8, DP>::kBlo
                     }
                 }
             }
-            const float ref[2] = {m[0] == -CUDART_INF_F ? 0.f : m[0], m[1] == -CUDART_INF_F ? 0.f : m[1]};
+            constexpr float kUp = ProbScale<MB>::kBits;
+            const float ref[2] = {m[0] == -CUDART_INF_F ? 0.f : m[0] - kUp, m[1] == -CUDART_INF_F ? 0.f : m[1] - kUp};
 #pragma unroll
             for (int i = 0; i < KT; ++i)
 #pragma unroll
@@ -515,7 +516,8 @@ __global__ void __launch_bounds__(Rows16<F8, DP>::kThreads, Rows16<F8, DP>::kBlo
                         const float inv = ll == 0.f ? 0.f : vscale / ll;
                         store_out4<BF16>(a, at, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                     }
-                    if (a.lse && col == 0) a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll)) * kLn2;
+                    if (a.lse && col == 0)
+                        a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll * ProbScale<MB>::kInverse)) * kLn2;
                 } else {
                     if (col < a.D)
                         *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * kRows + row) * a.D + col) = v;
@@ -595,7 +597,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
                         }
                     }
                     if (in) store_out4<BF16>(a, at, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-                    if (a.lse && col == 0) a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll)) * kLn2;
+                    if (a.lse && col == 0) a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll * a.sum_scale)) * kLn2;
                 }
             }
             continue;
@@ -662,7 +664,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
                     }
                     const long long at = attn_out_row(a, it.token0, it.head, it.row0 + row);
                     store_out4<BF16>(a, at, col, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
-                    if (a.lse && col == 0) a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll)) * kLn2;
+                    if (a.lse && col == 0) a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll * a.sum_scale)) * kLn2;
                 }
                 __syncthreads();
             }
@@ -798,6 +800,7 @@ extern "C" dspark_status dspark_paged_attention(const dspark_attention_params* p
     a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
     a.part_o = reinterpret_cast<float*>(ws + w.o);
     const bool bf16 = p->dtype == DSPARK_BF16;
+    a.sum_scale = bf16 && !e4m3 ? ProbScale<true>::kInverse : ProbScale<false>::kInverse;
     int parts = 0;
     const bool tc = wide_rows(p) && a.q_vec;
     const dspark_status ls = tc     ? launch_attn_tc(a, bf16, e4m3, sms, s, &parts)

@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
                         tmem_st16(tmem + lanes + s * DP + i, o);
                     }
                 }
-                const float ref = m == -CUDART_INF_F ? 0.f : m;
+                const float ref = m == -CUDART_INF_F ? 0.f : m - ProbScale<VB>::kBits;
                 const uint64_t f2 = pk2(f, f), r2 = pk2(-ref, -ref);
                 uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
                     if (!whole)
                         a.part_ml[slot * kTcRowTile + row] = make_float2(mm, ll);
                     else if (a.lse)
-                        a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll)) * kLn2;
+                        a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll * ProbScale<VB>::kInverse)) * kLn2;
                 }
                 if (!whole && tid == 0) mine->d[seg_first == 0 ? kHead : kTail] = part_desc(start, w, row0, rows, head);
                 tc_fence_before();

@@ -1,4 +1,4 @@
-"""Attention's scores at the ends of their range: softcaps far below and far above them."""
+"""Attention's scores at the ends of their range: softcaps far above them, probabilities far below the largest."""
 import math
 
 import pytest
@@ -65,3 +65,40 @@ def test_a_large_softcap_changes_nothing(max_new):
         assert bool(((lse - ref_lse).abs() <= 2.0 ** -15).all())
         big = float(v.abs().max())
         assert bool(((out - ref).abs() <= 2 * big * 2.0 ** -15 + 2 * 2.0 ** -8 * (ref.abs() + big)).all())
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("lead", [10.0, 14.0, 16.0, 18.0])
+@pytest.mark.parametrize("L,max_new", [(700, 1), (700, 17), (9000, 1), (9000, 17)])
+def test_a_key_that_dominates_with_a_small_value(dtype, cache, lead, L, max_new):
+    """An attention sink: the first key leads by `lead` nats and its value is 0, so the output is what the other keys'
+    small probabilities make of their values.
+
+    Bound: probabilities are taken against a reference r with at least one at 1 or more, times 2^7 as halves: half a
+    step of the subnormal halves is 2^-25, so each is off by 2^-32 / sum at most, or by its rounding (u_p); the output
+    by one rounding more (2 u |o|, 2^-25 where it is a subnormal half); scores in fp32 by 2^-18 (20 nats, D = 64
+    products and a few roundings)."""
+    G, D, n = 16, 64, 17
+    g = torch.Generator(device="cuda").manual_seed(int(lead) + L)
+    q = torch.zeros((n * G, D), device="cuda")
+    q[:, 0] = 1.0
+    q[:, 1] = torch.rand(n * G, generator=g, device="cuda").to(torch.float16).float() * 0.25
+    k = torch.zeros((L, D), device="cuda")
+    k[0, 0] = lead
+    k[1:, 1] = torch.randint(-4, 5, (L - 1,), generator=g, device="cuda") * 0.25
+    v = 100.0 + 10.0 * torch.randint(0, 20, (L, D), generator=g, device="cuda")
+    v[0] = 0.0
+    v = v.to(cache).float()
+    k = k.to(cache).float()
+    out, lse = one_head(q, k, v, G, n, dtype, cache, scale=1.0, max_new=max_new)
+    s = q.to(dtype).double() @ k.double().T
+    p = torch.softmax(s, -1)
+    want = p @ v.double()
+    assert bool((s[:, 0] - s[:, 1:].amax(-1) > lead - 1).all())
+    u = torch.finfo(dtype).eps / 2
+    u_p = u if cache != E4M3 else 2.0 ** -11
+    absolute = 0.0 if (dtype, cache) == (torch.bfloat16, torch.bfloat16) else 2.0 ** -32
+    away = p[:, 1:] @ v[1:].double()
+    tol = away * (u_p + 2.0 ** -17) + absolute * v.double().sum(0) + 2 * u * want + 2.0 ** -25
+    err = (out - want).abs()
+    assert bool((err <= tol).all()), (float((err / want).max()), float((err - tol).max()))
