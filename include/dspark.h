@@ -375,7 +375,7 @@ dspark_status dspark_markov_sample_block_noalloc(const dspark_sample_params* p, 
  *   slots [max_tokens]: of token offsets[j] + i, whose position is cache_len[j] + i; -1 from offsets[B] on
  *   positions [max_tokens] int32 (or NULL): those positions, -1 from offsets[B] on
  *   n_blocks_out[j] = n_blocks[j] + need_j;  n_free_out = n_free - sum need
- * Outputs must not overlap cache_len, new_len, n_blocks or n_free (DSPARK_ERR_INVALID_ARG).
+ * What is written (block_table and the outputs) must not overlap an input or one another (DSPARK_ERR_INVALID_ARG).
  * free_pages is not written.  The same inputs give the same outputs bit for bit.
  * Device status DSPARK_ERR_CACHE: a negative length, n_blocks outside [0, max_blocks], n_free outside
  * [0, num_pages] (each is clamped), more pages needed than the stack or a table row holds (pages are given
@@ -414,8 +414,8 @@ dspark_status dspark_cache_plan(const dspark_cache_params* p, const int32_t* cac
  *   in order: free_pages[n_free], free_pages[n_free + 1], ...;  n_free_out = n_free + their number
  *   A negative entry names no page and is left out: a caller that gives a page back itself (one wholly before a
  *   sliding window) puts the page on the stack and -1 in the table.
- * block_table and n_blocks are dspark_cache_plan's; the table is not written.  cache_len_out,
- * n_blocks_out and n_free_out must not overlap the inputs.
+ * block_table and n_blocks are dspark_cache_plan's; the table is not written.  free_pages and the outputs must not
+ * overlap an input or one another.
  * Device status DSPARK_ERR_CACHE: a length that is negative or longer than the request's pages, n_blocks or
  * n_free out of range (each is clamped), an entry past the pool (left out), more pages than the stack has room for
  * (the rest is dropped).

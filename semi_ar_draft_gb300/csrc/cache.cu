@@ -473,9 +473,24 @@ cudaError_t launch_append(const AppendArgs& a, bool aligned, int blocks, cudaStr
                              blocks, kAppendThreads, 0, s, a);
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return a && b && x < y + nb && y < x + na;
+struct Span {
+    const void* at;
+    size_t bytes;
+};
+// Whether something that is written lies over anything else (reads may share).
+template <int W, int R>
+bool clash(const Span (&written)[W], const Span (&read)[R]) {
+    auto over = [](const Span& a, const Span& b) {
+        const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+        return a.at && b.at && x < y + b.bytes && y < x + a.bytes;
+    };
+    for (int i = 0; i < W; ++i) {
+        for (const Span& r : read)
+            if (over(written[i], r)) return true;
+        for (int o = 0; o < i; ++o)
+            if (over(written[i], written[o])) return true;
+    }
+    return false;
 }
 
 dspark_status check_cache_params(const dspark_cache_params* p) {
@@ -521,14 +536,12 @@ extern "C" dspark_status dspark_cache_plan(const dspark_cache_params* p, const i
         (!slots && p->max_tokens) || !n_blocks_out || !n_free_out)
         return DSPARK_ERR_INVALID_ARG;
     // Every block reads all of the inputs while the first one writes the outputs.
-    const size_t nb = sizeof(int32_t) * (size_t)p->B;
-    const void* ins[] = {cache_len, new_len, n_blocks, n_free};
-    const size_t in_bytes[] = {nb, nb, nb, sizeof(int32_t)};
-    const void* outs[] = {seq_len, offsets, n_blocks_out, n_free_out};
-    const size_t out_bytes[] = {nb, nb + sizeof(int32_t), nb, sizeof(int32_t)};
-    for (int i = 0; i < 4; ++i)
-        for (int o = 0; o < 4; ++o)
-            if (overlap(ins[i], in_bytes[i], outs[o], out_bytes[o])) return DSPARK_ERR_INVALID_ARG;
+    const size_t nb = sizeof(int32_t) * (size_t)p->B, nt = (size_t)p->max_tokens;
+    const Span ins[] = {{cache_len, nb}, {new_len, nb}, {n_blocks, nb}, {n_free, sizeof(int32_t)},
+                        {free_pages, sizeof(int32_t) * (size_t)p->num_pages}};
+    const Span outs[] = {{seq_len, nb}, {offsets, nb + sizeof(int32_t)}, {n_blocks_out, nb}, {n_free_out, sizeof(int32_t)},
+                         {slots, sizeof(int64_t) * nt}, {positions, sizeof(int32_t) * nt}, {block_table, nb * (size_t)p->max_blocks}};
+    if (clash(outs, ins)) return DSPARK_ERR_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < kHeaderBytes) return DSPARK_ERR_WORKSPACE;
     int sms = 0, per_sm = 0;
     if (device_sm_count(&sms) != cudaSuccess) return DSPARK_ERR_CUDA;
@@ -557,13 +570,11 @@ extern "C" dspark_status dspark_cache_commit(const dspark_cache_params* p, const
         !n_free_out)
         return DSPARK_ERR_INVALID_ARG;
     const size_t nb = sizeof(int32_t) * (size_t)p->B;
-    const void* ins[] = {cache_len, add_len, n_blocks, n_free, done};
-    const size_t in_bytes[] = {nb, nb, nb, sizeof(int32_t), (size_t)p->B};
-    const void* outs[] = {cache_len_out, n_blocks_out, n_free_out};
-    const size_t out_bytes[] = {nb, nb, sizeof(int32_t)};
-    for (int i = 0; i < 5; ++i)
-        for (int o = 0; o < 3; ++o)
-            if (overlap(ins[i], in_bytes[i], outs[o], out_bytes[o])) return DSPARK_ERR_INVALID_ARG;
+    const Span ins[] = {{cache_len, nb}, {add_len, nb}, {n_blocks, nb}, {n_free, sizeof(int32_t)}, {done, (size_t)p->B},
+                        {block_table, nb * (size_t)p->max_blocks}};
+    const Span outs[] = {{cache_len_out, nb}, {n_blocks_out, nb}, {n_free_out, sizeof(int32_t)},
+                         {free_pages, sizeof(int32_t) * (size_t)p->num_pages}};
+    if (clash(outs, ins)) return DSPARK_ERR_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < kHeaderBytes) return DSPARK_ERR_WORKSPACE;
     int sms = 0, per_sm = 0;
     if (device_sm_count(&sms) != cudaSuccess) return DSPARK_ERR_CUDA;

@@ -1,4 +1,5 @@
 """Refusals of the paged cache's Python side and of the decoding rounds, on the host (no GPU is touched)."""
+import ctypes as C
 
 import pytest
 import torch
@@ -32,3 +33,47 @@ def test_a_misaligned_error_word_is_refused():
     assert b.dspark_paged_attention_workspace_size(p) > 256
     p.error = 0x1001
     assert b.dspark_paged_attention_workspace_size(p) == 0
+
+
+A = [C.c_void_p(0x10000 * (i + 1)) for i in range(16)]  # addresses that nothing reads
+
+
+@pytest.fixture(scope="module")
+def L():
+    from semi_ar_draft_gb300 import build
+
+    build.build()
+    from semi_ar_draft_gb300 import binding
+
+    return binding.lib()
+
+
+def test_plan_and_commit_refuse_every_output_over_an_input(L):
+    """Blocks read cache_len, new_len, n_blocks, n_free, the stack and the table while others write the outputs."""
+    from semi_ar_draft_gb300 import binding as b
+
+    p = b.CacheParams(4, 16, 10, 5, 40, 1)
+    # cache_len, new_len, block_table, n_blocks, free_pages, n_free | seq_len, offsets, slots, positions, n_blocks, n_free
+    size = [16, 16, 80, 16, 40, 4, 16, 20, 320, 160, 16, 4]
+    for i in range(6):
+        for o in range(6, 12):
+            for at in (A[i].value, A[i].value + size[i] - 4, A[i].value - size[o] + 4):  # over it, at its end, at its beginning
+                args = list(A[:13])
+                args[o] = C.c_void_p(at)
+                assert L.dspark_cache_plan(C.byref(p), *args, 256, None) == 1, (i, o, at)
+    for a, o in ((2, 0), (2, 4), (2, 5), (2, 3), (2, 1)):  # the table is written too
+        args = list(A[:13])
+        args[a] = A[o]
+        assert L.dspark_cache_plan(C.byref(p), *args, 256, None) == 1, (a, o)
+    # cache_len, add_len, done, block_table, n_blocks, free_pages, n_free | cache_len, n_blocks, n_free
+    size = [16, 16, 4, 80, 16, 40, 4, 16, 16, 4]
+    for i in range(7):
+        for o in range(7, 10):
+            for at in (A[i].value, A[i].value + size[i] - 4, A[i].value - size[o] + 4):
+                args = list(A[:11])
+                args[o] = C.c_void_p(at)
+                assert L.dspark_cache_commit(C.byref(p), *args, 256, None) == 1, (i, o, at)
+    for i in (0, 1, 2, 3, 4, 6):  # the stack is written too
+        args = list(A[:11])
+        args[5] = A[i]
+        assert L.dspark_cache_commit(C.byref(p), *args, 256, None) == 1, i
