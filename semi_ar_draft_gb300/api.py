@@ -146,10 +146,11 @@ def _raw(stream, *made):
     """The stream's address.  Tensors made here for a call on a stream of its own stay reserved for it."""
     if stream is None:
         return None
-    if isinstance(stream, torch.cuda.Stream):
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
+    kept = [t for t in made if t is not None]
+    if kept:
+        on = b.torch_stream(stream)
+        for t in kept:
+            t.record_stream(on)
     return b._stream(stream)
 
 

@@ -150,3 +150,26 @@ def test_the_error_word_of_the_calls():
         api.cache_plan(*args(3), error=torch.zeros(1, device="cuda"))
     with pytest.raises(ValueError):
         api.cache_commit(i32([9]), None, i32([[0, -1]]), i32([1]), i32([1, 2, 3, 0]), i32([3]), 4, error=i32([0, 0]))
+
+
+# ------------------------------------------------------------------ streams
+def test_tensors_made_for_a_stream_given_by_its_address_stay_reserved():
+    """Memory of an output that is let go while its stream still works is not handed out to the current stream."""
+    cache = PagedCache(1, 64, 16, 64, 1, 1, 64, 512)
+    cache.plan(i32([512]))
+    q = torch.zeros((512, 8, 64), dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)  # cycles: a tenth of a second of work before the call
+        out, _, ws = api.paged_attention(q, cache.k_pages[0], cache.v_pages[0], cache.block_table, cache.seq_len, cache.offsets,
+                                         stream=stream)
+        at, n, size = out.data_ptr(), out.numel(), ws.numel()
+        del out, ws
+        assert not side.query()
+        made = [torch.empty(n, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+        made += [torch.empty(size, dtype=torch.uint8, device="cuda")]
+        assert at not in [x.data_ptr() for x in made]
+        del made
+    torch.cuda.synchronize()
