@@ -7,10 +7,12 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
+#include <initializer_list>
 
 #include "dspark.h"
 
@@ -32,6 +34,18 @@ const at::Tensor& needed(PyObject* o) {
     const at::Tensor* t = tensor(o);
     if (!t) refuse(PyExc_TypeError, "expected a torch tensor, got None");
     return *t;
+}
+
+// All of a call's tensors on one device, and that the current one: it is where the library launches.
+void one_device(std::initializer_list<const at::Tensor*> tensors) {
+    const at::Tensor* first = nullptr;
+    for (const at::Tensor* t : tensors) {
+        if (!t) continue;
+        if (!first) first = t;
+        if (t->device() != first->device()) refuse(PyExc_ValueError, "the tensors of a call are on one device");
+    }
+    if (first && first->is_cuda() && first->device().index() != c10::cuda::current_device())
+        refuse(PyExc_ValueError, "the tensors are on another device than the current one");
 }
 
 void* address(const at::Tensor* t) {
@@ -153,6 +167,8 @@ PyObject* cache_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
                          &n_free = needed(a[5]), &seq = needed(a[9]), &off = needed(a[10]), &slots = needed(a[11]),
                          &n_blocks_out = needed(a[13]), &n_free_out = needed(a[14]), &ws = needed(a[15]);
         const at::Tensor *new_len = tensor(a[1]), *positions = tensor(a[12]);
+        one_device({&cache_len, new_len, &table, &n_blocks, &free_pages, &n_free, &seq, &off, &slots, positions, &n_blocks_out,
+                    &n_free_out, &ws, tensor(a[17])});
         const dspark_cache_params p = cache_params(cache_len, table, n_blocks, free_pages, n_free, a[6], small(a[7]), a[8], a[17]);
         want(new_len, at::kInt, p.B, "new_len is int32 [B]");
         want(&seq, at::kInt, p.B, "seq_len is int32 [B]");
@@ -179,6 +195,8 @@ PyObject* cache_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
                          &n_free = needed(a[6]), &len_out = needed(a[9]), &n_blocks_out = needed(a[10]),
                          &n_free_out = needed(a[11]), &ws = needed(a[12]);
         const at::Tensor *add_len = tensor(a[1]), *done = tensor(a[2]);
+        one_device({&cache_len, add_len, done, &table, &n_blocks, &free_pages, &n_free, &len_out, &n_blocks_out, &n_free_out, &ws,
+                    tensor(a[14])});
         const dspark_cache_params p = cache_params(cache_len, table, n_blocks, free_pages, n_free, a[7], 0, a[8], a[14]);
         want(add_len, at::kInt, p.B, "add_len is int32 [B]");
         if (done && ((done->scalar_type() != at::kByte && done->scalar_type() != at::kBool) || done->numel() != p.B))
@@ -200,6 +218,7 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         count_args(n, 8);
         const at::Tensor &k = needed(a[0]), &v = needed(a[1]), &kp = needed(a[2]), &vp = needed(a[3]), &slots = needed(a[4]);
         const at::Tensor *ks = tensor(a[5]), *vs = tensor(a[6]);
+        one_device({&k, &v, &kp, &vp, &slots, ks, vs});
         const Pools x = pools_of(kp, vp);
         if (k.dim() != 3 || v.sizes() != k.sizes() || k.size(1) != x.Hk || k.size(2) != x.D ||
             k.scalar_type() != v.scalar_type())
@@ -223,6 +242,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor &q = needed(a[0]), &kp = needed(a[1]), &vp = needed(a[2]), &table = needed(a[3]), &seq = needed(a[4]),
                          &out = needed(a[13]);
         const at::Tensor *off = tensor(a[5]), *ks = tensor(a[6]), *vs = tensor(a[7]), *lse = tensor(a[14]);
+        one_device({&q, &kp, &vp, &table, &seq, off, ks, vs, &out, lse, tensor(a[15]), tensor(a[17])});
         const Pools x = pools_of(kp, vp);
         if (q.dim() != 3 || q.size(2) != x.D) refuse(PyExc_ValueError, "q is [T, Hq, D]");
         const int64_t T = q.size(0), B = seq.numel();

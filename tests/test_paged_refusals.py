@@ -77,3 +77,22 @@ def test_plan_and_commit_refuse_every_output_over_an_input(L):
         args = list(A[:11])
         args[5] = A[i]
         assert L.dspark_cache_commit(C.byref(p), *args, 256, None) == 1, i
+
+
+def test_tensors_of_two_devices_are_refused():
+    """Told apart before anything else is looked at (here: host memory beside tensors without memory)."""
+    from semi_ar_draft_gb300 import api
+
+    i = lambda *s, device="cpu": torch.zeros(s, dtype=torch.int32, device=device)  # noqa: E731
+    z = lambda *s, device="cpu": torch.zeros(s, dtype=torch.bfloat16, device=device)  # noqa: E731
+    ws = torch.zeros(256, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="one device"):
+        api.cache_plan(i(4), i(4, device="meta"), i(4, 2), i(4), i(9), i(1), 16, 10, ws=ws)
+    with pytest.raises(ValueError, match="one device"):
+        api.cache_commit(i(4), i(4), i(4, 2), i(4), i(9, device="meta"), i(1), 16, ws=ws)
+    with pytest.raises(ValueError, match="one device"):
+        api.cache_append(z(4, 2, 64), z(4, 2, 64), z(5, 16, 2, 64), z(5, 16, 2, 64), torch.zeros(4, dtype=torch.int64, device="meta"))
+    with pytest.raises(ValueError, match="one device"):
+        api.paged_attention(z(4, 4, 64), z(5, 16, 2, 64), z(5, 16, 2, 64, device="meta"), i(4, 3), i(4))
+    with pytest.raises(ValueError, match="device tensors"):
+        api.paged_attention(z(4, 4, 64), z(5, 16, 2, 64), z(5, 16, 2, 64), i(4, 3), i(4), ws=ws)
