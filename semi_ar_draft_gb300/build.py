@@ -23,7 +23,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(NATIVE):
         return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "dspark.h")]
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "dspark.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -82,8 +82,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         for _, err in results:
             print(err)
     tmp = LIB + f".tmp{os.getpid()}"
+    # (with a name of its own, so that _native.so asks for it by that and finds it beside itself, wherever the tree is)
     subprocess.check_call([NVCC, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", "-cudart", "shared",
-                           "-o", tmp, *[o for o, _ in results]])
+                           "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp, *[o for o, _ in results]])
     os.replace(tmp, LIB)
     _link_native(native_obj)
     return LIB

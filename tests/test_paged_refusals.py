@@ -1,5 +1,9 @@
 """Refusals of the paged cache's Python side and of the decoding rounds, on the host (no GPU is touched)."""
 import ctypes as C
+import os
+import shutil
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -96,3 +100,19 @@ def test_tensors_of_two_devices_are_refused():
         api.paged_attention(z(4, 4, 64), z(5, 16, 2, 64), z(5, 16, 2, 64, device="meta"), i(4, 3), i(4))
     with pytest.raises(ValueError, match="device tensors"):
         api.paged_attention(z(4, 4, 64), z(5, 16, 2, 64), z(5, 16, 2, 64), i(4, 3), i(4), ws=ws)
+
+
+def test_a_built_package_works_where_it_is_moved(L, tmp_path):
+    """The native module finds the library beside it, and both loaders map the same one file."""
+    from semi_ar_draft_gb300 import binding as b
+
+    src = os.path.dirname(os.path.abspath(b.__file__))
+    dst = tmp_path / "moved" / "semi_ar_draft_gb300"
+    shutil.copytree(src, dst, ignore=shutil.ignore_patterns("__pycache__", "_build", "csrc"))
+    code = ("from semi_ar_draft_gb300 import binding as b; b.native(); "
+            "print('MAPS', sorted({l.split()[-1] for l in open('/proc/self/maps') if 'libdspark' in l or '_native.so' in l}))")
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path / "moved", capture_output=True, text=True,
+                       env={**os.environ, "PYTHONPATH": str(tmp_path / "moved")})
+    assert r.returncode == 0, r.stderr[-2000:]
+    want = sorted(str(dst.resolve() / f) for f in ("libdspark.so", "_native.so"))
+    assert f"MAPS {want}" in r.stdout, r.stdout
