@@ -35,7 +35,7 @@ class PagedCache:
                  kv_dtype=None, k_scale=None, v_scale=None, device="cuda"):
         i32 = {"dtype": torch.int32, "device": device}
         shape = (layers, num_pages, page_size, Hk, D)
-        self.k_pages = torch.zeros(shape, dtype=dtype, device=device).to(kv_dtype or dtype)
+        self.k_pages = torch.zeros(shape, dtype=kv_dtype or dtype, device=device)
         self.v_pages = torch.zeros_like(self.k_pages)
         if kv_dtype == torch.float8_e4m3fn:
             ones = torch.ones((layers, Hk), device=device)

@@ -173,3 +173,15 @@ def test_tensors_made_for_a_stream_given_by_its_address_stay_reserved():
         assert at not in [x.data_ptr() for x in made]
         del made
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ memory and steps
+def test_an_8_bit_cache_is_built_without_a_wider_copy():
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    cache = PagedCache(4, 4096, 64, 64, 1, 4, 128, 64, kv_dtype=E4M3)
+    pools = cache.k_pages.nbytes + cache.v_pages.nbytes
+    assert pools == 2 * 4096 * 64 * 4 * 128 and not cache.k_pages.view(torch.uint8).any()
+    assert torch.cuda.max_memory_allocated() - before <= pools + (4 << 20)
