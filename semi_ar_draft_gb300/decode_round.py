@@ -75,12 +75,13 @@ def generate(target, draft, prompts, rounds, T=0.0, budget=None, page_size=16, k
     rows = torch.arange(most, device=dev)
 
     def flat(table):  # table [B, width]: the planned tokens' values, request by request
-        j = torch.searchsorted(cache.offsets[1:], rows, right=True).clamp(max=B - 1)
-        i = (rows - cache.offsets[j]).clamp(0, table.shape[1] - 1)
+        t = rows[: len(cache.slots)]
+        j = torch.searchsorted(cache.offsets[1:], t, right=True).clamp(max=B - 1)
+        i = (t - cache.offsets[j]).clamp(0, table.shape[1] - 1)
         return table[j, i].long()
 
     # the prompts, whose last position gives the first token
-    cache.plan(None, extra=n, max_new=n)
+    cache.plan(None, extra=n, max_new=n, tokens=B * n)
     logits = target.forward(flat(prompts), cache.positions, cache)
     anchor = logits[(cache.offsets[1:] - 1).long()].argmax(-1).int()
     cache.commit(None, extra=n)
@@ -90,7 +91,7 @@ def generate(target, draft, prompts, rounds, T=0.0, budget=None, page_size=16, k
         base, conf = draft.block(B)
         tok, lse, zat, _ = api.markov_sample_block(base, draft.W1, draft.W2, anchor, T, seed + r)
         L, _, _, _ = api.schedule_verify_len(conf, budget)
-        cache.plan(L, extra=1, max_new=gamma + 1)
+        cache.plan(L, extra=1, max_new=gamma + 1, tokens=budget + B)
         logits = target.forward(flat(torch.cat([anchor[:, None], tok], 1)), cache.positions, cache)
         # draft logits are bf16, so the target's are rounded to it for the verification
         n_acc, corr, _ = api.verify(base, draft.W1, draft.W2, anchor, tok, lse, zat, logits.to(base.dtype), T, seed + r,

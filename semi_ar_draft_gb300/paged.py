@@ -28,7 +28,7 @@ def _on(stream):
 
 class PagedCache:
     """requests slots of at most max_blocks pages each; num_pages pages of page_size tokens in all; max_tokens:
-    the most new tokens of a step.  kv_dtype: dtype or torch.float8_e4m3fn, then with k_scale, v_scale
+    the most new tokens of any step (a step may say that it has fewer: plan's tokens).  kv_dtype: dtype or torch.float8_e4m3fn, then with k_scale, v_scale
     [layers, Hk] fp32 (ones if not given)."""
 
     def __init__(self, requests, num_pages, page_size, max_blocks, layers, Hk, D, max_tokens, dtype=torch.bfloat16,
@@ -51,8 +51,9 @@ class PagedCache:
                                                ((0, requests), (requests, 2 * requests), (2 * requests, 2 * requests + 1)))
         self._free[0].fill_(num_pages)
         self.seq_len, self.offsets = torch.empty(requests, **i32), torch.empty(requests + 1, **i32)
-        self.slots = torch.empty(max_tokens, dtype=torch.int64, device=device)
-        self.positions = torch.empty(max_tokens, **i32)
+        self._slots = torch.empty(max_tokens, dtype=torch.int64, device=device)
+        self._positions = torch.empty(max_tokens, **i32)
+        self.slots, self.positions = self._slots, self._positions
         self.ws = torch.zeros(256, dtype=torch.uint8, device=device)
         self._error = torch.zeros(1, **i32)  # the first device error since status() was last called
         self.max_new = 0
@@ -66,22 +67,29 @@ class PagedCache:
     def n_free(self):
         return self._free[0]
 
-    def plan(self, new_len=None, extra=0, max_new=0, stream=None):
+    def plan(self, new_len=None, extra=0, max_new=0, stream=None, tokens=None):
         """Pages and slots for new_len[j] + extra tokens of each request.  Sets seq_len, offsets, slots, positions.
-        max_new: the most new tokens of one request, if known (it chooses attend's kernel)."""
+        tokens: the most new tokens of this step, max_tokens if not given: the rows of slots, positions and of what
+        append and attend take until the next plan (few rows a step are then few rows to copy, and attend's choice
+        of kernel goes by their mean).  max_new: the most new tokens of one request, if known (for that choice too)."""
+        if tokens is None:
+            tokens = self.max_tokens
+        if not 0 <= tokens <= self.max_tokens:
+            raise ValueError(f"a step of {tokens} tokens; the cache was made for {self.max_tokens}")
+        self.slots, self.positions = self._slots[:tokens], self._positions[:tokens]
         api.cache_plan(self._len[0], new_len, self.block_table, self._blocks[0], self.free_pages, self._free[0],
-                       self.page_size, self.max_tokens, extra=extra, ws=self.ws, stream=stream, error=self._error,
+                       self.page_size, tokens, extra=extra, ws=self.ws, stream=stream, error=self._error,
                        out=(self.seq_len, self.offsets, self.slots, self.positions, self._blocks[1], self._free[1]))
         self._keep(len(self._len[0]), stream)
         self.max_new = max_new
 
     def append(self, layer, k, v, stream=None):
-        """k, v [max_tokens, Hk, D]: rows past offsets[-1] have no slot and are skipped."""
+        """k, v [the plan's tokens, Hk, D]: rows past offsets[-1] have no slot and are skipped."""
         api.cache_append(k, v, self.k_pages[layer], self.v_pages[layer], self.slots, self.k_scale[layer], self.v_scale[layer],
                          stream)
 
     def attend(self, layer, q, stream=None, **kw):
-        """q [max_tokens, Hq, D]; kw as for api.paged_attention.  Returns (out, lse or None)."""
+        """q [the plan's tokens, Hq, D]; kw as for api.paged_attention.  Returns (out, lse or None)."""
         out, lse, _ = api.paged_attention(q, self.k_pages[layer], self.v_pages[layer], self.block_table, self.seq_len,
                                           self.offsets, k_scale=self.k_scale[layer], v_scale=self.v_scale[layer],
                                           max_new=self.max_new, stream=stream, error=self._error, **kw)

@@ -185,3 +185,31 @@ def test_an_8_bit_cache_is_built_without_a_wider_copy():
     pools = cache.k_pages.nbytes + cache.v_pages.nbytes
     assert pools == 2 * 4096 * 64 * 4 * 128 and not cache.k_pages.view(torch.uint8).any()
     assert torch.cuda.max_memory_allocated() - before <= pools + (4 << 20)
+
+
+@pytest.mark.parametrize("kv", [None, E4M3])
+def test_steps_of_different_token_counts(kv):
+    """Prompts and decoding steps through one cache: a step's tensors have its own number of rows."""
+    B, D, Hk, Hq = 3, 64, 2, 8
+    g = torch.Generator(device="cuda").manual_seed(2)
+    small, full = (PagedCache(B, 60, 16, 20, 1, Hk, D, 300, kv_dtype=kv) for _ in range(2))
+    for new, tokens in (([100, 9, 120], 240), ([1, 1, 1], 3), ([4, 2, 1], 10)):
+        n = i32(new)
+        small.plan(n, tokens=tokens)
+        full.plan(n)
+        assert small.slots.numel() == small.positions.numel() == tokens and full.slots.numel() == 300
+        assert torch.equal(full.slots[:tokens], small.slots) and torch.equal(full.positions[:tokens], small.positions)
+        q, k, v = (torch.randn((300, h, D), generator=g, device="cuda").to(torch.bfloat16) for h in (Hq, Hk, Hk))
+        for c, T in ((small, tokens), (full, 300)):
+            c.append(0, k[:T], v[:T])
+        (out, _), (ref, _) = small.attend(0, q[:tokens]), full.attend(0, q)
+        # (the same keys and values; which kernel runs may differ, so a rounding of p and of the output either way)
+        assert bool(((out - ref[:tokens]).abs() <= 2.0 ** -7 * (ref[:tokens].abs() + 4)).all())
+        small.commit(n)
+        full.commit(n)
+    assert torch.equal(small.k_pages.view(torch.uint8), full.k_pages.view(torch.uint8))
+    assert small.status() == 0 and full.status() == 0
+    small.plan(i32([5, 5, 5]), tokens=12)  # fewer than there are: an error, as with max_tokens
+    assert small.status() == 8
+    with pytest.raises(ValueError):
+        small.plan(i32([1, 1, 1]), tokens=301)
