@@ -325,16 +325,6 @@ def _rows_ptr(t):
     return t.data_ptr()
 
 
-def pool_layout(k_pages, v_pages):
-    """(pages, page_size, Hk, D, page / token / head stride) of two pools [pages, page_size, Hk, D]."""
-    shape, stride = k_pages.shape, k_pages.stride()
-    if len(shape) != 4 or v_pages.shape != shape or v_pages.stride() != stride:
-        raise ValueError("k_pages and v_pages are [pages, page_size, Hk, D] of one shape and layout")
-    if k_pages.dtype is not v_pages.dtype:
-        raise TypeError("k_pages and v_pages are of one type")
-    return (*shape, stride[0], stride[1], stride[2])
-
-
 def dspark_cache_workspace_size(p: CacheParams) -> int:
     return int(lib().dspark_cache_workspace_size(C.byref(p)))
 
