@@ -266,7 +266,8 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         p.max_new = small(a[12]);
         p.dtype = type_code(q.scalar_type());
         p.kv_dtype = type_code(kp.scalar_type());
-        p.causal = PyObject_IsTrue(a[10]) == 1;
+        p.causal = PyObject_IsTrue(a[10]);
+        if (p.causal < 0) throw Refused{};
         p.window = small(a[11]);
         p.scale = real(a[8]);
         p.softcap = real(a[9]);

@@ -116,3 +116,18 @@ def test_a_built_package_works_where_it_is_moved(L, tmp_path):
     assert r.returncode == 0, r.stderr[-2000:]
     want = sorted(str(dst.resolve() / f) for f in ("libdspark.so", "_native.so"))
     assert f"MAPS {want}" in r.stdout, r.stdout
+
+
+def test_an_argument_without_a_truth_value_says_so():
+    """The error of `causal`'s own truth value comes through, and no result beside it."""
+    from semi_ar_draft_gb300 import api
+
+    class Neither:
+        def __bool__(self):
+            raise ArithmeticError("neither")
+
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    with pytest.raises(ArithmeticError, match="neither"):
+        api.paged_attention(z(4, 4, 64), z(5, 16, 2, 64), z(5, 16, 2, 64), i(4, 3), i(4), causal=Neither(),
+                            ws=torch.zeros(256, dtype=torch.uint8))
