@@ -456,6 +456,7 @@ dspark_status dspark_cache_append(const dspark_append_params* p, const void* k, 
  *   over the keys l < seq_len[j], if causal l <= pos, with a window w > 0 also l > pos - w:
  *   out = sum_l e^(s_l - lse) v_l,   lse = ln sum_l e^(s_l)
  * A row that sees no key gets out = 0 and lse = -inf, as does every row of q from offsets[B] on.
+ * Rows before offsets[0] are not written.
  * causal = 1, n_j = 1 is a decoding step; causal = 1, n_j = 1 + L_j the flattened verify; causal = 0 a
  * draft block, whose positions all see the context and each other (P1, the block attention mask).
  * Arguments

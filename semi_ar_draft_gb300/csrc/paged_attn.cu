@@ -12,7 +12,7 @@
 // between warps; the page numbers of a slice are fetched a step before its copies are issued.  The warps'
 // statistics and outputs meet once per segment, in the stages just consumed (a stage is as large as a warp's
 // output: 64 D bytes).  Two blocks a multiprocessor or more, so that one streams while another joins.
-// Measured: 32 requests of up to 8192 tokens, 8 kv heads of 128, bf16: 94 us = 6.0 TB/s (0.89 of the measured copy
+// Measured: 32 requests of up to 8192 tokens, 8 kv heads of 128, bf16: 95 us = 5.9 TB/s (0.87 of the measured copy
 // rate), of which 5 us are the join; 128 requests over an e4m3 cache 209 us = 5.4 TB/s (0.79), where the
 // conversions keep the issue slots busy; one request of 1024 tokens 12 us, latency.
 #include <cuda_fp16.h>
@@ -70,8 +70,8 @@ template <bool F8, int DP>
 struct Rows16 {
     static constexpr int kEsz = F8 ? 1 : 2;
     static constexpr int kKeys = F8 ? 32 : 16;           // keys of a warp's slice
-    // (heads of 256, one block a multiprocessor: six warps of two stages, 140 us for 16 kv heads of 192 over 32
-    // requests, against 174 us with four of three)
+    // (heads of 256, one block a multiprocessor: six warps of two stages, 204 us for 16 kv heads of 192 over 32
+    // requests of up to 5625 tokens, against 244 us with four of three)
     static constexpr int kWarps = DP == 256 ? 6 : 4;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kKeyTile = kWarps * kKeys;      // keys of a unit
@@ -79,9 +79,10 @@ struct Rows16 {
     static constexpr int kChunks = kRowBytes / 16;       // 16-byte groups of a row
     static constexpr int kHalf = kKeys * kRowBytes;      // K (or V) of a slice
     static constexpr int kStage = 2 * kHalf;             // = 64 DP: also a warp's output in fp32
-    // Blocks a multiprocessor and stages a warp, measured: 16-bit heads of 128 want two blocks of three (98
-    // us for 32 requests up to 8192 tokens, 102 us with three of two); heads of 64, and 8-bit ones of 128, which
-    // are bound by their conversions, three blocks (62 against 74 us; 221 against 238 us).
+    // Blocks a multiprocessor and stages a warp, measured: 16-bit heads of 128 want two blocks of three (95
+    // us for 32 requests up to 8192 tokens, 97 us with three of two); heads of 64 three of four (60 us for the same
+    // requests, 66 with two of four); 8-bit heads of 128, bound by their conversions, three of two (208 us for 128
+    // requests up to 8000 tokens, 210 with two of three).
     static constexpr bool kThree = DP == 64 || (F8 && DP == 128);
     static constexpr int kStages = DP == 64 ? 4 : (kThree || DP == 256 ? 2 : 3);
     static constexpr int kExtra = DP == 64 ? 4 : 2;      // what an item costs beside its key tiles
@@ -697,9 +698,9 @@ struct AttnWs {
 };
 // Whether a call takes row tiles of 128: when a request has more rows a kv head than the limit, on average
 // (T / B tokens) and at most (max_new, if given).  Measured, tiles of 16 against tiles of 128, us:
-//   16-bit   mean 11 rows 117 / 116 (long contexts) and 63 / 87 (short); mean 14: 130 / 111 and 71 / 86;
-//            mean 24: 88 / 69; heads of 256, mean 11: 214 / 249, mean 24: 159 / 135
-//   e4m3     mean 35 rows 72 / 88 and 37 / 43; 68 rows: 80 / 53; mean 70: 166 / 102; 119 rows: 267 / 93
+//   16-bit   mean 11 rows 117 / 115 (long contexts) and 63 / 84 (short); mean 14: 130 / 109 and 71 / 83;
+//            mean 24: 88 / 67; heads of 256, mean 11: 214 / 255, mean 24: 159 / 139
+//   e4m3     mean 35 rows 69 / 85 and 36 / 42; 68 rows: 80 / 58; mean 70: 159 / 101; 119 rows: 254 / 92
 // (an 8-bit tile has to be widened for the wide kernel, so it needs more rows to pay).
 bool wide_rows(const dspark_attention_params* p) {
     const long long G = p->Hq / p->Hk, limit = p->kv_dtype == p->dtype ? kRows : 48;

@@ -20,10 +20,10 @@
 //
 // Bound by the cache's bytes where a unit's softmax (about 2000 cycles for a stream's tile of 64 keys) is
 // shorter than its loads: 512 requests of up to 4096 tokens, 8 query heads of 128 a kv head, 5 new tokens on
-// average: 419 us = 6.0 TB/s (0.88 of the measured copy rate).  With heads of 64 a tile is half the bytes and the
-// softmax decides: 32 draft blocks of 16 over up to 4100 tokens 52 us = 2.9 TB/s (0.42).
-// Over an 8-bit cache the loaders' widening decides at few rows (32 requests, 35 rows on average: 88 us, of row
-// tiles of 16: 72) and pays at many (145 requests, 119 rows of 192 over 200 keys: 93 us against 267).
+// average: 417 us = 6.0 TB/s (0.88 of the measured copy rate).  With heads of 64 a tile is half the bytes and the
+// softmax decides: 32 draft blocks of 16 over up to 4100 tokens 52.5 us = 2.8 TB/s (0.42).
+// Over an 8-bit cache the loaders' widening decides at few rows (32 requests, 35 rows on average: 85 us, of row
+// tiles of 16: 69) and pays at many (145 requests, 119 rows of 192 over 200 keys: 92 us against 254).
 #include "host_util.h"
 #include "paged.cuh"
 #include "pdl.cuh"
