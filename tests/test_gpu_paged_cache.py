@@ -62,11 +62,12 @@ def test_rounds_replay_from_a_graph(calls):
     assert eager.status() == 0 and replayed.status() == 0 and int(eager.cache_len.max()) > 8
 
 
-def test_finished_requests_replay_from_a_graph():
+@pytest.mark.parametrize("times", [1, 60])  # the commit's kernel in one block; in a cluster of three
+def test_finished_requests_replay_from_a_graph(times):
     """A graph of a commit alone."""
-    cache = PagedCache(3, 12, 4, 4, 1, 1, 64, 24)
-    done = torch.ones(3, dtype=torch.uint8, device="cuda")
-    new = i32([5, 1, 8])
+    cache = PagedCache(3 * times, 12 * times, 4, 4, 1, 1, 64, 24 * times)
+    done = torch.ones(3 * times, dtype=torch.uint8, device="cuda")
+    new = i32([5, 1, 8] * times)
     cache.plan(new)
     cache.commit(new)
     graph = torch.cuda.CUDAGraph()
@@ -75,10 +76,11 @@ def test_finished_requests_replay_from_a_graph():
         cache.commit(done=done)
     for _ in range(3):
         graph.replay()
-        assert int(cache.n_free) == 12 and cache.cache_len.tolist() == [0, 0, 0]
+        assert int(cache.n_free) == 12 * times and cache.cache_len.tolist() == [0, 0, 0] * times
+        assert cache.free_pages.unique().numel() == 12 * times
         cache.plan(new)
         cache.commit(new)
-        assert int(cache.n_free) == 12 - 5 and cache.cache_len.tolist() == [5, 1, 8]
+        assert int(cache.n_free) == (12 - 5) * times and cache.cache_len.tolist() == [5, 1, 8] * times
 
 
 def test_counts_are_read_through_the_same_tensors():
@@ -159,10 +161,11 @@ def test_tensors_made_for_a_stream_given_by_its_address_stay_reserved():
     cache.plan(i32([512]))
     q = torch.zeros((512, 8, 64), dtype=torch.bfloat16, device="cuda")
     side = torch.cuda.Stream()
+    api.paged_attention(q, cache.k_pages[0], cache.v_pages[0], cache.block_table, cache.seq_len, cache.offsets)  # loads the kernels
     for stream in (side, side.cuda_stream):
         torch.cuda.synchronize()
         with torch.cuda.stream(side):
-            torch.cuda._sleep(200_000_000)  # cycles: a tenth of a second of work before the call
+            torch.cuda._sleep(600_000_000)  # cycles: a third of a second of work before the call
         out, _, ws = api.paged_attention(q, cache.k_pages[0], cache.v_pages[0], cache.block_table, cache.seq_len, cache.offsets,
                                          stream=stream)
         at, n, size = out.data_ptr(), out.numel(), ws.numel()
