@@ -396,6 +396,7 @@ typedef struct {
     int max_tokens; /* entries of slots and positions (dspark_cache_plan) */
     int extra;      /* tokens a request feeds or keeps beyond its new_len / add_len (>= 0) */
     int32_t* error; /* device word or NULL: see below */
+    int32_t* settled; /* dspark_cache_commit: [2 B + 1] or NULL, see there */
 } dspark_cache_params;
 
 size_t dspark_cache_workspace_size(const dspark_cache_params* p);
@@ -414,6 +415,9 @@ dspark_status dspark_cache_plan(const dspark_cache_params* p, const int32_t* cac
  *   in order: free_pages[n_free], free_pages[n_free + 1], ...;  n_free_out = n_free + their number
  *   A negative entry names no page and is left out: a caller that gives a page back itself (one wholly before a
  *   sliding window) puts the page on the stack and -1 in the table.
+ *   settled (where not NULL) gets cache_len_out, n_blocks_out and n_free_out once more, one after the other.  It may lie
+ *   over cache_len, n_blocks and n_free themselves, which every block has read by then: the next step then reads where
+ *   this one did, as a step replayed from a graph has to.
  * block_table and n_blocks are dspark_cache_plan's; the table is not written.  free_pages and the outputs must not
  * overlap an input or one another.
  * Device status DSPARK_ERR_CACHE: a length that is negative or longer than the request's pages, n_blocks or

@@ -178,18 +178,19 @@ def cache_plan(cache_len, new_len, block_table, n_blocks, free_pages, n_free, pa
 
 
 def cache_commit(cache_len, add_len, block_table, n_blocks, free_pages, n_free, page_size, extra=0, done=None, out=None,
-                 ws=None, stream=None, error=None):
+                 ws=None, stream=None, error=None, settled=None):
     """The requests' lengths after the verification, and the pages past them back on the stack
     (dspark_cache_commit): add_len [B] int32 (n_accepted) or None, done [B] uint8 or bool, or None; free_pages is
     written in place.  Returns (cache_len [B], n_blocks [B], n_free [1], workspace), new tensors.  error as for
-    cache_plan."""
+    cache_plan.  settled [2 B + 1] int32, or None: gets the three once more, and may hold the inputs cache_len, n_blocks
+    and n_free themselves."""
     made = ()
     if out is None:
         B, i32 = cache_len.numel(), {"dtype": torch.int32, "device": cache_len.device}
         made = out = (torch.empty(B, **i32), torch.empty(B, **i32), torch.empty(1, **i32))
     ws = _cache_ws(ws, cache_len)
     st = b.native().cache_commit(cache_len, add_len, done, block_table, n_blocks, free_pages, n_free, page_size, extra, *out, ws,
-                                 _raw(stream, ws, *made), error)
+                                 _raw(stream, ws, *made), error, settled)
     b._check(st, "dspark_cache_commit")
     return (*out, ws)
 

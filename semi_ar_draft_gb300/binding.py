@@ -40,7 +40,7 @@ class SampleParams(C.Structure):
 
 class CacheParams(C.Structure):
     _fields_ = [("B", C.c_int), ("page_size", C.c_int), ("num_pages", C.c_int), ("max_blocks", C.c_int),
-                ("max_tokens", C.c_int), ("extra", C.c_int), ("error", C.c_void_p)]
+                ("max_tokens", C.c_int), ("extra", C.c_int), ("error", C.c_void_p), ("settled", C.c_void_p)]
 
 
 class AppendParams(C.Structure):

@@ -7,7 +7,7 @@
 // from L2) and keeps it in shared memory, so that tokens and pages can be dealt out over any number
 // of blocks with no second launch and no grid-wide wait.  Both are bound by the latency of one launch
 // with three dependent rounds of memory (lengths, stack or table, result), not by their bytes: 3.4 us for a
-// step of 32 requests, 5.8 us for the 200000 tokens of 48 prompts, 5.9 us to take back the pages of 50 finished
+// step of 32 requests, 5.8 us for the 200000 tokens of 48 prompts, 6.1 us to take back the pages of 50 finished
 // requests of 512.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
@@ -211,7 +211,8 @@ struct CommitArgs {
     int32_t* n_blocks_out;
     int32_t* n_free_out;
     int32_t* status;
-    int32_t* error;  // or null
+    int32_t* error;    // or null
+    int32_t* settled;  // or null; may be cache_len, n_blocks and n_free
 };
 
 struct CommitReq {
@@ -238,8 +239,8 @@ __device__ __forceinline__ CommitReq commit_request(const CommitArgs& a, int j) 
 // given back before (a sliding window) has entries that name none, so where a page goes depends on all entries
 // before it: the warps count theirs, the blocks of the cluster (eight at most) send each other their counts, and
 // each warp writes its own, from registers where its run is kHeldSteps steps at most (32768 entries over eight blocks).
-// Measured: 32 requests, few pages: 3.3 us, one block and no cluster; 512 requests of up to 500 pages, a tenth of them
-// finished: 5.9 us, of which the exchange takes 1.
+// Measured: 32 requests, few pages: 3.5 us, one block and no cluster; 512 requests of up to 500 pages, a tenth of them
+// finished: 6.1 us, of which the exchange takes 1.
 constexpr int kCommitBlocks = 8;
 constexpr int kHeldSteps = 8;
 template <bool ALONE>  // one block, without a cluster
@@ -327,6 +328,14 @@ __global__ void __launch_bounds__(kPlanThreads) cache_commit_kernel(CommitArgs a
     }
     const int room = a.num_pages - n_free;
     any_bad |= total > room;
+    // Every block has read its inputs: settled may lie over them.
+    if (first && a.settled) {
+        for (int j = j0; j < j1; ++j) {
+            a.settled[j] = a.cache_len_out[j];  // (written by this thread)
+            a.settled[a.B + j] = keep[j];
+        }
+        if (tid == 0) a.settled[2 * a.B] = n_free + min(total, room);
+    }
     if (first && tid == 0) {
         *a.n_free_out = n_free + min(total, room);
         *a.status = any_bad ? DSPARK_ERR_CACHE : DSPARK_OK;
@@ -495,7 +504,7 @@ bool clash(const Span (&written)[W], const Span (&read)[R]) {
 
 dspark_status check_cache_params(const dspark_cache_params* p) {
     if (!p || p->B < 1 || p->num_pages < 1 || p->max_blocks < 1 || page_shift_of(p->page_size) < 0 ||
-        ((uintptr_t)p->error & 3u))
+        (((uintptr_t)p->error | (uintptr_t)p->settled) & 3u))
         return DSPARK_ERR_INVALID_ARG;
     if (p->B > kMaxRequests) return DSPARK_ERR_UNSUPPORTED;
     return DSPARK_OK;
@@ -574,7 +583,8 @@ extern "C" dspark_status dspark_cache_commit(const dspark_cache_params* p, const
                         {block_table, nb * (size_t)p->max_blocks}};
     const Span outs[] = {{cache_len_out, nb}, {n_blocks_out, nb}, {n_free_out, sizeof(int32_t)},
                          {free_pages, sizeof(int32_t) * (size_t)p->num_pages}};
-    if (clash(outs, ins)) return DSPARK_ERR_INVALID_ARG;
+    const Span settled[] = {{p->settled, 2 * nb + sizeof(int32_t)}}, kept[] = {ins[1], ins[4], ins[5], outs[0], outs[1], outs[2], outs[3]};
+    if (clash(outs, ins) || clash(settled, kept)) return DSPARK_ERR_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < kHeaderBytes) return DSPARK_ERR_WORKSPACE;
     int sms = 0, per_sm = 0;
     if (device_sm_count(&sms) != cudaSuccess) return DSPARK_ERR_CUDA;
@@ -587,7 +597,7 @@ extern "C" dspark_status dspark_cache_commit(const dspark_cache_params* p, const
         return DSPARK_ERR_CUDA;
     CommitArgs a{p->B, page_shift_of(p->page_size), p->num_pages, p->max_blocks, p->extra, cache_len, add_len, done,
                  block_table, n_blocks, free_pages, n_free, cache_len_out, n_blocks_out, n_free_out,
-                 &static_cast<WsHeader*>(workspace)->status, p->error};
+                 &static_cast<WsHeader*>(workspace)->status, p->error, p->settled};
     if (launch_overlapped_clusters(kernel, blocks, blocks, kPlanThreads, smem,
                                    reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
         return DSPARK_ERR_CUDA;

@@ -155,7 +155,7 @@ dspark_cache_params cache_params(const at::Tensor& cache_len, const at::Tensor& 
     want(&n_blocks, at::kInt, B, "n_blocks is int32 [B]");
     want(&n_free, at::kInt, 1, "n_free is int32 [1]");
     if (table.dim() != 2 || table.size(0) != B) refuse(PyExc_ValueError, "block_table is [B, max_blocks]");
-    return {size32(B), small(page_size), size32(free_pages.numel()), size32(table.size(1)), max_tokens, small(extra), error_word(error)};
+    return {size32(B), small(page_size), size32(free_pages.numel()), size32(table.size(1)), max_tokens, small(extra), error_word(error), nullptr};
 }
 
 // cache_len, new_len, block_table, n_blocks, free_pages, n_free, page_size, max_tokens, extra,
@@ -187,18 +187,20 @@ PyObject* cache_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // cache_len, add_len, done, block_table, n_blocks, free_pages, n_free, page_size, extra, cache_len_out,
-// n_blocks_out, n_free_out, workspace, stream, error
+// n_blocks_out, n_free_out, workspace, stream, error, settled
 PyObject* cache_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&] {
-        count_args(n, 15);
+        count_args(n, 16);
         const at::Tensor &cache_len = needed(a[0]), &table = needed(a[3]), &n_blocks = needed(a[4]), &free_pages = needed(a[5]),
                          &n_free = needed(a[6]), &len_out = needed(a[9]), &n_blocks_out = needed(a[10]),
                          &n_free_out = needed(a[11]), &ws = needed(a[12]);
-        const at::Tensor *add_len = tensor(a[1]), *done = tensor(a[2]);
+        const at::Tensor *add_len = tensor(a[1]), *done = tensor(a[2]), *settled = tensor(a[15]);
         one_device({&cache_len, add_len, done, &table, &n_blocks, &free_pages, &n_free, &len_out, &n_blocks_out, &n_free_out, &ws,
-                    tensor(a[14])});
-        const dspark_cache_params p = cache_params(cache_len, table, n_blocks, free_pages, n_free, a[7], 0, a[8], a[14]);
+                    tensor(a[14]), settled});
+        dspark_cache_params p = cache_params(cache_len, table, n_blocks, free_pages, n_free, a[7], 0, a[8], a[14]);
         want(add_len, at::kInt, p.B, "add_len is int32 [B]");
+        want(settled, at::kInt, 2 * (int64_t)p.B + 1, "settled is int32 [2 B + 1]");
+        p.settled = as<int32_t>(address(settled));
         if (done && ((done->scalar_type() != at::kByte && done->scalar_type() != at::kBool) || done->numel() != p.B))
             refuse(PyExc_ValueError, "done is uint8 or bool [B]");
         want(&len_out, at::kInt, p.B, "cache_len is int32 [B]");

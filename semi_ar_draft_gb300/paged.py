@@ -9,8 +9,9 @@ stack, and per layer a pool of keys and one of values.  A round is
     commit(add_len, extra)    how many of them stay; pages past them go back
 
 and nothing in it reads the device from the host.  plan and commit write their results to other tensors than
-they read; a copy of a few bytes a request then brings them back, so that every call reads the same addresses and any
-sequence of calls can be captured into a graph and replayed."""
+they read: plan goes from what the last commit left to what the next one reads, and commit writes there too.  So every
+call reads the same addresses, and any sequence of calls can be captured into a graph and replayed; a plan that no
+commit has followed is replaced by the next."""
 from __future__ import annotations
 
 import contextlib
@@ -28,8 +29,8 @@ def _on(stream):
 
 class PagedCache:
     """requests slots of at most max_blocks pages each; num_pages pages of page_size tokens in all; max_tokens:
-    the most new tokens of any step (a step may say that it has fewer: plan's tokens).  kv_dtype: dtype or torch.float8_e4m3fn, then with k_scale, v_scale
-    [layers, Hk] fp32 (ones if not given)."""
+    the most new tokens of any step (a step may say that it has fewer: plan's tokens).  kv_dtype: dtype or
+    torch.float8_e4m3fn, then with k_scale, v_scale [layers, Hk] fp32 (ones if not given)."""
 
     def __init__(self, requests, num_pages, page_size, max_blocks, layers, Hk, D, max_tokens, dtype=torch.bfloat16,
                  kv_dtype=None, k_scale=None, v_scale=None, device="cuda"):
@@ -45,11 +46,12 @@ class PagedCache:
         self.page_size, self.max_tokens = page_size, max_tokens
         self.block_table = torch.full((requests, max_blocks), -1, **i32)
         self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)
-        # lengths, blocks held, pages free: what every call reads, and where plan and commit write them
+        # lengths, blocks held, pages free: [0] now, [1] as the last commit left them
         self._counts = [torch.zeros(2 * requests + 1, **i32) for _ in range(2)]
         self._len, self._blocks, self._free = ([x[a:b] for x in self._counts] for a, b in
                                                ((0, requests), (requests, 2 * requests), (2 * requests, 2 * requests + 1)))
-        self._free[0].fill_(num_pages)
+        for x in self._free:
+            x.fill_(num_pages)
         self.seq_len, self.offsets = torch.empty(requests, **i32), torch.empty(requests + 1, **i32)
         self._slots = torch.empty(max_tokens, dtype=torch.int64, device=device)
         self._positions = torch.empty(max_tokens, **i32)
@@ -76,11 +78,11 @@ class PagedCache:
             tokens = self.max_tokens
         if not 0 <= tokens <= self.max_tokens:
             raise ValueError(f"a step of {tokens} tokens; the cache was made for {self.max_tokens}")
-        self.slots, self.positions = self._slots[:tokens], self._positions[:tokens]
-        api.cache_plan(self._len[0], new_len, self.block_table, self._blocks[0], self.free_pages, self._free[0],
+        if tokens != len(self.slots):
+            self.slots, self.positions = self._slots[:tokens], self._positions[:tokens]
+        api.cache_plan(self._len[0], new_len, self.block_table, self._blocks[1], self.free_pages, self._free[1],
                        self.page_size, tokens, extra=extra, ws=self.ws, stream=stream, error=self._error,
-                       out=(self.seq_len, self.offsets, self.slots, self.positions, self._blocks[1], self._free[1]))
-        self._keep(len(self._len[0]), stream)
+                       out=(self.seq_len, self.offsets, self.slots, self.positions, self._blocks[0], self._free[0]))
         self.max_new = max_new
 
     def append(self, layer, k, v, stream=None):
@@ -99,13 +101,7 @@ class PagedCache:
         """Keeps add_len[j] + extra of each request's new tokens (none of the whole request where done)."""
         api.cache_commit(self._len[0], add_len, self.block_table, self._blocks[0], self.free_pages, self._free[0],
                          self.page_size, extra=extra, done=done, ws=self.ws, stream=stream, error=self._error,
-                         out=(self._len[1], self._blocks[1], self._free[1]))
-        self._keep(0, stream)
-
-    def _keep(self, first, stream):
-        """The counts just written (from `first` on) to where the next call reads them."""
-        with _on(stream):
-            self._counts[0][first:].copy_(self._counts[1][first:])
+                         out=(self._len[1], self._blocks[1], self._free[1]), settled=self._counts[0])
 
     def status(self, stream=None):
         """The first device error of plan, attend and commit since this was last called, 0 if there was none

@@ -216,3 +216,19 @@ def test_steps_of_different_token_counts(kv):
     assert small.status() == 8
     with pytest.raises(ValueError):
         small.plan(i32([1, 1, 1]), tokens=301)
+
+
+def test_a_plan_replaces_the_one_that_no_commit_followed():
+    """Planning a step again, larger or smaller, ends as if it had been planned once."""
+    once, again = (PagedCache(2, 20, 4, 8, 1, 1, 64, 64) for _ in range(2))
+    for first, new, acc in (([9, 1], [5, 7], [5, 2]), ([2, 2], [12, 1], [3, 1]), ([20, 3], [1, 9], [1, 9])):
+        again.plan(i32(first))
+        for c in (once, again):
+            c.plan(i32(new))
+        assert torch.equal(once.slots[: sum(new)], again.slots[: sum(new)]) and int(once.n_free) == int(again.n_free)
+        for c in (once, again):
+            c.commit(i32(acc))
+        assert once.cache_len.tolist() == again.cache_len.tolist() and int(once.n_free) == int(again.n_free)
+        held = [p for j in range(2) for p in again.block_table[j, : -(-int(again.cache_len[j]) // 4)].tolist()]
+        assert sorted(held + again.free_pages[: int(again.n_free)].tolist()) == list(range(20))
+    assert once.status() == 0 and again.status() == 0

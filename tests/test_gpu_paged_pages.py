@@ -115,3 +115,29 @@ def test_blocks_without_a_page_name_none(B, short):
     pool = torch.zeros((P, page, 1, 64), dtype=torch.bfloat16, device="cuda")
     _, _, ws = api.paged_attention(q, pool, pool, t, seq, off)
     assert binding.dspark_get_device_status(ws) == 8
+
+
+@pytest.mark.parametrize("B", [1, 64, 65, 700, 5000])
+def test_commit_settles_the_counts_over_its_inputs(B):
+    """The three outputs once more, over cache_len, n_blocks and n_free: one block, clusters, several requests a thread."""
+    page, most = 8, 5
+    g = torch.Generator().manual_seed(B)
+    n_blocks = torch.randint(0, most + 1, (B,), generator=g).int()
+    cache_len = (n_blocks * page - torch.randint(0, page, (B,), generator=g).int()).clamp(min=0)
+    add = -(torch.rand(B, generator=g) * cache_len).int()
+    P = int(n_blocks.sum()) + 9
+    perm = torch.randperm(P, generator=g).int()
+    table, used = torch.full((B, most), -1, dtype=torch.int32), 0
+    for j, n in enumerate(n_blocks.tolist()):
+        table[j, :n] = perm[used:used + n]
+        used += n
+    free = torch.cat([perm[used:], torch.zeros(used, dtype=torch.int32)])
+    done = torch.rand(B, generator=g) < 0.2
+    dev = [x.cuda() for x in (add, table, done)]
+    counts = torch.cat([cache_len, n_blocks, torch.tensor([P - used], dtype=torch.int32)]).cuda()
+    stacks = [free.cuda() for _ in range(2)]
+    ref = api.cache_commit(counts[:B].clone(), dev[0], dev[1], counts[B:2 * B].clone(), stacks[0], counts[2 * B:].clone(), page,
+                           done=dev[2])
+    out = api.cache_commit(counts[:B], dev[0], dev[1], counts[B:2 * B], stacks[1], counts[2 * B:], page, done=dev[2], settled=counts)
+    assert all(torch.equal(x, y) for x, y in zip(out[:3], ref)) and torch.equal(*stacks)
+    assert torch.equal(counts, torch.cat(ref[:3])) and binding.dspark_get_device_status(out[3]) == 0

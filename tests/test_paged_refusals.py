@@ -131,3 +131,16 @@ def test_an_argument_without_a_truth_value_says_so():
     with pytest.raises(ArithmeticError, match="neither"):
         api.paged_attention(z(4, 4, 64), z(5, 16, 2, 64), z(5, 16, 2, 64), i(4, 3), i(4), causal=Neither(),
                             ws=torch.zeros(256, dtype=torch.uint8))
+
+
+def test_commit_refuses_settled_counts_over_anything_but_the_counts(L):
+    from semi_ar_draft_gb300 import binding as b
+
+    # cache_len, add_len, done, block_table, n_blocks, free_pages, n_free | cache_len, n_blocks, n_free
+    size = [16, 16, 4, 80, 16, 40, 4, 16, 16, 4]
+    for i in (1, 2, 3, 5, 7, 8, 9):
+        for at in (A[i].value, A[i].value + size[i] - 4, A[i].value - 36 + 4):
+            p = b.CacheParams(4, 16, 10, 5, 0, 1, None, at)
+            assert L.dspark_cache_commit(C.byref(p), *A[:11], 256, None) == 1, (i, at)
+    p = b.CacheParams(4, 16, 10, 5, 0, 1, None, 0x200002)
+    assert L.dspark_cache_commit(C.byref(p), *A[:11], 256, None) == 1
