@@ -51,11 +51,13 @@ typedef enum {
     DSPARK_ERR_BUDGET = 5,      /* scheduler: budget < B */
     DSPARK_ERR_WORKSPACE = 6,   /* workspace NULL, misaligned or too small */
     DSPARK_ERR_TOKEN_RANGE = 7, /* device: a token/anchor id outside [0, V) or a bad row count (status word only) */
-    DSPARK_ERR_CACHE = 8        /* device: the paged cache's lengths, tables or pages do not fit (status word only) */
+    DSPARK_ERR_CACHE = 8,       /* device: the paged cache's lengths, tables or pages do not fit (status word only) */
+    DSPARK_ERR_NOT_FINITE = 9   /* device: a value to be held as an integer is NaN or infinite (status word only) */
 } dspark_status;
 
-/* Logits and weights are DSPARK_F32 or DSPARK_BF16; the paged cache takes the other two as well. */
-enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2, DSPARK_E4M3 = 3 };
+/* Logits and weights are DSPARK_F32 or DSPARK_BF16; the paged cache takes the others as well (DSPARK_I8: the calls that
+ * end in _i8). */
+enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_F16 = 2, DSPARK_E4M3 = 3, DSPARK_I8 = 4 };
 
 /* Random-draw purposes (the fourth Philox counter word). */
 enum {
@@ -498,6 +500,64 @@ dspark_status dspark_paged_attention(const dspark_attention_params* p, const voi
                                      const void* v_pages, const int32_t* block_table, const int32_t* seq_len,
                                      const int32_t* offsets, const float* k_scale, const float* v_scale, void* out,
                                      float* lse, void* workspace, size_t ws_bytes, dspark_stream_t stream);
+
+/*
+ * The paged cache in 8-bit integers, with a scale for each block of tokens and kv head that comes from the values
+ * themselves (an e4m3 cache has one a head, which somebody has to know beforehand).  Pools, tables, slots and
+ * the plan and commit are those above, the pools int8.
+ *
+ * Format.  A block is `block` adjacent tokens of a page (a power of two up to 128 and to the page).  Of block b of page
+ * p and kv head h the byte at p page_stride + b block_stride + h head_stride (bytes; k for the keys, v for the values)
+ * holds e + 127, and its values are code 2^e, code in [-127, 127].  e lies in [-126, 121] in a cache for bf16 and in
+ * [-24, 9] for fp16, where code 2^e is a number of that type; a byte outside is read as the nearest one inside.
+ *
+ * dspark_cache_append_i8 writes the keys and values of T tokens to their slots, as dspark_cache_append does.  For a
+ * block and head let M be the largest finite magnitude among the call's tokens of the block:
+ *   e = the smallest exponent of the range with M <= 127 2^e (the last one where there is none)
+ *   unless the block's first token is among them (the block is begun anew, whatever it held): e = max(e, the block's)
+ *   code = x 2^-e rounded to nearest even, within [-127, 127]
+ *   where e has grown by n: every code of the block that this call does not write becomes code 2^-n, rounded to
+ *   nearest even
+ * So a token's error is at most half a step 2^e of the scale that it was written with, and below one step of the block's
+ * last one where that grew later.  A token that is overwritten or forgotten leaves its scale until the block is begun anew.
+ * NaN is stored as 0 and infinities as +-127 steps; either is reported as DSPARK_ERR_NOT_FINITE in `error` (a device
+ * word as of dspark_cache_params, or NULL).
+ * Slots outside the pool are skipped.  The tokens of one block have to follow one another in slots, in any order,
+ * with fewer than 32 skipped entries between two of them (as dspark_cache_plan lays them out); a block that other tokens
+ * interrupt ends up with codes and a scale of either part.  Of two tokens of one slot the later one stays; both count
+ * for the scale.
+ * Apart from that the same inputs give the same outputs bit for bit.
+ *
+ * dspark_cache_read_i8 is the way back: k, v [T, Hk, D] dense (dtype), 16-byte aligned, become the values of the T
+ * slots, exactly; those of slots outside the pool are 0.
+ *
+ * Both take a dspark_append_params with kv_dtype DSPARK_I8 (dspark_cache_read_i8: the strides of k and v are the
+ * dense ones).  Host errors: DSPARK_ERR_UNSUPPORTED unless D is a multiple of 16 up to 256.  No workspace; T = 0
+ * enqueues nothing.
+ */
+typedef struct {
+    uint8_t* k; /* exponents of the keys' blocks, of the values' */
+    uint8_t* v;
+    int block; /* tokens of a block */
+    int64_t page_stride, block_stride, head_stride;
+} dspark_block_exponents;
+
+dspark_status dspark_cache_append_i8(const dspark_append_params* p, const dspark_block_exponents* x, const void* k,
+                                     const void* v, void* k_pages, void* v_pages, const int64_t* slots, int32_t* error,
+                                     dspark_stream_t stream);
+dspark_status dspark_cache_read_i8(const dspark_append_params* p, const dspark_block_exponents* x, const void* k_pages,
+                                   const void* v_pages, const int64_t* slots, void* k, void* v, dspark_stream_t stream);
+
+/*
+ * dspark_paged_attention over int8 pools: the same scores, masks, outputs, statuses and workspace, with k_l and v_l the
+ * values code 2^e; p->kv_dtype is DSPARK_I8.  It is the attention over the cache that dspark_cache_read_i8 gives.
+ * Probabilities are rounded to 16 bits (fp16, or for many rows a kv head dtype) before they meet the values.
+ * Host errors besides: DSPARK_ERR_UNSUPPORTED for a scale other than 0 outside 2^-32 .. 2^32.
+ */
+dspark_status dspark_paged_attention_i8(const dspark_attention_params* p, const dspark_block_exponents* x, const void* q,
+                                        const void* k_pages, const void* v_pages, const int32_t* block_table,
+                                        const int32_t* seq_len, const int32_t* offsets, void* out, float* lse,
+                                        void* workspace, size_t ws_bytes, dspark_stream_t stream);
 
 /* Reads the device status word of `workspace` after synchronising `stream`
  * (DSPARK_OK when no device-side error was recorded).  `workspace` is a device pointer;

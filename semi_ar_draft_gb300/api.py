@@ -201,11 +201,34 @@ def cache_append(k, v, k_pages, v_pages, slots, k_scale=None, v_scale=None, stre
     b._check(b.native().cache_append(k, v, k_pages, v_pages, slots, k_scale, v_scale, _raw(stream)), "dspark_cache_append")
 
 
+def cache_append_i8(k, v, k_pages, v_pages, k_exp, v_exp, slots, stream=None, error=None):
+    """Quantises k, v [T, Hk, D] (bf16 or fp16; any strides with a dense last dimension) into their slots [T] int64 of
+    int8 k_pages, v_pages [pages, page_size, Hk, D], with a power of two for each block of tokens and kv head
+    (dspark_cache_append_i8): k_exp, v_exp [pages, Hk, page_size / block] uint8.  A block's tokens follow one another in
+    slots.  error as for cache_plan: status 9 for values that are not finite."""
+    st = b.native().cache_append_i8(k, v, k_pages, v_pages, k_exp, v_exp, slots, _raw(stream), error)
+    b._check(st, "dspark_cache_append_i8")
+
+
+def cache_read_i8(k_pages, v_pages, k_exp, v_exp, slots, dtype=torch.bfloat16, out=None, stream=None):
+    """The values of the slots [T] int64 of an int8 cache, exactly, in the 16-bit type that it was written from
+    (dspark_cache_read_i8); 0 for slots outside the pool.  out: (k, v) [T, Hk, D] dense, or None: new ones of dtype.
+    Returns (k, v)."""
+    made = ()
+    if out is None:
+        shape = (slots.numel(), *k_pages.shape[2:])
+        made = out = tuple(torch.empty(shape, dtype=dtype, device=k_pages.device) for _ in range(2))
+    st = b.native().cache_read_i8(k_pages, v_pages, k_exp, v_exp, slots, *out, _raw(stream, *made))
+    b._check(st, "dspark_cache_read_i8")
+    return out
+
+
 def _attention_sizes(q, k_pages, seq_len, max_new):
     """The parameters that decide the workspace's size."""
     T, Hq, D = q.shape
+    kv = b.I8 if k_pages.dtype == torch.int8 else b.cache_dtype_code(k_pages.dtype)
     return b.AttentionParams(T, seq_len.numel(), Hq, k_pages.shape[2], D, 1, 1, 1, max_new, b.cache_dtype_code(q.dtype),
-                             b.cache_dtype_code(k_pages.dtype), 1, 0, 1.0, 0.0, 0, 0, 0, 0, 0)
+                             kv, 1, 0, 1.0, 0.0, 0, 0, 0, 0, 0)
 
 
 def paged_attention(q, k_pages, v_pages, block_table, seq_len, offsets=None, scale=None, causal=True, window=0,
@@ -225,4 +248,21 @@ def paged_attention(q, k_pages, v_pages, block_table, seq_len, offsets=None, sca
                                         q.shape[-1] ** -0.5 if scale is None else scale, softcap, causal, window, max_new, out,
                                         lse, ws, _raw(stream, ws, out, lse), error)
     b._check(st, "dspark_paged_attention")
+    return out, lse, ws
+
+
+def paged_attention_i8(q, k_pages, v_pages, k_exp, v_exp, block_table, seq_len, offsets=None, scale=None, causal=True, window=0,
+                       softcap=0.0, max_new=0, out=None, lse=None, ws=None, stream=None, error=None):
+    """paged_attention over int8 pages [pages, page_size, Hk, D] and their exponents [pages, Hk, page_size / block]
+    uint8 (dspark_paged_attention_i8), as cache_append_i8 writes them.  Returns (out [T, Hq, D], lse or None, workspace)."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is True:
+        lse = torch.empty(q.shape[:2], device=q.device)
+    if ws is None and stream is not None:  # (else it is made in the native call, on the current stream)
+        ws = b.workspace(b.dspark_paged_attention_workspace_size(_attention_sizes(q, k_pages, seq_len, max_new)), q.device)
+    st, ws = b.native().paged_attention_i8(q, k_pages, v_pages, block_table, seq_len, offsets, k_exp, v_exp,
+                                           q.shape[-1] ** -0.5 if scale is None else scale, softcap, causal, window, max_new, out,
+                                           lse, ws, _raw(stream, ws, out, lse), error)
+    b._check(st, "dspark_paged_attention_i8")
     return out, lse, ws

@@ -14,9 +14,10 @@ import torch
 
 from .build import LIB, NATIVE
 
-F32, BF16, F16, E4M3 = 0, 1, 2, 3
+F32, BF16, F16, E4M3, I8 = 0, 1, 2, 3, 4
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "CUDA error", 4: "device wait timed out",
-          5: "budget < B", 6: "bad workspace", 7: "token out of range", 8: "paged cache out of range"}
+          5: "budget < B", 6: "bad workspace", 7: "token out of range", 8: "paged cache out of range",
+          9: "value to be held as an integer not finite"}
 
 
 class DsparkError(RuntimeError):
@@ -48,6 +49,11 @@ class AppendParams(C.Structure):
                 ("dtype", C.c_int), ("kv_dtype", C.c_int), ("k_token_stride", C.c_int64), ("k_head_stride", C.c_int64),
                 ("v_token_stride", C.c_int64), ("v_head_stride", C.c_int64), ("kv_page_stride", C.c_int64),
                 ("kv_token_stride", C.c_int64), ("kv_head_stride", C.c_int64)]
+
+
+class BlockExponents(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("block", C.c_int), ("page_stride", C.c_int64),
+                ("block_stride", C.c_int64), ("head_stride", C.c_int64)]
 
 
 class AttentionParams(C.Structure):
@@ -116,6 +122,12 @@ def lib():
         L.dspark_paged_attention_workspace_size.restype = sz
         L.dspark_paged_attention.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.dspark_paged_attention.restype = i32
+        L.dspark_cache_append_i8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.dspark_cache_append_i8.restype = i32
+        L.dspark_cache_read_i8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
+        L.dspark_cache_read_i8.restype = i32
+        L.dspark_paged_attention_i8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dspark_paged_attention_i8.restype = i32
         L.dspark_get_device_status.argtypes = [vp, vp, C.POINTER(C.c_int32)]
         L.dspark_get_device_status.restype = i32
         L.dspark_set_wait_limit_ns.argtypes = [u64]
@@ -363,6 +375,33 @@ def dspark_paged_attention(p, q, k_pages, v_pages, block_table, seq_len, offsets
                                       _ptr(block_table), _ptr(seq_len), _ptr(offsets), _ptr(k_scale), _ptr(v_scale),
                                       _ptr(out), _ptr(lse), _ptr(workspace), workspace.nbytes, _stream(stream))
     _check(st, "dspark_paged_attention")
+
+
+def block_exponents(k_exp, v_exp, page_size) -> BlockExponents:
+    """k_exp, v_exp [pages, Hk, page_size / block] uint8 of one layout."""
+    if not (k_exp.is_cuda and v_exp.is_cuda):
+        raise ValueError("libdspark takes device tensors")
+    page, head, block = k_exp.stride()
+    return BlockExponents(k_exp.data_ptr(), v_exp.data_ptr(), page_size // k_exp.shape[2], page, block, head)
+
+
+def dspark_cache_append_i8(p, x, k, v, k_pages, v_pages, slots, error=None, stream=None):
+    st = lib().dspark_cache_append_i8(C.byref(p), C.byref(x), _rows_ptr(k), _rows_ptr(v), _rows_ptr(k_pages), _rows_ptr(v_pages),
+                                      _ptr(slots), _ptr(error), _stream(stream))
+    _check(st, "dspark_cache_append_i8")
+
+
+def dspark_cache_read_i8(p, x, k_pages, v_pages, slots, k, v, stream=None):
+    st = lib().dspark_cache_read_i8(C.byref(p), C.byref(x), _rows_ptr(k_pages), _rows_ptr(v_pages), _ptr(slots), _ptr(k), _ptr(v),
+                                    _stream(stream))
+    _check(st, "dspark_cache_read_i8")
+
+
+def dspark_paged_attention_i8(p, x, q, k_pages, v_pages, block_table, seq_len, offsets, out, lse, workspace, stream=None):
+    st = lib().dspark_paged_attention_i8(C.byref(p), C.byref(x), _rows_ptr(q), _rows_ptr(k_pages), _rows_ptr(v_pages),
+                                         _ptr(block_table), _ptr(seq_len), _ptr(offsets), _ptr(out), _ptr(lse), _ptr(workspace),
+                                         workspace.nbytes, _stream(stream))
+    _check(st, "dspark_paged_attention_i8")
 
 
 def dspark_get_device_status(workspace, stream=None) -> int:

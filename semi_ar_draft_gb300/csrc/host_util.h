@@ -22,6 +22,8 @@ uint64_t wait_limit_ns();               // bound of every grid-wide wait
 
 int page_shift_of(int page_size);  // log2 of a cache page's tokens (1 .. 4096, a power of two), else -1
 
+bool valid_block_exponents(const dspark_block_exponents* x, int page_size);
+
 dspark_status validate_sample_params(const dspark_sample_params* p);
 size_t sample_workspace_bytes(const dspark_sample_params* p);
 bool markov_use_mma(const dspark_sample_params* p);

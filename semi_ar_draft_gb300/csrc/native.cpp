@@ -129,6 +129,18 @@ void check_scales(const at::Tensor& pages, const at::Tensor* ks, const at::Tenso
     want(vs, at::kFloat, Hk, "a scale is fp32 [Hk]");
 }
 
+// Pools of an int8 cache and the exponents of its blocks, [pages, Hk, page_size / block] uint8 each.
+dspark_block_exponents exponents_of(const at::Tensor& kp, const Pools& x, const at::Tensor& ke, const at::Tensor& ve) {
+    if (kp.scalar_type() != at::kChar) refuse(PyExc_TypeError, "k_pages and v_pages are int8");
+    if (ke.scalar_type() != at::kByte || ve.scalar_type() != at::kByte || ke.dim() != 3 || ve.sizes() != ke.sizes() ||
+        ve.strides() != ke.strides() || ke.size(0) != x.pages || ke.size(1) != x.Hk || ke.size(2) < 1 ||
+        x.page_size % ke.size(2))
+        refuse(PyExc_ValueError, "k_exp and v_exp are uint8 [pages, Hk, page_size / block] of one layout");
+    if (!ke.is_cuda() || !ve.is_cuda()) refuse(PyExc_ValueError, "libdspark takes device tensors");
+    return {static_cast<uint8_t*>(ke.data_ptr()), static_cast<uint8_t*>(ve.data_ptr()), (int)(x.page_size / ke.size(2)),
+            ke.stride(0), ke.stride(2), ke.stride(1)};
+}
+
 // Runs a call's body; no C++ exception passes into Python.
 template <typename F>
 PyObject* guarded(F&& f) {
@@ -236,8 +248,52 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// k, v, k_pages, v_pages, k_exp, v_exp, slots, stream, error
+PyObject* cache_append_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        count_args(n, 9);
+        const at::Tensor &k = needed(a[0]), &v = needed(a[1]), &kp = needed(a[2]), &vp = needed(a[3]), &ke = needed(a[4]),
+                         &ve = needed(a[5]), &slots = needed(a[6]);
+        one_device({&k, &v, &kp, &vp, &ke, &ve, &slots, tensor(a[8])});
+        const Pools x = pools_of(kp, vp);
+        const dspark_block_exponents e = exponents_of(kp, x, ke, ve);
+        if (k.dim() != 3 || v.sizes() != k.sizes() || k.size(1) != x.Hk || k.size(2) != x.D || k.scalar_type() != v.scalar_type())
+            refuse(PyExc_ValueError, "k and v are [T, Hk, D] of one type");
+        want(&slots, at::kLong, k.size(0), "slots is int64 [T]");
+        const dspark_append_params p{size32(k.size(0)), x.Hk,     x.D,         x.page_size, x.pages,     type_code(k.scalar_type()),
+                                     DSPARK_I8,         k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                                     x.page,            x.token,     x.head};
+        return PyLong_FromLong(dspark_cache_append_i8(&p, &e, rows_address(k), rows_address(v), rows_address(kp), rows_address(vp),
+                                                      as<int64_t>(address(&slots)), error_word(a[8]), stream_of(a[7], k)));
+    });
+}
+
+// k_pages, v_pages, k_exp, v_exp, slots, k, v, stream
+PyObject* cache_read_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        count_args(n, 8);
+        const at::Tensor &kp = needed(a[0]), &vp = needed(a[1]), &ke = needed(a[2]), &ve = needed(a[3]), &slots = needed(a[4]),
+                         &k = needed(a[5]), &v = needed(a[6]);
+        one_device({&kp, &vp, &ke, &ve, &slots, &k, &v});
+        const Pools x = pools_of(kp, vp);
+        const dspark_block_exponents e = exponents_of(kp, x, ke, ve);
+        const int64_t T = slots.numel();
+        if (k.dim() != 3 || v.sizes() != k.sizes() || k.size(0) != T || k.size(1) != x.Hk || k.size(2) != x.D ||
+            k.scalar_type() != v.scalar_type())
+            refuse(PyExc_ValueError, "k and v are [slots, Hk, D] of one type");
+        want(&slots, at::kLong, T, "slots is int64 [T]");
+        const int64_t row = (int64_t)x.Hk * x.D;
+        const dspark_append_params p{size32(T), x.Hk, x.D, x.page_size, x.pages, type_code(k.scalar_type()), DSPARK_I8,
+                                     row,       x.D,  row, x.D,         x.page,  x.token,                    x.head};
+        return PyLong_FromLong(dspark_cache_read_i8(&p, &e, rows_address(kp), rows_address(vp), as<int64_t>(address(&slots)),
+                                                    address(&k), address(&v), stream_of(a[7], kp)));
+    });
+}
+
 // q, k_pages, v_pages, block_table, seq_len, offsets, k_scale, v_scale, scale, softcap, causal, window,
 // max_new, out, lse, workspace (or None: one is allocated), stream, error.  Returns (status, workspace).
+// int8 pools: k_exp and v_exp in the scales' places.
+template <bool I8>
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
         count_args(n, 18);
@@ -251,7 +307,11 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (seq.scalar_type() != at::kInt || table.scalar_type() != at::kInt || table.dim() != 2 || table.size(0) != B)
             refuse(PyExc_ValueError, "block_table [B, max_blocks] and seq_len [B] are int32");
         want(off, at::kInt, B + 1, "offsets is int32 [B + 1]");
-        check_scales(kp, ks, vs, x.Hk);
+        dspark_block_exponents e{};
+        if (I8)
+            e = exponents_of(kp, x, needed(a[6]), needed(a[7]));
+        else
+            check_scales(kp, ks, vs, x.Hk);
         if (out.sizes() != q.sizes() || out.scalar_type() != q.scalar_type())
             refuse(PyExc_ValueError, "out is [T, Hq, D] of q's type");
         if (lse && (lse->scalar_type() != at::kFloat || lse->dim() != 2 || lse->size(0) != T || lse->size(1) != q.size(1)))
@@ -267,7 +327,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         p.max_blocks = size32(table.size(1));
         p.max_new = small(a[12]);
         p.dtype = type_code(q.scalar_type());
-        p.kv_dtype = type_code(kp.scalar_type());
+        p.kv_dtype = I8 ? (int)DSPARK_I8 : type_code(kp.scalar_type());
         p.causal = PyObject_IsTrue(a[10]);
         if (p.causal < 0) throw Refused{};
         p.window = small(a[11]);
@@ -286,10 +346,14 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
             made = at::empty({(int64_t)dspark_paged_attention_workspace_size(&p) + 256}, q.options().dtype(at::kByte));
             ws = &made;
         }
-        const dspark_status st = dspark_paged_attention(
-            &p, rows_address(q), rows_address(kp), rows_address(vp), as<int32_t>(address(&table)),
-            as<int32_t>(address(&seq)), as<int32_t>(address(off)), as<float>(address(ks)), as<float>(address(vs)), address(&out),
-            as<float>(address(lse)), address(ws), ws->nbytes(), s);
+        const dspark_status st =
+            I8 ? dspark_paged_attention_i8(&p, &e, rows_address(q), rows_address(kp), rows_address(vp), as<int32_t>(address(&table)),
+                                           as<int32_t>(address(&seq)), as<int32_t>(address(off)), address(&out),
+                                           as<float>(address(lse)), address(ws), ws->nbytes(), s)
+               : dspark_paged_attention(&p, rows_address(q), rows_address(kp), rows_address(vp), as<int32_t>(address(&table)),
+                                        as<int32_t>(address(&seq)), as<int32_t>(address(off)), as<float>(address(ks)),
+                                        as<float>(address(vs)), address(&out), as<float>(address(lse)), address(ws),
+                                        ws->nbytes(), s);
         return Py_BuildValue("iN", (int)st, made.defined() ? THPVariable_Wrap(made) : (Py_INCREF(a[15]), a[15]));
     });
 }
@@ -298,7 +362,10 @@ PyMethodDef methods[] = {
     {"cache_plan", (PyCFunction)(void (*)())cache_plan, METH_FASTCALL, nullptr},
     {"cache_commit", (PyCFunction)(void (*)())cache_commit, METH_FASTCALL, nullptr},
     {"cache_append", (PyCFunction)(void (*)())cache_append, METH_FASTCALL, nullptr},
-    {"paged_attention", (PyCFunction)(void (*)())paged_attention, METH_FASTCALL, nullptr},
+    {"cache_append_i8", (PyCFunction)(void (*)())cache_append_i8, METH_FASTCALL, nullptr},
+    {"cache_read_i8", (PyCFunction)(void (*)())cache_read_i8, METH_FASTCALL, nullptr},
+    {"paged_attention", (PyCFunction)(void (*)())paged_attention<false>, METH_FASTCALL, nullptr},
+    {"paged_attention_i8", (PyCFunction)(void (*)())paged_attention<true>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

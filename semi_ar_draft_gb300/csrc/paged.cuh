@@ -21,9 +21,14 @@
 
 #include <cuda_fp16.h>
 
+#include "block_scale.cuh"
 #include "common.cuh"
 
 namespace dspark {
+
+// What the pools hold: values of q's 16-bit type, e4m3 with a scale a kv head, or int8 with an exponent for each block
+// of tokens and kv head.
+enum { kKv16 = 0, kKvE4M3 = 1, kKvI8 = 2 };
 
 struct AttnArgs {
     int T, B, Hq, Hk, G, D;
@@ -43,6 +48,7 @@ struct AttnArgs {
     const int32_t* offsets;  // or null: one token a request
     const float* k_scale;
     const float* v_scale;
+    BlockExp exp;        // int8 pools
     unsigned char* out;  // [T, Hq, D]
     float* lse;          // [T, Hq] or null
     // workspace
@@ -300,6 +306,23 @@ __device__ __forceinline__ bool odd_found(uint32_t acc) {
     return (acc & 0xffffu) >= inf || (acc >> 16) >= inf;
 }
 
+// Four codes of an int8 cache as halves, bytes A, B of the word in the low one: byte + 128 beside the exponent of 2^10 is
+// 1024 + 128 + code, and the difference is exact.
+template <int SELECT>
+__device__ __forceinline__ uint32_t i8x2_to_half2(uint32_t offset_word) {  // the word ^ 0x80808080
+    const uint32_t h = __byte_perm(offset_word, 0x64646464u, SELECT);
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
+    return r;
+}
+constexpr int kBytes01 = 0x4140, kBytes23 = 0x4342, kBytes02 = 0x4240, kBytes13 = 0x4341;
+
+// The exponents of a key's block, of the keys (low byte) and the values: at is its place in the page.
+__device__ __forceinline__ uint32_t block_exponents(const AttnArgs& a, int page, int at, int head) {
+    const long long e = page * a.exp.page + (long long)(at >> a.exp.shift) * a.exp.block + head * a.exp.head;
+    return (uint32_t)__ldg(a.exp.k + e) | (uint32_t)__ldg(a.exp.v + e) << 8;
+}
+
 // Probabilities as halves are taken against a reference 2^7 below the running maximum's (which follows within 2^8, so
 // they stay below 2^15): halves lose bits below 2^-14, which is then 2^-21 of the largest.  bf16 has fp32's exponents.
 // Sums carry the same factor; it cancels in the output and is taken out of lse.
@@ -323,6 +346,6 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 
 // Row tiles of 128 on the fifth-generation tensor cores (paged_attn_tc.cu); needs 16-byte
 // aligned query rows.
-dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, bool e4m3, int sms, cudaStream_t s, int* parts);
+dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int kv, int sms, cudaStream_t s, int* parts);
 
 }  // namespace dspark

@@ -774,8 +774,8 @@ dspark_status launch_tc_d(const AttnArgs& a, int sms, cudaStream_t s, int* parts
 
 }  // namespace
 
-dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, bool e4m3, int sms, cudaStream_t s, int* parts) {
-    if (e4m3) return bf16 ? launch_tc_d<true, true>(a, sms, s, parts) : launch_tc_d<false, true>(a, sms, s, parts);
+dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int kv, int sms, cudaStream_t s, int* parts) {
+    if (kv == kKvE4M3) return bf16 ? launch_tc_d<true, true>(a, sms, s, parts) : launch_tc_d<false, true>(a, sms, s, parts);
     return bf16 ? launch_tc_d<true, false>(a, sms, s, parts) : launch_tc_d<false, false>(a, sms, s, parts);
 }
 

@@ -1,7 +1,7 @@
 """Semi-autoregressive decoding rounds on one GPU, end to end: a draft block, the verify lengths, the target's
 pass over the flattened verify tokens on a paged cache, the verification, and the cache's commit.
 
-    python -m semi_ar_draft_gb300.decode_round [--requests 32] [--rounds 16] [--e4m3]
+    python -m semi_ar_draft_gb300.decode_round [--requests 32] [--rounds 16] [--e4m3 | --int8]
 
 The target here is a toy: two attention layers with random weights (the operators of the library do the
 drafting, scheduling, cache, attention and verification; torch does the projections).  Its purpose is the flow: every
@@ -111,7 +111,9 @@ def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     ap.add_argument("--requests", type=int, default=32)
     ap.add_argument("--rounds", type=int, default=16)
-    ap.add_argument("--e4m3", action="store_true", help="an 8-bit cache")
+    kind = ap.add_mutually_exclusive_group()
+    kind.add_argument("--e4m3", action="store_true", help="an 8-bit cache with one scale a kv head")
+    kind.add_argument("--int8", action="store_true", help="an 8-bit cache with a scale for each block of tokens and kv head")
     a = ap.parse_args(argv)
     V, d, gamma, n = 4096, 64, 8, 24
     max_len = max(512, n + a.rounds * (gamma + 1))
@@ -120,7 +122,7 @@ def main(argv=None):
     g = torch.Generator(device="cuda").manual_seed(3)
     prompts = torch.randint(0, V, (a.requests, n), generator=g, device="cuda", dtype=torch.int32)
     out, mean, cache = generate(target, draft, prompts, a.rounds, budget=a.requests * gamma // 2, max_len=max_len,
-                                kv_dtype=torch.float8_e4m3fn if a.e4m3 else None)
+                                kv_dtype=torch.float8_e4m3fn if a.e4m3 else torch.int8 if a.int8 else None)
     print(f"{a.requests} requests, {a.rounds} rounds: {mean:.2f} tokens a request and round "
           f"({sum(map(len, out))} in all), cache status {cache.status()}, {int(cache.n_free)} pages free")
     print("request 0:", " ".join(map(str, out[0][:16])))

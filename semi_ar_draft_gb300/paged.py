@@ -5,6 +5,7 @@ stack, and per layer a pool of keys and one of values.  A round is
 
     plan(new_len, extra)      pages, slots and offsets of the step's new tokens
     append(layer, k, v)       a layer's new keys and values into their slots
+    read(layer)               (int8 pages) and back, as later steps see them
     attend(layer, q)          a layer's attention of the new tokens
     commit(add_len, extra)    how many of them stay; pages past them go back
 
@@ -29,15 +30,29 @@ def _on(stream):
 
 class PagedCache:
     """requests slots of at most max_blocks pages each; num_pages pages of page_size tokens in all; max_tokens:
-    the most new tokens of any step (a step may say that it has fewer: plan's tokens).  kv_dtype: dtype or
-    torch.float8_e4m3fn, then with k_scale, v_scale [layers, Hk] fp32 (ones if not given)."""
+    the most new tokens of any step (a step may say that it has fewer: plan's tokens).  kv_dtype: dtype;
+    torch.float8_e4m3fn, then with k_scale, v_scale [layers, Hk] fp32 (ones if not given); or torch.int8, whose scales
+    come from the keys and values, one for each block of scale_block tokens (16, or the page where that is smaller) and
+    kv head."""
 
     def __init__(self, requests, num_pages, page_size, max_blocks, layers, Hk, D, max_tokens, dtype=torch.bfloat16,
-                 kv_dtype=None, k_scale=None, v_scale=None, device="cuda"):
+                 kv_dtype=None, k_scale=None, v_scale=None, device="cuda", scale_block=None):
+        self.dtype, self.k_exp, self.v_exp = dtype, None, None
+        if kv_dtype == torch.int8:
+            scale_block = min(16, page_size) if scale_block is None else scale_block
+            if not 1 <= scale_block <= min(128, page_size) or scale_block & (scale_block - 1):
+                raise ValueError(f"scale_block {scale_block}: a power of two up to 128 and to the page")
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("an int8 cache takes its scales from the keys and values")
+        elif scale_block is not None:
+            raise ValueError("scale_block belongs to an int8 cache")
         i32 = {"dtype": torch.int32, "device": device}
         shape = (layers, num_pages, page_size, Hk, D)
         self.k_pages = torch.zeros(shape, dtype=kv_dtype or dtype, device=device)
         self.v_pages = torch.zeros_like(self.k_pages)
+        if kv_dtype == torch.int8:
+            self.k_exp = torch.zeros((layers, num_pages, Hk, page_size // scale_block), dtype=torch.uint8, device=device)
+            self.v_exp = torch.zeros_like(self.k_exp)
         if kv_dtype == torch.float8_e4m3fn:
             ones = torch.ones((layers, Hk), device=device)
             k_scale, v_scale = (ones if s is None else s for s in (k_scale, v_scale))
@@ -87,15 +102,32 @@ class PagedCache:
 
     def append(self, layer, k, v, stream=None):
         """k, v [the plan's tokens, Hk, D]: rows past offsets[-1] have no slot and are skipped."""
+        if self.k_exp is not None:
+            api.cache_append_i8(k, v, self.k_pages[layer], self.v_pages[layer], self.k_exp[layer], self.v_exp[layer], self.slots,
+                                stream, self._error)
+            return
         api.cache_append(k, v, self.k_pages[layer], self.v_pages[layer], self.slots, self.k_scale[layer], self.v_scale[layer],
                          stream)
 
     def attend(self, layer, q, stream=None, **kw):
         """q [the plan's tokens, Hq, D]; kw as for api.paged_attention.  Returns (out, lse or None)."""
+        if self.k_exp is not None:
+            out, lse, _ = api.paged_attention_i8(q, self.k_pages[layer], self.v_pages[layer], self.k_exp[layer],
+                                                 self.v_exp[layer], self.block_table, self.seq_len, self.offsets,
+                                                 max_new=self.max_new, stream=stream, error=self._error, **kw)
+            return out, lse
         out, lse, _ = api.paged_attention(q, self.k_pages[layer], self.v_pages[layer], self.block_table, self.seq_len,
                                           self.offsets, k_scale=self.k_scale[layer], v_scale=self.v_scale[layer],
                                           max_new=self.max_new, stream=stream, error=self._error, **kw)
         return out, lse
+
+    def read(self, layer, slots=None, stream=None):
+        """Keys and values [slots, Hk, D] of an int8 cache as later steps see them, in its 16-bit type: of the plan's new
+        tokens (a prompt's own attention, for instance), or of other slots int64."""
+        if self.k_exp is None:
+            raise ValueError("a cache of 16-bit or e4m3 pages is read as it is: k_pages, v_pages")
+        return api.cache_read_i8(self.k_pages[layer], self.v_pages[layer], self.k_exp[layer], self.v_exp[layer],
+                                 self.slots if slots is None else slots, self.dtype, stream=stream)
 
     def commit(self, add_len=None, extra=0, done=None, stream=None):
         """Keeps add_len[j] + extra of each request's new tokens (none of the whole request where done)."""
@@ -104,7 +136,7 @@ class PagedCache:
                          out=(self._len[1], self._blocks[1], self._free[1]), settled=self._counts[0])
 
     def status(self, stream=None):
-        """The first device error of plan, attend and commit since this was last called, 0 if there was none
+        """The first device error of plan, attend, commit and an int8 cache's append since this was last called, 0 if none
         (synchronises the stream; calls made on others count once they have run)."""
         code = b.dspark_get_device_status(self._error, stream)
         if code:
