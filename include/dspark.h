@@ -524,8 +524,8 @@ dspark_status dspark_paged_attention(const dspark_attention_params* p, const voi
  * word as of dspark_cache_params, or NULL).
  * Slots outside the pool are skipped.  The tokens of one block have to follow one another in slots, in any order,
  * with fewer than 32 skipped entries between two of them (as dspark_cache_plan lays them out); a block that other tokens
- * interrupt ends up with codes and a scale of either part.  Of two tokens of one slot the later one stays; both count
- * for the scale.
+ * interrupt ends up with codes and a scale of either part.  Of two tokens of one slot the later one stays; the earlier may
+ * still count for the scale.
  * Apart from that the same inputs give the same outputs bit for bit.
  *
  * dspark_cache_read_i8 is the way back: k, v [T, Hk, D] dense (dtype), 16-byte aligned, become the values of the T

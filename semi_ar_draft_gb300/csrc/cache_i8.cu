@@ -18,13 +18,12 @@ namespace dspark {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 
 struct I8Args {
     int T, Hk, D, page_shift, block_shift;
-    int chunks;          // D / 8
-    uint32_t chunk_mul;  // i / chunks = i chunk_mul >> 16 for i < 32 chunks
-    int window_shift;    // entries of slots a warp looks after
+    int chunks;          // D / 16
+    int lanes_shift;     // 2^lanes_shift lanes, one for each sixteen values, take a token
+    int heads;           // kv heads a block of threads takes
     long long slots_end, items;
     const uint16_t* x[2];             // keys, values: [T, Hk, D]
     long long x_token[2], x_head[2];  // strides, elements
@@ -47,6 +46,13 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p) {
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
+struct Values {  // sixteen adjacent ones
+    uint4 lo, hi;
+};
+template <bool ALIGNED>
+__device__ __forceinline__ Values load16(const uint16_t* p) {
+    return {load8<ALIGNED>(p), load8<ALIGNED>(p + 8)};
+}
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
     if (BF16) return make_float2(bf16_lo(w), bf16_hi(w));
@@ -62,6 +68,7 @@ __device__ __forceinline__ uint32_t mag_max(uint32_t acc, const uint4& x) {
     acc = __vmaxu2(acc, x.z & 0x7fff7fffu);
     return __vmaxu2(acc, x.w & 0x7fff7fffu);
 }
+__device__ __forceinline__ uint32_t mag_max(uint32_t acc, const Values& x) { return mag_max(mag_max(acc, x.lo), x.hi); }
 // The largest magnitude below `inf` of either half of each word.
 __device__ __forceinline__ uint32_t finite_max(uint32_t acc, const uint4& x, uint32_t inf) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -72,6 +79,10 @@ __device__ __forceinline__ uint32_t finite_max(uint32_t acc, const uint4& x, uin
         if (hi < inf) acc = max(acc, hi);
     }
     return acc;
+}
+
+__device__ __forceinline__ uint32_t finite_max(uint32_t acc, const Values& x, uint32_t inf) {
+    return finite_max(finite_max(acc, x.lo, inf), x.hi, inf);
 }
 
 // Eight values times inv = 2^-e, rounded to whole numbers: 1.5 2^23 added, the low byte is the code.  CLAMP: where the
@@ -96,6 +107,12 @@ __device__ __forceinline__ uint2 quantize8(const uint4& x, float inv) {
     return make_uint2(four(r[0], r[1], r[2], r[3]), four(r[4], r[5], r[6], r[7]));
 }
 
+template <bool BF16, bool CLAMP>
+__device__ __forceinline__ uint4 quantize16(const Values& x, float inv) {
+    const uint2 a = quantize8<BF16, CLAMP>(x.lo, inv), b = quantize8<BF16, CLAMP>(x.hi, inv);
+    return make_uint4(a.x, a.y, b.x, b.y);
+}
+
 // Four codes times 2^-n, n >= 1, to nearest even.
 __device__ __forceinline__ uint32_t shrink4(uint32_t w, int n) {
     if (n > 8) return 0;
@@ -109,172 +126,352 @@ __device__ __forceinline__ uint32_t shrink4(uint32_t w, int n) {
     return y;
 }
 
-// The tokens of one block among the 32 entries of slots from `base` on: n of them, in order, in `list` (entry - base, and
-// the place in the block << 8; bit 31 where a later one of these entries has the same place).  A run of a block's tokens
-// ends where another block's begins.
-struct Members {
-    int n, last;        // last: entry - base of the last one
-    uint32_t place[4];  // places in the block
-    bool more;          // the run may go on behind these entries
-};
-__device__ __forceinline__ Members members(const I8Args& a, long long block, long long base, int before, uint32_t* list) {
-    const int lane = threadIdx.x & 31;
-    const long long slot = base + lane < a.T ? __ldg(a.slots + base + lane) : -1;
-    const bool valid = slot >= 0 && slot < a.slots_end;
-    const uint32_t vm = __ballot_sync(0xffffffffu, valid);
-    uint32_t mm = __ballot_sync(0xffffffffu, valid && (slot >> a.block_shift) == block);
-    const uint32_t other = vm & ~mm;
-    if (other) mm &= (other & (0u - other)) - 1u;
-    if (mm && __ffs(mm) - 1 > before) mm = 0;  // 32 skipped entries or more: another run
-    const bool in = (mm >> lane) & 1u;
-    const int place = (int)(slot & ((1 << a.block_shift) - 1));
-    const uint32_t same = __match_any_sync(0xffffffffu, in ? place : -1 - lane);
-    Members r;
-    r.n = __popc(mm);
-    r.last = 31 - __clz(mm);
-    r.more = !other && mm && base + 32 < a.T;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        r.place[i] = i == 0 || a.block_shift > 5 ? __reduce_or_sync(0xffffffffu, in && (place >> 5) == i ? 1u << (place & 31) : 0u) : 0u;
-    __syncwarp();
-    if (in)
-        list[__popc(mm & ((1u << lane) - 1u))] = (uint32_t)lane | (uint32_t)place << 8 | (31 - __clz(same) != lane ? 0x80000000u : 0u);
-    __syncwarp();
-    return r;
+// The smallest exponent whose 127 steps hold a magnitude, not yet within the range.  127 / 64 is 1.984375: a mantissa up
+// to that stays in its binade's steps, a larger one carries into the exponent.
+template <bool BF16>
+__device__ __forceinline__ int wanted_exponent(uint32_t mag) {
+    return (int)((__float_as_uint(mag_to_float<BF16>(mag)) + 0x1ffffu) >> 23) - 127 - 6;
+}
+template <bool BF16>
+__device__ __forceinline__ int within(int e) {
+    return min(max(e, ExpRange<BF16>::kLo), ExpRange<BF16>::kHi);
 }
 
-// A warp takes keys or values of one kv head of a run: the tokens of a block that follow one another in slots.  It is
-// the warp whose window of slots holds the run's first entry.  The values are read once where the run fits the
-// registers (4 KB: 16 tokens of 128), and a second time, from L2, where it does not.
-constexpr int kHold = 8;
+// Block of an entry of slots, or -1 for one that is skipped.
+__device__ __forceinline__ long long block_at(const I8Args& a, long long t) {
+    if (t < 0 || t >= a.T) return -1;
+    const long long slot = __ldg(a.slots + t);
+    return slot >= 0 && slot < a.slots_end ? slot >> a.block_shift : -1;
+}
+// The first byte of a block's codes and its exponent.
+__device__ __forceinline__ signed char* block_codes(const I8Args& a, int kv, int head, long long block) {
+    const long long slot = block << a.block_shift;
+    return a.pages[kv] + (slot >> a.page_shift) * a.page + (slot & ((1 << a.page_shift) - 1)) * a.token + head * a.head;
+}
+__device__ __forceinline__ unsigned char* block_exp(const I8Args& a, int kv, int head, long long block) {
+    const long long slot = block << a.block_shift;
+    return a.exps[kv] + (slot >> a.page_shift) * a.e_page +
+           (long long)((int)(slot & ((1 << a.page_shift) - 1)) >> a.block_shift) * a.e_block + head * a.e_head;
+}
+// The codes of a block's tokens that `written` (a bit a place) does not name, times 2^-n.  By a warp.
+__device__ void shrink_block(const I8Args& a, signed char* codes, const uint32_t* written, int n) {
+    const int per = a.D / 16;
+    for (int i = threadIdx.x & 31; i < per << a.block_shift; i += 32) {
+        const int p = i / per;
+        if ((written[p >> 5] >> (p & 31)) & 1u) continue;
+        uint4* y = reinterpret_cast<uint4*>(codes + p * a.token + 16 * (i - p * per));
+        uint4 v = *y;
+        v.x = shrink4(v.x, n);
+        v.y = shrink4(v.y, n);
+        v.z = shrink4(v.z, n);
+        v.w = shrink4(v.w, n);
+        *y = v;
+    }
+}
+
+// One run, however long, by a warp: keys or values of one head of the tokens of `block` from entry t0 of slots on, up to
+// another block's token or 32 skipped entries.  (Runs that repeat slots or skip many: the kernel below takes the others.)
+// scratch: [4] words of the warp's.
 template <bool BF16, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) cache_append_i8_kernel(I8Args a) {
-    __shared__ uint32_t s_list[kWarps][32];
+__device__ __noinline__ void append_long_run(const I8Args& a, int kv, int head, long long t0, long long block, uint32_t* scratch) {
     const int lane = threadIdx.x & 31;
-    uint32_t* list = s_list[threadIdx.x >> 5];
+    constexpr uint32_t inf = BF16 ? 0x7f80u : 0x7c00u;
+    const uint16_t* x = a.x[kv] + head * a.x_head[kv];
+    auto each_token = [&](auto&& f) {  // f(entry, place in the block), one after the other
+        int before = 32;
+        for (long long base = t0; base < a.T; base += 32) {
+            const long long at = block_at(a, base + lane);
+            const uint32_t valid = __ballot_sync(0xffffffffu, at >= 0);
+            uint32_t mine = __ballot_sync(0xffffffffu, at == block);
+            const uint32_t other = valid & ~mine;
+            if (other) mine &= (other & (0u - other)) - 1u;
+            if (!mine || __ffs(mine) - 1 > before) return;
+            before = 31 - __clz(mine);
+            for (uint32_t m = mine; m; m &= m - 1) {
+                const long long t = base + __ffs(m) - 1;
+                f(t, (int)(__ldg(a.slots + t) & ((1 << a.block_shift) - 1)));
+            }
+            if (other) return;
+        }
+    };
+    if (lane < 4) scratch[lane] = 0;
+    __syncwarp();
+    uint32_t top = 0, fine = 0;
+    each_token([&](long long t, int place) {
+        if (lane < a.chunks) {
+            const Values v = load16<ALIGNED>(x + t * a.x_token[kv] + 16 * lane);
+            top = mag_max(top, v);
+            fine = finite_max(fine, v, inf);
+        }
+        if (lane == 0) scratch[place >> 5] |= 1u << (place & 31);
+    });
+    __syncwarp();
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+    fine = __reduce_max_sync(0xffffffffu, fine);
+    const bool odd = top >= inf;
+    if (odd && lane == 0 && a.error) record_status(a.error, DSPARK_ERR_NOT_FINITE);
+    unsigned char* exp = block_exp(a, kv, head, block);
+    signed char* codes = block_codes(a, kv, head, block);
+    const int wanted = wanted_exponent<BF16>(fine), old = exponent_of<BF16>(*exp);
+    int e = within<BF16>(wanted);
+    if (!(scratch[0] & 1u)) {
+        e = max(e, old);
+        if (e > old) shrink_block(a, codes, scratch, e - old);
+    }
+    __syncwarp();
+    if (lane == 0) *exp = (unsigned char)(e + 127);
+    each_token([&](long long t, int place) {
+        if (lane < a.chunks)
+            *reinterpret_cast<uint4*>(codes + place * a.token + 16 * lane) =
+                quantize16<BF16, true>(load16<ALIGNED>(x + t * a.x_token[kv] + 16 * lane), two_to(-e));
+        __syncwarp();  // a later token of the same slot lands later
+    });
+}
+
+// A block of threads takes keys and values of a few kv heads of the runs that begin among W entries of slots (a run: the
+// tokens of a block that follow one another, with fewer than 32 skipped entries between).  W is 32 or a block's tokens,
+// so a run that repeats no slot ends within 2 W entries, and all 2 W are looked at; one that does not goes to
+// append_long_run.  A head's values stay in registers between the maximum and the codes (kHold tokens a thread;
+// more are read a second time, from L2).
+constexpr int kHold = 2;
+__host__ __device__ constexpr int window_threads(int W) { return 8 * W; }
+template <bool BF16, bool ALIGNED, int W>
+__global__ void __launch_bounds__(window_threads(W), 1024 / window_threads(W)) cache_append_i8_kernel(I8Args a) {
+    constexpr int kT = window_threads(W);
+    constexpr int kChunksOf32 = 2 * W / 32, kWords = W / 32;
+    __shared__ uint32_t s_list[2 * W];         // entry | place << 8 | run << 16, bit 31: a later token has its slot
+    __shared__ uint32_t s_first[kChunksOf32];  // entries that begin a run, that are not skipped, that are taken
+    __shared__ uint32_t s_valid[kChunksOf32], s_taken[kChunksOf32];
+    __shared__ long long s_block[W], s_start[W];  // of each run
+    __shared__ uint32_t s_place[W][kWords];
+    __shared__ uint32_t s_top[2][W], s_fine[2][W];  // largest magnitude of a run's keys and values, of the finite ones
+    __shared__ int s_exp[2][W], s_grow[2][W];          // exponent | clamp << 16; binades that old codes lose
+    __shared__ uint32_t s_scratch[2][4];
+    __shared__ int s_twice;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr uint32_t inf = BF16 ? 0x7f80u : 0x7c00u;
     wait_primary();
     launch_dependents();
-    const uint32_t per_window = 2u * (uint32_t)a.Hk;
-    for (long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); item < a.items; item += (long long)gridDim.x * kWarps) {
-        const long long window = item / per_window;
-        const int rest = (int)(item - window * per_window), kv = rest & 1, head = rest >> 1;
-        const long long t0 = window << a.window_shift;
-        // The window's entries that begin a run: no token of the same block stands before them, but for fewer than 32
-        // skipped entries.
-        auto block_at = [&](long long t) -> long long {
-            if (t < 0 || t >= a.T) return -1;
-            const long long slot = __ldg(a.slots + t);
-            return slot >= 0 && slot < a.slots_end ? slot >> a.block_shift : -1;
+    const int groups = (a.Hk + a.heads - 1) / a.heads;
+    for (long long item = blockIdx.x; item < a.items; item += gridDim.x) {
+        const long long window = item / groups, t0 = window * W;
+        const int head0 = (int)(item - window * groups) * a.heads, head1 = min(head0 + a.heads, a.Hk);
+        // ---- the runs
+        long long block = -1;
+        uint32_t firsts = 0;
+        if (warp < kChunksOf32) {
+            const long long t = t0 + 32 * warp + lane;
+            block = block_at(a, t);
+            const long long behind = block_at(a, t - 32);
+            const uint32_t bm = __ballot_sync(0xffffffffu, behind >= 0), vm = __ballot_sync(0xffffffffu, block >= 0);
+            const uint32_t below = vm & ((1u << lane) - 1u);
+            const int far = bm ? 31 - __clz(bm) : -1;
+            const long long near_block = __shfl_sync(0xffffffffu, block, below ? 31 - __clz(below) : 0);
+            const long long far_block = __shfl_sync(0xffffffffu, behind, max(far, 0));
+            const long long prev = below ? near_block : (far >= lane ? far_block : -1);
+            firsts = __ballot_sync(0xffffffffu, block >= 0 && block != prev);
+            if (lane == 0) {
+                s_first[warp] = firsts;
+                s_valid[warp] = vm;
+            }
+        }
+        if (tid < W) {
+            s_top[0][tid] = s_top[1][tid] = 0;
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) s_place[tid][j] = 0;
+        }
+        if (tid == 0) s_twice = 0;
+        __syncthreads();
+        int runs = 0, behind = 0;  // runs that begin in the window, and behind it
+#pragma unroll
+        for (int c = 0; c < kChunksOf32; ++c) (c < kWords ? runs : behind) += __popc(s_first[c]);
+        const bool unsure = runs > 0 && behind == 0 && s_valid[kChunksOf32 - 1] != 0 && t0 + 2 * W < a.T;  // may go on
+        const int whole = runs - unsure;
+        int run = -1;
+        if (warp < kChunksOf32) {
+            int n = __popc(firsts & ((2u << lane) - 1u));
+#pragma unroll
+            for (int c = 0; c < kChunksOf32; ++c)
+                if (c < warp) n += __popc(s_first[c]);
+            run = block >= 0 && n <= runs ? n - 1 : -1;
+            if (run >= 0 && ((firsts >> lane) & 1u)) {
+                s_block[run] = block;
+                s_start[run] = t0 + 32 * warp + lane;
+            }
+            if (run >= whole) run = -1;
+            const uint32_t mine = __ballot_sync(0xffffffffu, run >= 0);
+            if (lane == 0) s_taken[warp] = mine;
+            if (run >= 0) {
+                const int place = (int)(__ldg(a.slots + t0 + 32 * warp + lane) & ((1 << a.block_shift) - 1));
+                if (atomicOr(&s_place[run][place >> 5], 1u << (place & 31)) >> (place & 31) & 1u) s_twice = 1;
+            }
+        }
+        __syncthreads();
+        int n = 0;
+        if (warp < kChunksOf32) {
+            int at = __popc(s_taken[warp] & ((1u << lane) - 1u));
+#pragma unroll
+            for (int c = 0; c < kChunksOf32; ++c)
+                if (c < warp) at += __popc(s_taken[c]);
+            if (run >= 0) {
+                const long long t = t0 + 32 * warp + lane, slot = __ldg(a.slots + t);
+                uint32_t later = 0;
+                if (s_twice)
+                    for (int i = 32 * warp + lane + 1; i < 2 * W; ++i)
+                        if ((s_taken[i >> 5] >> (i & 31)) & 1u && __ldg(a.slots + t0 + i) == slot) later = 0x80000000u;
+                s_list[at] = (uint32_t)(32 * warp + lane) | (uint32_t)(slot & ((1 << a.block_shift) - 1)) << 8 | (uint32_t)run << 16 | later;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < kChunksOf32; ++c) n += __popc(s_taken[c]);
+        __syncthreads();
+        const int kv_of = tid / W, run_of = tid - kv_of * W;
+        const bool owner = kv_of < 2 && run_of < whole;  // a thread for each run's keys and one for its values
+        // Keys and values of listed token tid / lanes + u threads / lanes, sixteen of each, for u = 0, 1, ...
+        const int c = tid & ((1 << a.lanes_shift) - 1), m0 = tid >> a.lanes_shift, m_step = kT >> a.lanes_shift;
+        const bool inside = c < a.chunks;
+        auto fetch = [&](int head, int m, Values (&v)[2]) {
+            v[0] = v[1] = Values{};
+            if (inside && m < n) {
+                const long long t = t0 + (s_list[m] & 255u);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) v[kv] = load16<ALIGNED>(a.x[kv] + head * a.x_head[kv] + t * a.x_token[kv] + 16 * c);
+            }
         };
-        const long long bp = block_at(t0 - 32 + lane), bc = block_at(t0 + lane);
-        const uint32_t pm = __ballot_sync(0xffffffffu, bp >= 0), below = __ballot_sync(0xffffffffu, bc >= 0) & ((1u << lane) - 1u);
-        const int far = pm ? 31 - __clz(pm) : -1;
-        const long long near_block = __shfl_sync(0xffffffffu, bc, below ? 31 - __clz(below) : 0);
-        const long long far_block = __shfl_sync(0xffffffffu, bp, max(far, 0));
-        const long long prev = below ? near_block : (far >= lane ? far_block : -1);
-        uint32_t first = __ballot_sync(0xffffffffu, bc >= 0 && bc != prev && lane < (1 << a.window_shift));
+        // A token's largest magnitudes, keys in the upper half, go to its run's.  By whole warps.
+        auto note = [&](int m, const Values (&v)[2]) {
+            const uint32_t k = mag_max(0, v[0]), w = mag_max(0, v[1]);
+            uint32_t top = __vmaxu2(__byte_perm(k, w, 0x3276), __byte_perm(k, w, 0x1054));  // (k hi, w hi), (k lo, w lo)
+            for (int o = (1 << a.lanes_shift) >> 1; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (c == 0 && m < n) {
+                const uint32_t run = (s_list[m] >> 16) & 127u;
+                atomicMax(&s_top[0][run], top >> 16);
+                atomicMax(&s_top[1][run], top & 0xffffu);
+            }
+            return top >> 16 >= inf || (top & 0xffffu) >= inf;
+        };
 #pragma unroll 1
-        for (; first; first &= first - 1) {
-            const int at = __ffs(first) - 1;
-            const long long block = __shfl_sync(0xffffffffu, bc, at);
-            const uint16_t* x = a.x[kv] + head * a.x_head[kv];
-            auto vec = [&](long long base, int i) {  // of the listed tokens' i-th eight values
-                const int m = (int)((uint32_t)i * a.chunk_mul >> 16);
-                return load8<ALIGNED>(x + (base + (list[m] & 31u)) * a.x_token[kv] + 8 * (i - m * a.chunks));
-            };
-            // ---- the largest magnitude
-            long long base = t0 + at;
-            Members r = members(a, block, base, 32, list);
-            const int n0 = r.n * a.chunks;
-            const bool held = !r.more && n0 <= 32 * kHold;
-            uint4 h[kHold];
-            uint32_t acc = 0, place[4] = {r.place[0], r.place[1], r.place[2], r.place[3]};
+        for (int head = head0; head < head1; ++head) {
+            Values h[kHold][2];
+#pragma unroll
+            for (int u = 0; u < kHold; ++u) fetch(head, m0 + u * m_step, h[u]);
+            const uint32_t old_byte = owner ? *block_exp(a, kv_of, head, s_block[run_of]) : 0;
+            // ---- the largest magnitudes
+            bool odd = false;
 #pragma unroll
             for (int u = 0; u < kHold; ++u)
-                h[u] = lane + 32 * u < n0 ? vec(base, lane + 32 * u) : make_uint4(0, 0, 0, 0);
-            unsigned char* exp_at;
-            signed char* row0;  // the block's first token
-            {
-                const long long slot = block << a.block_shift, page = slot >> a.page_shift;
-                const int i = (int)(slot & ((1 << a.page_shift) - 1));
-                exp_at = a.exps[kv] + page * a.e_page + (i >> a.block_shift) * a.e_block + head * a.e_head;
-                row0 = a.pages[kv] + page * a.page + i * a.token + head * a.head;
+                if (u * m_step < n) odd |= note(m0 + u * m_step, h[u]);
+            for (int u = kHold; u * m_step < n; ++u) {
+                Values v[2];
+                fetch(head, m0 + u * m_step, v);
+                odd |= note(m0 + u * m_step, v);
             }
-            const uint32_t old_byte = *exp_at;
-#pragma unroll
-            for (int u = 0; u < kHold; ++u) acc = mag_max(acc, h[u]);
-            auto rest_of = [&](auto&& f) {  // every listed value past the held ones, chunk of entries by chunk
-                for (int i = lane + 32 * kHold; i < n0; i += 32) f(vec(base, i));
-                for (Members y = r; y.more;) {
-                    base += 32;
-                    y = members(a, block, base, y.last, list);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) place[j] |= y.place[j];
-                    for (int i = lane; i < y.n * a.chunks; i += 32) f(vec(base, i));
-                }
-                if (r.more) {
-                    base = t0 + at;
-                    members(a, block, base, 32, list);
-                }
-            };
-            if (!held) rest_of([&](const uint4& v) { acc = mag_max(acc, v); });
-            constexpr uint32_t inf = BF16 ? 0x7f80u : 0x7c00u;
-            uint32_t top = __reduce_max_sync(0xffffffffu, max(acc & 0xffffu, acc >> 16));
-            const bool odd = top >= inf;
+            odd = __syncthreads_or(odd);
             if (odd) {  // of the finite ones
-                acc = 0;
+                if (tid < W) s_fine[0][tid] = s_fine[1][tid] = 0;
+                __syncthreads();
+                for (int m = m0; m < n; m += m_step) {
+                    Values v[2];
+                    fetch(head, m, v);
 #pragma unroll
-                for (int u = 0; u < kHold; ++u) acc = finite_max(acc, h[u], inf);
-                if (!held) rest_of([&](const uint4& v) { acc = finite_max(acc, v, inf); });
-                top = __reduce_max_sync(0xffffffffu, acc);
-                if (lane == 0 && a.error) record_status(a.error, DSPARK_ERR_NOT_FINITE);
-            }
-            // ---- the scale.  127 / 64 is 1.984375: a mantissa up to that stays in its binade's steps, a larger one
-            // carries into the exponent.
-            const int wanted = (int)((__float_as_uint(mag_to_float<BF16>(top)) + 0x1ffffu) >> 23) - 127 - 6;
-            int e = min(max(wanted, ExpRange<BF16>::kLo), ExpRange<BF16>::kHi);
-            const int old = exponent_of<BF16>(old_byte);
-            const bool begun = place[0] & 1u;
-            if (!begun) e = max(e, old);
-            if (!begun && e > old) {  // the block's other tokens
-                const int per = a.D / 16;
-                for (int i = lane; i < per << a.block_shift; i += 32) {
-                    const int p = i / per;
-                    uint32_t word = place[0];  // (by selects: an indexed register array would go to local memory)
-                    if (p >= 32) word = p >= 96 ? place[3] : (p >= 64 ? place[2] : place[1]);
-                    if ((word >> (p & 31)) & 1u) continue;
-                    uint4* y = reinterpret_cast<uint4*>(row0 + p * a.token + 16 * (i - p * per));
-                    uint4 v = *y;
-                    v.x = shrink4(v.x, e - old);
-                    v.y = shrink4(v.y, e - old);
-                    v.z = shrink4(v.z, e - old);
-                    v.w = shrink4(v.w, e - old);
-                    *y = v;
+                    for (int kv = 0; kv < 2; ++kv) atomicMax(&s_fine[kv][(s_list[m] >> 16) & 127u], finite_max(0, v[kv], inf));
                 }
+                if (tid == 0 && a.error) record_status(a.error, DSPARK_ERR_NOT_FINITE);
+                __syncthreads();
             }
-            __syncwarp();  // (every lane has read the old exponent)
-            if (lane == 0) *exp_at = (unsigned char)(e + 127);
+            // ---- the scales
+            if (owner) {
+                const int wanted = wanted_exponent<BF16>(odd ? s_fine[kv_of][run_of] : s_top[kv_of][run_of]);
+                int e = within<BF16>(wanted), grow = 0;
+                if (!(s_place[run_of][0] & 1u)) {
+                    const int old = exponent_of<BF16>(old_byte);
+                    e = max(e, old);
+                    grow = e - old;
+                }
+                s_grow[kv_of][run_of] = grow;
+                s_exp[kv_of][run_of] = (e & 0xffff) | (odd || wanted > ExpRange<BF16>::kHi ? 0x10000 : 0);
+                s_top[kv_of][run_of] = 0;
+                *block_exp(a, kv_of, head, s_block[run_of]) = (unsigned char)(e + 127);
+            }
+            __syncthreads();
             // ---- the codes
-            const float inv = two_to(-e);
-            const bool clamp = odd || wanted > ExpRange<BF16>::kHi;
-            auto put = [&](int i, const uint4& v) {
-                const int m = (int)((uint32_t)i * a.chunk_mul >> 16);
-                const uint32_t it = list[m];
-                const uint2 y = clamp ? quantize8<BF16, true>(v, inv) : quantize8<BF16, false>(v, inv);
-                if (!(it >> 31)) *reinterpret_cast<uint2*>(row0 + (long long)((it >> 8) & 127u) * a.token + 8 * (i - m * a.chunks)) = y;
+            auto put = [&](int m, const Values (&v)[2]) {
+                const uint32_t it = s_list[m];
+                const int run = (int)((it >> 16) & 127u);
+                if (it >> 31) return;
+                const long long slot = (s_block[run] << a.block_shift) + (int)((it >> 8) & 127u);
+                const long long to = (slot >> a.page_shift) * a.page + (slot & ((1 << a.page_shift) - 1)) * a.token + head * a.head + 16 * c;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int e = s_exp[kv][run];
+                    const float inv = two_to(-(int)(short)(e & 0xffff));
+                    *reinterpret_cast<uint4*>(a.pages[kv] + to) =
+                        e >> 16 & 1 ? quantize16<BF16, true>(v[kv], inv) : quantize16<BF16, false>(v[kv], inv);
+                }
             };
 #pragma unroll
             for (int u = 0; u < kHold; ++u)
-                if (lane + 32 * u < n0) put(lane + 32 * u, h[u]);
-            if (!held) {
-                for (int i = lane + 32 * kHold; i < n0; i += 32) put(i, vec(base, i));
-                for (Members y = r; y.more;) {
-                    base += 32;
-                    y = members(a, block, base, y.last, list);  // (a warp's barrier: later tokens of a slot land later)
-                    for (int i = lane; i < y.n * a.chunks; i += 32) put(i, vec(base, i));
+                if (inside && m0 + u * m_step < n) put(m0 + u * m_step, h[u]);
+            for (int m = m0 + kHold * m_step; inside && m < n; m += m_step) {
+                Values v[2];
+                fetch(head, m, v);
+                put(m, v);
+            }
+            for (int k = warp; k < 2 * whole; k += kT / 32) {
+                const int kv = k >= whole, r = k - kv * whole, grow = s_grow[kv][r];
+                if (grow > 0) shrink_block(a, block_codes(a, kv, head, s_block[r]), s_place[r], grow);
+            }
+            if (unsure && warp < 2) append_long_run<BF16, ALIGNED>(a, warp, head, s_start[runs - 1], s_block[runs - 1], s_scratch[warp]);
+        }  // (the next head's maxima are noted after every thread has passed the second barrier, its scales after the first)
+        __syncthreads();
+    }
+}
+
+// A scale for every token: nothing of the block is older.  2^lanes_shift lanes take keys and values of a (token, kv head); the token is left out where the next entry that is not skipped has its slot.
+template <bool BF16, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) cache_append_i8_token_kernel(I8Args a) {
+    wait_primary();
+    launch_dependents();
+    const int lanes = 1 << a.lanes_shift;
+    const long long stride = (long long)gridDim.x * kThreads;
+    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; (i & ~31ll) < a.items << a.lanes_shift; i += stride) {
+        const long long pair = i >> a.lanes_shift;
+        const int c = (int)i & (lanes - 1);
+        const long long t = min(pair, a.items - 1) / a.Hk;
+        const int h = (int)(min(pair, a.items - 1) - t * a.Hk);
+        const long long slot = __ldg(a.slots + t);
+        bool live = pair < a.items && c < a.chunks && slot >= 0 && slot < a.slots_end;
+        Values x[2] = {};
+        if (live) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) x[kv] = load16<ALIGNED>(a.x[kv] + t * a.x_token[kv] + h * a.x_head[kv] + 16 * c);
+            for (long long next = t + 1; next < a.T && next <= t + 32; ++next) {
+                const long long y = __ldg(a.slots + next);
+                if (y >= 0 && y < a.slots_end) {
+                    live = y != slot;
+                    break;
                 }
             }
-            __syncwarp();
+        }
+        const long long page = slot >> a.page_shift;
+        const int at = (int)(slot & ((1 << a.page_shift) - 1));
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            constexpr uint32_t inf = BF16 ? 0x7f80u : 0x7c00u;
+            uint32_t top = mag_max(0, x[kv]);
+            top = max(top & 0xffffu, top >> 16);
+            for (int o = lanes >> 1; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const bool odd = top >= inf;
+            if (__any_sync(0xffffffffu, odd)) {
+                top = finite_max(0, x[kv], inf);
+                for (int o = lanes >> 1; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                if (odd && a.error) record_status(a.error, DSPARK_ERR_NOT_FINITE);
+            }
+            const int wanted = wanted_exponent<BF16>(top), e = within<BF16>(wanted);
+            if (!live) continue;
+            *reinterpret_cast<uint4*>(a.pages[kv] + page * a.page + at * a.token + h * a.head + 16 * c) =
+                odd || wanted > ExpRange<BF16>::kHi ? quantize16<BF16, true>(x[kv], two_to(-e)) : quantize16<BF16, false>(x[kv], two_to(-e));
+            if (c == 0) a.exps[kv][page * a.e_page + at * a.e_block + h * a.e_head] = (unsigned char)(e + 127);
         }
     }
 }
@@ -338,6 +535,15 @@ __global__ void __launch_bounds__(kThreads) cache_read_i8_kernel(ReadArgs a) {
     }
 }
 
+template <bool BF16>
+auto append_kernel(bool aligned, int W) {
+    if (aligned)
+        return W == 32 ? cache_append_i8_kernel<BF16, true, 32>
+                       : (W == 64 ? cache_append_i8_kernel<BF16, true, 64> : cache_append_i8_kernel<BF16, true, 128>);
+    return W == 32 ? cache_append_i8_kernel<BF16, false, 32>
+                   : (W == 64 ? cache_append_i8_kernel<BF16, false, 64> : cache_append_i8_kernel<BF16, false, 128>);
+}
+
 dspark_status check_i8(const dspark_append_params* p, const dspark_block_exponents* x, const void* k_pages, const void* v_pages) {
     if (!p || !x || p->T < 0 || p->Hk < 1 || p->D < 1 || p->num_pages < 1 || page_shift_of(p->page_size) < 0)
         return DSPARK_ERR_INVALID_ARG;
@@ -382,8 +588,8 @@ extern "C" dspark_status dspark_cache_append_i8(const dspark_append_params* p, c
     a.D = p->D;
     a.page_shift = page_shift_of(p->page_size);
     a.block_shift = log2_of(x->block);
-    a.chunks = p->D / 8;
-    a.chunk_mul = (65536u + a.chunks - 1) / a.chunks;
+    a.chunks = p->D / 16;
+    a.lanes_shift = log2_of(a.chunks);
     a.slots_end = (long long)p->num_pages * p->page_size;
     a.x[0] = static_cast<const uint16_t*>(k);
     a.x[1] = static_cast<const uint16_t*>(v);
@@ -403,19 +609,29 @@ extern "C" dspark_status dspark_cache_append_i8(const dspark_append_params* p, c
     a.e_head = x->head_stride;
     a.slots = slots;
     a.error = error;
-    // A warp looks after one entry of slots, or, where that would be more warps than are resident at once, after up to a
-    // block's worth (most of a prompt's entries begin no run).
-    a.window_shift = 0;
-    auto items = [&] { return ((long long)a.T + (1 << a.window_shift) - 1 >> a.window_shift) * 2 * a.Hk; };
-    while (a.window_shift < 5 && a.window_shift < a.block_shift && items() > (long long)sms * 32) ++a.window_shift;
-    a.items = items();
     const bool aligned = !((((uintptr_t)k | (uintptr_t)v) & 15u) || (a.x_token[0] | a.x_token[1] | a.x_head[0] | a.x_head[1]) % 8);
-    const long long want = (a.items + kWarps - 1) / kWarps, most = (long long)sms * 16;
-    const int blocks = (int)(want < most ? want : most);
     const bool bf16 = p->dtype == DSPARK_BF16;
-    const auto kernel = bf16 ? (aligned ? cache_append_i8_kernel<true, true> : cache_append_i8_kernel<true, false>)
-                             : (aligned ? cache_append_i8_kernel<false, true> : cache_append_i8_kernel<false, false>);
-    if (launch_overlapped(kernel, blocks, kThreads, 0, reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess) return DSPARK_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto blocks_for = [&](long long threads) {
+        const long long want = (threads + kThreads - 1) / kThreads, most = (long long)sms * 16;
+        return (int)(want < most ? want : most);
+    };
+    cudaError_t e;
+    if (x->block == 1) {
+        a.items = (long long)a.T * a.Hk;
+        const auto kernel = bf16 ? (aligned ? cache_append_i8_token_kernel<true, true> : cache_append_i8_token_kernel<true, false>)
+                                 : (aligned ? cache_append_i8_token_kernel<false, true> : cache_append_i8_token_kernel<false, false>);
+        e = launch_overlapped(kernel, blocks_for(a.items << a.lanes_shift), kThreads, 0, s, a);
+    } else {
+        const int W = x->block > 64 ? 128 : (x->block > 32 ? 64 : 32);
+        const long long windows = ((long long)a.T + W - 1) / W, most = (long long)sms * (2048 / window_threads(W));
+        a.heads = 1;
+        while (a.heads < a.Hk && windows * ((a.Hk + a.heads - 1) / a.heads) > 2 * most) a.heads *= 2;
+        a.items = windows * ((a.Hk + a.heads - 1) / a.heads);
+        const auto kernel = bf16 ? append_kernel<true>(aligned, W) : append_kernel<false>(aligned, W);
+        e = launch_overlapped(kernel, (int)(a.items < most ? a.items : most), window_threads(W), 0, s, a);
+    }
+    if (e != cudaSuccess) return DSPARK_ERR_CUDA;
     note_launch();
     return DSPARK_OK;
 }

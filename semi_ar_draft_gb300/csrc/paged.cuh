@@ -317,10 +317,10 @@ __device__ __forceinline__ uint32_t i8x2_to_half2(uint32_t offset_word) {  // th
 }
 constexpr int kBytes01 = 0x4140, kBytes23 = 0x4342, kBytes02 = 0x4240, kBytes13 = 0x4341;
 
-// The exponents of a key's block, of the keys (low byte) and the values: at is its place in the page.
-__device__ __forceinline__ uint32_t block_exponents(const AttnArgs& a, int page, int at, int head) {
-    const long long e = page * a.exp.page + (long long)(at >> a.exp.shift) * a.exp.block + head * a.exp.head;
-    return (uint32_t)__ldg(a.exp.k + e) | (uint32_t)__ldg(a.exp.v + e) << 8;
+// Where the exponents of a key's block lie: at is its place in the page.  (Both bytes are kept as they arrive until they
+// are used: putting them together at once would wait for them.)
+__device__ __forceinline__ long long exponents_at(const AttnArgs& a, int page, int at, int head) {
+    return page * a.exp.page + (long long)(at >> a.exp.shift) * a.exp.block + head * a.exp.head;
 }
 
 // Probabilities as halves are taken against a reference 2^7 below the running maximum's (which follows within 2^8, so
@@ -347,5 +347,8 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // Row tiles of 128 on the fifth-generation tensor cores (paged_attn_tc.cu); needs 16-byte
 // aligned query rows.
 dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int kv, int sms, cudaStream_t s, int* parts);
+
+// Row tiles of 8 or 16 over int8 pools (paged_attn_i8.cu).
+dspark_status launch_attn_i8(const AttnArgs& a, bool bf16, int row_tile, int sms, cudaStream_t s, int* parts);
 
 }  // namespace dspark

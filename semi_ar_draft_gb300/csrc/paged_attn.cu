@@ -19,6 +19,7 @@
 #include <cuda_fp8.h>
 
 #include "host_util.h"
+#include "mma16.cuh"
 #include "paged.cuh"
 #include "pdl.cuh"
 #include "tc05.cuh"
@@ -29,31 +30,6 @@ namespace {
 constexpr int kRows = 16;
 constexpr int kTcRows = 128;  // rows of a tile of launch_attn_tc
 
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-template <bool BF16>
-__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if (BF16)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 // Two e4m3 values (low 16 bits) as two halves.
 __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t w) {
     uint32_t r;
@@ -66,9 +42,8 @@ __device__ __forceinline__ float half_bits_to_f32(uint32_t w) {
     return __half2float(__ushort_as_half((unsigned short)w));
 }
 
-template <int KV, int DP>
+template <bool F8, int DP>
 struct Rows16 {
-    static constexpr bool F8 = KV != kKv16;  // 8-bit pools
     static constexpr int kEsz = F8 ? 1 : 2;
     static constexpr int kKeys = F8 ? 32 : 16;           // keys of a warp's slice
     // (heads of 256, one block a multiprocessor: six warps of two stages, 204 us for 16 kv heads of 192 over 32
@@ -111,12 +86,11 @@ __device__ __forceinline__ void store_out4(const AttnArgs& a, long long row, int
     *reinterpret_cast<uint2*>(a.out + ((size_t)row * a.D + col) * 2) = w;
 }
 
-template <bool BF16, int KV, int DP>
-__global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlocksPerSm) attn_rows16_kernel(AttnArgs a) {
-    using C = Rows16<KV, DP>;
-    constexpr bool F8 = KV != kKv16, I8 = KV == kKvI8;
+template <bool BF16, bool F8, int DP>
+__global__ void __launch_bounds__(Rows16<F8, DP>::kThreads, Rows16<F8, DP>::kBlocksPerSm) attn_rows16_kernel(AttnArgs a) {
+    using C = Rows16<F8, DP>;
     constexpr int kThreads = C::kThreads, kWarps = C::kWarps;
-    constexpr bool MB = BF16 && !F8;  // an 8-bit cache is multiplied as halves, which hold e4m3 and int8 exactly
+    constexpr bool MB = BF16 && !F8;  // an 8-bit cache is multiplied as halves, which hold e4m3 exactly
     constexpr int KT = C::kKeys / 8;  // key n-tiles of a slice
     constexpr int DT = DP / 8;        // output n-tiles
     constexpr int KS = DP / 16;       // k-steps over the head dimension
@@ -163,16 +137,12 @@ __global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlo
         }
     };
     if (warp == 0 && !ld.done()) touch_queries();
-    // int8: the exponents of this lane's key of the slices on their way; exps[0] are those of the slice in hand
-    uint32_t exps[I8 ? C::kStages : 1];
-    auto load_step = [&](int queue) {
-        if (I8) exps[I8 ? queue : 0] = 0;
+    auto load_step = [&]() {
         if (!ld.done() && slice_key(ld) < ld.r.seq) {
             const int key = slice_key(ld) + lane;
             const bool live = lane < C::kKeys && key < ld.r.seq && key >= ld.r.lo;
             const bool found = live && pid >= 0 && pid < a.num_pages;
             if (live && !found) err = DSPARK_ERR_CACHE;
-            if (I8 && found) exps[I8 ? queue : 0] = block_exponents(a, pid, key & ((1 << a.page_shift) - 1), ld.item / ld.rts);
             const long long off = found ? pid * a.page + (key & ((1 << a.page_shift) - 1)) * a.token +
                                               (ld.item / ld.rts) * a.head
                                         : -1;
@@ -199,7 +169,7 @@ __global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlo
         }
     };
 #pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) load_step(i + 1);
+    for (int i = 0; i < C::kStages - 1; ++i) load_step();
 
     // ---- arithmetic
     AttnWalk w = walk_begin(a, start, kRows, C::kKeyTile, C::kExtra);
@@ -209,7 +179,6 @@ __global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlo
     uint32_t qf[C::kQInSmem ? 1 : KS][4];
     const float cap_out = a.softcap * kLog2e;
     float m[2], l[2], row_scale[2];
-    float mv[2];  // int8: reference of the weighted probabilities
     int see_lo[2], see_hi[2], all_lo = 0, all_hi = 0, rows = 0, head = 0, row0 = 0, seg_first = 0;
     bool fresh = true;
     int st = 0;
@@ -290,11 +259,11 @@ __global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlo
                 const bool real = row < rows;
                 see_lo[r] = real ? attn_see_lo(a, w.r, token) : 0;
                 see_hi[r] = real ? attn_see_hi(a, w.r, token) : 0;
-                m[r] = mv[r] = -CUDART_INF_F;
+                m[r] = -CUDART_INF_F;
                 l[r] = 0.f;
                 // to the log2 domain, or to the cap's exponent
                 row_scale[r] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale *
-                               (KV == kKvE4M3 && a.k_scale ? __ldg(a.k_scale + head) : 1.f);
+                               (F8 && a.k_scale ? __ldg(a.k_scale + head) : 1.f);
                 if (kRescale) row_scale[r] *= __uint_as_float((uint32_t)(127 - raise(row)) << 23);
             }
             if (!C::kQInSmem) {
@@ -307,11 +276,7 @@ __global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlo
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
         }
-        if (I8) {
-#pragma unroll
-            for (int i = 0; i + 1 < C::kStages; ++i) exps[I8 ? i : 0] = exps[I8 ? i + 1 : 0];
-        }
-        load_step(C::kStages - 1);
+        load_step();
         cp_async_wait_group<C::kStages - 1>();
         __syncwarp();
         const int key0 = slice_key(w);
@@ -335,14 +300,8 @@ __global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlo
                 if (F8) {
                     ldsm4(b, kb + C::at(lane, ks));  // matrix i: keys 8 i .. 8 i + 7, k = 16 ks .. + 15
 #pragma unroll
-                    for (int i = 0; i < KT; ++i) {
-                        if (I8) {
-                            const uint32_t u = b[i] ^ 0x80808080u;
-                            mma16<MB>(s[i], q4, i8x2_to_half2<kBytes01>(u), i8x2_to_half2<kBytes23>(u));
-                        } else {
-                            mma16<MB>(s[i], q4, e4m3x2_to_half2(b[i]), e4m3x2_to_half2(b[i] >> 16));
-                        }
-                    }
+                    for (int i = 0; i < KT; ++i)
+                        mma16<MB>(s[i], q4, e4m3x2_to_half2(b[i]), e4m3x2_to_half2(b[i] >> 16));
                 } else {
                     const int row = (lane & 7) + ((lane >> 4) << 3);
                     ldsm4(b, kb + C::at(row, 2 * ks + ((lane >> 3) & 1)));
@@ -350,34 +309,15 @@ __global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlo
                     mma16<MB>(s[1], q4, b[2], b[3]);
                 }
             }
-            // int8: each key's 2^e (as bf16, in the low half) and its values' e (as bf16), from the lane of the key's
-            // number: this lane's are keys 8 i + 2 t and 8 i + 2 t + 1.
-            uint32_t with[I8 ? KT : 1][2];
-            if (I8) {
-                const uint32_t mine = (uint32_t)(exponent_of<BF16>(exps[0] & 0xffu) + 127) << 7 |
-                                      (__float_as_uint((float)exponent_of<BF16>(exps[0] >> 8)) & 0xffff0000u);
-#pragma unroll
-                for (int i = 0; i < KT; ++i)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) with[I8 ? i : 0][c] = __shfl_sync(0xffffffffu, mine, 8 * i + 2 * t + c);
-            }
-            auto key_scale = [&](int i, int c) { return __uint_as_float(with[I8 ? i : 0][c] << 16); };
-            auto value_exp = [&](int i, int c) { return __uint_as_float(with[I8 ? i : 0][c] & 0xffff0000u); };
             // scores in the log2 domain, hidden ones -inf
             const bool edge = key0 < all_lo || key0 + C::kKeys > all_hi;
-            float mx[2] = {-CUDART_INF_F, -CUDART_INF_F}, mz[2] = {-CUDART_INF_F, -CUDART_INF_F};
+            float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
             for (int i = 0; i < KT; ++i)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     float2 x = make_float2(s[i][2 * r] * row_scale[r], s[i][2 * r + 1] * row_scale[r]);
-                    if (I8) {
-                        x.x *= key_scale(i, 0);
-                        x.y *= key_scale(i, 1);
-                        if (a.softcap > 0.f) x = softcap2(x.x, x.y, 1.f, cap_out);
-                    } else if (a.softcap > 0.f) {
-                        x = softcap2(s[i][2 * r], s[i][2 * r + 1], row_scale[r], cap_out);
-                    }
+                    if (a.softcap > 0.f) x = softcap2(s[i][2 * r], s[i][2 * r + 1], row_scale[r], cap_out);
                     if (edge) {
                         const int key = key0 + 8 * i + 2 * t;
                         if (key < see_lo[r] || key >= see_hi[r]) x.x = -CUDART_INF_F;
@@ -386,7 +326,6 @@ __global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlo
                     s[i][2 * r] = x.x;
                     s[i][2 * r + 1] = x.y;
                     mx[r] = fmaxf(mx[r], fmaxf(x.x, x.y));
-                    if (I8) mz[r] = fmaxf(mz[r], fmaxf(x.x + value_exp(i, 0), x.y + value_exp(i, 1)));
                 }
             bool grow = false;
 #pragma unroll
@@ -394,11 +333,6 @@ __global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlo
                 mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
                 mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
                 grow |= mx[r] > m[r] + 8.f;
-                if (I8) {
-                    mz[r] = fmaxf(mz[r], __shfl_xor_sync(0xffffffffu, mz[r], 1));
-                    mz[r] = fmaxf(mz[r], __shfl_xor_sync(0xffffffffu, mz[r], 2));
-                    grow |= mz[r] > mv[r] + 8.f;
-                }
             }
             // The reference of the exponents follows the maximum only when it is 2^8 behind (values up
             // to 2^8 lose nothing), so most slices do not touch the output.
@@ -409,36 +343,27 @@ __global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlo
                     const float f = mn == m[r] ? 1.f : ex2(m[r] - mn);  // m = -inf: 0
                     m[r] = mn;
                     l[r] *= f;
-                    float fo = f;
-                    if (I8) {
-                        const float zn = fmaxf(mv[r], mz[r]);
-                        fo = zn == mv[r] ? 1.f : ex2(mv[r] - zn);
-                        mv[r] = zn;
-                    }
 #pragma unroll
                     for (int i = 0; i < DT; ++i) {
-                        o[i][2 * r] *= fo;
-                        o[i][2 * r + 1] *= fo;
+                        o[i][2 * r] *= f;
+                        o[i][2 * r + 1] *= f;
                     }
                 }
             }
             constexpr float kUp = ProbScale<MB>::kBits;
             const float ref[2] = {m[0] == -CUDART_INF_F ? 0.f : m[0] - kUp, m[1] == -CUDART_INF_F ? 0.f : m[1] - kUp};
-            const float ref_v[2] = {mv[0] == -CUDART_INF_F ? 0.f : mv[0] - kUp, mv[1] == -CUDART_INF_F ? 0.f : mv[1] - kUp};
 #pragma unroll
             for (int i = 0; i < KT; ++i)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const float x = s[i][c];
-                    s[i][c] = ex2(x - ref[c >> 1]);
+                    s[i][c] = ex2(s[i][c] - ref[c >> 1]);
                     l[c >> 1] += s[i][c];
-                    if (I8) s[i][c] = ex2(x + value_exp(i, c & 1) - ref_v[c >> 1]);
                 }
             // A hidden key's value must not reach a row that does not see it, even as 0 x inf.  Values of
             // an edge slice that are not finite (never, in a healthy cache) take the long way: products key by
             // key, over the rows that see it.
             bool odd = false;
-            if (edge && !I8) {  // (codes are finite)
+            if (edge) {
                 uint32_t acc = 0;
                 const uint4* vs = reinterpret_cast<const uint4*>(ring + st * C::kStage + C::kHalf);
                 for (int i = lane; i < C::kHalf / 16; i += 32) {
@@ -467,12 +392,6 @@ __global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlo
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
                                 // bytes (k0 d0, k0 d1, k1 d0, k1 d1) -> (k0 d0, k1 d0 | k0 d1, k1 d1)
-                                if (I8) {
-                                    const uint32_t x = b[2 * u] ^ 0x80808080u, y = b[2 * u + 1] ^ 0x80808080u;
-                                    mma16<MB>(o[2 * (c + u)], p, i8x2_to_half2<kBytes02>(x), i8x2_to_half2<kBytes02>(y));
-                                    mma16<MB>(o[2 * (c + u) + 1], p, i8x2_to_half2<kBytes13>(x), i8x2_to_half2<kBytes13>(y));
-                                    continue;
-                                }
                                 const uint32_t x = __byte_perm(b[2 * u], 0, 0x3120);
                                 const uint32_t y = __byte_perm(b[2 * u + 1], 0, 0x3120);
                                 mma16<MB>(o[2 * (c + u)], p, e4m3x2_to_half2(x), e4m3x2_to_half2(y));
@@ -528,14 +447,6 @@ __global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlo
             float* mine_o = reinterpret_cast<float*>(ring + st * C::kStage);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                if (I8) {  // to the reference of the sums, in two steps: 2^e may be as large as fp32's numbers
-                    const float f = m[r] == -CUDART_INF_F ? 1.f : ex2(0.5f * (mv[r] - m[r]));
-#pragma unroll
-                    for (int i = 0; i < DT; ++i) {
-                        o[i][2 * r] = o[i][2 * r] * f * f;
-                        o[i][2 * r + 1] = o[i][2 * r + 1] * f * f;
-                    }
-                }
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
                 const int row = g + 8 * r, x = (row & 3) << 3;
@@ -555,7 +466,7 @@ __global__ void __launch_bounds__(Rows16<KV, DP>::kThreads, Rows16<KV, DP>::kBlo
             __syncthreads();
             const bool whole = last_of_item && seg_first == 0;
             const int slot = 2 * part + (seg_first == 0 ? kHead : kTail);
-            const float vscale = KV == kKvE4M3 && a.v_scale ? __ldg(a.v_scale + head) : 1.f;
+            const float vscale = F8 && a.v_scale ? __ldg(a.v_scale + head) : 1.f;
             for (int i = tid; i < rows * (DP / 4); i += kThreads) {
                 const int row = i / (DP / 4), col = 4 * (i % (DP / 4));
                 float mm = -CUDART_INF_F, ll = 0.f;
@@ -738,11 +649,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
     }
 }
 
-template <bool BF16, int KV, int DP>
+template <bool BF16, bool F8, int DP>
 dspark_status launch_rows16(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
-    using C = Rows16<KV, DP>;
+    using C = Rows16<F8, DP>;
     int per_sm = 0;
-    auto fn = attn_rows16_kernel<BF16, KV, DP>;
+    auto fn = attn_rows16_kernel<BF16, F8, DP>;
     if (prepare_kernel((const void*)fn, C::kSmem, C::kThreads, &per_sm) != cudaSuccess || per_sm < 1)
         return DSPARK_ERR_CUDA;
     int n = sms * (per_sm < C::kBlocksPerSm ? per_sm : C::kBlocksPerSm);
@@ -751,17 +662,11 @@ dspark_status launch_rows16(const AttnArgs& a, int sms, cudaStream_t s, int* par
     return launch_overlapped(fn, n, C::kThreads, C::kSmem, s, a) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
-template <bool BF16, int KV>
+template <bool BF16, bool F8>
 dspark_status launch_rows16_d(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
-    if (a.D <= 64) return launch_rows16<BF16, KV, 64>(a, sms, s, parts);
-    if (a.D <= 128) return launch_rows16<BF16, KV, 128>(a, sms, s, parts);
-    return launch_rows16<BF16, KV, 256>(a, sms, s, parts);
-}
-template <bool BF16>
-dspark_status launch_rows16_kv(const AttnArgs& a, int kv, int sms, cudaStream_t s, int* parts) {
-    if (kv == kKvI8) return launch_rows16_d<BF16, kKvI8>(a, sms, s, parts);
-    if (kv == kKvE4M3) return launch_rows16_d<BF16, kKvE4M3>(a, sms, s, parts);
-    return launch_rows16_d<BF16, kKv16>(a, sms, s, parts);
+    if (a.D <= 64) return launch_rows16<BF16, F8, 64>(a, sms, s, parts);
+    if (a.D <= 128) return launch_rows16<BF16, F8, 128>(a, sms, s, parts);
+    return launch_rows16<BF16, F8, 256>(a, sms, s, parts);
 }
 
 struct AttnWs {
@@ -774,9 +679,13 @@ struct AttnWs {
 //   e4m3     mean 35 rows 69 / 85 and 36 / 42; 68 rows: 80 / 58; mean 70: 159 / 101; 119 rows: 254 / 92
 // (an 8-bit tile has to be widened for the wide kernel, so it needs more rows to pay).
 bool wide_rows(const dspark_attention_params* p) {
-    if (p->kv_dtype == DSPARK_I8) return false;
     const long long G = p->Hq / p->Hk, limit = p->kv_dtype == p->dtype ? kRows : 48;
     return G * p->T > limit * p->B && (p->max_new <= 0 || G * p->max_new > limit);
+}
+// Rows of a tile of launch_attn_i8.
+int i8_row_tile(const dspark_attention_params* p) {
+    const long long G = p->Hq / p->Hk, rows = p->max_new > 0 ? G * p->max_new : (G * p->T + p->B - 1) / p->B;
+    return rows <= 8 ? 8 : 16;
 }
 AttnWs attn_ws(const dspark_attention_params* p) {
     const size_t rows = wide_rows(p) ? (size_t)2 * kMaxTcParts * kTcRows : (size_t)2 * kMaxParts * kRows;
@@ -874,15 +783,19 @@ dspark_status paged_attention(const dspark_attention_params* p, const dspark_blo
     a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
     a.part_o = reinterpret_cast<float*>(ws + w.o);
     const bool bf16 = p->dtype == DSPARK_BF16;
-    a.sum_scale = bf16 && kv == kKv16 ? ProbScale<true>::kInverse : ProbScale<false>::kInverse;
     int parts = 0;
     const bool tc = wide_rows(p) && a.q_vec;
-    const dspark_status ls = tc     ? launch_attn_tc(a, bf16, kv, sms, s, &parts)
-                             : bf16 ? launch_rows16_kv<true>(a, kv, sms, s, &parts)
-                                    : launch_rows16_kv<false>(a, kv, sms, s, &parts);
+    // the type of the probabilities: q's, or halves (an e4m3 cache; int8, row tiles of 16)
+    a.sum_scale = bf16 && (kv == kKv16 || (kv == kKvI8 && tc)) ? ProbScale<true>::kInverse : ProbScale<false>::kInverse;
+    const dspark_status ls = tc             ? launch_attn_tc(a, bf16, kv, sms, s, &parts)
+                             : kv == kKvI8 ? launch_attn_i8(a, bf16, i8_row_tile(p), sms, s, &parts)
+                             : bf16        ? (e4m3 ? launch_rows16_d<true, true>(a, sms, s, &parts)
+                                                   : launch_rows16_d<true, false>(a, sms, s, &parts))
+                                           : (e4m3 ? launch_rows16_d<false, true>(a, sms, s, &parts)
+                                                   : launch_rows16_d<false, false>(a, sms, s, &parts));
     if (ls != DSPARK_OK) return ls;
     note_launch();
-    const int row_tile = tc ? kTcRows : kRows;
+    const int row_tile = tc ? kTcRows : (kv == kKvI8 ? i8_row_tile(p) : kRows);
     // The join's blocks become resident as the attention kernel's leave.
     const dim3 grid(parts, 8), block(32 * kJoinWarps);
     const cudaError_t e = bf16 ? launch_overlapped(attn_join_kernel<true>, grid, block, 0, s, a, row_tile, parts)

@@ -1,0 +1,580 @@
+// paged_attn_i8.cu -- dspark_paged_attention_i8 for few rows a kv head: row tiles of 8 and 16 (paged.cuh has the split
+// of the work and the join, paged_attn_tc.cu the row tiles of 128).
+//
+// With k_l = c_l 2^(e_l) and v_l = d_l 2^(f_l), c and d the codes:
+//   s_l = scale (q . c_l) 2^(e_l), capped;  sum = sum_l 2^(s_l log2 e - m)
+//   o = sum_l 2^(s_l log2 e + f_l - M) d_l;  out = o 2^(M - m) / sum
+// m follows the largest score of a row and M the largest s_l log2 e + f_l, each by itself: a value's weight keeps its bits
+// as a half whatever the scales of the blocks before it, and blocks of zeros (whose scale is the smallest there is) do not
+// move the sum's reference.  Codes are halves exactly, and so is a query times a power of two; nothing else is rounded
+// before the products but the weights.
+//
+// What bounds it is issue slots, not the cache's bytes: a code costs 5/4 instructions on its way to a half, so the rest
+// has to be little.  Keys and values are therefore the products' A operand (16 keys, 16 values of a head), and the rows
+// are B, eight at a time: S^T = K Q^T and O^T = V^T P^T.  With the rows in A, as the other caches have them, a decoding
+// step of eight heads a kv head computes 16 rows of everything, scores, exponentials and output registers alike.
+// P^T is S^T's fragment transposed (movmatrix).  A warp streams slices of its own through a ring of its own in shared
+// memory, as in paged_attn.cu.
+#include "host_util.h"
+#include "mma16.cuh"
+#include "paged.cuh"
+#include "pdl.cuh"
+#include "tc05.cuh"
+
+namespace dspark {
+namespace {
+
+template <int DP, int NT>
+struct SliceI8 {
+    static constexpr int kRowTile = 8 * NT;
+    static constexpr int kKeys = DP == 256 ? 16 : 32;  // keys of a warp's slice
+    static constexpr int kMt = kKeys / 16;
+    static constexpr int kWarps = 4, kThreads = 32 * kWarps;
+    static constexpr int kKeyTile = kWarps * kKeys;  // keys of a unit
+    static constexpr int kChunks = DP / 16;          // 16-byte groups of a row
+    static constexpr int kHalf = kKeys * DP;         // K (or V) of a slice
+    static constexpr int kStage = 2 * kHalf;
+    static constexpr int kStages = DP == 64 ? 4 : (NT * DP > 256 ? 3 : 2);
+    static constexpr int kExtra = DP == 64 ? 4 : 2;  // what an item costs beside its key tiles
+    static constexpr int kBlocksPerSm = NT * DP > 256 ? 2 : 3;
+    static constexpr bool kQInSmem = NT * DP > 128;  // (else in registers)
+    static constexpr int kQBytes = kRowTile * DP * 2;
+    static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage + kQBytes;
+    // A warp's output in fp32 goes through the stage just consumed, in as many rounds as it takes.
+    static constexpr int kRounds = kRowTile * DP * 4 > kStage ? kRowTile * DP * 4 / kStage : 1;
+    static constexpr int kRoundRows = kRowTile / kRounds;
+    static_assert(kRoundRows % 8 == 0, "a round is whole n-tiles");
+    // Rows are a multiple of 128 bytes apart (or 64): the swizzle spreads eight rows' same 16-byte group over all banks.
+    static __device__ __forceinline__ uint32_t at(int row, int chunk) {
+        const int x = kChunks >= 8 ? (row & 7) : ((row >> 1) & 3);
+        return (uint32_t)(row * DP + ((chunk ^ x) << 4));
+    }
+    static __device__ __forceinline__ uint32_t q_at(int row, int chunk) {  // rows of q as halves
+        return (uint32_t)(row * (DP * 2) + ((chunk ^ (row & 7)) << 4));
+    }
+};
+
+template <bool BF16>
+__device__ __forceinline__ void store_out4(const AttnArgs& a, long long row, int col, float4 v) {
+    uint2 w = make_uint2(pack16<BF16>(v.x, v.y), pack16<BF16>(v.z, v.w));
+    *reinterpret_cast<uint2*>(a.out + ((size_t)row * a.D + col) * 2) = w;
+}
+
+template <bool BF16, int DP, int NT>
+__global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kBlocksPerSm) attn_i8_kernel(AttnArgs a) {
+    using C = SliceI8<DP, NT>;
+    constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kRows = C::kRowTile, MT = C::kMt;
+    constexpr int KS = DP / 16;  // k-steps over the head dimension, and m-tiles of the output
+    constexpr int R = 2 * NT;    // rows of a lane: 8 j + 2 t + (0, 1)
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float2 s_ml[kWarps][kRows];
+    __shared__ int s_err;
+    __shared__ AttnScratch s_start;
+    __shared__ uint32_t s_qmax[kRows];  // largest |q| of each row (its bits)
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int part = blockIdx.x, parts = gridDim.x;
+    wait_primary();
+    launch_dependents();
+    if (tid == 0) s_err = 0;
+    bool bad;
+    const AttnStart start = attn_start<kThreads>(a, kRows, C::kKeyTile, C::kExtra, parts, part, 2 + C::kExtra, &s_start, &bad);
+
+    attn_tail_rows(a, (size_t)part * kThreads + tid, (size_t)parts * kThreads);
+    unsigned char* ring = smem + (size_t)warp * C::kStages * C::kStage;
+    const uint32_t ring_addr = smem_addr(ring);
+    unsigned char* qs = smem + (size_t)kWarps * C::kStages * C::kStage;
+    const uint32_t qs_addr = smem_addr(qs);
+    int err = bad ? DSPARK_ERR_CACHE : 0;
+
+    // ---- loads: `ld` walks ahead of the arithmetic; `pid` is the page of this lane's key of its slice
+    AttnWalk ld = walk_begin(a, start, kRows, C::kKeyTile, C::kExtra);
+    int ld_head = ld.done() ? 0 : ld.item / ld.rts;
+    auto slice_key = [&](const AttnWalk& w) { return (w.kt_first + w.kt) * C::kKeyTile + warp * C::kKeys; };
+    auto fetch_page = [&]() -> int {
+        const int key = slice_key(ld) + lane;
+        if (ld.done() || lane >= C::kKeys || key >= ld.r.seq) return -1;
+        return __ldg(a.block_table + (size_t)ld.j * a.max_blocks + (key >> a.page_shift));
+    };
+    int pid = fetch_page();
+    int ld_stage = 0;
+    // An item's queries, asked for (into L1) when its first keys are.
+    auto touch_queries = [&]() {
+        const int first = (ld.item - ld_head * ld.rts) * kRows;
+        const int last = min(ld.r.n * a.G, first + kRows);
+        for (int i = lane; i < kRows * (DP / 64); i += 32) {
+            const int row = first + i / (DP / 64), token = attn_token(a, row), d = 64 * (i % (DP / 64));
+            if (row < last && d < a.D)
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + 2 * ((ld.r.token0 + token) * a.q_token +
+                                                                        (ld_head * a.G + row - token * a.G) * a.q_head + d)));
+        }
+    };
+    if (warp == 0 && !ld.done()) touch_queries();
+    // The exponents of this lane's key of the slices on their way, as they arrive; [0] are those of the slice in hand.
+    uint32_t k_exp[C::kStages], v_exp[C::kStages];
+    auto load_step = [&](int queue) {
+        k_exp[queue] = v_exp[queue] = 0;
+        if (!ld.done() && slice_key(ld) < ld.r.seq) {
+            const int key = slice_key(ld) + lane, place = key & ((1 << a.page_shift) - 1);
+            const bool live = lane < C::kKeys && key < ld.r.seq && key >= ld.r.lo;
+            const bool found = live && pid >= 0 && pid < a.num_pages;
+            if (live && !found) err = DSPARK_ERR_CACHE;
+            if (found) {
+                const long long e = exponents_at(a, pid, place, ld_head);
+                k_exp[queue] = __ldg(a.exp.k + e);
+                v_exp[queue] = __ldg(a.exp.v + e);
+            }
+            const long long off = found ? pid * a.page + place * a.token + ld_head * a.head : -1;
+            const uint32_t dst = ring_addr + ld_stage * C::kStage;
+            constexpr int kPer = 32 / C::kChunks;  // rows a warp copies at a time
+            const int chunk = lane % C::kChunks;
+            const bool inside = chunk * 16 < a.D;
+#pragma unroll
+            for (int i = 0; i < C::kKeys / kPer; ++i) {
+                const int row = i * kPer + lane / C::kChunks;
+                const long long o = __shfl_sync(0xffffffffu, off, row);
+                const bool real = inside && o >= 0;
+                const long long src = real ? o + chunk * 16 : 0;
+                copy16(dst + C::at(row, chunk), a.k_pages + src, real);
+                copy16(dst + C::kHalf + C::at(row, chunk), a.v_pages + src, real);
+            }
+        }
+        cp_async_commit();
+        if (++ld_stage == C::kStages) ld_stage = 0;
+        if (!ld.done()) {
+            walk_next(a, ld, kRows, C::kKeyTile);
+            pid = fetch_page();
+            if (ld.kt == 0 && !ld.done()) {
+                ld_head = ld.item / ld.rts;
+                if (warp == 0) touch_queries();
+            }
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) load_step(i + 1);
+
+    // ---- arithmetic
+    AttnWalk w = walk_begin(a, start, kRows, C::kKeyTile, C::kExtra);
+    PartItem* mine = a.items + part;  // written by thread 0
+    if (tid == 0) mine->d[kTail].first = mine->d[kHead].first = -1;
+    float o[KS][NT][4];  // [16 values of a head][8 rows]: values 2 g (rows 2 t, 2 t + 1), 2 g + 1
+    uint32_t qf[C::kQInSmem ? 1 : KS][NT][2];
+    const float cap_out = a.softcap * kLog2e;
+    float m[R], mv[R], l[R], row_scale[R];
+    int all_lo = 0, all_hi = 0, rows = 0, head = 0, row0 = 0, seg_first = 0;
+    bool fresh = true;
+    int st = 0;
+    auto row_of = [&](int r) { return 8 * (r >> 1) + 2 * t + (r & 1); };
+    // The queries' fragments of k-steps ks and ks + 1 (NT = 1), or of ks (NT = 2), by one ldmatrix.
+    auto load_q = [&](uint32_t (&b)[4], int ks) {
+        if (NT == 1)
+            ldsm4(b, qs_addr + C::q_at(lane & 7, 2 * ks + (lane >> 3)));
+        else
+            ldsm4(b, qs_addr + C::q_at((lane & 7) + (lane >> 4) * 8, 2 * ks + ((lane >> 3) & 1)));
+    };
+    while (!w.done()) {
+        if (fresh) {  // a new segment: its rows, their queries and what each may see
+            fresh = false;
+            seg_first = w.kt;
+            head = w.item / w.rts;
+            row0 = (w.item - head * w.rts) * kRows;
+            rows = min(w.r.n * a.G - row0, kRows);
+            all_lo = attn_see_lo(a, w.r, attn_token(a, row0 + rows - 1));
+            all_hi = attn_see_hi(a, w.r, attn_token(a, row0));
+            // The queries, through shared memory: 16 bytes a thread, then fragments by ldmatrix.  (The previous segment's
+            // readers are past its last barrier.)
+            constexpr int kQc = DP / 8;
+            constexpr int kQSteps = (kRows * kQc + kThreads - 1) / kThreads;
+            uint4 qv[kQSteps];
+            if (BF16) {
+                if (tid < kRows) s_qmax[tid] = 0;
+                __syncthreads();
+            }
+#pragma unroll
+            for (int u = 0; u < kQSteps; ++u) {
+                const int row = (tid + u * kThreads) / kQc, c = (tid + u * kThreads) % kQc, token = attn_token(a, row0 + row);
+                qv[u] = make_uint4(0, 0, 0, 0);
+                if (kRows * kQc % kThreads && row >= kRows) continue;
+                if (row < rows && 8 * c < a.D) {
+                    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (w.r.token0 + token) * a.q_token +
+                                          (head * a.G + row0 + row - token * a.G) * a.q_head + 8 * c;
+                    if (a.q_vec) {
+                        qv[u] = __ldg(reinterpret_cast<const uint4*>(src));
+                    } else {  // rows may start at any element
+                        uint32_t* y = reinterpret_cast<uint32_t*>(&qv[u]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = (uint32_t)__ldg(src + 2 * e) | ((uint32_t)__ldg(src + 2 * e + 1) << 16);
+                    }
+                }
+                if (BF16) {
+                    float big = 0.f;
+                    const uint32_t* y = reinterpret_cast<const uint32_t*>(&qv[u]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) big = fmaxf(big, fmaxf(fabsf(bf16_lo(y[e])), fabsf(bf16_hi(y[e]))));
+                    atomicMax(&s_qmax[row], __float_as_uint(big));
+                }
+            }
+            // bf16 queries as halves: each row times the power of two that brings its largest value to 2^14, taken back
+            // in the scores' scale; what a half then cannot hold is below 2^-38 of the row's largest, less than fp32
+            // keeps of the sum.
+            auto raise = [&](int row) {
+                const int e = (int)(s_qmax[row] >> 23) - 127;  // floor(log2) of a normal number
+                return e > -127 && e < 128 ? min(max(14 - e, -120), 120) : 0;
+            };
+            if (BF16) __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kQSteps; ++u) {
+                const int row = (tid + u * kThreads) / kQc, c = (tid + u * kThreads) % kQc;
+                if (kRows * kQc % kThreads && row >= kRows) continue;
+                // codes arrive four k a lane: the MMA's k slots (2t, 2t + 1 | 2t + 8, 2t + 9) hold k = 4t .. 4t + 3, so
+                // pair p of 16 values goes to pair p / 2 + 4 (p % 2)
+                const uint32_t* y = reinterpret_cast<const uint32_t*>(&qv[u]);
+                const float up = BF16 ? two_to(raise(row)) : 1.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int p = 4 * (c & 1) + e, to = (p >> 1) + 4 * (p & 1);
+                    const uint32_t x = BF16 ? pack16<false>(bf16_lo(y[e]) * up, bf16_hi(y[e]) * up) : y[e];
+                    *reinterpret_cast<uint32_t*>(qs + C::q_at(row, (c & ~1) + (to >> 2)) + 4 * (to & 3)) = x;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                m[r] = mv[r] = -CUDART_INF_F;
+                l[r] = 0.f;
+                // to the log2 domain, or to the cap's exponent
+                row_scale[r] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale;
+                if (BF16) row_scale[r] *= two_to(-raise(row_of(r)));
+            }
+            if (!C::kQInSmem) {
+#pragma unroll
+                for (int ks = 0; ks < KS; ks += NT == 1 ? 2 : 1) {
+                    uint32_t b[4];
+                    load_q(b, ks);
+                    if (NT == 1) {
+                        qf[C::kQInSmem ? 0 : ks][0][0] = b[0];
+                        qf[C::kQInSmem ? 0 : ks][0][1] = b[1];
+                        qf[C::kQInSmem ? 0 : ks + 1][0][0] = b[2];
+                        qf[C::kQInSmem ? 0 : ks + 1][0][1] = b[3];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            qf[C::kQInSmem ? 0 : ks][j][0] = b[2 * j];
+                            qf[C::kQInSmem ? 0 : ks][j][1] = b[2 * j + 1];
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[i][j][c] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i + 1 < C::kStages; ++i) {
+            k_exp[i] = k_exp[i + 1];
+            v_exp[i] = v_exp[i + 1];
+        }
+        load_step(C::kStages - 1);
+        cp_async_wait_group<C::kStages - 1>();
+        __syncwarp();
+        const int key0 = slice_key(w);
+        if (key0 < w.r.seq) {
+            const uint32_t kb = ring_addr + st * C::kStage, vb = kb + C::kHalf;
+            // ---- S^T: lane (g, t) gets keys 16 i + g (c < 2), + 8, of rows 8 j + 2 t + (c & 1)
+            float s[MT][NT][4];
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[i][j][c] = 0.f;
+            auto codes_a = [](uint32_t (&f)[4], uint32_t lo, uint32_t hi) {  // four k of keys g and g + 8
+                const uint32_t x = lo ^ 0x80808080u, y = hi ^ 0x80808080u;
+                f[0] = i8x2_to_half2<kBytes01>(x);
+                f[1] = i8x2_to_half2<kBytes01>(y);
+                f[2] = i8x2_to_half2<kBytes23>(x);
+                f[3] = i8x2_to_half2<kBytes23>(y);
+            };
+#pragma unroll
+            for (int ks = 0; ks < KS; ks += 2) {
+                uint32_t q[2][NT][2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (!C::kQInSmem) {
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) q[u][j][e] = qf[C::kQInSmem ? 0 : ks + u][j][e];
+                    } else if (NT > 1) {
+                        uint32_t b[4];
+                        load_q(b, ks + u);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            q[u][j][0] = b[2 * j];
+                            q[u][j][1] = b[2 * j + 1];
+                        }
+                    }
+                }
+                if (C::kQInSmem && NT == 1) {
+                    uint32_t b[4];
+                    load_q(b, ks);
+                    q[0][0][0] = b[0];
+                    q[0][0][1] = b[1];
+                    q[1][0][0] = b[2];
+                    q[1][0][1] = b[3];
+                }
+                uint32_t b[2][4];
+                if (MT == 2) {  // matrix i: keys 8 i .. 8 i + 7
+                    ldsm4(b[0], kb + C::at(lane, ks));
+                    ldsm4(b[1], kb + C::at(lane, ks + 1));
+                } else {  // keys 0 .. 7, 8 .. 15 of both k-steps
+                    ldsm4(b[0], kb + C::at(lane & 15, ks + (lane >> 4)));
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        uint32_t f[4];
+                        if (MT == 2)
+                            codes_a(f, b[u][2 * i], b[u][2 * i + 1]);
+                        else
+                            codes_a(f, b[0][2 * u], b[0][2 * u + 1]);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) mma16<false>(s[i][j], f, q[u][j][0], q[u][j][1]);
+                    }
+            }
+            // each key's 2^e (as bf16, in the low half) and its values' e (as bf16), from the lane of the key's number
+            const uint32_t both = (uint32_t)(exponent_of<BF16>(k_exp[0]) + 127) << 7 |
+                                  (__float_as_uint((float)exponent_of<BF16>(v_exp[0])) & 0xffff0000u);
+            float key_scale[MT][2], value_exp[MT][2];
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t x = __shfl_sync(0xffffffffu, both, 16 * i + 8 * h + g);
+                    key_scale[i][h] = __uint_as_float(x << 16);
+                    value_exp[i][h] = __uint_as_float(x & 0xffff0000u);
+                }
+            // scores in the log2 domain, hidden ones -inf
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[i][j][c] = s[i][j][c] * row_scale[2 * j + (c & 1)] * key_scale[i][c >> 1];
+            if (a.softcap > 0.f) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float2 x = softcap2(s[i][j][2 * h], s[i][j][2 * h + 1], 1.f, cap_out);
+                            s[i][j][2 * h] = x.x;
+                            s[i][j][2 * h + 1] = x.y;
+                        }
+            }
+            if (key0 < all_lo || key0 + C::kKeys > all_hi) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int row = row_of(r), token = attn_token(a, row0 + row);
+                    const int lo = attn_see_lo(a, w.r, token), hi = row < rows ? attn_see_hi(a, w.r, token) : 0;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int key = key0 + 16 * i + 8 * h + g;
+                            if (key < lo || key >= hi) s[i][r >> 1][2 * h + (r & 1)] = -CUDART_INF_F;
+                        }
+                }
+            }
+            float mx[R], mz[R];
+            bool grow = false;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                mx[r] = mz[r] = -CUDART_INF_F;
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float x = s[i][r >> 1][2 * h + (r & 1)];
+                        mx[r] = fmaxf(mx[r], x);
+                        mz[r] = fmaxf(mz[r], x + value_exp[i][h]);
+                    }
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], d));
+                    mz[r] = fmaxf(mz[r], __shfl_xor_sync(0xffffffffu, mz[r], d));
+                }
+                grow |= mx[r] > m[r] + 8.f || mz[r] > mv[r] + 8.f;
+            }
+            // The references follow the maxima only when they are 2^8 behind (values up to 2^8 lose nothing), so most
+            // slices do not touch the output.
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float mn = fmaxf(m[r], mx[r]), zn = fmaxf(mv[r], mz[r]);
+                    if (mn != m[r]) l[r] *= ex2(m[r] - mn);  // m = -inf: 0
+                    m[r] = mn;
+                    const float f = zn == mv[r] ? 1.f : ex2(mv[r] - zn);
+                    mv[r] = zn;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        o[i][r >> 1][r & 1] *= f;
+                        o[i][r >> 1][2 + (r & 1)] *= f;
+                    }
+                }
+            }
+            // ---- P^T as halves, fragments of the second product's B
+            constexpr float kUp = ProbScale<false>::kBits;
+            uint32_t p[MT][NT][2];
+            float ref[R], ref_v[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                ref[r] = m[r] == -CUDART_INF_F ? 0.f : m[r] - kUp;
+                ref_v[r] = mv[r] == -CUDART_INF_F ? 0.f : mv[r] - kUp;
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float x = s[i][j][2 * h], y = s[i][j][2 * h + 1];
+                        l[2 * j] += ex2(x - ref[2 * j]);
+                        l[2 * j + 1] += ex2(y - ref[2 * j + 1]);
+                        p[i][j][h] = transpose8x8(pack16<false>(ex2(x + value_exp[i][h] - ref_v[2 * j]),
+                                                                ex2(y + value_exp[i][h] - ref_v[2 * j + 1])));
+                    }
+            // ---- O^T += V^T P^T: bytes (k0 d0, k0 d1, k1 d0, k1 d1) are rows 2 g and 2 g + 1 of the m-tile, which are
+            // its rows g and g + 8 to the MMA.  (What nobody sees needs no care: codes are finite.)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int c = 0; c < KS; c += 2) {
+                    uint32_t b[4];
+                    ldsm4_trans(b, vb + C::at(16 * i + (lane & 15), c + (lane >> 4)));
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t x = b[2 * u] ^ 0x80808080u, y = b[2 * u + 1] ^ 0x80808080u;
+                        const uint32_t f[4] = {i8x2_to_half2<kBytes02>(x), i8x2_to_half2<kBytes13>(x), i8x2_to_half2<kBytes02>(y),
+                                               i8x2_to_half2<kBytes13>(y)};
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) mma16<false>(o[c + u][j], f, p[i][j][0], p[i][j][1]);
+                    }
+                }
+        }
+        __syncwarp();  // the slice has been read by every lane
+
+        const bool last_of_item = w.kt + 1 == w.kts;
+        if (last_of_item || w.left == 1) {
+            // ---- the warps' parts of the segment meet
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], d);
+                if (g == 0) s_ml[warp][row_of(r)] = make_float2(m[r], l[r]);
+                // to the reference of the sums, in two steps: 2^f may be as large as fp32's numbers
+                const float f = m[r] == -CUDART_INF_F ? 1.f : ex2(0.5f * (mv[r] - m[r]));
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    o[i][r >> 1][r & 1] = o[i][r >> 1][r & 1] * f * f;
+                    o[i][r >> 1][2 + (r & 1)] = o[i][r >> 1][2 + (r & 1)] * f * f;
+                }
+            }
+            const bool whole = last_of_item && seg_first == 0;
+            const int slot = 2 * part + (seg_first == 0 ? kHead : kTail);
+            float* mine_o = reinterpret_cast<float*>(ring + st * C::kStage);
+            auto o_at = [](int row, int col) { return (row % C::kRoundRows) * DP + (col ^ (((row >> 1) & 3) << 4)); };
+#pragma unroll
+            for (int round = 0; round < C::kRounds; ++round) {
+                if (round) __syncthreads();
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    if ((r >> 1) * 8 / C::kRoundRows != round) continue;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+                        *reinterpret_cast<float2*>(mine_o + o_at(row_of(r), 16 * i + 2 * g)) =
+                            make_float2(o[i][r >> 1][r & 1], o[i][r >> 1][2 + (r & 1)]);
+                }
+                __syncthreads();
+                const int end = min(rows - round * C::kRoundRows, C::kRoundRows);
+                for (int i = tid; i < end * (DP / 4); i += kThreads) {
+                    const int row = round * C::kRoundRows + i / (DP / 4), col = 4 * (i % (DP / 4));
+                    float mm = -CUDART_INF_F, ll = 0.f;
+#pragma unroll
+                    for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, s_ml[x][row].x);
+                    const float ref = mm == -CUDART_INF_F ? 0.f : mm;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int x = 0; x < kWarps; ++x) {
+                        const float2 ml = s_ml[x][row];
+                        const float f = ex2(ml.x - ref);
+                        if (ml.y == 0.f) continue;  // saw nothing
+                        ll = fmaf(ml.y, f, ll);
+                        const float4 y = *reinterpret_cast<const float4*>(
+                            smem + (size_t)(x * C::kStages + st) * C::kStage + 4 * o_at(row, col));
+                        v.x = fmaf(y.x, f, v.x);
+                        v.y = fmaf(y.y, f, v.y);
+                        v.z = fmaf(y.z, f, v.z);
+                        v.w = fmaf(y.w, f, v.w);
+                    }
+                    if (whole) {
+                        const long long at = attn_out_row(a, w.r.token0, head, row0 + row);
+                        if (col < a.D) {
+                            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                            store_out4<BF16>(a, at, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                        }
+                        if (a.lse && col == 0)
+                            a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll * ProbScale<false>::kInverse)) * kLn2;
+                    } else {
+                        if (col < a.D) *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * kRows + row) * a.D + col) = v;
+                        if (col == 0) a.part_ml[(size_t)slot * kRows + row] = make_float2(mm, ll);
+                    }
+                }
+            }
+            if (!whole && tid == 0) mine->d[seg_first == 0 ? kHead : kTail] = part_desc(start, w, row0, rows, head);
+            __syncthreads();
+            fresh = true;
+        }
+        if (++st == C::kStages) st = 0;
+        walk_next(a, w, kRows, C::kKeyTile);
+    }
+    cp_async_wait_group<0>();
+    if (err) s_err = err;  // any of the block's errors: all are the same code
+    __syncthreads();
+    if (tid == 0) mine->err = s_err;
+}
+
+template <bool BF16, int DP, int NT>
+dspark_status launch_slices(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
+    using C = SliceI8<DP, NT>;
+    int per_sm = 0;
+    auto fn = attn_i8_kernel<BF16, DP, NT>;
+    if (prepare_kernel((const void*)fn, C::kSmem, C::kThreads, &per_sm) != cudaSuccess || per_sm < 1) return DSPARK_ERR_CUDA;
+    int n = sms * (per_sm < C::kBlocksPerSm ? per_sm : C::kBlocksPerSm);
+    if (n > kMaxParts) n = kMaxParts;
+    *parts = n;
+    return launch_overlapped(fn, n, C::kThreads, C::kSmem, s, a) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+template <bool BF16, int DP>
+dspark_status launch_slices_d(const AttnArgs& a, int row_tile, int sms, cudaStream_t s, int* parts) {
+    return row_tile == 8 ? launch_slices<BF16, DP, 1>(a, sms, s, parts) : launch_slices<BF16, DP, 2>(a, sms, s, parts);
+}
+template <bool BF16>
+dspark_status launch_slices_t(const AttnArgs& a, int row_tile, int sms, cudaStream_t s, int* parts) {
+    if (a.D <= 64) return launch_slices_d<BF16, 64>(a, row_tile, sms, s, parts);
+    if (a.D <= 128) return launch_slices_d<BF16, 128>(a, row_tile, sms, s, parts);
+    return launch_slices_d<BF16, 256>(a, row_tile, sms, s, parts);
+}
+
+}  // namespace
+
+dspark_status launch_attn_i8(const AttnArgs& a, bool bf16, int row_tile, int sms, cudaStream_t s, int* parts) {
+    return bf16 ? launch_slices_t<true>(a, row_tile, sms, s, parts) : launch_slices_t<false>(a, row_tile, sms, s, parts);
+}
+
+}  // namespace dspark

@@ -24,6 +24,8 @@
 // softmax decides: 32 draft blocks of 16 over up to 4100 tokens 52.5 us = 2.8 TB/s (0.42).
 // Over an 8-bit cache the loaders' widening decides at few rows (32 requests, 35 rows on average: 85 us, of row
 // tiles of 16: 69) and pays at many (145 requests, 119 rows of 192 over 200 keys: 92 us against 254).
+#include <cuda_bf16.h>
+
 #include "host_util.h"
 #include "paged.cuh"
 #include "pdl.cuh"
@@ -34,8 +36,9 @@ namespace {
 
 constexpr int kTcRowTile = 128;
 
-template <bool F8, int DP>
+template <int KV, int DP>
 struct TcAttn {
+    static constexpr bool F8 = KV != kKv16;  // 8-bit pools
     static constexpr int kStreams = DP == 256 ? 1 : 2;
     static constexpr int kKt = DP == 256 ? 32 : 64;  // keys of a tile
     static constexpr int kUnit = kStreams * kKt;
@@ -149,6 +152,36 @@ __device__ __forceinline__ void widen16(const uint4 v, uint4& lo, uint4& hi) {
     hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
+// Sixteen int8 codes times `scale` (twice 2^e in the 16-bit type, which holds the products exactly), in order.  bf16: the
+// byte's low seven bits beside the exponent of 2^7 are 128 + them, from which 128 is taken, or 256 where bit 7 is set.
+template <bool BF16>
+__device__ __forceinline__ void widen16_i8(const uint4 v, uint32_t scale, uint4& lo, uint4& hi) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (BF16) {
+            const uint32_t x = __byte_perm(w[i >> 1], 0, i & 1 ? 0x4342 : 0x4140);
+            const uint32_t a = (x & 0x007f007fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
+            __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+            y = __hmul2(y, *reinterpret_cast<const __nv_bfloat162*>(&scale));
+            r[i] = *reinterpret_cast<const uint32_t*>(&y);
+        } else {
+            const uint32_t u = w[i >> 1] ^ 0x80808080u;
+            const uint32_t h = i & 1 ? i8x2_to_half2<kBytes23>(u) : i8x2_to_half2<kBytes01>(u);
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(h), "r"(scale));
+        }
+    }
+    lo = make_uint4(r[0], r[1], r[2], r[3]);
+    hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+// 2^e twice in the 16-bit type.
+template <bool BF16>
+__device__ __forceinline__ uint32_t scale_pair(int e) {
+    const float s = two_to(e);
+    return pack16<BF16>(s, s);
+}
+
 // MMAs and commits by one elected lane of a converged warp (always the same one).  Descriptors come in
 // halves; kind::f16, fp32 accumulation; accumulate = 0 overwrites D.
 __device__ __forceinline__ void mma_elect_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
@@ -190,10 +223,13 @@ struct TcBars {
 };
 static_assert(sizeof(TcBars) <= 512, "barriers");
 
-template <bool BF16, bool F8, int DP>
-__global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(AttnArgs a, uint64_t limit_ns) {
-    using C = TcAttn<F8, DP>;
-    constexpr bool VB = BF16 && !F8;  // type of P and V: an 8-bit cache's values meet the probabilities as halves
+template <bool BF16, int KV, int DP>
+__global__ void __launch_bounds__(TcAttn<KV, DP>::kThreads, 1) attn_tc_kernel(AttnArgs a, uint64_t limit_ns) {
+    using C = TcAttn<KV, DP>;
+    constexpr bool F8 = KV != kKv16, I8 = KV == kKvI8;
+    // type of P and V: an e4m3 cache's values meet the probabilities as halves, an int8 cache's as q's type, with their
+    // scales in them
+    constexpr bool VB = BF16 && KV != kKvE4M3;
     constexpr int KT = C::kKt, NS = C::kStreams;
     extern __shared__ __align__(1024) unsigned char smem[];
     float2* s_ml = reinterpret_cast<float2*>(smem + C::kMeta);  // [kStreams][128]
@@ -278,14 +314,21 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
         int head = 0, slot = lw / C::kTileLoaders, round = 0;
         const int tile_row = (lw % C::kTileLoaders) * kKeys + sub_row;
         // 8-bit caches: a tile arrives as it is, each lane's pieces in places of its own, `ahead` tiles at a time; the
-        // lane that copied a piece widens it into the slot, keys to q's type, values to halves (both exact).
+        // lane that copied a piece widens it into the slot, keys to q's type, values to halves (int8: q's type), all exact.
         constexpr int kSteps = kKeys / kPer;
         int raw_slot = 0, raw_old = 0, ahead = 0;
+        uint32_t k_exp[I8 ? C::kRawSlots : 1], v_exp[I8 ? C::kRawSlots : 1];  // of this lane's key of the raw tiles
         unsigned char* raw = smem + C::kRaw + lw * (C::kRawSlots * C::kRawTile) + lane * 16;
         auto widen = [&]() {
             if (round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) return false;
             unsigned char* to = smem + C::kRing + slot * (2 * C::kTile) + ((2 * chunk) >> 3) * (KT * 128);
             const unsigned char* from = raw + raw_old * C::kRawTile;
+            uint32_t e = 0;
+            if (I8) {
+#pragma unroll
+                for (int i = 0; i < C::kRawSlots; ++i)
+                    if (raw_old == i) e = k_exp[I8 ? i : 0] | v_exp[I8 ? i : 0] << 8;
+            }
 #pragma unroll 2
             for (int u = 0; u < kSteps; ++u) {
                 const uint32_t at0 = sw128_offset(tile_row + u * kPer, (2 * chunk) & 7);
@@ -293,10 +336,19 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
                 const uint4 k = *reinterpret_cast<const uint4*>(from + 2 * u * 512);
                 const uint4 v = *reinterpret_cast<const uint4*>(from + (2 * u + 1) * 512);
                 uint4 x, y;
-                widen16<BF16>(k, x, y);
+                uint32_t with = 0;
+                if (I8) {
+                    with = __shfl_sync(0xffffffffu, e, u * kPer + sub_row);
+                    widen16_i8<BF16>(k, scale_pair<BF16>(exponent_of<BF16>(with & 0xffu)), x, y);
+                } else {
+                    widen16<BF16>(k, x, y);
+                }
                 *reinterpret_cast<uint4*>(to + at0) = x;
                 *reinterpret_cast<uint4*>(to + at1) = y;
-                widen16<false>(v, x, y);
+                if (I8)
+                    widen16_i8<BF16>(v, scale_pair<BF16>(exponent_of<BF16>(with >> 8)), x, y);
+                else
+                    widen16<false>(v, x, y);
                 *reinterpret_cast<uint4*>(to + at0 + C::kTile) = x;
                 *reinterpret_cast<uint4*>(to + at1 + C::kTile) = y;
             }
@@ -354,6 +406,15 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
                 pid = -1;
             }
             if (none) pid = -1;
+            if (I8) {  // (entry 0 where there is no key, whose codes are zeros)
+                const long long at = pid >= 0 && lane < kKeys ? exponents_at(a, pid, (key0 + lane) & mask, head) : 0;
+#pragma unroll
+                for (int i = 0; i < C::kRawSlots; ++i)
+                    if (raw_slot == i) {
+                        k_exp[I8 ? i : 0] = __ldg(a.exp.k + at);
+                        v_exp[I8 ? i : 0] = __ldg(a.exp.v + at);
+                    }
+            }
             const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + (uint32_t)(chunk >> 3) * (KT * 128);
             const uint32_t rb = smem_addr(raw) + (uint32_t)(raw_slot * C::kRawTile);
 #pragma unroll 8
@@ -505,7 +566,7 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
                 see_hi = row < rows ? attn_see_hi(a, w.r, token) : 0;
                 m = -CUDART_INF_F;
                 l = 0.f;
-                if (F8 && a.k_scale) {
+                if (KV == kKvE4M3 && a.k_scale) {
                     c = a.scale * kLog2e * __ldg(a.k_scale + head);
                     plain = a.softcap == 0.f && c > 0.f;
                     cap_in = a.softcap > 0.f ? 2.f * c / a.softcap : 0.f;
@@ -620,7 +681,7 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
             // A hidden key's value must not reach a row that does not see it, even as 0 x inf: values of an
             // edge tile that are not finite (never, in a healthy cache) are added by hand to the rows that
             // see them, and taken out of the tile.
-            if (edge) {
+            if (edge && !I8) {  // (codes are finite)
                 const int tile = n * NS + s, slot = tile % C::kSlots;
                 if (!warp_wait(&bars->full[slot], (uint32_t)((tile / C::kSlots) & 1))) break;
                 unsigned char* v = smem + C::kRing + slot * (2 * C::kTile) + C::kTile;
@@ -692,7 +753,7 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
                 }
                 const bool whole = last_of_item && seg_first == 0;
                 const size_t slot = 2 * (size_t)part + (seg_first == 0 ? kHead : kTail);
-                const float inv = !whole ? 1.f : (ll == 0.f ? 0.f : (F8 && a.v_scale ? __ldg(a.v_scale + head) : 1.f) / ll);
+                const float inv = !whole ? 1.f : (ll == 0.f ? 0.f : (KV == kKvE4M3 && a.v_scale ? __ldg(a.v_scale + head) : 1.f) / ll);
                 const long long at = attn_out_row(a, w.r.token0, head, row0 + row);
                 unsigned char* dst = a.out + (size_t)at * a.D * 2;
                 float* part_dst = a.part_o + (slot * kTcRowTile + row) * a.D;
@@ -753,11 +814,11 @@ __global__ void __launch_bounds__(TcAttn<F8, DP>::kThreads, 1) attn_tc_kernel(At
     if (tid == 0) mine->err = bars->status ? bars->status : (bad ? DSPARK_ERR_CACHE : 0);
 }
 
-template <bool BF16, bool F8, int DP>
+template <bool BF16, int KV, int DP>
 dspark_status launch_tc(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
-    using C = TcAttn<F8, DP>;
+    using C = TcAttn<KV, DP>;
     int per_sm = 0;
-    auto fn = attn_tc_kernel<BF16, F8, DP>;
+    auto fn = attn_tc_kernel<BF16, KV, DP>;
     if (prepare_kernel((const void*)fn, C::kSmem, C::kThreads, &per_sm) != cudaSuccess || per_sm < 1)
         return DSPARK_ERR_CUDA;
     const int n = sms < kMaxTcParts ? sms : kMaxTcParts;
@@ -765,18 +826,19 @@ dspark_status launch_tc(const AttnArgs& a, int sms, cudaStream_t s, int* parts) 
     return launch_overlapped(fn, n, C::kThreads, C::kSmem, s, a, wait_limit_ns()) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
-template <bool BF16, bool F8>
+template <bool BF16, int KV>
 dspark_status launch_tc_d(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
-    if (a.D <= 64) return launch_tc<BF16, F8, 64>(a, sms, s, parts);
-    if (a.D <= 128) return launch_tc<BF16, F8, 128>(a, sms, s, parts);
-    return launch_tc<BF16, F8, 256>(a, sms, s, parts);
+    if (a.D <= 64) return launch_tc<BF16, KV, 64>(a, sms, s, parts);
+    if (a.D <= 128) return launch_tc<BF16, KV, 128>(a, sms, s, parts);
+    return launch_tc<BF16, KV, 256>(a, sms, s, parts);
 }
 
 }  // namespace
 
 dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int kv, int sms, cudaStream_t s, int* parts) {
-    if (kv == kKvE4M3) return bf16 ? launch_tc_d<true, true>(a, sms, s, parts) : launch_tc_d<false, true>(a, sms, s, parts);
-    return bf16 ? launch_tc_d<true, false>(a, sms, s, parts) : launch_tc_d<false, false>(a, sms, s, parts);
+    if (kv == kKvI8) return bf16 ? launch_tc_d<true, kKvI8>(a, sms, s, parts) : launch_tc_d<false, kKvI8>(a, sms, s, parts);
+    if (kv == kKvE4M3) return bf16 ? launch_tc_d<true, kKvE4M3>(a, sms, s, parts) : launch_tc_d<false, kKvE4M3>(a, sms, s, parts);
+    return bf16 ? launch_tc_d<true, kKv16>(a, sms, s, parts) : launch_tc_d<false, kKv16>(a, sms, s, parts);
 }
 
 }  // namespace dspark
