@@ -64,7 +64,7 @@ struct PartDesc {
     int first, last;  // blocks that begin and end it
     int row0, rows;   // first row of the tile within the request and kv head, its real rows
     int token0;       // row of q and out of the request's first token
-    int head;         // kv head
+    int head;         // kv head, or group of them
     int pad[2];
 };
 struct PartItem {
@@ -348,7 +348,8 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // aligned query rows.
 dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int kv, int sms, cudaStream_t s, int* parts);
 
-// Row tiles of 8 or 16 over int8 pools (paged_attn_i8.cu).
+// Row tiles of 8 or 16 over int8 pools (paged_attn_i8.cu), for i8_head_group kv heads at a time.
+int i8_head_group(int D, int Hk);
 dspark_status launch_attn_i8(const AttnArgs& a, bool bf16, int row_tile, int sms, cudaStream_t s, int* parts);
 
 }  // namespace dspark

@@ -522,8 +522,10 @@ __global__ void __launch_bounds__(Rows16<F8, DP>::kThreads, Rows16<F8, DP>::kBlo
 constexpr int kJoinWarps = 4;
 constexpr int kJoinAhead = 4;
 constexpr int kJoinFew = 8;  // up to so many parts, a warp joins a row by itself (20 -> 8 us for 64 rows of 2 parts)
+// An item may cover several kv heads (an int8 cache): its rows are then those of the first one, row_tile places, those of
+// the second one and so on, and it.rows are real of each.
 template <bool BF16>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, int row_tile, int parts) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, int row_tile, int heads, int parts) {
     __shared__ float s_f[kMaxParts];
     __shared__ float4 s_acc[kJoinWarps][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -543,13 +545,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
         if (it.first < 0) continue;
         const int n = it.last - it.first + 1;  // parts: the first block's head, then tails
         auto slot_of = [&](int i) { return (size_t)(2 * (it.first + i) + (i == 0 ? kHead : kTail)); };
+        const int places = heads * row_tile, all_rows = places - row_tile + it.rows;
+        auto real = [&](int row) { return heads == 1 || row % row_tile < it.rows; };
+        auto head_of = [&](int row) { return heads == 1 ? it.head : it.head * heads + row / row_tile; };
+        auto out_row = [&](int row) {
+            return attn_out_row(a, it.token0, head_of(row), it.row0 + (heads == 1 ? row : row % row_tile));
+        };
         if (n <= kJoinFew) {
             const int worker = (((int)blockIdx.x - it.first) * gridDim.y + blockIdx.y) * kJoinWarps + warp;
 #pragma unroll 1
-            for (int row = worker; row < it.rows; row += n * gridDim.y * kJoinWarps) {
-                const float2 ml = lane < n ? a.part_ml[slot_of(lane) * row_tile + row] : make_float2(-CUDART_INF_F, 0.f);
+            for (int row = worker; row < all_rows; row += n * gridDim.y * kJoinWarps) {
+                if (!real(row)) continue;
+                const float2 ml = lane < n ? a.part_ml[slot_of(lane) * places + row] : make_float2(-CUDART_INF_F, 0.f);
                 const float vscale = a.v_scale ? __ldg(a.v_scale + it.head) : 1.f;
-                const long long at = attn_out_row(a, it.token0, it.head, it.row0 + row);
+                const long long at = out_row(row);
 #pragma unroll 1
                 for (int col = 4 * lane; col - 4 * lane < a.D; col += 128) {
                     const bool in = col < a.D;
@@ -557,7 +566,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
 #pragma unroll
                     for (int i = 0; i < kJoinFew; ++i)
                         if (i < n && in)
-                            y[i] = *reinterpret_cast<const float4*>(a.part_o + (slot_of(i) * row_tile + row) * a.D + col);
+                            y[i] = *reinterpret_cast<const float4*>(a.part_o + (slot_of(i) * places + row) * a.D + col);
                     const float mm = warp_max(ml.x);
                     const float f = ml.y == 0.f ? 0.f : ex2(ml.x - (mm == -CUDART_INF_F ? 0.f : mm));
                     const float ll = warp_sum(ml.y * f);
@@ -580,14 +589,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
             continue;
         }
 #pragma unroll 1
-        for (int row = ((int)blockIdx.x - it.first) * gridDim.y + blockIdx.y; row < it.rows; row += n * gridDim.y) {
+        for (int row = ((int)blockIdx.x - it.first) * gridDim.y + blockIdx.y; row < all_rows; row += n * gridDim.y) {
+            if (!real(row)) continue;
             const float vscale = a.v_scale ? __ldg(a.v_scale + it.head) : 1.f;
             float ll = 0.f, mm = -CUDART_INF_F;
 #pragma unroll 1
             for (int col = 4 * lane; col - 4 * lane < a.D; col += 128) {
                 const bool in = col < a.D;
                 auto part = [&](int i) {
-                    return *reinterpret_cast<const float4*>(a.part_o + (slot_of(i) * row_tile + row) * a.D + col);
+                    return *reinterpret_cast<const float4*>(a.part_o + (slot_of(i) * places + row) * a.D + col);
                 };
                 float4 y[kJoinAhead];
 #pragma unroll
@@ -596,14 +606,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
                     y[u] = in && i < n ? part(i) : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
                 if (col < 128) {  // the parts' weights, once a row
-                    for (int i = tid; i < n; i += 32 * kJoinWarps) s_f[i] = a.part_ml[slot_of(i) * row_tile + row].x;
+                    for (int i = tid; i < n; i += 32 * kJoinWarps) s_f[i] = a.part_ml[slot_of(i) * places + row].x;
                     __syncthreads();
                     for (int i = lane; i < n; i += 32) mm = fmaxf(mm, s_f[i]);
                     mm = warp_max(mm);
                     const float ref = mm == -CUDART_INF_F ? 0.f : mm;
                     __syncthreads();
                     for (int i = lane; i < n; i += 32) {  // (every warp: the same sum in the same order)
-                        const float2 ml = a.part_ml[slot_of(i) * row_tile + row];
+                        const float2 ml = a.part_ml[slot_of(i) * places + row];
                         const float f = ml.y == 0.f ? 0.f : ex2(ml.x - ref);
                         ll = fmaf(ml.y, f, ll);
                         if (warp == 0) s_f[i] = f;
@@ -639,7 +649,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
                         t.z += z.z;
                         t.w += z.w;
                     }
-                    const long long at = attn_out_row(a, it.token0, it.head, it.row0 + row);
+                    const long long at = out_row(row);
                     store_out4<BF16>(a, at, col, make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv));
                     if (a.lse && col == 0) a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll * a.sum_scale)) * kLn2;
                 }
@@ -688,7 +698,8 @@ int i8_row_tile(const dspark_attention_params* p) {
     return rows <= 8 ? 8 : 16;
 }
 AttnWs attn_ws(const dspark_attention_params* p) {
-    const size_t rows = wide_rows(p) ? (size_t)2 * kMaxTcParts * kTcRows : (size_t)2 * kMaxParts * kRows;
+    const int heads = p->kv_dtype == DSPARK_I8 ? i8_head_group(p->D, p->Hk) : 1;
+    const size_t rows = wide_rows(p) ? (size_t)2 * kMaxTcParts * kTcRows : (size_t)2 * kMaxParts * kRows * heads;
     AttnWs w;
     w.items = kHeaderBytes;
     w.ml = align_up(w.items + sizeof(PartItem) * kMaxParts, 256);
@@ -796,10 +807,11 @@ dspark_status paged_attention(const dspark_attention_params* p, const dspark_blo
     if (ls != DSPARK_OK) return ls;
     note_launch();
     const int row_tile = tc ? kTcRows : (kv == kKvI8 ? i8_row_tile(p) : kRows);
+    const int heads = !tc && kv == kKvI8 ? i8_head_group(p->D, p->Hk) : 1;
     // The join's blocks become resident as the attention kernel's leave.
     const dim3 grid(parts, 8), block(32 * kJoinWarps);
-    const cudaError_t e = bf16 ? launch_overlapped(attn_join_kernel<true>, grid, block, 0, s, a, row_tile, parts)
-                               : launch_overlapped(attn_join_kernel<false>, grid, block, 0, s, a, row_tile, parts);
+    const cudaError_t e = bf16 ? launch_overlapped(attn_join_kernel<true>, grid, block, 0, s, a, row_tile, heads, parts)
+                               : launch_overlapped(attn_join_kernel<false>, grid, block, 0, s, a, row_tile, heads, parts);
     if (e != cudaSuccess) return DSPARK_ERR_CUDA;
     note_launch();
     return DSPARK_OK;

@@ -24,22 +24,23 @@
 namespace dspark {
 namespace {
 
-template <int DP, int NT>
+template <int DP, int NT, int HG>
 struct SliceI8 {
-    static constexpr int kRowTile = 8 * NT;
+    static constexpr int kRowTile = 8 * NT;            // rows of a kv head
     static constexpr int kKeys = DP == 256 ? 16 : 32;  // keys of a warp's slice
     static constexpr int kMt = kKeys / 16;
     static constexpr int kWarps = 4, kThreads = 32 * kWarps;
-    static constexpr int kKeyTile = kWarps * kKeys;  // keys of a unit
+    static constexpr int kKeyWarps = kWarps / HG;       // warps of a head, each with slices of its own
+    static constexpr int kKeyTile = kKeyWarps * kKeys;  // keys of a unit
     static constexpr int kChunks = DP / 16;          // 16-byte groups of a row
     static constexpr int kHalf = kKeys * DP;         // K (or V) of a slice
     static constexpr int kStage = 2 * kHalf;
-    static constexpr int kStages = DP == 64 ? 4 : (NT * DP > 256 ? 3 : 2);
-    static constexpr int kExtra = DP == 64 ? 4 : 2;  // what an item costs beside its key tiles
-    static constexpr int kBlocksPerSm = NT * DP > 256 ? 2 : 3;
+    static constexpr int kStages = DP == 64 ? 4 : (NT == 2 ? 3 : 2);
+    static constexpr int kExtra = 2;  // what an item costs beside its key tiles
+    static constexpr int kBlocksPerSm = NT == 2 && DP >= 128 ? 2 : 3;
     static constexpr bool kQInSmem = NT * DP > 128;  // (else in registers)
-    static constexpr int kQBytes = kRowTile * DP * 2;
-    static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage + kQBytes;
+    static constexpr int kQBytes = kRowTile * DP * 2;  // of a head
+    static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage + HG * kQBytes;
     // A warp's output in fp32 goes through the stage just consumed, in as many rounds as it takes.
     static constexpr int kRounds = kRowTile * DP * 4 > kStage ? kRowTile * DP * 4 / kStage : 1;
     static constexpr int kRoundRows = kRowTile / kRounds;
@@ -54,15 +55,20 @@ struct SliceI8 {
     }
 };
 
+__device__ __forceinline__ void copy16_all(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <bool BF16>
 __device__ __forceinline__ void store_out4(const AttnArgs& a, long long row, int col, float4 v) {
     uint2 w = make_uint2(pack16<BF16>(v.x, v.y), pack16<BF16>(v.z, v.w));
     *reinterpret_cast<uint2*>(a.out + ((size_t)row * a.D + col) * 2) = w;
 }
 
-template <bool BF16, int DP, int NT>
-__global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kBlocksPerSm) attn_i8_kernel(AttnArgs a) {
-    using C = SliceI8<DP, NT>;
+// a.Hk counts groups of HG heads here.
+template <bool BF16, int DP, int NT, int HG>
+__global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT, HG>::kBlocksPerSm) attn_i8_kernel(AttnArgs a) {
+    using C = SliceI8<DP, NT, HG>;
     constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kRows = C::kRowTile, MT = C::kMt;
     constexpr int KS = DP / 16;  // k-steps over the head dimension, and m-tiles of the output
     constexpr int R = 2 * NT;    // rows of a lane: 8 j + 2 t + (0, 1)
@@ -70,27 +76,32 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
     __shared__ float2 s_ml[kWarps][kRows];
     __shared__ int s_err;
     __shared__ AttnScratch s_start;
-    __shared__ uint32_t s_qmax[kRows];  // largest |q| of each row (its bits)
+    __shared__ uint32_t s_qmax[HG * kRows];        // largest |q| of each row (its bits); rows of the first head, the second, ...
+    __shared__ float s_qsum[HG * kRows][DP / 8];  // sums of a row's query, eight values each
+    __shared__ float s_base[HG * kRows], s_scale[HG * kRows];  // where a row's products begin, its scores' factor
+    __shared__ AttnStart s_range;                    // the block's units
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
+    const int my_head = warp % HG, my_keys = warp / HG;  // of the group's heads, of the unit's slices
     const int part = blockIdx.x, parts = gridDim.x;
     wait_primary();
     launch_dependents();
     if (tid == 0) s_err = 0;
     bool bad;
-    const AttnStart start = attn_start<kThreads>(a, kRows, C::kKeyTile, C::kExtra, parts, part, 2 + C::kExtra, &s_start, &bad);
+    const AttnStart start = attn_start<kThreads>(a, kRows, C::kKeyTile, C::kExtra, parts, part, 1 + C::kExtra, &s_start, &bad);
 
     attn_tail_rows(a, (size_t)part * kThreads + tid, (size_t)parts * kThreads);
     unsigned char* ring = smem + (size_t)warp * C::kStages * C::kStage;
     const uint32_t ring_addr = smem_addr(ring);
     unsigned char* qs = smem + (size_t)kWarps * C::kStages * C::kStage;
-    const uint32_t qs_addr = smem_addr(qs);
+    const uint32_t qs_addr = smem_addr(qs) + my_head * C::kQBytes;
     int err = bad ? DSPARK_ERR_CACHE : 0;
+    if (tid == 0) s_range = start;  // (read by this thread)
 
     // ---- loads: `ld` walks ahead of the arithmetic; `pid` is the page of this lane's key of its slice
     AttnWalk ld = walk_begin(a, start, kRows, C::kKeyTile, C::kExtra);
-    int ld_head = ld.done() ? 0 : ld.item / ld.rts;
-    auto slice_key = [&](const AttnWalk& w) { return (w.kt_first + w.kt) * C::kKeyTile + warp * C::kKeys; };
+    int ld_group = ld.done() ? 0 : ld.item / ld.rts;
+    auto slice_key = [&](const AttnWalk& w) { return (w.kt_first + w.kt) * C::kKeyTile + my_keys * C::kKeys; };
     auto fetch_page = [&]() -> int {
         const int key = slice_key(ld) + lane;
         if (ld.done() || lane >= C::kKeys || key >= ld.r.seq) return -1;
@@ -100,13 +111,14 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
     int ld_stage = 0;
     // An item's queries, asked for (into L1) when its first keys are.
     auto touch_queries = [&]() {
-        const int first = (ld.item - ld_head * ld.rts) * kRows;
+        const int first = (ld.item - ld_group * ld.rts) * kRows;
         const int last = min(ld.r.n * a.G, first + kRows);
-        for (int i = lane; i < kRows * (DP / 64); i += 32) {
-            const int row = first + i / (DP / 64), token = attn_token(a, row), d = 64 * (i % (DP / 64));
+        for (int i = lane; i < HG * kRows * (DP / 64); i += 32) {
+            const int head = ld_group * HG + i / (kRows * (DP / 64)), row = first + i / (DP / 64) % kRows;
+            const int token = attn_token(a, row), d = 64 * (i % (DP / 64));
             if (row < last && d < a.D)
                 asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + 2 * ((ld.r.token0 + token) * a.q_token +
-                                                                        (ld_head * a.G + row - token * a.G) * a.q_head + d)));
+                                                                        (head * a.G + row - token * a.G) * a.q_head + d)));
         }
     };
     if (warp == 0 && !ld.done()) touch_queries();
@@ -115,28 +127,29 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
     auto load_step = [&](int queue) {
         k_exp[queue] = v_exp[queue] = 0;
         if (!ld.done() && slice_key(ld) < ld.r.seq) {
-            const int key = slice_key(ld) + lane, place = key & ((1 << a.page_shift) - 1);
+            const int key = slice_key(ld) + lane, place = key & ((1 << a.page_shift) - 1), head = ld_group * HG + my_head;
             const bool live = lane < C::kKeys && key < ld.r.seq && key >= ld.r.lo;
             const bool found = live && pid >= 0 && pid < a.num_pages;
             if (live && !found) err = DSPARK_ERR_CACHE;
             if (found) {
-                const long long e = exponents_at(a, pid, place, ld_head);
+                const long long e = exponents_at(a, pid, place, head);
                 k_exp[queue] = __ldg(a.exp.k + e);
                 v_exp[queue] = __ldg(a.exp.v + e);
             }
-            const long long off = found ? pid * a.page + place * a.token + ld_head * a.head : -1;
+            const long long off = found ? pid * a.page + place * a.token + head * a.head : -1;
             const uint32_t dst = ring_addr + ld_stage * C::kStage;
             constexpr int kPer = 32 / C::kChunks;  // rows a warp copies at a time
             const int chunk = lane % C::kChunks;
-            const bool inside = chunk * 16 < a.D;
+            // What is not there is not copied: the bytes that a stage still holds are codes too, and finite ones, which meet
+            // queries of zero, weights of zero or values that nobody stores.
 #pragma unroll
             for (int i = 0; i < C::kKeys / kPer; ++i) {
                 const int row = i * kPer + lane / C::kChunks;
                 const long long o = __shfl_sync(0xffffffffu, off, row);
-                const bool real = inside && o >= 0;
-                const long long src = real ? o + chunk * 16 : 0;
-                copy16(dst + C::at(row, chunk), a.k_pages + src, real);
-                copy16(dst + C::kHalf + C::at(row, chunk), a.v_pages + src, real);
+                if (chunk * 16 < a.D && o >= 0) {
+                    copy16_all(dst + C::at(row, chunk), a.k_pages + o + chunk * 16);
+                    copy16_all(dst + C::kHalf + C::at(row, chunk), a.v_pages + o + chunk * 16);
+                }
             }
         }
         cp_async_commit();
@@ -145,7 +158,7 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
             walk_next(a, ld, kRows, C::kKeyTile);
             pid = fetch_page();
             if (ld.kt == 0 && !ld.done()) {
-                ld_head = ld.item / ld.rts;
+                ld_group = ld.item / ld.rts;
                 if (warp == 0) touch_queries();
             }
         }
@@ -160,8 +173,12 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
     float o[KS][NT][4];  // [16 values of a head][8 rows]: values 2 g (rows 2 t, 2 t + 1), 2 g + 1
     uint32_t qf[C::kQInSmem ? 1 : KS][NT][2];
     const float cap_out = a.softcap * kLog2e;
-    float m[R], mv[R], l[R], row_scale[R];
-    int all_lo = 0, all_hi = 0, rows = 0, head = 0, row0 = 0, seg_first = 0;
+    constexpr float kUp = ProbScale<false>::kBits;
+    // What is taken off the exponents of sums and weights: kUp less than the largest that a row followed (kNone: it has seen
+    // nothing), and the sums.
+    constexpr float kNone = -3e38f;
+    float ref[R], ref_v[R], l[R];
+    int all_lo = 0, all_hi = 0, rows = 0, group = 0, row0 = 0, seg_first = 0;
     bool fresh = true;
     int st = 0;
     auto row_of = [&](int r) { return 8 * (r >> 1) + 2 * t + (r & 1); };
@@ -176,25 +193,26 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
         if (fresh) {  // a new segment: its rows, their queries and what each may see
             fresh = false;
             seg_first = w.kt;
-            head = w.item / w.rts;
-            row0 = (w.item - head * w.rts) * kRows;
+            group = w.item / w.rts;
+            row0 = (w.item - group * w.rts) * kRows;
             rows = min(w.r.n * a.G - row0, kRows);
             all_lo = attn_see_lo(a, w.r, attn_token(a, row0 + rows - 1));
             all_hi = attn_see_hi(a, w.r, attn_token(a, row0));
             // The queries, through shared memory: 16 bytes a thread, then fragments by ldmatrix.  (The previous segment's
             // readers are past its last barrier.)
             constexpr int kQc = DP / 8;
-            constexpr int kQSteps = (kRows * kQc + kThreads - 1) / kThreads;
+            constexpr int kQRows = HG * kRows, kQSteps = (kQRows * kQc + kThreads - 1) / kThreads;
             uint4 qv[kQSteps];
             if (BF16) {
-                if (tid < kRows) s_qmax[tid] = 0;
+                if (tid < kQRows) s_qmax[tid] = 0;
                 __syncthreads();
             }
 #pragma unroll
             for (int u = 0; u < kQSteps; ++u) {
-                const int row = (tid + u * kThreads) / kQc, c = (tid + u * kThreads) % kQc, token = attn_token(a, row0 + row);
+                const int qrow = (tid + u * kThreads) / kQc, c = (tid + u * kThreads) % kQc;
+                const int row = qrow % kRows, head = group * HG + qrow / kRows, token = attn_token(a, row0 + row);
                 qv[u] = make_uint4(0, 0, 0, 0);
-                if (kRows * kQc % kThreads && row >= kRows) continue;
+                if (kQRows * kQc % kThreads && qrow >= kQRows) continue;
                 if (row < rows && 8 * c < a.D) {
                     const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (w.r.token0 + token) * a.q_token +
                                           (head * a.G + row0 + row - token * a.G) * a.q_head + 8 * c;
@@ -211,41 +229,55 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
                     const uint32_t* y = reinterpret_cast<const uint32_t*>(&qv[u]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) big = fmaxf(big, fmaxf(fabsf(bf16_lo(y[e])), fabsf(bf16_hi(y[e]))));
-                    atomicMax(&s_qmax[row], __float_as_uint(big));
+                    atomicMax(&s_qmax[qrow], __float_as_uint(big));
                 }
             }
             // bf16 queries as halves: each row times the power of two that brings its largest value to 2^14, taken back
             // in the scores' scale; what a half then cannot hold is below 2^-38 of the row's largest, less than fp32
             // keeps of the sum.
-            auto raise = [&](int row) {
-                const int e = (int)(s_qmax[row] >> 23) - 127;  // floor(log2) of a normal number
+            auto raise = [&](int qrow) {
+                const int e = (int)(s_qmax[qrow] >> 23) - 127;  // floor(log2) of a normal number
                 return e > -127 && e < 128 ? min(max(14 - e, -120), 120) : 0;
             };
             if (BF16) __syncthreads();
 #pragma unroll
             for (int u = 0; u < kQSteps; ++u) {
-                const int row = (tid + u * kThreads) / kQc, c = (tid + u * kThreads) % kQc;
-                if (kRows * kQc % kThreads && row >= kRows) continue;
-                // codes arrive four k a lane: the MMA's k slots (2t, 2t + 1 | 2t + 8, 2t + 9) hold k = 4t .. 4t + 3, so
-                // pair p of 16 values goes to pair p / 2 + 4 (p % 2)
-                const uint32_t* y = reinterpret_cast<const uint32_t*>(&qv[u]);
-                const float up = BF16 ? two_to(raise(row)) : 1.f;
+                const int qrow = (tid + u * kThreads) / kQc, c = (tid + u * kThreads) % kQc;
+                if (kQRows * kQc % kThreads && qrow >= kQRows) continue;
+                // Codes arrive four k a lane and are taken apart by even and odd bytes: the MMA's k slots 2t, 2t + 1 hold
+                // k = 4t, 4t + 2 and its slots 2t + 8, 2t + 9 hold k = 4t + 1, 4t + 3.
+                uint32_t* y = reinterpret_cast<uint32_t*>(&qv[u]);
+                const float up = BF16 ? two_to(raise(qrow)) : 1.f;
+                float sum = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int p = 4 * (c & 1) + e, to = (p >> 1) + 4 * (p & 1);
-                    const uint32_t x = BF16 ? pack16<false>(bf16_lo(y[e]) * up, bf16_hi(y[e]) * up) : y[e];
-                    *reinterpret_cast<uint32_t*>(qs + C::q_at(row, (c & ~1) + (to >> 2)) + 4 * (to & 3)) = x;
+                    if (BF16) y[e] = pack16<false>(bf16_lo(y[e]) * up, bf16_hi(y[e]) * up);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[e]));
+                    sum += f.x + f.y;
                 }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int at = 4 * (e + 2 * (c & 1));
+                    *reinterpret_cast<uint32_t*>(qs + C::q_at(qrow, c & ~1) + at) = __byte_perm(y[2 * e], y[2 * e + 1], 0x5410);
+                    *reinterpret_cast<uint32_t*>(qs + C::q_at(qrow, c | 1) + at) = __byte_perm(y[2 * e], y[2 * e + 1], 0x7632);
+                }
+                s_qsum[qrow][c] = sum;
             }
             __syncthreads();
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                m[r] = mv[r] = -CUDART_INF_F;
+                ref[r] = ref_v[r] = kNone;
                 l[r] = 0.f;
-                // to the log2 domain, or to the cap's exponent
-                row_scale[r] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale;
-                if (BF16) row_scale[r] *= two_to(-raise(row_of(r)));
             }
+            if (tid < kQRows) {
+                float sum = 0.f;
+#pragma unroll 4
+                for (int i = 0; i < DP / 8; ++i) sum += s_qsum[tid][i];
+                s_base[tid] = -128.f * 0x1p-24f * sum;
+                // to the log2 domain, or to the cap's exponent
+                s_scale[tid] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale * 0x1p24f * (BF16 ? two_to(-raise(tid)) : 1.f);
+            }
+            __syncthreads();
             if (!C::kQInSmem) {
 #pragma unroll
                 for (int ks = 0; ks < KS; ks += NT == 1 ? 2 : 1) {
@@ -284,19 +316,23 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
         if (key0 < w.r.seq) {
             const uint32_t kb = ring_addr + st * C::kStage, vb = kb + C::kHalf;
             // ---- S^T: lane (g, t) gets keys 16 i + g (c < 2), + 8, of rows 8 j + 2 t + (c & 1)
-            float s[MT][NT][4];
+            float s[MT][NT][4], row_base[R], row_scale[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) row_base[r] = s_base[my_head * kRows + row_of(r)];
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[i][j][c] = 0.f;
-            auto codes_a = [](uint32_t (&f)[4], uint32_t lo, uint32_t hi) {  // four k of keys g and g + 8
-                const uint32_t x = lo ^ 0x80808080u, y = hi ^ 0x80808080u;
-                f[0] = i8x2_to_half2<kBytes01>(x);
-                f[1] = i8x2_to_half2<kBytes01>(y);
-                f[2] = i8x2_to_half2<kBytes23>(x);
-                f[3] = i8x2_to_half2<kBytes23>(y);
+                    for (int c = 0; c < 4; ++c) s[i][j][c] = row_base[2 * j + (c & 1)];
+            // Four k of keys g and g + 8.  A byte alone in a half is the subnormal number byte 2^-24, so a key's code needs
+            // no arithmetic: code + 128 goes in, and the products begin at - 128 times the sum of the row's query instead
+            // of zero.  (What fp32 loses by that is 2^-24 of 128 sum |q|, the error of 2^-16 of a code.)
+            auto codes_a = [](uint32_t (&f)[4], uint32_t lo, uint32_t hi) {
+                f[0] = (lo & 0x00ff00ffu) ^ 0x00800080u;
+                f[1] = (hi & 0x00ff00ffu) ^ 0x00800080u;
+                f[2] = ((lo >> 8) & 0x00ff00ffu) ^ 0x00800080u;
+                f[3] = ((hi >> 8) & 0x00ff00ffu) ^ 0x00800080u;
             };
 #pragma unroll
             for (int ks = 0; ks < KS; ks += 2) {
@@ -360,6 +396,8 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
                 }
             // scores in the log2 domain, hidden ones -inf
 #pragma unroll
+            for (int r = 0; r < R; ++r) row_scale[r] = s_scale[my_head * kRows + row_of(r)];
+#pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
@@ -391,6 +429,8 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
                         }
                 }
             }
+            // The references follow a row's maxima only when these are 2^8 ahead (values up to 2^8 lose nothing), so most
+            // slices need no maximum over the lanes and do not touch the output.
             float mx[R], mz[R];
             bool grow = false;
 #pragma unroll
@@ -404,23 +444,21 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
                         mx[r] = fmaxf(mx[r], x);
                         mz[r] = fmaxf(mz[r], x + value_exp[i][h]);
                     }
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], d));
-                    mz[r] = fmaxf(mz[r], __shfl_xor_sync(0xffffffffu, mz[r], d));
-                }
-                grow |= mx[r] > m[r] + 8.f || mz[r] > mv[r] + 8.f;
+                grow |= mx[r] > ref[r] + (kUp + 8.f) || mz[r] > ref_v[r] + (kUp + 8.f);
             }
-            // The references follow the maxima only when they are 2^8 behind (values up to 2^8 lose nothing), so most
-            // slices do not touch the output.
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float mn = fmaxf(m[r], mx[r]), zn = fmaxf(mv[r], mz[r]);
-                    if (mn != m[r]) l[r] *= ex2(m[r] - mn);  // m = -inf: 0
-                    m[r] = mn;
-                    const float f = zn == mv[r] ? 1.f : ex2(mv[r] - zn);
-                    mv[r] = zn;
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) {
+                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], d));
+                        mz[r] = fmaxf(mz[r], __shfl_xor_sync(0xffffffffu, mz[r], d));
+                    }
+                    const float mn = fmaxf(ref[r], mx[r] - kUp), zn = fmaxf(ref_v[r], mz[r] - kUp);
+                    if (mn != ref[r]) l[r] *= ex2(ref[r] - mn);
+                    const float f = zn == ref_v[r] ? 1.f : ex2(ref_v[r] - zn);
+                    ref[r] = mn;
+                    ref_v[r] = zn;
 #pragma unroll
                     for (int i = 0; i < KS; ++i) {
                         o[i][r >> 1][r & 1] *= f;
@@ -429,14 +467,7 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
                 }
             }
             // ---- P^T as halves, fragments of the second product's B
-            constexpr float kUp = ProbScale<false>::kBits;
             uint32_t p[MT][NT][2];
-            float ref[R], ref_v[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                ref[r] = m[r] == -CUDART_INF_F ? 0.f : m[r] - kUp;
-                ref_v[r] = mv[r] == -CUDART_INF_F ? 0.f : mv[r] - kUp;
-            }
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -476,9 +507,9 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
             for (int r = 0; r < R; ++r) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], d);
-                if (g == 0) s_ml[warp][row_of(r)] = make_float2(m[r], l[r]);
+                if (g == 0) s_ml[warp][row_of(r)] = make_float2(ref[r] == kNone ? -CUDART_INF_F : ref[r] + kUp, l[r]);
                 // to the reference of the sums, in two steps: 2^f may be as large as fp32's numbers
-                const float f = m[r] == -CUDART_INF_F ? 1.f : ex2(0.5f * (mv[r] - m[r]));
+                const float f = ex2(0.5f * (ref_v[r] - ref[r]));
 #pragma unroll
                 for (int i = 0; i < KS; ++i) {
                     o[i][r >> 1][r & 1] = o[i][r >> 1][r & 1] * f * f;
@@ -501,16 +532,17 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
                             make_float2(o[i][r >> 1][r & 1], o[i][r >> 1][2 + (r & 1)]);
                 }
                 __syncthreads();
-                const int end = min(rows - round * C::kRoundRows, C::kRoundRows);
-                for (int i = tid; i < end * (DP / 4); i += kThreads) {
-                    const int row = round * C::kRoundRows + i / (DP / 4), col = 4 * (i % (DP / 4));
+                for (int i = tid; i < HG * C::kRoundRows * (DP / 4); i += kThreads) {
+                    const int hd = i / (C::kRoundRows * (DP / 4)), head = group * HG + hd;
+                    const int row = round * C::kRoundRows + i / (DP / 4) % C::kRoundRows, col = 4 * (i % (DP / 4));
+                    if (row >= rows) continue;
                     float mm = -CUDART_INF_F, ll = 0.f;
 #pragma unroll
-                    for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, s_ml[x][row].x);
+                    for (int x = hd; x < kWarps; x += HG) mm = fmaxf(mm, s_ml[x][row].x);
                     const float ref = mm == -CUDART_INF_F ? 0.f : mm;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int x = 0; x < kWarps; ++x) {
+                    for (int x = hd; x < kWarps; x += HG) {
                         const float2 ml = s_ml[x][row];
                         const float f = ex2(ml.x - ref);
                         if (ml.y == 0.f) continue;  // saw nothing
@@ -531,12 +563,13 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
                         if (a.lse && col == 0)
                             a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll * ProbScale<false>::kInverse)) * kLn2;
                     } else {
-                        if (col < a.D) *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * kRows + row) * a.D + col) = v;
-                        if (col == 0) a.part_ml[(size_t)slot * kRows + row] = make_float2(mm, ll);
+                        const size_t at = (size_t)slot * (HG * kRows) + hd * kRows + row;
+                        if (col < a.D) *reinterpret_cast<float4*>(a.part_o + at * a.D + col) = v;
+                        if (col == 0) a.part_ml[at] = make_float2(mm, ll);
                     }
                 }
             }
-            if (!whole && tid == 0) mine->d[seg_first == 0 ? kHead : kTail] = part_desc(start, w, row0, rows, head);
+            if (!whole && tid == 0) mine->d[seg_first == 0 ? kHead : kTail] = part_desc(s_range, w, row0, rows, group);
             __syncthreads();
             fresh = true;
         }
@@ -549,32 +582,42 @@ __global__ void __launch_bounds__(SliceI8<DP, NT>::kThreads, SliceI8<DP, NT>::kB
     if (tid == 0) mine->err = s_err;
 }
 
-template <bool BF16, int DP, int NT>
-dspark_status launch_slices(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
-    using C = SliceI8<DP, NT>;
+template <bool BF16, int DP, int NT, int HG>
+dspark_status launch_slices(AttnArgs a, int sms, cudaStream_t s, int* parts) {
+    using C = SliceI8<DP, NT, HG>;
     int per_sm = 0;
-    auto fn = attn_i8_kernel<BF16, DP, NT>;
+    auto fn = attn_i8_kernel<BF16, DP, NT, HG>;
     if (prepare_kernel((const void*)fn, C::kSmem, C::kThreads, &per_sm) != cudaSuccess || per_sm < 1) return DSPARK_ERR_CUDA;
     int n = sms * (per_sm < C::kBlocksPerSm ? per_sm : C::kBlocksPerSm);
     if (n > kMaxParts) n = kMaxParts;
     *parts = n;
+    a.Hk /= HG;
     return launch_overlapped(fn, n, C::kThreads, C::kSmem, s, a) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
-template <bool BF16, int DP>
-dspark_status launch_slices_d(const AttnArgs& a, int row_tile, int sms, cudaStream_t s, int* parts) {
-    return row_tile == 8 ? launch_slices<BF16, DP, 1>(a, sms, s, parts) : launch_slices<BF16, DP, 2>(a, sms, s, parts);
-}
-template <bool BF16>
-dspark_status launch_slices_t(const AttnArgs& a, int row_tile, int sms, cudaStream_t s, int* parts) {
-    if (a.D <= 64) return launch_slices_d<BF16, 64>(a, row_tile, sms, s, parts);
-    if (a.D <= 128) return launch_slices_d<BF16, 128>(a, row_tile, sms, s, parts);
-    return launch_slices_d<BF16, 256>(a, row_tile, sms, s, parts);
+template <bool BF16, int NT>
+dspark_status launch_slices_d(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
+    const int heads = i8_head_group(a.D, a.Hk);
+    if (a.D <= 64) {
+        if (heads == 4) return launch_slices<BF16, 64, NT, 4>(a, sms, s, parts);
+        return heads == 2 ? launch_slices<BF16, 64, NT, 2>(a, sms, s, parts) : launch_slices<BF16, 64, NT, 1>(a, sms, s, parts);
+    }
+    if (a.D <= 128) return heads == 2 ? launch_slices<BF16, 128, NT, 2>(a, sms, s, parts) : launch_slices<BF16, 128, NT, 1>(a, sms, s, parts);
+    return launch_slices<BF16, 256, NT, 1>(a, sms, s, parts);
 }
 
 }  // namespace
 
+// Heads that lie side by side are read together where one head's row is less than a 128-byte line or not many: the warps
+// of a block take a head each.  (Otherwise the lines that two heads share are read twice, by blocks far apart in time: 128
+// requests up to 3000 tokens, 8 heads of 64: 445 MB read for 223.)
+int i8_head_group(int D, int Hk) {
+    if (D <= 64 && Hk % 4 == 0) return 4;
+    return D <= 128 && Hk % 2 == 0 ? 2 : 1;
+}
+
 dspark_status launch_attn_i8(const AttnArgs& a, bool bf16, int row_tile, int sms, cudaStream_t s, int* parts) {
-    return bf16 ? launch_slices_t<true>(a, row_tile, sms, s, parts) : launch_slices_t<false>(a, row_tile, sms, s, parts);
+    if (bf16) return row_tile == 8 ? launch_slices_d<true, 1>(a, sms, s, parts) : launch_slices_d<true, 2>(a, sms, s, parts);
+    return row_tile == 8 ? launch_slices_d<false, 1>(a, sms, s, parts) : launch_slices_d<false, 2>(a, sms, s, parts);
 }
 
 }  // namespace dspark

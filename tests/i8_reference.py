@@ -74,7 +74,8 @@ def attention(q, codes, exps, table, seq_len, offsets, scale, causal, window, so
     magnitude of at most |s| + |e| + 8, with s in the log2 domain.  An error d of the exponents changes out by at most 2 d
     sum p |v| and lse by d.  The hardware exponential and logarithm are within 2^-21 and the fp32 sums over N keys, taken
     by 16 lanes and joined, within (N / 16 + 400) 2^-24.  A weight below 2^-21 of the largest is a subnormal half, off by
-    at most 2^-32 of the largest weight, times 127."""
+    at most 2^-32 of the largest weight, times 127; in the kernel of many rows, where the values carry their scales, so is a
+    probability (fp16), times its value."""
     T, Hq, D = q.shape
     P, page, Hk, _ = codes[0].shape
     G, dtype, dev = Hq // Hk, q.dtype, q.device
@@ -117,10 +118,16 @@ def attention(q, codes, exps, table, seq_len, offsets, scale, causal, window, so
             w = p * two_to(e.long())
             top = w.amax(-1, keepdim=True)
             tiny = 127 * 2.0 ** -32 * top[..., 0] * ((w < 2.0 ** -21 * top) & see[:, None]).sum(-1)
+            if wide and dtype == torch.float16:  # 2^7 p / p_ref with p_ref within 2^-8 .. 1 of the largest, off by 2^-25
+                most = p.amax(-1, keepdim=True)
+                small = ((p < 2.0 ** -21 * most) & see[:, None]).double()
+                away_tiny = 2.0 ** -32 * most * torch.einsum("ngl,ld->ngd", small, v.abs())
+            else:
+                away_tiny = 0.0
             rows = slice(h * G, (h + 1) * G)
             out[a:b, rows], lse[a:b, rows] = o, ls
             tol[a:b, rows] = (u * (o.abs() + 2 * u_p * away) + away * (u_p + 2 * d + 2 * N * 2.0 ** -24)[..., None]
-                              + tiny[..., None])
+                              + tiny[..., None] + away_tiny)
             tol_lse[a:b, rows] = d + N * 2.0 ** -24 + torch.where(dead, 0.0, ls).abs() * 2.0 ** -22
     if dtype == torch.float16:
         tol += 2.0 ** -25  # half a step of the subnormal halves
