@@ -75,6 +75,7 @@ struct PartItem {
 enum { kTail = 0, kHead = 1 };
 constexpr int kMaxParts = 480;    // blocks of the largest grid with row tiles of 16 (three a multiprocessor)
 constexpr int kMaxTcParts = 160;  // and of 128 (one)
+constexpr int kMaxI8Parts = 640;  // and over an int8 cache (four)
 
 // One request as the kernels see it: every number clamped to the buffers (bad: it was not).  Keys before lo,
 // the first that any row sees, have no pages any more as far as a call is concerned.
@@ -117,7 +118,7 @@ struct AttnStart {
 };
 
 struct AttnScratch {  // in shared memory, for attn_start
-    long long warp_sum[16], at;
+    long long warp_sum[20], at;
     int j;
 };
 
@@ -126,7 +127,7 @@ struct AttnScratch {  // in shared memory, for attn_start
 template <int THREADS>
 __device__ AttnStart attn_start(const AttnArgs& a, int row_tile, int key_tile, int extra, int parts, int part, int min_units,
                                 AttnScratch* scratch, bool* bad) {
-    static_assert(THREADS / 32 <= 16, "scratch");
+    static_assert(THREADS / 32 <= 20, "scratch");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int m = (a.B + THREADS - 1) / THREADS;
     const int j0 = min(tid * m, a.B), j1 = min(j0 + m, a.B);
@@ -351,5 +352,8 @@ dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int kv, int sms, cuda
 // Row tiles of 8 or 16 over int8 pools (paged_attn_i8.cu), for i8_head_group kv heads at a time.
 int i8_head_group(int D, int Hk);
 dspark_status launch_attn_i8(const AttnArgs& a, bool bf16, int row_tile, int sms, cudaStream_t s, int* parts);
+
+// Row tiles of 16, 32 or 64 over int8 pools (paged_attn_i8_rows.cu).
+dspark_status launch_attn_i8_rows(const AttnArgs& a, bool bf16, int row_tile, int sms, cudaStream_t s, int* parts);
 
 }  // namespace dspark

@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
     // What is taken off the exponents of sums and weights: kUp less than the largest that a row followed (kNone: it has seen
     // nothing), and the sums.
     constexpr float kNone = -3e38f;
-    float ref[R], ref_v[R], l[R];
+    float ref[R], ref_v[R];
+    uint64_t sums[NT];  // of rows 8 j + 2 t and the next
     int all_lo = 0, all_hi = 0, rows = 0, group = 0, row0 = 0, seg_first = 0;
     bool fresh = true;
     int st = 0;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 ref[r] = ref_v[r] = kNone;
-                l[r] = 0.f;
+                if (!(r & 1)) sums[r >> 1] = 0;
             }
             if (tid < kQRows) {
                 float sum = 0.f;
@@ -402,7 +403,12 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[i][j][c] = s[i][j][c] * row_scale[2 * j + (c & 1)] * key_scale[i][c >> 1];
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 x = up2(mul2(mul2(pk2(s[i][j][2 * h], s[i][j][2 * h + 1]), pk2(row_scale[2 * j], row_scale[2 * j + 1])),
+                                                  pk2(key_scale[i][h], key_scale[i][h])));
+                        s[i][j][2 * h] = x.x;
+                        s[i][j][2 * h + 1] = x.y;
+                    }
             if (a.softcap > 0.f) {
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
@@ -437,13 +443,11 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
             for (int r = 0; r < R; ++r) {
                 mx[r] = mz[r] = -CUDART_INF_F;
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float x = s[i][r >> 1][2 * h + (r & 1)];
-                        mx[r] = fmaxf(mx[r], x);
-                        mz[r] = fmaxf(mz[r], x + value_exp[i][h]);
-                    }
+                for (int i = 0; i < MT; ++i) {
+                    const float x = s[i][r >> 1][r & 1], y = s[i][r >> 1][2 + (r & 1)];
+                    mx[r] = fmax3(mx[r], x, y);
+                    mz[r] = fmax3(mz[r], x + value_exp[i][0], y + value_exp[i][1]);
+                }
                 grow |= mx[r] > ref[r] + (kUp + 8.f) || mz[r] > ref_v[r] + (kUp + 8.f);
             }
             if (__any_sync(0xffffffffu, grow)) {
@@ -455,7 +459,11 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
                         mz[r] = fmaxf(mz[r], __shfl_xor_sync(0xffffffffu, mz[r], d));
                     }
                     const float mn = fmaxf(ref[r], mx[r] - kUp), zn = fmaxf(ref_v[r], mz[r] - kUp);
-                    if (mn != ref[r]) l[r] *= ex2(ref[r] - mn);
+                    if (mn != ref[r]) {
+                        const float fl = ex2(ref[r] - mn);
+                        const float2 l = up2(sums[r >> 1]);
+                        sums[r >> 1] = r & 1 ? pk2(l.x, l.y * fl) : pk2(l.x * fl, l.y);
+                    }
                     const float f = zn == ref_v[r] ? 1.f : ex2(ref_v[r] - zn);
                     ref[r] = mn;
                     ref_v[r] = zn;
@@ -474,11 +482,11 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float x = s[i][j][2 * h], y = s[i][j][2 * h + 1];
-                        l[2 * j] += ex2(x - ref[2 * j]);
-                        l[2 * j + 1] += ex2(y - ref[2 * j + 1]);
-                        p[i][j][h] = transpose8x8(pack16<false>(ex2(x + value_exp[i][h] - ref_v[2 * j]),
-                                                                ex2(y + value_exp[i][h] - ref_v[2 * j + 1])));
+                        const uint64_t x = pk2(s[i][j][2 * h], s[i][j][2 * h + 1]);
+                        const float2 e = up2(add2(x, pk2(-ref[2 * j], -ref[2 * j + 1])));
+                        const float2 z = up2(add2(add2(x, pk2(value_exp[i][h], value_exp[i][h])), pk2(-ref_v[2 * j], -ref_v[2 * j + 1])));
+                        sums[j] = add2(sums[j], pk2(ex2(e.x), ex2(e.y)));
+                        p[i][j][h] = transpose8x8(pack16<false>(ex2(z.x), ex2(z.y)));
                     }
             // ---- O^T += V^T P^T: bytes (k0 d0, k0 d1, k1 d0, k1 d1) are rows 2 g and 2 g + 1 of the m-tile, which are
             // its rows g and g + 8 to the MMA.  (What nobody sees needs no care: codes are finite.)
@@ -505,9 +513,11 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
             // ---- the warps' parts of the segment meet
 #pragma unroll
             for (int r = 0; r < R; ++r) {
+                const float2 both = up2(sums[r >> 1]);
+                float l = r & 1 ? both.y : both.x;
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], d);
-                if (g == 0) s_ml[warp][row_of(r)] = make_float2(ref[r] == kNone ? -CUDART_INF_F : ref[r] + kUp, l[r]);
+                for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+                if (g == 0) s_ml[warp][row_of(r)] = make_float2(ref[r] == kNone ? -CUDART_INF_F : ref[r] + kUp, l);
                 // to the reference of the sums, in two steps: 2^f may be as large as fp32's numbers
                 const float f = ex2(0.5f * (ref_v[r] - ref[r]));
 #pragma unroll

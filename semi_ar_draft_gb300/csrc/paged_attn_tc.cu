@@ -46,15 +46,23 @@ struct TcAttn {
     static constexpr int kSoftmaxWarps = 4 * kStreams;
     // Four loader warps, two a stream: a warp that copied a part of every tile spent more time between tiles
     // (waits, page numbers, the walk) than on its copies.
-    static constexpr int kLoaders = 4;
+    // An int8 cache has eight: widening its tiles is most of the work.
+    static constexpr int kLoaders = KV == kKvI8 ? 8 : 4;
     static constexpr int kTileLoaders = kLoaders / kStreams;
     // Warps after the softmax's: multiprocessor quarter (warp % 4) 0 has none of them and quarter 1 the MMA
     // warps, one a stream; the loaders are in quarters 2 and 3.  Short row tiles keep quarter 0 busiest.
-    static constexpr int kWarps = kSoftmaxWarps + 8;
-    static __device__ __forceinline__ int loader_of(int warp) {  // 0 .. 3, or -1
+    // (int8: the other two loaders in quarters 1 and 0.)
+    static constexpr int kWarps = kSoftmaxWarps + (KV == kKvI8 ? 12 : 8);
+    static __device__ __forceinline__ int loader_of(int warp) {  // 0 .. kLoaders - 1, or -1
         const int h = warp - kSoftmaxWarps;
-        return h >= 0 && (h & 2) ? (h >> 2) * 2 + (h & 1) : -1;
+        if (h >= 0 && (h & 2)) return (h >> 2) * 2 + (h & 1);
+        return KV == kKvI8 && (h == 8 || h == 9) ? h - 2 : -1;
     }
+    // Twenty warps are launched with 96 registers a thread (61440), which is too little for the softmax and more than the
+    // others need: whole warpgroups give and take (the softmax's warps come first).
+    static constexpr bool kDealRegisters = KV == kKvI8 && kStreams == 2;
+    static constexpr int kSoftmaxRegisters = 120, kHelperRegisters = 80;
+    static_assert(!kDealRegisters || 32 * (kSoftmaxWarps * kSoftmaxRegisters + 12 * kHelperRegisters) <= 32 * 20 * 96, "the launch's registers");
     static __device__ __forceinline__ int mma_of(int warp) {  // the stream, or -1
         const int h = warp - kSoftmaxWarps;
         return h == 1 ? 0 : (h == 5 && kStreams == 2 ? 1 : -1);
@@ -283,6 +291,9 @@ __global__ void __launch_bounds__(TcAttn<KV, DP>::kThreads, 1) attn_tc_kernel(At
     PartItem* mine = a.items + part;  // written by thread 0
     if (tid == 0) mine->d[kTail].first = mine->d[kHead].first = -1;
 
+    // (The register counts change inside the branches: the compiler goes by that.)
+    if (warp >= C::kSoftmaxWarps) {
+        if constexpr (C::kDealRegisters) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kHelperRegisters));
     if (C::loader_of(warp) >= 0) {
         // ---------------------------------------------------------------- loaders
         constexpr int kChunks = DP / (F8 ? 16 : 8);  // 16-byte groups of a row in the cache
@@ -417,7 +428,7 @@ __global__ void __launch_bounds__(TcAttn<KV, DP>::kThreads, 1) attn_tc_kernel(At
             }
             const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + (uint32_t)(chunk >> 3) * (KT * 128);
             const uint32_t rb = smem_addr(raw) + (uint32_t)(raw_slot * C::kRawTile);
-#pragma unroll 8
+#pragma unroll (I8 ? 2 : 8)
             for (int i = 0; i < kKeys; i += kPer) {
                 const int p = __shfl_sync(0xffffffffu, pid, i + sub_row);
                 const bool real = inside && p >= 0;
@@ -520,8 +531,10 @@ __global__ void __launch_bounds__(TcAttn<KV, DP>::kThreads, 1) attn_tc_kernel(At
         commit_elect(&bars->drain[s]);  // everything issued has completed before tensor memory is freed
         mbar_wait_bounded(&bars->drain[s], 0, status, limit_ns);
         __syncwarp();
-    } else if (warp < C::kSoftmaxWarps) {
+    }
+    } else {
         // ---------------------------------------------------------------- softmax
+        if constexpr (C::kDealRegisters) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegisters));
         const int s = warp >> 2, row = tid & 127, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const uint32_t ts = tmem + lanes + C::kColS + s * KT;
