@@ -13,8 +13,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdspark.so")
 NATIVE = os.path.join(HERE, "_native.so")
 SOURCES = ["api.cu", "sample.cu", "sample_tc.cu", "verify.cu", "tv.cu", "schedule.cu", "logits.cu", "cache.cu", "cache_i8.cu",
-           "paged_attn.cu", "paged_attn_i8.cu", "paged_attn_i8_rows.cu",
-           "paged_attn_tc.cu"]
+           "paged_attn.cu", "paged_attn_i8.cu", "paged_attn_i8_rows.cu", "paged_attn_tc.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else "nvcc")
 FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "-I", INCLUDE, "-I", CSRC]

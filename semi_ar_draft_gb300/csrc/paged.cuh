@@ -75,7 +75,6 @@ struct PartItem {
 enum { kTail = 0, kHead = 1 };
 constexpr int kMaxParts = 480;    // blocks of the largest grid with row tiles of 16 (three a multiprocessor)
 constexpr int kMaxTcParts = 160;  // and of 128 (one)
-constexpr int kMaxI8Parts = 640;  // and over an int8 cache (four)
 
 // One request as the kernels see it: every number clamped to the buffers (bad: it was not).  Keys before lo,
 // the first that any row sees, have no pages any more as far as a call is concerned.
@@ -349,11 +348,11 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // aligned query rows.
 dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int kv, int sms, cudaStream_t s, int* parts);
 
-// Row tiles of 8 or 16 over int8 pools (paged_attn_i8.cu), for i8_head_group kv heads at a time.
+// Row tiles of 8 over int8 pools (paged_attn_i8.cu), for i8_head_group kv heads at a time.
 int i8_head_group(int D, int Hk);
-dspark_status launch_attn_i8(const AttnArgs& a, bool bf16, int row_tile, int sms, cudaStream_t s, int* parts);
+dspark_status launch_attn_i8(const AttnArgs& a, bool bf16, int sms, cudaStream_t s, int* parts);
 
-// Row tiles of 16, 32 or 64 over int8 pools (paged_attn_i8_rows.cu).
-dspark_status launch_attn_i8_rows(const AttnArgs& a, bool bf16, int row_tile, int sms, cudaStream_t s, int* parts);
+// Row tiles of 16 over int8 pools (paged_attn_i8_rows.cu).
+dspark_status launch_attn_i8_rows(const AttnArgs& a, bool bf16, int sms, cudaStream_t s, int* parts);
 
 }  // namespace dspark

@@ -526,7 +526,7 @@ constexpr int kJoinFew = 8;  // up to so many parts, a warp joins a row by itsel
 // the second one and so on, and it.rows are real of each.
 template <bool BF16>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, int row_tile, int heads, int parts) {
-    __shared__ float s_f[kMaxI8Parts];
+    __shared__ float s_f[kMaxParts];
     __shared__ float4 s_acc[kJoinWarps][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     wait_primary();
@@ -687,29 +687,26 @@ struct AttnWs {
 //   16-bit   mean 11 rows 117 / 115 (long contexts) and 63 / 84 (short); mean 14: 130 / 109 and 71 / 83;
 //            mean 24: 88 / 67; heads of 256, mean 11: 214 / 255, mean 24: 159 / 139
 //   e4m3     mean 35 rows 69 / 85 and 36 / 42; 68 rows: 80 / 58; mean 70: 159 / 101; 119 rows: 254 / 92
+//   int8     mean 23 rows 66 / 101, 33 rows 584 / 621 and 87 / 83, heads of 256, 36 rows 111 / 124; 54 rows 75 / 65, 64 rows
+//            107 / 60 and 153 / 91
 // (an 8-bit tile has to be widened for the wide kernel, so it needs more rows to pay).
-int g_wide = -1;
 bool wide_rows(const dspark_attention_params* p) {
-    if (p->kv_dtype == DSPARK_I8 && g_wide >= 0) return g_wide != 0;
-    const long long G = p->Hq / p->Hk, limit = p->kv_dtype == p->dtype ? kRows : 48;
+    const long long G = p->Hq / p->Hk, limit = p->kv_dtype == p->dtype ? kRows : (p->kv_dtype == DSPARK_I8 ? 36 : 48);
     return G * p->T > limit * p->B && (p->max_new <= 0 || G * p->max_new > limit);
 }
-int g_tile = 0;
-// Rows of a tile over an int8 cache: 8 (launch_attn_i8), 16, 32 or 64 (launch_attn_i8_rows).
-int i8_row_tile(const dspark_attention_params* p) {
-    if (g_tile) return g_tile;
-    const long long G = p->Hq / p->Hk, mean = (G * p->T + p->B - 1) / p->B, rows = p->max_new > 0 ? min(mean, G * p->max_new) : mean;
-    return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 64));
+// Whether a call over an int8 cache takes row tiles of 8 (else of 16, where it is not wide): by the mean rows of a request
+// and kv head, or the most if they are fewer.  Measured, tiles of 8 against tiles of 16, us: 4 rows 65 / 74, 7 rows 43 / 50
+// and 48 / 62, 8 rows 60 / 69; 13 rows 98 / 82, 16 rows 99 / 73.
+bool few_rows_i8(const dspark_attention_params* p) {
+    const long long G = p->Hq / p->Hk;
+    return G * p->T <= 8ll * p->B || (p->max_new > 0 && G * p->max_new <= 8);
 }
 AttnWs attn_ws(const dspark_attention_params* p) {
     size_t rows = wide_rows(p) ? (size_t)2 * kMaxTcParts * kTcRows : (size_t)2 * kMaxParts * kRows;
-    if (p->kv_dtype == DSPARK_I8 && !wide_rows(p)) {
-        const int tile = i8_row_tile(p);
-        rows = tile == 8 ? (size_t)2 * kMaxParts * 8 * i8_head_group(p->D, p->Hk) : (size_t)2 * kMaxI8Parts * tile;
-    }
+    if (p->kv_dtype == DSPARK_I8 && !wide_rows(p) && few_rows_i8(p)) rows = rows / kRows * 8 * i8_head_group(p->D, p->Hk);
     AttnWs w;
     w.items = kHeaderBytes;
-    w.ml = align_up(w.items + sizeof(PartItem) * kMaxI8Parts, 256);
+    w.ml = align_up(w.items + sizeof(PartItem) * kMaxParts, 256);
     w.o = align_up(w.ml + sizeof(float2) * rows, 256);
     w.bytes = align_up(w.o + sizeof(float) * rows * (size_t)p->D, 256);
     return w;
@@ -805,17 +802,17 @@ dspark_status paged_attention(const dspark_attention_params* p, const dspark_blo
     const bool tc = wide_rows(p) && a.q_vec;
     // the type of the probabilities: q's, or halves (an e4m3 cache; int8, row tiles of 16)
     a.sum_scale = bf16 && (kv == kKv16 || (kv == kKvI8 && tc)) ? ProbScale<true>::kInverse : ProbScale<false>::kInverse;
+    const bool few = kv == kKvI8 && !tc && few_rows_i8(p);
     const dspark_status ls = tc             ? launch_attn_tc(a, bf16, kv, sms, s, &parts)
-                             : kv == kKvI8 ? (i8_row_tile(p) == 8 ? launch_attn_i8(a, bf16, 8, sms, s, &parts)
-                                                                   : launch_attn_i8_rows(a, bf16, i8_row_tile(p), sms, s, &parts))
+                             : few         ? launch_attn_i8(a, bf16, sms, s, &parts)
+                             : kv == kKvI8 ? launch_attn_i8_rows(a, bf16, sms, s, &parts)
                              : bf16        ? (e4m3 ? launch_rows16_d<true, true>(a, sms, s, &parts)
                                                    : launch_rows16_d<true, false>(a, sms, s, &parts))
                                            : (e4m3 ? launch_rows16_d<false, true>(a, sms, s, &parts)
                                                    : launch_rows16_d<false, false>(a, sms, s, &parts));
     if (ls != DSPARK_OK) return ls;
     note_launch();
-    const int row_tile = tc ? kTcRows : (kv == kKvI8 ? i8_row_tile(p) : kRows);
-    const int heads = kv == kKvI8 && row_tile == 8 ? i8_head_group(p->D, p->Hk) : 1;
+    const int row_tile = tc ? kTcRows : (few ? 8 : kRows), heads = few ? i8_head_group(p->D, p->Hk) : 1;
     // The join's blocks become resident as the attention kernel's leave.
     const dim3 grid(parts, 8), block(32 * kJoinWarps);
     const cudaError_t e = bf16 ? launch_overlapped(attn_join_kernel<true>, grid, block, 0, s, a, row_tile, heads, parts)
@@ -852,5 +849,3 @@ extern "C" dspark_status dspark_paged_attention_i8(const dspark_attention_params
     return paged_attention(p, x, q, k_pages, v_pages, block_table, seq_len, offsets, nullptr, nullptr, out, lse, workspace, ws_bytes,
                            stream);
 }
-
-extern "C" void dspark_debug_wide(int w, int t) { g_wide = w; g_tile = t; }

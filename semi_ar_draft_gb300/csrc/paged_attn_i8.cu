@@ -1,5 +1,5 @@
-// paged_attn_i8.cu -- dspark_paged_attention_i8 for few rows a kv head: row tiles of 8 and 16 (paged.cuh has the split
-// of the work and the join, paged_attn_tc.cu the row tiles of 128).
+// paged_attn_i8.cu -- dspark_paged_attention_i8 for up to eight rows a kv head, a decoding step's (paged.cuh has the split
+// of the work and the join, paged_attn_i8_rows.cu more rows, paged_attn_tc.cu many).
 //
 // With k_l = c_l 2^(e_l) and v_l = d_l 2^(f_l), c and d the codes:
 //   s_l = scale (q . c_l) 2^(e_l), capped;  sum = sum_l 2^(s_l log2 e - m)
@@ -9,12 +9,15 @@
 // move the sum's reference.  Codes are halves exactly, and so is a query times a power of two; nothing else is rounded
 // before the products but the weights.
 //
-// What bounds it is issue slots, not the cache's bytes: a code costs 5/4 instructions on its way to a half, so the rest
-// has to be little.  Keys and values are therefore the products' A operand (16 keys, 16 values of a head), and the rows
-// are B, eight at a time: S^T = K Q^T and O^T = V^T P^T.  With the rows in A, as the other caches have them, a decoding
-// step of eight heads a kv head computes 16 rows of everything, scores, exponentials and output registers alike.
-// P^T is S^T's fragment transposed (movmatrix).  A warp streams slices of its own through a ring of its own in shared
-// memory, as in paged_attn.cu.
+// What bounds it is issue slots as much as the cache's bytes, so everything beside the products has to be little.  Keys and
+// values are therefore the products' A operand (16 keys, 16 values of a head), and the rows are B, eight at a time:
+// S^T = K Q^T and O^T = V^T P^T.  With the rows in A, as the other caches have them, a decoding step of eight heads a kv
+// head computes 16 rows of everything, scores, exponentials and output registers alike.  P^T is S^T's fragment transposed
+// (movmatrix).  A warp streams slices of its own through a ring of its own in shared memory, as in paged_attn.cu.
+//
+// Measured: 32 requests of up to 8192 tokens, 8 kv heads of 128, 58 us = 4.9 TB/s (0.73 of the measured copy rate; the rows
+// in A 73 us); 128 requests of up to 8000 tokens 190 us = 5.9 TB/s (0.88; 237 us); heads of 64, 128 requests, 122 us (183
+// before the block's warps took a head each).
 #include "host_util.h"
 #include "mma16.cuh"
 #include "paged.cuh"
@@ -24,9 +27,8 @@
 namespace dspark {
 namespace {
 
-template <int DP, int NT, int HG>
+template <int DP, int HG>
 struct SliceI8 {
-    static constexpr int kRowTile = 8 * NT;            // rows of a kv head
     static constexpr int kKeys = DP == 256 ? 16 : 32;  // keys of a warp's slice
     static constexpr int kMt = kKeys / 16;
     static constexpr int kWarps = 4, kThreads = 32 * kWarps;
@@ -35,16 +37,13 @@ struct SliceI8 {
     static constexpr int kChunks = DP / 16;          // 16-byte groups of a row
     static constexpr int kHalf = kKeys * DP;         // K (or V) of a slice
     static constexpr int kStage = 2 * kHalf;
-    static constexpr int kStages = DP == 64 ? 4 : (NT == 2 ? 3 : 2);
+    static constexpr int kStages = DP == 64 ? 4 : 2;
     static constexpr int kExtra = 2;  // what an item costs beside its key tiles
-    static constexpr int kBlocksPerSm = NT == 2 && DP >= 128 ? 2 : 3;
-    static constexpr bool kQInSmem = NT * DP > 128;  // (else in registers)
-    static constexpr int kQBytes = kRowTile * DP * 2;  // of a head
+    static constexpr int kBlocksPerSm = 3;
+    static constexpr bool kQInSmem = DP > 128;    // (else in registers)
+    static constexpr int kQBytes = 8 * DP * 2;    // of a head
     static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage + HG * kQBytes;
-    // A warp's output in fp32 goes through the stage just consumed, in as many rounds as it takes.
-    static constexpr int kRounds = kRowTile * DP * 4 > kStage ? kRowTile * DP * 4 / kStage : 1;
-    static constexpr int kRoundRows = kRowTile / kRounds;
-    static_assert(kRoundRows % 8 == 0, "a round is whole n-tiles");
+    static_assert(kStage >= 8 * DP * 4, "a stage holds a warp's output");
     // Rows are a multiple of 128 bytes apart (or 64): the swizzle spreads eight rows' same 16-byte group over all banks.
     static __device__ __forceinline__ uint32_t at(int row, int chunk) {
         const int x = kChunks >= 8 ? (row & 7) : ((row >> 1) & 3);
@@ -66,19 +65,18 @@ __device__ __forceinline__ void store_out4(const AttnArgs& a, long long row, int
 }
 
 // a.Hk counts groups of HG heads here.
-template <bool BF16, int DP, int NT, int HG>
-__global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT, HG>::kBlocksPerSm) attn_i8_kernel(AttnArgs a) {
-    using C = SliceI8<DP, NT, HG>;
-    constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kRows = C::kRowTile, MT = C::kMt;
+template <bool BF16, int DP, int HG>
+__global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kBlocksPerSm) attn_i8_kernel(AttnArgs a) {
+    using C = SliceI8<DP, HG>;
+    constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kRows = 8, MT = C::kMt;
     constexpr int KS = DP / 16;  // k-steps over the head dimension, and m-tiles of the output
-    constexpr int R = 2 * NT;    // rows of a lane: 8 j + 2 t + (0, 1)
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float2 s_ml[kWarps][kRows];
     __shared__ int s_err;
     __shared__ AttnScratch s_start;
     __shared__ uint32_t s_qmax[HG * kRows];        // largest |q| of each row (its bits); rows of the first head, the second, ...
     __shared__ float s_qsum[HG * kRows][DP / 8];  // sums of a row's query, eight values each
-    __shared__ float s_base[HG * kRows], s_scale[HG * kRows];  // where a row's products begin, its scores' factor
+    __shared__ __align__(8) float s_base[HG * kRows], s_scale[HG * kRows];  // where a row's products begin, its scores' factor
     __shared__ AttnStart s_range;                    // the block's units
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -170,26 +168,20 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
     AttnWalk w = walk_begin(a, start, kRows, C::kKeyTile, C::kExtra);
     PartItem* mine = a.items + part;  // written by thread 0
     if (tid == 0) mine->d[kTail].first = mine->d[kHead].first = -1;
-    float o[KS][NT][4];  // [16 values of a head][8 rows]: values 2 g (rows 2 t, 2 t + 1), 2 g + 1
-    uint32_t qf[C::kQInSmem ? 1 : KS][NT][2];
+    float o[KS][4];  // of 16 values of the head: values 2 g (rows 2 t, 2 t + 1), 2 g + 1
+    uint32_t qf[C::kQInSmem ? 1 : KS][2];
     const float cap_out = a.softcap * kLog2e;
     constexpr float kUp = ProbScale<false>::kBits;
     // What is taken off the exponents of sums and weights: kUp less than the largest that a row followed (kNone: it has seen
     // nothing), and the sums.
     constexpr float kNone = -3e38f;
-    float ref[R], ref_v[R];
-    uint64_t sums[NT];  // of rows 8 j + 2 t and the next
+    float ref[2], ref_v[2];
+    uint64_t sums;
     int all_lo = 0, all_hi = 0, rows = 0, group = 0, row0 = 0, seg_first = 0;
     bool fresh = true;
     int st = 0;
-    auto row_of = [&](int r) { return 8 * (r >> 1) + 2 * t + (r & 1); };
-    // The queries' fragments of k-steps ks and ks + 1 (NT = 1), or of ks (NT = 2), by one ldmatrix.
-    auto load_q = [&](uint32_t (&b)[4], int ks) {
-        if (NT == 1)
-            ldsm4(b, qs_addr + C::q_at(lane & 7, 2 * ks + (lane >> 3)));
-        else
-            ldsm4(b, qs_addr + C::q_at((lane & 7) + (lane >> 4) * 8, 2 * ks + ((lane >> 3) & 1)));
-    };
+    // The queries' fragments of k-steps ks and ks + 1.
+    auto load_q = [&](uint32_t (&b)[4], int ks) { ldsm4(b, qs_addr + C::q_at(lane & 7, 2 * ks + (lane >> 3))); };
     while (!w.done()) {
         if (fresh) {  // a new segment: its rows, their queries and what each may see
             fresh = false;
@@ -265,11 +257,8 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
                 s_qsum[qrow][c] = sum;
             }
             __syncthreads();
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                ref[r] = ref_v[r] = kNone;
-                if (!(r & 1)) sums[r >> 1] = 0;
-            }
+            ref[0] = ref[1] = ref_v[0] = ref_v[1] = kNone;
+            sums = 0;
             if (tid < kQRows) {
                 float sum = 0.f;
 #pragma unroll 4
@@ -281,29 +270,17 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
             __syncthreads();
             if (!C::kQInSmem) {
 #pragma unroll
-                for (int ks = 0; ks < KS; ks += NT == 1 ? 2 : 1) {
+                for (int ks = 0; ks < KS; ks += 2) {
                     uint32_t b[4];
                     load_q(b, ks);
-                    if (NT == 1) {
-                        qf[C::kQInSmem ? 0 : ks][0][0] = b[0];
-                        qf[C::kQInSmem ? 0 : ks][0][1] = b[1];
-                        qf[C::kQInSmem ? 0 : ks + 1][0][0] = b[2];
-                        qf[C::kQInSmem ? 0 : ks + 1][0][1] = b[3];
-                    } else {
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            qf[C::kQInSmem ? 0 : ks][j][0] = b[2 * j];
-                            qf[C::kQInSmem ? 0 : ks][j][1] = b[2 * j + 1];
-                        }
-                    }
+                    for (int e = 0; e < 4; ++e) qf[C::kQInSmem ? 0 : ks + (e >> 1)][e & 1] = b[e];
                 }
             }
 #pragma unroll
             for (int i = 0; i < KS; ++i)
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) o[i][j][c] = 0.f;
+                for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
         }
 #pragma unroll
         for (int i = 0; i + 1 < C::kStages; ++i) {
@@ -316,16 +293,14 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
         const int key0 = slice_key(w);
         if (key0 < w.r.seq) {
             const uint32_t kb = ring_addr + st * C::kStage, vb = kb + C::kHalf;
-            // ---- S^T: lane (g, t) gets keys 16 i + g (c < 2), + 8, of rows 8 j + 2 t + (c & 1)
-            float s[MT][NT][4], row_base[R], row_scale[R];
+            // ---- S^T: lane (g, t) gets keys 16 i + g (h = 0) and + 8, of rows 2 t and 2 t + 1
+            float s[MT][4];
+            const float2 base = *reinterpret_cast<const float2*>(&s_base[my_head * kRows + 2 * t]);
 #pragma unroll
-            for (int r = 0; r < R; ++r) row_base[r] = s_base[my_head * kRows + row_of(r)];
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) s[i][j][c] = row_base[2 * j + (c & 1)];
+            for (int i = 0; i < MT; ++i) {
+                s[i][0] = s[i][2] = base.x;
+                s[i][1] = s[i][3] = base.y;
+            }
             // Four k of keys g and g + 8.  A byte alone in a half is the subnormal number byte 2^-24, so a key's code needs
             // no arithmetic: code + 128 goes in, and the products begin at - 128 times the sum of the row's query instead
             // of zero.  (What fp32 loses by that is 2^-24 of 128 sum |q|, the error of 2^-16 of a code.)
@@ -337,31 +312,12 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
             };
 #pragma unroll
             for (int ks = 0; ks < KS; ks += 2) {
-                uint32_t q[2][NT][2];
+                uint32_t q[4];
+                if (C::kQInSmem) {
+                    load_q(q, ks);
+                } else {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    if (!C::kQInSmem) {
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) q[u][j][e] = qf[C::kQInSmem ? 0 : ks + u][j][e];
-                    } else if (NT > 1) {
-                        uint32_t b[4];
-                        load_q(b, ks + u);
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            q[u][j][0] = b[2 * j];
-                            q[u][j][1] = b[2 * j + 1];
-                        }
-                    }
-                }
-                if (C::kQInSmem && NT == 1) {
-                    uint32_t b[4];
-                    load_q(b, ks);
-                    q[0][0][0] = b[0];
-                    q[0][0][1] = b[1];
-                    q[1][0][0] = b[2];
-                    q[1][0][1] = b[3];
+                    for (int e = 0; e < 4; ++e) q[e] = qf[C::kQInSmem ? 0 : ks + (e >> 1)][e & 1];
                 }
                 uint32_t b[2][4];
                 if (MT == 2) {  // matrix i: keys 8 i .. 8 i + 7
@@ -379,8 +335,7 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
                             codes_a(f, b[u][2 * i], b[u][2 * i + 1]);
                         else
                             codes_a(f, b[0][2 * u], b[0][2 * u + 1]);
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) mma16<false>(s[i][j], f, q[u][j][0], q[u][j][1]);
+                        mma16<false>(s[i], f, q[2 * u], q[2 * u + 1]);
                     }
             }
             // each key's 2^e (as bf16, in the low half) and its values' e (as bf16), from the lane of the key's number
@@ -396,98 +351,79 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
                     value_exp[i][h] = __uint_as_float(x & 0xffff0000u);
                 }
             // scores in the log2 domain, hidden ones -inf
-#pragma unroll
-            for (int r = 0; r < R; ++r) row_scale[r] = s_scale[my_head * kRows + row_of(r)];
+            const float2 row_scale = *reinterpret_cast<const float2*>(&s_scale[my_head * kRows + 2 * t]);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float2 x = up2(mul2(mul2(pk2(s[i][j][2 * h], s[i][j][2 * h + 1]), pk2(row_scale[2 * j], row_scale[2 * j + 1])),
-                                                  pk2(key_scale[i][h], key_scale[i][h])));
-                        s[i][j][2 * h] = x.x;
-                        s[i][j][2 * h + 1] = x.y;
-                    }
-            if (a.softcap > 0.f) {
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float2 x = softcap2(s[i][j][2 * h], s[i][j][2 * h + 1], 1.f, cap_out);
-                            s[i][j][2 * h] = x.x;
-                            s[i][j][2 * h + 1] = x.y;
-                        }
-            }
+                for (int h = 0; h < 2; ++h) {
+                    float2 x = up2(mul2(mul2(pk2(s[i][2 * h], s[i][2 * h + 1]), pk2(row_scale.x, row_scale.y)),
+                                        pk2(key_scale[i][h], key_scale[i][h])));
+                    if (a.softcap > 0.f) x = softcap2(x.x, x.y, 1.f, cap_out);
+                    s[i][2 * h] = x.x;
+                    s[i][2 * h + 1] = x.y;
+                }
             if (key0 < all_lo || key0 + C::kKeys > all_hi) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int row = row_of(r), token = attn_token(a, row0 + row);
-                    const int lo = attn_see_lo(a, w.r, token), hi = row < rows ? attn_see_hi(a, w.r, token) : 0;
+                for (int r = 0; r < 2; ++r) {
+                    const int token = attn_token(a, row0 + 2 * t + r);
+                    const int lo = attn_see_lo(a, w.r, token), hi = 2 * t + r < rows ? attn_see_hi(a, w.r, token) : 0;
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int key = key0 + 16 * i + 8 * h + g;
-                            if (key < lo || key >= hi) s[i][r >> 1][2 * h + (r & 1)] = -CUDART_INF_F;
+                            if (key < lo || key >= hi) s[i][2 * h + r] = -CUDART_INF_F;
                         }
                 }
             }
             // The references follow a row's maxima only when these are 2^8 ahead (values up to 2^8 lose nothing), so most
             // slices need no maximum over the lanes and do not touch the output.
-            float mx[R], mz[R];
+            float mx[2], mz[2];
             bool grow = false;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
+            for (int r = 0; r < 2; ++r) {
                 mx[r] = mz[r] = -CUDART_INF_F;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
-                    const float x = s[i][r >> 1][r & 1], y = s[i][r >> 1][2 + (r & 1)];
-                    mx[r] = fmax3(mx[r], x, y);
-                    mz[r] = fmax3(mz[r], x + value_exp[i][0], y + value_exp[i][1]);
+                    mx[r] = fmax3(mx[r], s[i][r], s[i][2 + r]);
+                    mz[r] = fmax3(mz[r], s[i][r] + value_exp[i][0], s[i][2 + r] + value_exp[i][1]);
                 }
                 grow |= mx[r] > ref[r] + (kUp + 8.f) || mz[r] > ref_v[r] + (kUp + 8.f);
             }
             if (__any_sync(0xffffffffu, grow)) {
+                float less[2];
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
+                for (int r = 0; r < 2; ++r) {
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) {
                         mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], d));
                         mz[r] = fmaxf(mz[r], __shfl_xor_sync(0xffffffffu, mz[r], d));
                     }
                     const float mn = fmaxf(ref[r], mx[r] - kUp), zn = fmaxf(ref_v[r], mz[r] - kUp);
-                    if (mn != ref[r]) {
-                        const float fl = ex2(ref[r] - mn);
-                        const float2 l = up2(sums[r >> 1]);
-                        sums[r >> 1] = r & 1 ? pk2(l.x, l.y * fl) : pk2(l.x * fl, l.y);
-                    }
+                    less[r] = mn == ref[r] ? 1.f : ex2(ref[r] - mn);
                     const float f = zn == ref_v[r] ? 1.f : ex2(ref_v[r] - zn);
                     ref[r] = mn;
                     ref_v[r] = zn;
 #pragma unroll
                     for (int i = 0; i < KS; ++i) {
-                        o[i][r >> 1][r & 1] *= f;
-                        o[i][r >> 1][2 + (r & 1)] *= f;
+                        o[i][r] *= f;
+                        o[i][2 + r] *= f;
                     }
                 }
+                sums = mul2(sums, pk2(less[0], less[1]));
             }
             // ---- P^T as halves, fragments of the second product's B
-            uint32_t p[MT][NT][2];
+            uint32_t p[MT][2];
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint64_t x = pk2(s[i][j][2 * h], s[i][j][2 * h + 1]);
-                        const float2 e = up2(add2(x, pk2(-ref[2 * j], -ref[2 * j + 1])));
-                        const float2 z = up2(add2(add2(x, pk2(value_exp[i][h], value_exp[i][h])), pk2(-ref_v[2 * j], -ref_v[2 * j + 1])));
-                        sums[j] = add2(sums[j], pk2(ex2(e.x), ex2(e.y)));
-                        p[i][j][h] = transpose8x8(pack16<false>(ex2(z.x), ex2(z.y)));
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    const uint64_t x = pk2(s[i][2 * h], s[i][2 * h + 1]);
+                    const float2 e = up2(add2(x, pk2(-ref[0], -ref[1])));
+                    const float2 z = up2(add2(add2(x, pk2(value_exp[i][h], value_exp[i][h])), pk2(-ref_v[0], -ref_v[1])));
+                    sums = add2(sums, pk2(ex2(e.x), ex2(e.y)));
+                    p[i][h] = transpose8x8(pack16<false>(ex2(z.x), ex2(z.y)));
+                }
             // ---- O^T += V^T P^T: bytes (k0 d0, k0 d1, k1 d0, k1 d1) are rows 2 g and 2 g + 1 of the m-tile, which are
             // its rows g and g + 8 to the MMA.  (What nobody sees needs no care: codes are finite.)
 #pragma unroll
@@ -501,8 +437,7 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
                         const uint32_t x = b[2 * u] ^ 0x80808080u, y = b[2 * u + 1] ^ 0x80808080u;
                         const uint32_t f[4] = {i8x2_to_half2<kBytes02>(x), i8x2_to_half2<kBytes13>(x), i8x2_to_half2<kBytes02>(y),
                                                i8x2_to_half2<kBytes13>(y)};
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) mma16<false>(o[c + u][j], f, p[i][j][0], p[i][j][1]);
+                        mma16<false>(o[c + u], f, p[i][0], p[i][1]);
                     }
                 }
         }
@@ -510,73 +445,59 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
 
         const bool last_of_item = w.kt + 1 == w.kts;
         if (last_of_item || w.left == 1) {
-            // ---- the warps' parts of the segment meet
+            // ---- the warps' parts of the segment meet, in the stages just consumed
+            float* mine_o = reinterpret_cast<float*>(ring + st * C::kStage);
+            auto o_at = [](int row, int col) { return row * DP + (col ^ (((row >> 1) & 3) << 4)); };
+            const float2 both = up2(sums);
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float2 both = up2(sums[r >> 1]);
-                float l = r & 1 ? both.y : both.x;
+            for (int r = 0; r < 2; ++r) {
+                float l = r ? both.y : both.x;
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-                if (g == 0) s_ml[warp][row_of(r)] = make_float2(ref[r] == kNone ? -CUDART_INF_F : ref[r] + kUp, l);
+                if (g == 0) s_ml[warp][2 * t + r] = make_float2(ref[r] == kNone ? -CUDART_INF_F : ref[r] + kUp, l);
                 // to the reference of the sums, in two steps: 2^f may be as large as fp32's numbers
                 const float f = ex2(0.5f * (ref_v[r] - ref[r]));
 #pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    o[i][r >> 1][r & 1] = o[i][r >> 1][r & 1] * f * f;
-                    o[i][r >> 1][2 + (r & 1)] = o[i][r >> 1][2 + (r & 1)] * f * f;
-                }
+                for (int i = 0; i < KS; ++i)
+                    *reinterpret_cast<float2*>(mine_o + o_at(2 * t + r, 16 * i + 2 * g)) = make_float2(o[i][r] * f * f, o[i][2 + r] * f * f);
             }
+            __syncthreads();
             const bool whole = last_of_item && seg_first == 0;
             const int slot = 2 * part + (seg_first == 0 ? kHead : kTail);
-            float* mine_o = reinterpret_cast<float*>(ring + st * C::kStage);
-            auto o_at = [](int row, int col) { return (row % C::kRoundRows) * DP + (col ^ (((row >> 1) & 3) << 4)); };
+            for (int i = tid; i < HG * kRows * (DP / 4); i += kThreads) {
+                const int hd = i / (kRows * (DP / 4)), head = group * HG + hd;
+                const int row = i / (DP / 4) % kRows, col = 4 * (i % (DP / 4));
+                if (row >= rows) continue;
+                float mm = -CUDART_INF_F, ll = 0.f;
 #pragma unroll
-            for (int round = 0; round < C::kRounds; ++round) {
-                if (round) __syncthreads();
+                for (int x = hd; x < kWarps; x += HG) mm = fmaxf(mm, s_ml[x][row].x);
+                const float ref = mm == -CUDART_INF_F ? 0.f : mm;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    if ((r >> 1) * 8 / C::kRoundRows != round) continue;
-#pragma unroll
-                    for (int i = 0; i < KS; ++i)
-                        *reinterpret_cast<float2*>(mine_o + o_at(row_of(r), 16 * i + 2 * g)) =
-                            make_float2(o[i][r >> 1][r & 1], o[i][r >> 1][2 + (r & 1)]);
+                for (int x = hd; x < kWarps; x += HG) {
+                    const float2 ml = s_ml[x][row];
+                    const float f = ex2(ml.x - ref);
+                    if (ml.y == 0.f) continue;  // saw nothing
+                    ll = fmaf(ml.y, f, ll);
+                    const float4 y = *reinterpret_cast<const float4*>(
+                        smem + (size_t)(x * C::kStages + st) * C::kStage + 4 * o_at(row, col));
+                    v.x = fmaf(y.x, f, v.x);
+                    v.y = fmaf(y.y, f, v.y);
+                    v.z = fmaf(y.z, f, v.z);
+                    v.w = fmaf(y.w, f, v.w);
                 }
-                __syncthreads();
-                for (int i = tid; i < HG * C::kRoundRows * (DP / 4); i += kThreads) {
-                    const int hd = i / (C::kRoundRows * (DP / 4)), head = group * HG + hd;
-                    const int row = round * C::kRoundRows + i / (DP / 4) % C::kRoundRows, col = 4 * (i % (DP / 4));
-                    if (row >= rows) continue;
-                    float mm = -CUDART_INF_F, ll = 0.f;
-#pragma unroll
-                    for (int x = hd; x < kWarps; x += HG) mm = fmaxf(mm, s_ml[x][row].x);
-                    const float ref = mm == -CUDART_INF_F ? 0.f : mm;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int x = hd; x < kWarps; x += HG) {
-                        const float2 ml = s_ml[x][row];
-                        const float f = ex2(ml.x - ref);
-                        if (ml.y == 0.f) continue;  // saw nothing
-                        ll = fmaf(ml.y, f, ll);
-                        const float4 y = *reinterpret_cast<const float4*>(
-                            smem + (size_t)(x * C::kStages + st) * C::kStage + 4 * o_at(row, col));
-                        v.x = fmaf(y.x, f, v.x);
-                        v.y = fmaf(y.y, f, v.y);
-                        v.z = fmaf(y.z, f, v.z);
-                        v.w = fmaf(y.w, f, v.w);
+                if (whole) {
+                    const long long at = attn_out_row(a, w.r.token0, head, row0 + row);
+                    if (col < a.D) {
+                        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                        store_out4<BF16>(a, at, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                     }
-                    if (whole) {
-                        const long long at = attn_out_row(a, w.r.token0, head, row0 + row);
-                        if (col < a.D) {
-                            const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                            store_out4<BF16>(a, at, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-                        }
-                        if (a.lse && col == 0)
-                            a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll * ProbScale<false>::kInverse)) * kLn2;
-                    } else {
-                        const size_t at = (size_t)slot * (HG * kRows) + hd * kRows + row;
-                        if (col < a.D) *reinterpret_cast<float4*>(a.part_o + at * a.D + col) = v;
-                        if (col == 0) a.part_ml[at] = make_float2(mm, ll);
-                    }
+                    if (a.lse && col == 0)
+                        a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll * ProbScale<false>::kInverse)) * kLn2;
+                } else {
+                    const size_t at = (size_t)slot * (HG * kRows) + hd * kRows + row;
+                    if (col < a.D) *reinterpret_cast<float4*>(a.part_o + at * a.D + col) = v;
+                    if (col == 0) a.part_ml[at] = make_float2(mm, ll);
                 }
             }
             if (!whole && tid == 0) mine->d[seg_first == 0 ? kHead : kTail] = part_desc(s_range, w, row0, rows, group);
@@ -592,11 +513,11 @@ __global__ void __launch_bounds__(SliceI8<DP, NT, HG>::kThreads, SliceI8<DP, NT,
     if (tid == 0) mine->err = s_err;
 }
 
-template <bool BF16, int DP, int NT, int HG>
+template <bool BF16, int DP, int HG>
 dspark_status launch_slices(AttnArgs a, int sms, cudaStream_t s, int* parts) {
-    using C = SliceI8<DP, NT, HG>;
+    using C = SliceI8<DP, HG>;
     int per_sm = 0;
-    auto fn = attn_i8_kernel<BF16, DP, NT, HG>;
+    auto fn = attn_i8_kernel<BF16, DP, HG>;
     if (prepare_kernel((const void*)fn, C::kSmem, C::kThreads, &per_sm) != cudaSuccess || per_sm < 1) return DSPARK_ERR_CUDA;
     int n = sms * (per_sm < C::kBlocksPerSm ? per_sm : C::kBlocksPerSm);
     if (n > kMaxParts) n = kMaxParts;
@@ -604,15 +525,15 @@ dspark_status launch_slices(AttnArgs a, int sms, cudaStream_t s, int* parts) {
     a.Hk /= HG;
     return launch_overlapped(fn, n, C::kThreads, C::kSmem, s, a) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
-template <bool BF16, int NT>
+template <bool BF16>
 dspark_status launch_slices_d(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
     const int heads = i8_head_group(a.D, a.Hk);
     if (a.D <= 64) {
-        if (heads == 4) return launch_slices<BF16, 64, NT, 4>(a, sms, s, parts);
-        return heads == 2 ? launch_slices<BF16, 64, NT, 2>(a, sms, s, parts) : launch_slices<BF16, 64, NT, 1>(a, sms, s, parts);
+        if (heads == 4) return launch_slices<BF16, 64, 4>(a, sms, s, parts);
+        return heads == 2 ? launch_slices<BF16, 64, 2>(a, sms, s, parts) : launch_slices<BF16, 64, 1>(a, sms, s, parts);
     }
-    if (a.D <= 128) return heads == 2 ? launch_slices<BF16, 128, NT, 2>(a, sms, s, parts) : launch_slices<BF16, 128, NT, 1>(a, sms, s, parts);
-    return launch_slices<BF16, 256, NT, 1>(a, sms, s, parts);
+    if (a.D <= 128) return heads == 2 ? launch_slices<BF16, 128, 2>(a, sms, s, parts) : launch_slices<BF16, 128, 1>(a, sms, s, parts);
+    return launch_slices<BF16, 256, 1>(a, sms, s, parts);
 }
 
 }  // namespace
@@ -625,9 +546,8 @@ int i8_head_group(int D, int Hk) {
     return D <= 128 && Hk % 2 == 0 ? 2 : 1;
 }
 
-dspark_status launch_attn_i8(const AttnArgs& a, bool bf16, int row_tile, int sms, cudaStream_t s, int* parts) {
-    if (bf16) return row_tile == 8 ? launch_slices_d<true, 1>(a, sms, s, parts) : launch_slices_d<true, 2>(a, sms, s, parts);
-    return row_tile == 8 ? launch_slices_d<false, 1>(a, sms, s, parts) : launch_slices_d<false, 2>(a, sms, s, parts);
+dspark_status launch_attn_i8(const AttnArgs& a, bool bf16, int sms, cudaStream_t s, int* parts) {
+    return bf16 ? launch_slices_d<true>(a, sms, s, parts) : launch_slices_d<false>(a, sms, s, parts);
 }
 
 }  // namespace dspark

@@ -1,11 +1,16 @@
-// paged_attn_i8_rows.cu -- dspark_paged_attention_i8 for more than eight rows a kv head (several new tokens a request, or
-// many query heads a kv head): row tiles of 16, 32 and 64.  paged_attn_i8.cu has the arithmetic, paged.cuh the split
-// of the work and the join.
+// paged_attn_i8_rows.cu -- dspark_paged_attention_i8 for 9 to some 36 rows a kv head (several new tokens a request, or many
+// query heads a kv head): row tiles of 16.  paged_attn_i8.cu has the arithmetic, paged.cuh the split of the work and the
+// join.
 //
-// A block's four warps share a tile of 64 keys, and every code is widened once for all the rows: for S^T = K Q^T a
-// warp takes 16 of the keys and for O^T = V^T P^T a quarter of the head's values.  P^T goes from one to the other through
-// shared memory.  A row's references are the block's: whether one has to follow is asked of all warps at the
+// A block's four warps share a tile of 128 keys (64 with heads past 128), and every code is widened once: for S^T = K Q^T a
+// warp takes a quarter of the keys, for O^T = V^T P^T a quarter of the head's values.  P^T goes from one to the other
+// through shared memory.  A row's references are the block's: whether one has to follow is asked of all warps at a
 // barrier that a tile needs anyway.  Outputs need no meeting of the warps, each has all keys of its values; only sums do.
+//
+// Bound by issue slots (about half of them are used by twelve warps a multiprocessor).  Measured, against the 8-row
+// kernel's layout with two row tiles a warp: 32 requests of up to 8192 tokens, 16 rows, 8 kv heads of 128: 73 us (82);
+// 64 requests, 23 rows, 4 kv heads: 66 us (79).  Row tiles of 32 and 64 need more registers or shared memory than three
+// blocks a multiprocessor leave: 105 and 207 us, 79 and 132 us.
 #include "host_util.h"
 #include "mma16.cuh"
 #include "paged.cuh"
@@ -15,22 +20,24 @@
 namespace dspark {
 namespace {
 
-template <int DP, int NT>
+constexpr int kRows = 16;
+constexpr int NT = kRows / 8;  // n-tiles of rows
+
+template <int DP>
 struct RowsI8 {
-    static constexpr int kRowTile = 8 * NT;
     static constexpr int kWarps = 4, kThreads = 32 * kWarps;
-    static constexpr int kMt = DP == 256 || NT == 8 ? 1 : 2;
+    static constexpr int kMt = DP == 256 ? 1 : 2;    // m-tiles of a warp's keys
     static constexpr int kKeys = 16 * kMt;           // keys of a tile that a warp takes
     static constexpr int kKeyTile = kKeys * kWarps;  // keys of a unit
     static constexpr int kChunks = DP / 16;       // 16-byte groups of a row
     static constexpr int kHalf = kKeyTile * DP;   // K (or V) of a tile
     static constexpr int kStage = 2 * kHalf;
-    static constexpr int kStages = DP == 64 || (DP == 128 && kMt == 1) ? 3 : 2;
+    static constexpr int kStages = DP == 64 ? 3 : 2;
     static constexpr int kExtra = 1;     // what an item costs beside its key tiles
     static constexpr int kDm = DP / 64;  // 16-value groups of a warp's quarter of a head
-    static constexpr int kBlocksPerSm = NT == 8 ? (DP == 256 ? 1 : 2) : (DP == 256 || (DP == 128 && NT == 4) ? 2 : 3);
-    static constexpr int kQBytes = kRowTile * DP * 2;
-    static constexpr int kPBytes = kRowTile * kKeyTile * 2;
+    static constexpr int kBlocksPerSm = DP == 256 ? 2 : 3;
+    static constexpr int kQBytes = kRows * DP * 2;
+    static constexpr int kPBytes = kRows * kKeyTile * 2;
     static constexpr size_t kSmem = (size_t)kStages * kStage + kQBytes + kPBytes;
     static __device__ __forceinline__ uint32_t at(int row, int chunk) {  // of codes
         const int x = kChunks >= 8 ? (row & 7) : ((row >> 1) & 3);
@@ -54,10 +61,10 @@ __device__ __forceinline__ void stsm4_trans(uint32_t addr, const uint32_t (&r)[4
                  : "memory");
 }
 
-template <bool BF16, int DP, int NT>
-__global__ void __launch_bounds__(RowsI8<DP, NT>::kThreads, RowsI8<DP, NT>::kBlocksPerSm) attn_i8_rows_kernel(AttnArgs a) {
-    using C = RowsI8<DP, NT>;
-    constexpr int kThreads = C::kThreads, kWarps = C::kWarps, kRows = C::kRowTile, MT = C::kMt, DM = C::kDm;
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm) attn_i8_rows_kernel(AttnArgs a) {
+    using C = RowsI8<DP>;
+    constexpr int kThreads = C::kThreads, kWarps = C::kWarps, MT = C::kMt, DM = C::kDm;
     constexpr int KS = DP / 16;  // k-steps over the head dimension
     constexpr int R = 2 * NT;    // rows of a lane: 8 j + 2 t + (0, 1)
     extern __shared__ __align__(128) unsigned char smem[];
@@ -511,34 +518,28 @@ __global__ void __launch_bounds__(RowsI8<DP, NT>::kThreads, RowsI8<DP, NT>::kBlo
     if (tid == 0) mine->err = s_err;
 }
 
-template <bool BF16, int DP, int NT>
+template <bool BF16, int DP>
 dspark_status launch_rows(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
-    using C = RowsI8<DP, NT>;
+    using C = RowsI8<DP>;
     int per_sm = 0;
-    auto fn = attn_i8_rows_kernel<BF16, DP, NT>;
+    auto fn = attn_i8_rows_kernel<BF16, DP>;
     if (prepare_kernel((const void*)fn, C::kSmem, C::kThreads, &per_sm) != cudaSuccess || per_sm < 1) return DSPARK_ERR_CUDA;
     int n = sms * (per_sm < C::kBlocksPerSm ? per_sm : C::kBlocksPerSm);
-    if (n > kMaxI8Parts) n = kMaxI8Parts;
+    if (n > kMaxParts) n = kMaxParts;
     *parts = n;
     return launch_overlapped(fn, n, C::kThreads, C::kSmem, s, a) == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
-template <bool BF16, int NT>
-dspark_status launch_rows_d(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
-    if (a.D <= 64) return launch_rows<BF16, 64, NT>(a, sms, s, parts);
-    if (a.D <= 128) return launch_rows<BF16, 128, NT>(a, sms, s, parts);
-    return launch_rows<BF16, 256, NT>(a, sms, s, parts);
-}
 template <bool BF16>
-dspark_status launch_rows_t(const AttnArgs& a, int row_tile, int sms, cudaStream_t s, int* parts) {
-    if (row_tile == 16) return launch_rows_d<BF16, 2>(a, sms, s, parts);
-    if (row_tile == 32) return launch_rows_d<BF16, 4>(a, sms, s, parts);
-    return launch_rows_d<BF16, 8>(a, sms, s, parts);
+dspark_status launch_rows_d(const AttnArgs& a, int sms, cudaStream_t s, int* parts) {
+    if (a.D <= 64) return launch_rows<BF16, 64>(a, sms, s, parts);
+    if (a.D <= 128) return launch_rows<BF16, 128>(a, sms, s, parts);
+    return launch_rows<BF16, 256>(a, sms, s, parts);
 }
 
 }  // namespace
 
-dspark_status launch_attn_i8_rows(const AttnArgs& a, bool bf16, int row_tile, int sms, cudaStream_t s, int* parts) {
-    return bf16 ? launch_rows_t<true>(a, row_tile, sms, s, parts) : launch_rows_t<false>(a, row_tile, sms, s, parts);
+dspark_status launch_attn_i8_rows(const AttnArgs& a, bool bf16, int sms, cudaStream_t s, int* parts) {
+    return bf16 ? launch_rows_d<true>(a, sms, s, parts) : launch_rows_d<false>(a, sms, s, parts);
 }
 
 }  // namespace dspark

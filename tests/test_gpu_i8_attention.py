@@ -49,9 +49,9 @@ def attend(c, **kw):
 
 
 def takes_wide(c, max_new):
-    """Whether the call goes to the kernel of many rows (or may: the bound is then the wider one)."""
+    """Whether the call goes to the kernel of many rows."""
     G, T, B = c["q"].shape[1] // c["codes"][0].shape[2], c["q"].shape[0], len(c["seq"])
-    return G * T > 16 * B and (max_new <= 0 or G * max_new > 16)
+    return G * T > 36 * B and (max_new <= 0 or G * max_new > 36)
 
 
 def check(c, lens, offsets, causal=True, window=0, softcap=0.0, scale=None, max_new=0):
@@ -91,7 +91,7 @@ def test_decoding_heads_and_pages(dtype, Hq, Hk, D, page, block):
 @pytest.mark.parametrize("causal,window,softcap,scale", [(True, 0, 0.0, None), (False, 0, 0.0, None), (True, 1, 0.0, None), (True, 20, 0.0, 0.3),
                                                          (False, 100, 0.0, None), (True, 0, 30.0, None), (True, 50, 2.0, None),
                                                          (True, 0, 0.0, -0.05), (True, 0, 1e4, None)])
-@pytest.mark.parametrize("G,D,max_new", [(4, 128, 4), (4, 64, 0), (16, 128, 0), (8, 256, 0)])
+@pytest.mark.parametrize("G,D,max_new", [(4, 128, 4), (4, 64, 0), (16, 128, 0), (8, 256, 0), (3, 128, 0), (12, 256, 3), (1, 64, 0)])
 def test_masks(dtype, causal, window, softcap, scale, G, D, max_new):
     """Several new tokens a request, at both kernels' row counts; requests without new tokens, padding."""
     lens, news = [300, 5, 64, 129, 17, 700, 40], [9, 5, 1, 16, 17, 0, 12]
