@@ -552,7 +552,9 @@ dspark_status dspark_cache_read_i8(const dspark_append_params* p, const dspark_b
  * dspark_paged_attention over int8 pools: the same scores, masks, outputs, statuses and workspace, with k_l and v_l the
  * values code 2^e; p->kv_dtype is DSPARK_I8.  It is the attention over the cache that dspark_cache_read_i8 gives.
  * Probabilities are rounded to 16 bits (fp16, or for many rows a kv head dtype) before they meet the values.
- * Host errors besides: DSPARK_ERR_UNSUPPORTED for a scale other than 0 outside 2^-32 .. 2^32.
+ * Host errors besides: DSPARK_ERR_UNSUPPORTED for a scale other than 0 outside 2^-32 .. 2^32, and for a pool that spans
+ * 2^32 times the largest power of two up to 4096 that its three strides are multiples of (64 GB at least), or exponents
+ * that span 4 GB.
  */
 dspark_status dspark_paged_attention_i8(const dspark_attention_params* p, const dspark_block_exponents* x, const void* q,
                                         const void* k_pages, const void* v_pages, const int32_t* block_table,

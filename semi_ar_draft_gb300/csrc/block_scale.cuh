@@ -34,6 +34,13 @@ struct BlockExp {
     int shift;
 };
 
+// The pools and exponents of an int8 cache in 32-bit steps: codes in units that all three strides are multiples of,
+// exponents in bytes (a stride that meets 0 alone, of a pool's only page or head, may be cut off).
+struct Steps32 {
+    uint32_t unit, page, token, head;
+    uint32_t e_page, e_block, e_head;
+};
+
 // The four codes of a word as fp32: byte + 128 beside the exponent of 2^23 is 2^23 + 128 + code.
 __device__ __forceinline__ void widen4(uint32_t w, float (&f)[4]) {
     const uint32_t u = w ^ 0x80808080u;

@@ -49,6 +49,7 @@ struct AttnArgs {
     const float* k_scale;
     const float* v_scale;
     BlockExp exp;        // int8 pools
+    Steps32 steps;       // the same and the pools, for launch_attn_i8 and launch_attn_i8_rows
     unsigned char* out;  // [T, Hq, D]
     float* lse;          // [T, Hq] or null
     // workspace

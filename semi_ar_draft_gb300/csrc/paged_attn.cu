@@ -723,6 +723,22 @@ dspark_status check_attention_params(const dspark_attention_params* p) {
     return DSPARK_OK;
 }
 
+// False where an offset does not fit 32 bits.
+bool steps32(const dspark_attention_params* p, const dspark_block_exponents* x, Steps32* s) {
+    const long long all = p->kv_page_stride | p->kv_token_stride | p->kv_head_stride;
+    int shift = 4;
+    while (shift < 12 && !(all >> shift & 1)) ++shift;
+    auto span = [](long long a, long long n, long long b, long long m, long long c, long long k) {
+        return (double)a * (n - 1) + (double)b * (m - 1) + (double)c * (k - 1);
+    };
+    if (span(p->kv_page_stride >> shift, p->num_pages, p->kv_token_stride >> shift, p->page_size, p->kv_head_stride >> shift, p->Hk) >= 4294967295.0 ||
+        span(x->page_stride, p->num_pages, x->block_stride, p->page_size / x->block, x->head_stride, p->Hk) >= 4294967295.0)
+        return false;
+    *s = {1u << shift, (uint32_t)(p->kv_page_stride >> shift), (uint32_t)(p->kv_token_stride >> shift), (uint32_t)(p->kv_head_stride >> shift),
+          (uint32_t)x->page_stride, (uint32_t)x->block_stride, (uint32_t)x->head_stride};
+    return true;
+}
+
 // Both entry points; x: the exponents of an int8 cache, or null.
 dspark_status paged_attention(const dspark_attention_params* p, const dspark_block_exponents* x, const void* q, const void* k_pages,
                               const void* v_pages, const int32_t* block_table, const int32_t* seq_len, const int32_t* offsets,
@@ -746,6 +762,8 @@ dspark_status paged_attention(const dspark_attention_params* p, const dspark_blo
     if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < w.bytes) return DSPARK_ERR_WORKSPACE;
     for (const long long x : {p->kv_page_stride, p->kv_token_stride, p->kv_head_stride})  // 32 bits of 16 bytes
         if (x < 0 || x * esz / 16 > INT32_MAX) return DSPARK_ERR_INVALID_ARG;
+    Steps32 steps = {};
+    if (x && !steps32(p, x, &steps)) return DSPARK_ERR_UNSUPPORTED;
     int sms = 0;
     if (device_sm_count(&sms) != cudaSuccess) return DSPARK_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -786,9 +804,11 @@ dspark_status paged_attention(const dspark_attention_params* p, const dspark_blo
     a.k_scale = e4m3 ? k_scale : nullptr;
     a.v_scale = e4m3 ? v_scale : nullptr;
     a.exp = {};
+    a.steps = {};
     if (x) {
         a.exp = {x->k, x->v, x->page_stride, x->block_stride, x->head_stride, 0};
         while ((1 << a.exp.shift) < x->block) ++a.exp.shift;
+        a.steps = steps;
     }
     a.out = static_cast<unsigned char*>(out);
     a.lse = lse;

@@ -51,6 +51,8 @@ struct RowsI8 {
     }
 };
 
+constexpr uint32_t kNoKey = 0xffffffffu;
+
 __device__ __forceinline__ void copy16_all(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -112,23 +114,25 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
             const bool live = lane < C::kKeys && key < ld.r.seq && key >= ld.r.lo;
             const bool found = live && pid >= 0 && pid < a.num_pages;
             if (live && !found) err = DSPARK_ERR_CACHE;
+            const Steps32& by = a.steps;
             if (found) {
-                const long long e = exponents_at(a, pid, place, ld_head);
+                const uint32_t e = pid * by.e_page + (place >> a.exp.shift) * by.e_block + ld_head * by.e_head;
                 k_exp[queue] = __ldg(a.exp.k + e);
                 v_exp[queue] = __ldg(a.exp.v + e);
             }
-            const long long off = found ? pid * a.page + place * a.token + ld_head * a.head : -1;
+            const uint32_t off = found ? pid * by.page + place * by.token + ld_head * by.head : kNoKey;
             const uint32_t dst = ring + ld_stage * C::kStage;
             constexpr int kPer = 32 / C::kChunks;  // rows a warp copies at a time
             const int chunk = lane % C::kChunks;
+            const unsigned char *k_from = a.k_pages + chunk * 16, *v_from = a.v_pages + chunk * 16;
             // (What is not there is not copied: see paged_attn_i8.cu.)
 #pragma unroll
             for (int i = 0; i < C::kKeys / kPer; ++i) {
                 const int row = i * kPer + lane / C::kChunks;
-                const long long o = __shfl_sync(0xffffffffu, off, row);
-                if (chunk * 16 < a.D && o >= 0) {
-                    copy16_all(dst + C::at(C::kKeys * warp + row, chunk), a.k_pages + o + chunk * 16);
-                    copy16_all(dst + C::kHalf + C::at(C::kKeys * warp + row, chunk), a.v_pages + o + chunk * 16);
+                const uint32_t o = __shfl_sync(0xffffffffu, off, row);
+                if (chunk * 16 < a.D && o != kNoKey) {
+                    copy16_all(dst + C::at(C::kKeys * warp + row, chunk), k_from + (uint64_t)o * by.unit);
+                    copy16_all(dst + C::kHalf + C::at(C::kKeys * warp + row, chunk), v_from + (uint64_t)o * by.unit);
                 }
             }
         }

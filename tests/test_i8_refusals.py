@@ -100,6 +100,12 @@ def test_attention_takes_int8_pools_with_exponents_only(L):
         p.scale = scale
         assert L.dspark_paged_attention_i8(C.byref(p), C.byref(x), *args(), A[6], None, A[7], size, None) == 2
     p.scale = 0.1
+    # offsets that do not fit 32 bits of the strides' common power of two (16 bytes here), or of a byte of the exponents
+    p.kv_token_stride, p.kv_page_stride = 272, 16 * (2 ** 32 // 8)
+    assert L.dspark_paged_attention_i8(C.byref(p), C.byref(x), *args(), A[6], None, A[7], size, None) == 2
+    p.kv_token_stride, p.kv_page_stride = 256, 4096
+    y = exps(page_stride=2 ** 29)
+    assert L.dspark_paged_attention_i8(C.byref(p), C.byref(y), *args(), A[6], None, A[7], size, None) == 2
     for kv in (b.BF16, b.E4M3):
         p.kv_dtype = kv
         assert L.dspark_paged_attention_i8(C.byref(p), C.byref(x), *args(), A[6], None, A[7], 1 << 30, None) == 1
