@@ -531,6 +531,9 @@ dspark_status dspark_paged_attention(const dspark_attention_params* p, const voi
  * dspark_cache_read_i8 is the way back: k, v [T, Hk, D] dense (dtype), 16-byte aligned, become the values of the T
  * slots, exactly; those of slots outside the pool are 0.
  *
+ * dspark_cache_append_i8 writes: k_pages and v_pages, and k and v of the exponents, are different memory, and no two
+ * blocks share an exponent (DSPARK_ERR_INVALID_ARG where pointers or strides of 0 say so).
+ *
  * Both take a dspark_append_params with kv_dtype DSPARK_I8 (dspark_cache_read_i8: the strides of k and v are the
  * dense ones).  Host errors: DSPARK_ERR_UNSUPPORTED unless D is a multiple of 16 up to 256.  No workspace; T = 0
  * enqueues nothing.

@@ -319,7 +319,8 @@ __global__ void __launch_bounds__(window_threads(W), 1280 / window_threads(W)) c
                 if (s_twice)
                     for (int i = 32 * warp + lane + 1; i < 2 * W; ++i)
                         if ((s_taken[i >> 5] >> (i & 31)) & 1u && __ldg(a.slots + t0 + i) == slot) later = 0x80000000u;
-                s_list[at] = (uint32_t)(32 * warp + lane) | (uint32_t)(slot & ((1 << a.block_shift) - 1)) << 8 | (uint32_t)run << 16 | later;
+                s_list[at] = (uint32_t)(32 * warp + lane) | (uint32_t)(slot & ((1 << a.block_shift) - 1)) << 8 |
+                             (uint32_t)run << 16 | later;
             }
         }
 #pragma unroll
@@ -400,7 +401,8 @@ __global__ void __launch_bounds__(window_threads(W), 1280 / window_threads(W)) c
                 const int run = (int)((it >> 16) & 127u);
                 if (it >> 31) return;
                 const long long slot = (s_block[run] << a.block_shift) + (int)((it >> 8) & 127u);
-                const long long to = (slot >> a.page_shift) * a.page + (slot & ((1 << a.page_shift) - 1)) * a.token + head * a.head + 16 * c;
+                const long long to = (slot >> a.page_shift) * a.page + (slot & ((1 << a.page_shift) - 1)) * a.token +
+                                     head * a.head + 16 * c;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     const int e = s_exp[kv][run];
@@ -427,7 +429,8 @@ __global__ void __launch_bounds__(window_threads(W), 1280 / window_threads(W)) c
     }
 }
 
-// A scale for every token: nothing of the block is older.  2^lanes_shift lanes take keys and values of a (token, kv head); the token is left out where the next entry that is not skipped has its slot.
+// A scale for every token: nothing of the block is older.  2^lanes_shift lanes take keys and values of a (token, kv head);
+// the token is left out where the next entry that is not skipped has its slot.
 template <bool BF16, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) cache_append_i8_token_kernel(I8Args a) {
     wait_primary();
@@ -470,7 +473,8 @@ __global__ void __launch_bounds__(kThreads) cache_append_i8_token_kernel(I8Args 
             const int wanted = wanted_exponent<BF16>(top), e = within<BF16>(wanted);
             if (!live) continue;
             *reinterpret_cast<uint4*>(a.pages[kv] + page * a.page + at * a.token + h * a.head + 16 * c) =
-                odd || wanted > ExpRange<BF16>::kHi ? quantize16<BF16, true>(x[kv], two_to(-e)) : quantize16<BF16, false>(x[kv], two_to(-e));
+                odd || wanted > ExpRange<BF16>::kHi ? quantize16<BF16, true>(x[kv], two_to(-e))
+                                                    : quantize16<BF16, false>(x[kv], two_to(-e));
             if (c == 0) a.exps[kv][page * a.e_page + at * a.e_block + h * a.e_head] = (unsigned char)(e + 127);
         }
     }
@@ -590,6 +594,9 @@ extern "C" dspark_status dspark_cache_append_i8(const dspark_append_params* p, c
     if (st != DSPARK_OK) return st;
     if ((p->T && (!k || !v || !slots)) || (((uintptr_t)k | (uintptr_t)v) & 1u) || ((uintptr_t)error & 3u)) return DSPARK_ERR_INVALID_ARG;
     if (k_pages == v_pages || x->k == x->v) return DSPARK_ERR_INVALID_ARG;
+    // (blocks that share an exponent are for reading)
+    if ((!x->page_stride && p->num_pages > 1) || (!x->block_stride && x->block < p->page_size) || (!x->head_stride && p->Hk > 1))
+        return DSPARK_ERR_INVALID_ARG;
     if (p->T == 0) return DSPARK_OK;
     int sms = 0;
     if (device_sm_count(&sms) != cudaSuccess) return DSPARK_ERR_CUDA;

@@ -731,11 +731,13 @@ bool steps32(const dspark_attention_params* p, const dspark_block_exponents* x, 
     auto span = [](long long a, long long n, long long b, long long m, long long c, long long k) {
         return (double)a * (n - 1) + (double)b * (m - 1) + (double)c * (k - 1);
     };
-    if (span(p->kv_page_stride >> shift, p->num_pages, p->kv_token_stride >> shift, p->page_size, p->kv_head_stride >> shift, p->Hk) >= 4294967295.0 ||
-        span(x->page_stride, p->num_pages, x->block_stride, p->page_size / x->block, x->head_stride, p->Hk) >= 4294967295.0)
+    const long long page = p->kv_page_stride >> shift, token = p->kv_token_stride >> shift, head = p->kv_head_stride >> shift;
+    constexpr double most = 4294967295.0;
+    if (span(page, p->num_pages, token, p->page_size, head, p->Hk) >= most ||
+        span(x->page_stride, p->num_pages, x->block_stride, p->page_size / x->block, x->head_stride, p->Hk) >= most)
         return false;
-    *s = {1u << shift, (uint32_t)(p->kv_page_stride >> shift), (uint32_t)(p->kv_token_stride >> shift), (uint32_t)(p->kv_head_stride >> shift),
-          (uint32_t)x->page_stride, (uint32_t)x->block_stride, (uint32_t)x->head_stride};
+    *s = {1u << shift,           (uint32_t)page,            (uint32_t)token,         (uint32_t)head, (uint32_t)x->page_stride,
+          (uint32_t)x->block_stride, (uint32_t)x->head_stride};
     return true;
 }
 

@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
                 for (int i = 0; i < DP / 8; ++i) sum += s_qsum[tid][i];
                 s_base[tid] = -128.f * 0x1p-24f * sum;
                 // to the log2 domain, or to the cap's exponent
-                s_scale[tid] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale * 0x1p24f * (BF16 ? two_to(-raise(tid)) : 1.f);
+                s_scale[tid] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale * 0x1p24f *
+                               (BF16 ? two_to(-raise(tid)) : 1.f);
             }
             __syncthreads();
             if (!C::kQInSmem) {
@@ -463,7 +464,8 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
                 const float f = ex2(0.5f * (ref_v[r] - ref[r]));
 #pragma unroll
                 for (int i = 0; i < KS; ++i)
-                    *reinterpret_cast<float2*>(mine_o + o_at(2 * t + r, 16 * i + 2 * g)) = make_float2(o[i][r] * f * f, o[i][2 + r] * f * f);
+                    *reinterpret_cast<float2*>(mine_o + o_at(2 * t + r, 16 * i + 2 * g)) =
+                        make_float2(o[i][r] * f * f, o[i][2 + r] * f * f);
             }
             __syncthreads();
             const bool whole = last_of_item && seg_first == 0;

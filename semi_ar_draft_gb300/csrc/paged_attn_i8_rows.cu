@@ -35,10 +35,11 @@ struct RowsI8 {
     static constexpr int kStages = DP == 64 ? 3 : 2;
     static constexpr int kExtra = 1;     // what an item costs beside its key tiles
     static constexpr int kDm = DP / 64;  // 16-value groups of a warp's quarter of a head
-    static constexpr int kBlocksPerSm = DP == 256 ? 2 : 3;
+    static constexpr int kBlocksPerSm = 3;
     static constexpr int kQBytes = kRows * DP * 2;
-    static constexpr int kPBytes = kRows * kKeyTile * 2;
-    static constexpr size_t kSmem = (size_t)kStages * kStage + kQBytes + kPBytes;
+    // The weights of a tile lie over its keys, which every warp has done with by then.
+    static_assert(kRows * kKeyTile * 2 <= kHalf, "room for the weights");
+    static constexpr size_t kSmem = (size_t)kStages * kStage + kQBytes;
     static __device__ __forceinline__ uint32_t at(int row, int chunk) {  // of codes
         const int x = kChunks >= 8 ? (row & 7) : ((row >> 1) & 3);
         return (uint32_t)(row * DP + ((chunk ^ x) << 4));
@@ -75,7 +76,6 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
     __shared__ int s_err;
     __shared__ AttnScratch s_start;
     __shared__ uint32_t s_qmax[kRows];                 // largest |q| of each row (its bits)
-    __shared__ float s_qsum[kRows][DP / 8];           // sums of a row's query, eight values each
     __shared__ __align__(8) float s_base[kRows], s_scale[kRows];  // where a row's products begin, its scores' factor
     __shared__ AttnStart s_range;                     // the block's units
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
     attn_tail_rows(a, (size_t)part * kThreads + tid, (size_t)parts * kThreads);
     const uint32_t ring = smem_addr(smem);
     unsigned char* qs = smem + (size_t)C::kStages * C::kStage;
-    const uint32_t qs_addr = smem_addr(qs), ps_addr = qs_addr + C::kQBytes;
+    const uint32_t qs_addr = smem_addr(qs);
     int err = bad ? DSPARK_ERR_CACHE : 0;
     if (tid == 0) s_range = start;  // (read by this thread)
 
@@ -230,16 +230,15 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
                     *reinterpret_cast<uint32_t*>(qs + C::q_at(row, c & ~1) + at) = __byte_perm(y[2 * e], y[2 * e + 1], 0x5410);
                     *reinterpret_cast<uint32_t*>(qs + C::q_at(row, c | 1) + at) = __byte_perm(y[2 * e], y[2 * e + 1], 0x7632);
                 }
-                s_qsum[row][c] = sum;
-            }
-            __syncthreads();
-            for (int i = tid; i < kRows; i += kThreads) {
-                float sum = 0.f;
-#pragma unroll 4
-                for (int c = 0; c < DP / 8; ++c) sum += s_qsum[i][c];
-                s_base[i] = -128.f * 0x1p-24f * sum;
-                // to the log2 domain, or to the cap's exponent
-                s_scale[i] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale * 0x1p24f * (BF16 ? two_to(-raise(i)) : 1.f);
+                // the row's sum, from the lanes that hold it
+#pragma unroll
+                for (int d = 1; d < kQc; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (c == 0) {
+                    s_base[row] = -128.f * 0x1p-24f * sum;
+                    // to the log2 domain, or to the cap's exponent
+                    s_scale[row] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale * 0x1p24f *
+                                   (BF16 ? two_to(-raise(row)) : 1.f);
+                }
             }
             __syncthreads();
 #pragma unroll
@@ -416,7 +415,7 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
                 }
             }
         }
-        // ---- P^T as halves, rows of P in shared memory
+        // ---- P^T as halves, rows of P over the tile's keys
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
 #pragma unroll
@@ -434,7 +433,7 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
                         p[2 * u + h] = pack16<false>(ex2(z.x), ex2(z.y));
                     }
                 }
-                stsm4_trans(ps_addr + C::p_at(8 * j + (lane & 7) + (lane >> 4) * 8, 2 * (MT * warp + i) + ((lane >> 3) & 1)), p);
+                stsm4_trans(kb + C::p_at(8 * j + (lane & 7) + (lane >> 4) * 8, 2 * (MT * warp + i) + ((lane >> 3) & 1)), p);
             }
         }
         __syncthreads();
@@ -445,7 +444,7 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
 #pragma unroll
             for (int j = 0; j < NT; j += 2) {
                 uint32_t b[4];
-                ldsm4(b, ps_addr + C::p_at(8 * j + (lane & 7) + (lane >> 4) * 8, 2 * kk + ((lane >> 3) & 1)));
+                ldsm4(b, kb + C::p_at(8 * j + (lane & 7) + (lane >> 4) * 8, 2 * kk + ((lane >> 3) & 1)));
                 p[j][0] = b[0];
                 p[j][1] = b[1];
                 p[j + 1][0] = b[2];

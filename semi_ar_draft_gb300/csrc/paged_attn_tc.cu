@@ -1,10 +1,10 @@
-// paged_attn_tc.cu -- dspark_paged_attention on the fifth-generation tensor cores: row tiles of 128 for
-// requests whose new tokens give more than 16 rows a kv head, 48 with an 8-bit cache (the flattened verify, draft
-// blocks).
+// paged_attn_tc.cu -- dspark_paged_attention and dspark_paged_attention_i8 on the fifth-generation tensor cores: row tiles of 128 for
+// requests whose new tokens give more than 16 rows a kv head, 48 with an e4m3 cache, 36 with an int8 one (the flattened
+// verify, draft blocks).
 //
 // One persistent CTA a multiprocessor walks its range of units (paged.cuh).  Roles:
-//   loaders (4 warps)    copy the item's queries and, tile by tile, KT keys and values into a ring in
-//                        shared memory, 16 bytes a thread and copy, in the 128-byte-swizzled layout the MMA
+//   loaders (4 or 8      copy the item's queries and, tile by tile, KT keys and values into a ring in
+//     warps)             shared memory, 16 bytes a thread and copy, in the 128-byte-swizzled layout the MMA
 //                        reads; several tiles in flight, across items; tiles of an 8-bit cache arrive as they are
 //                        and are widened into the ring by the lanes that copied them
 //   MMA (1 warp a stream) S = Q K^T into tensor memory, and O += P V with P from tensor memory
@@ -22,8 +22,11 @@
 // shorter than its loads: 512 requests of up to 4096 tokens, 8 query heads of 128 a kv head, 5 new tokens on
 // average: 417 us = 6.0 TB/s (0.88 of the measured copy rate).  With heads of 64 a tile is half the bytes and the
 // softmax decides: 32 draft blocks of 16 over up to 4100 tokens 52.5 us = 2.8 TB/s (0.42).
-// Over an 8-bit cache the loaders' widening decides at few rows (32 requests, 35 rows on average: 85 us, of row
-// tiles of 16: 69) and pays at many (145 requests, 119 rows of 192 over 200 keys: 92 us against 254).
+// Over an 8-bit cache the loaders' widening decides at few rows (32 requests, 35 rows on average, e4m3: 85 us, of row
+// tiles of 16: 69) and pays at many (145 requests, 119 rows of 192 over 200 keys, e4m3: 92 us against 254).  An int8
+// cache's codes take five instructions a pair and their scales' product besides, so it has eight loaders: 64 requests of up
+// to 4096 tokens, 63 rows, 4 kv heads of 128: 109 us (row tiles of 16: 139); 32 draft blocks of 16, heads of 64: 60 us;
+// two prompts of 2000 tokens over 6000: 0.68 ms (1.87).
 #include <cuda_bf16.h>
 
 #include "host_util.h"
@@ -294,244 +297,244 @@ __global__ void __launch_bounds__(TcAttn<KV, DP>::kThreads, 1) attn_tc_kernel(At
     // (The register counts change inside the branches: the compiler goes by that.)
     if (warp >= C::kSoftmaxWarps) {
         if constexpr (C::kDealRegisters) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kHelperRegisters));
-    if (C::loader_of(warp) >= 0) {
-        // ---------------------------------------------------------------- loaders
-        constexpr int kChunks = DP / (F8 ? 16 : 8);  // 16-byte groups of a row in the cache
-        constexpr int kPer = 32 / kChunks;           // rows a warp copies at a time
-        const int lw = C::loader_of(warp);
-        const int chunk = lane % kChunks, sub_row = lane / kChunks;
-        const bool inside = chunk * (F8 ? 16 : 8) < a.D;
-        const uint32_t base = smem_addr(smem);
-        const uint32_t mask = (1u << a.page_shift) - 1;
-        const uint32_t page16 = (uint32_t)(a.page >> 4), token16 = (uint32_t)(a.token >> 4);
-        const unsigned char* k_at = a.k_pages + chunk * 16;
-        const long long v_after_k = a.v_pages - a.k_pages;
-        AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit, C::kExtra);
-        int err = 0, seg = 0;
-        // This warp's keys of its stream's tiles.
-        constexpr int kKeys = KT / C::kTileLoaders;
-        const int first_key = (lw / C::kTileLoaders) * KT + (lw % C::kTileLoaders) * kKeys;
-        auto tile_key = [&]() { return (w.kt_first + w.kt) * C::kUnit + first_key; };
-        // Page of this lane's key of the next tile, asked for a tile ahead.  The load is unconditional (entry 0
-        // where there is no key) and looked at when the copies are issued, so that nothing waits for it here.
-        int pid;
-        auto fetch_pages = [&]() {
-            const int key = min(tile_key() + lane, w.r.seq - 1);
-            const size_t at = w.done() || key < 0 ? 0 : (size_t)w.j * a.max_blocks + (key >> a.page_shift);
-            pid = __ldg(a.block_table + at);
-        };
-        fetch_pages();
-        bool fresh = true;
-        int head = 0, slot = lw / C::kTileLoaders, round = 0;
-        const int tile_row = (lw % C::kTileLoaders) * kKeys + sub_row;
-        // 8-bit caches: a tile arrives as it is, each lane's pieces in places of its own, `ahead` tiles at a time; the
-        // lane that copied a piece widens it into the slot, keys to q's type, values to halves (int8: q's type), all exact.
-        constexpr int kSteps = kKeys / kPer;
-        int raw_slot = 0, raw_old = 0, ahead = 0;
-        uint32_t k_exp[I8 ? C::kRawSlots : 1], v_exp[I8 ? C::kRawSlots : 1];  // of this lane's key of the raw tiles
-        unsigned char* raw = smem + C::kRaw + lw * (C::kRawSlots * C::kRawTile) + lane * 16;
-        auto widen = [&]() {
-            if (round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) return false;
-            unsigned char* to = smem + C::kRing + slot * (2 * C::kTile) + ((2 * chunk) >> 3) * (KT * 128);
-            const unsigned char* from = raw + raw_old * C::kRawTile;
-            uint32_t e = 0;
-            if (I8) {
-#pragma unroll
-                for (int i = 0; i < C::kRawSlots; ++i)
-                    if (raw_old == i) e = k_exp[I8 ? i : 0] | v_exp[I8 ? i : 0] << 8;
-            }
-#pragma unroll 2
-            for (int u = 0; u < kSteps; ++u) {
-                const uint32_t at0 = sw128_offset(tile_row + u * kPer, (2 * chunk) & 7);
-                const uint32_t at1 = sw128_offset(tile_row + u * kPer, (2 * chunk + 1) & 7);
-                const uint4 k = *reinterpret_cast<const uint4*>(from + 2 * u * 512);
-                const uint4 v = *reinterpret_cast<const uint4*>(from + (2 * u + 1) * 512);
-                uint4 x, y;
-                uint32_t with = 0;
+        if (C::loader_of(warp) >= 0) {
+            // ---------------------------------------------------------------- loaders
+            constexpr int kChunks = DP / (F8 ? 16 : 8);  // 16-byte groups of a row in the cache
+            constexpr int kPer = 32 / kChunks;           // rows a warp copies at a time
+            const int lw = C::loader_of(warp);
+            const int chunk = lane % kChunks, sub_row = lane / kChunks;
+            const bool inside = chunk * (F8 ? 16 : 8) < a.D;
+            const uint32_t base = smem_addr(smem);
+            const uint32_t mask = (1u << a.page_shift) - 1;
+            const uint32_t page16 = (uint32_t)(a.page >> 4), token16 = (uint32_t)(a.token >> 4);
+            const unsigned char* k_at = a.k_pages + chunk * 16;
+            const long long v_after_k = a.v_pages - a.k_pages;
+            AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit, C::kExtra);
+            int err = 0, seg = 0;
+            // This warp's keys of its stream's tiles.
+            constexpr int kKeys = KT / C::kTileLoaders;
+            const int first_key = (lw / C::kTileLoaders) * KT + (lw % C::kTileLoaders) * kKeys;
+            auto tile_key = [&]() { return (w.kt_first + w.kt) * C::kUnit + first_key; };
+            // Page of this lane's key of the next tile, asked for a tile ahead.  The load is unconditional (entry 0
+            // where there is no key) and looked at when the copies are issued, so that nothing waits for it here.
+            int pid;
+            auto fetch_pages = [&]() {
+                const int key = min(tile_key() + lane, w.r.seq - 1);
+                const size_t at = w.done() || key < 0 ? 0 : (size_t)w.j * a.max_blocks + (key >> a.page_shift);
+                pid = __ldg(a.block_table + at);
+            };
+            fetch_pages();
+            bool fresh = true;
+            int head = 0, slot = lw / C::kTileLoaders, round = 0;
+            const int tile_row = (lw % C::kTileLoaders) * kKeys + sub_row;
+            // 8-bit caches: a tile arrives as it is, each lane's pieces in places of its own, `ahead` tiles at a time; the
+            // lane that copied a piece widens it into the slot, keys to q's type, values to halves (int8: q's type), all exact.
+            constexpr int kSteps = kKeys / kPer;
+            int raw_slot = 0, raw_old = 0, ahead = 0;
+            uint32_t k_exp[I8 ? C::kRawSlots : 1], v_exp[I8 ? C::kRawSlots : 1];  // of this lane's key of the raw tiles
+            unsigned char* raw = smem + C::kRaw + lw * (C::kRawSlots * C::kRawTile) + lane * 16;
+            auto widen = [&]() {
+                if (round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) return false;
+                unsigned char* to = smem + C::kRing + slot * (2 * C::kTile) + ((2 * chunk) >> 3) * (KT * 128);
+                const unsigned char* from = raw + raw_old * C::kRawTile;
+                uint32_t e = 0;
                 if (I8) {
-                    with = __shfl_sync(0xffffffffu, e, u * kPer + sub_row);
-                    widen16_i8<BF16>(k, scale_pair<BF16>(exponent_of<BF16>(with & 0xffu)), x, y);
-                } else {
-                    widen16<BF16>(k, x, y);
-                }
-                *reinterpret_cast<uint4*>(to + at0) = x;
-                *reinterpret_cast<uint4*>(to + at1) = y;
-                if (I8)
-                    widen16_i8<BF16>(v, scale_pair<BF16>(exponent_of<BF16>(with >> 8)), x, y);
-                else
-                    widen16<false>(v, x, y);
-                *reinterpret_cast<uint4*>(to + at0 + C::kTile) = x;
-                *reinterpret_cast<uint4*>(to + at1 + C::kTile) = y;
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive_local(&bars->full[slot]);
-            slot += NS;
-            if (slot >= C::kSlots) {
-                slot -= C::kSlots;
-                ++round;
-            }
-            if (++raw_old == C::kRawSlots) raw_old = 0;
-            return true;
-        };
-        // An item's queries: with two streams after its first keys, since their buffer is free later than a
-        // slot (421 against 426 us for the 512-request verify); with heads of 256, where they are as large as two
-        // tiles, before (122 against 131 us for three long contexts, with a softcap 8 us cheaper than now).
-        constexpr bool kQueriesFirst = NS == 1;
-        auto queries = [&]() {
-            const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
-            if (F8 && use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1)))) {
-                // the products that still read it may be waiting for raw tiles
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                while (ahead > 0 && widen()) --ahead;
-            }
-            if (use > 0 && !warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) return false;
-            ++seg;
-            const int row0 = (w.item - head * w.rts) * kTcRowTile;
-            const int rows = min(w.r.n * a.G - row0, kTcRowTile);
-            constexpr int kQPer = 256 / DP;  // rows a warp copies at a time
-            const int qc = lane % (DP / 8);
-            const uint32_t qbase = base + (uint32_t)qb * C::kQ + (uint32_t)(qc >> 3) * (kTcRowTile * 128);
-            for (int r = lw * kQPer + lane / (DP / 8); r < ((rows + 31) & ~31); r += C::kLoaders * kQPer) {
-                const bool real = qc * 8 < a.D && r < rows;
-                const int row = row0 + r;
-                const int token = attn_token(a, row);
-                const long long src = real ? (w.r.token0 + token) * a.q_token +
-                                                 (head * a.G + row - token * a.G) * a.q_head + qc * 8
-                                           : 0;
-                copy16(qbase + sw128_offset(r, qc & 7), a.q + 2 * src, real);
-            }
-            copy_arrive(&bars->qfull[qb]);
-            return true;
-        };
-        while (!w.done()) {
-            if (fresh) {
-                head = w.item / w.rts;
-                if (kQueriesFirst && !queries()) break;
-            }
-            if (!F8 && round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) break;
-            const int key0 = tile_key();
-            const unsigned char* head_at = k_at + head * a.head;
-            const bool none = key0 + lane >= w.r.seq || key0 + lane < w.r.lo;
-            if ((uint32_t)pid >= (uint32_t)a.num_pages) {
-                if (!none && lane < kKeys) err = DSPARK_ERR_CACHE;
-                pid = -1;
-            }
-            if (none) pid = -1;
-            if (I8) {  // (entry 0 where there is no key, whose codes are zeros)
-                const long long at = pid >= 0 && lane < kKeys ? exponents_at(a, pid, (key0 + lane) & mask, head) : 0;
 #pragma unroll
-                for (int i = 0; i < C::kRawSlots; ++i)
-                    if (raw_slot == i) {
-                        k_exp[I8 ? i : 0] = __ldg(a.exp.k + at);
-                        v_exp[I8 ? i : 0] = __ldg(a.exp.v + at);
-                    }
-            }
-            const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + (uint32_t)(chunk >> 3) * (KT * 128);
-            const uint32_t rb = smem_addr(raw) + (uint32_t)(raw_slot * C::kRawTile);
-#pragma unroll (I8 ? 2 : 8)
-            for (int i = 0; i < kKeys; i += kPer) {
-                const int p = __shfl_sync(0xffffffffu, pid, i + sub_row);
-                const bool real = inside && p >= 0;
-                const uint64_t at16 = (uint64_t)(uint32_t)max(p, 0) * page16 +
-                                      (uint64_t)((uint32_t)(key0 + i + sub_row) & mask) * token16;
-                const unsigned char* src = real ? head_at + 16 * at16 : a.k_pages;
-                const uint32_t dst = F8 ? rb + (uint32_t)(i / kPer) * 1024u : kb + sw128_offset(tile_row + i, chunk & 7);
-                copy16(dst, src, real);
-                copy16(dst + (F8 ? 512 : C::kTile), src + v_after_k, real);
-            }
-            if constexpr (F8) {
-                cp_async_commit();
-                if (++raw_slot == C::kRawSlots) raw_slot = 0;
-                if (++ahead == C::kRawSlots) {  // the oldest has landed once the others alone are in flight
-                    cp_async_wait_group<C::kRawSlots - 1>();
-                    --ahead;
-                    if (!widen()) break;
+                    for (int i = 0; i < C::kRawSlots; ++i)
+                        if (raw_old == i) e = k_exp[I8 ? i : 0] | v_exp[I8 ? i : 0] << 8;
                 }
-            } else {
-                // The slot is full once its loaders' copies so far have landed; nobody waits for that here, so
-                // the whole ring can be in flight.
-                copy_arrive(&bars->full[slot]);
+#pragma unroll 2
+                for (int u = 0; u < kSteps; ++u) {
+                    const uint32_t at0 = sw128_offset(tile_row + u * kPer, (2 * chunk) & 7);
+                    const uint32_t at1 = sw128_offset(tile_row + u * kPer, (2 * chunk + 1) & 7);
+                    const uint4 k = *reinterpret_cast<const uint4*>(from + 2 * u * 512);
+                    const uint4 v = *reinterpret_cast<const uint4*>(from + (2 * u + 1) * 512);
+                    uint4 x, y;
+                    uint32_t with = 0;
+                    if (I8) {
+                        with = __shfl_sync(0xffffffffu, e, u * kPer + sub_row);
+                        widen16_i8<BF16>(k, scale_pair<BF16>(exponent_of<BF16>(with & 0xffu)), x, y);
+                    } else {
+                        widen16<BF16>(k, x, y);
+                    }
+                    *reinterpret_cast<uint4*>(to + at0) = x;
+                    *reinterpret_cast<uint4*>(to + at1) = y;
+                    if (I8)
+                        widen16_i8<BF16>(v, scale_pair<BF16>(exponent_of<BF16>(with >> 8)), x, y);
+                    else
+                        widen16<false>(v, x, y);
+                    *reinterpret_cast<uint4*>(to + at0 + C::kTile) = x;
+                    *reinterpret_cast<uint4*>(to + at1 + C::kTile) = y;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive_local(&bars->full[slot]);
                 slot += NS;
                 if (slot >= C::kSlots) {
                     slot -= C::kSlots;
                     ++round;
                 }
-            }
-            if (fresh && !kQueriesFirst && !queries()) break;
-            fresh = w.kt + 1 == w.kts;
-            walk_next(a, w, kTcRowTile, C::kUnit);
-            fetch_pages();
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if constexpr (F8)
-            while (ahead > 0 && widen()) --ahead;
-        if (err) bars->status = err;
-    } else if (C::mma_of(warp) >= 0) {
-        // ---------------------------------------------------------------- MMA issue
-        // The whole warp runs this with equal values and one elected lane issues: descriptors then stay in
-        // uniform registers (from one divergent lane each MMA cost 90 to 160 cycles to issue).
-        constexpr uint32_t idesc_s = idesc16<BF16>(kTcRowTile, KT, false);
-        constexpr uint32_t idesc_o = idesc16<VB>(kTcRowTile, DP, true);
-        const uint32_t base = smem_addr(smem);
-        // The upper halves of the descriptors hold layout and stride only (and the leading offset, V's, sits in
-        // the lower half's upper bits; with one group of 64 values it is not used).
-        const uint64_t k_desc = umma_desc_sw128(base, 1024);
-        const uint64_t v_desc = umma_desc_sw128_mn(base, C::kSub > 1 ? KT * 128 : 1024, 1024);
-        const uint32_t k_hi = (uint32_t)(k_desc >> 32), k_lo = (uint32_t)k_desc & 0xffff0000u;
-        const uint32_t v_hi = (uint32_t)(v_desc >> 32), v_lo = (uint32_t)v_desc & 0xffff0000u;
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit, C::kExtra);
-        const int s = C::mma_of(warp);
-        int seg = 0, slot = s, turn = 0, held = 0;  // turn: parity of the ring's round; held: the slot whose values
-        bool ok = true, behind = false;             // are still to come, if behind
-        auto values = [&](int n) {  // O_s += P_s V of the stream's n-th tile
-            if (!warp_wait(&bars->pfull[s], (uint32_t)(n & 1))) return false;
-            tc_fence_after();
-            const uint32_t vd = v_lo + ((base + C::kRing + (uint32_t)held * (2 * C::kTile) + C::kTile) >> 4);
-#pragma unroll
-            for (int k = 0; k < KT / 16; ++k)
-                mma_elect_ts(tm + s * DP, tm + C::kColP + (2 * s + (n & 1)) * (KT / 2) + 8 * k, vd + k * (2048 >> 4), v_hi, idesc_o,
-                             1u);
-            commit_elect(&bars->empty[held]);
-            commit_elect(&bars->pvdone[s]);
-            return true;
-        };
-        for (int unit = 0; ok && __shfl_sync(0xffffffffu, !w.done(), 0); ++unit) {
-            const int qb = seg % C::kQBufs;
-            if ((!behind && !warp_wait(&bars->qfull[qb], (uint32_t)((seg / C::kQBufs) & 1))) ||  // an item's first tile
-                !warp_wait(&bars->full[slot], (uint32_t)turn) ||
-                (unit > 0 && !warp_wait(&bars->sfree[s], (uint32_t)((unit - 1) & 1))))
-                break;
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the loaders' copies, to the MMA
-            tc_fence_after();
-            const uint32_t qd = k_lo + ((base + (uint32_t)qb * C::kQ) >> 4);
-            const uint32_t kd = k_lo + ((base + C::kRing + (uint32_t)slot * (2 * C::kTile)) >> 4);
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k)
-                mma_elect_ss(tm + C::kColS + s * KT, qd + (k >> 2) * (kTcRowTile * 128 >> 4) + 2 * (k & 3), k_hi,
-                             kd + (k >> 2) * (KT * 128 >> 4) + 2 * (k & 3), k_hi, idesc_s, k > 0 ? 1u : 0u);
-            commit_elect(&bars->sfull[s]);
-            if (behind && !values(unit - 1)) break;
-            held = slot;
-            slot += NS;
-            if (slot >= C::kSlots) {
-                slot -= C::kSlots;
-                turn ^= 1;
-            }
-            // An item's last values do not wait for the next item's keys.
-            const bool end = __shfl_sync(0xffffffffu, w.kt + 1 == w.kts || w.left == 1, 0);
-            if (end) {
-                commit_elect(&bars->qempty[qb]);
+                if (++raw_old == C::kRawSlots) raw_old = 0;
+                return true;
+            };
+            // An item's queries: with two streams after its first keys, since their buffer is free later than a
+            // slot (421 against 426 us for the 512-request verify); with heads of 256, where they are as large as two
+            // tiles, before (122 against 131 us for three long contexts, with a softcap 8 us cheaper than now).
+            constexpr bool kQueriesFirst = NS == 1;
+            auto queries = [&]() {
+                const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
+                if (F8 && use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1)))) {
+                    // the products that still read it may be waiting for raw tiles
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    while (ahead > 0 && widen()) --ahead;
+                }
+                if (use > 0 && !warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) return false;
                 ++seg;
-                ok = values(unit);
+                const int row0 = (w.item - head * w.rts) * kTcRowTile;
+                const int rows = min(w.r.n * a.G - row0, kTcRowTile);
+                constexpr int kQPer = 256 / DP;  // rows a warp copies at a time
+                const int qc = lane % (DP / 8);
+                const uint32_t qbase = base + (uint32_t)qb * C::kQ + (uint32_t)(qc >> 3) * (kTcRowTile * 128);
+                for (int r = lw * kQPer + lane / (DP / 8); r < ((rows + 31) & ~31); r += C::kLoaders * kQPer) {
+                    const bool real = qc * 8 < a.D && r < rows;
+                    const int row = row0 + r;
+                    const int token = attn_token(a, row);
+                    const long long src = real ? (w.r.token0 + token) * a.q_token +
+                                                     (head * a.G + row - token * a.G) * a.q_head + qc * 8
+                                               : 0;
+                    copy16(qbase + sw128_offset(r, qc & 7), a.q + 2 * src, real);
+                }
+                copy_arrive(&bars->qfull[qb]);
+                return true;
+            };
+            while (!w.done()) {
+                if (fresh) {
+                    head = w.item / w.rts;
+                    if (kQueriesFirst && !queries()) break;
+                }
+                if (!F8 && round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) break;
+                const int key0 = tile_key();
+                const unsigned char* head_at = k_at + head * a.head;
+                const bool none = key0 + lane >= w.r.seq || key0 + lane < w.r.lo;
+                if ((uint32_t)pid >= (uint32_t)a.num_pages) {
+                    if (!none && lane < kKeys) err = DSPARK_ERR_CACHE;
+                    pid = -1;
+                }
+                if (none) pid = -1;
+                if (I8) {  // (entry 0 where there is no key, whose codes are zeros)
+                    const long long at = pid >= 0 && lane < kKeys ? exponents_at(a, pid, (key0 + lane) & mask, head) : 0;
+#pragma unroll
+                    for (int i = 0; i < C::kRawSlots; ++i)
+                        if (raw_slot == i) {
+                            k_exp[I8 ? i : 0] = __ldg(a.exp.k + at);
+                            v_exp[I8 ? i : 0] = __ldg(a.exp.v + at);
+                        }
+                }
+                const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + (uint32_t)(chunk >> 3) * (KT * 128);
+                const uint32_t rb = smem_addr(raw) + (uint32_t)(raw_slot * C::kRawTile);
+#pragma unroll (I8 ? 2 : 8)
+                for (int i = 0; i < kKeys; i += kPer) {
+                    const int p = __shfl_sync(0xffffffffu, pid, i + sub_row);
+                    const bool real = inside && p >= 0;
+                    const uint64_t at16 = (uint64_t)(uint32_t)max(p, 0) * page16 +
+                                          (uint64_t)((uint32_t)(key0 + i + sub_row) & mask) * token16;
+                    const unsigned char* src = real ? head_at + 16 * at16 : a.k_pages;
+                    const uint32_t dst = F8 ? rb + (uint32_t)(i / kPer) * 1024u : kb + sw128_offset(tile_row + i, chunk & 7);
+                    copy16(dst, src, real);
+                    copy16(dst + (F8 ? 512 : C::kTile), src + v_after_k, real);
+                }
+                if constexpr (F8) {
+                    cp_async_commit();
+                    if (++raw_slot == C::kRawSlots) raw_slot = 0;
+                    if (++ahead == C::kRawSlots) {  // the oldest has landed once the others alone are in flight
+                        cp_async_wait_group<C::kRawSlots - 1>();
+                        --ahead;
+                        if (!widen()) break;
+                    }
+                } else {
+                    // The slot is full once its loaders' copies so far have landed; nobody waits for that here, so
+                    // the whole ring can be in flight.
+                    copy_arrive(&bars->full[slot]);
+                    slot += NS;
+                    if (slot >= C::kSlots) {
+                        slot -= C::kSlots;
+                        ++round;
+                    }
+                }
+                if (fresh && !kQueriesFirst && !queries()) break;
+                fresh = w.kt + 1 == w.kts;
+                walk_next(a, w, kTcRowTile, C::kUnit);
+                fetch_pages();
             }
-            behind = !end;
-            walk_next(a, w, kTcRowTile, C::kUnit);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if constexpr (F8)
+                while (ahead > 0 && widen()) --ahead;
+            if (err) bars->status = err;
+        } else if (C::mma_of(warp) >= 0) {
+            // ---------------------------------------------------------------- MMA issue
+            // The whole warp runs this with equal values and one elected lane issues: descriptors then stay in
+            // uniform registers (from one divergent lane each MMA cost 90 to 160 cycles to issue).
+            constexpr uint32_t idesc_s = idesc16<BF16>(kTcRowTile, KT, false);
+            constexpr uint32_t idesc_o = idesc16<VB>(kTcRowTile, DP, true);
+            const uint32_t base = smem_addr(smem);
+            // The upper halves of the descriptors hold layout and stride only (and the leading offset, V's, sits in
+            // the lower half's upper bits; with one group of 64 values it is not used).
+            const uint64_t k_desc = umma_desc_sw128(base, 1024);
+            const uint64_t v_desc = umma_desc_sw128_mn(base, C::kSub > 1 ? KT * 128 : 1024, 1024);
+            const uint32_t k_hi = (uint32_t)(k_desc >> 32), k_lo = (uint32_t)k_desc & 0xffff0000u;
+            const uint32_t v_hi = (uint32_t)(v_desc >> 32), v_lo = (uint32_t)v_desc & 0xffff0000u;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit, C::kExtra);
+            const int s = C::mma_of(warp);
+            int seg = 0, slot = s, turn = 0, held = 0;  // turn: parity of the ring's round; held: the slot whose values
+            bool ok = true, behind = false;             // are still to come, if behind
+            auto values = [&](int n) {  // O_s += P_s V of the stream's n-th tile
+                if (!warp_wait(&bars->pfull[s], (uint32_t)(n & 1))) return false;
+                tc_fence_after();
+                const uint32_t vd = v_lo + ((base + C::kRing + (uint32_t)held * (2 * C::kTile) + C::kTile) >> 4);
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k)
+                    mma_elect_ts(tm + s * DP, tm + C::kColP + (2 * s + (n & 1)) * (KT / 2) + 8 * k, vd + k * (2048 >> 4), v_hi, idesc_o,
+                                 1u);
+                commit_elect(&bars->empty[held]);
+                commit_elect(&bars->pvdone[s]);
+                return true;
+            };
+            for (int unit = 0; ok && __shfl_sync(0xffffffffu, !w.done(), 0); ++unit) {
+                const int qb = seg % C::kQBufs;
+                if ((!behind && !warp_wait(&bars->qfull[qb], (uint32_t)((seg / C::kQBufs) & 1))) ||  // an item's first tile
+                    !warp_wait(&bars->full[slot], (uint32_t)turn) ||
+                    (unit > 0 && !warp_wait(&bars->sfree[s], (uint32_t)((unit - 1) & 1))))
+                    break;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the loaders' copies, to the MMA
+                tc_fence_after();
+                const uint32_t qd = k_lo + ((base + (uint32_t)qb * C::kQ) >> 4);
+                const uint32_t kd = k_lo + ((base + C::kRing + (uint32_t)slot * (2 * C::kTile)) >> 4);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    mma_elect_ss(tm + C::kColS + s * KT, qd + (k >> 2) * (kTcRowTile * 128 >> 4) + 2 * (k & 3), k_hi,
+                                 kd + (k >> 2) * (KT * 128 >> 4) + 2 * (k & 3), k_hi, idesc_s, k > 0 ? 1u : 0u);
+                commit_elect(&bars->sfull[s]);
+                if (behind && !values(unit - 1)) break;
+                held = slot;
+                slot += NS;
+                if (slot >= C::kSlots) {
+                    slot -= C::kSlots;
+                    turn ^= 1;
+                }
+                // An item's last values do not wait for the next item's keys.
+                const bool end = __shfl_sync(0xffffffffu, w.kt + 1 == w.kts || w.left == 1, 0);
+                if (end) {
+                    commit_elect(&bars->qempty[qb]);
+                    ++seg;
+                    ok = values(unit);
+                }
+                behind = !end;
+                walk_next(a, w, kTcRowTile, C::kUnit);
+            }
+            commit_elect(&bars->drain[s]);  // everything issued has completed before tensor memory is freed
+            mbar_wait_bounded(&bars->drain[s], 0, status, limit_ns);
+            __syncwarp();
         }
-        commit_elect(&bars->drain[s]);  // everything issued has completed before tensor memory is freed
-        mbar_wait_bounded(&bars->drain[s], 0, status, limit_ns);
-        __syncwarp();
-    }
     } else {
         // ---------------------------------------------------------------- softmax
         if constexpr (C::kDealRegisters) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegisters));

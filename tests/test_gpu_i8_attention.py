@@ -166,7 +166,7 @@ def test_magnitudes_of_keys_and_queries(dtype, max_new):
         check(c, lens, offsets, scale=0.1 / std, max_new=max_new)
 
 
-@pytest.mark.parametrize("G,max_new", [(4, 1), (32, 4)])
+@pytest.mark.parametrize("G,max_new", [(4, 1), (5, 3), (32, 4)])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_what_is_hidden_does_not_touch_a_row(dtype, G, max_new):
     """Keys and values behind a row's last one, before its window, behind the request's end and in other pages, set to the
@@ -256,9 +256,43 @@ def test_queries_at_any_element(dtype):
     c, lens, offsets = make_case([100, 40], [7, 2], 32, 1, 64, 16, 16, dtype, 3, q_shift=5)
     check(c, lens, offsets)
     check(c, lens, offsets, max_new=7)
+    c, lens, offsets = make_case([100, 40], [1, 2], 6, 2, 80, 16, 16, dtype, 3, q_shift=3)
+    check(c, lens, offsets)
 
 
-@pytest.mark.parametrize("G,max_new", [(4, 1), (32, 5)])
+@pytest.mark.parametrize("G,max_new", [(8, 1), (6, 3), (40, 2)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_query_that_is_not_finite_stays_in_its_row(dtype, G, max_new):
+    n = max_new
+    c, lens, offsets = make_case([300, 45], [n, 1], G, 1, 128, 16, 4, dtype, 6)
+    ref, ref_lse, _ = attend(c, max_new=max_new)
+    for bad in (math.nan, math.inf, -math.inf):
+        c["q"][0, 2, 5] = bad
+        out, lse, ws = attend(c, max_new=max_new)
+        others = torch.ones(ref_lse.shape, dtype=torch.bool, device="cuda")
+        others[0, 2] = False
+        assert status(ws) == 0 and not torch.isfinite(out[0, 2].float()).all()
+        assert torch.equal(out[others], ref[others]) and torch.equal(lse[others], ref_lse[others])
+
+
+@pytest.mark.parametrize("G,max_new", [(8, 1), (12, 1), (40, 1)])
+def test_pools_past_32_bits(G, max_new):
+    """Pages whose offsets in bytes do not fit 32 bits (pools of 4.4 GB): the same bits as from a small pool."""
+    page, D = 128, 256
+    P = (1 << 32) // (page * D) + 3000
+    c, lens, offsets = make_case([700, 90], [1, 1], G, 1, D, page, 64, torch.bfloat16, 4)
+    ref, ref_lse, _ = attend(c, max_new=max_new)
+    small = c["codes"][0].shape[0]
+    big = [torch.empty((P, page, 1, D), dtype=torch.int8, device="cuda") for _ in range(2)]
+    exps = [torch.zeros((P, 1, 2), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for x, y in zip((*big, *exps), (*c["codes"], *c["exps"])):
+        x[P - small:] = y
+    table = torch.where(c["table"] >= 0, c["table"] + (P - small), c["table"])
+    out, lse, ws = attend({**c, "codes": big, "exps": exps, "table": table}, max_new=max_new)
+    assert status(ws) == 0 and torch.equal(out, ref) and torch.equal(lse, ref_lse)
+
+
+@pytest.mark.parametrize("G,max_new", [(4, 1), (5, 4), (32, 5)])
 def test_other_stream_and_graph(G, max_new):
     """On a side stream, and replayed from a graph after the lengths, the codes and the scales changed."""
     c, lens, offsets = make_case([700, 200, 64], [1, 5 if max_new > 1 else 1, 1], G, 1, 128, 16, 8, torch.bfloat16, 12)

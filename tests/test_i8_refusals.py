@@ -67,8 +67,9 @@ def test_addresses(L):
     args = list(good)
     args[3] = args[2]  # keys and values into one pool
     assert L.dspark_cache_append_i8(C.byref(p), C.byref(x), *args) == 1
-    y = exps(v=0x900000)
-    assert L.dspark_cache_append_i8(C.byref(p), C.byref(y), *good) == 1
+    for kw in ({"v": 0x900000}, {"page_stride": 0}, {"block_stride": 0}, {"head_stride": 0}):  # exponents that two blocks share
+        y = exps(**kw)
+        assert L.dspark_cache_append_i8(C.byref(p), C.byref(y), *good) == 1
     for i in range(5):
         args = [A[2], A[3], A[4], A[0], A[1], None]
         args[i] = None
