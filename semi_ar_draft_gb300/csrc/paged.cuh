@@ -345,6 +345,36 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 
 
+// The lanes of a row (LANES neighbours, each with eight of its values) make halves of a query for an int8 cache: bf16 times
+// the power of two 2^raise that brings the row's largest value to 2^14, which is taken back in the scores' scale; what a half
+// then cannot hold is below 2^-38 of the row's largest, less than fp32 keeps of the sum.  Returns raise; sum is the
+// halves' over the row.  By whole warps.
+template <bool BF16, int LANES>
+__device__ __forceinline__ int query_halves(uint32_t (&y)[4], float& sum) {
+    int raise = 0;
+    if (BF16) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(y[e] & 0x7fffu, (y[e] >> 16) & 0x7fffu));
+#pragma unroll
+        for (int d = 1; d < LANES; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const int e = (int)(top >> 7) - 127;  // floor(log2) of a normal number
+        raise = e > -127 && e < 128 ? min(max(14 - e, -120), 120) : 0;
+        const float up = two_to(raise);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = pack16<false>(bf16_lo(y[i]) * up, bf16_hi(y[i]) * up);
+    }
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
+        sum += f.x + f.y;
+    }
+#pragma unroll
+    for (int d = 1; d < LANES; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    return raise;
+}
+
 // Row tiles of 128 on the fifth-generation tensor cores (paged_attn_tc.cu); needs 16-byte
 // aligned query rows.
 dspark_status launch_attn_tc(const AttnArgs& a, bool bf16, int kv, int sms, cudaStream_t s, int* parts);

@@ -836,7 +836,8 @@ dspark_status paged_attention(const dspark_attention_params* p, const dspark_blo
     note_launch();
     const int row_tile = tc ? kTcRows : (few ? 8 : kRows), heads = few ? i8_head_group(p->D, p->Hk) : 1;
     // The join's blocks become resident as the attention kernel's leave.
-    const dim3 grid(parts, 8), block(32 * kJoinWarps);
+    // (Few rows an item want few of them: 456 parts, 2 blocks each against 8: 57.7 against 59.6 us for 32 requests.)
+    const dim3 grid(parts, kv == kKvI8 && !tc ? 2 : 8), block(32 * kJoinWarps);
     const cudaError_t e = bf16 ? launch_overlapped(attn_join_kernel<true>, grid, block, 0, s, a, row_tile, heads, parts)
                                : launch_overlapped(attn_join_kernel<false>, grid, block, 0, s, a, row_tile, heads, parts);
     if (e != cudaSuccess) return DSPARK_ERR_CUDA;

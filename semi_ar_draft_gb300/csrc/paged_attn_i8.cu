@@ -76,9 +76,8 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
     __shared__ float2 s_ml[kWarps][kRows];
     __shared__ int s_err;
     __shared__ AttnScratch s_start;
-    __shared__ uint32_t s_qmax[HG * kRows];        // largest |q| of each row (its bits); rows of the first head, the second, ...
-    __shared__ float s_qsum[HG * kRows][DP / 8];  // sums of a row's query, eight values each
-    __shared__ __align__(8) float s_base[HG * kRows], s_scale[HG * kRows];  // where a row's products begin, its scores' factor
+    // where a row's products begin, its scores' factor: rows of the first head, of the second, ...
+    __shared__ __align__(8) float s_base[HG * kRows], s_scale[HG * kRows];
     __shared__ AttnStart s_range;                    // the block's units
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -88,7 +87,7 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
     launch_dependents();
     if (tid == 0) s_err = 0;
     bool bad;
-    const AttnStart start = attn_start<kThreads>(a, kRows, C::kKeyTile, C::kExtra, parts, part, 1 + C::kExtra, &s_start, &bad);
+    const AttnStart start = attn_start<kThreads>(a, kRows, C::kKeyTile, C::kExtra, parts, part, 1, &s_start, &bad);
 
     attn_tail_rows(a, (size_t)part * kThreads + tid, (size_t)parts * kThreads);
     unsigned char* ring = smem + (size_t)warp * C::kStages * C::kStage;
@@ -197,82 +196,44 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
             all_hi = attn_see_hi(a, w.r, attn_token(a, row0));
             // The queries, through shared memory: 16 bytes a thread, then fragments by ldmatrix.  (The previous segment's
             // readers are past its last barrier.)
-            constexpr int kQc = DP / 8;
+            constexpr int kQc = DP / 8;  // threads of a row
             constexpr int kQRows = HG * kRows, kQSteps = (kQRows * kQc + kThreads - 1) / kThreads;
-            uint4 qv[kQSteps];
-            if (BF16) {
-                if (tid < kQRows) s_qmax[tid] = 0;
-                __syncthreads();
-            }
 #pragma unroll
             for (int u = 0; u < kQSteps; ++u) {
                 const int qrow = (tid + u * kThreads) / kQc, c = (tid + u * kThreads) % kQc;
+                if (kQRows * kQc % kThreads && qrow >= kQRows) break;  // (whole warps)
                 const int row = qrow % kRows, head = group * HG + qrow / kRows, token = attn_token(a, row0 + row);
-                qv[u] = make_uint4(0, 0, 0, 0);
-                if (kQRows * kQc % kThreads && qrow >= kQRows) continue;
+                uint32_t y[4] = {0, 0, 0, 0};
                 if (row < rows && 8 * c < a.D) {
                     const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (w.r.token0 + token) * a.q_token +
                                           (head * a.G + row0 + row - token * a.G) * a.q_head + 8 * c;
                     if (a.q_vec) {
-                        qv[u] = __ldg(reinterpret_cast<const uint4*>(src));
+                        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src));
+                        y[0] = q.x, y[1] = q.y, y[2] = q.z, y[3] = q.w;
                     } else {  // rows may start at any element
-                        uint32_t* y = reinterpret_cast<uint32_t*>(&qv[u]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) y[e] = (uint32_t)__ldg(src + 2 * e) | ((uint32_t)__ldg(src + 2 * e + 1) << 16);
                     }
                 }
-                if (BF16) {
-                    float big = 0.f;
-                    const uint32_t* y = reinterpret_cast<const uint32_t*>(&qv[u]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) big = fmaxf(big, fmaxf(fabsf(bf16_lo(y[e])), fabsf(bf16_hi(y[e]))));
-                    atomicMax(&s_qmax[qrow], __float_as_uint(big));
-                }
-            }
-            // bf16 queries as halves: each row times the power of two that brings its largest value to 2^14, taken back
-            // in the scores' scale; what a half then cannot hold is below 2^-38 of the row's largest, less than fp32
-            // keeps of the sum.
-            auto raise = [&](int qrow) {
-                const int e = (int)(s_qmax[qrow] >> 23) - 127;  // floor(log2) of a normal number
-                return e > -127 && e < 128 ? min(max(14 - e, -120), 120) : 0;
-            };
-            if (BF16) __syncthreads();
-#pragma unroll
-            for (int u = 0; u < kQSteps; ++u) {
-                const int qrow = (tid + u * kThreads) / kQc, c = (tid + u * kThreads) % kQc;
-                if (kQRows * kQc % kThreads && qrow >= kQRows) continue;
+                float sum;
+                const int raise = query_halves<BF16, kQc>(y, sum);
                 // Codes arrive four k a lane and are taken apart by even and odd bytes: the MMA's k slots 2t, 2t + 1 hold
                 // k = 4t, 4t + 2 and its slots 2t + 8, 2t + 9 hold k = 4t + 1, 4t + 3.
-                uint32_t* y = reinterpret_cast<uint32_t*>(&qv[u]);
-                const float up = BF16 ? two_to(raise(qrow)) : 1.f;
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (BF16) y[e] = pack16<false>(bf16_lo(y[e]) * up, bf16_hi(y[e]) * up);
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[e]));
-                    sum += f.x + f.y;
-                }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int at = 4 * (e + 2 * (c & 1));
                     *reinterpret_cast<uint32_t*>(qs + C::q_at(qrow, c & ~1) + at) = __byte_perm(y[2 * e], y[2 * e + 1], 0x5410);
                     *reinterpret_cast<uint32_t*>(qs + C::q_at(qrow, c | 1) + at) = __byte_perm(y[2 * e], y[2 * e + 1], 0x7632);
                 }
-                s_qsum[qrow][c] = sum;
+                if (c == 0) {
+                    s_base[qrow] = -128.f * 0x1p-24f * sum;
+                    // to the log2 domain, or to the cap's exponent
+                    s_scale[qrow] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale * 0x1p24f * two_to(-raise);
+                }
             }
             __syncthreads();
             ref[0] = ref[1] = ref_v[0] = ref_v[1] = kNone;
             sums = 0;
-            if (tid < kQRows) {
-                float sum = 0.f;
-#pragma unroll 4
-                for (int i = 0; i < DP / 8; ++i) sum += s_qsum[tid][i];
-                s_base[tid] = -128.f * 0x1p-24f * sum;
-                // to the log2 domain, or to the cap's exponent
-                s_scale[tid] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale * 0x1p24f *
-                               (BF16 ? two_to(-raise(tid)) : 1.f);
-            }
-            __syncthreads();
             if (!C::kQInSmem) {
 #pragma unroll
                 for (int ks = 0; ks < KS; ks += 2) {

@@ -75,7 +75,6 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
     __shared__ float s_sum[kWarps][kRows];
     __shared__ int s_err;
     __shared__ AttnScratch s_start;
-    __shared__ uint32_t s_qmax[kRows];                 // largest |q| of each row (its bits)
     __shared__ __align__(8) float s_base[kRows], s_scale[kRows];  // where a row's products begin, its scores' factor
     __shared__ AttnStart s_range;                     // the block's units
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -85,7 +84,7 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
     launch_dependents();
     if (tid == 0) s_err = 0;
     bool bad;
-    const AttnStart start = attn_start<kThreads>(a, kRows, C::kKeyTile, C::kExtra, parts, part, 1 + C::kExtra, &s_start, &bad);
+    const AttnStart start = attn_start<kThreads>(a, kRows, C::kKeyTile, C::kExtra, parts, part, 1, &s_start, &bad);
 
     attn_tail_rows(a, (size_t)part * kThreads + tid, (size_t)parts * kThreads);
     const uint32_t ring = smem_addr(smem);
@@ -171,58 +170,26 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
             all_hi = attn_see_hi(a, w.r, attn_token(a, row0));
             // The queries, through shared memory: 16 bytes a thread, then fragments by ldmatrix.  (The previous segment's
             // readers are past its last barrier.)
-            constexpr int kQc = DP / 8;
+            constexpr int kQc = DP / 8;  // threads of a row
             constexpr int kQSteps = kRows * kQc / kThreads;
             static_assert(kRows * kQc % kThreads == 0, "whole steps");
-            auto query = [&](int i) {  // the i-th eight values of the tile's queries
-                const int row = i / kQc, c = i % kQc, token = attn_token(a, row0 + row);
-                uint4 q = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < kQSteps; ++u) {
+                const int row = (tid + u * kThreads) / kQc, c = (tid + u * kThreads) % kQc, token = attn_token(a, row0 + row);
+                uint32_t y[4] = {0, 0, 0, 0};
                 if (row < rows && 8 * c < a.D) {
                     const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (w.r.token0 + token) * a.q_token +
                                           (head * a.G + row0 + row - token * a.G) * a.q_head + 8 * c;
                     if (a.q_vec) {
-                        q = __ldg(reinterpret_cast<const uint4*>(src));
+                        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src));
+                        y[0] = q.x, y[1] = q.y, y[2] = q.z, y[3] = q.w;
                     } else {  // rows may start at any element
-                        uint32_t* y = reinterpret_cast<uint32_t*>(&q);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) y[e] = (uint32_t)__ldg(src + 2 * e) | ((uint32_t)__ldg(src + 2 * e + 1) << 16);
                     }
                 }
-                return q;
-            };
-            if (BF16) {
-                for (int i = tid; i < kRows; i += kThreads) s_qmax[i] = 0;
-                __syncthreads();
-#pragma unroll 4
-                for (int u = 0; u < kQSteps; ++u) {
-                    const uint4 q = query(tid + u * kThreads);
-                    const uint32_t y[4] = {q.x, q.y, q.z, q.w};
-                    float big = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) big = fmaxf(big, fmaxf(fabsf(bf16_lo(y[e])), fabsf(bf16_hi(y[e]))));
-                    atomicMax(&s_qmax[(tid + u * kThreads) / kQc], __float_as_uint(big));
-                }
-                __syncthreads();
-            }
-            // bf16 queries as halves: each row times the power of two that brings its largest value to 2^14 (as in
-            // paged_attn_i8.cu); the second look finds them in L1.
-            auto raise = [&](int row) {
-                const int e = (int)(s_qmax[row] >> 23) - 127;  // floor(log2) of a normal number
-                return e > -127 && e < 128 ? min(max(14 - e, -120), 120) : 0;
-            };
-#pragma unroll 4
-            for (int u = 0; u < kQSteps; ++u) {
-                const int row = (tid + u * kThreads) / kQc, c = (tid + u * kThreads) % kQc;
-                const uint4 q = query(tid + u * kThreads);
-                uint32_t y[4] = {q.x, q.y, q.z, q.w};
-                const float up = BF16 ? two_to(raise(row)) : 1.f;
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (BF16) y[e] = pack16<false>(bf16_lo(y[e]) * up, bf16_hi(y[e]) * up);
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[e]));
-                    sum += f.x + f.y;
-                }
+                float sum;
+                const int raise = query_halves<BF16, kQc>(y, sum);
                 // the MMA's k slots 2t, 2t + 1 hold k = 4t, 4t + 2 and its slots 2t + 8, 2t + 9 hold k = 4t + 1, 4t + 3
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -230,14 +197,10 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
                     *reinterpret_cast<uint32_t*>(qs + C::q_at(row, c & ~1) + at) = __byte_perm(y[2 * e], y[2 * e + 1], 0x5410);
                     *reinterpret_cast<uint32_t*>(qs + C::q_at(row, c | 1) + at) = __byte_perm(y[2 * e], y[2 * e + 1], 0x7632);
                 }
-                // the row's sum, from the lanes that hold it
-#pragma unroll
-                for (int d = 1; d < kQc; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 if (c == 0) {
                     s_base[row] = -128.f * 0x1p-24f * sum;
                     // to the log2 domain, or to the cap's exponent
-                    s_scale[row] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale * 0x1p24f *
-                                   (BF16 ? two_to(-raise(row)) : 1.f);
+                    s_scale[row] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale * 0x1p24f * two_to(-raise);
                 }
             }
             __syncthreads();
