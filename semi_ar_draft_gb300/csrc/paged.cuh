@@ -318,11 +318,8 @@ __device__ __forceinline__ uint32_t i8x2_to_half2(uint32_t offset_word) {  // th
 }
 constexpr int kBytes01 = 0x4140, kBytes23 = 0x4342, kBytes02 = 0x4240, kBytes13 = 0x4341;
 
-// Where the exponents of a key's block lie: at is its place in the page.  (Both bytes are kept as they arrive until they
-// are used: putting them together at once would wait for them.)
-__device__ __forceinline__ long long exponents_at(const AttnArgs& a, int page, int at, int head) {
-    return page * a.exp.page + (long long)(at >> a.exp.shift) * a.exp.block + head * a.exp.head;
-}
+// An int8 cache's offset of a key (in 32 bits: Steps32) that is not there.
+constexpr uint32_t kNoKey = 0xffffffffu;
 
 // Probabilities as halves are taken against a reference 2^7 below the running maximum's (which follows within 2^8, so
 // they stay below 2^15): halves lose bits below 2^-14, which is then 2^-21 of the largest.  bf16 has fp32's exponents.

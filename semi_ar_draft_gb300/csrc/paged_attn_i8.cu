@@ -54,7 +54,6 @@ struct SliceI8 {
     }
 };
 
-constexpr uint32_t kNoKey = 0xffffffffu;
 
 __device__ __forceinline__ void copy16_all(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");

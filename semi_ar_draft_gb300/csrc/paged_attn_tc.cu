@@ -54,12 +54,13 @@ struct TcAttn {
     static constexpr int kTileLoaders = kLoaders / kStreams;
     // Warps after the softmax's: multiprocessor quarter (warp % 4) 0 has none of them and quarter 1 the MMA
     // warps, one a stream; the loaders are in quarters 2 and 3.  Short row tiles keep quarter 0 busiest.
-    // (int8: the other two loaders in quarters 1 and 0.)
+    // (int8: two loaders a quarter, one of each stream, since three that widen at once wait for the quarter's integer unit;
+    // the second stream's MMA warp makes room in quarter 1.)
     static constexpr int kWarps = kSoftmaxWarps + (KV == kKvI8 ? 12 : 8);
     static __device__ __forceinline__ int loader_of(int warp) {  // 0 .. kLoaders - 1, or -1
         const int h = warp - kSoftmaxWarps;
-        if (h >= 0 && (h & 2)) return (h >> 2) * 2 + (h & 1);
-        return KV == kKvI8 && (h == 8 || h == 9) ? h - 2 : -1;
+        if (KV == kKvI8) return h < 0 || h == 1 || h == 8 || h > 9 ? -1 : (h == 5 ? 1 : (h == 9 ? 5 : h));
+        return h >= 0 && (h & 2) ? (h >> 2) * 2 + (h & 1) : -1;
     }
     // Twenty warps are launched with 96 registers a thread (61440), which is too little for the softmax and more than the
     // others need: whole warpgroups give and take (the softmax's warps come first).
@@ -68,7 +69,7 @@ struct TcAttn {
     static_assert(!kDealRegisters || 32 * (kSoftmaxWarps * kSoftmaxRegisters + 12 * kHelperRegisters) <= 32 * 20 * 96, "the launch's registers");
     static __device__ __forceinline__ int mma_of(int warp) {  // the stream, or -1
         const int h = warp - kSoftmaxWarps;
-        return h == 1 ? 0 : (h == 5 && kStreams == 2 ? 1 : -1);
+        return h == 1 ? 0 : (h == (KV == kKvI8 ? 8 : 5) && kStreams == 2 ? 1 : -1);
     }
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSub = DP / 64;                  // 64-value groups of a row
@@ -163,22 +164,26 @@ __device__ __forceinline__ void widen16(const uint4 v, uint4& lo, uint4& hi) {
     hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// Sixteen int8 codes times `scale` (twice 2^e in the 16-bit type, which holds the products exactly), in order.  bf16: the
-// byte's low seven bits beside the exponent of 2^7 are 128 + them, from which 128 is taken, or 256 where bit 7 is set.
+// Sixteen int8 codes times `scale` (twice 2^e in the 16-bit type, which holds the products exactly), in order.
+// bf16: the byte of code + 128 beside the exponent of 2^7 reads 256 + code where the code is negative and, bit 7 being the
+// exponent's last, 256 + 2 code where it is not.  Half of that less 128, y, is code / 2 or code, and 2 y - max(y, 0) is the
+// code.  What is returned is that with its sign changed, one instruction less, which the MMAs undo (kNegateB).  Measured, 512
+// requests of 34 rows on average: 581 us with the sign bit taken out first, 545 so, 528 with the sign left to the MMAs.
 template <bool BF16>
 __device__ __forceinline__ void widen16_i8(const uint4 v, uint32_t scale, uint4& lo, uint4& hi) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t minus_twice = scale + 0x80808080u;  // (bf16: -2^(e + 1))
     uint32_t r[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+        const uint32_t u = w[i >> 1] ^ 0x80808080u;
         if (BF16) {
-            const uint32_t x = __byte_perm(w[i >> 1], 0, i & 1 ? 0x4342 : 0x4140);
-            const uint32_t a = (x & 0x007f007fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
-            __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-            y = __hmul2(y, *reinterpret_cast<const __nv_bfloat162*>(&scale));
-            r[i] = *reinterpret_cast<const uint32_t*>(&y);
+            const uint32_t x = __byte_perm(u, 0x43434343u, i & 1 ? 0x4342 : 0x4140);
+            uint32_t y, z;
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0x3f003f00u), "r"(0xc300c300u));
+            asm("fma.rn.relu.bf16x2 %0, %1, %2, %3;" : "=r"(z) : "r"(y), "r"(scale), "r"(0u));
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r[i]) : "r"(y), "r"(minus_twice), "r"(z));
         } else {
-            const uint32_t u = w[i >> 1] ^ 0x80808080u;
             const uint32_t h = i & 1 ? i8x2_to_half2<kBytes23>(u) : i8x2_to_half2<kBytes01>(u);
             asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(h), "r"(scale));
         }
@@ -294,144 +299,155 @@ __global__ void __launch_bounds__(TcAttn<KV, DP>::kThreads, 1) attn_tc_kernel(At
     PartItem* mine = a.items + part;  // written by thread 0
     if (tid == 0) mine->d[kTail].first = mine->d[kHead].first = -1;
 
-    // (The register counts change inside the branches: the compiler goes by that.)
-    if (warp >= C::kSoftmaxWarps) {
-        if constexpr (C::kDealRegisters) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kHelperRegisters));
-        if (C::loader_of(warp) >= 0) {
-            // ---------------------------------------------------------------- loaders
-            constexpr int kChunks = DP / (F8 ? 16 : 8);  // 16-byte groups of a row in the cache
-            constexpr int kPer = 32 / kChunks;           // rows a warp copies at a time
-            const int lw = C::loader_of(warp);
-            const int chunk = lane % kChunks, sub_row = lane / kChunks;
-            const bool inside = chunk * (F8 ? 16 : 8) < a.D;
-            const uint32_t base = smem_addr(smem);
-            const uint32_t mask = (1u << a.page_shift) - 1;
-            const uint32_t page16 = (uint32_t)(a.page >> 4), token16 = (uint32_t)(a.token >> 4);
-            const unsigned char* k_at = a.k_pages + chunk * 16;
-            const long long v_after_k = a.v_pages - a.k_pages;
-            AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit, C::kExtra);
-            int err = 0, seg = 0;
-            // This warp's keys of its stream's tiles.
-            constexpr int kKeys = KT / C::kTileLoaders;
-            const int first_key = (lw / C::kTileLoaders) * KT + (lw % C::kTileLoaders) * kKeys;
-            auto tile_key = [&]() { return (w.kt_first + w.kt) * C::kUnit + first_key; };
-            // Page of this lane's key of the next tile, asked for a tile ahead.  The load is unconditional (entry 0
-            // where there is no key) and looked at when the copies are issued, so that nothing waits for it here.
-            int pid;
-            auto fetch_pages = [&]() {
-                const int key = min(tile_key() + lane, w.r.seq - 1);
-                const size_t at = w.done() || key < 0 ? 0 : (size_t)w.j * a.max_blocks + (key >> a.page_shift);
-                pid = __ldg(a.block_table + at);
-            };
-            fetch_pages();
-            bool fresh = true;
-            int head = 0, slot = lw / C::kTileLoaders, round = 0;
-            const int tile_row = (lw % C::kTileLoaders) * kKeys + sub_row;
-            // 8-bit caches: a tile arrives as it is, each lane's pieces in places of its own, `ahead` tiles at a time; the
-            // lane that copied a piece widens it into the slot, keys to q's type, values to halves (int8: q's type), all exact.
-            constexpr int kSteps = kKeys / kPer;
-            int raw_slot = 0, raw_old = 0, ahead = 0;
-            uint32_t k_exp[I8 ? C::kRawSlots : 1], v_exp[I8 ? C::kRawSlots : 1];  // of this lane's key of the raw tiles
-            unsigned char* raw = smem + C::kRaw + lw * (C::kRawSlots * C::kRawTile) + lane * 16;
-            auto widen = [&]() {
-                if (round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) return false;
-                unsigned char* to = smem + C::kRing + slot * (2 * C::kTile) + ((2 * chunk) >> 3) * (KT * 128);
-                const unsigned char* from = raw + raw_old * C::kRawTile;
-                uint32_t e = 0;
-                if (I8) {
+    // ---------------------------------------------------------------- loaders
+    auto load = [&]() {
+        constexpr int kChunks = DP / (F8 ? 16 : 8);  // 16-byte groups of a row in the cache
+        constexpr int kPer = 32 / kChunks;           // rows a warp copies at a time
+        const int lw = C::loader_of(warp);
+        // (8-bit: four groups of two rows to eight lanes, whose widened 16-byte stores then fall into different banks.)
+        const int chunk = F8 ? (lane & 3) | ((lane >> 3) << 2 & (kChunks - 1)) : lane % kChunks;
+        const int sub_row = F8 ? (lane >> 2 & 1) | (lane >> 3) / (kChunks / 4) << 1 : lane / kChunks;
+        const bool inside = chunk * (F8 ? 16 : 8) < a.D;
+        const uint32_t base = smem_addr(smem);
+        const uint32_t mask = (1u << a.page_shift) - 1;
+        const uint32_t page16 = (uint32_t)(a.page >> 4), token16 = (uint32_t)(a.token >> 4);
+        const unsigned char* k_at = a.k_pages + (inside ? chunk * 16 : 0);
+        const long long v_after_k = a.v_pages - a.k_pages;
+        AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit, C::kExtra);
+        int err = 0, seg = 0;
+        // This warp's keys of its stream's tiles.
+        constexpr int kKeys = KT / C::kTileLoaders;
+        const int first_key = (lw / C::kTileLoaders) * KT + (lw % C::kTileLoaders) * kKeys;
+        auto tile_key = [&]() { return (w.kt_first + w.kt) * C::kUnit + first_key; };
+        // Page of this lane's key of the next tile, asked for a tile ahead.  The load is unconditional (entry 0
+        // where there is no key) and looked at when the copies are issued, so that nothing waits for it here.
+        int pid;
+        auto fetch_pages = [&]() {
+            const int key = min(tile_key() + lane, w.r.seq - 1);
+            const size_t at = w.done() || key < 0 ? 0 : (size_t)w.j * a.max_blocks + (key >> a.page_shift);
+            pid = __ldg(a.block_table + at);
+        };
+        fetch_pages();
+        bool fresh = true;
+        int head = 0, slot = lw / C::kTileLoaders, round = 0;
+        const int tile_row = (lw % C::kTileLoaders) * kKeys + sub_row;
+        // 8-bit caches: a tile arrives as it is, each lane's pieces in places of its own, `ahead` tiles at a time; the
+        // lane that copied a piece widens it into the slot, keys to q's type, values to halves (int8: q's type), all exact.
+        constexpr int kSteps = kKeys / kPer;
+        int raw_slot = 0, raw_old = 0, ahead = 0;
+        uint32_t k_exp[I8 ? C::kRawSlots : 1], v_exp[I8 ? C::kRawSlots : 1];  // of this lane's key of the raw tiles
+        unsigned char* raw = smem + C::kRaw + lw * (C::kRawSlots * C::kRawTile) + lane * 16;
+        auto widen = [&]() {
+            if (round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) return false;
+            unsigned char* to = smem + C::kRing + slot * (2 * C::kTile) + ((2 * chunk) >> 3) * (KT * 128);
+            const unsigned char* from = raw + raw_old * C::kRawTile;
+            uint32_t k_two = 0, v_two = 0;  // (of this lane's key)
+            if (I8) {
+                uint32_t ke = 0, ve = 0;
 #pragma unroll
-                    for (int i = 0; i < C::kRawSlots; ++i)
-                        if (raw_old == i) e = k_exp[I8 ? i : 0] | v_exp[I8 ? i : 0] << 8;
-                }
+                for (int i = 0; i < C::kRawSlots; ++i)
+                    if (raw_old == i) ke = k_exp[I8 ? i : 0], ve = v_exp[I8 ? i : 0];
+                k_two = scale_pair<BF16>(exponent_of<BF16>(ke));
+                v_two = scale_pair<BF16>(exponent_of<BF16>(ve));
+            }
 #pragma unroll 2
-                for (int u = 0; u < kSteps; ++u) {
-                    const uint32_t at0 = sw128_offset(tile_row + u * kPer, (2 * chunk) & 7);
-                    const uint32_t at1 = sw128_offset(tile_row + u * kPer, (2 * chunk + 1) & 7);
-                    const uint4 k = *reinterpret_cast<const uint4*>(from + 2 * u * 512);
-                    const uint4 v = *reinterpret_cast<const uint4*>(from + (2 * u + 1) * 512);
-                    uint4 x, y;
-                    uint32_t with = 0;
-                    if (I8) {
-                        with = __shfl_sync(0xffffffffu, e, u * kPer + sub_row);
-                        widen16_i8<BF16>(k, scale_pair<BF16>(exponent_of<BF16>(with & 0xffu)), x, y);
-                    } else {
-                        widen16<BF16>(k, x, y);
-                    }
-                    *reinterpret_cast<uint4*>(to + at0) = x;
-                    *reinterpret_cast<uint4*>(to + at1) = y;
-                    if (I8)
-                        widen16_i8<BF16>(v, scale_pair<BF16>(exponent_of<BF16>(with >> 8)), x, y);
-                    else
-                        widen16<false>(v, x, y);
-                    *reinterpret_cast<uint4*>(to + at0 + C::kTile) = x;
-                    *reinterpret_cast<uint4*>(to + at1 + C::kTile) = y;
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive_local(&bars->full[slot]);
-                slot += NS;
-                if (slot >= C::kSlots) {
-                    slot -= C::kSlots;
-                    ++round;
-                }
-                if (++raw_old == C::kRawSlots) raw_old = 0;
-                return true;
-            };
-            // An item's queries: with two streams after its first keys, since their buffer is free later than a
-            // slot (421 against 426 us for the 512-request verify); with heads of 256, where they are as large as two
-            // tiles, before (122 against 131 us for three long contexts, with a softcap 8 us cheaper than now).
-            constexpr bool kQueriesFirst = NS == 1;
-            auto queries = [&]() {
-                const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
-                if (F8 && use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1)))) {
-                    // the products that still read it may be waiting for raw tiles
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    while (ahead > 0 && widen()) --ahead;
-                }
-                if (use > 0 && !warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) return false;
-                ++seg;
-                const int row0 = (w.item - head * w.rts) * kTcRowTile;
-                const int rows = min(w.r.n * a.G - row0, kTcRowTile);
-                constexpr int kQPer = 256 / DP;  // rows a warp copies at a time
-                const int qc = lane % (DP / 8);
-                const uint32_t qbase = base + (uint32_t)qb * C::kQ + (uint32_t)(qc >> 3) * (kTcRowTile * 128);
-                for (int r = lw * kQPer + lane / (DP / 8); r < ((rows + 31) & ~31); r += C::kLoaders * kQPer) {
-                    const bool real = qc * 8 < a.D && r < rows;
-                    const int row = row0 + r;
-                    const int token = attn_token(a, row);
-                    const long long src = real ? (w.r.token0 + token) * a.q_token +
-                                                     (head * a.G + row - token * a.G) * a.q_head + qc * 8
-                                               : 0;
-                    copy16(qbase + sw128_offset(r, qc & 7), a.q + 2 * src, real);
-                }
-                copy_arrive(&bars->qfull[qb]);
-                return true;
-            };
-            while (!w.done()) {
-                if (fresh) {
-                    head = w.item / w.rts;
-                    if (kQueriesFirst && !queries()) break;
-                }
-                if (!F8 && round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) break;
-                const int key0 = tile_key();
-                const unsigned char* head_at = k_at + head * a.head;
-                const bool none = key0 + lane >= w.r.seq || key0 + lane < w.r.lo;
-                if ((uint32_t)pid >= (uint32_t)a.num_pages) {
-                    if (!none && lane < kKeys) err = DSPARK_ERR_CACHE;
-                    pid = -1;
-                }
-                if (none) pid = -1;
-                if (I8) {  // (entry 0 where there is no key, whose codes are zeros)
-                    const long long at = pid >= 0 && lane < kKeys ? exponents_at(a, pid, (key0 + lane) & mask, head) : 0;
+            for (int u = 0; u < kSteps; ++u) {
+                const uint32_t at0 = sw128_offset(tile_row + u * kPer, (2 * chunk) & 7);
+                const uint32_t at1 = sw128_offset(tile_row + u * kPer, (2 * chunk + 1) & 7);
+                const uint4 k = *reinterpret_cast<const uint4*>(from + 2 * u * 512);
+                const uint4 v = *reinterpret_cast<const uint4*>(from + (2 * u + 1) * 512);
+                uint4 x, y;
+                if (I8)
+                    widen16_i8<BF16>(k, __shfl_sync(0xffffffffu, k_two, u * kPer + sub_row), x, y);
+                else
+                    widen16<BF16>(k, x, y);
+                *reinterpret_cast<uint4*>(to + at0) = x;
+                *reinterpret_cast<uint4*>(to + at1) = y;
+                if (I8)
+                    widen16_i8<BF16>(v, __shfl_sync(0xffffffffu, v_two, u * kPer + sub_row), x, y);
+                else
+                    widen16<false>(v, x, y);
+                *reinterpret_cast<uint4*>(to + at0 + C::kTile) = x;
+                *reinterpret_cast<uint4*>(to + at1 + C::kTile) = y;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive_local(&bars->full[slot]);
+            slot += NS;
+            if (slot >= C::kSlots) {
+                slot -= C::kSlots;
+                ++round;
+            }
+            if (++raw_old == C::kRawSlots) raw_old = 0;
+            return true;
+        };
+        // An item's queries: with two streams after its first keys, since their buffer is free later than a
+        // slot (421 against 426 us for the 512-request verify); with heads of 256, where they are as large as two
+        // tiles, before (122 against 131 us for three long contexts, with a softcap 8 us cheaper than now).
+        constexpr bool kQueriesFirst = NS == 1;
+        auto queries = [&]() {
+            const int qb = seg % C::kQBufs, use = seg / C::kQBufs;
+            if (F8 && use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1)))) {
+                // the products that still read it may be waiting for raw tiles
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                while (ahead > 0 && widen()) --ahead;
+            }
+            if (use > 0 && !warp_wait(&bars->qempty[qb], (uint32_t)((use - 1) & 1))) return false;
+            ++seg;
+            const int row0 = (w.item - head * w.rts) * kTcRowTile;
+            const int rows = min(w.r.n * a.G - row0, kTcRowTile);
+            constexpr int kQPer = 256 / DP;  // rows a warp copies at a time
+            const int qc = lane % (DP / 8);
+            const uint32_t qbase = base + (uint32_t)qb * C::kQ + (uint32_t)(qc >> 3) * (kTcRowTile * 128);
+            for (int r = lw * kQPer + lane / (DP / 8); r < ((rows + 31) & ~31); r += C::kLoaders * kQPer) {
+                const bool real = qc * 8 < a.D && r < rows;
+                const int row = row0 + r;
+                const int token = attn_token(a, row);
+                const long long src = real ? (w.r.token0 + token) * a.q_token +
+                                                 (head * a.G + row - token * a.G) * a.q_head + qc * 8
+                                           : 0;
+                copy16(qbase + sw128_offset(r, qc & 7), a.q + 2 * src, real);
+            }
+            copy_arrive(&bars->qfull[qb]);
+            return true;
+        };
+        while (!w.done()) {
+            if (fresh) {
+                head = w.item / w.rts;
+                if (kQueriesFirst && !queries()) break;
+            }
+            if (!F8 && round > 0 && !warp_wait(&bars->empty[slot], (uint32_t)((round - 1) & 1))) break;
+            const int key0 = tile_key();
+            const unsigned char* head_at = k_at + head * a.head;
+            const bool none = key0 + lane >= w.r.seq || key0 + lane < w.r.lo;
+            if ((uint32_t)pid >= (uint32_t)a.num_pages) {
+                if (!none && lane < kKeys) err = DSPARK_ERR_CACHE;
+                pid = -1;
+            }
+            if (none) pid = -1;
+            const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + (uint32_t)(chunk >> 3) * (KT * 128);
+            const uint32_t rb = smem_addr(raw) + (uint32_t)(raw_slot * C::kRawTile);
+            if constexpr (I8) {  // (entry 0 where there is no key, whose codes are zeros)
+                const Steps32& by = a.steps;
+                const uint32_t place = (uint32_t)(key0 + lane) & mask;
+                const bool found = pid >= 0 && lane < kKeys;
+                const uint32_t off = found ? pid * by.page + place * by.token + head * by.head : kNoKey;
+                const uint32_t at = found ? pid * by.e_page + (place >> a.exp.shift) * by.e_block + head * by.e_head : 0u;
 #pragma unroll
-                    for (int i = 0; i < C::kRawSlots; ++i)
-                        if (raw_slot == i) {
-                            k_exp[I8 ? i : 0] = __ldg(a.exp.k + at);
-                            v_exp[I8 ? i : 0] = __ldg(a.exp.v + at);
-                        }
+                for (int i = 0; i < C::kRawSlots; ++i)
+                    if (raw_slot == i) {
+                        k_exp[i] = __ldg(a.exp.k + at);
+                        v_exp[i] = __ldg(a.exp.v + at);
+                    }
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const uint32_t o = __shfl_sync(0xffffffffu, off, i * kPer + sub_row);
+                    const bool real = inside && o != kNoKey;
+                    const unsigned char* src = k_at + (uint64_t)(real ? o : 0u) * by.unit;
+                    copy16(rb + i * 1024u, src, real);
+                    copy16(rb + i * 1024u + 512, src + v_after_k, real);
                 }
-                const uint32_t kb = base + C::kRing + (uint32_t)slot * (2 * C::kTile) + (uint32_t)(chunk >> 3) * (KT * 128);
-                const uint32_t rb = smem_addr(raw) + (uint32_t)(raw_slot * C::kRawTile);
-#pragma unroll (I8 ? 2 : 8)
+            } else {
+#pragma unroll 8
                 for (int i = 0; i < kKeys; i += kPer) {
                     const int p = __shfl_sync(0xffffffffu, pid, i + sub_row);
                     const bool real = inside && p >= 0;
@@ -442,102 +458,104 @@ __global__ void __launch_bounds__(TcAttn<KV, DP>::kThreads, 1) attn_tc_kernel(At
                     copy16(dst, src, real);
                     copy16(dst + (F8 ? 512 : C::kTile), src + v_after_k, real);
                 }
-                if constexpr (F8) {
-                    cp_async_commit();
-                    if (++raw_slot == C::kRawSlots) raw_slot = 0;
-                    if (++ahead == C::kRawSlots) {  // the oldest has landed once the others alone are in flight
-                        cp_async_wait_group<C::kRawSlots - 1>();
-                        --ahead;
-                        if (!widen()) break;
-                    }
-                } else {
-                    // The slot is full once its loaders' copies so far have landed; nobody waits for that here, so
-                    // the whole ring can be in flight.
-                    copy_arrive(&bars->full[slot]);
-                    slot += NS;
-                    if (slot >= C::kSlots) {
-                        slot -= C::kSlots;
-                        ++round;
-                    }
-                }
-                if (fresh && !kQueriesFirst && !queries()) break;
-                fresh = w.kt + 1 == w.kts;
-                walk_next(a, w, kTcRowTile, C::kUnit);
-                fetch_pages();
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            if constexpr (F8)
-                while (ahead > 0 && widen()) --ahead;
-            if (err) bars->status = err;
-        } else if (C::mma_of(warp) >= 0) {
-            // ---------------------------------------------------------------- MMA issue
-            // The whole warp runs this with equal values and one elected lane issues: descriptors then stay in
-            // uniform registers (from one divergent lane each MMA cost 90 to 160 cycles to issue).
-            constexpr uint32_t idesc_s = idesc16<BF16>(kTcRowTile, KT, false);
-            constexpr uint32_t idesc_o = idesc16<VB>(kTcRowTile, DP, true);
-            const uint32_t base = smem_addr(smem);
-            // The upper halves of the descriptors hold layout and stride only (and the leading offset, V's, sits in
-            // the lower half's upper bits; with one group of 64 values it is not used).
-            const uint64_t k_desc = umma_desc_sw128(base, 1024);
-            const uint64_t v_desc = umma_desc_sw128_mn(base, C::kSub > 1 ? KT * 128 : 1024, 1024);
-            const uint32_t k_hi = (uint32_t)(k_desc >> 32), k_lo = (uint32_t)k_desc & 0xffff0000u;
-            const uint32_t v_hi = (uint32_t)(v_desc >> 32), v_lo = (uint32_t)v_desc & 0xffff0000u;
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit, C::kExtra);
-            const int s = C::mma_of(warp);
-            int seg = 0, slot = s, turn = 0, held = 0;  // turn: parity of the ring's round; held: the slot whose values
-            bool ok = true, behind = false;             // are still to come, if behind
-            auto values = [&](int n) {  // O_s += P_s V of the stream's n-th tile
-                if (!warp_wait(&bars->pfull[s], (uint32_t)(n & 1))) return false;
-                tc_fence_after();
-                const uint32_t vd = v_lo + ((base + C::kRing + (uint32_t)held * (2 * C::kTile) + C::kTile) >> 4);
-#pragma unroll
-                for (int k = 0; k < KT / 16; ++k)
-                    mma_elect_ts(tm + s * DP, tm + C::kColP + (2 * s + (n & 1)) * (KT / 2) + 8 * k, vd + k * (2048 >> 4), v_hi, idesc_o,
-                                 1u);
-                commit_elect(&bars->empty[held]);
-                commit_elect(&bars->pvdone[s]);
-                return true;
-            };
-            for (int unit = 0; ok && __shfl_sync(0xffffffffu, !w.done(), 0); ++unit) {
-                const int qb = seg % C::kQBufs;
-                if ((!behind && !warp_wait(&bars->qfull[qb], (uint32_t)((seg / C::kQBufs) & 1))) ||  // an item's first tile
-                    !warp_wait(&bars->full[slot], (uint32_t)turn) ||
-                    (unit > 0 && !warp_wait(&bars->sfree[s], (uint32_t)((unit - 1) & 1))))
-                    break;
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the loaders' copies, to the MMA
-                tc_fence_after();
-                const uint32_t qd = k_lo + ((base + (uint32_t)qb * C::kQ) >> 4);
-                const uint32_t kd = k_lo + ((base + C::kRing + (uint32_t)slot * (2 * C::kTile)) >> 4);
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-                    mma_elect_ss(tm + C::kColS + s * KT, qd + (k >> 2) * (kTcRowTile * 128 >> 4) + 2 * (k & 3), k_hi,
-                                 kd + (k >> 2) * (KT * 128 >> 4) + 2 * (k & 3), k_hi, idesc_s, k > 0 ? 1u : 0u);
-                commit_elect(&bars->sfull[s]);
-                if (behind && !values(unit - 1)) break;
-                held = slot;
+            if constexpr (F8) {
+                cp_async_commit();
+                if (++raw_slot == C::kRawSlots) raw_slot = 0;
+                if (++ahead == C::kRawSlots) {  // the oldest has landed once the others alone are in flight
+                    cp_async_wait_group<C::kRawSlots - 1>();
+                    --ahead;
+                    if (!widen()) break;
+                }
+            } else {
+                // The slot is full once its loaders' copies so far have landed; nobody waits for that here, so
+                // the whole ring can be in flight.
+                copy_arrive(&bars->full[slot]);
                 slot += NS;
                 if (slot >= C::kSlots) {
                     slot -= C::kSlots;
-                    turn ^= 1;
+                    ++round;
                 }
-                // An item's last values do not wait for the next item's keys.
-                const bool end = __shfl_sync(0xffffffffu, w.kt + 1 == w.kts || w.left == 1, 0);
-                if (end) {
-                    commit_elect(&bars->qempty[qb]);
-                    ++seg;
-                    ok = values(unit);
-                }
-                behind = !end;
-                walk_next(a, w, kTcRowTile, C::kUnit);
             }
-            commit_elect(&bars->drain[s]);  // everything issued has completed before tensor memory is freed
-            mbar_wait_bounded(&bars->drain[s], 0, status, limit_ns);
-            __syncwarp();
+            if (fresh && !kQueriesFirst && !queries()) break;
+            fresh = w.kt + 1 == w.kts;
+            walk_next(a, w, kTcRowTile, C::kUnit);
+            fetch_pages();
         }
-    } else {
-        // ---------------------------------------------------------------- softmax
-        if constexpr (C::kDealRegisters) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegisters));
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (F8)
+            while (ahead > 0 && widen()) --ahead;
+        if (err) bars->status = err;
+    };
+    // ---------------------------------------------------------------- MMA issue
+    auto issue = [&]() {
+        // The whole warp runs this with equal values and one elected lane issues: descriptors then stay in
+        // uniform registers (from one divergent lane each MMA cost 90 to 160 cycles to issue).
+        constexpr uint32_t kNegateB = I8 && BF16 ? 1u << 14 : 0u;  // (widen16_i8)
+        constexpr uint32_t idesc_s = idesc16<BF16>(kTcRowTile, KT, false) | kNegateB;
+        constexpr uint32_t idesc_o = idesc16<VB>(kTcRowTile, DP, true) | kNegateB;
+        const uint32_t base = smem_addr(smem);
+        // The upper halves of the descriptors hold layout and stride only (and the leading offset, V's, sits in
+        // the lower half's upper bits; with one group of 64 values it is not used).
+        const uint64_t k_desc = umma_desc_sw128(base, 1024);
+        const uint64_t v_desc = umma_desc_sw128_mn(base, C::kSub > 1 ? KT * 128 : 1024, 1024);
+        const uint32_t k_hi = (uint32_t)(k_desc >> 32), k_lo = (uint32_t)k_desc & 0xffff0000u;
+        const uint32_t v_hi = (uint32_t)(v_desc >> 32), v_lo = (uint32_t)v_desc & 0xffff0000u;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        AttnWalk w = walk_begin(a, start, kTcRowTile, C::kUnit, C::kExtra);
+        const int s = C::mma_of(warp);
+        int seg = 0, slot = s, turn = 0, held = 0;  // turn: parity of the ring's round; held: the slot whose values
+        bool ok = true, behind = false;             // are still to come, if behind
+        auto values = [&](int n) {  // O_s += P_s V of the stream's n-th tile
+            if (!warp_wait(&bars->pfull[s], (uint32_t)(n & 1))) return false;
+            tc_fence_after();
+            const uint32_t vd = v_lo + ((base + C::kRing + (uint32_t)held * (2 * C::kTile) + C::kTile) >> 4);
+#pragma unroll
+            for (int k = 0; k < KT / 16; ++k)
+                mma_elect_ts(tm + s * DP, tm + C::kColP + (2 * s + (n & 1)) * (KT / 2) + 8 * k, vd + k * (2048 >> 4), v_hi, idesc_o,
+                             1u);
+            commit_elect(&bars->empty[held]);
+            commit_elect(&bars->pvdone[s]);
+            return true;
+        };
+        for (int unit = 0; ok && __shfl_sync(0xffffffffu, !w.done(), 0); ++unit) {
+            const int qb = seg % C::kQBufs;
+            if ((!behind && !warp_wait(&bars->qfull[qb], (uint32_t)((seg / C::kQBufs) & 1))) ||  // an item's first tile
+                !warp_wait(&bars->full[slot], (uint32_t)turn) ||
+                (unit > 0 && !warp_wait(&bars->sfree[s], (uint32_t)((unit - 1) & 1))))
+                break;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the loaders' copies, to the MMA
+            tc_fence_after();
+            const uint32_t qd = k_lo + ((base + (uint32_t)qb * C::kQ) >> 4);
+            const uint32_t kd = k_lo + ((base + C::kRing + (uint32_t)slot * (2 * C::kTile)) >> 4);
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+                mma_elect_ss(tm + C::kColS + s * KT, qd + (k >> 2) * (kTcRowTile * 128 >> 4) + 2 * (k & 3), k_hi,
+                             kd + (k >> 2) * (KT * 128 >> 4) + 2 * (k & 3), k_hi, idesc_s, k > 0 ? 1u : 0u);
+            commit_elect(&bars->sfull[s]);
+            if (behind && !values(unit - 1)) break;
+            held = slot;
+            slot += NS;
+            if (slot >= C::kSlots) {
+                slot -= C::kSlots;
+                turn ^= 1;
+            }
+            // An item's last values do not wait for the next item's keys.
+            const bool end = __shfl_sync(0xffffffffu, w.kt + 1 == w.kts || w.left == 1, 0);
+            if (end) {
+                commit_elect(&bars->qempty[qb]);
+                ++seg;
+                ok = values(unit);
+            }
+            behind = !end;
+            walk_next(a, w, kTcRowTile, C::kUnit);
+        }
+        commit_elect(&bars->drain[s]);  // everything issued has completed before tensor memory is freed
+        mbar_wait_bounded(&bars->drain[s], 0, status, limit_ns);
+        __syncwarp();
+    };
+    // ---------------------------------------------------------------- softmax
+    auto softmax = [&]() {
         const int s = warp >> 2, row = tid & 127, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const uint32_t ts = tmem + lanes + C::kColS + s * KT;
@@ -822,6 +840,27 @@ __global__ void __launch_bounds__(TcAttn<KV, DP>::kThreads, 1) attn_tc_kernel(At
             ++n;
             walk_next(a, w, kTcRowTile, C::kUnit);
         }
+    };
+    // Where registers are dealt a warpgroup's warps have to meet one setmaxnreg, and the compiler goes by those inside the
+    // branches.  Without, the softmax comes last of three: with the other two in a branch of their own the code is laid out
+    // in another order, and three long contexts with a softcap (heads of 256, bf16) took 155 us for 130.
+    if constexpr (C::kDealRegisters) {
+        if (warp >= C::kSoftmaxWarps) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kHelperRegisters));
+            if (C::loader_of(warp) >= 0)
+                load();
+            else if (C::mma_of(warp) >= 0)
+                issue();
+        } else {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegisters));
+            softmax();
+        }
+    } else if (C::loader_of(warp) >= 0) {
+        load();
+    } else if (C::mma_of(warp) >= 0) {
+        issue();
+    } else if (warp < C::kSoftmaxWarps) {
+        softmax();
     }
     tc_fence_before();
     __syncthreads();
