@@ -687,11 +687,12 @@ struct AttnWs {
 //   16-bit   mean 11 rows 117 / 115 (long contexts) and 63 / 84 (short); mean 14: 130 / 109 and 71 / 83;
 //            mean 24: 88 / 67; heads of 256, mean 11: 214 / 255, mean 24: 159 / 139
 //   e4m3     mean 35 rows 69 / 85 and 36 / 42; 68 rows: 80 / 58; mean 70: 159 / 101; 119 rows: 254 / 92
-//   int8     mean 23 rows 66 / 101, 33 rows 584 / 621 and 87 / 83, heads of 256, 36 rows 111 / 124; 54 rows 75 / 65, 64 rows
-//            107 / 60 and 153 / 91
+//   int8     heads of 64, 32 rows 193 / 189, mean 30: 288 / 292; of 128, 32 rows 135 / 128, mean 28: 194 / 206, mean 33:
+//            581 / 524; of 256, 32 rows 156 / 158 (167 / 174 with a softcap), mean 29: 212 / 250, 36 rows 198 / 162; 24 rows
+//            191 / 187, 126 / 127 and 144 / 159.  Three tiles of 16 are more than the wide kernel takes.
 // (an 8-bit tile has to be widened for the wide kernel, so it needs more rows to pay).
 bool wide_rows(const dspark_attention_params* p) {
-    const long long G = p->Hq / p->Hk, limit = p->kv_dtype == p->dtype ? kRows : (p->kv_dtype == DSPARK_I8 ? 36 : 48);
+    const long long G = p->Hq / p->Hk, limit = p->kv_dtype == p->dtype ? kRows : (p->kv_dtype == DSPARK_I8 ? (p->D <= 128 ? 31 : 32) : 48);
     return G * p->T > limit * p->B && (p->max_new <= 0 || G * p->max_new > limit);
 }
 // Whether a call over an int8 cache takes row tiles of 8 (else of 16, where it is not wide): by the mean rows of a request

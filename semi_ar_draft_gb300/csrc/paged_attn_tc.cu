@@ -1,5 +1,5 @@
 // paged_attn_tc.cu -- dspark_paged_attention and dspark_paged_attention_i8 on the fifth-generation tensor cores: row tiles of 128 for
-// requests whose new tokens give more than 16 rows a kv head, 48 with an e4m3 cache, 36 with an int8 one (the flattened
+// requests whose new tokens give more than 16 rows a kv head, 48 with an e4m3 cache, 31 with an int8 one (the flattened
 // verify, draft blocks).
 //
 // One persistent CTA a multiprocessor walks its range of units (paged.cuh).  Roles:

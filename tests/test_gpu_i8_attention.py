@@ -51,7 +51,8 @@ def attend(c, **kw):
 def takes_wide(c, max_new):
     """Whether the call goes to the kernel of many rows."""
     G, T, B = c["q"].shape[1] // c["codes"][0].shape[2], c["q"].shape[0], len(c["seq"])
-    return G * T > 36 * B and (max_new <= 0 or G * max_new > 36)
+    limit = 31 if c["q"].shape[2] <= 128 else 32
+    return G * T > limit * B and (max_new <= 0 or G * max_new > limit)
 
 
 def check(c, lens, offsets, causal=True, window=0, softcap=0.0, scale=None, max_new=0):
