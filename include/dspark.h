@@ -554,7 +554,9 @@ dspark_status dspark_cache_read_i8(const dspark_append_params* p, const dspark_b
 /*
  * dspark_paged_attention over int8 pools: the same scores, masks, outputs, statuses and workspace, with k_l and v_l the
  * values code 2^e; p->kv_dtype is DSPARK_I8.  It is the attention over the cache that dspark_cache_read_i8 gives.
- * Probabilities are rounded to 16 bits (fp16, or for many rows a kv head dtype) before they meet the values.
+ * Probabilities are rounded to 16 bits (fp16, or for many rows a kv head dtype) before they meet the values.  For many
+ * rows a kv head the sums of weighted bf16 values are taken before they are divided, as over 16-bit pages: values past 2^100
+ * may leave fp32's range there.
  * Host errors besides: DSPARK_ERR_UNSUPPORTED for a scale other than 0 outside 2^-32 .. 2^32, and for a pool that spans
  * 2^32 times the largest power of two up to 4096 that its three strides are multiples of (64 GB at least), or exponents
  * that span 4 GB.

@@ -57,7 +57,8 @@ struct AttnArgs {
     int32_t* error;  // the caller's word for the first error, or null
     struct PartItem* items;  // [parts]
     float2* part_ml;         // [2 parts][rows of a tile]: (maximum, log2 domain; sum)
-    float* part_o;           // [2 parts][rows of a tile][D]
+    float* part_o;           // [2 parts][rows of a tile][D]: sums of weighted values
+    int averages;            // or those divided by their parts' sums, for the join (launch_attn_i8, launch_attn_i8_rows)
 };
 
 // An item spread over blocks, as each of them describes it (first < 0: none).

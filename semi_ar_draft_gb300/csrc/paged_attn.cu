@@ -523,7 +523,7 @@ constexpr int kJoinWarps = 4;
 constexpr int kJoinAhead = 4;
 constexpr int kJoinFew = 8;  // up to so many parts, a warp joins a row by itself (20 -> 8 us for 64 rows of 2 parts)
 // An item may cover several kv heads (an int8 cache): its rows are then those of the first one, row_tile places, those of
-// the second one and so on, and it.rows are real of each.
+// the second one and so on, and it.rows are real of each.  Its parts are averages (a.averages), weighed by their sums here.
 template <bool BF16>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, int row_tile, int heads, int parts) {
     __shared__ float s_f[kMaxParts];
@@ -570,11 +570,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
                     const float mm = warp_max(ml.x);
                     const float f = ml.y == 0.f ? 0.f : ex2(ml.x - (mm == -CUDART_INF_F ? 0.f : mm));
                     const float ll = warp_sum(ml.y * f);
-                    const float inv = ll == 0.f ? 0.f : vscale / ll;
+                    float inv = ll == 0.f ? 0.f : vscale / ll, weight = f;
+                    if (a.averages) weight = f * ml.y * inv, inv = 1.f;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int i = 0; i < kJoinFew; ++i) {
-                        const float fi = __shfl_sync(0xffffffffu, f, i);
+                        const float fi = __shfl_sync(0xffffffffu, weight, i);
                         if (i < n && in) {
                             v.x = fmaf(y[i].x, fi, v.x);
                             v.y = fmaf(y[i].y, fi, v.y);
@@ -616,11 +617,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
                         const float2 ml = a.part_ml[slot_of(i) * places + row];
                         const float f = ml.y == 0.f ? 0.f : ex2(ml.x - ref);
                         ll = fmaf(ml.y, f, ll);
-                        if (warp == 0) s_f[i] = f;
+                        if (warp == 0) s_f[i] = a.averages ? f * ml.y : f;
                     }
                     ll = warp_sum(ll);
                     __syncthreads();
                 }
+                const float share = a.averages ? (ll == 0.f ? 0.f : __fdividef(1.f, ll)) : 1.f;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 auto add = [&](float f, const float4& x) {
                     v.x = fmaf(x.x, f, v.x);
@@ -631,15 +633,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(AttnArgs a, 
 #pragma unroll
                 for (int u = 0; u < kJoinAhead; ++u) {
                     const int i = warp + u * kJoinWarps;
-                    if (i < n) add(s_f[i], y[u]);
+                    if (i < n) add(s_f[i] * share, y[u]);
                 }
                 if (in)
 #pragma unroll 4
-                    for (int i = warp + kJoinAhead * kJoinWarps; i < n; i += kJoinWarps) add(s_f[i], part(i));
+                    for (int i = warp + kJoinAhead * kJoinWarps; i < n; i += kJoinWarps) add(s_f[i] * share, part(i));
                 s_acc[warp][lane] = v;
                 __syncthreads();
                 if (warp == 0 && in) {
-                    const float inv = ll == 0.f ? 0.f : vscale / ll;
+                    const float inv = a.averages ? 1.f : (ll == 0.f ? 0.f : vscale / ll);
                     float4 t = s_acc[0][lane];
 #pragma unroll
                     for (int x = 1; x < kJoinWarps; ++x) {
@@ -692,7 +694,8 @@ struct AttnWs {
 //            191 / 187, 126 / 127 and 144 / 159.  Three tiles of 16 are more than the wide kernel takes.
 // (an 8-bit tile has to be widened for the wide kernel, so it needs more rows to pay).
 bool wide_rows(const dspark_attention_params* p) {
-    const long long G = p->Hq / p->Hk, limit = p->kv_dtype == p->dtype ? kRows : (p->kv_dtype == DSPARK_I8 ? (p->D <= 128 ? 31 : 32) : 48);
+    const long long G = p->Hq / p->Hk, i8_limit = p->D <= 128 ? 31 : 32;
+    const long long limit = p->kv_dtype == p->dtype ? kRows : (p->kv_dtype == DSPARK_I8 ? i8_limit : 48);
     return G * p->T > limit * p->B && (p->max_new <= 0 || G * p->max_new > limit);
 }
 // Whether a call over an int8 cache takes row tiles of 8 (else of 16, where it is not wide): by the mean rows of a request
@@ -825,7 +828,8 @@ dspark_status paged_attention(const dspark_attention_params* p, const dspark_blo
     const bool tc = wide_rows(p) && a.q_vec;
     // the type of the probabilities: q's, or halves (an e4m3 cache; int8, row tiles of 16)
     a.sum_scale = bf16 && (kv == kKv16 || (kv == kKvI8 && tc)) ? ProbScale<true>::kInverse : ProbScale<false>::kInverse;
-    const bool few = kv == kKvI8 && !tc && few_rows_i8(p);
+    a.averages = kv == kKvI8 && !tc;
+    const bool few = a.averages && few_rows_i8(p);
     const dspark_status ls = tc             ? launch_attn_tc(a, bf16, kv, sms, s, &parts)
                              : few         ? launch_attn_i8(a, bf16, sms, s, &parts)
                              : kv == kKvI8 ? launch_attn_i8_rows(a, bf16, sms, s, &parts)
@@ -838,7 +842,7 @@ dspark_status paged_attention(const dspark_attention_params* p, const dspark_blo
     const int row_tile = tc ? kTcRows : (few ? 8 : kRows), heads = few ? i8_head_group(p->D, p->Hk) : 1;
     // The join's blocks become resident as the attention kernel's leave.
     // (Few rows an item want few of them: 456 parts, 2 blocks each against 8: 57.7 against 59.6 us for 32 requests.)
-    const dim3 grid(parts, kv == kKvI8 && !tc ? 2 : 8), block(32 * kJoinWarps);
+    const dim3 grid(parts, a.averages ? 2 : 8), block(32 * kJoinWarps);
     const cudaError_t e = bf16 ? launch_overlapped(attn_join_kernel<true>, grid, block, 0, s, a, row_tile, heads, parts)
                                : launch_overlapped(attn_join_kernel<false>, grid, block, 0, s, a, row_tile, heads, parts);
     if (e != cudaSuccess) return DSPARK_ERR_CUDA;

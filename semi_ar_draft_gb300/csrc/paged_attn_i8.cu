@@ -15,9 +15,10 @@
 // head computes 16 rows of everything, scores, exponentials and output registers alike.  P^T is S^T's fragment transposed
 // (movmatrix).  A warp streams slices of its own through a ring of its own in shared memory, as in paged_attn.cu.
 //
-// Measured: 32 requests of up to 8192 tokens, 8 kv heads of 128, 58 us = 4.9 TB/s (0.73 of the measured copy rate; the rows
-// in A 73 us); 128 requests of up to 8000 tokens 190 us = 5.9 TB/s (0.88; 237 us); heads of 64, 128 requests, 122 us (183
-// before the block's warps took a head each).
+// Measured: 32 requests of up to 8192 tokens, 8 kv heads of 128, 57 us = 5.0 TB/s (0.74 of the measured copy rate; the rows
+// in A 73 us); 128 requests of up to 8000 tokens 191 us = 5.9 TB/s (0.87; 237 us); heads of 64, 128 requests, 118 us (183
+// before the block's warps took a head each); 48 requests of 1000 tokens' window, five rows of 96, 29 us; one request of
+// up to 1024 tokens 10.5 us, latency.
 #include "host_util.h"
 #include "mma16.cuh"
 #include "paged.cuh"
@@ -420,12 +421,13 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
                 if (g == 0) s_ml[warp][2 * t + r] = make_float2(ref[r] == kNone ? -CUDART_INF_F : ref[r] + kUp, l);
-                // to the reference of the sums, in two steps: 2^f may be as large as fp32's numbers
-                const float f = ex2(0.5f * (ref_v[r] - ref[r]));
+                // Averages, which are no larger than the values (127 2^121 is nearly fp32's largest number); to the
+                // reference of the sums in two steps, since 2^f may be as large as that too.
+                const float f = ex2(0.5f * (ref_v[r] - ref[r])), inv = l == 0.f ? 0.f : __fdividef(1.f, l);
 #pragma unroll
                 for (int i = 0; i < KS; ++i)
                     *reinterpret_cast<float2*>(mine_o + o_at(2 * t + r, 16 * i + 2 * g)) =
-                        make_float2(o[i][r] * f * f, o[i][2 + r] * f * f);
+                        make_float2(o[i][r] * inv * f * f, o[i][2 + r] * inv * f * f);
             }
             __syncthreads();
             const bool whole = last_of_item && seg_first == 0;
@@ -438,15 +440,20 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
 #pragma unroll
                 for (int x = hd; x < kWarps; x += HG) mm = fmaxf(mm, s_ml[x][row].x);
                 const float ref = mm == -CUDART_INF_F ? 0.f : mm;
+                float weight[C::kKeyWarps];
+#pragma unroll
+                for (int x = 0; x < C::kKeyWarps; ++x) {
+                    const float2 ml = s_ml[hd + x * HG][row];
+                    weight[x] = ml.y == 0.f ? 0.f : ml.y * ex2(ml.x - ref);  // (0: saw nothing)
+                    ll += weight[x];
+                }
+                const float inv = ll == 0.f ? 0.f : __fdividef(1.f, ll);
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int x = hd; x < kWarps; x += HG) {
-                    const float2 ml = s_ml[x][row];
-                    const float f = ex2(ml.x - ref);
-                    if (ml.y == 0.f) continue;  // saw nothing
-                    ll = fmaf(ml.y, f, ll);
+                for (int x = 0; x < C::kKeyWarps; ++x) {
+                    const float f = weight[x] * inv;
                     const float4 y = *reinterpret_cast<const float4*>(
-                        smem + (size_t)(x * C::kStages + st) * C::kStage + 4 * o_at(row, col));
+                        smem + (size_t)((hd + x * HG) * C::kStages + st) * C::kStage + 4 * o_at(row, col));
                     v.x = fmaf(y.x, f, v.x);
                     v.y = fmaf(y.y, f, v.y);
                     v.z = fmaf(y.z, f, v.z);
@@ -454,10 +461,7 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
                 }
                 if (whole) {
                     const long long at = attn_out_row(a, w.r.token0, head, row0 + row);
-                    if (col < a.D) {
-                        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                        store_out4<BF16>(a, at, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-                    }
+                    if (col < a.D) store_out4<BF16>(a, at, col, v);
                     if (a.lse && col == 0)
                         a.lse[at] = ll == 0.f ? -CUDART_INF_F : (mm + lg2(ll * ProbScale<false>::kInverse)) * kLn2;
                 } else {

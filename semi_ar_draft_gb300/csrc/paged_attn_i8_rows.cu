@@ -1,4 +1,4 @@
-// paged_attn_i8_rows.cu -- dspark_paged_attention_i8 for 9 to some 36 rows a kv head (several new tokens a request, or many
+// paged_attn_i8_rows.cu -- dspark_paged_attention_i8 for 9 to some 32 rows a kv head (several new tokens a request, or many
 // query heads a kv head): row tiles of 16.  paged_attn_i8.cu has the arithmetic, paged.cuh the split of the work and the
 // join.
 //
@@ -9,8 +9,9 @@
 //
 // Bound by issue slots (about half of them are used by twelve warps a multiprocessor).  Measured, against the 8-row
 // kernel's layout with two row tiles a warp: 32 requests of up to 8192 tokens, 16 rows, 8 kv heads of 128: 73 us (82);
-// 64 requests, 23 rows, 4 kv heads: 66 us (79).  Row tiles of 32 and 64 need more registers or shared memory than three
-// blocks a multiprocessor leave: 105 and 207 us, 79 and 132 us.
+// 64 requests, 23 rows, 4 kv heads: 66 us (79).  Three contexts of up to 200000 tokens, two tiles of 16 rows of 256,
+// softcap: 167 us.  Row tiles of 32 and 64 need more registers or shared memory than three blocks a multiprocessor leave:
+// 105 and 207 us for the first case.
 #include "host_util.h"
 #include "mma16.cuh"
 #include "paged.cuh"
@@ -449,15 +450,14 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
 #pragma unroll
                 for (int x = 0; x < kWarps; ++x) ll += s_sum[x][row];
                 const float m = ref[r] == kNone ? -CUDART_INF_F : ref[r] + kUp;
-                // to the reference of the sums, in two steps: 2^f may be as large as fp32's numbers
-                const float f = ex2(0.5f * (ref_v[r] - ref[r]));
-                const float inv = !whole ? 1.f : (ll == 0.f ? 0.f : 1.f / ll);
+                // (averages, and in two steps: see paged_attn_i8.cu)
+                const float f = ex2(0.5f * (ref_v[r] - ref[r])), inv = ll == 0.f ? 0.f : __fdividef(1.f, ll);
                 const long long at = attn_out_row(a, w.r.token0, head, row0 + row);
                 const size_t part_at = (size_t)slot * kRows + row;
 #pragma unroll
                 for (int i = 0; i < DM; ++i) {
                     const int col = 16 * (DM * warp + i) + 2 * g;
-                    const float x = o[i][r >> 1][r & 1] * f * f * inv, y = o[i][r >> 1][2 + (r & 1)] * f * f * inv;
+                    const float x = o[i][r >> 1][r & 1] * inv * f * f, y = o[i][r >> 1][2 + (r & 1)] * inv * f * f;
                     if (col >= a.D) continue;
                     if (whole)
                         *reinterpret_cast<uint32_t*>(a.out + ((size_t)at * a.D + col) * 2) = pack16<BF16>(x, y);

@@ -1,6 +1,6 @@
-// paged_attn_tc.cu -- dspark_paged_attention and dspark_paged_attention_i8 on the fifth-generation tensor cores: row tiles of 128 for
-// requests whose new tokens give more than 16 rows a kv head, 48 with an e4m3 cache, 31 with an int8 one (the flattened
-// verify, draft blocks).
+// paged_attn_tc.cu -- dspark_paged_attention and dspark_paged_attention_i8 on the fifth-generation tensor cores: row tiles
+// of 128 for requests whose new tokens give more than 16 rows a kv head, 48 with an e4m3 cache, 31 or 32 with an int8 one
+// (the flattened verify, draft blocks).
 //
 // One persistent CTA a multiprocessor walks its range of units (paged.cuh).  Roles:
 //   loaders (4 or 8      copy the item's queries and, tile by tile, KT keys and values into a ring in
@@ -24,9 +24,11 @@
 // softmax decides: 32 draft blocks of 16 over up to 4100 tokens 52.5 us = 2.8 TB/s (0.42).
 // Over an 8-bit cache the loaders' widening decides at few rows (32 requests, 35 rows on average, e4m3: 85 us, of row
 // tiles of 16: 69) and pays at many (145 requests, 119 rows of 192 over 200 keys, e4m3: 92 us against 254).  An int8
-// cache's codes take five instructions a pair and their scales' product besides, so it has eight loaders: 64 requests of up
-// to 4096 tokens, 63 rows, 4 kv heads of 128: 109 us (row tiles of 16: 139); 32 draft blocks of 16, heads of 64: 60 us;
-// two prompts of 2000 tokens over 6000: 0.68 ms (1.87).
+// cache's codes take four and a half instructions a pair (bf16; fp16 three and a half), so it has eight loaders.  A tile of
+// 64 keys of 128 then takes some 3900 cycles, of which a loader is busy for 3000 (widening 1550 to 1900, copies 500, walk
+// and queries 450) and the softmax, beside it in the same issue slots, for 2700.  Measured, bf16, heads of 128: 512 requests of
+// up to 4096 tokens, 33 rows on average, 524 us (row tiles of 16: 581); 64 requests, 68 rows, 82 us; two prompts of 2000
+// tokens over 6000: 0.53 ms.  32 draft blocks of 16, fp16 heads of 64: 60 us, as over 16-bit pages the softmax's chain.
 #include <cuda_bf16.h>
 
 #include "host_util.h"
@@ -66,7 +68,7 @@ struct TcAttn {
     // others need: whole warpgroups give and take (the softmax's warps come first).
     static constexpr bool kDealRegisters = KV == kKvI8 && kStreams == 2;
     static constexpr int kSoftmaxRegisters = 120, kHelperRegisters = 80;
-    static_assert(!kDealRegisters || 32 * (kSoftmaxWarps * kSoftmaxRegisters + 12 * kHelperRegisters) <= 32 * 20 * 96, "the launch's registers");
+    static_assert(!kDealRegisters || kSoftmaxWarps * kSoftmaxRegisters + 12 * kHelperRegisters <= 20 * 96, "the launch's registers");
     static __device__ __forceinline__ int mma_of(int warp) {  // the stream, or -1
         const int h = warp - kSoftmaxWarps;
         return h == 1 ? 0 : (h == (KV == kKvI8 ? 8 : 5) && kStreams == 2 ? 1 : -1);

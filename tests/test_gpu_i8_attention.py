@@ -132,6 +132,41 @@ def test_scales_over_the_whole_range(dtype, max_new):
     check(c, lens, offsets, max_new=max_new, scale=2.0)  # a few keys take all
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [3, 16, 40])
+def test_every_code_at_every_scale_is_read_exactly(dtype, D, G):
+    """Queries of zeros over one key a request: the weight is 1, and the output the value, bit for bit."""
+    every = torch.arange(-127, 128, device="cuda")
+    lo, hi = (-126, 121) if dtype == torch.bfloat16 else (-24, 9)
+    scales = sorted({lo, lo + 1, -1, 0, 1, hi - 1, hi, 5, -13})
+    per = -(-255 // D)
+    rows = torch.cat([every, every[:per * D - 255]]).view(per, D).to(torch.int8)
+    codes = rows.repeat(len(scales), 1)[:, None, None].contiguous()  # [pages of one token, 1, 1, D]
+    exps = torch.tensor([e + 127 for e in scales for _ in range(per)], dtype=torch.uint8, device="cuda")[:, None, None].contiguous()
+    B = per * len(scales)
+    c = {"q": torch.zeros((B, G, D), dtype=dtype, device="cuda"), "codes": [codes, codes], "exps": [exps, exps],
+         "table": i32([[b] for b in range(B)]), "seq": i32([1] * B), "offsets": i32(list(range(B + 1)))}
+    out, lse, ws = attend(c)
+    assert status(ws) == 0 and not lse.any()
+    want = R.values(codes, exps, dtype)[:, 0]  # [B, 1, D]
+    assert torch.equal(out.double(), want.expand(B, G, D))
+
+
+@pytest.mark.parametrize("G,max_new", [(4, 1), (1, 3), (8, 3)])
+def test_values_up_to_the_type_s_largest(G, max_new):
+    """Sums of such values are past fp32's range, averages are not: short contexts, and long ones split over blocks."""
+    for lens in ([3000, 40], [60000], [7] * 50):
+        c, lens, offsets = make_case(lens, [min(max_new, n) for n in lens], G, 1, 128, 16, 4, torch.bfloat16, 11 + G)
+        c["exps"][0].fill_(121)
+        g = torch.Generator(device="cuda").manual_seed(G)
+        c["exps"][1].copy_(torch.randint(240, 249, c["exps"][1].shape, generator=g, device="cuda").to(torch.uint8))
+        c["codes"][1][..., :8] = 127  # an average as large as the values
+        c["codes"][1][..., 8:16] = -127
+        out, _ = check(c, lens, offsets, max_new=max_new)
+        assert bool(out.isfinite().all())
+
+
 def test_one_key_far_above_with_a_small_value():
     """A dominating key whose values are 2^40 below the others' (as an attention sink's): its row keeps its bits."""
     c, lens, offsets = make_case([100], [1], 2, 1, 64, 16, 1, torch.bfloat16, 5)
