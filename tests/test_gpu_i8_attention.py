@@ -88,6 +88,15 @@ def test_decoding_heads_and_pages(dtype, Hq, Hk, D, page, block):
     assert torch.equal(out, attend(c)[0])
 
 
+@pytest.mark.parametrize("D", [16, 48, 80, 96, 112, 144, 176, 192, 208])
+@pytest.mark.parametrize("G", [5, 12, 40])
+def test_heads_that_do_not_fill_their_rows(D, G):
+    """Every kernel, with one kv head and with groups of them; parts of a request in several blocks."""
+    for Hk, lens in ((3, [1, 17, 130, 700, 40]), (2, [5000]), (4, [63, 64, 65])):
+        c, lens, offsets = make_case(lens, [1] * len(lens), G * Hk, Hk, D, 32, 8, torch.bfloat16, D + G)
+        check(c, lens, offsets)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("causal,window,softcap,scale", [(True, 0, 0.0, None), (False, 0, 0.0, None), (True, 1, 0.0, None), (True, 20, 0.0, 0.3),
                                                          (False, 100, 0.0, None), (True, 0, 30.0, None), (True, 50, 2.0, None),
