@@ -38,6 +38,8 @@ struct AttnArgs {
     float sum_scale;  // ProbScale's inverse, for lse
     int q_vec;        // rows of q start on 16-byte boundaries
     float scale, softcap;
+    float score_m;  // score_m 2^score_e = log2 e scale, or with a softcap 2 log2 e scale / softcap (int8 pools)
+    int score_e;
     const unsigned char* q;
     long long q_token, q_head;  // strides, elements
     const unsigned char* k_pages;
@@ -371,6 +373,19 @@ __device__ __forceinline__ int query_halves(uint32_t (&y)[4], float& sum) {
 #pragma unroll
     for (int d = 1; d < LANES; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     return raise;
+}
+
+// What a row's sums of (codes and halves of the query times 2^raise, 2^-24) are multiplied by on their way to the log2 domain, or
+// to the cap's exponent, beside a key's 2^e: log2 e scale 2^(24 - raise) leaves fp32 for queries past 2^117 (which are halves
+// times 2^113), and again for small ones, where key scales bring the scores back.  So it comes in two: one that takes
+// no sum out of fp32 with or without the key's scale unless the score is, and the power of two that is left, which is 1
+// but for such queries, scales and caps.  (Sums are at most 2^16 and exact to 2^-48; a cap's score past 2^53 is the cap.)
+struct ScoreFactor {
+    float near, far;
+};
+__device__ __forceinline__ ScoreFactor score_factor(const AttnArgs& a, int raise) {
+    const int e = a.score_e + 24 - raise, e1 = min(max(e, -110), 100);
+    return {a.score_m * two_to(e1), two_to(min(max(e - e1, -126), 127))};
 }
 
 // Row tiles of 128 on the fifth-generation tensor cores (paged_attn_tc.cu); needs 16-byte

@@ -754,7 +754,7 @@ dspark_status paged_attention(const dspark_attention_params* p, const dspark_blo
     if (st != DSPARK_OK) return st;
     if ((p->kv_dtype == DSPARK_I8) != (x != nullptr)) return DSPARK_ERR_INVALID_ARG;
     if (x && !valid_block_exponents(x, p->page_size)) return DSPARK_ERR_INVALID_ARG;
-    // (a score is formed as the product of codes and raised queries, of the row's factor and of 2^e, one after the other)
+    // (the range that score_factor's two factors are made for)
     if (x && p->scale != 0.f && (fabsf(p->scale) < 0x1p-32f || fabsf(p->scale) > 0x1p32f)) return DSPARK_ERR_UNSUPPORTED;
     if (!k_pages || !v_pages || !block_table || !seq_len || (p->T && (!q || !out))) return DSPARK_ERR_INVALID_ARG;
     if (!offsets && p->T < p->B) return DSPARK_ERR_INVALID_ARG;
@@ -811,7 +811,11 @@ dspark_status paged_attention(const dspark_attention_params* p, const dspark_blo
     a.v_scale = e4m3 ? v_scale : nullptr;
     a.exp = {};
     a.steps = {};
+    a.score_m = 0.f;
+    a.score_e = 0;
     if (x) {
+        const double log2e = 1.4426950408889634;
+        a.score_m = (float)frexp(log2e * p->scale * (a.softcap > 0.f ? 2. / (double)a.softcap : 1.), &a.score_e);
         a.exp = {x->k, x->v, x->page_stride, x->block_stride, x->head_stride, 0};
         while ((1 << a.exp.shift) < x->block) ++a.exp.shift;
         a.steps = steps;

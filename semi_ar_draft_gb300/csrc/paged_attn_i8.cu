@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
     __shared__ float2 s_ml[kWarps][kRows];
     __shared__ int s_err;
     __shared__ AttnScratch s_start;
-    // where a row's products begin, its scores' factor: rows of the first head, of the second, ...
-    __shared__ __align__(8) float s_base[HG * kRows], s_scale[HG * kRows];
+    // where a row's products begin, its scores' factor in two (score_factor): rows of the first head, of the second, ...
+    __shared__ __align__(8) float s_base[HG * kRows], s_scale[HG * kRows], s_far[HG * kRows];
     __shared__ AttnStart s_range;                    // the block's units
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
     float ref[2], ref_v[2];
     uint64_t sums;
     int all_lo = 0, all_hi = 0, rows = 0, group = 0, row0 = 0, seg_first = 0;
-    bool fresh = true;
+    bool fresh = true, far = false;  // far: some row's second factor counts
     int st = 0;
     // The queries' fragments of k-steps ks and ks + 1.
     auto load_q = [&](uint32_t (&b)[4], int ks) { ldsm4(b, qs_addr + C::q_at(lane & 7, 2 * ks + (lane >> 3))); };
@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
             // The queries, through shared memory: 16 bytes a thread, then fragments by ldmatrix.  (The previous segment's
             // readers are past its last barrier.)
             constexpr int kQc = DP / 8;  // threads of a row
+            bool row_far = false;
             constexpr int kQRows = HG * kRows, kQSteps = (kQRows * kQc + kThreads - 1) / kThreads;
 #pragma unroll
             for (int u = 0; u < kQSteps; ++u) {
@@ -227,12 +228,14 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
                     *reinterpret_cast<uint32_t*>(qs + C::q_at(qrow, c | 1) + at) = __byte_perm(y[2 * e], y[2 * e + 1], 0x7632);
                 }
                 if (c == 0) {
+                    const ScoreFactor f = score_factor(a, raise);
                     s_base[qrow] = -128.f * 0x1p-24f * sum;
-                    // to the log2 domain, or to the cap's exponent
-                    s_scale[qrow] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale * 0x1p24f * two_to(-raise);
+                    s_scale[qrow] = f.near;
+                    s_far[qrow] = f.far;
+                    row_far |= f.far != 1.f;
                 }
             }
-            __syncthreads();
+            far = __syncthreads_or(row_far);
             ref[0] = ref[1] = ref_v[0] = ref_v[1] = kNone;
             sums = 0;
             if (!C::kQInSmem) {
@@ -323,12 +326,31 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float2 x = up2(mul2(mul2(pk2(s[i][2 * h], s[i][2 * h + 1]), pk2(row_scale.x, row_scale.y)),
-                                        pk2(key_scale[i][h], key_scale[i][h])));
-                    if (a.softcap > 0.f) x = softcap2(x.x, x.y, 1.f, cap_out);
+                    const float2 x = up2(mul2(mul2(pk2(s[i][2 * h], s[i][2 * h + 1]), pk2(row_scale.x, row_scale.y)),
+                                              pk2(key_scale[i][h], key_scale[i][h])));
                     s[i][2 * h] = x.x;
                     s[i][2 * h + 1] = x.y;
                 }
+            if (far) {
+                const float2 f = *reinterpret_cast<const float2*>(&s_far[my_head * kRows + 2 * t]);
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        s[i][2 * h] *= f.x;
+                        s[i][2 * h + 1] *= f.y;
+                    }
+            }
+            if (a.softcap > 0.f) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 x = softcap2(s[i][2 * h], s[i][2 * h + 1], 1.f, cap_out);
+                        s[i][2 * h] = x.x;
+                        s[i][2 * h + 1] = x.y;
+                    }
+            }
             if (key0 < all_lo || key0 + C::kKeys > all_hi) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {

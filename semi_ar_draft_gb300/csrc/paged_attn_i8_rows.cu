@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
     __shared__ float s_sum[kWarps][kRows];
     __shared__ int s_err;
     __shared__ AttnScratch s_start;
-    __shared__ __align__(8) float s_base[kRows], s_scale[kRows];  // where a row's products begin, its scores' factor
+    // where a row's products begin, its scores' factor in two (score_factor)
+    __shared__ __align__(8) float s_base[kRows], s_scale[kRows], s_far[kRows];
     __shared__ AttnStart s_range;                     // the block's units
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
     float ref[R], ref_v[R];
     uint64_t sums[NT];  // of rows 8 j + 2 t and the next
     int all_lo = 0, all_hi = 0, rows = 0, head = 0, row0 = 0, seg_first = 0;
-    bool fresh = true;
+    bool fresh = true, far = false;  // far: some row's second factor counts
     int st = 0;
     auto row_of = [&](int r) { return 8 * (r >> 1) + 2 * t + (r & 1); };
     while (!w.done()) {
@@ -174,6 +175,7 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
             constexpr int kQc = DP / 8;  // threads of a row
             constexpr int kQSteps = kRows * kQc / kThreads;
             static_assert(kRows * kQc % kThreads == 0, "whole steps");
+            bool row_far = false;
 #pragma unroll
             for (int u = 0; u < kQSteps; ++u) {
                 const int row = (tid + u * kThreads) / kQc, c = (tid + u * kThreads) % kQc, token = attn_token(a, row0 + row);
@@ -199,12 +201,14 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
                     *reinterpret_cast<uint32_t*>(qs + C::q_at(row, c | 1) + at) = __byte_perm(y[2 * e], y[2 * e + 1], 0x7632);
                 }
                 if (c == 0) {
+                    const ScoreFactor f = score_factor(a, raise);
                     s_base[row] = -128.f * 0x1p-24f * sum;
-                    // to the log2 domain, or to the cap's exponent
-                    s_scale[row] = (a.softcap > 0.f ? 2.f * kLog2e / a.softcap : kLog2e) * a.scale * 0x1p24f * two_to(-raise);
+                    s_scale[row] = f.near;
+                    s_far[row] = f.far;
+                    row_far |= f.far != 1.f;
                 }
             }
-            __syncthreads();
+            far = __syncthreads_or(row_far);
 #pragma unroll
             for (int r = 0; r < R; ++r) ref[r] = ref_v[r] = kNone;
 #pragma unroll
@@ -294,6 +298,19 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
                     s[i][j][2 * h] = x.x;
                     s[i][j][2 * h + 1] = x.y;
                 }
+        }
+        if (far) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const float2 f = *reinterpret_cast<const float2*>(&s_far[8 * j + 2 * t]);
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        s[i][j][2 * h] *= f.x;
+                        s[i][j][2 * h + 1] *= f.y;
+                    }
+            }
         }
         if (a.softcap > 0.f) {
 #pragma unroll

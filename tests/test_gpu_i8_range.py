@@ -1,0 +1,48 @@
+"""Int8 attention over the range of queries, keys and scores, in each of its kernels."""
+import math
+
+import pytest
+import torch
+
+import i8_bounds as bounds
+from semi_ar_draft_gb300 import api, binding
+from test_gpu_i8_attention import make_case
+
+pytestmark = pytest.mark.gpu
+
+KERNELS = [("few", 4, 1), ("rows", 5, 3), ("wide", 32, 2)]  # name, query heads of a kv head, the most new tokens
+
+
+def attend(c, kernel, **kw):
+    assert bounds.kernel_of(c, kw.get("max_new", 0)) == kernel
+    out, lse, ws = api.paged_attention_i8(c["q"], *c["codes"], *c["exps"], c["table"], c["seq"], c["offsets"], lse=True, **kw)
+    assert binding.dspark_get_device_status(ws) == 0
+    return out, lse
+
+
+def queries(shape, E, seed=1):
+    """bf16 of about 2^E, the largest of a row between 2^E and 2^(E + 1)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.rand(shape, generator=g, device="cuda", dtype=torch.float64) * 2 - 1
+    x = x / x.abs().amax(-1, keepdim=True) * 1.5
+    return (x * 2.0 ** E).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("kernel,G,max_new", KERNELS)
+@pytest.mark.parametrize("E,scale,softcap", [(60, None, 0.0), (100, None, 0.0), (116, None, 0.0), (118, 1.0, 0.0), (121, None, 0.0), (124, None, 0.0),
+                                             (126, None, 0.0), (127, None, 0.0), (87, 2.0 ** 32, 0.0), (95, 2.0 ** 32, 0.0), (121, None, 5.0),
+                                             (110, None, 1e-4), (40, None, 2.0 ** -90), (127, None, 1e4), (-100, None, 0.0), (-100, None, 2.0 ** 60),
+                                             (-110, 2.0 ** -6, 2.0 ** 99), (-117, None, 30.0)])
+def test_queries_of_any_size(kernel, G, max_new, E, scale, softcap):
+    """bf16 queries as large and as small as the type has them, over keys whose scales bring the scores back to a few (or as
+    near to it as scales go): the factors on the way leave fp32, the scores do not."""
+    D = 64
+    c, lens, offsets = make_case([90, 41, 3], [max_new, 1, 1], G, 1, D, 16, 8, torch.bfloat16, 8)
+    c["q"] = queries(c["q"].shape, E)
+    s = D ** -0.5 if scale is None else scale
+    e = max(-126, min(121, round(-E - math.log2(s) - 6 - 3)))  # sums of 64 products of 2^E and 2^6 2^e: about 2^3 more
+    g = torch.Generator(device="cuda").manual_seed(4)
+    c["exps"][0].copy_(torch.randint(max(e - 1, -126), e + 2, c["exps"][0].shape, generator=g, device="cuda") + 127)
+    c["codes"][0][c["table"][1, 0], 2:5] = 0  # keys of zeros
+    out, lse = attend(c, kernel, scale=scale, softcap=softcap, max_new=max_new)
+    bounds.compare(out, lse, bounds.attention(c, lens, offsets, kernel, scale, softcap=softcap))
