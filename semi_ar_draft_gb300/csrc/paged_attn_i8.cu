@@ -366,7 +366,8 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
                 }
             }
             // The references follow a row's maxima only when these are 2^8 ahead (values up to 2^8 lose nothing), so most
-            // slices need no maximum over the lanes and do not touch the output.
+            // slices need no maximum over the lanes and do not touch the output.  Each row's by itself: what another row
+            // sees must not decide how this one's weights are rounded.
             float mx[2], mz[2];
             bool grow = false;
 #pragma unroll
@@ -388,7 +389,8 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
                         mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], d));
                         mz[r] = fmaxf(mz[r], __shfl_xor_sync(0xffffffffu, mz[r], d));
                     }
-                    const float mn = fmaxf(ref[r], mx[r] - kUp), zn = fmaxf(ref_v[r], mz[r] - kUp);
+                    const float mn = mx[r] > ref[r] + (kUp + 8.f) ? mx[r] - kUp : ref[r];
+                    const float zn = mz[r] > ref_v[r] + (kUp + 8.f) ? mz[r] - kUp : ref_v[r];
                     less[r] = mn == ref[r] ? 1.f : ex2(ref[r] - mn);
                     const float f = zn == ref_v[r] ? 1.f : ex2(ref_v[r] - zn);
                     ref[r] = mn;
