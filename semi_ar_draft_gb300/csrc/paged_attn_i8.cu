@@ -3,10 +3,11 @@
 //
 // With k_l = c_l 2^(e_l) and v_l = d_l 2^(f_l), c and d the codes:
 //   s_l = scale (q . c_l) 2^(e_l), capped;  sum = sum_l 2^(s_l log2 e - m)
-//   o = sum_l 2^(s_l log2 e + f_l - M) d_l;  out = o 2^(M - m) / sum
-// m follows the largest score of a row and M the largest s_l log2 e + f_l, each by itself: a value's weight keeps its bits
+//   o = sum_l 2^(s_l log2 e - m + f_l - u) d_l;  out = o 2^u / sum
+// m follows the largest score of a row and m + u the largest s_l log2 e + f_l, each by itself: a value's weight keeps its bits
 // as a half whatever the scales of the blocks before it, and blocks of zeros (whose scale is the smallest there is) do not
-// move the sum's reference.  Codes are halves exactly, and so is a query times a power of two; nothing else is rounded
+// move the sum's reference.  u is held as such: f_l added to a score of 10^7 would be rounded away, and s_l log2 e - m is
+// the same number in both sums, so that a row of one key is its value however large the score.  Codes are halves exactly, and so is a query times a power of two; nothing else is rounded
 // before the products but the weights.
 //
 // What bounds it is issue slots as much as the cache's bytes, so everything beside the products has to be little.  Keys and
@@ -176,10 +177,10 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
     uint32_t qf[C::kQInSmem ? 1 : KS][2];
     const float cap_out = a.softcap * kLog2e;
     constexpr float kUp = ProbScale<false>::kBits;
-    // What is taken off the exponents of sums and weights: kUp less than the largest that a row followed (kNone: it has seen
-    // nothing), and the sums.
-    constexpr float kNone = -3e38f;
-    float ref[2], ref_v[2];
+    // What is taken off the scores for the sums, kUp less than the largest that a row followed, and off their differences and
+    // the values' exponents for the weights (kNone: the row has seen nothing); and the sums.
+    constexpr float kNone = -3.4028234e38f;
+    float ref[2], ref_u[2];
     uint64_t sums;
     int all_lo = 0, all_hi = 0, rows = 0, group = 0, row0 = 0, seg_first = 0;
     bool fresh = true, far = false;  // far: some row's second factor counts
@@ -236,7 +237,8 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
                 }
             }
             far = __syncthreads_or(row_far);
-            ref[0] = ref[1] = ref_v[0] = ref_v[1] = kNone;
+            ref[0] = ref[1] = 0.f;
+            ref_u[0] = ref_u[1] = kNone;
             sums = 0;
             if (!C::kQInSmem) {
 #pragma unroll
@@ -365,43 +367,63 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
                         }
                 }
             }
-            // The references follow a row's maxima only when these are 2^8 ahead (values up to 2^8 lose nothing), so most
-            // slices need no maximum over the lanes and do not touch the output.  Each row's by itself: what another row
-            // sees must not decide how this one's weights are rounded.
+            // s becomes the differences from the row's reference.  The references follow a row's maxima only when these are 2^8
+            // ahead (values up to 2^8 lose nothing), so most slices need no maximum over the lanes and do not touch the
+            // output.  Each row's by itself: what another row sees must not decide how this one's weights are rounded.
             float mx[2], mz[2];
             bool grow = false;
+            auto take = [&](float x, float y) {  // off the differences
+                const uint64_t both = pk2(-x, -y);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 e = up2(add2(pk2(s[i][2 * h], s[i][2 * h + 1]), both));
+                        s[i][2 * h] = e.x;
+                        s[i][2 * h + 1] = e.y;
+                    }
+            };
+            auto largest = [&](int r) {  // of the lane's differences of a row, and with the values' exponents
                 mx[r] = mz[r] = -CUDART_INF_F;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     mx[r] = fmax3(mx[r], s[i][r], s[i][2 + r]);
                     mz[r] = fmax3(mz[r], s[i][r] + value_exp[i][0], s[i][2 + r] + value_exp[i][1]);
                 }
-                grow |= mx[r] > ref[r] + (kUp + 8.f) || mz[r] > ref_v[r] + (kUp + 8.f);
+            };
+            take(ref[0], ref[1]);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                largest(r);
+                grow |= mx[r] > kUp + 8.f || mz[r] > ref_u[r] + (kUp + 8.f);
             }
             if (__any_sync(0xffffffffu, grow)) {
-                float less[2];
+                float by[2], down[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) {
-                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], d));
-                        mz[r] = fmaxf(mz[r], __shfl_xor_sync(0xffffffffu, mz[r], d));
-                    }
-                    const float mn = mx[r] > ref[r] + (kUp + 8.f) ? mx[r] - kUp : ref[r];
-                    const float zn = mz[r] > ref_v[r] + (kUp + 8.f) ? mz[r] - kUp : ref_v[r];
-                    less[r] = mn == ref[r] ? 1.f : ex2(ref[r] - mn);
-                    const float f = zn == ref_v[r] ? 1.f : ex2(ref_v[r] - zn);
-                    ref[r] = mn;
-                    ref_v[r] = zn;
+                    for (int d = 4; d < 32; d <<= 1) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], d));
+                    const bool first = ref_u[r] == kNone && mx[r] > -CUDART_INF_F;  // (scores, not differences yet)
+                    by[r] = first || mx[r] > kUp + 8.f ? mx[r] - kUp : 0.f;
+                    down[r] = first ? 1.f : ex2(-by[r]);  // (the first time the sum is 0)
+                    ref[r] += by[r];
+                }
+                take(by[0], by[1]);
+                sums = mul2(sums, pk2(down[0], down[1]));
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    largest(r);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mz[r] = fmaxf(mz[r], __shfl_xor_sync(0xffffffffu, mz[r], d));
+                    const float was = ref_u[r] == kNone ? kNone : ref_u[r] - by[r];
+                    ref_u[r] = mz[r] > was + (kUp + 8.f) ? mz[r] - kUp : was;
+                    const float f = ex2(was - ref_u[r]);
 #pragma unroll
                     for (int i = 0; i < KS; ++i) {
                         o[i][r] *= f;
                         o[i][2 + r] *= f;
                     }
                 }
-                sums = mul2(sums, pk2(less[0], less[1]));
             }
             // ---- P^T as halves, fragments of the second product's B
             uint32_t p[MT][2];
@@ -409,10 +431,9 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint64_t x = pk2(s[i][2 * h], s[i][2 * h + 1]);
-                    const float2 e = up2(add2(x, pk2(-ref[0], -ref[1])));
-                    const float2 z = up2(add2(add2(x, pk2(value_exp[i][h], value_exp[i][h])), pk2(-ref_v[0], -ref_v[1])));
-                    sums = add2(sums, pk2(ex2(e.x), ex2(e.y)));
+                    const uint64_t e = pk2(s[i][2 * h], s[i][2 * h + 1]);
+                    const float2 z = up2(add2(add2(e, pk2(value_exp[i][h], value_exp[i][h])), pk2(-ref_u[0], -ref_u[1])));
+                    sums = add2(sums, pk2(ex2(s[i][2 * h]), ex2(s[i][2 * h + 1])));
                     p[i][h] = transpose8x8(pack16<false>(ex2(z.x), ex2(z.y)));
                 }
             // ---- O^T += V^T P^T: bytes (k0 d0, k0 d1, k1 d0, k1 d1) are rows 2 g and 2 g + 1 of the m-tile, which are
@@ -445,10 +466,10 @@ __global__ void __launch_bounds__(SliceI8<DP, HG>::kThreads, SliceI8<DP, HG>::kB
                 float l = r ? both.y : both.x;
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-                if (g == 0) s_ml[warp][2 * t + r] = make_float2(ref[r] == kNone ? -CUDART_INF_F : ref[r] + kUp, l);
+                if (g == 0) s_ml[warp][2 * t + r] = make_float2(ref_u[r] == kNone ? -CUDART_INF_F : ref[r] + kUp, l);
                 // Averages, which are no larger than the values (127 2^121 is nearly fp32's largest number); to the
                 // reference of the sums in two steps, since 2^f may be as large as that too.
-                const float f = ex2(0.5f * (ref_v[r] - ref[r])), inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+                const float f = ex2(0.5f * ref_u[r]), inv = l == 0.f ? 0.f : __fdividef(1.f, l);
 #pragma unroll
                 for (int i = 0; i < KS; ++i)
                     *reinterpret_cast<float2*>(mine_o + o_at(2 * t + r, 16 * i + 2 * g)) =

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
     constexpr int DM = DU / 64;  // 16-value groups of a warp's quarter of a head
     constexpr int R = 2 * NT;    // rows of a lane: 8 j + 2 t + (0, 1)
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float2 s_max[kWarps][kRows];  // a tile's largest scores and weights' exponents
+    __shared__ float s_max[2][kWarps][kRows];  // a tile's largest scores, and weights' exponents
     __shared__ float s_sum[kWarps][kRows];
     __shared__ int s_err;
     __shared__ AttnScratch s_start;
@@ -154,8 +154,8 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
     if (tid == 0) mine->d[kTail].first = mine->d[kHead].first = -1;
     float o[DM][NT][4];  // [16 of the warp's values][8 rows]: values 2 g (rows 2 t, 2 t + 1), 2 g + 1
     const float cap_out = a.softcap * kLog2e;
-    constexpr float kUp = ProbScale<false>::kBits, kNone = -3e38f;  // (as in paged_attn_i8.cu)
-    float ref[R], ref_v[R];
+    constexpr float kUp = ProbScale<false>::kBits, kNone = -3.4028234e38f;  // (as in paged_attn_i8.cu)
+    float ref[R], ref_u[R];
     uint64_t sums[NT];  // of rows 8 j + 2 t and the next
     int all_lo = 0, all_hi = 0, rows = 0, head = 0, row0 = 0, seg_first = 0;
     bool fresh = true, far = false;  // far: some row's second factor counts
@@ -210,7 +210,10 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
             }
             far = __syncthreads_or(row_far);
 #pragma unroll
-            for (int r = 0; r < R; ++r) ref[r] = ref_v[r] = kNone;
+            for (int r = 0; r < R; ++r) {
+                ref[r] = 0.f;
+                ref_u[r] = kNone;
+            }
 #pragma unroll
             for (int j = 0; j < NT; ++j) sums[j] = 0;
 #pragma unroll
@@ -338,9 +341,23 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
                     }
             }
         }
-        // The references follow a row's maxima only when these are 2^8 ahead, in all warps alike.
-        bool grow = false;
-        auto largest = [&](int r, float& mx, float& mz) {  // of the lane's scores of a row, of its weights' exponents
+        // s becomes the differences from the rows' references, which follow a row's maxima only when these are 2^8 ahead, in
+        // all warps alike.
+        auto take = [&](const float (&x)[R]) {  // off the differences
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint64_t both = pk2(-x[2 * j], -x[2 * j + 1]);
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 e = up2(add2(pk2(s[i][j][2 * h], s[i][j][2 * h + 1]), both));
+                        s[i][j][2 * h] = e.x;
+                        s[i][j][2 * h + 1] = e.y;
+                    }
+            }
+        };
+        auto largest = [&](int r, float& mx, float& mz) {  // of the lane's differences of a row, and with the values' exponents
             mx = mz = -CUDART_INF_F;
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
@@ -349,50 +366,58 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
                 mz = fmax3(mz, x + value_exp[i][0], y + value_exp[i][1]);
             }
         };
+        take(ref);
+        bool grow = false;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float mx, mz;
             largest(r, mx, mz);
-            grow |= mx > ref[r] + (kUp + 8.f) || mz > ref_v[r] + (kUp + 8.f);
+            grow |= mx > kUp + 8.f || mz > ref_u[r] + (kUp + 8.f);
         }
         grow = __syncthreads_or(grow);  // (and every warp is done with the tile before this one)
         load_step(C::kStages - 1);
         if (grow) {
+            // The largest of a row in all warps: of the differences, then, from their new reference, with the exponents.
+            auto meet = [&](bool exponents, float (&top)[R]) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float mx, mz;
+                    largest(r, mx, mz);
+                    float x = exponents ? mz : mx;
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                    if (g == 0) s_max[exponents][warp][row_of(r)] = x;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    top[r] = s_max[exponents][0][row_of(r)];
+#pragma unroll
+                    for (int x = 1; x < kWarps; ++x) top[r] = fmaxf(top[r], s_max[exponents][x][row_of(r)]);
+                }
+            };
+            float top[R], by[R];
+            meet(false, top);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                float mx, mz;
-                largest(r, mx, mz);
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    mz = fmaxf(mz, __shfl_xor_sync(0xffffffffu, mz, d));
-                }
-                if (g == 0) s_max[warp][row_of(r)] = make_float2(mx, mz);
+                const bool first = ref_u[r] == kNone && top[r] > -CUDART_INF_F;  // (scores, not differences yet)
+                by[r] = first || top[r] > kUp + 8.f ? top[r] - kUp : 0.f;
+                const float down = first ? 1.f : ex2(-by[r]);  // (the first time the sum is 0)
+                const float2 l = up2(sums[r >> 1]);
+                sums[r >> 1] = r & 1 ? pk2(l.x, l.y * down) : pk2(l.x * down, l.y);
+                ref[r] += by[r];
             }
-            __syncthreads();
+            take(by);
+            meet(true, top);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                float mx = -CUDART_INF_F, mz = mx;
+                const float was = ref_u[r] == kNone ? kNone : ref_u[r] - by[r];
+                ref_u[r] = top[r] > was + (kUp + 8.f) ? top[r] - kUp : was;
+                const float f = ex2(was - ref_u[r]);
 #pragma unroll
-                for (int x = 0; x < kWarps; ++x) {
-                    const float2 y = s_max[x][row_of(r)];
-                    mx = fmaxf(mx, y.x);
-                    mz = fmaxf(mz, y.y);
-                }
-                if (mx > ref[r] + (kUp + 8.f)) {
-                    const float f = ex2(ref[r] - (mx - kUp));
-                    const float2 l = up2(sums[r >> 1]);
-                    sums[r >> 1] = r & 1 ? pk2(l.x, l.y * f) : pk2(l.x * f, l.y);
-                    ref[r] = mx - kUp;
-                }
-                if (mz > ref_v[r] + (kUp + 8.f)) {
-                    const float f = ex2(ref_v[r] - (mz - kUp));
-                    ref_v[r] = mz - kUp;
-#pragma unroll
-                    for (int i = 0; i < DM; ++i) {
-                        o[i][r >> 1][r & 1] *= f;
-                        o[i][r >> 1][2 + (r & 1)] *= f;
-                    }
+                for (int i = 0; i < DM; ++i) {
+                    o[i][r >> 1][r & 1] *= f;
+                    o[i][r >> 1][2 + (r & 1)] *= f;
                 }
             }
         }
@@ -404,13 +429,12 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
                 uint32_t p[4];  // keys 16 i .. + 7, + 8 .. of rows 8 j .., of rows 8 j + 8 ..
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int r = 2 * (j + u);
-                    const uint64_t less = pk2(-ref[r], -ref[r + 1]), less_v = pk2(-ref_v[r], -ref_v[r + 1]);
+                    const uint64_t less_u = pk2(-ref_u[2 * (j + u)], -ref_u[2 * (j + u) + 1]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint64_t x = pk2(s[i][j + u][2 * h], s[i][j + u][2 * h + 1]);
-                        const float2 e = up2(add2(x, less)), z = up2(add2(add2(x, pk2(value_exp[i][h], value_exp[i][h])), less_v));
-                        sums[j + u] = add2(sums[j + u], pk2(ex2(e.x), ex2(e.y)));
+                        const float x = s[i][j + u][2 * h], y = s[i][j + u][2 * h + 1];
+                        const float2 z = up2(add2(add2(pk2(x, y), pk2(value_exp[i][h], value_exp[i][h])), less_u));
+                        sums[j + u] = add2(sums[j + u], pk2(ex2(x), ex2(y)));
                         p[2 * u + h] = pack16<false>(ex2(z.x), ex2(z.y));
                     }
                 }
@@ -467,9 +491,9 @@ __global__ void __launch_bounds__(RowsI8<DP>::kThreads, RowsI8<DP>::kBlocksPerSm
                 float ll = 0.f;
 #pragma unroll
                 for (int x = 0; x < kWarps; ++x) ll += s_sum[x][row];
-                const float m = ref[r] == kNone ? -CUDART_INF_F : ref[r] + kUp;
+                const float m = ref_u[r] == kNone ? -CUDART_INF_F : ref[r] + kUp;
                 // (averages, and in two steps: see paged_attn_i8.cu)
-                const float f = ex2(0.5f * (ref_v[r] - ref[r])), inv = ll == 0.f ? 0.f : __fdividef(1.f, ll);
+                const float f = ex2(0.5f * ref_u[r]), inv = ll == 0.f ? 0.f : __fdividef(1.f, ll);
                 const long long at = attn_out_row(a, w.r.token0, head, row0 + row);
                 const size_t part_at = (size_t)slot * kRows + row;
 #pragma unroll

@@ -46,3 +46,31 @@ def test_queries_of_any_size(kernel, G, max_new, E, scale, softcap):
     c["codes"][0][c["table"][1, 0], 2:5] = 0  # keys of zeros
     out, lse = attend(c, kernel, scale=scale, softcap=softcap, max_new=max_new)
     bounds.compare(out, lse, bounds.attention(c, lens, offsets, kernel, scale, softcap=softcap))
+
+
+@pytest.mark.parametrize("kernel,G,max_new", KERNELS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("e", [-10, 0, 9])
+@pytest.mark.parametrize("scale", [None, -0.25])
+def test_a_row_of_one_key_is_its_value(kernel, G, max_new, dtype, e, scale):
+    """However large the score (60, 6e4, 3e7 and up to twice that): keys so far below one that nothing else has a weight, and
+    requests of few keys.  The weight and the output are rounded once each, the rest is fp32's."""
+    u = torch.finfo(dtype).eps / 2
+    u_p = u if kernel == "wide" else 2.0 ** -11
+    D, n = 128, max_new
+    c, lens, offsets = make_case([n, 300, 40, n], [n] * 4, G, 1, D, 16, 1, dtype, 5)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    sign = torch.randint(0, 2, (D,), generator=g, device="cuda") * 2 - 1
+    c["q"] = ((0.5 + 0.5 * torch.rand(c["q"].shape, generator=g, device="cuda")) * 64 * sign).to(dtype)
+    c["exps"][0].fill_(e + 127)
+    V, want = bounds.R.values(c["codes"][1], c["exps"][1], dtype), []
+    for j, length in enumerate(lens):
+        for l in range(length):
+            at = (int(c["table"][j, l // 16]), l % 16, 0)
+            c["codes"][0][at] = (sign * (120 if (l == length // 2) == (scale is None) else -120)).to(torch.int8)
+            if l == length // 2:
+                want += [V[at]] * n
+    out, _ = attend(c, kernel, scale=scale, max_new=n, causal=False)
+    want = torch.stack(want)[:, None]
+    err = (out.double() - want).abs()
+    assert bool((err <= want.abs() * (u + u_p + u * u_p + 2.0 ** -18) + 2.0 ** -40).all()), float(err.max())
