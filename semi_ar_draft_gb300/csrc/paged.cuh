@@ -347,8 +347,8 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 
 // The lanes of a row (LANES neighbours, each with eight of its values) make halves of a query for an int8 cache: bf16 times
 // the power of two 2^raise that brings the row's largest value to 2^14, which is taken back in the scores' scale; what a half
-// then cannot hold is below 2^-38 of the row's largest, less than fp32 keeps of the sum.  Returns raise; sum is the
-// halves' over the row.  By whole warps.
+// then cannot hold is below 2^-38 of the row's largest, less than fp32 keeps of the sum.  (raise is 120 at most, which makes
+// halves of bf16's subnormal numbers too.)  Returns raise; sum is the halves' over the row.  By whole warps.
 template <bool BF16, int LANES>
 __device__ __forceinline__ int query_halves(uint32_t (&y)[4], float& sum) {
     int raise = 0;
@@ -358,8 +358,8 @@ __device__ __forceinline__ int query_halves(uint32_t (&y)[4], float& sum) {
         for (int e = 0; e < 4; ++e) top = max(top, max(y[e] & 0x7fffu, (y[e] >> 16) & 0x7fffu));
 #pragma unroll
         for (int d = 1; d < LANES; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const int e = (int)(top >> 7) - 127;  // floor(log2) of a normal number
-        raise = e > -127 && e < 128 ? min(max(14 - e, -120), 120) : 0;
+        const int e = (int)(top >> 7) - 127;  // floor(log2) of a normal number; -127 below them, 128 past the finite ones
+        raise = top && e < 128 ? min(14 - e, 120) : 0;
         const float up = two_to(raise);
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = pack16<false>(bf16_lo(y[i]) * up, bf16_hi(y[i]) * up);

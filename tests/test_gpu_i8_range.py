@@ -74,3 +74,15 @@ def test_a_row_of_one_key_is_its_value(kernel, G, max_new, dtype, e, scale):
     want = torch.stack(want)[:, None]
     err = (out.double() - want).abs()
     assert bool((err <= want.abs() * (u + u_p + u * u_p + 2.0 ** -18) + 2.0 ** -40).all()), float(err.max())
+
+
+@pytest.mark.parametrize("kernel,G,max_new", KERNELS)
+@pytest.mark.parametrize("E", [-127, -130, -133])
+def test_queries_below_the_normal_numbers(kernel, G, max_new, E):
+    """Rows of subnormal bf16 queries, over keys that bring the scores to 2^-3 .. 2^4."""
+    c, lens, offsets = make_case([90, 41, 3], [max_new, 1, 1], G, 1, 64, 16, 8, torch.bfloat16, 8)
+    c["q"] = queries(c["q"].shape, E)
+    assert bool((c["q"].float().abs().amax(-1) > 0).all()) and float(c["q"].float().abs().max()) < 2.0 ** -126
+    c["exps"][0].fill_(121 + 127)
+    out, lse = attend(c, kernel, scale=2.0 ** 4, max_new=max_new)
+    bounds.compare(out, lse, bounds.attention(c, lens, offsets, kernel, 2.0 ** 4))
