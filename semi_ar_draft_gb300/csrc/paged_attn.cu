@@ -335,11 +335,12 @@ __global__ void __launch_bounds__(Rows16<F8, DP>::kThreads, Rows16<F8, DP>::kBlo
                 grow |= mx[r] > m[r] + 8.f;
             }
             // The reference of the exponents follows the maximum only when it is 2^8 behind (values up
-            // to 2^8 lose nothing), so most slices do not touch the output.
+            // to 2^8 lose nothing), so most slices do not touch the output.  Each row's by itself: what another row
+            // sees must not decide how this one's probabilities are rounded.
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float mn = fmaxf(m[r], mx[r]);
+                    const float mn = mx[r] > m[r] + 8.f ? mx[r] : m[r];
                     const float f = mn == m[r] ? 1.f : ex2(m[r] - mn);  // m = -inf: 0
                     m[r] = mn;
                     l[r] *= f;
