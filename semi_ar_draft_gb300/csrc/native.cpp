@@ -113,12 +113,20 @@ int type_code(at::ScalarType t) {
     }
 }
 
+// Whether an index means the same element of both: one shape, and one stride wherever there is more than one index.
+bool same_layout(const at::Tensor& x, const at::Tensor& y) {
+    if (x.sizes() != y.sizes()) return false;
+    for (int64_t i = 0; i < x.dim(); ++i)
+        if (x.size(i) > 1 && x.stride(i) != y.stride(i)) return false;
+    return true;
+}
+
 struct Pools {
     int pages, page_size, Hk, D;
     int64_t page, token, head;
 };
 Pools pools_of(const at::Tensor& k, const at::Tensor& v) {
-    if (k.dim() != 4 || v.sizes() != k.sizes() || v.strides() != k.strides())
+    if (k.dim() != 4 || !same_layout(k, v))
         refuse(PyExc_ValueError, "k_pages and v_pages are [pages, page_size, Hk, D] of one shape and layout");
     if (k.scalar_type() != v.scalar_type()) refuse(PyExc_TypeError, "k_pages and v_pages are of one type");
     return {size32(k.size(0)), size32(k.size(1)), size32(k.size(2)), size32(k.size(3)), k.stride(0), k.stride(1), k.stride(2)};
@@ -132,9 +140,8 @@ void check_scales(const at::Tensor& pages, const at::Tensor* ks, const at::Tenso
 // Pools of an int8 cache and the exponents of its blocks, [pages, Hk, page_size / block] uint8 each.
 dspark_block_exponents exponents_of(const at::Tensor& kp, const Pools& x, const at::Tensor& ke, const at::Tensor& ve) {
     if (kp.scalar_type() != at::kChar) refuse(PyExc_TypeError, "k_pages and v_pages are int8");
-    if (ke.scalar_type() != at::kByte || ve.scalar_type() != at::kByte || ke.dim() != 3 || ve.sizes() != ke.sizes() ||
-        ve.strides() != ke.strides() || ke.size(0) != x.pages || ke.size(1) != x.Hk || ke.size(2) < 1 ||
-        x.page_size % ke.size(2))
+    if (ke.scalar_type() != at::kByte || ve.scalar_type() != at::kByte || ke.dim() != 3 || !same_layout(ke, ve) ||
+        ke.size(0) != x.pages || ke.size(1) != x.Hk || ke.size(2) < 1 || x.page_size % ke.size(2))
         refuse(PyExc_ValueError, "k_exp and v_exp are uint8 [pages, Hk, page_size / block] of one layout");
     if (!ke.is_cuda() || !ve.is_cuda()) refuse(PyExc_ValueError, "libdspark takes device tensors");
     return {static_cast<uint8_t*>(ke.data_ptr()), static_cast<uint8_t*>(ve.data_ptr()), (int)(x.page_size / ke.size(2)),
