@@ -39,6 +39,8 @@ class PagedCache:
                  kv_dtype=None, k_scale=None, v_scale=None, device="cuda", scale_block=None):
         self.dtype, self.k_exp, self.v_exp = dtype, None, None
         if kv_dtype == torch.int8:
+            if dtype not in (torch.bfloat16, torch.float16):
+                raise ValueError(f"an int8 cache goes with bf16 or fp16, not {dtype}")
             scale_block = min(16, page_size) if scale_block is None else scale_block
             if not 1 <= scale_block <= min(128, page_size) or scale_block & (scale_block - 1):
                 raise ValueError(f"scale_block {scale_block}: a power of two up to 128 and to the page")
@@ -100,9 +102,16 @@ class PagedCache:
                        out=(self.seq_len, self.offsets, self.slots, self.positions, self._blocks[0], self._free[0]))
         self.max_new = max_new
 
+    def _typed(self, *tensors):
+        """An int8 cache's exponents have the range of its 16-bit type, which the pools do not say."""
+        for t in tensors:
+            if t.dtype != self.dtype:
+                raise TypeError(f"the int8 cache goes with {self.dtype}, got {t.dtype}")
+
     def append(self, layer, k, v, stream=None):
         """k, v [the plan's tokens, Hk, D]: rows past offsets[-1] have no slot and are skipped."""
         if self.k_exp is not None:
+            self._typed(k, v)
             api.cache_append_i8(k, v, self.k_pages[layer], self.v_pages[layer], self.k_exp[layer], self.v_exp[layer], self.slots,
                                 stream, self._error)
             return
@@ -112,6 +121,7 @@ class PagedCache:
     def attend(self, layer, q, stream=None, **kw):
         """q [the plan's tokens, Hq, D]; kw as for api.paged_attention.  Returns (out, lse or None)."""
         if self.k_exp is not None:
+            self._typed(q)
             out, lse, _ = api.paged_attention_i8(q, self.k_pages[layer], self.v_pages[layer], self.k_exp[layer],
                                                  self.v_exp[layer], self.block_table, self.seq_len, self.offsets,
                                                  max_new=self.max_new, stream=stream, error=self._error, **kw)
