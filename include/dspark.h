@@ -521,6 +521,9 @@ dspark_status dspark_paged_attention(const dspark_attention_params* p, const voi
  *   nearest even
  * So a token's error is at most half a step 2^e of the scale that it was written with, and below one step of the block's
  * last one where that grew later.  A token that is overwritten or forgotten leaves its scale until the block is begun anew.
+ * A verify step writes all drafted tokens before its attention, so with blocks longer than a token a later draft, kept or
+ * not, may coarsen the tokens before it: the target's scores at a position then depend on drafts behind it.  With
+ * block = 1 they do not.
  * NaN is stored as 0 and infinities as +-127 steps; either is reported as DSPARK_ERR_NOT_FINITE in `error` (a device
  * word as of dspark_cache_params, or NULL).
  * Slots outside the pool are skipped.  The tokens of one block have to follow one another in slots, in any order,

@@ -5,7 +5,8 @@ pass over the flattened verify tokens on a paged cache, the verification, and th
 
 The target here is a toy: two attention layers with random weights (the operators of the library do the
 drafting, scheduling, cache, attention and verification; torch does the projections).  Its purpose is the flow: every
-length stays on the device, and with temperature 0 the tokens are those of decoding one by one."""
+length stays on the device, and with temperature 0 the tokens are those of decoding one by one (on an int8 cache too: it
+has a scale for every token here, so no draft changes what the target reads of the tokens before it)."""
 from __future__ import annotations
 
 import argparse
@@ -71,7 +72,8 @@ def generate(target, draft, prompts, rounds, T=0.0, budget=None, page_size=16, k
     budget = budget or B * gamma
     most = max(budget + B, B * n)
     blocks = -(-max_len // page_size)
-    cache = PagedCache(B, B * blocks, page_size, blocks, len(target.qkv), target.Hk, target.D, most, kv_dtype=kv_dtype, device=dev)
+    cache = PagedCache(B, B * blocks, page_size, blocks, len(target.qkv), target.Hk, target.D, most, kv_dtype=kv_dtype, device=dev,
+                       scale_block=1 if kv_dtype == torch.int8 else None)
     rows = torch.arange(most, device=dev)
 
     def flat(table):  # table [B, width]: the planned tokens' values, request by request
@@ -113,7 +115,7 @@ def main(argv=None):
     ap.add_argument("--rounds", type=int, default=16)
     kind = ap.add_mutually_exclusive_group()
     kind.add_argument("--e4m3", action="store_true", help="an 8-bit cache with one scale a kv head")
-    kind.add_argument("--int8", action="store_true", help="an 8-bit cache with a scale for each block of tokens and kv head")
+    kind.add_argument("--int8", action="store_true", help="an 8-bit cache with a scale for each token and kv head")
     a = ap.parse_args(argv)
     V, d, gamma, n = 4096, 64, 8, 24
     max_len = max(512, n + a.rounds * (gamma + 1))

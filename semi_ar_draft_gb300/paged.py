@@ -33,7 +33,12 @@ class PagedCache:
     the most new tokens of any step (a step may say that it has fewer: plan's tokens).  kv_dtype: dtype;
     torch.float8_e4m3fn, then with k_scale, v_scale [layers, Hk] fp32 (ones if not given); or torch.int8, whose scales
     come from the keys and values, one for each block of scale_block tokens (16, or the page where that is smaller) and
-    kv head."""
+    kv head.
+
+    A verify step appends all its drafts before it attends, and a draft of large magnitude coarsens the earlier tokens of
+    its block, those that stay included.  scale_block=1 keeps a token as it is whatever follows it, so that the target's
+    distribution at a position depends on what is before it only, as the verification's losslessness has it; it costs a
+    byte a token, head and pool."""
 
     def __init__(self, requests, num_pages, page_size, max_blocks, layers, Hk, D, max_tokens, dtype=torch.bfloat16,
                  kv_dtype=None, k_scale=None, v_scale=None, device="cuda", scale_block=None):
