@@ -519,8 +519,9 @@ dspark_status dspark_paged_attention(const dspark_attention_params* p, const voi
  *   code = x 2^-e rounded to nearest even, within [-127, 127]
  *   where e has grown by n: every code of the block that this call does not write becomes code 2^-n, rounded to
  *   nearest even
- * So a token's error is at most half a step 2^e of the scale that it was written with, and below one step of the block's
- * last one where that grew later.  A token that is overwritten or forgotten leaves its scale until the block is begun anew.
+ * So a token's error is at most half a step 2^e of the scale that it was written with (less than one where M > 127 2^e,
+ * which fp16 past 65024 can be: 65504 is stored as 65024), and below one step of the block's last one where that grew
+ * later.  A token that is overwritten or forgotten leaves its scale until the block is begun anew.
  * A verify step writes all drafted tokens before its attention, so with blocks longer than a token a later draft, kept or
  * not, may coarsen the tokens before it: the target's scores at a position then depend on drafts behind it.  With
  * block = 1 they do not.
