@@ -534,7 +534,7 @@ dspark_status dspark_paged_attention(const dspark_attention_params* p, const voi
  * Apart from that the same inputs give the same outputs bit for bit.
  *
  * dspark_cache_read_i8 is the way back: k, v [T, Hk, D] dense (dtype), 16-byte aligned, become the values of the T
- * slots, exactly; those of slots outside the pool are 0.
+ * slots, exactly; those of slots outside the pool are 0.  k and v are different memory (DSPARK_ERR_INVALID_ARG).
  *
  * dspark_cache_append_i8 writes: k_pages and v_pages, and k and v of the exponents, are different memory, and no two
  * blocks share an exponent (DSPARK_ERR_INVALID_ARG where pointers or strides of 0 say so).

@@ -669,6 +669,8 @@ extern "C" dspark_status dspark_cache_read_i8(const dspark_append_params* p, con
     if (p->k_token_stride != row || p->v_token_stride != row || p->k_head_stride != p->D || p->v_head_stride != p->D)
         return DSPARK_ERR_INVALID_ARG;
     if (p->T == 0) return DSPARK_OK;
+    const uintptr_t k0 = (uintptr_t)k, v0 = (uintptr_t)v, bytes = (uintptr_t)p->T * row * 2;
+    if (k0 < v0 + bytes && v0 < k0 + bytes) return DSPARK_ERR_INVALID_ARG;  // (keys and values over one another)
     int sms = 0;
     if (device_sm_count(&sms) != cudaSuccess) return DSPARK_ERR_CUDA;
     ReadArgs a;
