@@ -38,8 +38,6 @@ struct AttnArgs {
     float sum_scale;  // ProbScale's inverse, for lse
     int q_vec;        // rows of q start on 16-byte boundaries
     float scale, softcap;
-    float score_m;  // score_m 2^score_e = log2 e scale, or with a softcap 2 log2 e scale / softcap (int8 pools)
-    int score_e;
     const unsigned char* q;
     long long q_token, q_head;  // strides, elements
     const unsigned char* k_pages;
@@ -51,7 +49,7 @@ struct AttnArgs {
     const float* k_scale;
     const float* v_scale;
     BlockExp exp;        // int8 pools
-    Steps32 steps;       // the same and the pools, for launch_attn_i8 and launch_attn_i8_rows
+    Steps32 steps;       // the same and the pools, in 32 bits
     unsigned char* out;  // [T, Hq, D]
     float* lse;          // [T, Hq] or null
     // workspace
@@ -61,6 +59,8 @@ struct AttnArgs {
     float2* part_ml;         // [2 parts][rows of a tile]: (maximum, log2 domain; sum)
     float* part_o;           // [2 parts][rows of a tile][D]: sums of weighted values
     int averages;            // or those divided by their parts' sums, for the join (launch_attn_i8, launch_attn_i8_rows)
+    float score_m;  // score_m 2^score_e = log2 e scale, or with a softcap 2 log2 e scale / softcap (int8 pools)
+    int score_e;
 };
 
 // An item spread over blocks, as each of them describes it (first < 0: none).
