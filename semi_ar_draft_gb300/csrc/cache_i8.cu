@@ -597,7 +597,8 @@ extern "C" dspark_status dspark_cache_append_i8(const dspark_append_params* p, c
                                                 int32_t* error, dspark_stream_t stream) {
     const dspark_status st = check_i8(p, x, k_pages, v_pages);
     if (st != DSPARK_OK) return st;
-    if ((p->T && (!k || !v || !slots)) || (((uintptr_t)k | (uintptr_t)v) & 1u) || ((uintptr_t)error & 3u)) return DSPARK_ERR_INVALID_ARG;
+    if ((p->T && (!k || !v || !slots)) || (((uintptr_t)k | (uintptr_t)v) & 1u) || ((uintptr_t)slots & 7u) || ((uintptr_t)error & 3u))
+        return DSPARK_ERR_INVALID_ARG;
     if (k_pages == v_pages || x->k == x->v) return DSPARK_ERR_INVALID_ARG;
     // (blocks that share an exponent are for reading)
     if ((!x->page_stride && p->num_pages > 1) || (!x->block_stride && x->block < p->page_size) || (!x->head_stride && p->Hk > 1))
@@ -664,7 +665,7 @@ extern "C" dspark_status dspark_cache_read_i8(const dspark_append_params* p, con
                                               dspark_stream_t stream) {
     const dspark_status st = check_i8(p, x, k_pages, v_pages);
     if (st != DSPARK_OK) return st;
-    if ((p->T && (!k || !v || !slots)) || (((uintptr_t)k | (uintptr_t)v) & 15u)) return DSPARK_ERR_INVALID_ARG;
+    if ((p->T && (!k || !v || !slots)) || (((uintptr_t)k | (uintptr_t)v) & 15u) || ((uintptr_t)slots & 7u)) return DSPARK_ERR_INVALID_ARG;
     const long long row = (long long)p->Hk * p->D;
     if (p->k_token_stride != row || p->v_token_stride != row || p->k_head_stride != p->D || p->v_head_stride != p->D)
         return DSPARK_ERR_INVALID_ARG;

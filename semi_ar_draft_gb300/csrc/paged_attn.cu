@@ -763,6 +763,7 @@ dspark_status paged_attention(const dspark_attention_params* p, const dspark_blo
     const int kv = x ? kKvI8 : (e4m3 ? kKvE4M3 : kKv16);
     const long long esz = kv == kKv16 ? 2 : 1;
     if ((((uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)out) & 15u) || ((uintptr_t)q & 1u) ||
+        (((uintptr_t)block_table | (uintptr_t)seq_len | (uintptr_t)offsets | (uintptr_t)lse) & 3u) ||
         (p->kv_page_stride * esz) % 16 || (p->kv_token_stride * esz) % 16 || (p->kv_head_stride * esz) % 16)
         return DSPARK_ERR_INVALID_ARG;
     const AttnWs w = attn_ws(p);
