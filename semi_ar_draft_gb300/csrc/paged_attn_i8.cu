@@ -17,7 +17,7 @@
 // (movmatrix).  A warp streams slices of its own through a ring of its own in shared memory, as in paged_attn.cu.
 //
 // Measured: 32 requests of up to 8192 tokens, 8 kv heads of 128, 57 us = 5.0 TB/s (0.74 of the measured copy rate; the rows
-// in A 73 us); 128 requests of up to 8000 tokens 191 us = 5.9 TB/s (0.87; 237 us); heads of 64, 128 requests, 118 us (183
+// in A 73 us); 128 requests of up to 8000 tokens 191 us = 5.9 TB/s (0.87; 237 us); heads of 64, 128 requests, 121 us (183
 // before the block's warps took a head each); 48 requests of 1000 tokens' window, five rows of 96, 29 us; one request of
 // up to 1024 tokens 10.5 us, latency.
 #include "host_util.h"
