@@ -510,7 +510,8 @@ dspark_status dspark_paged_attention(const dspark_attention_params* p, const voi
  * p and kv head h the byte at p page_stride + b block_stride + h head_stride (bytes; k for the keys, v for the values)
  * holds e + 127, and its values are code 2^e, code in [-127, 127].  e lies in [-126, 121] in a cache for bf16 and in
  * [-24, 9] for fp16, where code 2^e is a number of that type; a byte outside is read as the nearest one inside.  (So all
- * calls on one cache are of one dtype, which the pools do not record.)
+ * calls on one cache are of one dtype, which the pools do not record.  -128 is no code and is never written; beside the
+ * largest exponents it is past the type.)
  *
  * dspark_cache_append_i8 writes the keys and values of T tokens to their slots, as dspark_cache_append does.  For a
  * block and head let M be the largest finite magnitude among the call's tokens of the block:

@@ -10,8 +10,8 @@
 // Bound by issue slots (about half of them are used by twelve warps a multiprocessor).  Measured, against the 8-row
 // kernel's layout with two row tiles a warp: 32 requests of up to 8192 tokens, 16 rows, 8 kv heads of 128: 73 us (82);
 // 64 requests, 23 rows, 4 kv heads: 65 us (79).  Three contexts of up to 200000 tokens, two or three tiles of 16
-// rows of 256, softcap: 164 us, each tile reading the cache for itself (752 MB for 264, 4.6 TB/s).  Row tiles of 32 and 64 need more registers or shared memory than three blocks a multiprocessor leave:
-// 105 and 207 us for the first case.
+// rows of 256, softcap: 164 us, each tile reading the cache for itself (752 MB for 264, 4.6 TB/s).  Row tiles of 32 and 64
+// need more registers or shared memory than three blocks a multiprocessor leave: 105 and 207 us for the first case.
 #include "host_util.h"
 #include "mma16.cuh"
 #include "paged.cuh"

@@ -86,3 +86,23 @@ def test_queries_below_the_normal_numbers(kernel, G, max_new, E):
     c["exps"][0].fill_(121 + 127)
     out, lse = attend(c, kernel, scale=2.0 ** 4, max_new=max_new)
     bounds.compare(out, lse, bounds.attention(c, lens, offsets, kernel, 2.0 ** 4))
+
+
+@pytest.mark.parametrize("kernel,G,Hk,D,max_new", [("few", 2, 4, 64, 3), ("few", 4, 2, 96, 2), ("few", 8, 1, 256, 1), ("rows", 5, 2, 128, 3), ("wide", 16, 2, 64, 4)])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_rows_of_every_size_in_one_call(kernel, G, Hk, D, max_new, softcap):
+    """Each row of a magnitude of its own, from subnormal to the largest, over keys of the smallest scales: nearly equal weights
+    beside dominating ones, in one tile.  A row's bits are the same when the others are ordinary."""
+    c, lens, offsets = make_case([300, 41, 77], [max_new, 1, max_new], G * Hk, Hk, D, 16, 8, torch.bfloat16, 9)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    T, Hq = c["q"].shape[:2]
+    plain = queries((T, Hq, D), 0)
+    E = torch.randint(-132, 128, (T, Hq, 1), generator=g, device="cuda").double()
+    c["q"] = torch.where(E < 0, plain.double() * torch.exp2(E.clamp(-132, 0)), plain.double() * torch.exp2(E.clamp(0, 127))).to(torch.bfloat16)
+    c["exps"][0].copy_(torch.randint(1, 5, c["exps"][0].shape, generator=g, device="cuda"))
+    out, lse = attend(c, kernel, max_new=max_new, softcap=softcap)
+    bounds.compare(out, lse, bounds.attention(c, lens, offsets, kernel, softcap=softcap))
+    some = torch.rand((T, Hq), generator=g, device="cuda") < 0.5
+    c["q"] = torch.where(some[..., None], c["q"], plain)
+    again, again_lse = attend(c, kernel, max_new=max_new, softcap=softcap)
+    assert torch.equal(again[some], out[some]) and torch.equal(again_lse[some], lse[some])
